@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(HERE, "_lib", "libbq.so")
 
 BQ_OK, BQ_EINVAL, BQ_EINFEASIBLE, BQ_EALIGN, BQ_ECUDA, BQ_ENOSPC, BQ_EDEVICE = 0, -1, -2, -3, -4, -5, -6
 ADAM_FLAT256, ADAM_TILE128, OPT_MUON, ADAM_TILE32 = 0, 1, 2, 3
+ROWS_BF16, ROWS_FP32, ROWS_FP8 = 0, 1, 2
 
 # every entry point include/bq.h declares
 SYMBOLS = [
@@ -27,6 +28,9 @@ SYMBOLS = [
     "bq_step_adam8", "bq_quant_fp8", "bq_muon_ns_workspace", "bq_muon_ns", "bq_muon_ns_check",
     "bq_muon_ns_noalloc", "bq_muon_roots", "bq_muon_momentum", "bq_muon_apply", "bq_dequant_fp8",
     "bq_group_place", "bq_group_upload_bytes", "bq_group_upload",
+    "bq_embed", "bq_embed_grad_workspace", "bq_embed_grad", "bq_rmsnorm", "bq_rmsnorm_grad_workspace",
+    "bq_rmsnorm_grad", "bq_quant_rows_fp8", "bq_linear_fp8_workspace", "bq_linear_fp8", "bq_linear_fp8_dx",
+    "bq_linear_fp8_dw", "bq_linear_check",
 ]
 
 
@@ -117,6 +121,19 @@ def load():
     lib.bq_group_upload.argtypes = [C.POINTER(Member), C.c_int, P, C.c_size_t, P, C.POINTER(P)]
     lib.bq_muon_ns_noalloc.argtypes = [C.c_int, C.POINTER(Mat), C.c_int, C.c_float, C.c_float, C.c_float,
                                        C.c_float, P]
+    I, L, F, S = C.c_int, C.c_int64, C.c_float, C.c_size_t
+    lib.bq_embed.argtypes = [P, I, P, L, L, L, P, I, L, F, P, L, P]
+    lib.bq_embed_grad_workspace.argtypes = [L, L, L, C.POINTER(S)]
+    lib.bq_embed_grad.argtypes = [P, L, P, I, L, F, L, L, P, I, L, I, P, S, P]
+    lib.bq_rmsnorm.argtypes = [P, L, P, L, P, F, L, L, P, L, P, L, P, L, P, L, P, P]
+    lib.bq_rmsnorm_grad_workspace.argtypes = [L, L, C.POINTER(S)]
+    lib.bq_rmsnorm_grad.argtypes = [P, L, P, L, P, P, P, L, L, L, P, L, P, I, I, P, S, P]
+    lib.bq_quant_rows_fp8.argtypes = [P, L, L, L, P, L, P, L, P]
+    lib.bq_linear_fp8_workspace.argtypes = [L, L, L, C.POINTER(S)]
+    lib.bq_linear_fp8.argtypes = [P, L, P, L, P, L, P, L, L, L, P, L, P, S, P]
+    lib.bq_linear_fp8_dx.argtypes = [P, L, P, L, P, L, L, L, P, L, P, S, P]
+    lib.bq_linear_fp8_dw.argtypes = [P, L, P, L, P, L, L, L, L, P, L, I, P, S, P]
+    lib.bq_linear_check.argtypes = [P, S, P]
     for name in SYMBOLS:
         if name not in ("bq_strerror", "bq_last_error", "bq_layout_free", "bq_shard_free"):
             getattr(lib, name).restype = C.c_int
@@ -372,3 +389,192 @@ def muon_ns_noalloc(mats, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, stre
     arr = _mats(mats)
     _check(load().bq_muon_ns_noalloc(len(arr), arr, int(steps), float(a), float(b), float(c), float(eps),
                                      _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- layer operators
+#
+# Matrices are 2-D torch tensors on the GPU whose last dimension is contiguous (a
+# row pitch is read off the tensor); 1-D tensors are contiguous.  Outputs are the
+# caller's, as everywhere.  Shapes and types are checked here, the rest by the
+# library.
+
+_KINDS = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
+          "torch.uint8": ROWS_FP8}
+
+
+def _refuse(msg):
+    raise BQError(BQ_EINVAL, f"invalid argument: {msg}")
+
+
+def _mat2(name, x, kinds, rows=None, cols=None):
+    """(pointer, row pitch, rows, cols, kind) of a matrix."""
+    if x is None:
+        _refuse(f"{name} is None")
+    kind = _KINDS.get(str(x.dtype))
+    if kind not in kinds:
+        _refuse(f"{name} has type {x.dtype}")
+    if x.dim() != 2:
+        _refuse(f"{name} must be a matrix")
+    r, c = x.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        _refuse(f"{name} is {r} x {c}, expected {rows if rows is not None else 'any'} x {cols if cols is not None else 'any'}")
+    ld, step = x.stride()
+    if step != 1 and c > 1:
+        _refuse(f"{name}'s rows must be contiguous")
+    return x.data_ptr(), ld, r, c, kind
+
+
+def _vec(name, x, kinds, n=None):
+    """(pointer, length, kind) of a contiguous vector."""
+    if x is None:
+        _refuse(f"{name} is None")
+    kind = _KINDS.get(str(x.dtype))
+    if kind not in kinds:
+        _refuse(f"{name} has type {x.dtype}")
+    if x.dim() != 1 or (n is not None and x.shape[0] != n) or (x.shape[0] > 1 and x.stride(0) != 1):
+        _refuse(f"{name} must be a contiguous vector" + (f" of {n}" if n is not None else ""))
+    return x.data_ptr(), x.shape[0], kind
+
+
+def _ids(ids):
+    bits = {"torch.int32": 32, "torch.int64": 64}.get(str(ids.dtype))
+    if bits is None or ids.dim() != 1 or (ids.shape[0] > 1 and ids.stride(0) != 1):
+        _refuse("ids must be a contiguous int32 or int64 vector")
+    return ids.data_ptr(), bits, ids.shape[0]
+
+
+def _tile_scale(name, s, rows, cols):
+    """Pointer of an FP8 weight's tile scales, [ceil(rows/128), ceil(cols/128)] or flat, contiguous."""
+    if s is None:
+        _refuse(f"{name} is None")
+    if str(s.dtype) != "torch.float32" or not s.is_contiguous() or s.numel() != -(-rows // 128) * -(-cols // 128):
+        _refuse(f"{name} must hold one contiguous fp32 scale per 128 x 128 tile of {rows} x {cols}")
+    return s.data_ptr()
+
+
+def _ws(ws):
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def embed(table, ids, out, scale=1.0, table_scale=None, stream=None):
+    """out[t] = bf16(scale * table[ids[t]]); table bf16, or FP8 codes with table_scale
+    (one fp32 scale per 128 x 128 tile).  An id outside the table gives a zero row."""
+    tp, ld, rows, cols, kind = _mat2("table", table, (ROWS_BF16, ROWS_FP8))
+    ip, bits, n = _ids(ids)
+    op, ldo, _, _, _ = _mat2("out", out, (ROWS_BF16,), n, cols)
+    sp = _tile_scale("table_scale", table_scale, rows, cols) if kind == ROWS_FP8 else None
+    _check(load().bq_embed(tp, kind, sp, rows, cols, ld, ip, bits, n, float(scale), op, ldo, _stream(stream)))
+
+
+def embed_grad_workspace(n, rows, cols):
+    b = C.c_size_t()
+    _check(load().bq_embed_grad_workspace(int(n), int(rows), int(cols), C.byref(b)))
+    return b.value
+
+
+def embed_grad(dy, ids, out, ws, scale=1.0, accumulate=False, stream=None):
+    """out[v] = scale * sum of dy[t] over the tokens t of id v, every row of out
+    written (accumulate: added to the rows that tokens name); out bf16 or fp32."""
+    ip, bits, n = _ids(ids)
+    op, ldo, rows, cols, kind = _mat2("out", out, (ROWS_BF16, ROWS_FP32))
+    dp, ldd, _, _, _ = _mat2("dy", dy, (ROWS_BF16,), n, cols)
+    wp, wb = _ws(ws)
+    _check(load().bq_embed_grad(dp, ldd, ip, bits, n, float(scale), rows, cols, op, kind, ldo, int(bool(accumulate)),
+                                wp, wb, _stream(stream)))
+
+
+def _code_rows(name, codes, code_scale, n, cols):
+    cp, ldc, _, _, _ = _mat2(name, codes, (ROWS_FP8,), n, cols)
+    sp, lds, _, _, _ = _mat2(f"{name}'s scale", code_scale, (ROWS_FP32,), -(-cols // 128), n)
+    return cp, ldc, sp, lds
+
+
+def rmsnorm(x, weight, eps, residual=None, h=None, y=None, codes=None, code_scale=None, rstd=None, stream=None):
+    """h = bf16(x + residual), y = h / sqrt(mean(h^2) + eps) * weight; any of: h
+    (needed with a residual), y in bf16, codes with code_scale [ceil(cols/128), n] (FP8
+    rows of y), rstd (fp32, n)."""
+    xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
+    wp, _, _ = _vec("weight", weight, (ROWS_BF16,), cols)
+    rp, ldr = _mat2("residual", residual, (ROWS_BF16,), n, cols)[:2] if residual is not None else (None, 0)
+    hp, ldh = _mat2("h", h, (ROWS_BF16,), n, cols)[:2] if h is not None else (None, 0)
+    yp, ldy = _mat2("y", y, (ROWS_BF16,), n, cols)[:2] if y is not None else (None, 0)
+    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols) if codes is not None else (None, 0, None, 0)
+    qp = _vec("rstd", rstd, (ROWS_FP32,), n)[0] if rstd is not None else None
+    _check(load().bq_rmsnorm(xp, ldx, rp, ldr, wp, float(eps), n, cols, hp, ldh, yp, ldy, cp, ldc, sp, lds, qp,
+                             _stream(stream)))
+
+
+def rmsnorm_grad_workspace(n, cols):
+    b = C.c_size_t()
+    _check(load().bq_rmsnorm_grad_workspace(int(n), int(cols), C.byref(b)))
+    return b.value
+
+
+def rmsnorm_grad(dy, h, weight, rstd, dx, dw, ws, dh=None, accumulate=False, stream=None):
+    """dx (of x and residual alike; dh, the gradient of h past the norm, is added) and
+    dw (bf16 or fp32; accumulate: added to it) from dy and the forward's h and rstd."""
+    hp, ldh, n, cols, _ = _mat2("h", h, (ROWS_BF16,))
+    yp, ldy = _mat2("dy", dy, (ROWS_BF16,), n, cols)[:2]
+    wp, _, _ = _vec("weight", weight, (ROWS_BF16,), cols)
+    qp = _vec("rstd", rstd, (ROWS_FP32,), n)[0]
+    gp, ldg = _mat2("dh", dh, (ROWS_BF16,), n, cols)[:2] if dh is not None else (None, 0)
+    xp, ldx = _mat2("dx", dx, (ROWS_BF16,), n, cols)[:2]
+    dp, _, kind = _vec("dw", dw, (ROWS_BF16, ROWS_FP32), cols)
+    sp, sb = _ws(ws)
+    _check(load().bq_rmsnorm_grad(yp, ldy, hp, ldh, wp, qp, gp, ldg, n, cols, xp, ldx, dp, kind, int(bool(accumulate)),
+                                  sp, sb, _stream(stream)))
+
+
+def quant_rows_fp8(x, codes, code_scale, stream=None):
+    """FP8 rows of a bf16 matrix: codes, and code_scale [ceil(cols/128), n]."""
+    xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
+    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
+    _check(load().bq_quant_rows_fp8(xp, ldx, n, cols, cp, ldc, sp, lds, _stream(stream)))
+
+
+def linear_fp8_workspace(n, rows, cols):
+    """Bytes for linear_fp8, linear_fp8_dx and linear_fp8_dw of n tokens and a rows x
+    cols weight; zero the first 256 once before the first use."""
+    b = C.c_size_t()
+    _check(load().bq_linear_fp8_workspace(int(n), int(rows), int(cols), C.byref(b)))
+    return b.value
+
+
+def linear_fp8(codes, code_scale, w, w_scale, out, ws, stream=None):
+    """out [n, rows] = X W^T: X the FP8 rows (codes [n, cols], code_scale), W the FP8
+    weight [rows, cols] with its tile scales."""
+    wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
+    n = codes.shape[0]
+    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
+    op, ldo = _mat2("out", out, (ROWS_BF16,), n, rows)[:2]
+    tp = _tile_scale("w_scale", w_scale, rows, cols)
+    bp, bb = _ws(ws)
+    _check(load().bq_linear_fp8(cp, ldc, sp, lds, wp, ldw, tp, n, rows, cols, op, ldo, bp, bb, _stream(stream)))
+
+
+def linear_fp8_dx(dy, w, w_scale, dx, ws, stream=None):
+    """dx [n, cols] = Q W: Q the FP8 rows of dy [n, rows] (quantised in the call)."""
+    wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
+    yp, ldy, n, _, _ = _mat2("dy", dy, (ROWS_BF16,), None, rows)
+    xp, ldx = _mat2("dx", dx, (ROWS_BF16,), n, cols)[:2]
+    tp = _tile_scale("w_scale", w_scale, rows, cols)
+    bp, bb = _ws(ws)
+    _check(load().bq_linear_fp8_dx(yp, ldy, wp, ldw, tp, n, rows, cols, xp, ldx, bp, bb, _stream(stream)))
+
+
+def linear_fp8_dw(dy, codes, code_scale, dw, ws, accumulate=False, stream=None):
+    """dw [rows, cols] = dy^T X (accumulate: added to dw), X the forward's FP8 rows."""
+    yp, ldy, n, rows, _ = _mat2("dy", dy, (ROWS_BF16,))
+    cols = codes.shape[1]
+    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
+    dp, ldd = _mat2("dw", dw, (ROWS_BF16,), rows, cols)[:2]
+    bp, bb = _ws(ws)
+    _check(load().bq_linear_fp8_dw(yp, ldy, cp, ldc, sp, lds, n, rows, cols, dp, ldd, int(bool(accumulate)), bp, bb,
+                                   _stream(stream)))
+
+
+def linear_check(ws, stream=None):
+    """Synchronise the stream and raise if a device wait of a projection on this
+    workspace timed out since the last check."""
+    bp, bb = _ws(ws)
+    _check(load().bq_linear_check(bp, bb, _stream(stream)))

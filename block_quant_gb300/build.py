@@ -29,8 +29,11 @@ SOURCES = {
     "planner.cpp": [],
     "step_kernels.cu": ["-lineinfo", "-fmad=false"],
     "ns_gemm.cu": ["-lineinfo"],
+    "ops_api.cpp": [],
+    "row_ops.cu": ["-lineinfo"],
+    "linear_fp8.cu": ["-lineinfo"],
 }
-HEADERS = ["bq_internal.h", "tmem_ptx.h"]
+HEADERS = ["bq_internal.h", "fp8_codes.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
 
 
 def nvcc():

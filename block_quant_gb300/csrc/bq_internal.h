@@ -183,11 +183,14 @@ int muon_ns_noalloc(int batch, const bq_mat* mats, int steps, float a, float b, 
 // a 2-D tiled tensor map (no swizzle) over `rows` x `cols` elements of elem_bytes
 // each at base with row pitch cols; boxes of box_cols x box_rows.  map: 128 bytes.
 int encode_map_2d(void* map, const void* base, int elem_bytes, int64_t cols, int64_t rows, int box_cols, int box_rows);
+// a 2-D tiled tensor map with 128-byte swizzle over `outer` rows of `inner` E4M3
+// codes at base with row pitch `pitch`; boxes of 128 codes x box_outer rows.
+int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_outer);
 
 // errors
 int set_error(int code, const std::string& msg);
 int sm_count();  // SMs of the current device (cached per device)
 bool once_per_device(int key);  // true once per (current device, key); keys below
-constexpr int kOnceStripAttr = 0, kOnceGemmAttr = 1, kOnceTileAttr = 2;
+constexpr int kOnceStripAttr = 0, kOnceGemmAttr = 1, kOnceTileAttr = 2, kOnceLinearAttr = 3;
 
 }  // namespace bq

@@ -28,7 +28,9 @@
 #include <vector>
 
 #include "bq_internal.h"
+#include "row_ops.h"
 #include "tmem_ptx.h"
+#include "umma_ptx.h"
 
 namespace bq {
 namespace {
@@ -41,7 +43,6 @@ constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
 constexpr int EPI_WARPS = 8;       // two per TMEM lane quarter, each half of a tile's columns
 constexpr int GEMM_THREADS = 64 + 32 * EPI_WARPS;  // warp 0 TMA, warp 1 MMA + TMEM, then the epilogue
 constexpr int GEMM_SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 256 /*barriers*/;
-constexpr long long kWaitCycles = 1ll << 32;  // ~2 s at 2 GHz
 // X X^T and (A A^T with A symmetric) have symmetric results: compute and store the
 // tiles touching the upper triangle only (0: every product runs whole)
 #ifndef BQ_NS_SYMMETRIC
@@ -49,93 +50,6 @@ constexpr long long kWaitCycles = 1ll << 32;  // ~2 s at 2 GHz
 #endif
 constexpr int kSymmetric = BQ_NS_SYMMETRIC;
 
-
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// bounded wait: false (and an error word) when the phase does not complete
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* status, int code) {
-  const long long t0 = clock64();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try(bar, parity)) return true;
-    if ((it & 255) == 255 && clock64() - t0 > kWaitCycles) {
-      if (status) atomicExch(status, code);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-
-// c MN-major 64 x 64 chunks in one copy: a 3-D map {64 columns, rows, 64-column
-// chunks} (chunk stride 128 bytes) lands them 8 KB apart, the layout of c
-// separate 64 x 64 boxes
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int row, int chunk, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// ---------------------------------------------------------------- UMMA descriptors
-// Shared-memory matrix descriptor (tcgen05): start address >> 4 in bits 0-13,
-// leading-dimension byte offset >> 4 in bits 16-29, stride-dimension byte
-// offset >> 4 in bits 32-45, the fixed version value 1 in bits 46-47, base
-// offset 0, swizzle mode in bits 61-63 (2 = 128-byte swizzle).
-//  K-major, 128B swizzle: rows of 64 bf16 (128 B), 8-row groups 1024 B apart
-//    (SBO = 1024; LBO unused for this layout).  The k-th 16-element slice of a
-//    row starts 32*k bytes further.
-//  MN-major, 128B swizzle: each k row holds 64 MN-contiguous elements (128 B);
-//    8 k rows form a 1024 B group (SBO = 1024 between groups); 64-element MN
-//    chunks sit LBO apart (one TMA box of BK rows each, LBO = BK * 128 B).
-__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
-         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
 
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits
 // 7-9 = 1, 10-12 = 1), A K-major (bit 15 = 0), B major in bit 16, N >> 3 in bits
@@ -156,6 +70,7 @@ struct GemmArgs {
   int ntiles;  // tiles that run (symmetric: those touching the upper triangle), set by the launcher
   int a_sym;   // the A operand is such a symmetric result: its tiles below the stored ones are read transposed
   int b_sym;   // the same for a K-major B operand
+  int a_mn = 0;  // the A operand is given transposed (MN-major) throughout
 };
 
 // A symmetric result is stored as the 128 x 256 output tiles that touch its
@@ -233,10 +148,6 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& g, uint32_t tmem, 
 // "empty" barrier (the eight epilogue warps' arrivals) before reusing it, and
 // commits its "full" barrier when the tile's products are done.
 constexpr int TMEM_COLS_P = 2 * BN;
-
-__device__ __forceinline__ void mbar_arrive_cta(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 
 // u-th tile that runs -> (m0, n0).  Full products: every tile, column blocks
 // fastest.  Symmetric results: the tiles touching the upper triangle, listed row
@@ -416,107 +327,10 @@ constexpr int HALF_STAGE = 128 * BK * 2;       // 128 rows (or columns) x 64 bf1
 constexpr int STAGE2_BYTES = 2 * HALF_STAGE;   // one CTA's part of a k-block
 constexpr int GEMM2_SMEM = STAGES2 * STAGE2_BYTES + 1024 /*align*/ + 256 /*barriers*/;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// the shared::cluster address of `addr` (a shared::cta address) in CTA `rank`
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
-
-// every thread of both CTAs
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// bounded wait on a barrier that the other CTA of the pair also arrives on
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int* status, int code) {
-  const long long t0 = clock64();
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_cluster(bar, parity)) return true;
-    if ((it & 255) == 255 && clock64() - t0 > kWaitCycles) {
-      if (status) atomicExch(status, code);
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
-// a box into this CTA's shared memory, its bytes completed on `cluster_bar`
-// (a barrier of either CTA of the pair)
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                                 uint32_t cluster_bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(cluster_bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int row, int chunk,
-                                                 uint32_t cluster_bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
-      "%3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(chunk), "r"(cluster_bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// arrive on the barrier at this shared::cta offset in both CTAs once the products
-// issued so far have completed
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  const uint16_t both = 3;
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(both)
-      : "memory");
-}
-
-// made collectively by one warp of each CTA of the pair: the same columns in both
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
 // D = alpha * (A B) + beta * C with B given as [K x N] N-contiguous (tmB: a 3-D
 // map of 64-column chunks, two chunks a copy) and A K-major (tmA: boxes of 64
 // columns x 128 rows; with a_sym, tmAt's two-chunk boxes give the transposed
-// reads of A's k-blocks below its stored tiles).  Pairs walk the 256 x 256 tiles t = cluster, + clusters, ..., row
+// reads of A's k-blocks below its stored tiles; with a_mn, of all of them).  Pairs walk the 256 x 256 tiles t = cluster, + clusters, ..., row
 // blocks fastest.  A pair tile's rows start at a multiple of 256, so its two
 // 128-row halves of a k-block are stored or transposed together and one
 // instruction descriptor serves both.
@@ -572,7 +386,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t b_dst = a_dst + HALF_STAGE;
         const uint32_t fb = map_rank(full_bar(s), 0);
         if (rank == 0) mbar_expect_tx(full_bar(s), 2 * STAGE2_BYTES);
-        if (g.a_sym && !sym_stored(ma, kb * BK)) {
+        if (g.a_mn || (g.a_sym && !sym_stored(ma, kb * BK))) {
           tma_load_3d_pair(a_dst, &tmAt, kb * BK, ma / 64, fb);  // two 64-row chunks
         } else {
           tma_load_2d_pair(a_dst, &tmA, kb * BK, ma, fb);
@@ -604,7 +418,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         tc_fence_after();
         const uint32_t a_addr = base + uint32_t(s) * STAGE2_BYTES;
         const uint32_t b_addr = a_addr + HALF_STAGE;
-        const bool a_t = g.a_sym && !sym_stored(m0, kb * BK);
+        const bool a_t = g.a_mn || (g.a_sym && !sym_stored(m0, kb * BK));
         const uint32_t id = idesc_bf16(PM, BN, 1, a_t ? 1 : 0);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
@@ -1141,6 +955,34 @@ int encode_map_2d(void* map, const void* base, int elem_bytes, int64_t cols, int
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? BQ_OK : BQ_EINVAL;
+}
+
+int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_outer) {
+  EncodeTiled enc = encoder();
+  if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)};
+  const cuuint64_t strides[1] = {cuuint64_t(pitch)};
+  const cuuint32_t box[2] = {128u, cuuint32_t(box_outer)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(BQ_EINVAL, "bq_linear_fp8: tensor map encoding failed (" + std::to_string(int(r)) + ")");
+  return BQ_OK;
+}
+
+// The weight gradient's product on the CTA pairs: A and B both MN-major, their
+// rows the summed index.  The pitches are multiples of 64 elements with the
+// padding allocated, which a 64-column chunk of the last columns reads.
+int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t t, int m, int n, void* D,
+                   int64_t ldd, int accumulate, int* status, void* stream) {
+  CUtensorMap ta, tb;
+  if (int rc = make_map3(&ta, A, m, t, lda, 2)) return rc;
+  if (int rc = make_map3(&tb, B, n, t, ldb, 2)) return rc;
+  auto* d = static_cast<__nv_bfloat16*>(D);
+  GemmArgs g{m, n, int(t), 1.f, accumulate ? 1.f : 0.f, accumulate ? d : nullptr, d, ldd, ldd, status, 0, 0, 0, 0};
+  g.a_mn = 1;
+  return gemm_pair(ta, tb, ta, g, static_cast<cudaStream_t>(stream));
 }
 
 int muon_ns(int batch, const bq_mat* mats, int steps, float a, float b, float c, float eps, void* ws, size_t ws_bytes,

@@ -1,0 +1,286 @@
+// C ABI of the layer operators: argument checks and dispatch to the kernels of
+// row_ops.cu, linear_fp8.cu and ns_gemm.cu.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "bq_internal.h"
+#include "row_ops.h"
+
+using namespace bq;
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 27, kMaxCols = 65536, kMaxRows = int64_t(1) << 30;
+constexpr size_t kStatusBytes = 256;  // device error word at the head of a projection's workspace
+
+int fail(int code, const char* who, const char* what) { return set_error(code, std::string(who) + ": " + what); }
+
+bool off(const void* p, uintptr_t align) { return (reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0; }
+
+// a pitch that a matrix of at most one row never uses counts as its width
+int64_t pitch(int64_t ld, int64_t n, int64_t width) { return n <= 1 ? std::max(ld, width) : ld; }
+
+int check_sizes(const char* who, int64_t n, int64_t rows, int64_t cols) {
+  if (n < 0 || n > kMaxTokens) return fail(BQ_EINVAL, who, "n outside [0, 2^27]");
+  if (rows < 1 || rows > kMaxRows) return fail(BQ_EINVAL, who, "rows outside [1, 2^30]");
+  if (cols < 1 || cols > kMaxCols) return fail(BQ_EINVAL, who, "cols outside [1, 65536]");
+  return BQ_OK;
+}
+
+int check_ws(const char* who, const void* ws, size_t have, size_t need) {
+  if (!ws) return fail(BQ_EINVAL, who, "NULL workspace");
+  if (off(ws, 256)) return fail(BQ_EALIGN, who, "workspace must be 256-byte aligned");
+  if (have < need) return fail(BQ_ENOSPC, who, "workspace too small");
+  return BQ_OK;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
+int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// dx: codes and scales of dy; dw: bf16 rows of X and, where dy's own pitch does not
+// serve, of dy
+struct LinearWs {
+  size_t codes, scales, x, dy, bytes;
+};
+
+LinearWs linear_ws(int64_t n, int64_t rows, int64_t cols) {
+  LinearWs p;
+  p.codes = kStatusBytes;
+  p.scales = p.codes + up(size_t(n) * size_t(up16(rows)));
+  const size_t dx = p.scales + up(size_t((rows + 127) / 128) * size_t(n) * 4);
+  p.x = kStatusBytes;
+  p.dy = p.x + up(size_t(n) * size_t(up64(cols)) * 2);
+  const size_t dw = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
+  p.bytes = std::max(dx, dw);
+  return p;
+}
+
+// tensor-core operands: rows of the product's summed index and tile counts as ints
+int check_linear(const char* who, int64_t n, int64_t rows, int64_t cols) {
+  if (int rc = check_sizes(who, n, rows, cols)) return rc;
+  if (rows > (int64_t(1) << 24)) return fail(BQ_EINVAL, who, "rows above 2^24");
+  if (cols % 16) return fail(BQ_EALIGN, who, "cols must be a multiple of 16");
+  return BQ_OK;
+}
+
+int check_weight(const char* who, const uint8_t* w, int64_t ldw, const float* w_scale, int64_t cols) {
+  if (!w || !w_scale) return fail(BQ_EINVAL, who, "NULL weight");
+  if (ldw < cols) return fail(BQ_EINVAL, who, "weight pitch below cols");
+  if (off(w, 16) || ldw % 16 || off(w_scale, 4))
+    return fail(BQ_EALIGN, who, "weight codes 16-byte aligned with a pitch multiple of 16, scales 4-byte aligned");
+  return BQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bq_embed(const void* table, int kind, const float* table_scale, int64_t rows, int64_t cols, int64_t ld_table,
+             const void* ids, int id_bits, int64_t n, float scale, void* out, int64_t ld_out, bq_stream_t stream) {
+  const char* who = "bq_embed";
+  if (int rc = check_sizes(who, n, rows, cols)) return rc;
+  if (kind != BQ_ROWS_BF16 && kind != BQ_ROWS_FP8) return fail(BQ_EINVAL, who, "table kind must be bf16 or FP8");
+  if (id_bits != 32 && id_bits != 64) return fail(BQ_EINVAL, who, "id_bits must be 32 or 64");
+  if (n == 0) return BQ_OK;
+  if (!table || !ids || !out || (kind == BQ_ROWS_FP8 && !table_scale)) return fail(BQ_EINVAL, who, "NULL argument");
+  ld_table = pitch(ld_table, rows, cols), ld_out = pitch(ld_out, n, cols);
+  if (ld_table < cols || ld_out < cols) return fail(BQ_EINVAL, who, "pitch below cols");
+  if ((kind == BQ_ROWS_BF16 && off(table, 2)) || off(out, 2) || off(ids, uintptr_t(id_bits / 8)) || off(table_scale, 4))
+    return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  return launch_embed(EmbedArgs{table, table_scale, ids, out, rows, ld_table, n, ld_out, scale, int(cols), kind, id_bits},
+                      stream);
+}
+
+int bq_embed_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(BQ_EINVAL, "bq_embed_grad_workspace", "NULL argument");
+  if (int rc = check_sizes("bq_embed_grad_workspace", n, rows, cols)) return rc;
+  *bytes = embed_grad_bytes(n, cols);
+  return BQ_OK;
+}
+
+int bq_embed_grad(const void* dy, int64_t ld_dy, const void* ids, int id_bits, int64_t n, float scale, int64_t rows,
+                  int64_t cols, void* out, int out_kind, int64_t ld_out, int accumulate, void* ws, size_t ws_bytes,
+                  bq_stream_t stream) {
+  const char* who = "bq_embed_grad";
+  if (int rc = check_sizes(who, n, rows, cols)) return rc;
+  if (out_kind != BQ_ROWS_BF16 && out_kind != BQ_ROWS_FP32) return fail(BQ_EINVAL, who, "out kind must be bf16 or fp32");
+  if (id_bits != 32 && id_bits != 64) return fail(BQ_EINVAL, who, "id_bits must be 32 or 64");
+  if (!out || (n > 0 && (!dy || !ids))) return fail(BQ_EINVAL, who, "NULL argument");
+  ld_dy = pitch(ld_dy, n, cols), ld_out = pitch(ld_out, rows, cols);
+  if (ld_dy < cols || ld_out < cols) return fail(BQ_EINVAL, who, "pitch below cols");
+  if (off(dy, 2) || off(out, out_kind == BQ_ROWS_FP32 ? 4 : 2) || off(ids, uintptr_t(id_bits / 8)))
+    return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  if (int rc = check_ws(who, ws, ws_bytes, embed_grad_bytes(n, cols))) return rc;
+  if (n == 0 && accumulate) return BQ_OK;
+  return launch_embed_grad(EmbedGradArgs{dy, ids, out, ld_dy, n, rows, ld_out, scale, int(cols), id_bits, out_kind,
+                                         accumulate ? 1 : 0},
+                           ws, stream);
+}
+
+int bq_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight, float eps,
+               int64_t n, int64_t cols, void* h, int64_t ld_h, void* y, int64_t ld_y, uint8_t* codes, int64_t ld_codes,
+               float* code_scale, int64_t ld_scale, float* rstd, bq_stream_t stream) {
+  const char* who = "bq_rmsnorm";
+  if (int rc = check_sizes(who, n, 1, cols)) return rc;
+  if (!(eps >= 0.f)) return fail(BQ_EINVAL, who, "eps must not be negative or NaN");
+  if (n == 0) return BQ_OK;
+  if (!x || !weight || (residual && !h) || (codes && !code_scale)) return fail(BQ_EINVAL, who, "NULL argument");
+  if (!h && !y && !codes && !rstd) return fail(BQ_EINVAL, who, "no output");
+  if (!residual) h = nullptr;
+  ld_x = pitch(ld_x, n, cols), ld_residual = pitch(ld_residual, n, cols), ld_h = pitch(ld_h, n, cols);
+  ld_y = pitch(ld_y, n, cols), ld_codes = pitch(ld_codes, n, cols), ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
+  if (ld_x < cols || (residual && ld_residual < cols) || (h && ld_h < cols) || (y && ld_y < cols) ||
+      (codes && (ld_codes < cols || ld_scale < n)))
+    return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(x, 2) || off(residual, 2) || off(weight, 2) || off(h, 2) || off(y, 2) || off(code_scale, 4) || off(rstd, 4))
+    return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  return launch_rmsnorm(RmsnormArgs{x, residual, weight, h, y, codes, code_scale, rstd, ld_x, ld_residual, ld_h, ld_y,
+                                    ld_codes, ld_scale, n, eps, int(cols)},
+                        stream);
+}
+
+int bq_rmsnorm_grad_workspace(int64_t n, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(BQ_EINVAL, "bq_rmsnorm_grad_workspace", "NULL argument");
+  if (int rc = check_sizes("bq_rmsnorm_grad_workspace", n, 1, cols)) return rc;
+  *bytes = rmsnorm_grad_bytes(n, cols);
+  return BQ_OK;
+}
+
+int bq_rmsnorm_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight, const float* rstd,
+                    const void* dh, int64_t ld_dh, int64_t n, int64_t cols, void* dx, int64_t ld_dx, void* dw,
+                    int dw_kind, int accumulate, void* ws, size_t ws_bytes, bq_stream_t stream) {
+  const char* who = "bq_rmsnorm_grad";
+  if (int rc = check_sizes(who, n, 1, cols)) return rc;
+  if (dw_kind != BQ_ROWS_BF16 && dw_kind != BQ_ROWS_FP32) return fail(BQ_EINVAL, who, "dw kind must be bf16 or fp32");
+  if (!weight || !dw || (n > 0 && (!dy || !h || !rstd || !dx))) return fail(BQ_EINVAL, who, "NULL argument");
+  ld_dy = pitch(ld_dy, n, cols), ld_h = pitch(ld_h, n, cols), ld_dh = pitch(ld_dh, n, cols);
+  ld_dx = pitch(ld_dx, n, cols);
+  if (ld_dy < cols || ld_h < cols || (dh && ld_dh < cols) || ld_dx < cols)
+    return fail(BQ_EINVAL, who, "pitch below cols");
+  if (off(dy, 2) || off(h, 2) || off(weight, 2) || off(rstd, 4) || off(dh, 2) || off(dx, 2) ||
+      off(dw, dw_kind == BQ_ROWS_FP32 ? 4 : 2))
+    return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  if (int rc = check_ws(who, ws, ws_bytes, rmsnorm_grad_bytes(n, cols))) return rc;
+  if (n == 0 && accumulate) return BQ_OK;
+  return launch_rmsnorm_grad(RmsnormGradArgs{dy, h, weight, dh, rstd, dx, dw, ld_dy, ld_h, ld_dh, ld_dx, n, int(cols),
+                                             dw_kind, accumulate ? 1 : 0},
+                             ws, stream);
+}
+
+int bq_quant_rows_fp8(const void* x, int64_t ld_x, int64_t n, int64_t cols, uint8_t* codes, int64_t ld_codes,
+                      float* code_scale, int64_t ld_scale, bq_stream_t stream) {
+  const char* who = "bq_quant_rows_fp8";
+  if (int rc = check_sizes(who, n, 1, cols)) return rc;
+  if (n == 0) return BQ_OK;
+  if (!x || !codes || !code_scale) return fail(BQ_EINVAL, who, "NULL argument");
+  ld_x = pitch(ld_x, n, cols), ld_codes = pitch(ld_codes, n, cols);
+  ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
+  if (ld_x < cols || ld_codes < cols || ld_scale < n) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(x, 2) || off(code_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  return launch_quant_rows(x, ld_x, n, int(cols), codes, ld_codes, code_scale, ld_scale, stream);
+}
+
+int bq_linear_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(BQ_EINVAL, "bq_linear_fp8_workspace", "NULL argument");
+  if (int rc = check_linear("bq_linear_fp8_workspace", n, rows, cols)) return rc;
+  *bytes = linear_ws(n, rows, cols).bytes;
+  return BQ_OK;
+}
+
+int bq_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                  int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, void* out, int64_t ld_out,
+                  void* ws, size_t ws_bytes, bq_stream_t stream) {
+  const char* who = "bq_linear_fp8";
+  if (int rc = check_linear(who, n, rows, cols)) return rc;
+  if (int rc = check_ws(who, ws, ws_bytes, kStatusBytes)) return rc;
+  if (n == 0) return BQ_OK;
+  ld_x = n == 1 ? std::max(up16(ld_x), cols) : ld_x;
+  ld_out = pitch(ld_out, n, rows), ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
+  ld_w = rows == 1 ? std::max(up16(ld_w), cols) : ld_w;
+  if (int rc = check_weight(who, w, ld_w, w_scale, cols)) return rc;
+  if (!x || !x_scale || !out) return fail(BQ_EINVAL, who, "NULL argument");
+  if (ld_x < cols || ld_out < rows || ld_scale < n) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(x, 16) || ld_x % 16) return fail(BQ_EALIGN, who, "codes must be 16-byte aligned with a pitch multiple of 16");
+  if (off(x_scale, 4) || off(out, 2)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  return launch_linear_fp8(LinearArgs{x, x_scale, w, w_scale, out, ld_x, ld_scale, ld_w, ld_out, n, int(rows), int(cols),
+                                      0, static_cast<int*>(ws)},
+                           stream);
+}
+
+int bq_linear_fp8_dx(const void* dy, int64_t ld_dy, const uint8_t* w, int64_t ld_w, const float* w_scale, int64_t n,
+                     int64_t rows, int64_t cols, void* dx, int64_t ld_dx, void* ws, size_t ws_bytes,
+                     bq_stream_t stream) {
+  const char* who = "bq_linear_fp8_dx";
+  if (int rc = check_linear(who, n, rows, cols)) return rc;
+  const LinearWs p = linear_ws(n, rows, cols);
+  if (int rc = check_ws(who, ws, ws_bytes, p.bytes)) return rc;
+  if (n == 0) return BQ_OK;
+  ld_dy = pitch(ld_dy, n, rows), ld_dx = pitch(ld_dx, n, cols);
+  ld_w = rows == 1 ? std::max(up16(ld_w), cols) : ld_w;
+  if (int rc = check_weight(who, w, ld_w, w_scale, cols)) return rc;
+  if (!dy || !dx) return fail(BQ_EINVAL, who, "NULL argument");
+  if (ld_dy < rows || ld_dx < cols) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(dy, 2) || off(dx, 2)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  auto* base = static_cast<unsigned char*>(ws);
+  auto* codes = base + p.codes;
+  auto* scales = reinterpret_cast<float*>(base + p.scales);
+  const int64_t ldc = up16(rows);
+  if (int rc = launch_quant_rows(dy, ld_dy, n, int(rows), codes, ldc, scales, n, stream)) return rc;
+  return launch_linear_fp8(LinearArgs{codes, scales, w, w_scale, dx, ldc, n, ld_w, ld_dx, n, int(rows), int(cols), 1,
+                                      static_cast<int*>(ws)},
+                           stream);
+}
+
+int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld_x, const float* x_scale,
+                     int64_t ld_scale, int64_t n, int64_t rows, int64_t cols, void* dw, int64_t ld_dw, int accumulate,
+                     void* ws, size_t ws_bytes, bq_stream_t stream) {
+  const char* who = "bq_linear_fp8_dw";
+  if (int rc = check_linear(who, n, rows, cols)) return rc;
+  const LinearWs p = linear_ws(n, rows, cols);
+  if (int rc = check_ws(who, ws, ws_bytes, p.bytes)) return rc;
+  ld_dw = pitch(ld_dw, rows, cols);
+  if (!dw) return fail(BQ_EINVAL, who, "NULL argument");
+  if (ld_dw < cols) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(dw, 2)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  if (n == 0) {
+    if (accumulate) return BQ_OK;
+    const cudaError_t e = cudaMemset2DAsync(dw, size_t(ld_dw) * 2, 0, size_t(cols) * 2, size_t(rows),
+                                            reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BQ_OK : fail(BQ_ECUDA, who, cudaGetErrorString(e));
+  }
+  ld_dy = pitch(ld_dy, n, rows), ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
+  ld_x = n == 1 ? std::max(up16(ld_x), cols) : ld_x;
+  if (!dy || !x || !x_scale) return fail(BQ_EINVAL, who, "NULL argument");
+  if (ld_dy < rows || ld_x < cols || ld_scale < n) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(x, 16) || ld_x % 16) return fail(BQ_EALIGN, who, "codes must be 16-byte aligned with a pitch multiple of 16");
+  if (off(dy, 2) || off(x_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  auto* base = static_cast<unsigned char*>(ws);
+  const int64_t ldxb = up64(cols);
+  if (int rc = launch_dequant_rows(x, ld_x, x_scale, ld_scale, n, int(cols), base + p.x, ldxb, stream)) return rc;
+  // dy as it stands where the product's copies can read it: whole 64-column chunks
+  // inside each row, 16-byte aligned rows
+  const void* a = dy;
+  int64_t lda = ld_dy;
+  if (off(dy, 16) || ld_dy % 8 || rows % 64) {
+    a = base + p.dy;
+    lda = up64(rows);
+    if (int rc = launch_copy_rows(dy, ld_dy, n, int(rows), base + p.dy, lda, stream)) return rc;
+  }
+  return launch_gemm_tn(a, lda, base + p.x, ldxb, n, int(rows), int(cols), dw, ld_dw, accumulate ? 1 : 0,
+                        static_cast<int*>(ws), stream);
+}
+
+int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream) {
+  if (!ws || ws_bytes < kStatusBytes) return fail(BQ_EINVAL, "bq_linear_check", "bad workspace");
+  int status = 0;
+  cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaMemcpy(&status, ws, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && status) e = cudaMemset(ws, 0, sizeof(int));
+  if (e != cudaSuccess) return fail(BQ_ECUDA, "bq_linear_check", cudaGetErrorString(e));
+  if (status) return set_error(BQ_ECUDA, "bq_linear_fp8: a device wait timed out (site " + std::to_string(status) + ")");
+  return BQ_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,78 @@
+// Launchers of the layer operators (row_ops.cu, linear_fp8.cu).  Their callers
+// (ops_api.cpp) have checked every argument; counts of zero never reach them
+// unless said otherwise.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace bq {
+
+struct EmbedArgs {
+  const void* table;  // bf16 or E4M3
+  const float* tscale;
+  const void* ids;
+  void* out;
+  int64_t rows, ldt, n, ldo;
+  float scale;
+  int cols, kind, id_bits;
+};
+int launch_embed(const EmbedArgs& a, void* stream);
+
+struct EmbedGradArgs {
+  const void *dy, *ids;
+  void* out;
+  int64_t ld_dy, n, rows, ldo;
+  float scale;
+  int cols, id_bits, out_kind, accumulate;
+};
+size_t embed_grad_bytes(int64_t n, int64_t cols);
+int launch_embed_grad(const EmbedGradArgs& a, void* ws, void* stream);  // n may be 0
+
+struct RmsnormArgs {
+  const void *x, *residual, *weight;
+  void *h, *y;
+  uint8_t* codes;
+  float *code_scale, *rstd;
+  int64_t ld_x, ld_r, ld_h, ld_y, ld_codes, ld_scale, n;
+  float eps;
+  int cols;
+};
+int launch_rmsnorm(const RmsnormArgs& a, void* stream);
+
+struct RmsnormGradArgs {
+  const void *dy, *h, *weight, *dh;
+  const float* rstd;
+  void *dx, *dw;
+  int64_t ld_dy, ld_h, ld_dh, ld_dx, n;
+  int cols, dw_kind, accumulate;
+};
+size_t rmsnorm_grad_bytes(int64_t n, int64_t cols);
+int launch_rmsnorm_grad(const RmsnormGradArgs& a, void* ws, void* stream);  // n may be 0
+
+int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* codes, int64_t ldc, float* scale,
+                      int64_t lds, void* stream);
+int launch_dequant_rows(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols,
+                        void* out, int64_t ldo, void* stream);
+int launch_copy_rows(const void* x, int64_t ldx, int64_t n, int cols, void* out, int64_t ldo, void* stream);
+
+// FP8 projections (linear_fp8.cu)
+struct LinearArgs {
+  const uint8_t* x;      // codes [n, red], pitch ldx (a multiple of 16)
+  const float* x_scale;  // [ceil(red / 128)][ld_xs]
+  const uint8_t* w;      // codes of the weight [rows, cols], pitch ldw (a multiple of 16)
+  const float* w_scale;  // [ceil(rows / 128)][ceil(cols / 128)]
+  void* out;             // bf16 [n, rows] (or [n, cols]: transposed weight)
+  int64_t ldx, ld_xs, ldw, ldo, n;
+  int rows, cols;
+  int transposed;        // 0: out = x W^T (red = cols); 1: out = x W (red = rows)
+  int* status;
+};
+int launch_linear_fp8(const LinearArgs& a, void* stream);
+
+// D [m, n] (+)= A^T B over t rows, bf16, A [t, m] and B [t, n] with pitches that
+// are multiples of 64 elements (ns_gemm.cu)
+int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t t, int m, int n, void* D,
+                   int64_t ldd, int accumulate, int* status, void* stream);
+
+}  // namespace bq

@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include "bq_internal.h"
+#include "fp8_codes.h"
 #include "tmem_ptx.h"
 
 namespace bq {
@@ -47,12 +48,6 @@ constexpr int kAdamCtas = BQ_ADAM_CTAS_PER_SM;
 
 // ---------------------------------------------------------------- element helpers
 
-__device__ __forceinline__ float bf16f(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
-
-__device__ __forceinline__ uint32_t f2bf(float x) {
-  return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(x)));
-}
-
 struct Hp {
   float lr, b1, b2, eps, omb1, omb2, rbc1, rbc2;
 };
@@ -60,17 +55,6 @@ struct Hp {
 __device__ __forceinline__ Hp make_hp(const bq_adam_hp& h) {
   return Hp{h.lr, h.b1, h.b2, h.eps, h.omb1, h.omb2, h.rbc1, h.rbc2};
 }
-
-// Blackwell's packed fp32 pair arithmetic: each component is rounded exactly
-// like the scalar round-to-nearest operation.  A packed add takes no product as
-// an operand anywhere below: ptxas contracts a packed multiply feeding a packed
-// add into a fused multiply-add even when both carry an explicit .rn, so every
-// multiply-then-add is written as the explicit fused operation the contract
-// specifies.
-__device__ __forceinline__ float2 dup(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }  // operands never products
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 // The Adam update of two elements; per element, each step one IEEE fp32
 // operation rounded to nearest, fma(x, y, z) = x*y + z rounded once:
@@ -85,32 +69,6 @@ __device__ __forceinline__ void adam_pair(const Hp& h, float2 g, float2 p, float
   const float2 den = add2(make_float2(__fsqrt_rn(vh.x), __fsqrt_rn(vh.y)), dup(h.eps));
   const float2 u = make_float2(__fdiv_rn(mh.x, den.x), __fdiv_rn(mh.y, den.y));
   p1 = fma2(dup(-h.lr), u, p);
-}
-
-// Block scale from an absmax (fp32 bits; all values >= 0 so bit order == value
-// order): stored scale s = amax/qmax, reciprocal r = qmax/amax (one division each
-// per block).  mode 0: s == 0 -> zero codes; 1: codes from x*r; 2: r overflowed
-// (tiny amax) -> codes from x/s.
-// max of three floats; a NaN operand gives NaN (so a NaN in a block reaches its
-// scale, as a maximum over the raw bit patterns would)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-struct QScale {
-  float s, r;
-  int mode;
-};
-
-__device__ __forceinline__ QScale qscale(uint32_t amax_bits, float qmax) {
-  const float a = __uint_as_float(amax_bits);
-  QScale q;
-  q.s = __fdiv_rn(a, qmax);
-  q.r = __fdiv_rn(qmax, a);
-  q.mode = q.s == 0.f ? 0 : (isinf(q.r) ? 2 : 1);
-  return q;
 }
 
 // Exact small-integer conversions without I2F / F2I:
@@ -174,27 +132,6 @@ __device__ __forceinline__ uint2 codes_uint8(const float* x, const QScale& q) {
       b[i] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(x[i], q.s), 0.f), 255.f), 8388608.f));
   }
   return make_uint2(low_bytes(b[0], b[1], b[2], b[3]), low_bytes(b[4], b[5], b[6], b[7]));
-}
-
-// 8 E4M3 codes (round to nearest even, saturating); scale 0 keeps each sign
-__device__ __forceinline__ uint2 codes_e4m3(const float* x, const QScale& q) {
-  uint32_t w[4];
-  if (q.mode == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = ((__float_as_uint(x[2 * i]) >> 24) & 0x80u) | ((__float_as_uint(x[2 * i + 1]) >> 16) & 0x8000u);
-  } else if (q.mode == 1) {
-    const float2 r = dup(q.r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = uint32_t(__nv_cvt_float2_to_fp8x2(mul2(make_float2(x[2 * i], x[2 * i + 1]), r), __NV_SATFINITE, __NV_E4M3));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], q.s), __fdiv_rn(x[2 * i + 1], q.s)),
-                                               __NV_SATFINITE, __NV_E4M3));
-  }
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 __device__ __forceinline__ void store_p8(float* dst, const float* p) {

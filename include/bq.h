@@ -394,6 +394,112 @@ int bq_muon_apply(const bq_shard* shard, float* master, const void* const* updat
 int bq_muon_ns_noalloc(int batch, const bq_mat* mats, int steps, float a, float b, float c, float eps,
                        bq_stream_t stream);
 
+/* ------------------------------------------------------------------ layer operators
+ * What a layer computes on the buffers of the step: its FP8 parameters as the
+ * AllGather leaves them, and the bf16 gradients that bq_pack takes.  No passage of
+ * the pages defines these; the FP8 rule (codes and scales) is bq_step_adam8's.
+ *   - an FP8 weight (rows x cols) is the E4M3 codes of its row-major 2-D view and
+ *     one fp32 scale per 128 x 128 tile, tiles in row-major order: in a gathered
+ *     DBuffer, the codes from the tensor's start and the scales from its first
+ *     FP8 slot;
+ *   - FP8 rows (n x cols) have one fp32 scale per 128 values of a row: the scale
+ *     of row t, group j at code_scale[j * ld_scale + t], j < ceil(cols / 128);
+ *   - matrices are row-major with a row pitch ld_* in elements (>= their width; of
+ *     a matrix with at most one row it may be anything from the width up);
+ *   - n (rows, one per token) may be 0: nothing is read, and only a gradient that
+ *     is not accumulated is written (zeros).
+ * Common errors: BQ_EINVAL (a NULL argument, a negative count, a pitch below the
+ * width, an unknown kind; n above 2^27, cols above 65536, rows above 2^30),
+ * BQ_EALIGN (a pointer not aligned to its element type; where more is asked for,
+ * the call says so), BQ_ENOSPC (workspace too small), BQ_ECUDA.  Any pitch and any
+ * alignment of the elements works; 16-byte aligned pointers, pitches and widths of
+ * whole 16-byte words run the vector kernels. */
+enum {
+  BQ_ROWS_BF16 = 0,
+  BQ_ROWS_FP32 = 1,
+  BQ_ROWS_FP8 = 2
+};
+
+/* bq_embed - out[t] = bf16(scale * T[ids[t]]): rows of the token table, kind
+ * BQ_ROWS_BF16, or BQ_ROWS_FP8 with table_scale (its tiles' scales; else NULL).
+ * An FP8 value is code x tile scale in fp32 (one rounding), then the factor (one),
+ * then bf16.  ids: int32 or int64 (id_bits); an id outside [0, rows), as padding
+ * has, gives a zero row. */
+int bq_embed(const void* table, int kind, const float* table_scale, int64_t rows, int64_t cols, int64_t ld_table,
+             const void* ids, int id_bits, int64_t n, float scale, void* out, int64_t ld_out, bq_stream_t stream);
+
+/* bq_embed_grad - the table's gradient: out[v] = scale * sum of dy[t] over the t
+ * with ids[t] == v, for every v in [0, rows): rows that no token names become 0
+ * (accumulate: out[v] += ..., and those rows are not touched).  dy: bf16; out:
+ * out_kind BQ_ROWS_BF16 or BQ_ROWS_FP32.  The batch's tokens are sorted by id and
+ * summed in fp32 in a fixed order: the same arguments give the same bits.
+ * ws: bq_embed_grad_workspace(n, rows, cols) bytes, 256-byte aligned. */
+int bq_embed_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
+int bq_embed_grad(const void* dy, int64_t ld_dy, const void* ids, int id_bits, int64_t n, float scale, int64_t rows,
+                  int64_t cols, void* out, int out_kind, int64_t ld_out, int accumulate, void* ws, size_t ws_bytes,
+                  bq_stream_t stream);
+
+/* bq_rmsnorm - residual addition, root-mean-square norm, 8-bit output.  Per row:
+ *   h = bf16(x + residual)  (residual NULL: h = x and nothing is written to h);
+ *   rstd = 1 / sqrt(mean(h^2) + eps);  y = (h * rstd) * weight  in fp32;
+ *   y_out = bf16(y) if not NULL;  codes, code_scale of y if not NULL: per 128
+ *   values a = max |y|, s = a / 448, code = e4m3(y * (448 / a)), as bq_step_adam8.
+ * rstd (fp32, n) may be NULL.  x, residual, weight, h, y: bf16.  h may be x or
+ * residual itself (same pointer and pitch).  A NaN or infinity in a row reaches
+ * the scale or the codes of its groups. */
+int bq_rmsnorm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual, const void* weight, float eps,
+               int64_t n, int64_t cols, void* h, int64_t ld_h, void* y, int64_t ld_y, uint8_t* codes, int64_t ld_codes,
+               float* code_scale, int64_t ld_scale, float* rstd, bq_stream_t stream);
+
+/* bq_rmsnorm_grad - gradients of bq_rmsnorm: with u = h * rstd and t = dy * weight,
+ *   dx = rstd * (t - u * mean(t * u)) + dh   (dh NULL: 0), bf16, the gradient of x
+ *        and of residual alike (dh: the gradient that reaches h past the norm);
+ *   dw = sum over rows of dy * u  (accumulate: += ), dw_kind BQ_ROWS_BF16 or
+ *        BQ_ROWS_FP32, summed in fp32 in an order that n and the GPU fix.
+ * dx may be dy or dh itself.  ws: bq_rmsnorm_grad_workspace(n, cols) bytes,
+ * 256-byte aligned. */
+int bq_rmsnorm_grad_workspace(int64_t n, int64_t cols, size_t* bytes);
+int bq_rmsnorm_grad(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const void* weight, const float* rstd,
+                    const void* dh, int64_t ld_dh, int64_t n, int64_t cols, void* dx, int64_t ld_dx, void* dw,
+                    int dw_kind, int accumulate, void* ws, size_t ws_bytes, bq_stream_t stream);
+
+/* bq_quant_rows_fp8 - FP8 rows of a bf16 matrix, the rule of bq_rmsnorm's codes. */
+int bq_quant_rows_fp8(const void* x, int64_t ld_x, int64_t n, int64_t cols, uint8_t* codes, int64_t ld_codes,
+                      float* code_scale, int64_t ld_scale, bq_stream_t stream);
+
+/* bq_linear_fp8* - a projection with an FP8 weight W (rows x cols, out features x
+ * in features) and its gradients, on tcgen05 tensor cores:
+ *   bq_linear_fp8     out [n, rows]  = X W^T,  X: FP8 rows (n x cols);
+ *   bq_linear_fp8_dx  dx  [n, cols]  = Q W,    Q: FP8 rows of the bf16 dy (n x rows),
+ *                                     quantised by the call as bq_quant_rows_fp8;
+ *   bq_linear_fp8_dw  dw [rows, cols] = dy^T bf16(X)  (accumulate: += ), dy bf16.
+ * Each 128 of the summed index is one fp32 tensor-core sum of code products, which
+ * is multiplied by its two scales and added in fp32 (dw: bf16 operands, fp32 sum);
+ * results are rounded once to bf16.  Sums are taken in an order that the sizes and
+ * the GPU fix.  The codes of X and W must be 16-byte aligned with pitches that are
+ * multiples of 16, and cols a multiple of 16 (BQ_EALIGN); n and rows are free.
+ * ws: bq_linear_fp8_workspace(n, rows, cols) bytes for any of the three, 256-byte
+ * aligned, whose first 256 bytes are 0 before its first use (later calls leave
+ * them so); calls that can overlap need workspaces of their own.
+ * Resources: the kernels hold tensor memory while they run (all 512 columns of an
+ * SM, or 256); a CTA whose columns are held by a co-resident kernel waits. */
+int bq_linear_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
+int bq_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                  int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, void* out, int64_t ld_out,
+                  void* ws, size_t ws_bytes, bq_stream_t stream);
+int bq_linear_fp8_dx(const void* dy, int64_t ld_dy, const uint8_t* w, int64_t ld_w, const float* w_scale, int64_t n,
+                     int64_t rows, int64_t cols, void* dx, int64_t ld_dx, void* ws, size_t ws_bytes,
+                     bq_stream_t stream);
+int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld_x, const float* x_scale,
+                     int64_t ld_scale, int64_t n, int64_t rows, int64_t cols, void* dw, int64_t ld_dw, int accumulate,
+                     void* ws, size_t ws_bytes, bq_stream_t stream);
+
+/* bq_linear_check - synchronise `stream` and read the workspace's device error
+ * word: every wait of the tensor-core kernels gives up after about two seconds,
+ * records where and lets the kernel exit.  BQ_OK if it is clear; otherwise it is
+ * cleared and BQ_ECUDA returned (also on a CUDA error). */
+int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,478 @@
+"""The layer operators on the GPU against their formulas in fp64: embedding lookup
+and gradient, root-mean-square norm with FP8 rows and its gradients, FP8
+projections and theirs.
+
+Tolerances: u = 2^-8 bounds a rounding to bf16 relative to its result, e = 2^-24 one
+to fp32.  A sum of k fp32 terms is off by at most k e times the sum of their
+magnitudes; a tensor-core sum of k products by k 2^-23 times it (its additions may
+truncate)."""
+
+import numpy as np
+import pytest
+
+import block_quant_gb300 as bq
+from oracle import layer as L
+from oracle.codecs import bf16_bits_to_f32, e4m3_decode, e4m3_encode
+
+pytestmark = pytest.mark.gpu
+
+U, E = 2.0 ** -8, 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from block_quant_gb300 import build
+
+    build.build()
+    return bq.load()
+
+
+# ----------------------------------------------------------------------------- helpers
+
+
+def bf16(x, dev, pitch=0, shift=0):
+    """A bf16 matrix (or vector) on the GPU with `pitch` spare columns, starting
+    `shift` elements past an aligned address, and its values in fp64."""
+    import torch
+
+    x = torch.as_tensor(np.asarray(x, np.float32)).bfloat16()
+    want = x.double().numpy()
+    if x.dim() == 1:
+        flat = torch.full((x.shape[0] + shift,), 7.0, dtype=torch.bfloat16, device=dev)
+        flat[shift:] = x.to(dev)
+        return flat[shift:], want
+    n, c = x.shape
+    flat = torch.full((n * (c + pitch) + shift,), 7.0, dtype=torch.bfloat16, device=dev)
+    m = flat[shift:].view(n, c + pitch)[:, :c]
+    m.copy_(x.to(dev))
+    return m, want
+
+
+def empty(n, c, dev, dtype, pitch=0, shift=0, fill=7.0):
+    """(matrix, the allocation it lies in) with every value `fill`."""
+    import torch
+
+    flat = torch.full((n * (c + pitch) + shift,), fill, dtype=dtype, device=dev)
+    return flat[shift:].view(n, c + pitch)[:, :c], flat
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def outside_kept(m, flat, shift, fill=7.0):
+    """The spare columns around a strided output still hold what they held."""
+    n, c = m.shape
+    ld = m.stride(0)
+    rest = flat[shift:].double().cpu().numpy().reshape(n, ld)[:, c:]
+    return np.all(rest == fill) and np.all(flat[:shift].double().cpu().numpy() == fill)
+
+
+def fp8_weight(rng, rows, cols, dev):
+    """Codes and tile scales of a random weight, and its values in fp64."""
+    import torch
+
+    codes = e4m3_encode((rng.standard_normal((rows, cols)) * 60).astype(np.float32))
+    scale = (np.exp(rng.standard_normal((-(-rows // 128), -(-cols // 128)))) * 1e-3).astype(np.float32)
+    return (torch.as_tensor(codes).to(dev), torch.as_tensor(scale).to(dev), L.decode_tiles(codes, scale))
+
+
+def fp8_rows(rng, n, cols, dev, pitch=0, spare=0):
+    import torch
+
+    codes = e4m3_encode((rng.standard_normal((n, cols)) * 60).astype(np.float32))
+    scale = np.exp(rng.standard_normal((-(-cols // 128), n))).astype(np.float32)
+    c = torch.full((n, cols + pitch), 0x7F, dtype=torch.uint8, device=dev)  # NaN codes beside the rows
+    c[:, :cols] = torch.as_tensor(codes).to(dev)
+    s = torch.full((scale.shape[0], n + spare), float("nan"), dtype=torch.float32, device=dev)
+    s[:, :n] = torch.as_tensor(scale).to(dev)
+    return c[:, :cols], s[:, :n], L.decode_rows(codes, scale)
+
+
+def check_codes(codes, scale, y, slack):
+    """Codes and scales of fp64 rows y whose fp32 value is off by at most slack |y|."""
+    got_s, got = f64(scale), e4m3_decode(codes.cpu().view(__import__("torch").uint8).numpy()).astype(np.float64)
+    want_s = L.row_scales(y)
+    assert np.all(np.abs(got_s - want_s) <= (slack + 4 * E) * want_s)
+    s = L.spread_rows(got_s, y.shape[1])
+    # E4M3: four significant bits (half a step is 2^-4 of the value), subnormal step 2^-9
+    assert np.all(np.abs(got * s - y) <= 2.0 ** -4 * np.abs(got) * s * 1.001 + 2.0 ** -10 * s * 1.001 + slack * np.abs(y))
+
+
+# ----------------------------------------------------------------------------- embedding
+
+
+@pytest.mark.parametrize("cols,pitch,shift", [(8, 0, 0), (128, 8, 0), (2880, 0, 0), (1032, 0, 0), (131, 0, 0), (256, 3, 0), (264, 0, 1), (1, 0, 0)])
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("bits", [32, 64])
+def test_embed(cuda, cols, pitch, shift, kind, bits):
+    import torch
+
+    rng = np.random.default_rng(cols + bits)
+    rows, n = 300, 41
+    ids = rng.integers(-3, rows + 3, n)
+    ids[:3] = [-1, rows, rows - 1]
+    if bits == 64:
+        ids[3] = 2 ** 40
+    tid = torch.as_tensor(ids.astype(np.int64 if bits == 64 else np.int32)).to(cuda)
+    out, flat = empty(n, cols, cuda, torch.bfloat16, pitch, shift)
+    if kind == "fp8":
+        t, ts, want = fp8_weight(rng, rows, cols, cuda)
+        bq.embed(t, tid, out, scale=0.37, table_scale=ts)
+    else:
+        t, want = bf16(rng.standard_normal((rows, cols)), cuda, pitch, shift)
+        bq.embed(t, tid, out, scale=0.37)
+    ref = L.embed(want, ids, np.float64(np.float32(0.37)))
+    assert np.all(np.abs(f64(out) - ref) <= U * 1.001 * np.abs(ref))
+    assert outside_kept(out, flat, shift)
+
+
+def test_embed_of_no_tokens_and_one(cuda):
+    import torch
+
+    t, want = bf16(np.arange(64, dtype=np.float32).reshape(4, 16), cuda)
+    out, _ = empty(0, 16, cuda, torch.bfloat16)
+    bq.embed(t, torch.empty(0, dtype=torch.int64, device=cuda), out)
+    out, _ = empty(1, 16, cuda, torch.bfloat16)
+    bq.embed(t, torch.tensor([3], device=cuda), out)
+    assert np.array_equal(f64(out)[0], want[3])
+
+
+@pytest.mark.parametrize("n,rows,cols,how", [
+    (1, 1, 8, "any"), (1, 1000, 264, "any"), (31, 7, 136, "any"), (32, 7, 128, "one"), (33, 7, 128, "one"),
+    (64, 65, 8, "one"), (65, 64, 16, "any"), (700, 300, 520, "zipf"), (1000, 513, 131, "zipf"), (777, 90, 1, "one"),
+    (5000, 70000, 24, "zipf"), (9000, 300000, 8, "any"), (40000, 1200, 8, "zipf"), (257, 200, 2880, "out"),
+])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad(cuda, n, rows, cols, how, kind, accumulate):
+    import torch
+
+    rng = np.random.default_rng(n + rows)
+    if how == "one":
+        ids = np.full(n, rows - 1)
+    elif how == "zipf":
+        ids = np.minimum(rng.zipf(1.3, n) - 1, rows)  # `rows`: outside
+    elif how == "out":
+        ids = np.where(rng.random(n) < 0.5, -1, rows + 5)
+    else:
+        ids = rng.integers(-1, rows, n)
+    pitch = 0 if cols % 8 else 8
+    dy, dyv = bf16(rng.standard_normal((n, cols)), cuda, pitch)
+    tid = torch.as_tensor(ids.astype(np.int32)).to(cuda)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float32
+    out, flat = empty(rows, cols, cuda, dt, pitch, 0, 0.5)
+    ws = torch.empty(bq.embed_grad_workspace(n, rows, cols), dtype=torch.uint8, device=cuda)
+    bq.embed_grad(dy, tid, out, ws, scale=1.5, accumulate=accumulate)
+    g, mag = L.embed_grad(dyv, ids, rows, 1.5)
+    k = np.bincount(ids[(ids >= 0) & (ids < rows)], minlength=rows)[:, None]
+    if accumulate:
+        g, mag = g + 0.5, mag + 0.5
+    tol = (k + 2) * E * mag + (U * 1.001 * np.abs(g) if kind == "bf16" else 0) + 1e-30
+    assert np.all(np.abs(f64(out) - g) <= tol)
+    if pitch:
+        assert outside_kept(out, flat, 0, 0.5)
+    if not accumulate:  # the same bits again, on another stream
+        first = out.clone()
+        out.fill_(3.0)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            bq.embed_grad(dy, tid, out, ws, scale=1.5)
+        s.synchronize()
+        assert torch.equal(first, out)
+
+
+def test_embed_grad_of_no_tokens(cuda):
+    import torch
+
+    out = torch.full((5, 12), 3.0, device=cuda)
+    ws = torch.empty(bq.embed_grad_workspace(0, 5, 12), dtype=torch.uint8, device=cuda)
+    none = torch.empty(0, 12, dtype=torch.bfloat16, device=cuda)
+    ids = torch.empty(0, dtype=torch.int64, device=cuda)
+    bq.embed_grad(none, ids, out, ws, accumulate=True)
+    assert torch.all(out == 3.0)
+    bq.embed_grad(none, ids, out, ws)
+    assert torch.all(out == 0.0)
+
+
+# ----------------------------------------------------------------------------- norm
+
+WIDTHS = [1, 7, 8, 100, 127, 128, 129, 136, 256, 264, 1000, 2880, 4096, 8192, 8200, 8193, 16384, 16392, 33000]
+
+
+@pytest.mark.parametrize("cols", WIDTHS)
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm(cuda, cols, residual):
+    import torch
+
+    rng = np.random.default_rng(cols)
+    n, eps = 5, 1e-5
+    pitch, shift = (8, 0) if cols % 16 == 0 else (0, 0) if cols % 8 == 0 else (3, 1)
+    a = rng.standard_normal((n, cols)) * np.array([1, 1e-4, 1e3, 0, 1])[:, None]
+    x, xv = bf16(a, cuda, pitch, shift)
+    r, rv = bf16(rng.standard_normal((n, cols)) * (a != 0), cuda, pitch, shift)
+    w, wv = bf16(1 + 0.3 * rng.standard_normal(cols), cuda)
+    h, hf = empty(n, cols, cuda, torch.bfloat16, pitch, shift)
+    y, yf = empty(n, cols, cuda, torch.bfloat16, pitch, shift)
+    codes = torch.full((n, cols + pitch), 0x55, dtype=torch.uint8, device=cuda)
+    scale = torch.full((-(-cols // 128), n + 2), 7.0, device=cuda)
+    rstd = torch.empty(n, device=cuda)
+    bq.rmsnorm(x, w, eps, residual=r if residual else None, h=h if residual else None, y=y, codes=codes[:, :cols],
+               code_scale=scale[:, :n], rstd=rstd)
+    if residual:
+        hv = f64(h)
+        assert np.all(np.abs(hv - (xv + rv)) <= U * 1.001 * np.abs(xv + rv))
+        assert outside_kept(h, hf, shift)
+    else:
+        hv = xv
+    want, rs = L.rmsnorm(hv, wv, np.float64(np.float32(eps)))
+    # the sum of squares, its mean and the root: (cols + 4) e, halved by the root, and
+    # an approximate reciprocal root of 2^-22
+    slack = (cols + 4) * E + 2.0 ** -21
+    assert np.all(np.abs(f64(rstd) - rs) <= slack * rs)
+    assert np.all(np.abs(f64(y) - want) <= (U * 1.001 + slack) * np.abs(want))
+    assert outside_kept(y, yf, shift)
+    check_codes(codes[:, :cols], scale[:, :n], want, slack + 2 * E)
+    assert torch.all(codes[:, cols:] == 0x55) and torch.all(scale[:, n:] == 7.0)
+
+
+def test_rmsnorm_in_place_and_parts(cuda):
+    """h over x, h over the residual, and each output on its own give the same bits."""
+    import torch
+
+    rng = np.random.default_rng(3)
+    x, _ = bf16(rng.standard_normal((9, 520)), cuda)
+    r, _ = bf16(rng.standard_normal((9, 520)), cuda)
+    w, _ = bf16(1 + 0.1 * rng.standard_normal(520), cuda)
+    h, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(9, device=cuda)
+    bq.rmsnorm(x, w, 1e-6, residual=r, h=h, y=y, rstd=rstd)
+    for k in range(2):
+        a, b = x.clone(), r.clone()
+        y2 = torch.empty_like(x)
+        bq.rmsnorm(a, w, 1e-6, residual=b, h=(a, b)[k], y=y2)
+        assert torch.equal((a, b)[k], h) and torch.equal(y2, y)
+    rs2 = torch.empty_like(rstd)
+    bq.rmsnorm(h, w, 1e-6, rstd=rs2)
+    assert torch.equal(rs2, rstd)
+
+
+@pytest.mark.parametrize("cols", [520, 515])
+def test_rmsnorm_rows_of_zeros_infinities_and_nan(cuda, cols):
+    import torch
+
+    a = np.ones((4, cols), np.float32)
+    a[0] = 0
+    a[1, 5] = np.inf
+    a[2, 300] = np.nan
+    x, _ = bf16(a, cuda)
+    w, _ = bf16(np.ones(cols), cuda)
+    y = torch.empty(4, cols, dtype=torch.bfloat16, device=cuda)
+    codes = torch.empty(4, cols, dtype=torch.uint8, device=cuda)
+    scale = torch.empty(-(-cols // 128), 4, device=cuda)
+    bq.rmsnorm(x, w, 1e-5, y=y, codes=codes, code_scale=scale)
+    y, s, c = f64(y), f64(scale), e4m3_decode(codes.cpu().numpy()).astype(np.float64)
+    assert np.all(y[0] == 0) and np.all(s[:, 0] == 0) and np.all(c[0] == 0)
+    assert np.isnan(y[1, 5]) and np.all(y[1, :5] == 0)  # 1 / inf, and inf * 0
+    assert np.isnan(c[1, 5] * s[0, 1])
+    assert np.all(np.isnan(y[2])) and np.all(np.isnan(s[:, 2]))
+    assert np.all(np.abs(y[3] - 1) <= 0.01) and np.all(c[3] == 448)  # untouched by its neighbours
+
+
+@pytest.mark.parametrize("n,cols", [(1, 8), (1, 8192), (2, 7), (3, 129), (37, 264), (301, 2880), (700, 520), (330, 515),
+                                    (5, 8200), (4, 8193), (3, 16392), (2, 33000)])
+@pytest.mark.parametrize("dh", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_rmsnorm_grad(cuda, n, cols, dh, kind):
+    import torch
+
+    rng = np.random.default_rng(n * cols)
+    pitch, shift = (8, 0) if cols % 16 == 0 else (0, 0) if cols % 8 == 0 else (3, 1)
+    h, hv = bf16(rng.standard_normal((n, cols)), cuda, pitch, shift)
+    dy, dyv = bf16(rng.standard_normal((n, cols)), cuda, pitch, shift)
+    g, gv = bf16(rng.standard_normal((n, cols)), cuda, pitch, shift)
+    w, wv = bf16(1 + 0.3 * rng.standard_normal(cols), cuda)
+    rstd = torch.as_tensor(1 / np.sqrt((hv * hv).mean(1) + 1e-5), dtype=torch.float32).to(cuda)
+    rv = f64(rstd)
+    dx, flat = empty(n, cols, cuda, torch.bfloat16, pitch, shift)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float32
+    dw = torch.full((cols,), 0.25, dtype=dt, device=cuda)
+    ws = torch.empty(bq.rmsnorm_grad_workspace(n, cols), dtype=torch.uint8, device=cuda)
+    bq.rmsnorm_grad(dy, h, w, rstd, dx, dw, ws, dh=g if dh else None)
+    want, wantw = L.rmsnorm_grad(dyv, hv, wv, rv)
+    if dh:
+        want = want + gv
+    u, t = np.abs(hv * rv[:, None]), np.abs(dyv * wv)
+    mag = rv[:, None] * (t + u * np.mean(t * u, axis=1, keepdims=True)) + (np.abs(gv) if dh else 0)
+    assert np.all(np.abs(f64(dx) - want) <= U * 1.001 * np.abs(want) + (cols + 8) * E * mag)
+    assert outside_kept(dx, flat, shift)
+    magw = np.sum(np.abs(dyv) * u, axis=0)
+    tolw = (n + 4) * E * magw
+    assert np.all(np.abs(f64(dw) - wantw) <= tolw + (U * 1.001 * np.abs(wantw) if kind == "bf16" else 0))
+    once = f64(dw)
+    bq.rmsnorm_grad(dy, h, w, rstd, dx, dw, ws, dh=g if dh else None, accumulate=True)
+    assert np.all(np.abs(f64(dw) - (once + wantw)) <= tolw + 2 * E * np.abs(once) + (U * 1.001 * np.abs(once + wantw) + 2 * U * np.abs(once) if kind == "bf16" else 2 * E * np.abs(wantw)))
+
+
+def test_rmsnorm_grad_in_place_and_of_no_rows(cuda):
+    import torch
+
+    rng = np.random.default_rng(8)
+    h, _ = bf16(rng.standard_normal((40, 384)), cuda)
+    dy, _ = bf16(rng.standard_normal((40, 384)), cuda)
+    g, _ = bf16(rng.standard_normal((40, 384)), cuda)
+    w, _ = bf16(rng.standard_normal(384), cuda)
+    rstd = torch.rand(40, device=cuda) + 0.5
+    ws = torch.empty(bq.rmsnorm_grad_workspace(40, 384), dtype=torch.uint8, device=cuda)
+    dx, dw = torch.empty_like(h), torch.empty(384, device=cuda)
+    bq.rmsnorm_grad(dy, h, w, rstd, dx, dw, ws, dh=g)
+    for k in range(2):
+        a, b, dw2 = dy.clone(), g.clone(), torch.empty_like(dw)
+        bq.rmsnorm_grad(a, h, w, rstd, (a, b)[k], dw2, ws, dh=b)
+        assert torch.equal((a, b)[k], dx) and torch.equal(dw2, dw)
+    none = torch.empty(0, 384, dtype=torch.bfloat16, device=cuda)
+    bq.rmsnorm_grad(none, none, w, rstd[:0], none, dw, ws, accumulate=True)
+    assert torch.equal(dw2, dw)
+    bq.rmsnorm_grad(none, none, w, rstd[:0], none, dw, ws)
+    assert torch.all(dw == 0)
+
+
+@pytest.mark.parametrize("cols", [1, 8, 100, 128, 130, 264, 1032, 2881])
+def test_quant_rows(cuda, cols):
+    import torch
+
+    rng = np.random.default_rng(cols)
+    n = 19
+    x, xv = bf16(rng.standard_normal((n, cols)) * np.exp(8 * rng.standard_normal((n, 1))), cuda)
+    x[3] = 0
+    xv[3] = 0
+    x[4] = 2.0 ** -130  # 448 / a overflows
+    xv[4] = 2.0 ** -130
+    codes = torch.empty(n, cols, dtype=torch.float8_e4m3fn, device=cuda)
+    scale = torch.empty(-(-cols // 128), n, device=cuda)
+    bq.quant_rows_fp8(x, codes, scale)
+    keep = np.arange(n) != 4
+    check_codes(codes[torch.as_tensor(keep)], scale[:, torch.as_tensor(keep)], xv[keep], 2 * E)
+    s4 = f64(scale)[:, 4]
+    assert np.all(s4 > 0) and np.all(np.abs(s4 - 2.0 ** -130 / 448) <= 2.0 ** -150)  # a subnormal scale
+
+
+# ----------------------------------------------------------------------------- projections
+
+SHAPES = [(1, 1, 16), (1, 128, 128), (1, 300, 4096), (2, 130, 144), (8, 256, 1024), (33, 257, 1040), (64, 200, 2064),
+          (100, 64, 8192), (128, 128, 128), (129, 300, 272), (256, 256, 256), (300, 520, 2064), (513, 1000, 528),
+          (1030, 2881, 272), (2048, 1024, 640), (700, 4000, 1536)]
+
+
+def workspace(n, rows, cols, dev):
+    import torch
+
+    ws = torch.full((bq.linear_fp8_workspace(n, rows, cols),), 0xFF, dtype=torch.uint8, device=dev)
+    ws[:256] = 0
+    return ws
+
+
+def sum_tol(a, b, red):
+    """Bound on the fp32 sum over `red` products of scaled codes: k-blocks of 128 on
+    the tensor cores, then one fp32 addition and three roundings of scales a block."""
+    return (128 * 2.0 ** -23 + (-(-red // 128) + 3) * E) * (np.abs(a) @ np.abs(b))
+
+
+@pytest.mark.parametrize("n,rows,cols", SHAPES)
+def test_linear(cuda, n, rows, cols):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    x, xs, xv = fp8_rows(rng, n, cols, cuda, pitch=16, spare=3)
+    w, ws_, wv = fp8_weight(rng, rows, cols, cuda)
+    for pitch, shift in [(0, 0), (5, 1)]:
+        out, flat = empty(n, rows, cuda, torch.bfloat16, pitch, shift)
+        ws = workspace(n, rows, cols, cuda)
+        bq.linear_fp8(x, xs, w, ws_, out, ws)
+        bq.linear_check(ws)
+        ref = xv @ wv.T
+        assert np.all(np.abs(f64(out) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(xv, wv.T, cols))
+        assert outside_kept(out, flat, shift)
+
+
+@pytest.mark.parametrize("n,rows,cols", SHAPES)
+def test_linear_dx(cuda, n, rows, cols):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    w, ws_, wv = fp8_weight(rng, rows, cols, cuda)
+    dy, _ = bf16(rng.standard_normal((n, rows)), cuda, 3 if rows % 8 else 0)
+    # the rows that the call quantises, taken from the row quantiser (tested above)
+    q = torch.empty(n, rows, dtype=torch.uint8, device=cuda)
+    qs = torch.empty(-(-rows // 128), n, device=cuda)
+    bq.quant_rows_fp8(dy, q, qs)
+    qv = L.decode_rows(q.cpu().numpy(), qs.cpu().numpy())
+    for pitch, shift in [(0, 0), (5, 1)]:
+        dx, flat = empty(n, cols, cuda, torch.bfloat16, pitch, shift)
+        ws = workspace(n, rows, cols, cuda)
+        bq.linear_fp8_dx(dy, w, ws_, dx, ws)
+        bq.linear_check(ws)
+        ref = qv @ wv
+        assert np.all(np.abs(f64(dx) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(qv, wv, rows))
+        assert outside_kept(dx, flat, shift)
+
+
+@pytest.mark.parametrize("n,rows,cols", SHAPES)
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_linear_dw(cuda, n, rows, cols, accumulate):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    x, xs, xv = fp8_rows(rng, n, cols, cuda, pitch=16, spare=1)
+    dy, dv = bf16(rng.standard_normal((n, rows)), cuda, 8 if rows % 64 == 0 else 0)
+    dw, flat = empty(rows, cols, cuda, torch.bfloat16, 8, 0, 0.5)
+    ws = workspace(n, rows, cols, cuda)
+    bq.linear_fp8_dw(dy, x, xs, dw, ws, accumulate=accumulate)
+    bq.linear_check(ws)
+    mag = np.abs(dv).T @ np.abs(xv)
+    ref = dv.T @ xv + (0.5 if accumulate else 0)
+    # X is rounded to bf16 once, products summed in fp32
+    tol = U * 1.001 * (np.abs(ref) + mag) + n * 2.0 ** -23 * mag
+    assert np.all(np.abs(f64(dw) - ref) <= tol)
+    assert outside_kept(dw, flat, 0, 0.5)
+
+
+def test_linear_of_no_tokens(cuda):
+    import torch
+
+    rng = np.random.default_rng(1)
+    w, ws_, _ = fp8_weight(rng, 48, 32, cuda)
+    x = torch.empty(0, 32, dtype=torch.uint8, device=cuda)
+    xs = torch.empty(1, 0, device=cuda)
+    y = torch.empty(0, 48, dtype=torch.bfloat16, device=cuda)
+    ws = workspace(0, 48, 32, cuda)
+    bq.linear_fp8(x, xs, w, ws_, y, ws)
+    bq.linear_fp8_dx(y, w, ws_, torch.empty(0, 32, dtype=torch.bfloat16, device=cuda), ws)
+    dw = torch.full((48, 32), 2.0, dtype=torch.bfloat16, device=cuda)
+    bq.linear_fp8_dw(y, x, xs, dw, ws, accumulate=True)
+    assert torch.all(dw == 2.0)
+    bq.linear_fp8_dw(y, x, xs, dw, ws)
+    assert torch.all(dw == 0.0)
+
+
+def test_linear_same_bits_again_and_rows_apart(cuda):
+    """The same call gives the same bits, a row's result does not depend on the rows
+    beside it, and a NaN stays in its row."""
+    import torch
+
+    rng = np.random.default_rng(5)
+    n, rows, cols = 40, 384, 1024
+    x, xs, _ = fp8_rows(rng, n, cols, cuda)
+    w, ws_, _ = fp8_weight(rng, rows, cols, cuda)
+    ws = workspace(n, rows, cols, cuda)
+    a, b = (torch.empty(n, rows, dtype=torch.bfloat16, device=cuda) for _ in range(2))
+    bq.linear_fp8(x, xs, w, ws_, a, ws)
+    bq.linear_fp8(x, xs, w, ws_, b, ws)
+    assert torch.equal(a, b)
+    x2 = x.clone()
+    x2[7, 100] = 0x7F
+    bq.linear_fp8(x2, xs, w, ws_, b, ws)
+    bad = torch.isnan(b).any(dim=1).cpu().numpy()
+    assert bad[7] and bad.sum() == 1
+    keep = np.arange(n) != 7
+    assert torch.equal(a[torch.as_tensor(keep)], b[torch.as_tensor(keep)])
