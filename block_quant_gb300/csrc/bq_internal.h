@@ -186,6 +186,12 @@ int encode_map_2d(void* map, const void* base, int elem_bytes, int64_t cols, int
 // a 2-D tiled tensor map with 128-byte swizzle over `outer` rows of `inner` E4M3
 // codes at base with row pitch `pitch`; boxes of 128 codes x box_outer rows.
 int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_outer);
+// a 2-D tiled tensor map over the fp32 scales of FP8 rows, [groups][pitch]: boxes of
+// one group's scales of 128 rows
+int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, int64_t pitch);
+// a 2-D tiled tensor map with 64-byte swizzle over bf16 rows (pitch in elements) for
+// stores of 32 x 32 boxes
+int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch);
 
 // errors
 int set_error(int code, const std::string& msg);

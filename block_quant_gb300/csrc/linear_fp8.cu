@@ -14,12 +14,18 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 #include <string>
 
 #include "bq_internal.h"
 #include "row_ops.h"
 #include "tmem_ptx.h"
 #include "umma_ptx.h"
+
+// fewest 256 x 256 tiles for the CTA pairs
+#ifndef BQ_LINEAR_PAIR_MIN
+#define BQ_LINEAR_PAIR_MIN 60
+#endif
 
 namespace bq {
 namespace {
@@ -57,6 +63,18 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// acc += f * r
+template <int N>
+__device__ __forceinline__ void add_scaled(float* acc, const uint32_t* r, float f) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const float2 o = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(f, f),
+                                make_float2(acc[j], acc[j + 1]));
+    acc[j] = o.x;
+    acc[j + 1] = o.y;
+  }
+}
+
 struct LinArgs {
   const float *xs, *ws;  // scales of X [groups][ld_xs] and of W's tiles
   __nv_bfloat16* out;
@@ -67,6 +85,7 @@ struct LinArgs {
   int transposed;        // 0: out = X W^T, 1: out = X W
   int split, stages;     // CTAs of a cluster that share a tile's k-blocks; pipeline stages
   int a_rows;            // rows of X that a stage holds (a multiple of 8, <= 128)
+  int tma_out;           // out takes TMA stores (16-byte aligned rows)
   int* status;
 };
 
@@ -179,21 +198,15 @@ __global__ void __launch_bounds__(THREADS, 2)
       tc_fence_after();
       const uint32_t at = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf) * BN + uint32_t(half) * (BN / 2);
 #pragma unroll
-      for (int j0 = 0; j0 < BN / 2; j0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(at + uint32_t(j0), r);
-        if (j0 + 32 == BN / 2) {
+      for (int j0 = 0; j0 < BN / 2; j0 += 8) {
+        uint32_t r[8];
+        tmem_ld8(at + uint32_t(j0), r);
+        if (j0 + 8 == BN / 2) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cta(tempty_bar(buf));
         }
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 o = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                      make_float2(fk, fk), make_float2(acc[j0 + j], acc[j0 + j + 1]));
-          acc[j0 + j] = o.x;
-          acc[j0 + j + 1] = o.y;
-        }
+        add_scaled<8>(acc + j0, r, fk);
       }
     }
   }
@@ -235,49 +248,382 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// Large products: pairs of CTAs (cta_group::2, one pair per two SMs) walk 256 x 256
+// tiles of out in bands of kBand row blocks.  Each CTA stages its 128 rows of X and its
+// 128 columns (W rows, or W columns when transposed) of a k-block; the leader issues
+// M = 256 products that read both CTAs' shared memory.  A tile's fp32 sums stay in the
+// epilogue warps' registers (64 a thread); its bf16 rows leave through shared memory
+// and TMA stores while the next tile's products run.
+//
+// What bounds it is the hand-over of an accumulator: products done -> epilogue warps
+// read it -> both CTAs' arrivals -> next products, about 800 cycles.  A k-block is
+// therefore two products of N = 128 with an accumulator each (four in all, every
+// column of tensor memory): while one is handed over the other three hold 768 cycles
+// of products, against 512 with two accumulators of N = 256.
+constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
+constexpr int HALF_STAGE = 128 * BK;            // 16 KB
+constexpr int PSTAGE_BYTES = 2 * HALF_STAGE;
+#ifndef BQ_UNITS
+#define BQ_UNITS 1
+#endif
+constexpr int UNITS = BQ_UNITS, UN = PN / UNITS;       // products (accumulators) of a k-block
+// Sixteen epilogue warps, four per tensor-memory lane quarter: part p of a quarter
+// reads columns 32p .. 32p + 31 of every accumulator.  Five warpgroups with TMA (warp
+// 0) and MMA (warp 1); of the launch's 640 x 96 registers the first group keeps 56 a
+// thread and the epilogue takes 104.
+constexpr int PEPI = 16, PCOLS = UN / 4, SEG = 32 * UNITS;  // SEG: columns from one 32-column box to the next
+constexpr int PAIR_THREADS = 128 + 32 * PEPI;
+constexpr int kRegsLaunch = 96, kRegsIssue = 56, kRegsEpilogue = 104;
+static_assert(128 * kRegsIssue + 32 * PEPI * kRegsEpilogue <= PAIR_THREADS * kRegsLaunch, "register split");
+constexpr int OUT_BOX = 32 * 64;                // 32 rows x 32 bf16 of out, one a warp
+// X's scales of a k-block (128 rows of this CTA) are copied with the stages, on the same
+// barrier: a plain load would queue behind the stages' copies.  An accumulator that is
+// full says that they have landed.  Slot it % SLOTS is free when the producer holds
+// stage it: its stage's last products were issued after every epilogue warp had handed
+// over the accumulators of k-block it - PSTAGES - 2.
+constexpr int SLOTS = 8, SLOT_BYTES = 128 * 4;
+static_assert(SLOTS > PSTAGES + 2, "scale slots");
+constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
+constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
+constexpr int kPairTmem = 2 * PN;
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <bool TRANS>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                  const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmO, const LinArgs g) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4 * UNITS];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(PSTAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * PSTAGES + a); };               // accumulator a:
+  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 * UNITS + a); };  // k-block parity x unit
+
+  const int rank = int(cluster_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (g.n + PM - 1) / PM, nt = (g.width + PN - 1) / PN, ntiles = mt * nt;
+  const int nk = (g.red + BK - 1) / BK;
+  const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(full_bar(s), 1);   // the leader's expect_tx
+      mbar_init(empty_bar(s), 1);  // the leader's commit
+    }
+    for (int a = 0; a < 2 * UNITS; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * PEPI);  // the epilogue warps of both CTAs
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // The issuing warps run whole (every lane waits, one elected lane issues), so that
+    // loop counters, addresses and descriptors stay in the uniform datapath: with the
+    // loops in one lane's branch a product took about 85 cycles to issue, and a k-block's
+    // waits, products and commits more than its 512 cycles of tensor work
+    if (warp == 0) {
+      // ---------------- TMA producer (both CTAs: this CTA's halves)
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        int bm, bn;
+        banded_tile(t, mt, nt, kBand, bm, bn);
+        const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = int(it % PSTAGES), l = int(it % SLOTS);
+          ok = mbar_wait(empty_bar(s), ((it / PSTAGES) & 1u) ^ 1u, g.status, 31);
+          if (!ok) break;
+          const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
+          const uint32_t fb = map_rank(full_bar(s), 0);
+          if (elect_one()) {
+            if (rank == 0) mbar_expect_tx(full_bar(s), 2 * (PSTAGE_BYTES + SLOT_BYTES));
+            tma_load_2d_pair(base + OFF_SCALES + uint32_t(l) * SLOT_BYTES, &tmS, ma, kb, fb);
+            tma_load_2d_pair(a_dst, &tmX, kb * BK, ma, fb);
+            if (TRANS)
+              tma_load_2d_pair(b_dst, &tmW, nb, kb * BK, fb);
+            else
+              tma_load_2d_pair(b_dst, &tmW, kb * BK, nb, fb);
+          }
+          __syncwarp();
+        }
+      }
+      // drain (leader): the pair's last copies have landed; the peer waits for this at
+      // the closing cluster barrier
+      if (rank == 0)
+        for (uint32_t d = it > uint32_t(PSTAGES) ? it - PSTAGES : 0; d < it; ++d)
+          mbar_wait(full_bar(int(d % PSTAGES)), (d / PSTAGES) & 1u, g.status, 32);
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer (leader).  A product's N are half of each CTA's: unit
+      // u takes columns UN / 2 u .. of both halves of the tile
+      const uint32_t id = idesc_e4m3(PM, UN, TRANS ? 1 : 0);
+      const uint32_t total = uint32_t((ntiles - pair + npairs - 1) / npairs) * uint32_t(nk);
+      uint32_t it = 0;
+      bool ok = true;
+      for (; it < total; ++it) {
+        const int s = int(it % PSTAGES), buf = int(it & 1u);
+        ok = mbar_wait(full_bar(s), (it / PSTAGES) & 1u, g.status, 34);
+        if (!ok) break;
+        const uint32_t a_addr = base + uint32_t(s) * PSTAGE_BYTES, b_addr = a_addr + HALF_STAGE;
+        // K-major: rows 128 bytes apart, 32-code k slices 32 bytes apart; MN-major: a
+        // column is a byte, 32 k rows of 128 bytes a slice
+        const uint64_t ad = sdesc(a_addr, 16, 1024), bd = TRANS ? sdesc(b_addr, BK * 128, 1024) : sdesc(b_addr, 16, 1024);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int acc = buf * UNITS + u;
+          if (it >= 2) ok = ok && mbar_wait_cluster_relaxed(tempty_bar(acc), ((it >> 1) & 1u) ^ 1u, g.status, 33);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma_e4m3_pair(tmem + uint32_t(acc) * UN, ad + uint64_t(2 * kk),
+                            bd + uint64_t(TRANS ? 4 * u + 256 * kk : 512 * u + 2 * kk), id, kk != 0 ? 1u : 0u);
+            mma_commit_pair(tfull_bar(acc));
+            if (u == UNITS - 1) mma_commit_pair(empty_bar(s));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      // every product issued here has finished before the accumulators are freed
+      if (it > 0 && ok)
+        mbar_wait(tfull_bar(int((it - 1) & 1u) * UNITS + UNITS - 1), ((it - 1) >> 1) & 1u, g.status, 36);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
+    // ---------------- scaled accumulation and output (both CTAs: this CTA's 128 rows)
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t te0 = map_rank(tempty_bar(0), 0);
+    const uint32_t box = base + OFF_OUT + uint32_t(warp - 4) * OUT_BOX;
+    const uint32_t my_scale = base + OFF_SCALES + 4u * uint32_t(32 * q + lane);
+    const uint32_t acc0 = tmem + (uint32_t(32 * q) << 16) + uint32_t(part) * PCOLS;
+    const int64_t ws_step = TRANS ? g.tile_cols : 1;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < ntiles; t += npairs) {
+      int bm, bn;
+      banded_tile(t, mt, nt, kBand, bm, bn);
+      const int row0 = bm * PM + 128 * rank + 32 * q;                        // the warp's first row of out
+      const int c0 = bn * PN + 128 * (part >> 1) + PCOLS * (part & 1);       // its columns: unit u's from c0 + 64u
+      const float* ws = TRANS ? g.ws + (c0 >> 7) : g.ws + int64_t(c0 >> 7) * g.tile_cols;
+      float acc[UNITS * PCOLS];
+#pragma unroll
+      for (int j = 0; j < UNITS * PCOLS; ++j) acc[j] = 0.f;
+      // W's scales for 32 k-blocks, block kb + l in lane l
+      float wl = 0.f, wn = c0 < g.width && lane < nk ? __ldg(ws + lane * ws_step) : 0.f;
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        if ((kb & 31) == 0) {
+          wl = wn;
+          wn = c0 < g.width && kb + 32 + lane < nk ? __ldg(ws + int64_t(kb + 32 + lane) * ws_step) : 0.f;
+        }
+        const uint32_t buf = it & 1u, l = it % SLOTS;
+        const float w = __shfl_sync(0xFFFFFFFFu, wl, kb & 31);
+        float f = 0.f;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const uint32_t a = buf * UNITS + u;
+          ok = ok && mbar_wait(tfull_bar(int(a)), (it >> 1) & 1u, g.status, 35);
+          tc_fence_after();
+          if (u == 0) {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(my_scale + l * SLOT_BYTES) : "memory");
+            f *= w;
+          }
+#pragma unroll
+          for (int j = 0; j < PCOLS; j += 32) {
+            uint32_t r[32];
+            tmem_ld32(acc0 + a * UN + uint32_t(j), r);
+            if (j + 32 == PCOLS) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * a);
+            }
+            add_scaled<32>(acc + u * PCOLS + j, r, f);
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      // the warp's bf16 box of each unit, 64-byte swizzle: 16-byte word c of row r at word c ^ ((r >> 1) & 3)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float* v = acc + 32 * u + 8 * c + 2 * e;
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
+            o[e] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+          const uint32_t to = box + 64u * uint32_t(lane) + 16u * uint32_t(c ^ ((lane >> 1) & 3));
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+        }
+        const int cu = c0 + SEG * u;
+        if (g.tma_out) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && row0 < g.n && cu < g.width) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(&tmO)),
+                         "r"(cu), "r"(row0), "r"(box)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {  // rows that TMA cannot store: lane l writes column l of each
+          __syncwarp();
+          for (int r = 0; r < 32 && row0 + r < g.n; ++r) {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(v)
+                         : "r"(box + 64u * uint32_t(r) + 16u * uint32_t((lane >> 3) ^ ((r >> 1) & 3)) + 2u * uint32_t(lane & 7))
+                         : "memory");
+            if (cu + lane < g.width) g.out[int64_t(row0 + r) * g.ldo + cu + lane] = __ushort_as_bfloat16(v);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+
+// X's scales at a pitch whose rows bulk copies can read
+__global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x, int64_t ldx, int64_t n,
+                                                     float* __restrict__ out, int64_t ldo) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) out[int64_t(blockIdx.y) * ldo + i] = x[int64_t(blockIdx.y) * ldx + i];
+}
+
+// Clusters of two k_linear_pair CTAs that fit the device at once (cached per
+// device; half the SMs if the occupancy query fails)
+int pair_slots() {
+  static std::mutex mu;
+  static int cached[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / 2;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(2 * sm_count()));
+    cfg.blockDim = dim3(PAIR_THREADS);
+    cfg.dynamicSmemBytes = PAIR_SMEM;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear_pair<false>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+int launch_clusters(const void* kernel, int clusters, int size, int threads, int smem, void** args, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(size);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(clusters) * unsigned(size));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelExC(&cfg, kernel, args);
+  return check("bq_linear_fp8");
+}
+
 }  // namespace
 
 int launch_linear_fp8(const LinearArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (once_per_device(kOnceLinearAttr) &&
+      (cudaFuncSetAttribute(k_linear, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+       cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
+       cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess))
+    return check("bq_linear_fp8 (shared memory attribute)");
   const int width = a.transposed ? a.cols : a.rows, red = a.transposed ? a.rows : a.cols;
   LinArgs g;
   g.xs = a.x_scale, g.ws = a.w_scale, g.out = static_cast<__nv_bfloat16*>(a.out);
   g.ld_xs = a.ld_xs, g.ldo = a.ldo, g.n = int(a.n), g.width = width, g.red = red;
   g.tile_cols = (a.cols + 127) / 128, g.transposed = a.transposed, g.status = a.status;
-  g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
-  const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
+  g.split = 1, g.stages = 0, g.a_rows = BM, g.tma_out = 0;
   const int nk = (red + BK - 1) / BK;
+  CUtensorMap tx, tw, ts, to;
+  if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
+  const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
+  if (pairs > 0x7FFFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
+  if (pairs >= BQ_LINEAR_PAIR_MIN) {
+    if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
+    to = tx;  // (unused without tma_out)
+    if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
+      const int64_t ld = (a.n + 3) / 4 * 4;
+      k_copy_scales<<<dim3(unsigned((a.n + 255) / 256), unsigned(nk)), 256, 0, s>>>(a.x_scale, a.ld_xs, a.n, a.scale_ws, ld);
+      if (int rc = check("bq_linear_fp8 (scales)")) return rc;
+      g.xs = a.scale_ws, g.ld_xs = ld;
+    }
+    if (a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+      if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo)) return rc;
+      g.tma_out = 1;
+    }
+    if (int rc = encode_map_scales(&ts, g.xs, a.n, nk, g.ld_xs)) return rc;
+    void* args[] = {&tx, &tw, &ts, &to, &g};
+    const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
+                                 : reinterpret_cast<const void*>(k_linear_pair<false>);
+    return launch_clusters(k, int(std::min<int64_t>(pairs, pair_slots())), 2, PAIR_THREADS, PAIR_SMEM, args, s);
+  }
+  const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
   // two CTAs share an SM.  The X stages come last, and a product reads 128 rows of
   // the last one whatever it holds: what follows it is spare shared memory
+  g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
   const int stage = B_STAGE + g.a_rows * BK, spare = (BM - g.a_rows) * BK;
   const int part = BM * kPartPitch * 4;
   g.stages = std::min(kMaxStages, (kSmem - 1024 - spare) / stage);
   // k-blocks are split while the tiles leave resident CTAs idle and a share keeps
   // at least four
-  g.split = 1;
   while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk / (g.split * 2) >= 4) g.split *= 2;
-  CUtensorMap tx, tw;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
-  if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
   const int smem = 1024 + std::max(part, g.stages * stage + spare);
-  if (once_per_device(kOnceLinearAttr) &&
-      cudaFuncSetAttribute(k_linear, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-    return check("bq_linear_fp8 (shared memory attribute)");
-  if (tiles * g.split > 0x7FFFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(g.split);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(tiles * g.split));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = size_t(smem);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, k_linear, tx, tw, g) != cudaSuccess) return check("bq_linear_fp8");
-  return check("bq_linear_fp8");
+  void* args[] = {&tx, &tw, &g};
+  return launch_clusters(reinterpret_cast<const void*>(k_linear), int(tiles), g.split, THREADS, smem, args, s);
 }
 
 }  // namespace bq

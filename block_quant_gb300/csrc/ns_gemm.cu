@@ -71,6 +71,7 @@ struct GemmArgs {
   int a_sym;   // the A operand is such a symmetric result: its tiles below the stored ones are read transposed
   int b_sym;   // the same for a K-major B operand
   int a_mn = 0;  // the A operand is given transposed (MN-major) throughout
+  int band = 1 << 16;  // row blocks of a band of CTA-pair tiles (banded_tile)
 };
 
 // A symmetric result is stored as the 128 x 256 output tiles that touch its
@@ -350,7 +351,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
   const uint32_t rank = cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (g.M + PM - 1) / PM, ntiles = g.ntiles;
+  const int mt = (g.M + PM - 1) / PM, nt = (g.N + PM - 1) / PM, ntiles = g.ntiles;
+  const int band = min(g.band, mt);
   const int nk = (g.K + BK - 1) / BK;
   const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
   if (threadIdx.x == 0) {
@@ -375,7 +377,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
-      const int ma = (t % mt) * PM + 128 * int(rank), nb = (t / mt) * PM + 128 * int(rank);
+      int bm, bn;
+      banded_tile(t, mt, nt, band, bm, bn);
+      const int ma = bm * PM + 128 * int(rank), nb = bn * PM + 128 * int(rank);
       for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = int(it % STAGES2);
         if (!mbar_wait(empty_bar(s), ((it / STAGES2) & 1u) ^ 1u, g.status, 11)) {
@@ -404,7 +408,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t it = 0, tc = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
-      const int m0 = (t % mt) * PM;
+      int bm, bn;
+      banded_tile(t, mt, nt, band, bm, bn);
+      const int m0 = bm * PM;
       const int buf = int(tc & 1u);
       if (tc >= 2 && !mbar_wait_cluster(tempty_bar(buf), ((tc >> 1) & 1u) ^ 1u, g.status, 15)) break;
       tc_fence_after();
@@ -440,7 +446,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t te0 = map_rank(tempty_bar(0), 0), te1 = map_rank(tempty_bar(1), 0);
     uint32_t tc = 0;
     for (int t = pair; t < ntiles; t += npairs) {
-      const int m0 = (t % mt) * PM + 128 * int(rank), n0 = (t / mt) * PM;
+      int bm, bn;
+      banded_tile(t, mt, nt, band, bm, bn);
+      const int m0 = bm * PM + 128 * int(rank), n0 = bn * PM;
       const int buf = int(tc & 1u);
       const bool ok = mbar_wait(tfull_bar(buf), (tc >> 1) & 1u, g.status, 14);
       tc_fence_after();
@@ -971,6 +979,34 @@ int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, 
   return BQ_OK;
 }
 
+int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, int64_t pitch) {
+  EncodeTiled enc = encoder();
+  if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {cuuint64_t(n), cuuint64_t(groups)};
+  const cuuint64_t strides[1] = {cuuint64_t(pitch) * 4};
+  const cuuint32_t box[2] = {128u, 1u};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(BQ_EINVAL, "bq_linear_fp8: tensor map encoding failed (" + std::to_string(int(r)) + ")");
+  return BQ_OK;
+}
+
+int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch) {
+  EncodeTiled enc = encoder();
+  if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(pitch) * 2};
+  const cuuint32_t box[2] = {32u, 32u};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(BQ_EINVAL, "bq_linear_fp8: tensor map encoding failed (" + std::to_string(int(r)) + ")");
+  return BQ_OK;
+}
+
 // The weight gradient's product on the CTA pairs: A and B both MN-major, their
 // rows the summed index.  The pitches are multiples of 64 elements with the
 // padding allocated, which a 64-column chunk of the last columns reads.
@@ -982,6 +1018,7 @@ int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64
   auto* d = static_cast<__nv_bfloat16*>(D);
   GemmArgs g{m, n, int(t), 1.f, accumulate ? 1.f : 0.f, accumulate ? d : nullptr, d, ldd, ldd, status, 0, 0, 0, 0};
   g.a_mn = 1;
+  g.band = 8;
   return gemm_pair(ta, tb, ta, g, static_cast<cudaStream_t>(stream));
 }
 

@@ -39,21 +39,24 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 
-// dx: codes and scales of dy; dw: bf16 rows of X and, where dy's own pitch does not
-// serve, of dy
+// forward: X's scales, where their own pitch does not serve; dx: codes and scales of
+// dy; dw: bf16 rows of X and, where dy's own pitch does not serve, of dy
 struct LinearWs {
   size_t codes, scales, x, dy, bytes;
 };
+
+int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
 
 LinearWs linear_ws(int64_t n, int64_t rows, int64_t cols) {
   LinearWs p;
   p.codes = kStatusBytes;
   p.scales = p.codes + up(size_t(n) * size_t(up16(rows)));
-  const size_t dx = p.scales + up(size_t((rows + 127) / 128) * size_t(n) * 4);
+  const size_t dx = p.scales + up(size_t((rows + 127) / 128) * size_t(up4(n)) * 4);
+  const size_t fwd = kStatusBytes + up(size_t((cols + 127) / 128) * size_t(up4(n)) * 4);
   p.x = kStatusBytes;
   p.dy = p.x + up(size_t(n) * size_t(up64(cols)) * 2);
   const size_t dw = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
-  p.bytes = std::max(dx, dw);
+  p.bytes = std::max({dx, dw, fwd});
   return p;
 }
 
@@ -194,7 +197,7 @@ int bq_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t 
                   void* ws, size_t ws_bytes, bq_stream_t stream) {
   const char* who = "bq_linear_fp8";
   if (int rc = check_linear(who, n, rows, cols)) return rc;
-  if (int rc = check_ws(who, ws, ws_bytes, kStatusBytes)) return rc;
+  if (int rc = check_ws(who, ws, ws_bytes, linear_ws(n, rows, cols).bytes)) return rc;
   if (n == 0) return BQ_OK;
   ld_x = n == 1 ? std::max(up16(ld_x), cols) : ld_x;
   ld_out = pitch(ld_out, n, rows), ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
@@ -205,7 +208,8 @@ int bq_linear_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t 
   if (off(x, 16) || ld_x % 16) return fail(BQ_EALIGN, who, "codes must be 16-byte aligned with a pitch multiple of 16");
   if (off(x_scale, 4) || off(out, 2)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
   return launch_linear_fp8(LinearArgs{x, x_scale, w, w_scale, out, ld_x, ld_scale, ld_w, ld_out, n, int(rows), int(cols),
-                                      0, static_cast<int*>(ws)},
+                                      0, static_cast<int*>(ws),
+                                      reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + kStatusBytes)},
                            stream);
 }
 
@@ -226,10 +230,10 @@ int bq_linear_fp8_dx(const void* dy, int64_t ld_dy, const uint8_t* w, int64_t ld
   auto* base = static_cast<unsigned char*>(ws);
   auto* codes = base + p.codes;
   auto* scales = reinterpret_cast<float*>(base + p.scales);
-  const int64_t ldc = up16(rows);
-  if (int rc = launch_quant_rows(dy, ld_dy, n, int(rows), codes, ldc, scales, n, stream)) return rc;
-  return launch_linear_fp8(LinearArgs{codes, scales, w, w_scale, dx, ldc, n, ld_w, ld_dx, n, int(rows), int(cols), 1,
-                                      static_cast<int*>(ws)},
+  const int64_t ldc = up16(rows), lds = up4(n);
+  if (int rc = launch_quant_rows(dy, ld_dy, n, int(rows), codes, ldc, scales, lds, stream)) return rc;
+  return launch_linear_fp8(LinearArgs{codes, scales, w, w_scale, dx, ldc, lds, ld_w, ld_dx, n, int(rows), int(cols), 1,
+                                      static_cast<int*>(ws), nullptr},
                            stream);
 }
 

@@ -67,6 +67,8 @@ struct LinearArgs {
   int rows, cols;
   int transposed;        // 0: out = x W^T (red = cols); 1: out = x W (red = rows)
   int* status;
+  float* scale_ws;       // room for x_scale at a pitch of n + 3 at most (not used if x_scale is 16-byte
+                         // aligned and ld_xs a multiple of 4)
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 

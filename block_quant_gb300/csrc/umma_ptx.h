@@ -35,8 +35,20 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // bounded wait: false (and an error word) when the phase does not complete
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* status, int code) {
+  if (mbar_try(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t it = 0;; ++it) {
     if (mbar_try(bar, parity)) return true;
@@ -148,6 +160,38 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same arrival and wait without memory ordering at cluster scope (a release
+// there waits for all of the warp's outstanding accesses, about a thousand cycles):
+// for barriers that hand over tensor memory alone, whose accesses are ordered by
+// tcgen05.wait and the tcgen05 fences on either side.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_cluster_relaxed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster_relaxed(uint32_t bar, uint32_t parity, int* status, int code) {
+  if (mbar_try_cluster_relaxed(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_cluster_relaxed(bar, parity)) return true;
+    if ((it & 255) == 255 && clock64() - t0 > kWaitCycles) {
+      if (status) atomicExch(status, code);
+      return false;
+    }
+  }
+}
+
 // a box into this CTA's shared memory, its bytes completed on `cluster_bar`
 // (a barrier of either CTA of the pair)
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -197,6 +241,16 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncol
 
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Tile t of mt x nt output tiles, walked in bands of `band` row blocks, a band's
+// columns one after another and the rows of a column fastest: consecutive tiles, which
+// run at the same time, share few row and few column blocks of the operands.
+__device__ __forceinline__ void banded_tile(int t, int mt, int nt, int band, int& bm, int& bn) {
+  const int b = t / (band * nt), r = t - b * band * nt;
+  const int rows = min(band, mt - b * band);
+  bn = r / rows;
+  bm = b * band + (r - bn * rows);
 }
 
 }  // namespace bq

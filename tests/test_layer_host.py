@@ -139,7 +139,7 @@ REFUSED = [
     (_quant, dict(x=None), INV), (_quant, dict(codes=None), INV), (_quant, dict(scale=None), INV),
     (_quant, dict(ldc=4), INV), (_quant, dict(scale=P + 1), ALIGN),
     (_lin, dict(x=None), INV), (_lin, dict(w=None), INV), (_lin, dict(ws_=None), INV), (_lin, dict(out=None), INV),
-    (_lin, dict(ws=None), INV), (_lin, dict(wb=128), SPACE), (_lin, dict(ws=P + 128), ALIGN), (_lin, dict(x=P + 8), ALIGN),
+    (_lin, dict(ws=None), INV), (_lin, dict(wb=128), SPACE), (_lin, dict(wb=256), SPACE), (_lin, dict(ws=P + 128), ALIGN), (_lin, dict(x=P + 8), ALIGN),
     (_lin, dict(w=P + 8), ALIGN), (_lin, dict(ldx=40), ALIGN), (_lin, dict(ldw=40), ALIGN),
     (_lin, dict(cols=24), ALIGN), (_lin, dict(ldx=16), INV), (_lin, dict(ldo=8), INV),
     (_lin, dict(cols=144, ldx=144, ldw=144, lds=3), INV), (_lin, dict(rows=(1 << 24) + 1, ldo=1 << 25), INV),
