@@ -11,6 +11,7 @@ torch's current stream on the current device.
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -30,7 +31,7 @@ SYMBOLS = [
     "bq_group_place", "bq_group_upload_bytes", "bq_group_upload",
     "bq_embed", "bq_embed_grad_workspace", "bq_embed_grad", "bq_rmsnorm", "bq_rmsnorm_grad_workspace",
     "bq_rmsnorm_grad", "bq_quant_rows_fp8", "bq_linear_fp8_workspace", "bq_linear_fp8", "bq_linear_fp8_dx",
-    "bq_linear_fp8_dw", "bq_linear_check",
+    "bq_linear_fp8_dw", "bq_linear_check", "bq_call",
 ]
 
 
@@ -134,6 +135,7 @@ def load():
     lib.bq_linear_fp8_dx.argtypes = [P, L, P, L, P, L, L, L, P, L, P, S, P]
     lib.bq_linear_fp8_dw.argtypes = [P, L, P, L, P, L, L, L, L, P, L, I, P, S, P]
     lib.bq_linear_check.argtypes = [P, S, P]
+    lib.bq_call.argtypes = [I, C.c_char_p]
     for name in SYMBOLS:
         if name not in ("bq_strerror", "bq_last_error", "bq_layout_free", "bq_shard_free"):
             getattr(lib, name).restype = C.c_int
@@ -155,11 +157,24 @@ def _ptr(x):
     return int(x.data_ptr())
 
 
+def _current_stream():
+    """torch's current stream on the current device, by the short way where torch has it."""
+    global _current_stream
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    now = torch.cuda.current_stream().cuda_stream  # (also brings CUDA up)
+    if raw is not None and device is not None and raw(device()) == now:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return now
+
+
 def _stream(s):
     if s is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)
@@ -396,50 +411,81 @@ def muon_ns_noalloc(mats, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, stre
 # Matrices are 2-D torch tensors on the GPU whose last dimension is contiguous (a
 # row pitch is read off the tensor); 1-D tensors are contiguous.  Outputs are the
 # caller's, as everywhere.  Shapes and types are checked here, the rest by the
-# library.
+# library.  The calls go through bq_call, their arguments packed into one string of
+# 64-bit words: a generated token's norm costs a few microseconds in all, of which
+# ctypes' conversion of twenty arguments would be two.
 
-_KINDS = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
-          "torch.uint8": ROWS_FP8}
+_KIND_NAMES = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
+               "torch.uint8": ROWS_FP8}
+_KINDS = {}  # torch dtype -> kind, filled as types are met
 
 
 def _refuse(msg):
     raise BQError(BQ_EINVAL, f"invalid argument: {msg}")
 
 
+def _kind(name, x):
+    d = getattr(x, "dtype", None)
+    k = _KINDS.get(d)
+    if k is None:
+        k = _KIND_NAMES.get(str(d))
+        if k is None:
+            _refuse(f"{name} has type {d}")
+        _KINDS[d] = k
+    return k
+
+
 def _mat2(name, x, kinds, rows=None, cols=None):
     """(pointer, row pitch, rows, cols, kind) of a matrix."""
     if x is None:
         _refuse(f"{name} is None")
-    kind = _KINDS.get(str(x.dtype))
+    kind = _kind(name, x)
     if kind not in kinds:
         _refuse(f"{name} has type {x.dtype}")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         _refuse(f"{name} must be a matrix")
-    r, c = x.shape
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
-        _refuse(f"{name} is {r} x {c}, expected {rows if rows is not None else 'any'} x {cols if cols is not None else 'any'}")
+        _refuse(f"{name} is {r} x {c}, expected {'any' if rows is None else rows} x {'any' if cols is None else cols}")
     ld, step = x.stride()
     if step != 1 and c > 1:
         _refuse(f"{name}'s rows must be contiguous")
     return x.data_ptr(), ld, r, c, kind
 
 
-def _vec(name, x, kinds, n=None):
-    """(pointer, length, kind) of a contiguous vector."""
+def _rows(name, x, rows, cols):
+    """(pointer, row pitch) of a bf16 matrix of that shape; (0, 0) for None."""
+    if x is None:
+        return 0, 0
+    return _mat2(name, x, (ROWS_BF16,), rows, cols)[:2]
+
+
+def _vec(name, x, kinds, n):
+    """(pointer, kind) of a contiguous vector of n."""
     if x is None:
         _refuse(f"{name} is None")
-    kind = _KINDS.get(str(x.dtype))
+    kind = _kind(name, x)
     if kind not in kinds:
         _refuse(f"{name} has type {x.dtype}")
-    if x.dim() != 1 or (n is not None and x.shape[0] != n) or (x.shape[0] > 1 and x.stride(0) != 1):
-        _refuse(f"{name} must be a contiguous vector" + (f" of {n}" if n is not None else ""))
-    return x.data_ptr(), x.shape[0], kind
+    if x.shape != (n,) or not x.is_contiguous():
+        _refuse(f"{name} must be a contiguous vector of {n}")
+    return x.data_ptr(), kind
+
+
+_ID_BITS = {}
 
 
 def _ids(ids):
-    bits = {"torch.int32": 32, "torch.int64": 64}.get(str(ids.dtype))
-    if bits is None or ids.dim() != 1 or (ids.shape[0] > 1 and ids.stride(0) != 1):
-        _refuse("ids must be a contiguous int32 or int64 vector")
+    d = getattr(ids, "dtype", None)
+    bits = _ID_BITS.get(d)
+    if bits is None:
+        bits = {"torch.int32": 32, "torch.int64": 64}.get(str(d))
+        if bits is None:
+            _refuse(f"ids have type {d}")
+        _ID_BITS[d] = bits
+    if len(ids.shape) != 1 or not ids.is_contiguous():
+        _refuse("ids must be a contiguous vector")
     return ids.data_ptr(), bits, ids.shape[0]
 
 
@@ -447,13 +493,25 @@ def _tile_scale(name, s, rows, cols):
     """Pointer of an FP8 weight's tile scales, [ceil(rows/128), ceil(cols/128)] or flat, contiguous."""
     if s is None:
         _refuse(f"{name} is None")
-    if str(s.dtype) != "torch.float32" or not s.is_contiguous() or s.numel() != -(-rows // 128) * -(-cols // 128):
+    if _kind(name, s) != ROWS_FP32 or not s.is_contiguous() or s.numel() != -(-rows // 128) * -(-cols // 128):
         _refuse(f"{name} must hold one contiguous fp32 scale per 128 x 128 tile of {rows} x {cols}")
     return s.data_ptr()
 
 
 def _ws(ws):
-    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+# bq_call's numbers and the layout of their arguments (q: integer or pointer, d: double)
+_CALLS = [struct.Struct(f).pack for f in (
+    "9qd3q", "5qd9q", "5qd12q", "18q", "9q", "15q", "13q", "15q")]
+CALL_EMBED, CALL_EMBED_GRAD, CALL_RMSNORM, CALL_RMSNORM_GRAD, CALL_QUANT, CALL_LINEAR, CALL_DX, CALL_DW = range(8)
+
+
+def _call(op, *args):
+    rc = load().bq_call(op, _CALLS[op](*args))
+    if rc != BQ_OK:
+        _check(rc)
 
 
 def embed(table, ids, out, scale=1.0, table_scale=None, stream=None):
@@ -461,9 +519,9 @@ def embed(table, ids, out, scale=1.0, table_scale=None, stream=None):
     (one fp32 scale per 128 x 128 tile).  An id outside the table gives a zero row."""
     tp, ld, rows, cols, kind = _mat2("table", table, (ROWS_BF16, ROWS_FP8))
     ip, bits, n = _ids(ids)
-    op, ldo, _, _, _ = _mat2("out", out, (ROWS_BF16,), n, cols)
-    sp = _tile_scale("table_scale", table_scale, rows, cols) if kind == ROWS_FP8 else None
-    _check(load().bq_embed(tp, kind, sp, rows, cols, ld, ip, bits, n, float(scale), op, ldo, _stream(stream)))
+    op, ldo = _mat2("out", out, (ROWS_BF16,), n, cols)[:2]
+    sp = _tile_scale("table_scale", table_scale, rows, cols) if kind == ROWS_FP8 else 0
+    _call(CALL_EMBED, tp, kind, sp, rows, cols, ld, ip, bits, n, scale, op, ldo, _stream(stream))
 
 
 def embed_grad_workspace(n, rows, cols):
@@ -477,15 +535,14 @@ def embed_grad(dy, ids, out, ws, scale=1.0, accumulate=False, stream=None):
     written (accumulate: added to the rows that tokens name); out bf16 or fp32."""
     ip, bits, n = _ids(ids)
     op, ldo, rows, cols, kind = _mat2("out", out, (ROWS_BF16, ROWS_FP32))
-    dp, ldd, _, _, _ = _mat2("dy", dy, (ROWS_BF16,), n, cols)
-    wp, wb = _ws(ws)
-    _check(load().bq_embed_grad(dp, ldd, ip, bits, n, float(scale), rows, cols, op, kind, ldo, int(bool(accumulate)),
-                                wp, wb, _stream(stream)))
+    dp, ldd = _mat2("dy", dy, (ROWS_BF16,), n, cols)[:2]
+    _call(CALL_EMBED_GRAD, dp, ldd, ip, bits, n, scale, rows, cols, op, kind, ldo, bool(accumulate), *_ws(ws),
+          _stream(stream))
 
 
 def _code_rows(name, codes, code_scale, n, cols):
-    cp, ldc, _, _, _ = _mat2(name, codes, (ROWS_FP8,), n, cols)
-    sp, lds, _, _, _ = _mat2(f"{name}'s scale", code_scale, (ROWS_FP32,), -(-cols // 128), n)
+    cp, ldc = _mat2(name, codes, (ROWS_FP8,), n, cols)[:2]
+    sp, lds = _mat2(f"{name}'s scale", code_scale, (ROWS_FP32,), -(-cols // 128), n)[:2]
     return cp, ldc, sp, lds
 
 
@@ -494,14 +551,13 @@ def rmsnorm(x, weight, eps, residual=None, h=None, y=None, codes=None, code_scal
     (needed with a residual), y in bf16, codes with code_scale [ceil(cols/128), n] (FP8
     rows of y), rstd (fp32, n)."""
     xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
-    wp, _, _ = _vec("weight", weight, (ROWS_BF16,), cols)
-    rp, ldr = _mat2("residual", residual, (ROWS_BF16,), n, cols)[:2] if residual is not None else (None, 0)
-    hp, ldh = _mat2("h", h, (ROWS_BF16,), n, cols)[:2] if h is not None else (None, 0)
-    yp, ldy = _mat2("y", y, (ROWS_BF16,), n, cols)[:2] if y is not None else (None, 0)
-    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols) if codes is not None else (None, 0, None, 0)
-    qp = _vec("rstd", rstd, (ROWS_FP32,), n)[0] if rstd is not None else None
-    _check(load().bq_rmsnorm(xp, ldx, rp, ldr, wp, float(eps), n, cols, hp, ldh, yp, ldy, cp, ldc, sp, lds, qp,
-                             _stream(stream)))
+    wp = _vec("weight", weight, (ROWS_BF16,), cols)[0]
+    rp, ldr = _rows("residual", residual, n, cols)
+    hp, ldh = _rows("h", h, n, cols)
+    yp, ldy = _rows("y", y, n, cols)
+    cp, ldc, sp, lds = (0, 0, 0, 0) if codes is None else _code_rows("codes", codes, code_scale, n, cols)
+    qp = 0 if rstd is None else _vec("rstd", rstd, (ROWS_FP32,), n)[0]
+    _call(CALL_RMSNORM, xp, ldx, rp, ldr, wp, eps, n, cols, hp, ldh, yp, ldy, cp, ldc, sp, lds, qp, _stream(stream))
 
 
 def rmsnorm_grad_workspace(n, cols):
@@ -515,21 +571,19 @@ def rmsnorm_grad(dy, h, weight, rstd, dx, dw, ws, dh=None, accumulate=False, str
     dw (bf16 or fp32; accumulate: added to it) from dy and the forward's h and rstd."""
     hp, ldh, n, cols, _ = _mat2("h", h, (ROWS_BF16,))
     yp, ldy = _mat2("dy", dy, (ROWS_BF16,), n, cols)[:2]
-    wp, _, _ = _vec("weight", weight, (ROWS_BF16,), cols)
+    wp = _vec("weight", weight, (ROWS_BF16,), cols)[0]
     qp = _vec("rstd", rstd, (ROWS_FP32,), n)[0]
-    gp, ldg = _mat2("dh", dh, (ROWS_BF16,), n, cols)[:2] if dh is not None else (None, 0)
+    gp, ldg = _rows("dh", dh, n, cols)
     xp, ldx = _mat2("dx", dx, (ROWS_BF16,), n, cols)[:2]
-    dp, _, kind = _vec("dw", dw, (ROWS_BF16, ROWS_FP32), cols)
-    sp, sb = _ws(ws)
-    _check(load().bq_rmsnorm_grad(yp, ldy, hp, ldh, wp, qp, gp, ldg, n, cols, xp, ldx, dp, kind, int(bool(accumulate)),
-                                  sp, sb, _stream(stream)))
+    dp, kind = _vec("dw", dw, (ROWS_BF16, ROWS_FP32), cols)
+    _call(CALL_RMSNORM_GRAD, yp, ldy, hp, ldh, wp, qp, gp, ldg, n, cols, xp, ldx, dp, kind, bool(accumulate), *_ws(ws),
+          _stream(stream))
 
 
 def quant_rows_fp8(x, codes, code_scale, stream=None):
     """FP8 rows of a bf16 matrix: codes, and code_scale [ceil(cols/128), n]."""
     xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
-    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
-    _check(load().bq_quant_rows_fp8(xp, ldx, n, cols, cp, ldc, sp, lds, _stream(stream)))
+    _call(CALL_QUANT, xp, ldx, n, cols, *_code_rows("codes", codes, code_scale, n, cols), _stream(stream))
 
 
 def linear_fp8_workspace(n, rows, cols):
@@ -545,32 +599,25 @@ def linear_fp8(codes, code_scale, w, w_scale, out, ws, stream=None):
     weight [rows, cols] with its tile scales."""
     wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
     n = codes.shape[0]
-    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
-    op, ldo = _mat2("out", out, (ROWS_BF16,), n, rows)[:2]
-    tp = _tile_scale("w_scale", w_scale, rows, cols)
-    bp, bb = _ws(ws)
-    _check(load().bq_linear_fp8(cp, ldc, sp, lds, wp, ldw, tp, n, rows, cols, op, ldo, bp, bb, _stream(stream)))
+    _call(CALL_LINEAR, *_code_rows("codes", codes, code_scale, n, cols), wp, ldw,
+          _tile_scale("w_scale", w_scale, rows, cols), n, rows, cols, *_mat2("out", out, (ROWS_BF16,), n, rows)[:2],
+          *_ws(ws), _stream(stream))
 
 
 def linear_fp8_dx(dy, w, w_scale, dx, ws, stream=None):
     """dx [n, cols] = Q W: Q the FP8 rows of dy [n, rows] (quantised in the call)."""
     wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
     yp, ldy, n, _, _ = _mat2("dy", dy, (ROWS_BF16,), None, rows)
-    xp, ldx = _mat2("dx", dx, (ROWS_BF16,), n, cols)[:2]
-    tp = _tile_scale("w_scale", w_scale, rows, cols)
-    bp, bb = _ws(ws)
-    _check(load().bq_linear_fp8_dx(yp, ldy, wp, ldw, tp, n, rows, cols, xp, ldx, bp, bb, _stream(stream)))
+    _call(CALL_DX, yp, ldy, wp, ldw, _tile_scale("w_scale", w_scale, rows, cols), n, rows, cols,
+          *_mat2("dx", dx, (ROWS_BF16,), n, cols)[:2], *_ws(ws), _stream(stream))
 
 
 def linear_fp8_dw(dy, codes, code_scale, dw, ws, accumulate=False, stream=None):
     """dw [rows, cols] = dy^T X (accumulate: added to dw), X the forward's FP8 rows."""
     yp, ldy, n, rows, _ = _mat2("dy", dy, (ROWS_BF16,))
     cols = codes.shape[1]
-    cp, ldc, sp, lds = _code_rows("codes", codes, code_scale, n, cols)
-    dp, ldd = _mat2("dw", dw, (ROWS_BF16,), rows, cols)[:2]
-    bp, bb = _ws(ws)
-    _check(load().bq_linear_fp8_dw(yp, ldy, cp, ldc, sp, lds, n, rows, cols, dp, ldd, int(bool(accumulate)), bp, bb,
-                                   _stream(stream)))
+    _call(CALL_DW, yp, ldy, *_code_rows("codes", codes, code_scale, n, cols), n, rows, cols,
+          *_mat2("dw", dw, (ROWS_BF16,), rows, cols)[:2], bool(accumulate), *_ws(ws), _stream(stream))
 
 
 def linear_check(ws, stream=None):

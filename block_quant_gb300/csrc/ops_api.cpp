@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "bq_internal.h"
 #include "row_ops.h"
@@ -285,6 +286,49 @@ int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream) {
   if (e != cudaSuccess) return fail(BQ_ECUDA, "bq_linear_check", cudaGetErrorString(e));
   if (status) return set_error(BQ_ECUDA, "bq_linear_fp8: a device wait timed out (site " + std::to_string(status) + ")");
   return BQ_OK;
+}
+
+int bq_call(int op, const void* args) {
+  if (!args) return fail(BQ_EINVAL, "bq_call", "NULL argument");
+  const unsigned char* at = static_cast<const unsigned char*>(args);
+  auto q = [&](int i) {
+    int64_t v;
+    std::memcpy(&v, at + 8 * i, 8);
+    return v;
+  };
+  auto f = [&](int i) {
+    double v;
+    std::memcpy(&v, at + 8 * i, 8);
+    return float(v);
+  };
+  auto p = [&](int i) { return reinterpret_cast<void*>(intptr_t(q(i))); };
+  auto b = [&](int i) { return static_cast<uint8_t*>(p(i)); };
+  auto s = [&](int i) { return static_cast<float*>(p(i)); };
+  auto st = [&](int i) { return static_cast<bq_stream_t>(p(i)); };
+  switch (op) {
+    case BQ_CALL_EMBED:
+      return bq_embed(p(0), int(q(1)), s(2), q(3), q(4), q(5), p(6), int(q(7)), q(8), f(9), p(10), q(11), st(12));
+    case BQ_CALL_EMBED_GRAD:
+      return bq_embed_grad(p(0), q(1), p(2), int(q(3)), q(4), f(5), q(6), q(7), p(8), int(q(9)), q(10), int(q(11)),
+                           p(12), size_t(q(13)), st(14));
+    case BQ_CALL_RMSNORM:
+      return bq_rmsnorm(p(0), q(1), p(2), q(3), p(4), f(5), q(6), q(7), p(8), q(9), p(10), q(11), b(12), q(13), s(14),
+                        q(15), s(16), st(17));
+    case BQ_CALL_RMSNORM_GRAD:
+      return bq_rmsnorm_grad(p(0), q(1), p(2), q(3), p(4), s(5), p(6), q(7), q(8), q(9), p(10), q(11), p(12),
+                             int(q(13)), int(q(14)), p(15), size_t(q(16)), st(17));
+    case BQ_CALL_QUANT_ROWS:
+      return bq_quant_rows_fp8(p(0), q(1), q(2), q(3), b(4), q(5), s(6), q(7), st(8));
+    case BQ_CALL_LINEAR:
+      return bq_linear_fp8(b(0), q(1), s(2), q(3), b(4), q(5), s(6), q(7), q(8), q(9), p(10), q(11), p(12),
+                           size_t(q(13)), st(14));
+    case BQ_CALL_LINEAR_DX:
+      return bq_linear_fp8_dx(p(0), q(1), b(2), q(3), s(4), q(5), q(6), q(7), p(8), q(9), p(10), size_t(q(11)), st(12));
+    case BQ_CALL_LINEAR_DW:
+      return bq_linear_fp8_dw(p(0), q(1), b(2), q(3), s(4), q(5), q(6), q(7), q(8), p(9), q(10), int(q(11)), p(12),
+                              size_t(q(13)), st(14));
+    default: return fail(BQ_EINVAL, "bq_call", "unknown call");
+  }
 }
 
 }  // extern "C"

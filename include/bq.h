@@ -500,6 +500,22 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
  * cleared and BQ_ECUDA returned (also on a CUDA error). */
 int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream);
 
+/* bq_call - one of the layer operators' calls with its arguments, in the order of its
+ * declaration, packed as 64-bit words: integers and pointers as int64, fp32 values as
+ * double.  For bindings that pay for every argument they convert: the result is that
+ * of the call itself.  BQ_EINVAL: unknown op or NULL args. */
+enum {
+  BQ_CALL_EMBED = 0,
+  BQ_CALL_EMBED_GRAD = 1,
+  BQ_CALL_RMSNORM = 2,
+  BQ_CALL_RMSNORM_GRAD = 3,
+  BQ_CALL_QUANT_ROWS = 4,
+  BQ_CALL_LINEAR = 5,
+  BQ_CALL_LINEAR_DX = 6,
+  BQ_CALL_LINEAR_DW = 7
+};
+int bq_call(int op, const void* args);
+
 #ifdef __cplusplus
 }
 #endif
