@@ -100,7 +100,7 @@ int bq_embed(const void* table, int kind, const float* table_scale, int64_t rows
 int bq_embed_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
   if (!bytes) return fail(BQ_EINVAL, "bq_embed_grad_workspace", "NULL argument");
   if (int rc = check_sizes("bq_embed_grad_workspace", n, rows, cols)) return rc;
-  *bytes = embed_grad_bytes(n, cols);
+  *bytes = embed_grad_bytes(n, rows, cols);
   return BQ_OK;
 }
 
@@ -116,7 +116,7 @@ int bq_embed_grad(const void* dy, int64_t ld_dy, const void* ids, int id_bits, i
   if (ld_dy < cols || ld_out < cols) return fail(BQ_EINVAL, who, "pitch below cols");
   if (off(dy, 2) || off(out, out_kind == BQ_ROWS_FP32 ? 4 : 2) || off(ids, uintptr_t(id_bits / 8)))
     return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
-  if (int rc = check_ws(who, ws, ws_bytes, embed_grad_bytes(n, cols))) return rc;
+  if (int rc = check_ws(who, ws, ws_bytes, embed_grad_bytes(n, rows, cols))) return rc;
   if (n == 0 && accumulate) return BQ_OK;
   return launch_embed_grad(EmbedGradArgs{dy, ids, out, ld_dy, n, rows, ld_out, scale, int(cols), id_bits, out_kind,
                                          accumulate ? 1 : 0},

@@ -2,8 +2,8 @@
 //   k_embed          rows of the token table (bf16, or E4M3 codes with 128x128
 //                    tile scales as the AllGather leaves them) times a factor
 //   k_embed_sort     stable sort of a batch's tokens by id (one cluster)
-//   k_embed_pieces,  the table's gradient: rows of dY summed over equal ids
-//   k_embed_rows
+//   k_embed_rows,    the table's gradient: rows of dY summed over equal ids, zeros
+//   k_embed_join     for the other rows
 //   k_norm*          residual addition, root-mean-square norm, E4M3 codes with
 //                    one scale per 128 values of a row (also without the norm:
 //                    the row quantiser)
@@ -100,6 +100,25 @@ __device__ __forceinline__ void load_bf16(const __nv_bfloat16* row, int c0, int 
       v[e] = c < cols ? __bfloat162float(row[c]) : 0.f;
     }
   }
+}
+
+// the same, eight bf16 packed as loaded
+template <bool VEC>
+__device__ __forceinline__ uint4 load_packed(const __nv_bfloat16* row, int c0, int cols, int lane) {
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  if (VEC) {
+    const int c = c0 + 8 * lane;
+    if (c < cols) w = *reinterpret_cast<const uint4*>(row + c);
+  } else {
+    uint32_t u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = c0 + 32 * e + lane;
+      u[e] = c < cols ? uint32_t(__bfloat16_as_ushort(row[c])) : 0u;
+    }
+    w = make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+  }
+  return w;
 }
 
 template <bool VEC>
@@ -218,6 +237,10 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int bits, int64_t i)
   return bits == 64 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
 }
 
+// A kernel launched by launch_after() may start while its predecessor on the stream
+// still runs (its launch is hidden); this waits until that has completed.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- embedding lookup
 
 constexpr int kRowWarps = 8;
@@ -277,28 +300,34 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 // A stable least-significant-digit radix sort of (id, position) in one launch: a
 // cluster of eight CTAs, each owning a contiguous eighth of the tokens.  Per
 // digit: CTA histograms, exchanged through distributed shared memory and scanned
-// by every CTA; then ranks in token order, 1024 x kSortKeys tokens a round, by
-// warp match and per-warp counters; the pairs go to the other buffer, which the
-// cluster barrier makes visible.  Ids outside [0, rows) become `rows` (last).
-constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = 32, kSortKeys = 4;
+// by every CTA; then ranks in token order, 1024 x KEYS tokens a round, by warp match
+// and per-warp counters; the pairs go to the other buffer, which the cluster barrier
+// makes visible.  Ids outside [0, rows) become `rows` (last).  One launch of a cluster
+// instead of a device-wide sort: at the token counts of a training step the passes are
+// bound by latency (8192 tokens, 17 bits: two passes).
+// touched (NULL: not wanted): a bit per row that some token names.
+constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = 32;
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 
 struct SortSmem {
-  uint32_t hist[kBins];              // this CTA's count of every digit (read by the whole cluster)
-  uint32_t base[kBins];              // where this CTA's next token of a digit goes
-  uint32_t round[kBins];             // a round's count of every digit
+  uint32_t hist[kBins];               // this CTA's count of every digit (read by the whole cluster)
+  uint32_t base[kBins];               // where this CTA's next token of a digit goes
+  uint32_t half[2][kBins];            // a round's count of every digit in warps 0-15, 16-31
   uint32_t warp_sum[kSortWarps];
   uint16_t count[kSortWarps][kBins];  // a round's counts, then offsets, by warp
 };
 
+template <int KEYS>
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1, 1)
     k_embed_sort(const void* __restrict__ ids, int id_bits, int n, int rows, int passes, uint2* __restrict__ buf0,
-                 uint2* __restrict__ buf1) {
+                 uint2* __restrict__ buf1, uint32_t* __restrict__ touched) {
   __shared__ SortSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = int(cluster_rank());
   const int seg = (n + kSortCtas - 1) / kSortCtas;
   const int lo = min(n, rank * seg), hi = min(n, lo + seg);
+  if (touched)
+    for (int i = rank * kSortThreads + tid; i < (rows >> 5) + 1; i += kSortCtas * kSortThreads) touched[i] = 0;
   for (int p = 0; p < passes; ++p) {
     const uint2* src = (p & 1) ? buf1 : buf0;  // pass 0 reads the ids themselves
     uint2* dst = (p & 1) ? buf0 : buf1;
@@ -311,17 +340,25 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
     if (tid < kBins) sm.hist[tid] = 0;
     __syncthreads();
     for (int i = lo + tid; i < hi; i += kSortThreads) atomicAdd(&sm.hist[(key_at(i).x >> shift) & (kBins - 1)], 1u);
+    if (p == 0) __threadfence();  // the cleared bits
     cluster_sync();
+    if (p == 0 && touched)
+      for (int i = lo + tid; i < hi; i += kSortThreads) {
+        const uint32_t v = key_at(i).x;
+        atomicOr(touched + (v >> 5), 1u << (v & 31));  // (bit `rows`: no row)
+      }
     // exclusive scan over (digit, CTA): thread d < kBins holds digit d
     uint32_t before = 0, total = 0;
     if (tid < kBins) {
       const uint32_t at = smem_addr(&sm.hist[tid]);
+      uint32_t h[kSortCtas];
+#pragma unroll
+      for (int c = 0; c < kSortCtas; ++c)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h[c]) : "r"(map_rank(at, uint32_t(c))) : "memory");
 #pragma unroll
       for (int c = 0; c < kSortCtas; ++c) {
-        uint32_t h;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(h) : "r"(map_rank(at, uint32_t(c))) : "memory");
-        if (c < rank) before += h;
-        total += h;
+        if (c < rank) before += h[c];
+        total += h[c];
       }
     }
     uint32_t x = total;
@@ -333,24 +370,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
     if (lane == 31) sm.warp_sum[warp] = x;
     __syncthreads();
     if (tid < kBins) {
-      uint32_t prior = 0;
-      for (int w = 0; w < warp; ++w) prior += sm.warp_sum[w];
+      uint32_t prior = lane < warp ? sm.warp_sum[lane] : 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) prior += __shfl_xor_sync(0xFFFFFFFFu, prior, o);
       sm.base[tid] = prior + x - total + before;
     }
     // ranks, in token order
-    for (int r0 = lo; r0 < hi; r0 += kSortThreads * kSortKeys) {
-      for (int i = tid; i < kSortWarps * kBins / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(sm.count)[i] = 0;
-      __syncthreads();
-      uint2 kv[kSortKeys];
-      uint32_t off[kSortKeys];
-      const int w0 = r0 + warp * 32 * kSortKeys;
+    for (int r0 = lo; r0 < hi; r0 += kSortThreads * KEYS) {
+      uint4* clear = reinterpret_cast<uint4*>(sm.count);
+      for (int i = tid; i < kSortWarps * kBins / 8; i += kSortThreads) clear[i] = make_uint4(0u, 0u, 0u, 0u);
+      uint2 kv[KEYS];
+      uint32_t off[KEYS];
+      const int w0 = r0 + warp * 32 * KEYS;
 #pragma unroll
-      for (int j = 0; j < kSortKeys; ++j) {
+      for (int j = 0; j < KEYS; ++j) {
         const int i = w0 + 32 * j + lane;
         if (i < hi) kv[j] = key_at(i);
       }
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kSortKeys; ++j) {
+      for (int j = 0; j < KEYS; ++j) {
         const bool on = w0 + 32 * j + lane < hi;
         const uint32_t d = on ? (kv[j].x >> shift) & (kBins - 1) : kBins;
         const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
@@ -363,24 +402,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
         off[j] = prior + below;
       }
       __syncthreads();
-      if (tid < kBins) {  // counts -> offsets of each warp inside the round
-        uint32_t run = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-          const uint32_t c = sm.count[w][tid];
-          sm.count[w][tid] = uint16_t(run);
-          run += c;
+      {  // counts -> offsets of each warp within its half of the warps
+        const int d = tid & (kBins - 1), h = tid >> kDigit;
+        uint32_t c[kSortWarps / 2], run = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps / 2; ++w) c[w] = sm.count[h * (kSortWarps / 2) + w][d];
+#pragma unroll
+        for (int w = 0; w < kSortWarps / 2; ++w) {
+          sm.count[h * (kSortWarps / 2) + w][d] = uint16_t(run);
+          run += c[w];
         }
-        sm.round[tid] = run;
+        sm.half[h][d] = run;
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kSortKeys; ++j) {
+      for (int j = 0; j < KEYS; ++j) {
         if (w0 + 32 * j + lane >= hi) continue;
         const uint32_t d = (kv[j].x >> shift) & (kBins - 1);
-        dst[sm.base[d] + sm.count[warp][d] + off[j]] = kv[j];
+        dst[sm.base[d] + (warp >= kSortWarps / 2 ? sm.half[0][d] : 0u) + sm.count[warp][d] + off[j]] = kv[j];
       }
       __syncthreads();
-      if (tid < kBins) sm.base[tid] += sm.round[tid];
+      if (tid < kBins) sm.base[tid] += sm.half[0][tid] + sm.half[1][tid];
     }
     __threadfence();
     cluster_sync();  // the next pass reads other CTAs' pairs; their histograms are done being read
@@ -390,138 +432,137 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
 // ---------------------------------------------------------------- embedding gradient
 
 // dT[v] (+)= f * sum of dY[t] over the tokens t of id v, summed in fp32 in token
-// order.  The sorted tokens are cut into pieces of kPiece: a run of equal ids
-// inside one piece is summed where its row is written (k_embed_rows); a run that
-// crosses a piece's end is summed piece by piece first (k_embed_pieces), so a
-// token that fills the batch is shared out over the whole GPU, and its row adds
-// the pieces' sums in order.  No atomics: the same batch gives the same bits.
-// Sum slot of a piece: 2c if its run begins at or before piece c's first token,
-// 2c + 1 if it begins inside.
-constexpr int kPiece = 32;
+// order.  The sorted tokens are cut into pieces of kPiece.  A run of equal ids inside
+// one piece is summed and its row written by the piece's CTA; of a run that crosses a
+// piece's end each piece's part is summed first, so that a token that fills the batch
+// is shared out over the whole GPU, and k_embed_join adds the parts in order.  No
+// atomics on values: the same batch gives the same bits.  Rows that no token names
+// (most of the table) are written as zeros by the same launch.
+// Slot of a piece's part: 2c for the one that starts with piece c, 2c + 1 otherwise.
+constexpr int kPiece = 32, kBatch = 8;   // tokens of a piece; rows of dY in flight
+constexpr int kZeroBytes = 16384;        // zeros a CTA writes, in address order: 7.6 TB/s (1 MB a CTA: 6.4)
 
-// sum of rows dY[pos[i]] over i in [b, e), one span
-template <bool VEC>
-__device__ __forceinline__ void sum_rows(const __nv_bfloat16* __restrict__ dy, int64_t ld, const uint32_t* pos, int b,
-                                         int e, int c0, int cols, int lane, float* acc) {
-  int i = b;
-  for (; i + 4 <= e; i += 4) {
-    float v[4][8];
+template <bool VEC, typename Out>
+__device__ __forceinline__ void write_sum(Out* row, int c0, int cols, int lane, float scale, int accumulate, float* acc) {
+  if (accumulate) {
+    float old[8];
+    load_row<VEC>(row, c0, cols, lane, old);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load_bf16<VEC>(dy + int64_t(pos[i + k]) * ld, c0, cols, lane, v[k]);
+    for (int x = 0; x < 8; ++x) acc[x] = fmaf(scale, acc[x], old[x]);
+  } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[k][x]);
+    for (int x = 0; x < 8; ++x) acc[x] = __fmul_rn(scale, acc[x]);
   }
-  for (; i < e; ++i) {
-    float v[8];
-    load_bf16<VEC>(dy + int64_t(pos[i]) * ld, c0, cols, lane, v);
-#pragma unroll
-    for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
-  }
+  store_row<VEC>(row, c0, cols, lane, acc);
 }
 
-// blockIdx.x: piece; blockIdx.y: group of kPieceWarps spans
-constexpr int kPieceWarps = 4;
-template <bool VEC>
-__global__ void __launch_bounds__(32 * kPieceWarps)
-    k_embed_pieces(const uint2* __restrict__ sorted, int n, int rows, const __nv_bfloat16* __restrict__ dy, int64_t ld,
-                   int cols, float* __restrict__ sums, int ldp) {
+struct EmbedRows {
+  const uint2* sorted;
+  const uint32_t* touched;
+  const __nv_bfloat16* dy;
+  float* sums;            // [2 pieces][ldp]
+  int64_t ld, rows, ldo;
+  int n, cols, ldp, accumulate;
+  int groups;             // CTAs of a piece: kRowWarps spans each
+  int piece_ctas, zero_rows;  // CTAs of pieces (they come first); rows of a zero CTA
+  float scale;
+};
+
+template <bool VEC, typename Out>
+__global__ void __launch_bounds__(32 * kRowWarps, 4) k_embed_rows(const EmbedRows a, Out* __restrict__ out) {
   __shared__ uint32_t key[kPiece + 2], pos[kPiece];  // key[1 + i]: token i of the piece; 0, len + 1: its neighbours
-  const int b = blockIdx.x * kPiece, len = min(kPiece, n - b);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
+  after_previous();
+  if (int(blockIdx.x) >= a.piece_ctas) {
+    // zeros
+    constexpr int V = VEC ? 16 / int(sizeof(Out)) : 1;
+    const int64_t v0 = int64_t(int(blockIdx.x) - a.piece_ctas) * a.zero_rows;
+    const int count = int(min(int64_t(a.zero_rows), a.rows - v0)), per = a.cols / V;
+    for (int i = tid; i < count * per; i += 32 * kRowWarps) {
+      const int r = i / per;
+      const int64_t v = v0 + r;
+      if (a.n > 0 && (__ldg(a.touched + (v >> 5)) >> (v & 31)) & 1u) continue;
+      Out* o = out + v * a.ldo + int64_t(i - r * per) * V;
+      if (VEC)
+        *reinterpret_cast<uint4*>(o) = make_uint4(0u, 0u, 0u, 0u);
+      else
+        *o = Out(0.f);
+    }
+    return;
+  }
+  const int piece = int(blockIdx.x) / a.groups;
+  const int b = piece * kPiece, len = min(kPiece, a.n - b);
   if (tid < len + 2) {
     const int i = b + tid - 1;
-    const uint2 kv = i >= 0 && i < n ? sorted[i] : make_uint2(0xFFFFFFFFu, 0u);
+    const uint2 kv = i >= 0 && i < a.n ? a.sorted[i] : make_uint2(0xFFFFFFFFu, 0u);
     key[tid] = kv.x;
     if (tid >= 1 && tid <= len) pos[tid - 1] = kv.y;
   }
   __syncthreads();
-  const uint32_t first = key[1], last = key[len];
-  const bool from = key[0] == first, to = key[len + 1] == last;
-  const int lane = tid & 31, c0 = (int(blockIdx.y) * kPieceWarps + (tid >> 5)) * kSpan;
-  if (c0 >= cols) return;
-  int head = 0, tail = len;  // [0, head) and [tail, len) are pieces of runs that cross the ends
-  if (from || (to && first == last)) {
-    while (head < len && key[1 + head] == first) ++head;
-  }
-  if (to && head < len) {
-    while (tail > head && key[tail] == last) --tail;
-  }
-  if (head > 0 && first < uint32_t(rows)) {
-    float acc[8] = {};
-    sum_rows<VEC>(dy, ld, pos, 0, head, c0, cols, lane, acc);
-    store_f32<true>(sums + int64_t(2 * blockIdx.x) * ldp, c0, ldp, lane, acc);
-  }
-  if (tail < len && last < uint32_t(rows)) {
-    float acc[8] = {};
-    sum_rows<VEC>(dy, ld, pos, tail, len, c0, cols, lane, acc);
-    store_f32<true>(sums + int64_t(2 * blockIdx.x + 1) * ldp, c0, ldp, lane, acc);
+  const int c0 = ((int(blockIdx.x) - piece * a.groups) * kRowWarps + (tid >> 5)) * kSpan;
+  if (c0 >= a.cols) return;
+  float acc[8] = {};
+  int start = 0;  // first token of the run being summed
+  for (int i0 = 0; i0 < len; i0 += kBatch) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k < len) w[k] = load_packed<VEC>(a.dy + int64_t(pos[i0 + k]) * a.ld, c0, a.cols, lane);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k;
+      if (i >= len) continue;
+      float v[8];
+      unpack8(w[k], v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
+      const uint32_t id = key[1 + i];
+      if (i + 1 < len && key[2 + i] == id) continue;
+      // the run (or this piece's part of it) ends here
+      if (id < uint32_t(a.rows)) {
+        const bool whole = (start > 0 || key[0] != id) && (i + 1 < len || key[len + 1] != id);
+        if (whole)
+          write_sum<VEC>(out + int64_t(id) * a.ldo, c0, a.cols, lane, a.scale, a.accumulate, acc);
+        else  // (a slot's values lie as the lanes hold them: VEC or not, its reader holds the same)
+          store_f32<true>(a.sums + int64_t(2 * piece + (start > 0 ? 1 : 0)) * a.ldp, c0, a.ldp, lane, acc);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+      start = i + 1;
+    }
   }
 }
 
-// a CTA writes kTableRows rows of the table's gradient
-constexpr int kTableRows = 64;
+// rows whose run begins in piece blockIdx.x / groups and goes on past its end
 template <bool VEC, typename Out>
-__global__ void __launch_bounds__(32 * kRowWarps)
-    k_embed_rows(const uint2* __restrict__ sorted, int n, int64_t rows, const __nv_bfloat16* __restrict__ dy,
-                 int64_t ld, int cols, const float* __restrict__ sums, int ldp, float scale, int accumulate,
-                 Out* __restrict__ out, int64_t ldo) {
-  __shared__ int first[kTableRows + 1];  // first sorted token of each row
-  __shared__ uint32_t pos[kRowWarps][kPiece];
-  const int64_t v0 = int64_t(blockIdx.x) * kTableRows;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid <= kTableRows) {
-    const uint32_t v = uint32_t(min(v0 + tid, rows));
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sorted[mid].x < v)
-        lo = mid + 1;
-      else
-        hi = mid;
+__global__ void __launch_bounds__(32 * kRowWarps) k_embed_join(const EmbedRows a, Out* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int piece = int(blockIdx.x) / a.groups, b = piece * kPiece, e = b + kPiece;
+  after_previous();
+  if (e >= a.n) return;
+  const uint32_t id = a.sorted[e - 1].x;
+  if (a.sorted[e].x != id || id >= uint32_t(a.rows)) return;
+  const bool from_start = a.sorted[b].x == id;
+  if (from_start && b > 0 && a.sorted[b - 1].x == id) return;  // it began in an earlier piece
+  const int c0 = ((int(blockIdx.x) - piece * a.groups) * kRowWarps + int(threadIdx.x >> 5)) * kSpan;
+  if (c0 >= a.cols) return;
+  float acc[8];
+  load_f32<true>(a.sums + int64_t(2 * piece + (from_start ? 0 : 1)) * a.ldp, c0, a.ldp, lane, acc);
+  // the pieces after it that start with the same id, 32 at a time
+  for (int p = piece + 1;; p += 32) {
+    const int at = (p + lane) * kPiece;
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < a.n && a.sorted[at].x == id);
+    const int count = same == 0xFFFFFFFFu ? 32 : __ffs(int(~same)) - 1;
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+      float v[8];
+      load_f32<true>(a.sums + int64_t(2 * (p + k)) * a.ldp, c0, a.ldp, lane, v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
     }
-    first[tid] = lo;
+    if (count < 32) break;
   }
-  __syncthreads();
-  const int spans = (cols + kSpan - 1) / kSpan;
-  const int count = int(min(int64_t(kTableRows), rows - v0));
-  for (int item = warp; item < count * spans; item += kRowWarps) {
-    const int r = item / spans, c0 = (item - r * spans) * kSpan;
-    const int b = first[r], e = first[r + 1];
-    if (b == e && accumulate) continue;
-    float acc[8] = {};
-    if (b < e) {
-      const int p0 = b / kPiece, p1 = (e - 1) / kPiece;
-      if (p0 == p1) {
-        __syncwarp();
-        if (lane < e - b) pos[warp][lane] = sorted[b + lane].y;
-        __syncwarp();
-        sum_rows<VEC>(dy, ld, pos[warp], 0, e - b, c0, cols, lane, acc);
-      } else {
-        for (int p = p0; p <= p1; ++p) {
-          const int slot = p == p0 && b % kPiece != 0 ? 2 * p + 1 : 2 * p;
-          float v[8];
-          load_f32<true>(sums + int64_t(slot) * ldp, c0, ldp, lane, v);
-          // the sums' rows hold whole spans: lane l has columns 8l .. 8l + 7 of
-          // the span, or what column() gives where the span was summed unaligned
-#pragma unroll
-          for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
-        }
-      }
-    }
-    Out* row = out + (v0 + r) * ldo;
-    if (accumulate) {
-      float old[8];
-      load_row<VEC>(row, c0, cols, lane, old);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) acc[x] = fmaf(scale, acc[x], old[x]);
-    } else {
-#pragma unroll
-      for (int x = 0; x < 8; ++x) acc[x] = __fmul_rn(scale, acc[x]);
-    }
-    store_row<VEC>(row, c0, cols, lane, acc);
-  }
+  write_sum<VEC>(out + int64_t(id) * a.ldo, c0, a.cols, lane, a.scale, a.accumulate, acc);
 }
 
 // ---------------------------------------------------------------- norm
@@ -582,18 +623,125 @@ __global__ void __launch_bounds__(row_threads(VPT)) k_norm(const NormArgs a) {
   }
 }
 
+// 16 bytes into shared memory without a register (zeros where !on)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n groups of this thread's copies have landed
+__device__ __forceinline__ void copy_wait(int n) {
+  switch (n) {
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+  return w;
+}
+
+// Many rows: resident CTAs walk the rows blockIdx.x, + gridDim.x, ..., each thread
+// copying its own vectors of the next `depth` - 1 rows into a ring in shared memory, so
+// that loads are in flight while a row waits for its sum (with a CTA per row they are
+// not).  A thread reads only what it copied: no barrier but the sum's.
+template <int VPT>
+__global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_many(const NormArgs a, int64_t n, int depth) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float part[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int ins = a.res ? 2 : 1;
+  const uint32_t step = blockDim.x * 16u;                    // one vector of every thread
+  const uint32_t row_bytes = uint32_t(ins) * VPT * step;     // a slot of the ring
+  const uint32_t mine = smem_addr(ring) + threadIdx.x * 16u;
+  uint4 w[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) w[i] = load_packed<true>(a.w, (warp + i * warps) * kSpan, a.cols, lane);
+  auto fetch = [&](int64_t t, int slot) {
+    if (t < n) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (warp + i * warps) * kSpan + 8 * lane;
+        const bool on = c < a.cols;
+        const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
+        copy16(at, a.x + t * a.ldx + (on ? c : 0), on);
+        if (a.res) copy16(at + VPT * step, a.res + t * a.ldr + (on ? c : 0), on);
+      }
+    }
+    copy_commit();
+  };
+  int64_t next = blockIdx.x;
+  for (int s = 0; s + 1 < depth; ++s, next += gridDim.x) fetch(next, s);
+  int slot = 0, flip = 0;
+  for (int64_t t = blockIdx.x; t < n; t += gridDim.x, next += gridDim.x, flip ^= 1) {
+    fetch(next, slot == 0 ? depth - 1 : slot - 1);  // the slot read last
+    copy_wait(depth - 1);
+    float h[VPT][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
+      unpack8(shared16(at), h[i]);
+      if (a.res) {
+        float r[8];
+        unpack8(shared16(at + VPT * step), r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] + r[e];
+        const uint4 b = pack8(h[i]);
+        unpack8(b, h[i]);
+        const int c = (warp + i * warps) * kSpan + 8 * lane;
+        if (c < a.cols) *reinterpret_cast<uint4*>(a.h + t * a.ldh + c) = b;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    }
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    ss = warp_sum(ss);
+    if (lane == 0) part[flip][warp] = ss;
+    __syncthreads();
+    ss = warp_sum(lane < warps ? part[flip][lane] : 0.f);
+    const float rstd = rsqrtf(__fadd_rn(__fdiv_rn(ss, float(a.cols)), a.eps));
+    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c0 = (warp + i * warps) * kSpan;
+      if (c0 >= a.cols) break;
+      float g[8];
+      unpack8(w[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = __fmul_rn(__fmul_rn(h[i][e], rstd), g[e]);
+      if (a.y) store_bf16<true>(a.y + t * a.ldy, c0, a.cols, lane, h[i]);
+      if (a.codes) quant_span<true>(h[i], c0, a.cols, lane, a.codes + t * a.ldc, a.scale + t, a.lds);
+    }
+  }
+}
+
+// a warp quantises kSpans spans of a row
 template <bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_quant_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, uint8_t* __restrict__ codes,
-                 int64_t ldc, float* __restrict__ scale, int64_t lds, int spans) {
+                 int64_t ldc, float* __restrict__ scale, int64_t lds, int segs) {
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int64_t t = item / spans;
+  const int64_t t = item / segs;
   if (t >= n) return;
-  const int c0 = int(item - t * spans) * kSpan;
-  float v[8];
-  load_bf16<VEC>(x + t * ldx, c0, cols, lane, v);
-  quant_span<VEC>(v, c0, cols, lane, codes + t * ldc, scale + t, lds);
+  const int c0 = int(item - t * segs) * kSeg;
+  uint4 w[kSpans];
+#pragma unroll
+  for (int j = 0; j < kSpans; ++j) w[j] = load_packed<VEC>(x + t * ldx, c0 + kSpan * j, cols, lane);
+#pragma unroll
+  for (int j = 0; j < kSpans; ++j) {
+    if (c0 + kSpan * j >= cols) break;
+    float v[8];
+    unpack8(w[j], v);
+    quant_span<VEC>(v, c0 + kSpan * j, cols, lane, codes + t * ldc, scale + t, lds);
+  }
 }
 
 // bf16(scale * code) of E4M3 rows with one scale per 128 values, pitch ldo (for the
@@ -690,38 +838,130 @@ __global__ void __launch_bounds__(row_threads(VPT)) k_norm_grad(const NormGradAr
   }
 }
 
-// dw = sum of the CTAs' parts in order: 32 columns x 8 runs of parts a CTA
+// the same with the rows to come copied into a ring, as k_norm_many
+template <int VPT>
+__global__ void __launch_bounds__(1024, 1) k_norm_grad_many(const NormGradArgs a, int depth) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float part[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int ins = a.dh ? 3 : 2;
+  const uint32_t step = blockDim.x * 16u;
+  const uint32_t row_bytes = uint32_t(ins) * VPT * step;
+  const uint32_t mine = smem_addr(ring) + threadIdx.x * 16u;
+  uint4 w[VPT];
+  float dw[VPT][8] = {};
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) w[i] = load_packed<true>(a.w, (warp + i * warps) * kSpan, a.cols, lane);
+  auto fetch = [&](int64_t t, int slot) {
+    if (t < a.n) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (warp + i * warps) * kSpan + 8 * lane;
+        const bool on = c < a.cols;
+        const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
+        copy16(at, a.dy + t * a.ld_dy + (on ? c : 0), on);
+        copy16(at + VPT * step, a.h + t * a.ld_h + (on ? c : 0), on);
+        if (a.dh) copy16(at + 2 * VPT * step, a.dh + t * a.ld_dh + (on ? c : 0), on);
+      }
+    }
+    copy_commit();
+  };
+  int64_t next = blockIdx.x;
+  for (int s = 0; s + 1 < depth; ++s, next += gridDim.x) fetch(next, s);
+  int slot = 0, flip = 0;
+  float rnext = a.rstd[blockIdx.x];
+  for (int64_t t = blockIdx.x; t < a.n; t += gridDim.x, next += gridDim.x, flip ^= 1) {
+    const float rstd = rnext;
+    if (t + gridDim.x < a.n) rnext = a.rstd[t + gridDim.x];
+    copy_wait(depth - 2);
+    float dy[VPT][8], u[VPT][8];
+    uint4 g[VPT];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
+      unpack8(shared16(at), dy[i]);
+      unpack8(shared16(at + VPT * step), u[i]);
+      g[i] = a.dh ? shared16(at + 2 * VPT * step) : make_uint4(0u, 0u, 0u, 0u);
+      float f[8];
+      unpack8(w[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[i][e] *= rstd;
+        dw[i][e] = fmaf(dy[i][e], u[i][e], dw[i][e]);
+        dy[i][e] *= f[e];
+        dot = fmaf(dy[i][e], u[i][e], dot);
+      }
+    }
+    fetch(next, slot == 0 ? depth - 1 : slot - 1);  // the slot read a row ago
+    slot = slot + 1 == depth ? 0 : slot + 1;
+    dot = warp_sum(dot);
+    if (lane == 0) part[flip][warp] = dot;
+    __syncthreads();
+    dot = warp_sum(lane < warps ? part[flip][lane] : 0.f) / float(a.cols);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c0 = (warp + i * warps) * kSpan;
+      float o[8];
+      unpack8(g[i], o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(rstd, fmaf(-dot, u[i][e], dy[i][e]), o[e]);
+      store_bf16<true>(a.dx + t * a.ld_dx, c0, a.cols, lane, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c0 = (warp + i * warps) * kSpan;
+    if (c0 < a.cols) store_f32<true>(a.part + int64_t(blockIdx.x) * a.ldp, c0, a.cols, lane, dw[i]);
+  }
+}
+
+// dw = sum of the CTAs' parts in a fixed order: 32 columns a CTA, every 32nd part a warp
 template <typename Out>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     k_norm_dw(const float* __restrict__ part, int parts, int ldp, int cols, int accumulate, Out* __restrict__ dw) {
-  __shared__ float run[8][32];
+  __shared__ float run[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  after_previous();
   float s = 0.f;
   if (c < cols) {
-    const int per = (parts + 7) / 8, b = warp * per, e = min(parts, b + per);
 #pragma unroll 8
-    for (int p = b; p < e; ++p) s += part[int64_t(p) * ldp + c];
+    for (int p = warp; p < parts; p += 32) s += part[int64_t(p) * ldp + c];
   }
   run[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += run[k][lane];
+  s = warp_sum(run[lane][warp]);  // warp w: column w of the CTA's
+  const int o = blockIdx.x * 32 + warp;
+  if (lane == 0 && o < cols) {
     if (sizeof(Out) == 2) {
-      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(dw);
-      if (accumulate) s += __bfloat162float(o[c]);
-      o[c] = __float2bfloat16_rn(s);
+      __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(dw);
+      if (accumulate) s += __bfloat162float(d[o]);
+      d[o] = __float2bfloat16_rn(s);
     } else {
-      float* o = reinterpret_cast<float*>(dw);
-      if (accumulate) s += o[c];
-      o[c] = s;
+      float* d = reinterpret_cast<float*>(dw);
+      if (accumulate) s += d[o];
+      d[o] = s;
     }
   }
 }
 
 // ---------------------------------------------------------------- host
+
+template <typename... Params, typename... Args>
+int launch_after(const char* what, void (*kernel)(Params...), unsigned ctas, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+  return check(what);
+}
 
 bool vec_ok(const void* p, int64_t ld, int values) { return aligned16(p) && ld % values == 0; }
 
@@ -740,24 +980,70 @@ int bits_of(int64_t x) {
 }
 
 struct EmbedGradPlan {
-  size_t off_b0, off_b1, off_sums, bytes;
+  size_t off_b0, off_b1, off_touched, off_sums, bytes;
   int ldp, pieces;
 };
 
-EmbedGradPlan embed_grad_plan(int64_t n, int64_t cols) {
+EmbedGradPlan embed_grad_plan(int64_t n, int64_t rows, int64_t cols) {
   EmbedGradPlan p;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p.ldp = int((cols + kSpan - 1) / kSpan * kSpan);
   p.pieces = int((n + kPiece - 1) / kPiece);
   p.off_b0 = 0;
   p.off_b1 = up(size_t(n) * 8);
-  p.off_sums = p.off_b1 + up(size_t(n) * 8);
+  p.off_touched = p.off_b1 + up(size_t(n) * 8);
+  p.off_sums = p.off_touched + up((size_t(rows) / 32 + 1) * 4);
   p.bytes = p.off_sums + up(size_t(p.pieces) * 2 * size_t(p.ldp) * 4);
-  if (p.bytes == 0) p.bytes = 256;
   return p;
 }
 
-int norm_grad_ctas(int64_t n) { return int(std::min<int64_t>(n, int64_t(sm_count()) * 2)); }
+// The ring of a kernel whose resident CTAs walk many rows: slots (0: it does not fit,
+// or there are too few rows for it) and CTAs an SM, for `warps` warps a CTA and
+// row_bytes of shared memory a row.  A CTA's barrier stalls it once a row, so an SM runs
+// up to eight of them, within 1024 threads (64 registers each).
+struct Ring {
+  int depth, per_sm;
+};
+
+constexpr int kRingBytes = 224 * 1024, kMaxDepth = 8;
+
+Ring ring_of(int warps, int row_bytes, int64_t n) {
+  Ring r;
+  r.per_sm = std::max(1, std::min(8, 32 / warps));
+  r.depth = std::min(kMaxDepth, (kRingBytes / r.per_sm - 1024) / row_bytes);
+  if (r.depth < 3 || n < int64_t(2) * r.per_sm * sm_count()) r.depth = 0;
+  return r;
+}
+
+struct NormGradPlan {
+  int ctas, warps, vpt, depth, smem;
+};
+
+// vec: every row of the operands is 16-byte aligned and of whole vectors.  The direct
+// kernel takes what the ring does not; ctas is the larger of the two where vec is not
+// known yet (a workspace's size).
+NormGradPlan norm_grad_plan(int64_t n, int cols, int ins, bool vec) {
+  NormGradPlan p;
+  const int spans = (cols + kSpan - 1) / kSpan;
+  p.vpt = spans <= 32 ? 1 : 2;
+  p.warps = (spans + p.vpt - 1) / p.vpt;
+  p.depth = 0;
+  if (vec && p.warps <= 32) {
+    const int row = ins * p.vpt * p.warps * 512;
+    const Ring r = ring_of(p.warps, row, n);
+    if (r.depth) {
+      p.depth = r.depth, p.smem = r.depth * row;
+      // as few CTAs as give every one the same number of rows, or one less
+      const int64_t most = int64_t(sm_count()) * r.per_sm, each = (n + most - 1) / most;
+      p.ctas = int((n + each - 1) / each);
+      return p;
+    }
+  }
+  row_shape(cols, &p.warps, &p.vpt);
+  p.smem = 0;
+  p.ctas = int(std::min<int64_t>(n, int64_t(sm_count()) * 2));
+  return p;
+}
 
 }  // namespace
 
@@ -774,41 +1060,71 @@ int launch_embed(const EmbedArgs& a, void* stream) {
   return check("bq_embed");
 }
 
-size_t embed_grad_bytes(int64_t n, int64_t cols) { return embed_grad_plan(n, cols).bytes; }
+size_t embed_grad_bytes(int64_t n, int64_t rows, int64_t cols) { return embed_grad_plan(n, rows, cols).bytes; }
 
-int launch_embed_grad(const EmbedGradArgs& a, void* ws, void* stream) {
+namespace {
+
+template <bool VEC, typename Out>
+int embed_rows(const EmbedRows& a, unsigned zero_ctas, int pieces, Out* out, cudaStream_t s) {
+  const unsigned ctas = unsigned(a.piece_ctas) + zero_ctas;
+  if (int rc = launch_after("bq_embed_grad (rows)", k_embed_rows<VEC, Out>, ctas, 32 * kRowWarps, s, a, out)) return rc;
+  if (pieces < 2) return BQ_OK;  // no run crosses a piece's end
+  return launch_after("bq_embed_grad (join)", k_embed_join<VEC, Out>, unsigned(a.piece_ctas), 32 * kRowWarps, s, a, out);
+}
+
+}  // namespace
+
+int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const EmbedGradPlan p = embed_grad_plan(a.n, a.cols);
+  const EmbedGradPlan p = embed_grad_plan(g.n, g.rows, g.cols);
   auto* w = static_cast<unsigned char*>(ws);
   auto* b0 = reinterpret_cast<uint2*>(w + p.off_b0);
   auto* b1 = reinterpret_cast<uint2*>(w + p.off_b1);
-  auto* sums = reinterpret_cast<float*>(w + p.off_sums);
-  const auto* dy = static_cast<const __nv_bfloat16*>(a.dy);
-  const int n = int(a.n);
-  const bool f32 = a.out_kind == BQ_ROWS_FP32;
-  const bool vec = a.cols % 8 == 0 && vec_ok(a.dy, a.ld_dy, 8) && vec_ok(a.out, a.ldo, f32 ? 4 : 8);
-  const int passes = (bits_of(a.rows) + kDigit - 1) / kDigit;
-  const uint2* sorted = (passes & 1) ? b1 : b0;
-  if (n > 0) {
-    k_embed_sort<<<kSortCtas, kSortThreads, 0, s>>>(a.ids, a.id_bits, n, int(a.rows), passes, b0, b1);
+  auto* touched = reinterpret_cast<uint32_t*>(w + p.off_touched);
+  const bool f32 = g.out_kind == BQ_ROWS_FP32;
+  const bool vec = g.cols % 8 == 0 && vec_ok(g.dy, g.ld_dy, 8) && vec_ok(g.out, g.ldo, f32 ? 4 : 8);
+  const int passes = (bits_of(g.rows) + kDigit - 1) / kDigit;
+  EmbedRows a;
+  a.sorted = (passes & 1) ? b1 : b0;
+  a.touched = touched;
+  a.dy = static_cast<const __nv_bfloat16*>(g.dy);
+  a.sums = reinterpret_cast<float*>(w + p.off_sums);
+  a.ld = g.ld_dy, a.rows = g.rows, a.ldo = g.ldo, a.n = int(g.n), a.cols = g.cols, a.ldp = p.ldp;
+  a.accumulate = g.accumulate, a.scale = g.scale;
+  a.groups = (g.cols + kRowWarps * kSpan - 1) / (kRowWarps * kSpan);
+  if (int64_t(p.pieces) * a.groups > 0x3FFFFFFF) return set_error(BQ_EINVAL, "bq_embed_grad: batch too large");
+  a.piece_ctas = p.pieces * a.groups;
+  a.zero_rows = std::max(1, kZeroBytes / (g.cols * (f32 ? 4 : 2)));
+  const unsigned zero_ctas = g.accumulate ? 0u : unsigned((g.rows + a.zero_rows - 1) / a.zero_rows);
+  if (g.n > 0) {
+    auto* k = g.n <= kSortCtas * kSortThreads ? k_embed_sort<1> : k_embed_sort<4>;
+    k<<<kSortCtas, kSortThreads, 0, s>>>(g.ids, g.id_bits, a.n, int(g.rows), passes, b0, b1,
+                                         g.accumulate ? nullptr : touched);
     if (int rc = check("bq_embed_grad (sort)")) return rc;
-    const dim3 g(unsigned(p.pieces), unsigned((a.cols + kPieceWarps * kSpan - 1) / (kPieceWarps * kSpan)));
-    auto* kp = vec ? k_embed_pieces<true> : k_embed_pieces<false>;
-    kp<<<g, 32 * kPieceWarps, 0, s>>>(sorted, n, int(a.rows), dy, a.ld_dy, a.cols, sums, p.ldp);
-    if (int rc = check("bq_embed_grad (pieces)")) return rc;
   }
-  const unsigned ctas = unsigned((a.rows + kTableRows - 1) / kTableRows);
   if (f32) {
-    auto* k = vec ? k_embed_rows<true, float> : k_embed_rows<false, float>;
-    k<<<ctas, 32 * kRowWarps, 0, s>>>(sorted, n, a.rows, dy, a.ld_dy, a.cols, sums, p.ldp, a.scale, a.accumulate,
-                                      static_cast<float*>(a.out), a.ldo);
-  } else {
-    auto* k = vec ? k_embed_rows<true, __nv_bfloat16> : k_embed_rows<false, __nv_bfloat16>;
-    k<<<ctas, 32 * kRowWarps, 0, s>>>(sorted, n, a.rows, dy, a.ld_dy, a.cols, sums, p.ldp, a.scale, a.accumulate,
-                                      static_cast<__nv_bfloat16*>(a.out), a.ldo);
+    auto* out = static_cast<float*>(g.out);
+    return vec ? embed_rows<true>(a, zero_ctas, p.pieces, out, s) : embed_rows<false>(a, zero_ctas, p.pieces, out, s);
   }
-  return check("bq_embed_grad (rows)");
+  auto* out = static_cast<__nv_bfloat16*>(g.out);
+  return vec ? embed_rows<true>(a, zero_ctas, p.pieces, out, s) : embed_rows<false>(a, zero_ctas, p.pieces, out, s);
 }
+
+namespace {
+
+// the ring kernels' shared-memory attribute, set once per device
+int ring_attrs() {
+  if (!once_per_device(kOnceRingAttr)) return BQ_OK;
+  const void* kernels[] = {reinterpret_cast<const void*>(k_norm_many<2>), reinterpret_cast<const void*>(k_norm_many<4>),
+                           reinterpret_cast<const void*>(k_norm_grad_many<1>),
+                           reinterpret_cast<const void*>(k_norm_grad_many<2>)};
+  for (const void* k : kernels)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+      return check("bq_rmsnorm (shared memory attribute)");
+  return BQ_OK;
+}
+
+}  // namespace
 
 int launch_rmsnorm(const RmsnormArgs& r, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -826,6 +1142,17 @@ int launch_rmsnorm(const RmsnormArgs& r, void* stream) {
                    (!r.codes || ((reinterpret_cast<uintptr_t>(r.codes) & 7) == 0 && r.ld_codes % 8 == 0));
   int warps, vpt;
   row_shape(r.cols, &warps, &vpt);
+  if (vec && vpt <= 4) {
+    const int row = (r.residual ? 2 : 1) * vpt * warps * 512;
+    const Ring ring = ring_of(warps, row, r.n);
+    if (ring.depth) {
+      auto* many = vpt == 2 ? k_norm_many<2> : k_norm_many<4>;
+      if (int rc = ring_attrs()) return rc;
+      const int64_t most = int64_t(sm_count()) * ring.per_sm, each = (r.n + most - 1) / most;
+      many<<<unsigned((r.n + each - 1) / each), 32 * warps, ring.depth * row, s>>>(a, r.n, ring.depth);
+      return check("bq_rmsnorm");
+    }
+  }
   auto* k = vec ? (vpt == 2 ? k_norm<true, 2> : vpt == 4 ? k_norm<true, 4> : k_norm<true, 8>)
                 : (vpt == 2 ? k_norm<false, 2> : vpt == 4 ? k_norm<false, 4> : k_norm<false, 8>);
   k<<<unsigned(r.n), 32 * warps, 0, s>>>(a);
@@ -836,11 +1163,11 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
                       int64_t lds, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = cols % 8 == 0 && vec_ok(x, ldx, 8) && (reinterpret_cast<uintptr_t>(codes) & 7) == 0 && ldc % 8 == 0;
-  const int spans = (cols + kSpan - 1) / kSpan;
-  const int64_t ctas = (n * spans + kRowWarps - 1) / kRowWarps;
+  const int segs = (cols + kSeg - 1) / kSeg;
+  const int64_t ctas = (n * segs + kRowWarps - 1) / kRowWarps;
   auto* k = vec ? k_quant_rows<true> : k_quant_rows<false>;
   k<<<unsigned(ctas), 32 * kRowWarps, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc, scale, lds,
-                                              spans);
+                                              segs);
   return check("bq_quant_rows_fp8");
 }
 
@@ -863,7 +1190,10 @@ int launch_copy_rows(const void* x, int64_t ldx, int64_t n, int cols, void* out,
 
 size_t rmsnorm_grad_bytes(int64_t n, int64_t cols) {
   const size_t ldp = size_t((cols + kSpan - 1) / kSpan * kSpan);
-  return std::max<size_t>(256, size_t(norm_grad_ctas(n)) * ldp * 4);
+  // the ring takes the most CTAs with the fewest operands; the direct kernel may have more
+  int ctas = norm_grad_plan(n, int(cols), 2, false).ctas;
+  for (int ins = 2; ins <= 3; ++ins) ctas = std::max(ctas, norm_grad_plan(n, int(cols), ins, true).ctas);
+  return std::max<size_t>(256, size_t(ctas) * ldp * 4);
 }
 
 int launch_rmsnorm_grad(const RmsnormGradArgs& r, void* ws, void* stream) {
@@ -878,23 +1208,26 @@ int launch_rmsnorm_grad(const RmsnormGradArgs& r, void* ws, void* stream) {
   a.part = static_cast<float*>(ws);
   a.ld_dy = r.ld_dy, a.ld_h = r.ld_h, a.ld_dh = r.ld_dh, a.ld_dx = r.ld_dx, a.n = r.n;
   a.cols = r.cols, a.ldp = (r.cols + kSpan - 1) / kSpan * kSpan;
-  const int ctas = norm_grad_ctas(r.n);
-  if (ctas > 0) {
-    const bool vec = r.cols % 8 == 0 && vec_ok(r.dy, r.ld_dy, 8) && vec_ok(r.h, r.ld_h, 8) && aligned16(r.weight) &&
-                     (!r.dh || vec_ok(r.dh, r.ld_dh, 8)) && vec_ok(r.dx, r.ld_dx, 8);
-    int warps, vpt;
-    row_shape(r.cols, &warps, &vpt);
-    auto* k = vec ? (vpt == 2 ? k_norm_grad<true, 2> : vpt == 4 ? k_norm_grad<true, 4> : k_norm_grad<true, 8>)
-                  : (vpt == 2 ? k_norm_grad<false, 2> : vpt == 4 ? k_norm_grad<false, 4> : k_norm_grad<false, 8>);
-    k<<<unsigned(ctas), 32 * warps, 0, s>>>(a);
-    if (int rc = check("bq_rmsnorm_grad")) return rc;
+  const bool vec = r.cols % 8 == 0 && vec_ok(r.dy, r.ld_dy, 8) && vec_ok(r.h, r.ld_h, 8) && aligned16(r.weight) &&
+                   (!r.dh || vec_ok(r.dh, r.ld_dh, 8)) && vec_ok(r.dx, r.ld_dx, 8);
+  const NormGradPlan p = norm_grad_plan(r.n, r.cols, r.dh ? 3 : 2, vec);
+  if (p.depth) {
+    if (int rc = ring_attrs()) return rc;
+    auto* k = p.vpt == 1 ? k_norm_grad_many<1> : k_norm_grad_many<2>;
+    k<<<unsigned(p.ctas), 32 * p.warps, p.smem, s>>>(a, p.depth);
+  } else if (p.ctas > 0) {
+    auto* k = vec ? (p.vpt == 2 ? k_norm_grad<true, 2> : p.vpt == 4 ? k_norm_grad<true, 4> : k_norm_grad<true, 8>)
+                  : (p.vpt == 2 ? k_norm_grad<false, 2> : p.vpt == 4 ? k_norm_grad<false, 4> : k_norm_grad<false, 8>);
+    k<<<unsigned(p.ctas), 32 * p.warps, 0, s>>>(a);
   }
+  if (int rc = check("bq_rmsnorm_grad")) return rc;
   const unsigned g = unsigned((r.cols + 31) / 32);
+  const float* part = a.part;
   if (r.dw_kind == BQ_ROWS_FP32)
-    k_norm_dw<<<g, 256, 0, s>>>(a.part, ctas, a.ldp, r.cols, r.accumulate, static_cast<float*>(r.dw));
-  else
-    k_norm_dw<<<g, 256, 0, s>>>(a.part, ctas, a.ldp, r.cols, r.accumulate, static_cast<__nv_bfloat16*>(r.dw));
-  return check("bq_rmsnorm_grad (dw)");
+    return launch_after("bq_rmsnorm_grad (dw)", k_norm_dw<float>, g, 1024, s, part, p.ctas, a.ldp, r.cols, r.accumulate,
+                        static_cast<float*>(r.dw));
+  return launch_after("bq_rmsnorm_grad (dw)", k_norm_dw<__nv_bfloat16>, g, 1024, s, part, p.ctas, a.ldp, r.cols,
+                      r.accumulate, static_cast<__nv_bfloat16*>(r.dw));
 }
 
 }  // namespace bq

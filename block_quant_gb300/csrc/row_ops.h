@@ -26,7 +26,7 @@ struct EmbedGradArgs {
   float scale;
   int cols, id_bits, out_kind, accumulate;
 };
-size_t embed_grad_bytes(int64_t n, int64_t cols);
+size_t embed_grad_bytes(int64_t n, int64_t rows, int64_t cols);
 int launch_embed_grad(const EmbedGradArgs& a, void* ws, void* stream);  // n may be 0
 
 struct RmsnormArgs {

@@ -237,6 +237,32 @@ def test_rmsnorm(cuda, cols, residual):
     assert torch.all(codes[:, cols:] == 0x55) and torch.all(scale[:, n:] == 7.0)
 
 
+@pytest.mark.parametrize("n,cols", [(5000, 256), (2600, 520), (1300, 4096), (700, 8192), (640, 8200), (650, 16384)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_many_rows(cuda, n, cols, residual):
+    """Counts of rows that the resident CTAs share: every row as the same row alone."""
+    import torch
+
+    rng = np.random.default_rng(cols)
+    x, _ = bf16(rng.standard_normal((n, cols)), cuda, 8)
+    r, _ = bf16(rng.standard_normal((n, cols)), cuda)
+    w, _ = bf16(1 + 0.3 * rng.standard_normal(cols), cuda)
+    got, want = [], []
+    for rows in (n, 50):
+        outs = []
+        for i in range(0, n, rows):
+            m = min(rows, n - i)
+            h, y = torch.empty(m, cols, dtype=torch.bfloat16, device=cuda), torch.empty(m, cols, dtype=torch.bfloat16, device=cuda)
+            codes = torch.empty(m, cols, dtype=torch.uint8, device=cuda)
+            scale, rstd = torch.empty(-(-cols // 128), m, device=cuda), torch.empty(m, device=cuda)
+            bq.rmsnorm(x[i:i + m], w, 1e-5, residual=r[i:i + m] if residual else None, h=h if residual else None, y=y,
+                       codes=codes, code_scale=scale, rstd=rstd)
+            outs.append((h if residual else y, y, codes, scale.t(), rstd))
+        (got if rows == n else want).extend(torch.cat(t) for t in zip(*outs))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_rmsnorm_in_place_and_parts(cuda):
     """h over x, h over the residual, and each output on its own give the same bits."""
     import torch
@@ -280,7 +306,8 @@ def test_rmsnorm_rows_of_zeros_infinities_and_nan(cuda, cols):
 
 
 @pytest.mark.parametrize("n,cols", [(1, 8), (1, 8192), (2, 7), (3, 129), (37, 264), (301, 2880), (700, 520), (330, 515),
-                                    (5, 8200), (4, 8193), (3, 16392), (2, 33000)])
+                                    (5, 8200), (4, 8193), (3, 16392), (2, 33000), (5000, 256), (1300, 4096),
+                                    (700, 8192), (640, 8200)])
 @pytest.mark.parametrize("dh", [False, True])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_rmsnorm_grad(cuda, n, cols, dh, kind):
