@@ -33,7 +33,7 @@ SOURCES = {
     "row_ops.cu": ["-lineinfo"],
     "linear_fp8.cu": ["-lineinfo"],
 }
-HEADERS = ["bq_internal.h", "fp8_codes.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
+HEADERS = ["bq_internal.h", "fp8_codes.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
 
 
 def nvcc():

@@ -18,6 +18,7 @@
 #include <string>
 
 #include "bq_internal.h"
+#include "pdl.h"
 #include "row_ops.h"
 #include "tmem_ptx.h"
 #include "umma_ptx.h"
@@ -44,6 +45,7 @@ constexpr int B_STAGE = BN * BK;
 constexpr int kMaxStages = 8;
 constexpr int kPartPitch = BN + 1;             // floats of a row of a split's partial tile in shared memory
 constexpr int kTmemCols = 2 * BN;
+constexpr int kAhead = 4;                      // k-blocks from a scale's load to its use
 constexpr int kSmem = 112 * 1024;               // dynamic shared memory at most: two CTAs per SM
 
 // Instruction descriptor, kind::f8f6f4: D fp32 (bits 4-5 = 1), A and B E4M3 (bits
@@ -82,7 +84,6 @@ struct LinArgs {
   int n, width;          // rows and columns of out
   int red;               // summed index
   int tile_cols;         // W's tiles in a row of tiles
-  int transposed;        // 0: out = X W^T, 1: out = X W
   int split, stages;     // CTAs of a cluster that share a tile's k-blocks; pipeline stages
   int a_rows;            // rows of X that a stage holds (a multiple of 8, <= 128)
   int tma_out;           // out takes TMA stores (16-byte aligned rows)
@@ -92,6 +93,7 @@ struct LinArgs {
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
 // share of the k-blocks, and the shares are added in order through distributed
 // shared memory.
+template <bool TRANS>
 __global__ void __launch_bounds__(THREADS, 2)
     k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const LinArgs g) {
   extern __shared__ unsigned char smem_raw[];
@@ -112,12 +114,22 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int nt = (g.width + BN - 1) / BN;
   const int m0 = (tile / nt) * BM, n0 = (tile % nt) * BN;
   const int nk = (g.red + BK - 1) / BK;
-  const int k0 = int(int64_t(nk) * rank / g.split), k1 = int(int64_t(nk) * (rank + 1) / g.split);
+  const int k0 = int(int64_t(nk) * rank / g.split), blocks = int(int64_t(nk) * (rank + 1) / g.split) - k0;
   const uint32_t b_base = base, a_base = base + uint32_t(g.stages) * B_STAGE;
   const uint32_t a_stage = uint32_t(g.a_rows) * BK;
   // lane quarters with rows of out: only their warps read the accumulators
   const int quarters = min(4, (g.n - m0 + 31) / 32);
 
+  auto load = [&](int it, int s) {  // one lane: k-block it of this CTA into stage s
+    const int kb = k0 + it;
+    mbar_expect_tx(full_bar(s), a_stage + B_STAGE);
+    if (TRANS)
+      tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, n0, kb * BK, full_bar(s));
+    else
+      tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
+    tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
+  };
+  after_previous();
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -128,11 +140,13 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_init(tempty_bar(b), uint32_t(2 * quarters));
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int it = 0; it < min(blocks, g.stages); ++it) load(it, it);  // the first stages, before the set-up below
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  next_may_start();
   const uint32_t tmem = tmem_slot;
 
   float acc[BN / 2];
@@ -140,73 +154,85 @@ __global__ void __launch_bounds__(THREADS, 2)
   for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
   const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps
 
-  if (warp == 0 && lane == 0) {
+  // (the issuing warps run whole, one elected lane issues: see k_linear_pair)
+  if (warp == 0) {
     // ---------------- TMA producer
-    int it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const int s = it % g.stages;
-      if (!mbar_wait(empty_bar(s), uint32_t((it / g.stages) & 1) ^ 1u, g.status, 21)) break;
-      mbar_expect_tx(full_bar(s), a_stage + B_STAGE);
-      tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
-      if (g.transposed)
-        tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, n0, kb * BK, full_bar(s));
-      else
-        tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
+    int it = min(blocks, g.stages);
+    for (int s = 0, use = 1; it < blocks; ++it) {
+      if (!mbar_wait(empty_bar(s), uint32_t(use & 1) ^ 1u, g.status, 21)) break;
+      if (elect_one()) load(it, s);
+      __syncwarp();
+      if (++s == g.stages) s = 0, ++use;
     }
     // drain: the last load issued to each stage has landed before this CTA can exit
     for (int d = max(0, it - g.stages); d < it; ++d)
       mbar_wait(full_bar(d % g.stages), uint32_t((d / g.stages) & 1), g.status, 22);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---------------- MMA issuer
-    const uint32_t id = idesc_e4m3(BM, BN, g.transposed);
+    const uint32_t id = idesc_e4m3(BM, BN, TRANS ? 1 : 0);
     int it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const int s = it % g.stages, buf = it & 1;
+    for (int s = 0, use = 0; it < blocks; ++it) {
+      const int buf = it & 1;
       if (it >= 2 && !mbar_wait(tempty_bar(buf), uint32_t((it >> 1) & 1) ^ 1u, g.status, 23)) break;
-      if (!mbar_wait(full_bar(s), uint32_t((it / g.stages) & 1), g.status, 24)) break;
+      if (!mbar_wait(full_bar(s), uint32_t(use & 1), g.status, 24)) break;
       tc_fence_after();
-      const uint32_t a_addr = a_base + uint32_t(s) * a_stage, b_addr = b_base + uint32_t(s) * B_STAGE;
+      // K-major: 32-code k slices 32 bytes apart; MN-major: 32 k rows of 128 bytes apart
+      const uint64_t ad = sdesc(a_base + uint32_t(s) * a_stage, 16, 1024);
+      const uint64_t bd = sdesc(b_base + uint32_t(s) * B_STAGE, TRANS ? BK * 128 : 16, 1024);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < BK / 32; ++kk) {
-        // K-major: 32-code k slices 32 bytes apart; MN-major: 32 k rows of 128 bytes apart
-        const uint64_t ad = sdesc(a_addr + 32u * kk, 16, 1024);
-        const uint64_t bd = g.transposed ? sdesc(b_addr + 32u * 128u * kk, BK * 128, 1024)
-                                         : sdesc(b_addr + 32u * kk, 16, 1024);
-        mma_e4m3(tmem + uint32_t(buf) * BN, ad, bd, id, kk != 0 ? 1u : 0u);
+        for (int kk = 0; kk < BK / 32; ++kk)
+          mma_e4m3(tmem + uint32_t(buf) * BN, ad + uint64_t(2 * kk), bd + uint64_t(TRANS ? 256 * kk : 2 * kk), id,
+                   kk != 0 ? 1u : 0u);
+        mma_commit(empty_bar(s));
+        mma_commit(tfull_bar(buf));
       }
-      mma_commit(empty_bar(s));
-      mma_commit(tfull_bar(buf));
+      __syncwarp();
+      if (++s == g.stages) s = 0, ++use;
     }
     // every product issued here has finished before the accumulators are freed
     if (it > 0) mbar_wait(tfull_bar((it - 1) & 1), uint32_t(((it - 1) >> 1) & 1), g.status, 26);
-  } else if (warp >= 2 && q < quarters) {
+  } else if (q < quarters) {
     // ---------------- scaled accumulation
     const int row = m0 + 32 * q + lane;
-    const float* xs = g.xs + row;
-    // the tile's 128 columns of out lie in one row (transposed: column) of W's tiles
-    const float* ws = g.transposed ? g.ws + (n0 >> 7) : g.ws + int64_t(n0 >> 7) * g.tile_cols;
-    const int64_t ws_step = g.transposed ? g.tile_cols : 1;
     const bool on = row < g.n;
-    float f = 0.f;
-    if (k0 < k1 && on) f = __ldg(xs + int64_t(k0) * g.ld_xs) * __ldg(ws + k0 * ws_step);
-    int it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const int buf = it & 1;
-      const float fk = f;
-      if (kb + 1 < k1 && on) f = __ldg(xs + int64_t(kb + 1) * g.ld_xs) * __ldg(ws + (kb + 1) * ws_step);
-      if (!mbar_wait(tfull_bar(buf), uint32_t((it >> 1) & 1), g.status, 25)) break;
-      tc_fence_after();
-      const uint32_t at = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf) * BN + uint32_t(half) * (BN / 2);
+    const float* xs = g.xs + row + int64_t(k0) * g.ld_xs;
+    // the tile's 128 columns of out lie in one row (transposed: column) of W's tiles
+    const int64_t ws_step = TRANS ? g.tile_cols : 1;
+    const float* ws = (TRANS ? g.ws + (n0 >> 7) : g.ws + int64_t(n0 >> 7) * g.tile_cols) + k0 * ws_step;
+    // scales come kAhead blocks before their use (their loads queue behind the stages'
+    // copies); W's for 32 blocks at a time, block b in lane b
+    float xn[kAhead], wl = 0.f, wn = lane < blocks ? __ldg(ws + lane * ws_step) : 0.f;
 #pragma unroll
-      for (int j0 = 0; j0 < BN / 2; j0 += 8) {
-        uint32_t r[8];
-        tmem_ld8(at + uint32_t(j0), r);
-        if (j0 + 8 == BN / 2) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta(tempty_bar(buf));
+    for (int b = 0; b < kAhead; ++b) xn[b] = on && b < blocks ? __ldg(xs + b * g.ld_xs) : 0.f;
+    bool ok = true;
+    for (int it0 = 0; it0 < blocks; it0 += kAhead) {
+      if ((it0 & 31) == 0) {
+        wl = wn;
+        wn = it0 + 32 + lane < blocks ? __ldg(ws + (it0 + 32 + lane) * ws_step) : 0.f;
+      }
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        const int it = it0 + b;
+        if (it >= blocks) continue;  // (no early exit: its copies of the sums would spill)
+        const float f = xn[b] * __shfl_sync(0xFFFFFFFFu, wl, it & 31);
+        if (on && it + kAhead < blocks) xn[b] = __ldg(xs + int64_t(it + kAhead) * g.ld_xs);
+        const int buf = it & 1;
+        ok = ok && mbar_wait(tfull_bar(buf), uint32_t((it >> 1) & 1), g.status, 25);
+        tc_fence_after();
+        const uint32_t at = tmem + (uint32_t(32 * q) << 16) + uint32_t(buf) * BN + uint32_t(half) * (BN / 2);
+#pragma unroll
+        for (int j0 = 0; j0 < BN / 2; j0 += 16) {
+          uint32_t r[16];
+          tmem_ld16_begin(at + uint32_t(j0), r);
+          tmem_wait_ld16(r);
+          if (j0 + 16 == BN / 2) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cta(tempty_bar(buf));
+          }
+          add_scaled<16>(acc + j0, r, f);
         }
-        add_scaled<8>(acc + j0, r, fk);
       }
     }
   }
@@ -329,11 +355,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  next_may_start();
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -520,6 +548,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // X's scales at a pitch whose rows bulk copies can read
 __global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x, int64_t ldx, int64_t n,
                                                      float* __restrict__ out, int64_t ldo) {
+  after_previous();
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i < n) out[int64_t(blockIdx.y) * ldo + i] = x[int64_t(blockIdx.y) * ldx + i];
 }
@@ -556,17 +585,19 @@ int pair_slots() {
 
 int launch_clusters(const void* kernel, int clusters, int size, int threads, int smem, void** args, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = unsigned(size);
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (after_previous)
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(unsigned(clusters) * unsigned(size));
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = s;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaLaunchKernelExC(&cfg, kernel, args);
   return check("bq_linear_fp8");
 }
@@ -576,7 +607,8 @@ int launch_clusters(const void* kernel, int clusters, int size, int threads, int
 int launch_linear_fp8(const LinearArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (once_per_device(kOnceLinearAttr) &&
-      (cudaFuncSetAttribute(k_linear, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+      (cudaFuncSetAttribute(k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+       cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
        cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
        cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess))
     return check("bq_linear_fp8 (shared memory attribute)");
@@ -584,7 +616,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   LinArgs g;
   g.xs = a.x_scale, g.ws = a.w_scale, g.out = static_cast<__nv_bfloat16*>(a.out);
   g.ld_xs = a.ld_xs, g.ldo = a.ldo, g.n = int(a.n), g.width = width, g.red = red;
-  g.tile_cols = (a.cols + 127) / 128, g.transposed = a.transposed, g.status = a.status;
+  g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
   g.split = 1, g.stages = 0, g.a_rows = BM, g.tma_out = 0;
   const int nk = (red + BK - 1) / BK;
   CUtensorMap tx, tw, ts, to;
@@ -623,7 +655,8 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   const int smem = 1024 + std::max(part, g.stages * stage + spare);
   void* args[] = {&tx, &tw, &g};
-  return launch_clusters(reinterpret_cast<const void*>(k_linear), int(tiles), g.split, THREADS, smem, args, s);
+  const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear<true>) : reinterpret_cast<const void*>(k_linear<false>);
+  return launch_clusters(k, int(tiles), g.split, THREADS, smem, args, s);
 }
 
 }  // namespace bq

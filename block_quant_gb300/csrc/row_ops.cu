@@ -14,6 +14,7 @@
 
 #include "bq_internal.h"
 #include "fp8_codes.h"
+#include "pdl.h"
 #include "row_ops.h"
 #include "umma_ptx.h"
 
@@ -227,6 +228,95 @@ __device__ __forceinline__ void quant_span(const float* y, int c0, int cols, int
   }
 }
 
+// s = a / 448 rounded to nearest (Markstein 1990: a quotient from the rounded reciprocal
+// and one exact residual is the rounded quotient), for 2^-100 <= a < infinity
+__device__ __forceinline__ float over_448(float a) {
+  constexpr float y = 1.f / 448.f;
+  const float q = __fmul_rn(a, y);
+  return __fmaf_rn(__fmaf_rn(-448.f, q, a), y, q);
+}
+
+// quant_span of N spans at once (aligned; N = 2 or 4), span i from column c0 + i * step:
+// the N maxima of a half-warp are reduced together, each step halving how many a lane
+// holds, so that one division pass serves all 2 N groups; the row kernels are bound by
+// instructions where every span reduces and divides for itself.
+template <int N>
+__device__ __forceinline__ void quant_spans(const float2 (*y)[4], int c0, int step, int cols, int lane, uint8_t* codes,
+                                            float* scale, int64_t ld_scale) {
+  float a[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    a[i] = max3(fabsf(y[i][0].x), fabsf(y[i][0].y), fabsf(y[i][1].x));
+    a[i] = max3(a[i], fabsf(y[i][1].y), fabsf(y[i][2].x));
+    a[i] = max3(a[i], fabsf(y[i][2].y), fabsf(y[i][3].x));
+    a[i] = max_nan(a[i], fabsf(y[i][3].y));
+  }
+  // lane bits from 3 down choose the span that the lane goes on with
+  int o = 8;
+#pragma unroll
+  for (int m = N; m > 1; m >>= 1, o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < m / 2; ++i) {
+      const float give = up ? a[i] : a[i + m / 2], keep = up ? a[i + m / 2] : a[i];
+      a[i] = max_nan(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o; o >>= 1) a[0] = max_nan(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], o));
+  constexpr int kShift = N == 4 ? 2 : 3;  // lanes of a group: its span is (lane & 15) >> kShift
+  const int mine = c0 + ((lane & 15) >> kShift) * step + (lane >> 4) * 128;
+  const bool store = (lane & ((1 << kShift) - 1)) == 0 && mine < cols;
+  if (__all_sync(0xFFFFFFFFu, mine >= cols || (a[0] >= 7.8886091e-31f && a[0] <= 3.4028235e38f))) {
+    const float r = __fdiv_rn(448.f, a[0]);
+    if (store) scale[int64_t(mine >> 7) * ld_scale] = over_448(a[0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 ri = dup(__shfl_sync(0xFFFFFFFFu, r, (lane & 16) | (i << kShift)));
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = uint32_t(__nv_cvt_float2_to_fp8x2(mul2(y[i][j], ri), __NV_SATFINITE, __NV_E4M3));
+      const int c = c0 + i * step + 8 * lane;
+      if (c < cols) *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
+  } else {  // a zero, tiny, infinite or NaN group among them
+    const QScale q = qscale(__float_as_uint(a[0]), 448.f);
+    if (store) scale[int64_t(mine >> 7) * ld_scale] = q.s;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int from = (lane & 16) | (i << kShift);
+      QScale qi;
+      qi.s = __shfl_sync(0xFFFFFFFFu, q.s, from);
+      qi.r = __shfl_sync(0xFFFFFFFFu, q.r, from);
+      qi.mode = __shfl_sync(0xFFFFFFFFu, q.mode, from);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[2 * j] = y[i][j].x, v[2 * j + 1] = y[i][j].y;
+      const int c = c0 + i * step + 8 * lane;
+      if (c < cols) *reinterpret_cast<uint2*>(codes + c) = codes_e4m3(v, qi);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float2* v) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const float2* v) {
+  return make_uint4(pack2(v[0].x, v[0].y), pack2(v[1].x, v[1].y), pack2(v[2].x, v[2].y), pack2(v[3].x, v[3].y));
+}
+
+// bf16(a + b), each pair's sums rounded once
+__device__ __forceinline__ uint4 add_bf16(const uint4& a, const uint4& b) {
+  auto add = [](uint32_t x, uint32_t y) {
+    const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&s);
+  };
+  return make_uint4(add(a.x, b.x), add(a.y, b.y), add(a.z, b.z), add(a.w, b.w));
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
@@ -236,10 +326,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 __device__ __forceinline__ int64_t load_id(const void* ids, int bits, int64_t i) {
   return bits == 64 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
 }
-
-// A kernel launched by launch_after() may start while its predecessor on the stream
-// still runs (its launch is hidden); this waits until that has completed.
-__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- embedding lookup
 
@@ -252,6 +338,8 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     k_embed(const void* __restrict__ table, const float* __restrict__ tscale, int64_t rows, int cols, int64_t ldt,
             const void* __restrict__ ids, int id_bits, int64_t n, float scale, __nv_bfloat16* __restrict__ out,
             int64_t ldo, int segs) {
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   const int64_t t = item / segs;
@@ -321,6 +409,8 @@ template <int KEYS>
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1, 1)
     k_embed_sort(const void* __restrict__ ids, int id_bits, int n, int rows, int passes, uint2* __restrict__ buf0,
                  uint2* __restrict__ buf1, uint32_t* __restrict__ touched) {
+  after_previous();
+  next_may_start();
   __shared__ SortSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = int(cluster_rank());
@@ -338,13 +428,16 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
       return make_uint2(id >= 0 && id < rows ? uint32_t(id) : uint32_t(rows), uint32_t(i));
     };
     if (tid < kBins) sm.hist[tid] = 0;
+    uint2 only = make_uint2(0u, 0u);  // KEYS == 1: a thread has one token at most
+    if (KEYS == 1 && lo + tid < hi) only = key_at(lo + tid);
     __syncthreads();
-    for (int i = lo + tid; i < hi; i += kSortThreads) atomicAdd(&sm.hist[(key_at(i).x >> shift) & (kBins - 1)], 1u);
+    for (int i = lo + tid; i < hi; i += kSortThreads)
+      atomicAdd(&sm.hist[((KEYS == 1 ? only.x : key_at(i).x) >> shift) & (kBins - 1)], 1u);
     if (p == 0) __threadfence();  // the cleared bits
     cluster_sync();
     if (p == 0 && touched)
       for (int i = lo + tid; i < hi; i += kSortThreads) {
-        const uint32_t v = key_at(i).x;
+        const uint32_t v = KEYS == 1 ? only.x : key_at(i).x;
         atomicOr(touched + (v >> 5), 1u << (v & 31));  // (bit `rows`: no row)
       }
     // exclusive scan over (digit, CTA): thread d < kBins holds digit d
@@ -385,7 +478,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
 #pragma unroll
       for (int j = 0; j < KEYS; ++j) {
         const int i = w0 + 32 * j + lane;
-        if (i < hi) kv[j] = key_at(i);
+        if (i < hi) kv[j] = KEYS == 1 ? only : key_at(i);
       }
       __syncthreads();
 #pragma unroll
@@ -473,6 +566,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, 4) k_embed_rows(const EmbedRow
   __shared__ uint32_t key[kPiece + 2], pos[kPiece];  // key[1 + i]: token i of the piece; 0, len + 1: its neighbours
   const int tid = threadIdx.x, lane = tid & 31;
   after_previous();
+  next_may_start();
   if (int(blockIdx.x) >= a.piece_ctas) {
     // zeros
     constexpr int V = VEC ? 16 / int(sizeof(Out)) : 1;
@@ -539,11 +633,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_embed_join(const EmbedRows a
   const int lane = threadIdx.x & 31;
   const int piece = int(blockIdx.x) / a.groups, b = piece * kPiece, e = b + kPiece;
   after_previous();
+  next_may_start();
   if (e >= a.n) return;
-  const uint32_t id = a.sorted[e - 1].x;
-  if (a.sorted[e].x != id || id >= uint32_t(a.rows)) return;
-  const bool from_start = a.sorted[b].x == id;
-  if (from_start && b > 0 && a.sorted[b - 1].x == id) return;  // it began in an earlier piece
+  const uint32_t id = a.sorted[e - 1].x, after = a.sorted[e].x, first = a.sorted[b].x;
+  const uint32_t before = a.sorted[max(b, 1) - 1].x;
+  const bool from_start = first == id;
+  if (after != id || id >= uint32_t(a.rows) || (from_start && b > 0 && before == id)) return;  // (began in an earlier piece)
   const int c0 = ((int(blockIdx.x) - piece * a.groups) * kRowWarps + int(threadIdx.x >> 5)) * kSpan;
   if (c0 >= a.cols) return;
   float acc[8];
@@ -582,6 +677,8 @@ constexpr int row_threads(int vpt) { return vpt <= 4 ? 512 : 1024; }
 
 template <bool VEC, int VPT>
 __global__ void __launch_bounds__(row_threads(VPT)) k_norm(const NormArgs a) {
+  after_previous();
+  next_may_start();
   __shared__ float part[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t t = blockIdx.x;
@@ -595,16 +692,22 @@ __global__ void __launch_bounds__(row_threads(VPT)) k_norm(const NormArgs a) {
       float r[8];
       load_bf16<VEC>(a.res + t * a.ldr, c0, a.cols, lane, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = __bfloat162float(__float2bfloat16_rn(h[i][e] + r[e]));
+      for (int e = 0; e < 8; ++e) {
+        const __nv_bfloat16 b = __hadd(__float2bfloat16_rn(h[i][e]), __float2bfloat16_rn(r[e]));  // (both exact)
+        h[i][e] = __bfloat162float(b);
+      }
       if (a.h) store_bf16<VEC>(a.h + t * a.ldh, c0, a.cols, lane, h[i]);
     }
   }
-  float ss = 0.f;
+  float2 s2 = dup(0.f);
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
-  ss = warp_sum(ss);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 v = make_float2(h[i][e], h[i][e + 1]);
+      s2 = fma2(v, v, s2);
+    }
+  float ss = warp_sum(s2.x + s2.y);
   if (lane == 0) part[warp] = ss;
   __syncthreads();
   ss = warp_sum(lane < warps ? part[lane] : 0.f);
@@ -653,6 +756,8 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
 // not).  A thread reads only what it copied: no barrier but the sum's.
 template <int VPT>
 __global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_many(const NormArgs a, int64_t n, int depth) {
+  after_previous();
+  next_may_start();
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float part[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -682,27 +787,23 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_man
   for (int64_t t = blockIdx.x; t < n; t += gridDim.x, next += gridDim.x, flip ^= 1) {
     fetch(next, slot == 0 ? depth - 1 : slot - 1);  // the slot read last
     copy_wait(depth - 1);
-    float h[VPT][8];
-    float ss = 0.f;
+    float2 h[VPT][4];
+    float2 s2 = dup(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
-      unpack8(shared16(at), h[i]);
+      uint4 b = shared16(at);
       if (a.res) {
-        float r[8];
-        unpack8(shared16(at + VPT * step), r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] + r[e];
-        const uint4 b = pack8(h[i]);
-        unpack8(b, h[i]);
+        b = add_bf16(b, shared16(at + VPT * step));
         const int c = (warp + i * warps) * kSpan + 8 * lane;
         if (c < a.cols) *reinterpret_cast<uint4*>(a.h + t * a.ldh + c) = b;
       }
+      unpack8(b, h[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+      for (int e = 0; e < 4; ++e) s2 = fma2(h[i][e], h[i][e], s2);
     }
     slot = slot + 1 == depth ? 0 : slot + 1;
-    ss = warp_sum(ss);
+    float ss = warp_sum(s2.x + s2.y);
     if (lane == 0) part[flip][warp] = ss;
     __syncthreads();
     ss = warp_sum(lane < warps ? part[flip][lane] : 0.f);
@@ -710,15 +811,15 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_man
     if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c0 = (warp + i * warps) * kSpan;
-      if (c0 >= a.cols) break;
-      float g[8];
+      float2 g[4];
       unpack8(w[i], g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = __fmul_rn(__fmul_rn(h[i][e], rstd), g[e]);
-      if (a.y) store_bf16<true>(a.y + t * a.ldy, c0, a.cols, lane, h[i]);
-      if (a.codes) quant_span<true>(h[i], c0, a.cols, lane, a.codes + t * a.ldc, a.scale + t, a.lds);
+      for (int e = 0; e < 4; ++e) h[i][e] = mul2(mul2(h[i][e], dup(rstd)), g[e]);
+      const int c = (warp + i * warps) * kSpan + 8 * lane;
+      if (a.y && c < a.cols) *reinterpret_cast<uint4*>(a.y + t * a.ldy + c) = pack8(h[i]);
     }
+    if (a.codes)
+      quant_spans<VPT>(h, warp * kSpan, warps * kSpan, a.cols, lane, a.codes + t * a.ldc, a.scale + t, a.lds);
   }
 }
 
@@ -727,6 +828,8 @@ template <bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_quant_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, uint8_t* __restrict__ codes,
                  int64_t ldc, float* __restrict__ scale, int64_t lds, int segs) {
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   const int64_t t = item / segs;
@@ -735,12 +838,19 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   uint4 w[kSpans];
 #pragma unroll
   for (int j = 0; j < kSpans; ++j) w[j] = load_packed<VEC>(x + t * ldx, c0 + kSpan * j, cols, lane);
+  if (VEC) {
+    float2 v[kSpans][4];
 #pragma unroll
-  for (int j = 0; j < kSpans; ++j) {
-    if (c0 + kSpan * j >= cols) break;
-    float v[8];
-    unpack8(w[j], v);
-    quant_span<VEC>(v, c0 + kSpan * j, cols, lane, codes + t * ldc, scale + t, lds);
+    for (int j = 0; j < kSpans; ++j) unpack8(w[j], v[j]);
+    quant_spans<kSpans>(v, c0, kSpan, cols, lane, codes + t * ldc, scale + t, lds);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kSpans; ++j) {
+      if (c0 + kSpan * j >= cols) break;
+      float v[8];
+      unpack8(w[j], v);
+      quant_span<VEC>(v, c0 + kSpan * j, cols, lane, codes + t * ldc, scale + t, lds);
+    }
   }
 }
 
@@ -749,6 +859,8 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_dequant_rows(const uint8_t* __restrict__ codes, int64_t ldc, const float* __restrict__ scale, int64_t lds,
                    int64_t n, int cols, __nv_bfloat16* __restrict__ out, int64_t ldo, int spans) {
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   const int64_t t = item / spans;
@@ -767,6 +879,8 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_copy_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, __nv_bfloat16* __restrict__ out,
                 int64_t ldo, int spans) {
+  after_previous();
+  next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   const int64_t t = item / spans;
@@ -794,6 +908,8 @@ struct NormGradArgs {
 // CTAs walk the rows blockIdx.x, + gridDim.x, ...; a thread keeps its columns' dw.
 template <bool VEC, int VPT>
 __global__ void __launch_bounds__(row_threads(VPT)) k_norm_grad(const NormGradArgs a) {
+  after_previous();
+  next_may_start();
   __shared__ float part[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float dw[VPT][8] = {};
@@ -841,6 +957,8 @@ __global__ void __launch_bounds__(row_threads(VPT)) k_norm_grad(const NormGradAr
 // the same with the rows to come copied into a ring, as k_norm_many
 template <int VPT>
 __global__ void __launch_bounds__(1024, 1) k_norm_grad_many(const NormGradArgs a, int depth) {
+  after_previous();
+  next_may_start();
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float part[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -849,7 +967,7 @@ __global__ void __launch_bounds__(1024, 1) k_norm_grad_many(const NormGradArgs a
   const uint32_t row_bytes = uint32_t(ins) * VPT * step;
   const uint32_t mine = smem_addr(ring) + threadIdx.x * 16u;
   uint4 w[VPT];
-  float dw[VPT][8] = {};
+  float2 dw[VPT][4] = {};
 #pragma unroll
   for (int i = 0; i < VPT; ++i) w[i] = load_packed<true>(a.w, (warp + i * warps) * kSpan, a.cols, lane);
   auto fetch = [&](int64_t t, int slot) {
@@ -874,45 +992,46 @@ __global__ void __launch_bounds__(1024, 1) k_norm_grad_many(const NormGradArgs a
     const float rstd = rnext;
     if (t + gridDim.x < a.n) rnext = a.rstd[t + gridDim.x];
     copy_wait(depth - 2);
-    float dy[VPT][8], u[VPT][8];
+    float2 dy[VPT][4], u[VPT][4];
     uint4 g[VPT];
-    float dot = 0.f;
+    float2 d2 = dup(0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const uint32_t at = mine + uint32_t(slot) * row_bytes + uint32_t(i) * step;
       unpack8(shared16(at), dy[i]);
       unpack8(shared16(at + VPT * step), u[i]);
       g[i] = a.dh ? shared16(at + 2 * VPT * step) : make_uint4(0u, 0u, 0u, 0u);
-      float f[8];
+      float2 f[4];
       unpack8(w[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        u[i][e] *= rstd;
-        dw[i][e] = fmaf(dy[i][e], u[i][e], dw[i][e]);
-        dy[i][e] *= f[e];
-        dot = fmaf(dy[i][e], u[i][e], dot);
+      for (int e = 0; e < 4; ++e) {
+        u[i][e] = mul2(u[i][e], dup(rstd));
+        dw[i][e] = fma2(dy[i][e], u[i][e], dw[i][e]);
+        dy[i][e] = mul2(dy[i][e], f[e]);
+        d2 = fma2(dy[i][e], u[i][e], d2);
       }
     }
     fetch(next, slot == 0 ? depth - 1 : slot - 1);  // the slot read a row ago
     slot = slot + 1 == depth ? 0 : slot + 1;
-    dot = warp_sum(dot);
+    float dot = warp_sum(d2.x + d2.y);
     if (lane == 0) part[flip][warp] = dot;
     __syncthreads();
     dot = warp_sum(lane < warps ? part[flip][lane] : 0.f) / float(a.cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int c0 = (warp + i * warps) * kSpan;
-      float o[8];
+      const int c = (warp + i * warps) * kSpan + 8 * lane;
+      float2 o[4];
       unpack8(g[i], o);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = fmaf(rstd, fmaf(-dot, u[i][e], dy[i][e]), o[e]);
-      store_bf16<true>(a.dx + t * a.ld_dx, c0, a.cols, lane, o);
+      for (int e = 0; e < 4; ++e) o[e] = fma2(dup(rstd), fma2(dup(-dot), u[i][e], dy[i][e]), o[e]);
+      if (c < a.cols) *reinterpret_cast<uint4*>(a.dx + t * a.ld_dx + c) = pack8(o);
     }
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c0 = (warp + i * warps) * kSpan;
-    if (c0 < a.cols) store_f32<true>(a.part + int64_t(blockIdx.x) * a.ldp, c0, a.cols, lane, dw[i]);
+    const float v[8] = {dw[i][0].x, dw[i][0].y, dw[i][1].x, dw[i][1].y, dw[i][2].x, dw[i][2].y, dw[i][3].x, dw[i][3].y};
+    if (c0 < a.cols) store_f32<true>(a.part + int64_t(blockIdx.x) * a.ldp, c0, a.cols, lane, v);
   }
 }
 
@@ -924,6 +1043,7 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   after_previous();
+  next_may_start();
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 8
@@ -947,21 +1067,6 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- host
-
-template <typename... Params, typename... Args>
-int launch_after(const char* what, void (*kernel)(Params...), unsigned ctas, int threads, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
-  return check(what);
-}
 
 bool vec_ok(const void* p, int64_t ld, int values) { return aligned16(p) && ld % values == 0; }
 
@@ -1055,7 +1160,7 @@ int launch_embed(const EmbedArgs& a, void* stream) {
   const int segs = (a.cols + kSeg - 1) / kSeg;
   const int64_t ctas = (a.n * segs + kRowWarps - 1) / kRowWarps;
   auto* k = fp8 ? (vec ? k_embed<true, true> : k_embed<false, true>) : (vec ? k_embed<true, false> : k_embed<false, false>);
-  k<<<unsigned(ctas), 32 * kRowWarps, 0, s>>>(a.table, a.tscale, a.rows, a.cols, a.ldt, a.ids, a.id_bits, a.n, a.scale,
+  launch_after(k, unsigned(ctas), 32 * kRowWarps, 0, s, a.table, a.tscale, a.rows, a.cols, a.ldt, a.ids, a.id_bits, a.n, a.scale,
                                               static_cast<__nv_bfloat16*>(a.out), a.ldo, segs);
   return check("bq_embed");
 }
@@ -1067,9 +1172,11 @@ namespace {
 template <bool VEC, typename Out>
 int embed_rows(const EmbedRows& a, unsigned zero_ctas, int pieces, Out* out, cudaStream_t s) {
   const unsigned ctas = unsigned(a.piece_ctas) + zero_ctas;
-  if (int rc = launch_after("bq_embed_grad (rows)", k_embed_rows<VEC, Out>, ctas, 32 * kRowWarps, s, a, out)) return rc;
+  launch_after(k_embed_rows<VEC, Out>, ctas, 32 * kRowWarps, 0, s, a, out);
+  if (int rc = check("bq_embed_grad (rows)")) return rc;
   if (pieces < 2) return BQ_OK;  // no run crosses a piece's end
-  return launch_after("bq_embed_grad (join)", k_embed_join<VEC, Out>, unsigned(a.piece_ctas), 32 * kRowWarps, s, a, out);
+  launch_after(k_embed_join<VEC, Out>, unsigned(a.piece_ctas), 32 * kRowWarps, 0, s, a, out);
+  return check("bq_embed_grad (join)");
 }
 
 }  // namespace
@@ -1098,8 +1205,8 @@ int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
   const unsigned zero_ctas = g.accumulate ? 0u : unsigned((g.rows + a.zero_rows - 1) / a.zero_rows);
   if (g.n > 0) {
     auto* k = g.n <= kSortCtas * kSortThreads ? k_embed_sort<1> : k_embed_sort<4>;
-    k<<<kSortCtas, kSortThreads, 0, s>>>(g.ids, g.id_bits, a.n, int(g.rows), passes, b0, b1,
-                                         g.accumulate ? nullptr : touched);
+    launch_after(k, kSortCtas, kSortThreads, 0, s, g.ids, g.id_bits, a.n, int(g.rows), passes, b0, b1,
+                 g.accumulate ? nullptr : touched);
     if (int rc = check("bq_embed_grad (sort)")) return rc;
   }
   if (f32) {
@@ -1149,13 +1256,13 @@ int launch_rmsnorm(const RmsnormArgs& r, void* stream) {
       auto* many = vpt == 2 ? k_norm_many<2> : k_norm_many<4>;
       if (int rc = ring_attrs()) return rc;
       const int64_t most = int64_t(sm_count()) * ring.per_sm, each = (r.n + most - 1) / most;
-      many<<<unsigned((r.n + each - 1) / each), 32 * warps, ring.depth * row, s>>>(a, r.n, ring.depth);
+      launch_after(many, unsigned((r.n + each - 1) / each), 32 * warps, size_t(ring.depth * row), s, a, r.n, ring.depth);
       return check("bq_rmsnorm");
     }
   }
   auto* k = vec ? (vpt == 2 ? k_norm<true, 2> : vpt == 4 ? k_norm<true, 4> : k_norm<true, 8>)
                 : (vpt == 2 ? k_norm<false, 2> : vpt == 4 ? k_norm<false, 4> : k_norm<false, 8>);
-  k<<<unsigned(r.n), 32 * warps, 0, s>>>(a);
+  launch_after(k, unsigned(r.n), 32 * warps, 0, s, a);
   return check("bq_rmsnorm");
 }
 
@@ -1166,7 +1273,7 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
   const int segs = (cols + kSeg - 1) / kSeg;
   const int64_t ctas = (n * segs + kRowWarps - 1) / kRowWarps;
   auto* k = vec ? k_quant_rows<true> : k_quant_rows<false>;
-  k<<<unsigned(ctas), 32 * kRowWarps, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc, scale, lds,
+  launch_after(k, unsigned(ctas), 32 * kRowWarps, 0, s, static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc, scale, lds,
                                               segs);
   return check("bq_quant_rows_fp8");
 }
@@ -1175,7 +1282,7 @@ int launch_dequant_rows(const uint8_t* codes, int64_t ldc, const float* scale, i
                         void* out, int64_t ldo, void* stream) {
   const int spans = (cols + kSpan - 1) / kSpan;
   const int64_t ctas = (n * spans + kRowWarps - 1) / kRowWarps;
-  k_dequant_rows<<<unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream)>>>(
+  launch_after(k_dequant_rows, unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream),
       codes, ldc, scale, lds, n, cols, static_cast<__nv_bfloat16*>(out), ldo, spans);
   return check("bq_linear_fp8_dw (input)");
 }
@@ -1183,7 +1290,7 @@ int launch_dequant_rows(const uint8_t* codes, int64_t ldc, const float* scale, i
 int launch_copy_rows(const void* x, int64_t ldx, int64_t n, int cols, void* out, int64_t ldo, void* stream) {
   const int spans = (cols + kSpan - 1) / kSpan;
   const int64_t ctas = (n * spans + kRowWarps - 1) / kRowWarps;
-  k_copy_rows<<<unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream)>>>(
+  launch_after(k_copy_rows, unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream),
       static_cast<const __nv_bfloat16*>(x), ldx, n, cols, static_cast<__nv_bfloat16*>(out), ldo, spans);
   return check("bq_linear_fp8_dw (copy)");
 }
@@ -1214,20 +1321,21 @@ int launch_rmsnorm_grad(const RmsnormGradArgs& r, void* ws, void* stream) {
   if (p.depth) {
     if (int rc = ring_attrs()) return rc;
     auto* k = p.vpt == 1 ? k_norm_grad_many<1> : k_norm_grad_many<2>;
-    k<<<unsigned(p.ctas), 32 * p.warps, p.smem, s>>>(a, p.depth);
+    launch_after(k, unsigned(p.ctas), 32 * p.warps, size_t(p.smem), s, a, p.depth);
   } else if (p.ctas > 0) {
     auto* k = vec ? (p.vpt == 2 ? k_norm_grad<true, 2> : p.vpt == 4 ? k_norm_grad<true, 4> : k_norm_grad<true, 8>)
                   : (p.vpt == 2 ? k_norm_grad<false, 2> : p.vpt == 4 ? k_norm_grad<false, 4> : k_norm_grad<false, 8>);
-    k<<<unsigned(p.ctas), 32 * p.warps, 0, s>>>(a);
+    launch_after(k, unsigned(p.ctas), 32 * p.warps, 0, s, a);
   }
   if (int rc = check("bq_rmsnorm_grad")) return rc;
   const unsigned g = unsigned((r.cols + 31) / 32);
   const float* part = a.part;
   if (r.dw_kind == BQ_ROWS_FP32)
-    return launch_after("bq_rmsnorm_grad (dw)", k_norm_dw<float>, g, 1024, s, part, p.ctas, a.ldp, r.cols, r.accumulate,
-                        static_cast<float*>(r.dw));
-  return launch_after("bq_rmsnorm_grad (dw)", k_norm_dw<__nv_bfloat16>, g, 1024, s, part, p.ctas, a.ldp, r.cols,
-                      r.accumulate, static_cast<__nv_bfloat16*>(r.dw));
+    launch_after(k_norm_dw<float>, g, 1024, 0, s, part, p.ctas, a.ldp, r.cols, r.accumulate, static_cast<float*>(r.dw));
+  else
+    launch_after(k_norm_dw<__nv_bfloat16>, g, 1024, 0, s, part, p.ctas, a.ldp, r.cols, r.accumulate,
+                 static_cast<__nv_bfloat16*>(r.dw));
+  return check("bq_rmsnorm_grad (dw)");
 }
 
 }  // namespace bq
