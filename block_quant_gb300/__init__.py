@@ -10,8 +10,9 @@ torch's current stream on the current device.
 """
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import numpy as np
 
@@ -410,118 +411,47 @@ def muon_ns_noalloc(mats, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, stre
 #
 # Matrices are 2-D torch tensors on the GPU whose last dimension is contiguous (a
 # row pitch is read off the tensor); 1-D tensors are contiguous.  Outputs are the
-# caller's, as everywhere.  Shapes and types are checked here, the rest by the
-# library.  The calls go through bq_call, their arguments packed into one string of
-# 64-bit words: a generated token's norm costs a few microseconds in all, of which
-# ctypes' conversion of twenty arguments would be two.
+# caller's, as everywhere.  Shapes and types are checked by the marshalling module
+# (csrc/binding.c), the rest by the library.
 
 _KIND_NAMES = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
-               "torch.uint8": ROWS_FP8}
-_KINDS = {}  # torch dtype -> kind, filled as types are met
+               "torch.uint8": ROWS_FP8, "torch.int32": 32, "torch.int64": 64}
+_calls = None
 
 
-def _refuse(msg):
-    raise BQError(BQ_EINVAL, f"invalid argument: {msg}")
+def _layer():
+    """The marshalling module, bound to the library.  Raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        path = os.path.join(HERE, "_lib", "_bqcall.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m block_quant_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_bqcall", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bqcall", loader))
+        loader.exec_module(module)
+        module.bind(C.cast(lib.bq_call, C.c_void_p).value, {}, lambda dtype: _KIND_NAMES.get(str(dtype)))
+        _calls = module
+    return _calls
 
 
-def _kind(name, x):
-    d = getattr(x, "dtype", None)
-    k = _KINDS.get(d)
-    if k is None:
-        k = _KIND_NAMES.get(str(d))
-        if k is None:
-            _refuse(f"{name} has type {d}")
-        _KINDS[d] = k
-    return k
-
-
-def _mat2(name, x, kinds, rows=None, cols=None):
-    """(pointer, row pitch, rows, cols, kind) of a matrix."""
-    if x is None:
-        _refuse(f"{name} is None")
-    kind = _kind(name, x)
-    if kind not in kinds:
-        _refuse(f"{name} has type {x.dtype}")
-    shape = x.shape
-    if len(shape) != 2:
-        _refuse(f"{name} must be a matrix")
-    r, c = shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        _refuse(f"{name} is {r} x {c}, expected {'any' if rows is None else rows} x {'any' if cols is None else cols}")
-    ld, step = x.stride()
-    if step != 1 and c > 1:
-        _refuse(f"{name}'s rows must be contiguous")
-    return x.data_ptr(), ld, r, c, kind
-
-
-def _rows(name, x, rows, cols):
-    """(pointer, row pitch) of a bf16 matrix of that shape; (0, 0) for None."""
-    if x is None:
-        return 0, 0
-    return _mat2(name, x, (ROWS_BF16,), rows, cols)[:2]
-
-
-def _vec(name, x, kinds, n):
-    """(pointer, kind) of a contiguous vector of n."""
-    if x is None:
-        _refuse(f"{name} is None")
-    kind = _kind(name, x)
-    if kind not in kinds:
-        _refuse(f"{name} has type {x.dtype}")
-    if x.shape != (n,) or not x.is_contiguous():
-        _refuse(f"{name} must be a contiguous vector of {n}")
-    return x.data_ptr(), kind
-
-
-_ID_BITS = {}
-
-
-def _ids(ids):
-    d = getattr(ids, "dtype", None)
-    bits = _ID_BITS.get(d)
-    if bits is None:
-        bits = {"torch.int32": 32, "torch.int64": 64}.get(str(d))
-        if bits is None:
-            _refuse(f"ids have type {d}")
-        _ID_BITS[d] = bits
-    if len(ids.shape) != 1 or not ids.is_contiguous():
-        _refuse("ids must be a contiguous vector")
-    return ids.data_ptr(), bits, ids.shape[0]
-
-
-def _tile_scale(name, s, rows, cols):
-    """Pointer of an FP8 weight's tile scales, [ceil(rows/128), ceil(cols/128)] or flat, contiguous."""
-    if s is None:
-        _refuse(f"{name} is None")
-    if _kind(name, s) != ROWS_FP32 or not s.is_contiguous() or s.numel() != -(-rows // 128) * -(-cols // 128):
-        _refuse(f"{name} must hold one contiguous fp32 scale per 128 x 128 tile of {rows} x {cols}")
-    return s.data_ptr()
+def _run(name, *args):
+    try:
+        rc = getattr(_calls or _layer(), name)(*args)
+    except (ValueError, AttributeError) as e:  # AttributeError: not a tensor
+        raise BQError(BQ_EINVAL, f"invalid argument: {e}") from None
+    if rc != BQ_OK:
+        _check(rc)
 
 
 def _ws(ws):
     return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-# bq_call's numbers and the layout of their arguments (q: integer or pointer, d: double)
-_CALLS = [struct.Struct(f).pack for f in (
-    "9qd3q", "5qd9q", "5qd12q", "18q", "9q", "15q", "13q", "15q")]
-CALL_EMBED, CALL_EMBED_GRAD, CALL_RMSNORM, CALL_RMSNORM_GRAD, CALL_QUANT, CALL_LINEAR, CALL_DX, CALL_DW = range(8)
-
-
-def _call(op, *args):
-    rc = load().bq_call(op, _CALLS[op](*args))
-    if rc != BQ_OK:
-        _check(rc)
-
-
 def embed(table, ids, out, scale=1.0, table_scale=None, stream=None):
     """out[t] = bf16(scale * table[ids[t]]); table bf16, or FP8 codes with table_scale
     (one fp32 scale per 128 x 128 tile).  An id outside the table gives a zero row."""
-    tp, ld, rows, cols, kind = _mat2("table", table, (ROWS_BF16, ROWS_FP8))
-    ip, bits, n = _ids(ids)
-    op, ldo = _mat2("out", out, (ROWS_BF16,), n, cols)[:2]
-    sp = _tile_scale("table_scale", table_scale, rows, cols) if kind == ROWS_FP8 else 0
-    _call(CALL_EMBED, tp, kind, sp, rows, cols, ld, ip, bits, n, scale, op, ldo, _stream(stream))
+    _run("embed", table, ids, out, scale, table_scale, _stream(stream))
 
 
 def embed_grad_workspace(n, rows, cols):
@@ -533,31 +463,14 @@ def embed_grad_workspace(n, rows, cols):
 def embed_grad(dy, ids, out, ws, scale=1.0, accumulate=False, stream=None):
     """out[v] = scale * sum of dy[t] over the tokens t of id v, every row of out
     written (accumulate: added to the rows that tokens name); out bf16 or fp32."""
-    ip, bits, n = _ids(ids)
-    op, ldo, rows, cols, kind = _mat2("out", out, (ROWS_BF16, ROWS_FP32))
-    dp, ldd = _mat2("dy", dy, (ROWS_BF16,), n, cols)[:2]
-    _call(CALL_EMBED_GRAD, dp, ldd, ip, bits, n, scale, rows, cols, op, kind, ldo, bool(accumulate), *_ws(ws),
-          _stream(stream))
-
-
-def _code_rows(name, codes, code_scale, n, cols):
-    cp, ldc = _mat2(name, codes, (ROWS_FP8,), n, cols)[:2]
-    sp, lds = _mat2(f"{name}'s scale", code_scale, (ROWS_FP32,), -(-cols // 128), n)[:2]
-    return cp, ldc, sp, lds
+    _run("embed_grad", dy, ids, out, *_ws(ws), scale, accumulate, _stream(stream))
 
 
 def rmsnorm(x, weight, eps, residual=None, h=None, y=None, codes=None, code_scale=None, rstd=None, stream=None):
     """h = bf16(x + residual), y = h / sqrt(mean(h^2) + eps) * weight; any of: h
     (needed with a residual), y in bf16, codes with code_scale [ceil(cols/128), n] (FP8
     rows of y), rstd (fp32, n)."""
-    xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
-    wp = _vec("weight", weight, (ROWS_BF16,), cols)[0]
-    rp, ldr = _rows("residual", residual, n, cols)
-    hp, ldh = _rows("h", h, n, cols)
-    yp, ldy = _rows("y", y, n, cols)
-    cp, ldc, sp, lds = (0, 0, 0, 0) if codes is None else _code_rows("codes", codes, code_scale, n, cols)
-    qp = 0 if rstd is None else _vec("rstd", rstd, (ROWS_FP32,), n)[0]
-    _call(CALL_RMSNORM, xp, ldx, rp, ldr, wp, eps, n, cols, hp, ldh, yp, ldy, cp, ldc, sp, lds, qp, _stream(stream))
+    _run("rmsnorm", x, weight, eps, residual, h, y, codes, code_scale, rstd, _stream(stream))
 
 
 def rmsnorm_grad_workspace(n, cols):
@@ -569,21 +482,12 @@ def rmsnorm_grad_workspace(n, cols):
 def rmsnorm_grad(dy, h, weight, rstd, dx, dw, ws, dh=None, accumulate=False, stream=None):
     """dx (of x and residual alike; dh, the gradient of h past the norm, is added) and
     dw (bf16 or fp32; accumulate: added to it) from dy and the forward's h and rstd."""
-    hp, ldh, n, cols, _ = _mat2("h", h, (ROWS_BF16,))
-    yp, ldy = _mat2("dy", dy, (ROWS_BF16,), n, cols)[:2]
-    wp = _vec("weight", weight, (ROWS_BF16,), cols)[0]
-    qp = _vec("rstd", rstd, (ROWS_FP32,), n)[0]
-    gp, ldg = _rows("dh", dh, n, cols)
-    xp, ldx = _mat2("dx", dx, (ROWS_BF16,), n, cols)[:2]
-    dp, kind = _vec("dw", dw, (ROWS_BF16, ROWS_FP32), cols)
-    _call(CALL_RMSNORM_GRAD, yp, ldy, hp, ldh, wp, qp, gp, ldg, n, cols, xp, ldx, dp, kind, bool(accumulate), *_ws(ws),
-          _stream(stream))
+    _run("rmsnorm_grad", dy, h, weight, rstd, dx, dw, *_ws(ws), dh, accumulate, _stream(stream))
 
 
 def quant_rows_fp8(x, codes, code_scale, stream=None):
     """FP8 rows of a bf16 matrix: codes, and code_scale [ceil(cols/128), n]."""
-    xp, ldx, n, cols, _ = _mat2("x", x, (ROWS_BF16,))
-    _call(CALL_QUANT, xp, ldx, n, cols, *_code_rows("codes", codes, code_scale, n, cols), _stream(stream))
+    _run("quant_rows_fp8", x, codes, code_scale, _stream(stream))
 
 
 def linear_fp8_workspace(n, rows, cols):
@@ -597,27 +501,17 @@ def linear_fp8_workspace(n, rows, cols):
 def linear_fp8(codes, code_scale, w, w_scale, out, ws, stream=None):
     """out [n, rows] = X W^T: X the FP8 rows (codes [n, cols], code_scale), W the FP8
     weight [rows, cols] with its tile scales."""
-    wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
-    n = codes.shape[0]
-    _call(CALL_LINEAR, *_code_rows("codes", codes, code_scale, n, cols), wp, ldw,
-          _tile_scale("w_scale", w_scale, rows, cols), n, rows, cols, *_mat2("out", out, (ROWS_BF16,), n, rows)[:2],
-          *_ws(ws), _stream(stream))
+    _run("linear_fp8", codes, code_scale, w, w_scale, out, *_ws(ws), _stream(stream))
 
 
 def linear_fp8_dx(dy, w, w_scale, dx, ws, stream=None):
     """dx [n, cols] = Q W: Q the FP8 rows of dy [n, rows] (quantised in the call)."""
-    wp, ldw, rows, cols, _ = _mat2("w", w, (ROWS_FP8,))
-    yp, ldy, n, _, _ = _mat2("dy", dy, (ROWS_BF16,), None, rows)
-    _call(CALL_DX, yp, ldy, wp, ldw, _tile_scale("w_scale", w_scale, rows, cols), n, rows, cols,
-          *_mat2("dx", dx, (ROWS_BF16,), n, cols)[:2], *_ws(ws), _stream(stream))
+    _run("linear_fp8_dx", dy, w, w_scale, dx, *_ws(ws), _stream(stream))
 
 
 def linear_fp8_dw(dy, codes, code_scale, dw, ws, accumulate=False, stream=None):
     """dw [rows, cols] = dy^T X (accumulate: added to dw), X the forward's FP8 rows."""
-    yp, ldy, n, rows, _ = _mat2("dy", dy, (ROWS_BF16,))
-    cols = codes.shape[1]
-    _call(CALL_DW, yp, ldy, *_code_rows("codes", codes, code_scale, n, cols), n, rows, cols,
-          *_mat2("dw", dw, (ROWS_BF16,), rows, cols)[:2], bool(accumulate), *_ws(ws), _stream(stream))
+    _run("linear_fp8_dw", dy, codes, code_scale, dw, *_ws(ws), accumulate, _stream(stream))
 
 
 def linear_check(ws, stream=None):

@@ -1,4 +1,5 @@
-"""Builds libbq.so in-tree for GB300 (sm_103a) with nvcc.
+"""Builds libbq.so in-tree for GB300 (sm_103a) with nvcc, and with the host compiler
+the CPython module that marshals the layer operators' arguments.
 
     python -m block_quant_gb300.build [--force] [--verbose]
 
@@ -13,11 +14,13 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libbq.so")
+CALLS = os.path.join(OUT_DIR, "_bqcall.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -33,6 +36,7 @@ SOURCES = {
     "row_ops.cu": ["-lineinfo"],
     "linear_fp8.cu": ["-lineinfo"],
 }
+BINDING = "binding.c"  # CPython module: argument marshalling of the layer operators
 HEADERS = ["bq_internal.h", "fp8_codes.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
 
 
@@ -45,7 +49,7 @@ def nvcc():
 
 def _digest():
     h = hashlib.sha256()
-    for name in sorted(list(SOURCES) + HEADERS):
+    for name in sorted(list(SOURCES) + HEADERS + [BINDING]):
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(name.encode() + f.read())
     with open(os.path.join(INCLUDE, "bq.h"), "rb") as f:
@@ -59,7 +63,7 @@ def build(force=False, verbose=False):
     os.makedirs(OUT_DIR, exist_ok=True)
     stamp = os.path.join(OUT_DIR, "libbq.stamp")
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
                 return LIB
@@ -71,6 +75,8 @@ def build(force=False, verbose=False):
         obj = os.path.join(OUT_DIR, name + ".o")
         objs.append(obj)
         cmds.append([cc, *ARCH, *COMMON, *extra, "-c", src, "-o", obj])
+    cmds.append([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-fPIC", "-shared", "-I",
+                 sysconfig.get_paths()["include"], os.path.join(CSRC, BINDING), "-o", CALLS + ".tmp"])
     if verbose:
         cmds = [c[:1] + ["-Xptxas", "-v"] + c[1:] if c[-3].endswith(".cu") else c for c in cmds]
 
@@ -93,6 +99,7 @@ def build(force=False, verbose=False):
         print(r.stdout + r.stderr)
         raise RuntimeError("link of libbq.so failed")
     os.replace(tmp, LIB)
+    os.replace(CALLS + ".tmp", CALLS)
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB
