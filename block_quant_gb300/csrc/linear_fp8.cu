@@ -23,11 +23,6 @@
 #include "tmem_ptx.h"
 #include "umma_ptx.h"
 
-// fewest 256 x 256 tiles for the CTA pairs
-#ifndef BQ_LINEAR_PAIR_MIN
-#define BQ_LINEAR_PAIR_MIN 60
-#endif
-
 namespace bq {
 namespace {
 
@@ -313,6 +308,10 @@ static_assert(SLOTS > PSTAGES + 2, "scale slots");
 constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
 constexpr int kPairTmem = 2 * PN;
+// Fewest tiles for the pairs (half of the pairs that run at once are 38): 32 tiles of 32
+// k-blocks take 16.6 us here and 15.7 us on k_linear's smaller tiles, 56 take 18.6 and
+// 24.0 us, 64 take 17.5 and 24.1 us.
+constexpr int kPairMin = 44;
 
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
@@ -623,7 +622,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
   if (pairs > 0x7FFFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  if (pairs >= BQ_LINEAR_PAIR_MIN) {
+  if (pairs >= kPairMin) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (unused without tma_out)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
@@ -649,9 +648,12 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   const int stage = B_STAGE + g.a_rows * BK, spare = (BM - g.a_rows) * BK;
   const int part = BM * kPartPitch * 4;
   g.stages = std::min(kMaxStages, (kSmem - 1024 - spare) / stage);
-  // k-blocks are split while the tiles leave resident CTAs idle and a share keeps
-  // at least four
-  while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk / (g.split * 2) >= 4) g.split *= 2;
+  // k-blocks are split while that leaves every CTA resident (a second wave costs a whole
+  // set-up: 64 tiles of 64 k-blocks, 14.0 us by 4 and 17.7 us by 8) and a share has one
+  // at least, by 8 four (24 tiles of 16: 5.2 us by 4, 6.3 us by 8; 3 tiles of 94: 12.2 and
+  // 8.7 us)
+  while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk >= (g.split == 4 ? 32 : g.split * 2))
+    g.split *= 2;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   const int smem = 1024 + std::max(part, g.stages * stage + spare);
   void* args[] = {&tx, &tw, &g};

@@ -41,9 +41,10 @@ int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 
 // forward: X's scales, where their own pitch does not serve; dx: codes and scales of
-// dy; dw: bf16 rows of X and, where dy's own pitch does not serve, of dy
+// dy; dw: bf16 rows of X and, where dy's own pitch does not serve, of dy, and the parts
+// of a product split over the tokens
 struct LinearWs {
-  size_t codes, scales, x, dy, bytes;
+  size_t codes, scales, x, dy, part, bytes;
 };
 
 int64_t up4(int64_t x) { return (x + 3) / 4 * 4; }
@@ -56,7 +57,9 @@ LinearWs linear_ws(int64_t n, int64_t rows, int64_t cols) {
   const size_t fwd = kStatusBytes + up(size_t((cols + 127) / 128) * size_t(up4(n)) * 4);
   p.x = kStatusBytes;
   p.dy = p.x + up(size_t(n) * size_t(up64(cols)) * 2);
-  const size_t dw = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
+  p.part = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
+  const int splits = gemm_tn_splits(n, rows, cols);
+  const size_t dw = p.part + (splits > 1 ? size_t(splits) * size_t(rows) * size_t(cols) * 4 : 0);
   p.bytes = std::max({dx, dw, fwd});
   return p;
 }
@@ -100,7 +103,7 @@ int bq_embed(const void* table, int kind, const float* table_scale, int64_t rows
 int bq_embed_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
   if (!bytes) return fail(BQ_EINVAL, "bq_embed_grad_workspace", "NULL argument");
   if (int rc = check_sizes("bq_embed_grad_workspace", n, rows, cols)) return rc;
-  *bytes = embed_grad_bytes(n, rows, cols);
+  *bytes = embed_grad_bytes(n, cols);
   return BQ_OK;
 }
 
@@ -116,7 +119,7 @@ int bq_embed_grad(const void* dy, int64_t ld_dy, const void* ids, int id_bits, i
   if (ld_dy < cols || ld_out < cols) return fail(BQ_EINVAL, who, "pitch below cols");
   if (off(dy, 2) || off(out, out_kind == BQ_ROWS_FP32 ? 4 : 2) || off(ids, uintptr_t(id_bits / 8)))
     return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
-  if (int rc = check_ws(who, ws, ws_bytes, embed_grad_bytes(n, rows, cols))) return rc;
+  if (int rc = check_ws(who, ws, ws_bytes, embed_grad_bytes(n, cols))) return rc;
   if (n == 0 && accumulate) return BQ_OK;
   return launch_embed_grad(EmbedGradArgs{dy, ids, out, ld_dy, n, rows, ld_out, scale, int(cols), id_bits, out_kind,
                                          accumulate ? 1 : 0},
@@ -263,18 +266,15 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
   if (off(dy, 2) || off(x_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
   auto* base = static_cast<unsigned char*>(ws);
   const int64_t ldxb = up64(cols);
-  if (int rc = launch_dequant_rows(x, ld_x, x_scale, ld_scale, n, int(cols), base + p.x, ldxb, stream)) return rc;
   // dy as it stands where the product's copies can read it: whole 64-column chunks
   // inside each row, 16-byte aligned rows
-  const void* a = dy;
-  int64_t lda = ld_dy;
-  if (off(dy, 16) || ld_dy % 8 || rows % 64) {
-    a = base + p.dy;
-    lda = up64(rows);
-    if (int rc = launch_copy_rows(dy, ld_dy, n, int(rows), base + p.dy, lda, stream)) return rc;
-  }
-  return launch_gemm_tn(a, lda, base + p.x, ldxb, n, int(rows), int(cols), dw, ld_dw, accumulate ? 1 : 0,
-                        static_cast<int*>(ws), stream);
+  const bool copy = off(dy, 16) || ld_dy % 8 || rows % 64;
+  const int64_t lda = copy ? up64(rows) : ld_dy;
+  if (int rc = launch_dw_inputs(x, ld_x, x_scale, ld_scale, n, int(cols), base + p.x, ldxb, copy ? dy : nullptr, ld_dy,
+                                int(rows), base + p.dy, lda, stream))
+    return rc;
+  return launch_gemm_tn(copy ? base + p.dy : dy, lda, base + p.x, ldxb, n, int(rows), int(cols), dw, ld_dw,
+                        accumulate ? 1 : 0, reinterpret_cast<float*>(base + p.part), static_cast<int*>(ws), stream);
 }
 
 int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream) {

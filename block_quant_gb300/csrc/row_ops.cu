@@ -1,9 +1,9 @@
 // Row-wise operators of a layer around the DBuffer step on GB300 (sm_103a):
 //   k_embed          rows of the token table (bf16, or E4M3 codes with 128x128
 //                    tile scales as the AllGather leaves them) times a factor
-//   k_embed_sort     stable sort of a batch's tokens by id (one cluster)
-//   k_embed_rows,    the table's gradient: rows of dY summed over equal ids, zeros
-//   k_embed_join     for the other rows
+//   k_embed_sort*    stable sort of a batch's tokens by id; zeros into the gradient
+//   k_embed_rows,    the table's gradient: rows of dY summed over equal ids
+//   k_embed_join, k_embed_few
 //   k_norm*          residual addition, root-mean-square norm, E4M3 codes with
 //                    one scale per 128 values of a row (also without the norm:
 //                    the row quantiser)
@@ -236,7 +236,7 @@ __device__ __forceinline__ float over_448(float a) {
   return __fmaf_rn(__fmaf_rn(-448.f, q, a), y, q);
 }
 
-// quant_span of N spans at once (aligned; N = 2 or 4), span i from column c0 + i * step:
+// quant_span of N spans at once (aligned; N = 1, 2 or 4), span i from column c0 + i * step:
 // the N maxima of a half-warp are reduced together, each step halving how many a lane
 // holds, so that one division pass serves all 2 N groups; the row kernels are bound by
 // instructions where every span reduces and divides for itself.
@@ -264,7 +264,7 @@ __device__ __forceinline__ void quant_spans(const float2 (*y)[4], int c0, int st
   }
 #pragma unroll
   for (; o; o >>= 1) a[0] = max_nan(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], o));
-  constexpr int kShift = N == 4 ? 2 : 3;  // lanes of a group: its span is (lane & 15) >> kShift
+  constexpr int kShift = N == 4 ? 2 : N == 2 ? 3 : 4;  // lanes of a group: its span is (lane & 15) >> kShift
   const int mine = c0 + ((lane & 15) >> kShift) * step + (lane >> 4) * 128;
   const bool store = (lane & ((1 << kShift) - 1)) == 0 && mine < cols;
   if (__all_sync(0xFFFFFFFFu, mine >= cols || (a[0] >= 7.8886091e-31f && a[0] <= 3.4028235e38f))) {
@@ -352,15 +352,21 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     if (FP8) {
       const uint8_t* row = static_cast<const uint8_t*>(table) + id * ldt;
       const float* srow = tscale + (id >> 7) * ((cols + 127) >> 7);
+      uint2 q[kSpans];
+      float qs[kSpans];
+#pragma unroll
+      for (int j = 0; j < kSpans; ++j) {
+        const int c = c0 + kSpan * j + 8 * lane;
+        if (VEC && c < cols) q[j] = __ldg(reinterpret_cast<const uint2*>(row + c)), qs[j] = __ldg(srow + (c >> 7));
+      }
 #pragma unroll
       for (int j = 0; j < kSpans; ++j) {
         if (VEC) {
           const int c = c0 + kSpan * j + 8 * lane;
           if (c >= cols) continue;
-          decode8(__ldg(reinterpret_cast<const uint2*>(row + c)), v[j]);
-          const float s = __ldg(srow + (c >> 7));
+          decode8(q[j], v[j]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[j][e] = __fmul_rn(v[j][e], s);
+          for (int e = 0; e < 8; ++e) v[j][e] = __fmul_rn(v[j][e], qs[j]);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -384,23 +390,93 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 }
 
 // ---------------------------------------------------------------- tokens sorted by id
+// By (id, position), so that equal ids keep their order.  Ids outside [0, rows) become
+// `rows` (last).  The sort is bound by latency on a few SMs; the same launch writes the
+// gradient's rows as zeros on the others (ZeroRows), which most of a large table stays.
 
-// A stable least-significant-digit radix sort of (id, position) in one launch: a
-// cluster of eight CTAs, each owning a contiguous eighth of the tokens.  Per
-// digit: CTA histograms, exchanged through distributed shared memory and scanned
-// by every CTA; then ranks in token order, 1024 x KEYS tokens a round, by warp match
-// and per-warp counters; the pairs go to the other buffer, which the cluster barrier
-// makes visible.  Ids outside [0, rows) become `rows` (last).  One launch of a cluster
-// instead of a device-wide sort: at the token counts of a training step the passes are
-// bound by latency (8192 tokens, 17 bits: two passes).
-// touched (NULL: not wanted): a bit per row that some token names.
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = 32;
+// Zeros of a CTA, in address order: a share of an eighth of an SM's, as the launch of
+// clusters of large CTAs is what bounds small shares (1.05 GB and 8192 tokens: 354 us at
+// 32 KB a CTA, 210 at 128 KB, 177 at 512 KB), at least 16 KB.
+constexpr int kZeroMin = 16384, kZeroRows = 8192;
+
+struct ZeroRows {
+  unsigned char* out;
+  int64_t rows, pitch;     // bytes
+  int row_bytes, each;     // rows a CTA
+  int word;                // bytes a store: 16, 4 or 2
+};
+
+// CTA `cta` of the zeros
+__device__ __forceinline__ void write_zeros(const ZeroRows& z, int64_t cta) {
+  const int64_t v0 = cta * z.each;
+  if (v0 >= z.rows) return;
+  const int count = int(min(int64_t(z.each), z.rows - v0)), per = z.row_bytes / z.word;
+  for (int i = threadIdx.x; i < count * per; i += blockDim.x) {
+    const int r = i / per;
+    unsigned char* o = z.out + (v0 + r) * z.pitch + int64_t(i - r * per) * z.word;
+    if (z.word == 16)
+      *reinterpret_cast<uint4*>(o) = make_uint4(0u, 0u, 0u, 0u);
+    else if (z.word == 4)
+      *reinterpret_cast<uint32_t*>(o) = 0u;
+    else
+      *reinterpret_cast<uint16_t*>(o) = 0;
+  }
+}
+
+__device__ __forceinline__ uint32_t sort_key(const void* ids, int bits, int64_t i, int rows) {
+  const int64_t id = load_id(ids, bits, i);
+  return id >= 0 && id < rows ? uint32_t(id) : uint32_t(rows);
+}
+
+// Up to 1024 tokens: CTA 0 sorts (id, position) pairs, distinct keys, by a bitonic network
+// in registers and shared memory.
+__global__ void __launch_bounds__(kSortThreads)
+    k_embed_sort_few(const void* __restrict__ ids, int id_bits, int n, int rows, int width, uint2* __restrict__ out,
+                     const ZeroRows z) {
+  __shared__ uint64_t swap[2][kSortThreads];
+  const int tid = threadIdx.x;
+  after_previous();
+  next_may_start();
+  if (blockIdx.x > 0) {
+    write_zeros(z, blockIdx.x - 1);
+    return;
+  }
+  uint64_t v = ~uint64_t(0);  // past the tokens: last
+  if (tid < n) v = (uint64_t(sort_key(ids, id_bits, tid, rows)) << 32) | uint32_t(tid);
+  int flip = 0;
+  for (int k = 2; k <= width; k <<= 1)  // width: a power of two, at least n
+    for (int j = k >> 1; j; j >>= 1) {
+      uint64_t o;
+      if (j >= 32) {
+        swap[flip][tid] = v;
+        __syncthreads();
+        o = swap[flip][tid ^ j];
+        flip ^= 1;
+      } else {
+        o = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+      }
+      const bool low = ((tid & j) == 0) == ((tid & k) == 0);  // keeps the smaller of the two
+      v = (v < o) == low ? v : o;
+    }
+  if (tid < n) out[tid] = make_uint2(uint32_t(v >> 32), uint32_t(v));
+}
+
+// More tokens: a stable least-significant-digit radix sort on a cluster of eight CTAs (the
+// grid's first), each owning a contiguous eighth of the tokens.  Per digit: CTA histograms,
+// exchanged through distributed shared memory and scanned by every CTA; then ranks in
+// token order, 1024 x KEYS tokens a round, by warp match and per-warp counters; the pairs
+// go to their CTA's shared memory where a thread has one token at most (KEYS == 1; the
+// last pass writes buf0 or buf1), to the other buffer otherwise, which the cluster barrier
+// makes visible.  8192 tokens of 17 bits take 12 us (the eight CTAs' bitonic sorts and a
+// search in one another's shared memory took 20).
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 
 struct SortSmem {
   uint32_t hist[kBins];               // this CTA's count of every digit (read by the whole cluster)
   uint32_t base[kBins];               // where this CTA's next token of a digit goes
-  uint32_t half[2][kBins];            // a round's count of every digit in warps 0-15, 16-31
+  uint2 pair[kSortThreads];           // KEYS == 1: this CTA's tokens between the passes (written by the whole cluster)
+  uint16_t half[2][kBins];            // a round's count of every digit in warps 0-15, 16-31
   uint32_t warp_sum[kSortWarps];
   uint16_t count[kSortWarps][kBins];  // a round's counts, then offsets, by warp
 };
@@ -408,38 +484,32 @@ struct SortSmem {
 template <int KEYS>
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1, 1)
     k_embed_sort(const void* __restrict__ ids, int id_bits, int n, int rows, int passes, uint2* __restrict__ buf0,
-                 uint2* __restrict__ buf1, uint32_t* __restrict__ touched) {
-  after_previous();
-  next_may_start();
+                 uint2* __restrict__ buf1, const ZeroRows z) {
   __shared__ SortSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = int(cluster_rank());
   const int seg = (n + kSortCtas - 1) / kSortCtas;
   const int lo = min(n, rank * seg), hi = min(n, lo + seg);
-  if (touched)
-    for (int i = rank * kSortThreads + tid; i < (rows >> 5) + 1; i += kSortCtas * kSortThreads) touched[i] = 0;
+  after_previous();
+  next_may_start();
+  if (blockIdx.x >= kSortCtas) {
+    write_zeros(z, blockIdx.x - kSortCtas);
+    return;
+  }
   for (int p = 0; p < passes; ++p) {
     const uint2* src = (p & 1) ? buf1 : buf0;  // pass 0 reads the ids themselves
     uint2* dst = (p & 1) ? buf0 : buf1;
     const int shift = p * kDigit;
     auto key_at = [&](int i) -> uint2 {
-      if (p > 0) return __ldcg(src + i);
-      const int64_t id = load_id(ids, id_bits, i);
-      return make_uint2(id >= 0 && id < rows ? uint32_t(id) : uint32_t(rows), uint32_t(i));
+      return p > 0 ? __ldcg(src + i) : make_uint2(sort_key(ids, id_bits, i, rows), uint32_t(i));
     };
     if (tid < kBins) sm.hist[tid] = 0;
     uint2 only = make_uint2(0u, 0u);  // KEYS == 1: a thread has one token at most
-    if (KEYS == 1 && lo + tid < hi) only = key_at(lo + tid);
+    if (KEYS == 1 && lo + tid < hi) only = p > 0 ? sm.pair[tid] : key_at(lo + tid);
     __syncthreads();
     for (int i = lo + tid; i < hi; i += kSortThreads)
       atomicAdd(&sm.hist[((KEYS == 1 ? only.x : key_at(i).x) >> shift) & (kBins - 1)], 1u);
-    if (p == 0) __threadfence();  // the cleared bits
     cluster_sync();
-    if (p == 0 && touched)
-      for (int i = lo + tid; i < hi; i += kSortThreads) {
-        const uint32_t v = KEYS == 1 ? only.x : key_at(i).x;
-        atomicOr(touched + (v >> 5), 1u << (v & 31));  // (bit `rows`: no row)
-      }
     // exclusive scan over (digit, CTA): thread d < kBins holds digit d
     uint32_t before = 0, total = 0;
     if (tid < kBins) {
@@ -505,19 +575,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
           sm.count[h * (kSortWarps / 2) + w][d] = uint16_t(run);
           run += c[w];
         }
-        sm.half[h][d] = run;
+        sm.half[h][d] = uint16_t(run);
       }
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < KEYS; ++j) {
         if (w0 + 32 * j + lane >= hi) continue;
         const uint32_t d = (kv[j].x >> shift) & (kBins - 1);
-        dst[sm.base[d] + (warp >= kSortWarps / 2 ? sm.half[0][d] : 0u) + sm.count[warp][d] + off[j]] = kv[j];
+        const uint32_t to = sm.base[d] + (warp >= kSortWarps / 2 ? sm.half[0][d] : 0u) + sm.count[warp][d] + off[j];
+        if (KEYS == 1 && p + 1 < passes) {  // (its owner's pairs were read before the histograms were exchanged)
+          const uint32_t cta = to / uint32_t(seg);
+          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(map_rank(smem_addr(&sm.pair[to - cta * uint32_t(seg)]), cta)),
+                       "r"(kv[j].x), "r"(kv[j].y)
+                       : "memory");
+        } else {
+          dst[to] = kv[j];
+        }
       }
       __syncthreads();
-      if (tid < kBins) sm.base[tid] += sm.half[0][tid] + sm.half[1][tid];
+      if (tid < kBins) sm.base[tid] += uint32_t(sm.half[0][tid]) + sm.half[1][tid];
     }
-    __threadfence();
+    if (KEYS > 1) __threadfence();
     cluster_sync();  // the next pass reads other CTAs' pairs; their histograms are done being read
   }
 }
@@ -525,15 +603,16 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
 // ---------------------------------------------------------------- embedding gradient
 
 // dT[v] (+)= f * sum of dY[t] over the tokens t of id v, summed in fp32 in token
-// order.  The sorted tokens are cut into pieces of kPiece.  A run of equal ids inside
+// order.  The sorted tokens are cut into pieces.  A run of equal ids inside
 // one piece is summed and its row written by the piece's CTA; of a run that crosses a
 // piece's end each piece's part is summed first, so that a token that fills the batch
 // is shared out over the whole GPU, and k_embed_join adds the parts in order.  No
-// atomics on values: the same batch gives the same bits.  Rows that no token names
-// (most of the table) are written as zeros by the same launch.
+// atomics: the same batch gives the same bits.
 // Slot of a piece's part: 2c for the one that starts with piece c, 2c + 1 otherwise.
-constexpr int kPiece = 32, kBatch = 8;   // tokens of a piece; rows of dY in flight
-constexpr int kZeroBytes = 16384;        // zeros a CTA writes, in address order: 7.6 TB/s (1 MB a CTA: 6.4)
+// A piece is 32 tokens, or 16 up to 2048 tokens, where its rounds of loads are what
+// takes the time (300 tokens: 14.1 us with 32, 11.6 with 16; 8192: 31.6 and 36.6).
+constexpr int kMaxPiece = 32, kBatch = 8;   // tokens of a piece at most; rows of dY in flight
+constexpr int piece_of(int64_t n) { return n <= 2048 ? 16 : 32; }
 
 template <bool VEC, typename Out>
 __device__ __forceinline__ void write_sum(Out* row, int c0, int cols, int lane, float scale, int accumulate, float* acc) {
@@ -551,41 +630,22 @@ __device__ __forceinline__ void write_sum(Out* row, int c0, int cols, int lane, 
 
 struct EmbedRows {
   const uint2* sorted;
-  const uint32_t* touched;
   const __nv_bfloat16* dy;
   float* sums;            // [2 pieces][ldp]
   int64_t ld, rows, ldo;
-  int n, cols, ldp, accumulate;
+  int n, cols, ldp, accumulate, piece;
   int groups;             // CTAs of a piece: kRowWarps spans each
-  int piece_ctas, zero_rows;  // CTAs of pieces (they come first); rows of a zero CTA
   float scale;
 };
 
 template <bool VEC, typename Out>
 __global__ void __launch_bounds__(32 * kRowWarps, 4) k_embed_rows(const EmbedRows a, Out* __restrict__ out) {
-  __shared__ uint32_t key[kPiece + 2], pos[kPiece];  // key[1 + i]: token i of the piece; 0, len + 1: its neighbours
+  __shared__ uint32_t key[kMaxPiece + 2], pos[kMaxPiece];  // key[1 + i]: token i of the piece; 0, len + 1: its neighbours
   const int tid = threadIdx.x, lane = tid & 31;
   after_previous();
   next_may_start();
-  if (int(blockIdx.x) >= a.piece_ctas) {
-    // zeros
-    constexpr int V = VEC ? 16 / int(sizeof(Out)) : 1;
-    const int64_t v0 = int64_t(int(blockIdx.x) - a.piece_ctas) * a.zero_rows;
-    const int count = int(min(int64_t(a.zero_rows), a.rows - v0)), per = a.cols / V;
-    for (int i = tid; i < count * per; i += 32 * kRowWarps) {
-      const int r = i / per;
-      const int64_t v = v0 + r;
-      if (a.n > 0 && (__ldg(a.touched + (v >> 5)) >> (v & 31)) & 1u) continue;
-      Out* o = out + v * a.ldo + int64_t(i - r * per) * V;
-      if (VEC)
-        *reinterpret_cast<uint4*>(o) = make_uint4(0u, 0u, 0u, 0u);
-      else
-        *o = Out(0.f);
-    }
-    return;
-  }
   const int piece = int(blockIdx.x) / a.groups;
-  const int b = piece * kPiece, len = min(kPiece, a.n - b);
+  const int b = piece * a.piece, len = min(a.piece, a.n - b);
   if (tid < len + 2) {
     const int i = b + tid - 1;
     const uint2 kv = i >= 0 && i < a.n ? a.sorted[i] : make_uint2(0xFFFFFFFFu, 0u);
@@ -627,11 +687,89 @@ __global__ void __launch_bounds__(32 * kRowWarps, 4) k_embed_rows(const EmbedRow
   }
 }
 
+// Up to kFewTokens tokens: the whole gradient in one launch, without a sort.  The CTAs of
+// token t (one a group of spans) look through all ids: if t is the first of its id they
+// sum that id's tokens in order.  The others write zeros into the rows that no token names.
+constexpr int kFewTokens = 256;
+template <bool VEC, typename Out>
+__global__ void __launch_bounds__(32 * kRowWarps, 4)
+    k_embed_few(const EmbedRows a, const void* __restrict__ ids, int id_bits, const ZeroRows z, Out* __restrict__ out) {
+  __shared__ uint32_t list[kFewTokens], named[kZeroRows / 32];
+  __shared__ int count;
+  const int tid = threadIdx.x, lane = tid & 31;
+  after_previous();
+  next_may_start();
+  const uint32_t id = tid < a.n ? sort_key(ids, id_bits, tid, int(a.rows)) : uint32_t(a.rows);
+  if (int(blockIdx.x) >= a.n * a.groups) {
+    const int64_t cta = int64_t(blockIdx.x) - int64_t(a.n) * a.groups, v0 = cta * z.each;
+    for (int i = tid; i < (z.each + 31) / 32; i += 32 * kRowWarps) named[i] = 0;
+    __syncthreads();
+    const int64_t at = int64_t(id) - v0;
+    const bool mine = id < uint32_t(a.rows) && at >= 0 && at < z.each;
+    if (mine) atomicOr(&named[at >> 5], 1u << (at & 31));
+    if (!__syncthreads_or(mine)) {
+      write_zeros(z, cta);
+      return;
+    }
+    const int rows = int(min(int64_t(z.each), z.rows - v0));
+    for (int r = tid >> 5; r < rows; r += kRowWarps) {
+      if ((named[r >> 5] >> (r & 31)) & 1u) continue;
+      unsigned char* o = z.out + (v0 + r) * z.pitch;
+      for (int i = lane * z.word; i < z.row_bytes; i += 32 * z.word) {
+        if (z.word == 16)
+          *reinterpret_cast<uint4*>(o + i) = make_uint4(0u, 0u, 0u, 0u);
+        else if (z.word == 4)
+          *reinterpret_cast<uint32_t*>(o + i) = 0u;
+        else
+          *reinterpret_cast<uint16_t*>(o + i) = 0;
+      }
+    }
+    return;
+  }
+  const int t = int(blockIdx.x) / a.groups;
+  list[tid] = id;
+  __syncthreads();
+  const uint32_t want = list[t];
+  if (want >= uint32_t(a.rows)) return;
+  const bool same = id == want;
+  if (__syncthreads_or(same && tid < t)) return;  // (also: every thread has read list[t])
+  if (tid < 32) {  // its tokens, in order
+    int n = 0;
+    for (int i0 = 0; i0 < kFewTokens; i0 += 32) {
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, list[i0 + lane] == want);
+      __syncwarp();
+      if ((hit >> lane) & 1u) list[n + __popc(hit & ((1u << lane) - 1u))] = uint32_t(i0 + lane);
+      n += __popc(hit);
+      __syncwarp();
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int c0 = ((int(blockIdx.x) - t * a.groups) * kRowWarps + (tid >> 5)) * kSpan;
+  if (c0 >= a.cols) return;
+  float acc[8] = {};
+  for (int i0 = 0; i0 < count; i0 += kBatch) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k < count) w[k] = load_packed<VEC>(a.dy + int64_t(list[i0 + k]) * a.ld, c0, a.cols, lane);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k >= count) continue;
+      float v[8];
+      unpack8(w[k], v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
+    }
+  }
+  write_sum<VEC>(out + int64_t(want) * a.ldo, c0, a.cols, lane, a.scale, a.accumulate, acc);
+}
+
 // rows whose run begins in piece blockIdx.x / groups and goes on past its end
 template <bool VEC, typename Out>
 __global__ void __launch_bounds__(32 * kRowWarps) k_embed_join(const EmbedRows a, Out* __restrict__ out) {
   const int lane = threadIdx.x & 31;
-  const int piece = int(blockIdx.x) / a.groups, b = piece * kPiece, e = b + kPiece;
+  const int piece = int(blockIdx.x) / a.groups, b = piece * a.piece, e = b + a.piece;
   after_previous();
   next_may_start();
   if (e >= a.n) return;
@@ -645,15 +783,20 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_embed_join(const EmbedRows a
   load_f32<true>(a.sums + int64_t(2 * piece + (from_start ? 0 : 1)) * a.ldp, c0, a.ldp, lane, acc);
   // the pieces after it that start with the same id, 32 at a time
   for (int p = piece + 1;; p += 32) {
-    const int at = (p + lane) * kPiece;
+    const int at = (p + lane) * a.piece;
     const uint32_t same = __ballot_sync(0xFFFFFFFFu, at < a.n && a.sorted[at].x == id);
     const int count = same == 0xFFFFFFFFu ? 32 : __ffs(int(~same)) - 1;
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-      float v[8];
-      load_f32<true>(a.sums + int64_t(2 * (p + k)) * a.ldp, c0, a.ldp, lane, v);
+    for (int k0 = 0; k0 < count; k0 += 8) {
+      float v[8][8];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[x]);
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < count) load_f32<true>(a.sums + int64_t(2 * (p + k0 + k)) * a.ldp, c0, a.ldp, lane, v[k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k0 + k < count) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) acc[x] = __fadd_rn(acc[x], v[k][x]);
+        }
     }
     if (count < 32) break;
   }
@@ -755,7 +898,7 @@ __device__ __forceinline__ uint4 shared16(uint32_t at) {
 // that loads are in flight while a row waits for its sum (with a CTA per row they are
 // not).  A thread reads only what it copied: no barrier but the sum's.
 template <int VPT>
-__global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_many(const NormArgs a, int64_t n, int depth) {
+__global__ void __launch_bounds__(VPT <= 2 ? 1024 : 512, 1) k_norm_many(const NormArgs a, int64_t n, int depth) {
   after_previous();
   next_may_start();
   extern __shared__ __align__(16) unsigned char ring[];
@@ -823,8 +966,8 @@ __global__ void __launch_bounds__(row_threads(VPT), VPT <= 2 ? 2 : 1) k_norm_man
   }
 }
 
-// a warp quantises kSpans spans of a row
-template <bool VEC>
+// a warp quantises N spans of a row
+template <bool VEC, int N>
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_quant_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, uint8_t* __restrict__ codes,
                  int64_t ldc, float* __restrict__ scale, int64_t lds, int segs) {
@@ -834,18 +977,18 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   const int64_t t = item / segs;
   if (t >= n) return;
-  const int c0 = int(item - t * segs) * kSeg;
-  uint4 w[kSpans];
+  const int c0 = int(item - t * segs) * N * kSpan;
+  uint4 w[N];
 #pragma unroll
-  for (int j = 0; j < kSpans; ++j) w[j] = load_packed<VEC>(x + t * ldx, c0 + kSpan * j, cols, lane);
-  if (VEC) {
-    float2 v[kSpans][4];
+  for (int j = 0; j < N; ++j) w[j] = load_packed<VEC>(x + t * ldx, c0 + kSpan * j, cols, lane);
+  if (VEC && N > 1) {
+    float2 v[N][4];
 #pragma unroll
-    for (int j = 0; j < kSpans; ++j) unpack8(w[j], v[j]);
-    quant_spans<kSpans>(v, c0, kSpan, cols, lane, codes + t * ldc, scale + t, lds);
+    for (int j = 0; j < N; ++j) unpack8(w[j], v[j]);
+    quant_spans<N>(v, c0, kSpan, cols, lane, codes + t * ldc, scale + t, lds);
   } else {
 #pragma unroll
-    for (int j = 0; j < kSpans; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (c0 + kSpan * j >= cols) break;
       float v[8];
       unpack8(w[j], v);
@@ -854,43 +997,59 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   }
 }
 
-// bf16(scale * code) of E4M3 rows with one scale per 128 values, pitch ldo (for the
-// weight gradient's product); cols is a multiple of 16, so every vector is aligned
-__global__ void __launch_bounds__(32 * kRowWarps)
-    k_dequant_rows(const uint8_t* __restrict__ codes, int64_t ldc, const float* __restrict__ scale, int64_t lds,
-                   int64_t n, int cols, __nv_bfloat16* __restrict__ out, int64_t ldo, int spans) {
+// The weight gradient's operands in bf16 at pitches of their own: scale * code of E4M3
+// rows with one scale per 128 values (cols is a multiple of 16, so every vector is
+// aligned), by the first x_items warps; and, by the others, dY where its own pitch does
+// not serve.
+struct DwInputs {
+  const uint8_t* codes;
+  const float* scale;
+  const __nv_bfloat16* dy;
+  __nv_bfloat16 *x_out, *dy_out;
+  int64_t ldc, lds, ldo, ldy, ldyo, x_items, items;
+  int cols, x_spans, rows, y_spans;
+};
+
+__global__ void __launch_bounds__(32 * kRowWarps) k_dw_inputs(const DwInputs a) {
   after_previous();
   next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int64_t t = item / spans;
-  if (t >= n) return;
-  const int c = int(item - t * spans) * kSpan + 8 * lane;
-  if (c >= cols) return;
-  float v[8];
-  decode8(__ldg(reinterpret_cast<const uint2*>(codes + t * ldc + c)), v);
-  const float s = __ldg(scale + int64_t(c >> 7) * lds + t);
+  if (item < a.x_items) {
+    const int64_t t = item / a.x_spans;
+    const int c = int(item - t * a.x_spans) * kSpan + 8 * lane;
+    if (c >= a.cols) return;
+    float v[8];
+    decode8(__ldg(reinterpret_cast<const uint2*>(a.codes + t * a.ldc + c)), v);
+    const float s = __ldg(a.scale + int64_t(c >> 7) * a.lds + t);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], s);
-  *reinterpret_cast<uint4*>(out + t * ldo + c) = pack8(v);
+    for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], s);
+    *reinterpret_cast<uint4*>(a.x_out + t * a.ldo + c) = pack8(v);
+  } else if (item < a.items) {
+    const int64_t i = item - a.x_items, t = i / a.y_spans;
+    const int c0 = int(i - t * a.y_spans) * kSpan;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = c0 + 32 * e + lane;
+      if (c < a.rows) a.dy_out[t * a.ldyo + c] = a.dy[t * a.ldy + c];
+    }
+  }
 }
 
-// bf16 rows copied to a pitch of their own
-__global__ void __launch_bounds__(32 * kRowWarps)
-    k_copy_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, __nv_bfloat16* __restrict__ out,
-                int64_t ldo, int spans) {
+// dw = sum of the parts in order (+ dw), bf16
+__global__ void __launch_bounds__(256) k_dw_join(const float* __restrict__ part, int parts, int64_t m, int n, int64_t stride,
+                                                 __nv_bfloat16* __restrict__ out, int64_t ldo, int accumulate) {
   after_previous();
   next_may_start();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int64_t t = item / spans;
-  if (t >= n) return;
-  const int c0 = int(item - t * spans) * kSpan;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = c0 + 32 * e + lane;
-    if (c < cols) out[t * ldo + c] = x[t * ldx + c];
-  }
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= m * n) return;
+  const int64_t r = i / n;
+  __nv_bfloat16* o = out + r * ldo + (i - r * n);
+  float s = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) s += part[p * stride + i];
+  if (accumulate) s += __bfloat162float(*o);
+  *o = __float2bfloat16_rn(s);
 }
 
 // ---------------------------------------------------------------- norm gradient
@@ -907,7 +1066,7 @@ struct NormGradArgs {
 // u = h rstd, t = dy w: dx = rstd (t - u mean(t u)) + dh, dw = sum over rows of dy u.
 // CTAs walk the rows blockIdx.x, + gridDim.x, ...; a thread keeps its columns' dw.
 template <bool VEC, int VPT>
-__global__ void __launch_bounds__(row_threads(VPT)) k_norm_grad(const NormGradArgs a) {
+__global__ void __launch_bounds__(1024, 1) k_norm_grad(const NormGradArgs a) {
   after_previous();
   next_may_start();
   __shared__ float part[2][32];
@@ -1070,11 +1229,16 @@ __global__ void __launch_bounds__(1024)
 
 bool vec_ok(const void* p, int64_t ld, int values) { return aligned16(p) && ld % values == 0; }
 
-// warps of a one-CTA-per-row kernel and spans a warp, within row_threads(spans a
-// warp) threads for rows of up to 65536 columns
-void row_shape(int cols, int* warps, int* vpt) {
+// The norm's warps a row and spans a warp (VPT), within row_threads(VPT) threads for rows
+// of up to 65536 columns.  Four spans a warp: what a warp does once a row is a third of
+// its instructions with two (4096 columns: 43.5 us with two, 41.3 with four); fewer where
+// four would leave a fifth or more of the lanes idle.  One shape for any number of rows,
+// so that a row's sum does not depend on the rows beside it.
+// Rows that are not aligned are bound by their 2-byte accesses and want the warps (4095
+// columns: 69 us with two spans, 94 us with four).
+void norm_shape(int cols, bool vec, int* warps, int* vpt) {
   const int spans = (cols + kSpan - 1) / kSpan;
-  *vpt = spans <= 32 ? 2 : spans <= 64 ? 4 : 8;
+  *vpt = spans > 64 ? 8 : spans == 1 ? 1 : spans == 2 || spans == 5 || spans == 6 || (!vec && spans <= 32) ? 2 : 4;
   *warps = (spans + *vpt - 1) / *vpt;
 }
 
@@ -1085,37 +1249,36 @@ int bits_of(int64_t x) {
 }
 
 struct EmbedGradPlan {
-  size_t off_b0, off_b1, off_touched, off_sums, bytes;
+  size_t off_b0, off_b1, off_sums, bytes;
   int ldp, pieces;
 };
 
-EmbedGradPlan embed_grad_plan(int64_t n, int64_t rows, int64_t cols) {
+EmbedGradPlan embed_grad_plan(int64_t n, int64_t cols) {
   EmbedGradPlan p;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   p.ldp = int((cols + kSpan - 1) / kSpan * kSpan);
-  p.pieces = int((n + kPiece - 1) / kPiece);
+  p.pieces = int((n + piece_of(n) - 1) / piece_of(n));
   p.off_b0 = 0;
   p.off_b1 = up(size_t(n) * 8);
-  p.off_touched = p.off_b1 + up(size_t(n) * 8);
-  p.off_sums = p.off_touched + up((size_t(rows) / 32 + 1) * 4);
-  p.bytes = p.off_sums + up(size_t(p.pieces) * 2 * size_t(p.ldp) * 4);
+  p.off_sums = p.off_b1 + up(size_t(n) * 8);
+  p.bytes = std::max<size_t>(256, p.off_sums + up(size_t(p.pieces) * 2 * size_t(p.ldp) * 4));
   return p;
 }
 
 // The ring of a kernel whose resident CTAs walk many rows: slots (0: it does not fit,
 // or there are too few rows for it) and CTAs an SM, for `warps` warps a CTA and
 // row_bytes of shared memory a row.  A CTA's barrier stalls it once a row, so an SM runs
-// up to eight of them, within 1024 threads (64 registers each).
+// several of them, up to `most`, within `threads` threads (what the registers allow).
 struct Ring {
   int depth, per_sm;
 };
 
 constexpr int kRingBytes = 224 * 1024, kMaxDepth = 8;
 
-Ring ring_of(int warps, int row_bytes, int64_t n) {
+Ring ring_of(int warps, int row_bytes, int64_t n, int threads, int most) {
   Ring r;
-  r.per_sm = std::max(1, std::min(8, 32 / warps));
-  r.depth = std::min(kMaxDepth, (kRingBytes / r.per_sm - 1024) / row_bytes);
+  r.per_sm = std::max(1, std::min(most, threads / (32 * warps)));
+  r.depth = std::min(kMaxDepth, (kRingBytes / r.per_sm - 1280) / row_bytes);
   if (r.depth < 3 || n < int64_t(2) * r.per_sm * sm_count()) r.depth = 0;
   return r;
 }
@@ -1125,28 +1288,19 @@ struct NormGradPlan {
 };
 
 // vec: every row of the operands is 16-byte aligned and of whole vectors.  The direct
-// kernel takes what the ring does not; ctas is the larger of the two where vec is not
-// known yet (a workspace's size).
+// kernel (depth 0) takes what the ring does not.
 NormGradPlan norm_grad_plan(int64_t n, int cols, int ins, bool vec) {
   NormGradPlan p;
   const int spans = (cols + kSpan - 1) / kSpan;
-  p.vpt = spans <= 32 ? 1 : 2;
+  p.vpt = spans <= 32 ? 1 : spans <= 64 ? 2 : 8;
   p.warps = (spans + p.vpt - 1) / p.vpt;
-  p.depth = 0;
-  if (vec && p.warps <= 32) {
-    const int row = ins * p.vpt * p.warps * 512;
-    const Ring r = ring_of(p.warps, row, n);
-    if (r.depth) {
-      p.depth = r.depth, p.smem = r.depth * row;
-      // as few CTAs as give every one the same number of rows, or one less
-      const int64_t most = int64_t(sm_count()) * r.per_sm, each = (n + most - 1) / most;
-      p.ctas = int((n + each - 1) / each);
-      return p;
-    }
-  }
-  row_shape(cols, &p.warps, &p.vpt);
-  p.smem = 0;
-  p.ctas = int(std::min<int64_t>(n, int64_t(sm_count()) * 2));
+  p.depth = 0, p.smem = 0;
+  const int row = ins * p.vpt * p.warps * 512;
+  const Ring r = ring_of(p.warps, row, n, 1024, 8);  // (each CTA leaves a part of dw)
+  if (vec && p.vpt <= 2 && r.depth) p.depth = r.depth, p.smem = r.depth * row;
+  // as few CTAs as give every one the same number of rows, or one less
+  const int64_t most = int64_t(sm_count()) * r.per_sm, each = (n + most - 1) / most;
+  p.ctas = n > 0 ? int((n + each - 1) / each) : 0;
   return p;
 }
 
@@ -1165,17 +1319,17 @@ int launch_embed(const EmbedArgs& a, void* stream) {
   return check("bq_embed");
 }
 
-size_t embed_grad_bytes(int64_t n, int64_t rows, int64_t cols) { return embed_grad_plan(n, rows, cols).bytes; }
+size_t embed_grad_bytes(int64_t n, int64_t cols) { return embed_grad_plan(n, cols).bytes; }
 
 namespace {
 
 template <bool VEC, typename Out>
-int embed_rows(const EmbedRows& a, unsigned zero_ctas, int pieces, Out* out, cudaStream_t s) {
-  const unsigned ctas = unsigned(a.piece_ctas) + zero_ctas;
+int embed_rows(const EmbedRows& a, int pieces, Out* out, cudaStream_t s) {
+  const unsigned ctas = unsigned(pieces) * unsigned(a.groups);
   launch_after(k_embed_rows<VEC, Out>, ctas, 32 * kRowWarps, 0, s, a, out);
   if (int rc = check("bq_embed_grad (rows)")) return rc;
   if (pieces < 2) return BQ_OK;  // no run crosses a piece's end
-  launch_after(k_embed_join<VEC, Out>, unsigned(a.piece_ctas), 32 * kRowWarps, 0, s, a, out);
+  launch_after(k_embed_join<VEC, Out>, ctas, 32 * kRowWarps, 0, s, a, out);
   return check("bq_embed_grad (join)");
 }
 
@@ -1183,38 +1337,57 @@ int embed_rows(const EmbedRows& a, unsigned zero_ctas, int pieces, Out* out, cud
 
 int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const EmbedGradPlan p = embed_grad_plan(g.n, g.rows, g.cols);
+  const EmbedGradPlan p = embed_grad_plan(g.n, g.cols);
   auto* w = static_cast<unsigned char*>(ws);
   auto* b0 = reinterpret_cast<uint2*>(w + p.off_b0);
   auto* b1 = reinterpret_cast<uint2*>(w + p.off_b1);
-  auto* touched = reinterpret_cast<uint32_t*>(w + p.off_touched);
   const bool f32 = g.out_kind == BQ_ROWS_FP32;
-  const bool vec = g.cols % 8 == 0 && vec_ok(g.dy, g.ld_dy, 8) && vec_ok(g.out, g.ldo, f32 ? 4 : 8);
+  const int size = f32 ? 4 : 2;
+  const bool vec = g.cols % 8 == 0 && vec_ok(g.dy, g.ld_dy, 8) && vec_ok(g.out, g.ldo, 16 / size);
   const int passes = (bits_of(g.rows) + kDigit - 1) / kDigit;
+  const int n = int(g.n);
   EmbedRows a;
-  a.sorted = (passes & 1) ? b1 : b0;
-  a.touched = touched;
+  a.sorted = n <= kSortThreads || !(passes & 1) ? b0 : b1;
   a.dy = static_cast<const __nv_bfloat16*>(g.dy);
   a.sums = reinterpret_cast<float*>(w + p.off_sums);
-  a.ld = g.ld_dy, a.rows = g.rows, a.ldo = g.ldo, a.n = int(g.n), a.cols = g.cols, a.ldp = p.ldp;
-  a.accumulate = g.accumulate, a.scale = g.scale;
+  a.ld = g.ld_dy, a.rows = g.rows, a.ldo = g.ldo, a.n = n, a.cols = g.cols, a.ldp = p.ldp;
+  a.accumulate = g.accumulate, a.scale = g.scale, a.piece = piece_of(g.n);
   a.groups = (g.cols + kRowWarps * kSpan - 1) / (kRowWarps * kSpan);
   if (int64_t(p.pieces) * a.groups > 0x3FFFFFFF) return set_error(BQ_EINVAL, "bq_embed_grad: batch too large");
-  a.piece_ctas = p.pieces * a.groups;
-  a.zero_rows = std::max(1, kZeroBytes / (g.cols * (f32 ? 4 : 2)));
-  const unsigned zero_ctas = g.accumulate ? 0u : unsigned((g.rows + a.zero_rows - 1) / a.zero_rows);
-  if (g.n > 0) {
-    auto* k = g.n <= kSortCtas * kSortThreads ? k_embed_sort<1> : k_embed_sort<4>;
-    launch_after(k, kSortCtas, kSortThreads, 0, s, g.ids, g.id_bits, a.n, int(g.rows), passes, b0, b1,
-                 g.accumulate ? nullptr : touched);
-    if (int rc = check("bq_embed_grad (sort)")) return rc;
+  ZeroRows z;
+  z.out = static_cast<unsigned char*>(g.out);
+  z.rows = g.rows, z.pitch = g.ldo * size, z.row_bytes = g.cols * size;
+  // (the one launch for few tokens has small CTAs)
+  const int64_t share = n <= kFewTokens ? 32768 : g.rows * z.row_bytes / (int64_t(sm_count()) * 8);
+  z.each = int(std::min<int64_t>(kZeroRows, std::max<int64_t>(1, std::max<int64_t>(kZeroMin, share) / z.row_bytes)));
+  z.word = vec_ok(g.out, g.ldo, 16 / size) && z.row_bytes % 16 == 0 ? 16 : size;
+  const unsigned zeros = g.accumulate ? 0u : unsigned((g.rows + z.each - 1) / z.each);
+  if (n <= kFewTokens) {
+    const unsigned ctas = unsigned(n * a.groups) + zeros;
+    if (f32)
+      launch_after(vec ? k_embed_few<true, float> : k_embed_few<false, float>, ctas, 32 * kRowWarps, 0, s, a, g.ids,
+                   g.id_bits, z, static_cast<float*>(g.out));
+    else
+      launch_after(vec ? k_embed_few<true, __nv_bfloat16> : k_embed_few<false, __nv_bfloat16>, ctas, 32 * kRowWarps, 0, s,
+                   a, g.ids, g.id_bits, z, static_cast<__nv_bfloat16*>(g.out));
+    return check("bq_embed_grad");
   }
+  if (n <= kSortThreads) {
+    int width = 32;
+    while (width < n) width *= 2;
+    launch_after(k_embed_sort_few, 1 + zeros, kSortThreads, 0, s, g.ids, g.id_bits, n, int(g.rows), width, b0, z);
+  } else {
+    auto* k = n <= kSortCtas * kSortThreads ? k_embed_sort<1> : k_embed_sort<4>;
+    launch_after(k, (kSortCtas + zeros + kSortCtas - 1) / kSortCtas * kSortCtas, kSortThreads, 0, s, g.ids, g.id_bits, n,
+                 int(g.rows), passes, b0, b1, z);
+  }
+  if (int rc = check("bq_embed_grad (sort)")) return rc;
   if (f32) {
     auto* out = static_cast<float*>(g.out);
-    return vec ? embed_rows<true>(a, zero_ctas, p.pieces, out, s) : embed_rows<false>(a, zero_ctas, p.pieces, out, s);
+    return vec ? embed_rows<true>(a, p.pieces, out, s) : embed_rows<false>(a, p.pieces, out, s);
   }
   auto* out = static_cast<__nv_bfloat16*>(g.out);
-  return vec ? embed_rows<true>(a, zero_ctas, p.pieces, out, s) : embed_rows<false>(a, zero_ctas, p.pieces, out, s);
+  return vec ? embed_rows<true>(a, p.pieces, out, s) : embed_rows<false>(a, p.pieces, out, s);
 }
 
 namespace {
@@ -1222,7 +1395,8 @@ namespace {
 // the ring kernels' shared-memory attribute, set once per device
 int ring_attrs() {
   if (!once_per_device(kOnceRingAttr)) return BQ_OK;
-  const void* kernels[] = {reinterpret_cast<const void*>(k_norm_many<2>), reinterpret_cast<const void*>(k_norm_many<4>),
+  const void* kernels[] = {reinterpret_cast<const void*>(k_norm_many<1>), reinterpret_cast<const void*>(k_norm_many<2>),
+                           reinterpret_cast<const void*>(k_norm_many<4>),
                            reinterpret_cast<const void*>(k_norm_grad_many<1>),
                            reinterpret_cast<const void*>(k_norm_grad_many<2>)};
   for (const void* k : kernels)
@@ -1248,20 +1422,23 @@ int launch_rmsnorm(const RmsnormArgs& r, void* stream) {
                    aligned16(r.weight) && (!r.h || vec_ok(r.h, r.ld_h, 8)) && (!r.y || vec_ok(r.y, r.ld_y, 8)) &&
                    (!r.codes || ((reinterpret_cast<uintptr_t>(r.codes) & 7) == 0 && r.ld_codes % 8 == 0));
   int warps, vpt;
-  row_shape(r.cols, &warps, &vpt);
+  norm_shape(r.cols, vec, &warps, &vpt);
   if (vec && vpt <= 4) {
     const int row = (r.residual ? 2 : 1) * vpt * warps * 512;
-    const Ring ring = ring_of(warps, row, r.n);
+    const Ring ring = ring_of(warps, row, r.n, vpt <= 2 ? 1024 : 512, 32);
     if (ring.depth) {
-      auto* many = vpt == 2 ? k_norm_many<2> : k_norm_many<4>;
+      auto* many = vpt == 1 ? k_norm_many<1> : vpt == 2 ? k_norm_many<2> : k_norm_many<4>;
       if (int rc = ring_attrs()) return rc;
       const int64_t most = int64_t(sm_count()) * ring.per_sm, each = (r.n + most - 1) / most;
       launch_after(many, unsigned((r.n + each - 1) / each), 32 * warps, size_t(ring.depth * row), s, a, r.n, ring.depth);
       return check("bq_rmsnorm");
     }
   }
-  auto* k = vec ? (vpt == 2 ? k_norm<true, 2> : vpt == 4 ? k_norm<true, 4> : k_norm<true, 8>)
-                : (vpt == 2 ? k_norm<false, 2> : vpt == 4 ? k_norm<false, 4> : k_norm<false, 8>);
+  auto* k = vec ? (vpt == 1 ? k_norm<true, 1> : vpt == 2 ? k_norm<true, 2> : vpt == 4 ? k_norm<true, 4> : k_norm<true, 8>)
+                : (vpt == 1   ? k_norm<false, 1>
+                   : vpt == 2 ? k_norm<false, 2>
+                   : vpt == 4 ? k_norm<false, 4>
+                              : k_norm<false, 8>);
   launch_after(k, unsigned(r.n), 32 * warps, 0, s, a);
   return check("bq_rmsnorm");
 }
@@ -1270,36 +1447,43 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
                       int64_t lds, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = cols % 8 == 0 && vec_ok(x, ldx, 8) && (reinterpret_cast<uintptr_t>(codes) & 7) == 0 && ldc % 8 == 0;
-  const int segs = (cols + kSeg - 1) / kSeg;
+  // four spans a warp share one division pass (8192 x 14336: 57 us, 75 with one); one
+  // where that would not give every scheduler a warp
+  const int spans = (cols + kSpan - 1) / kSpan;
+  const int each = n * ((spans + 3) / 4) >= int64_t(sm_count()) * 4 ? 4 : 1;
+  const int segs = (spans + each - 1) / each;
   const int64_t ctas = (n * segs + kRowWarps - 1) / kRowWarps;
-  auto* k = vec ? k_quant_rows<true> : k_quant_rows<false>;
-  launch_after(k, unsigned(ctas), 32 * kRowWarps, 0, s, static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc, scale, lds,
-                                              segs);
+  auto* k = each == 4 ? (vec ? k_quant_rows<true, 4> : k_quant_rows<false, 4>)
+                      : (vec ? k_quant_rows<true, 1> : k_quant_rows<false, 1>);
+  launch_after(k, unsigned(ctas), 32 * kRowWarps, 0, s, static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc,
+               scale, lds, segs);
   return check("bq_quant_rows_fp8");
 }
 
-int launch_dequant_rows(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols,
-                        void* out, int64_t ldo, void* stream) {
-  const int spans = (cols + kSpan - 1) / kSpan;
-  const int64_t ctas = (n * spans + kRowWarps - 1) / kRowWarps;
-  launch_after(k_dequant_rows, unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream),
-      codes, ldc, scale, lds, n, cols, static_cast<__nv_bfloat16*>(out), ldo, spans);
-  return check("bq_linear_fp8_dw (input)");
+int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
+                     int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream) {
+  DwInputs a;
+  a.codes = codes, a.scale = scale, a.dy = static_cast<const __nv_bfloat16*>(dy);
+  a.x_out = static_cast<__nv_bfloat16*>(x_out), a.dy_out = static_cast<__nv_bfloat16*>(dy_out);
+  a.ldc = ldc, a.lds = lds, a.ldo = ldo, a.ldy = ldy, a.ldyo = ldyo;
+  a.cols = cols, a.rows = rows;
+  a.x_spans = (cols + kSpan - 1) / kSpan, a.y_spans = (rows + kSpan - 1) / kSpan;
+  a.x_items = n * a.x_spans, a.items = a.x_items + (dy ? n * a.y_spans : 0);
+  launch_after(k_dw_inputs, unsigned((a.items + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, 0,
+               static_cast<cudaStream_t>(stream), a);
+  return check("bq_linear_fp8_dw (inputs)");
 }
 
-int launch_copy_rows(const void* x, int64_t ldx, int64_t n, int cols, void* out, int64_t ldo, void* stream) {
-  const int spans = (cols + kSpan - 1) / kSpan;
-  const int64_t ctas = (n * spans + kRowWarps - 1) / kRowWarps;
-  launch_after(k_copy_rows, unsigned(ctas), 32 * kRowWarps, 0, static_cast<cudaStream_t>(stream),
-      static_cast<const __nv_bfloat16*>(x), ldx, n, cols, static_cast<__nv_bfloat16*>(out), ldo, spans);
-  return check("bq_linear_fp8_dw (copy)");
+int launch_dw_join(const float* part, int parts, int64_t m, int n, int64_t stride, void* out, int64_t ldo, int accumulate,
+                   void* stream) {
+  launch_after(k_dw_join, unsigned((m * n + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream), part, parts, m, n,
+               stride, static_cast<__nv_bfloat16*>(out), ldo, accumulate);
+  return check("bq_linear_fp8_dw (join)");
 }
 
 size_t rmsnorm_grad_bytes(int64_t n, int64_t cols) {
   const size_t ldp = size_t((cols + kSpan - 1) / kSpan * kSpan);
-  // the ring takes the most CTAs with the fewest operands; the direct kernel may have more
-  int ctas = norm_grad_plan(n, int(cols), 2, false).ctas;
-  for (int ins = 2; ins <= 3; ++ins) ctas = std::max(ctas, norm_grad_plan(n, int(cols), ins, true).ctas);
+  const int ctas = norm_grad_plan(n, int(cols), 2, false).ctas;  // (whatever the operands)
   return std::max<size_t>(256, size_t(ctas) * ldp * 4);
 }
 
@@ -1323,8 +1507,8 @@ int launch_rmsnorm_grad(const RmsnormGradArgs& r, void* ws, void* stream) {
     auto* k = p.vpt == 1 ? k_norm_grad_many<1> : k_norm_grad_many<2>;
     launch_after(k, unsigned(p.ctas), 32 * p.warps, size_t(p.smem), s, a, p.depth);
   } else if (p.ctas > 0) {
-    auto* k = vec ? (p.vpt == 2 ? k_norm_grad<true, 2> : p.vpt == 4 ? k_norm_grad<true, 4> : k_norm_grad<true, 8>)
-                  : (p.vpt == 2 ? k_norm_grad<false, 2> : p.vpt == 4 ? k_norm_grad<false, 4> : k_norm_grad<false, 8>);
+    auto* k = vec ? (p.vpt == 1 ? k_norm_grad<true, 1> : p.vpt == 2 ? k_norm_grad<true, 2> : k_norm_grad<true, 8>)
+                  : (p.vpt == 1 ? k_norm_grad<false, 1> : p.vpt == 2 ? k_norm_grad<false, 2> : k_norm_grad<false, 8>);
     launch_after(k, unsigned(p.ctas), 32 * p.warps, 0, s, a);
   }
   if (int rc = check("bq_rmsnorm_grad")) return rc;

@@ -26,7 +26,7 @@ struct EmbedGradArgs {
   float scale;
   int cols, id_bits, out_kind, accumulate;
 };
-size_t embed_grad_bytes(int64_t n, int64_t rows, int64_t cols);
+size_t embed_grad_bytes(int64_t n, int64_t cols);
 int launch_embed_grad(const EmbedGradArgs& a, void* ws, void* stream);  // n may be 0
 
 struct RmsnormArgs {
@@ -52,9 +52,11 @@ int launch_rmsnorm_grad(const RmsnormGradArgs& a, void* ws, void* stream);  // n
 
 int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* codes, int64_t ldc, float* scale,
                       int64_t lds, void* stream);
-int launch_dequant_rows(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols,
-                        void* out, int64_t ldo, void* stream);
-int launch_copy_rows(const void* x, int64_t ldx, int64_t n, int cols, void* out, int64_t ldo, void* stream);
+// bf16 rows of X (from FP8 rows) and of dY (dy NULL: not wanted) at pitches ldo, ldyo
+int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
+                     int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
+int launch_dw_join(const float* part, int parts, int64_t m, int n, int64_t stride, void* out, int64_t ldo, int accumulate,
+                   void* stream);
 
 // FP8 projections (linear_fp8.cu)
 struct LinearArgs {
@@ -73,8 +75,10 @@ struct LinearArgs {
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 
 // D [m, n] (+)= A^T B over t rows, bf16, A [t, m] and B [t, n] with pitches that
-// are multiples of 64 elements (ns_gemm.cu)
+// are multiples of 64 elements (ns_gemm.cu).  A product with too few tiles for the GPU is
+// split over the rows, its fp32 parts (gemm_tn_splits of them, m * n values each) in part.
+int gemm_tn_splits(int64_t t, int64_t m, int64_t n);
 int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t t, int m, int n, void* D,
-                   int64_t ldd, int accumulate, int* status, void* stream);
+                   int64_t ldd, int accumulate, float* part, int* status, void* stream);
 
 }  // namespace bq

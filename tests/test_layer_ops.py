@@ -142,6 +142,8 @@ def test_embed_of_no_tokens_and_one(cuda):
     (1, 1, 8, "any"), (1, 1000, 264, "any"), (31, 7, 136, "any"), (32, 7, 128, "one"), (33, 7, 128, "one"),
     (64, 65, 8, "one"), (65, 64, 16, "any"), (700, 300, 520, "zipf"), (1000, 513, 131, "zipf"), (777, 90, 1, "one"),
     (5000, 70000, 24, "zipf"), (9000, 300000, 8, "any"), (40000, 1200, 8, "zipf"), (257, 200, 2880, "out"),
+    (256, 40000, 16, "any"), (256, 3, 264, "zipf"), (200, 70, 2056, "one"), (1024, 5000, 136, "zipf"), (1025, 5000, 136, "one"),
+    (8192, 600, 24, "zipf"), (8193, 600, 24, "any"),
 ])
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 @pytest.mark.parametrize("accumulate", [False, True])
