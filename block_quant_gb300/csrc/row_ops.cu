@@ -1,7 +1,8 @@
 // Row-wise operators of a layer around the DBuffer step on GB300 (sm_103a):
 //   k_embed          rows of the token table (bf16, or E4M3 codes with 128x128
 //                    tile scales as the AllGather leaves them) times a factor
-//   k_embed_sort*    stable sort of a batch's tokens by id; zeros into the gradient
+//   k_embed_chunks,  stable sort of a batch's tokens by id; zeros into the gradient
+//   k_embed_place, k_embed_sort
 //   k_embed_rows,    the table's gradient: rows of dY summed over equal ids
 //   k_embed_join, k_embed_few
 //   k_norm*          residual addition, root-mean-square norm, E4M3 codes with
@@ -391,13 +392,13 @@ __global__ void __launch_bounds__(32 * kRowWarps)
 
 // ---------------------------------------------------------------- tokens sorted by id
 // By (id, position), so that equal ids keep their order.  Ids outside [0, rows) become
-// `rows` (last).  The sort is bound by latency on a few SMs; the same launch writes the
-// gradient's rows as zeros on the others (ZeroRows), which most of a large table stays.
+// `rows` (last).  The same launch writes the gradient's rows as zeros (ZeroRows), which
+// most of a large table stays.
 
 constexpr int kSortCtas = 8, kSortThreads = 1024, kSortWarps = 32;
-// Zeros of a CTA, in address order: a share of an eighth of an SM's, as the launch of
-// clusters of large CTAs is what bounds small shares (1.05 GB and 8192 tokens: 354 us at
-// 32 KB a CTA, 210 at 128 KB, 177 at 512 KB), at least 16 KB.
+// Zeros of a CTA, in address order: 16 KB (1.05 GB at 7.6 TB/s, 6.4 at 1 MB a CTA); beside
+// the radix sort, whose clusters of large CTAs are slow to launch, an eighth of an SM's
+// share (1.05 GB: 354 us at 32 KB, 210 at 128 KB, 177 at 512 KB).
 constexpr int kZeroMin = 16384, kZeroRows = 8192;
 
 struct ZeroRows {
@@ -429,23 +430,28 @@ __device__ __forceinline__ uint32_t sort_key(const void* ids, int bits, int64_t 
   return id >= 0 && id < rows ? uint32_t(id) : uint32_t(rows);
 }
 
-// Up to 1024 tokens: CTA 0 sorts (id, position) pairs, distinct keys, by a bitonic network
-// in registers and shared memory.
-__global__ void __launch_bounds__(kSortThreads)
-    k_embed_sort_few(const void* __restrict__ ids, int id_bits, int n, int rows, int width, uint2* __restrict__ out,
-                     const ZeroRows z) {
-  __shared__ uint64_t swap[2][kSortThreads];
+// Up to 8192 tokens, first half: each CTA sorts a chunk of 256 tokens by a bitonic network
+// over distinct (id, position) keys, in registers and shared memory.  key, pos: the
+// chunks one after another, padded to whole chunks with maximal ids.
+constexpr int kChunk = 32 * kRowWarps, kChunkTokens = 8192;
+
+__global__ void __launch_bounds__(kChunk)
+    k_embed_chunks(const void* __restrict__ ids, int id_bits, int n, int rows, uint32_t* __restrict__ key,
+                   uint32_t* __restrict__ pos, const ZeroRows z) {
+  __shared__ uint64_t swap[2][kChunk];
   const int tid = threadIdx.x;
   after_previous();
   next_may_start();
-  if (blockIdx.x > 0) {
-    write_zeros(z, blockIdx.x - 1);
+  const int chunks = (n + kChunk - 1) / kChunk;
+  if (int(blockIdx.x) >= chunks) {
+    write_zeros(z, int(blockIdx.x) - chunks);
     return;
   }
-  uint64_t v = ~uint64_t(0);  // past the tokens: last
-  if (tid < n) v = (uint64_t(sort_key(ids, id_bits, tid, rows)) << 32) | uint32_t(tid);
+  const int i = int(blockIdx.x) * kChunk + tid;
+  uint64_t v = ~uint64_t(0);
+  if (i < n) v = (uint64_t(sort_key(ids, id_bits, i, rows)) << 32) | uint32_t(i);
   int flip = 0;
-  for (int k = 2; k <= width; k <<= 1)  // width: a power of two, at least n
+  for (int k = 2; k <= kChunk; k <<= 1)
     for (int j = k >> 1; j; j >>= 1) {
       uint64_t o;
       if (j >= 32) {
@@ -459,29 +465,65 @@ __global__ void __launch_bounds__(kSortThreads)
       const bool low = ((tid & j) == 0) == ((tid & k) == 0);  // keeps the smaller of the two
       v = (v < o) == low ? v : o;
     }
-  if (tid < n) out[tid] = make_uint2(uint32_t(v >> 32), uint32_t(v));
+  key[i] = uint32_t(v >> 32);
+  pos[i] = uint32_t(v);
+}
+
+// Second half: a token's place is its place in its chunk and, by a binary search in each
+// other chunk, the number of tokens there before it: ids up to its own in the chunks
+// before, smaller ids in the chunks after.  Four threads a token share the chunks.
+// A radix sort on a cluster (below) takes as long for 8192 tokens, but its large CTAs hold
+// up the zeros beside it (8192 tokens of a 128256 x 4096 table: 169 us in all, 182 with it);
+// comparing every token with every other in one launch took 20 us more.
+constexpr int kPlaceEach = 64;
+__global__ void __launch_bounds__(4 * kPlaceEach)
+    k_embed_place(const uint32_t* __restrict__ key, const uint32_t* __restrict__ pos, int n, uint2* __restrict__ out) {
+  __shared__ __align__(16) uint32_t all[kChunkTokens];
+  const int tid = threadIdx.x, chunks = (n + kChunk - 1) / kChunk;
+  after_previous();
+  next_may_start();
+#pragma unroll 8
+  for (int i = tid; i < chunks * (kChunk / 4); i += 4 * kPlaceEach)
+    reinterpret_cast<uint4*>(all)[i] = reinterpret_cast<const uint4*>(key)[i];
+  const int i = int(blockIdx.x) * kPlaceEach + (tid >> 2);
+  const uint32_t p = i < chunks * kChunk ? pos[i] : 0u;
+  __syncthreads();
+  const int home = i / kChunk;
+  const uint32_t mine = home < chunks ? all[i] : 0xFFFFFFFFu;
+  int place = 0;
+  for (int c = tid & 3; c < chunks; c += 4) {
+    if (c == home) {
+      place += i - home * kChunk;
+      continue;
+    }
+    const uint32_t* k = all + c * kChunk;
+    const uint32_t first = c < home ? mine + 1 : mine;  // the smallest id that does not come before it
+    int at = 0;
+#pragma unroll
+    for (int step = kChunk / 2; step; step >>= 1)
+      if (k[at + step - 1] < first) at += step;
+    place += at + (k[at] < first ? 1 : 0);
+  }
+  place += __shfl_xor_sync(0xFFFFFFFFu, place, 1);
+  place += __shfl_xor_sync(0xFFFFFFFFu, place, 2);
+  if ((tid & 3) == 0 && mine != 0xFFFFFFFFu) out[place] = make_uint2(mine, p);  // (not the padding)
 }
 
 // More tokens: a stable least-significant-digit radix sort on a cluster of eight CTAs (the
 // grid's first), each owning a contiguous eighth of the tokens.  Per digit: CTA histograms,
 // exchanged through distributed shared memory and scanned by every CTA; then ranks in
-// token order, 1024 x KEYS tokens a round, by warp match and per-warp counters; the pairs
-// go to their CTA's shared memory where a thread has one token at most (KEYS == 1; the
-// last pass writes buf0 or buf1), to the other buffer otherwise, which the cluster barrier
-// makes visible.  8192 tokens of 17 bits take 12 us (the eight CTAs' bitonic sorts and a
-// search in one another's shared memory took 20).
-constexpr int kDigit = 9, kBins = 1 << kDigit;
+// token order, 1024 x kSortKeys tokens a round, by warp match and per-warp counters; the pairs
+// go to the other buffer, which the cluster barrier makes visible.
+constexpr int kDigit = 9, kBins = 1 << kDigit, kSortKeys = 4;
 
 struct SortSmem {
   uint32_t hist[kBins];               // this CTA's count of every digit (read by the whole cluster)
   uint32_t base[kBins];               // where this CTA's next token of a digit goes
-  uint2 pair[kSortThreads];           // KEYS == 1: this CTA's tokens between the passes (written by the whole cluster)
-  uint16_t half[2][kBins];            // a round's count of every digit in warps 0-15, 16-31
+  uint32_t half[2][kBins];            // a round's count of every digit in warps 0-15, 16-31
   uint32_t warp_sum[kSortWarps];
   uint16_t count[kSortWarps][kBins];  // a round's counts, then offsets, by warp
 };
 
-template <int KEYS>
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1, 1)
     k_embed_sort(const void* __restrict__ ids, int id_bits, int n, int rows, int passes, uint2* __restrict__ buf0,
                  uint2* __restrict__ buf1, const ZeroRows z) {
@@ -504,11 +546,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
       return p > 0 ? __ldcg(src + i) : make_uint2(sort_key(ids, id_bits, i, rows), uint32_t(i));
     };
     if (tid < kBins) sm.hist[tid] = 0;
-    uint2 only = make_uint2(0u, 0u);  // KEYS == 1: a thread has one token at most
-    if (KEYS == 1 && lo + tid < hi) only = p > 0 ? sm.pair[tid] : key_at(lo + tid);
     __syncthreads();
-    for (int i = lo + tid; i < hi; i += kSortThreads)
-      atomicAdd(&sm.hist[((KEYS == 1 ? only.x : key_at(i).x) >> shift) & (kBins - 1)], 1u);
+    for (int i = lo + tid; i < hi; i += kSortThreads) atomicAdd(&sm.hist[(key_at(i).x >> shift) & (kBins - 1)], 1u);
     cluster_sync();
     // exclusive scan over (digit, CTA): thread d < kBins holds digit d
     uint32_t before = 0, total = 0;
@@ -539,20 +578,20 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
       sm.base[tid] = prior + x - total + before;
     }
     // ranks, in token order
-    for (int r0 = lo; r0 < hi; r0 += kSortThreads * KEYS) {
+    for (int r0 = lo; r0 < hi; r0 += kSortThreads * kSortKeys) {
       uint4* clear = reinterpret_cast<uint4*>(sm.count);
       for (int i = tid; i < kSortWarps * kBins / 8; i += kSortThreads) clear[i] = make_uint4(0u, 0u, 0u, 0u);
-      uint2 kv[KEYS];
-      uint32_t off[KEYS];
-      const int w0 = r0 + warp * 32 * KEYS;
+      uint2 kv[kSortKeys];
+      uint32_t off[kSortKeys];
+      const int w0 = r0 + warp * 32 * kSortKeys;
 #pragma unroll
-      for (int j = 0; j < KEYS; ++j) {
+      for (int j = 0; j < kSortKeys; ++j) {
         const int i = w0 + 32 * j + lane;
-        if (i < hi) kv[j] = KEYS == 1 ? only : key_at(i);
+        if (i < hi) kv[j] = key_at(i);
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < KEYS; ++j) {
+      for (int j = 0; j < kSortKeys; ++j) {
         const bool on = w0 + 32 * j + lane < hi;
         const uint32_t d = on ? (kv[j].x >> shift) & (kBins - 1) : kBins;
         const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
@@ -575,27 +614,19 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortCtas, 1
           sm.count[h * (kSortWarps / 2) + w][d] = uint16_t(run);
           run += c[w];
         }
-        sm.half[h][d] = uint16_t(run);
+        sm.half[h][d] = run;
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < KEYS; ++j) {
+      for (int j = 0; j < kSortKeys; ++j) {
         if (w0 + 32 * j + lane >= hi) continue;
         const uint32_t d = (kv[j].x >> shift) & (kBins - 1);
-        const uint32_t to = sm.base[d] + (warp >= kSortWarps / 2 ? sm.half[0][d] : 0u) + sm.count[warp][d] + off[j];
-        if (KEYS == 1 && p + 1 < passes) {  // (its owner's pairs were read before the histograms were exchanged)
-          const uint32_t cta = to / uint32_t(seg);
-          asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(map_rank(smem_addr(&sm.pair[to - cta * uint32_t(seg)]), cta)),
-                       "r"(kv[j].x), "r"(kv[j].y)
-                       : "memory");
-        } else {
-          dst[to] = kv[j];
-        }
+        dst[sm.base[d] + (warp >= kSortWarps / 2 ? sm.half[0][d] : 0u) + sm.count[warp][d] + off[j]] = kv[j];
       }
       __syncthreads();
-      if (tid < kBins) sm.base[tid] += uint32_t(sm.half[0][tid]) + sm.half[1][tid];
+      if (tid < kBins) sm.base[tid] += sm.half[0][tid] + sm.half[1][tid];
     }
-    if (KEYS > 1) __threadfence();
+    __threadfence();
     cluster_sync();  // the next pass reads other CTAs' pairs; their histograms are done being read
   }
 }
@@ -1260,7 +1291,7 @@ EmbedGradPlan embed_grad_plan(int64_t n, int64_t cols) {
   p.pieces = int((n + piece_of(n) - 1) / piece_of(n));
   p.off_b0 = 0;
   p.off_b1 = up(size_t(n) * 8);
-  p.off_sums = p.off_b1 + up(size_t(n) * 8);
+  p.off_sums = p.off_b1 + up(size_t(n + kChunk) * 8);
   p.bytes = std::max<size_t>(256, p.off_sums + up(size_t(p.pieces) * 2 * size_t(p.ldp) * 4));
   return p;
 }
@@ -1347,7 +1378,7 @@ int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
   const int passes = (bits_of(g.rows) + kDigit - 1) / kDigit;
   const int n = int(g.n);
   EmbedRows a;
-  a.sorted = n <= kSortThreads || !(passes & 1) ? b0 : b1;
+  a.sorted = n <= kChunkTokens || !(passes & 1) ? b0 : b1;
   a.dy = static_cast<const __nv_bfloat16*>(g.dy);
   a.sums = reinterpret_cast<float*>(w + p.off_sums);
   a.ld = g.ld_dy, a.rows = g.rows, a.ldo = g.ldo, a.n = n, a.cols = g.cols, a.ldp = p.ldp;
@@ -1357,8 +1388,7 @@ int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
   ZeroRows z;
   z.out = static_cast<unsigned char*>(g.out);
   z.rows = g.rows, z.pitch = g.ldo * size, z.row_bytes = g.cols * size;
-  // (the one launch for few tokens has small CTAs)
-  const int64_t share = n <= kFewTokens ? 32768 : g.rows * z.row_bytes / (int64_t(sm_count()) * 8);
+  const int64_t share = n <= kChunkTokens ? 0 : g.rows * z.row_bytes / (int64_t(sm_count()) * 8);
   z.each = int(std::min<int64_t>(kZeroRows, std::max<int64_t>(1, std::max<int64_t>(kZeroMin, share) / z.row_bytes)));
   z.word = vec_ok(g.out, g.ldo, 16 / size) && z.row_bytes % 16 == 0 ? 16 : size;
   const unsigned zeros = g.accumulate ? 0u : unsigned((g.rows + z.each - 1) / z.each);
@@ -1372,14 +1402,18 @@ int launch_embed_grad(const EmbedGradArgs& g, void* ws, void* stream) {
                    a, g.ids, g.id_bits, z, static_cast<__nv_bfloat16*>(g.out));
     return check("bq_embed_grad");
   }
-  if (n <= kSortThreads) {
-    int width = 32;
-    while (width < n) width *= 2;
-    launch_after(k_embed_sort_few, 1 + zeros, kSortThreads, 0, s, g.ids, g.id_bits, n, int(g.rows), width, b0, z);
+  if (n <= kChunkTokens) {
+    // (chunks of ids and positions: n rounded up to whole chunks, in the second buffer)
+    const int chunks = (n + kChunk - 1) / kChunk;
+    auto* key = reinterpret_cast<uint32_t*>(b1);
+    auto* pos = key + chunks * kChunk;
+    launch_after(k_embed_chunks, unsigned(chunks) + zeros, kChunk, 0, s, g.ids, g.id_bits, n, int(g.rows), key, pos, z);
+    if (int rc = check("bq_embed_grad (chunks)")) return rc;
+    launch_after(k_embed_place, unsigned((chunks * kChunk + kPlaceEach - 1) / kPlaceEach), 4 * kPlaceEach, 0, s,
+                 static_cast<const uint32_t*>(key), static_cast<const uint32_t*>(pos), n, b0);
   } else {
-    auto* k = n <= kSortCtas * kSortThreads ? k_embed_sort<1> : k_embed_sort<4>;
-    launch_after(k, (kSortCtas + zeros + kSortCtas - 1) / kSortCtas * kSortCtas, kSortThreads, 0, s, g.ids, g.id_bits, n,
-                 int(g.rows), passes, b0, b1, z);
+    launch_after(k_embed_sort, (kSortCtas + zeros + kSortCtas - 1) / kSortCtas * kSortCtas, kSortThreads, 0, s, g.ids,
+                 g.id_bits, n, int(g.rows), passes, b0, b1, z);
   }
   if (int rc = check("bq_embed_grad (sort)")) return rc;
   if (f32) {
