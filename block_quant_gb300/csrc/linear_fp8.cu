@@ -308,7 +308,8 @@ static_assert(SLOTS > PSTAGES + 2, "scale slots");
 constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
 constexpr int kPairTmem = 2 * PN;
-// Fewest tiles for the pairs (half of the pairs that run at once are 38): 32 tiles of 32
+// The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
+// 5952 take 28 us there and 17 us on k_linear) and at least so many tiles (half of the pairs that run at once are 38): 32 tiles of 32
 // k-blocks take 16.6 us here and 15.7 us on k_linear's smaller tiles, 56 take 18.6 and
 // 24.0 us, 64 take 17.5 and 24.1 us.
 constexpr int kPairMin = 44;
@@ -622,7 +623,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
   if (pairs > 0x7FFFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  if (pairs >= kPairMin) {
+  if (a.n > BM && pairs >= kPairMin) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (unused without tma_out)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
