@@ -186,6 +186,10 @@ int encode_map_2d(void* map, const void* base, int elem_bytes, int64_t cols, int
 // a 2-D tiled tensor map with 128-byte swizzle over `outer` rows of `inner` E4M3
 // codes at base with row pitch `pitch`; boxes of 128 codes x box_outer rows.
 int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_outer);
+// bf16 rows read as 64-column chunks of 64 rows with 128-byte swizzle: chunks > 0, a 3-D
+// map whose boxes hold that many chunks (the last chunk of the last row reads up to the
+// next multiple of 64 columns: the pitch must cover it); 0, a 2-D map with boxes of one
+int encode_map_chunks(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int chunks);
 // a 2-D tiled tensor map over the fp32 scales of FP8 rows, [groups][pitch]: boxes of
 // one group's scales of 128 rows
 int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, int64_t pitch);
@@ -197,6 +201,6 @@ int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows,
 int set_error(int code, const std::string& msg);
 int sm_count();  // SMs of the current device (cached per device)
 bool once_per_device(int key);  // true once per (current device, key); keys below
-constexpr int kOnceStripAttr = 0, kOnceGemmAttr = 1, kOnceTileAttr = 2, kOnceLinearAttr = 3, kOnceRingAttr = 4;
+constexpr int kOnceStripAttr = 0, kOnceGemmAttr = 1, kOnceTileAttr = 2, kOnceLinearAttr = 3, kOnceRingAttr = 4, kOnceDwAttr = 5;
 
 }  // namespace bq

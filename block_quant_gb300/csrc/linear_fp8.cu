@@ -324,6 +324,51 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
+// A warp's box of out, 32 rows x 32 bf16 in shared memory with 64-byte swizzle: 16-byte word
+// c of row r at word c ^ ((r >> 1) & 3).  v: the lane's row.
+__device__ __forceinline__ void put_box(const float* v, uint32_t box, int lane) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[8 * c + 2 * e], v[8 * c + 2 * e + 1]);
+      o[e] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    const uint32_t to = box + 64u * uint32_t(lane) + 16u * uint32_t(c ^ ((lane >> 1) & 3));
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                 : "memory");
+  }
+}
+
+// the box to out's row0.., c0.., clipped to rows x cols: by TMA, or where out's rows are not
+// 16-byte aligned by plain stores, lane l column l of each row
+__device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int tma_out,
+                                          const CUtensorMap* map, int row0, int c0, uint32_t box, int lane) {
+  if (tma_out) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0 && row0 < rows && c0 < cols) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(c0), "r"(row0), "r"(box)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  } else {
+    __syncwarp();
+    for (int r = 0; r < 32 && row0 + r < rows; ++r) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];"
+                   : "=h"(v)
+                   : "r"(box + 64u * uint32_t(r) + 16u * uint32_t((lane >> 3) ^ ((r >> 1) & 3)) + 2u * uint32_t(lane & 7))
+                   : "memory");
+      if (c0 + lane < cols) out[int64_t(row0 + r) * ldo + c0 + lane] = __ushort_as_bfloat16(v);
+    }
+    __syncwarp();
+  }
+}
+
 template <bool TRANS>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -491,47 +536,206 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         if (!ok) break;
       }
       if (!ok) break;
-      // the warp's bf16 box of each unit, 64-byte swizzle: 16-byte word c of row r at word c ^ ((r >> 1) & 3)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
         __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float* v = acc + 32 * u + 8 * c + 2 * e;
-            const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]);
-            o[e] = *reinterpret_cast<const uint32_t*>(&p);
+        put_box(acc + 32 * u, box, lane);
+        store_box(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + SEG * u, box, lane);
+      }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+
+// ---------------------------------------------------------------- weight gradient
+// dW = dY^T X in bf16 on the same pairs and tiles: both operands MN-major (a token's row
+// holds 64-column chunks of 128 bytes), the summed index is the tokens, one accumulator of
+// a tile's whole sum, two of them in turn.  The tile leaves as in k_linear_pair; a split
+// product's fp32 sums leave from registers.
+constexpr int DK = 64;                          // tokens of a k-block
+constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
+constexpr int DW_SMEM = 1024 + PSTAGES * PSTAGE_BYTES + PEPI * OUT_BOX;
+
+struct DwKernelArgs {
+  __nv_bfloat16* out;
+  float* part;           // [splits][rows][cols], or NULL
+  int64_t ldo, n;
+  int rows, cols, splits;
+  int chunk_boxes;       // dY's copies bring one chunk each, not two
+  int accumulate, tma_out;
+  int* status;
+};
+
+// Instruction descriptor, kind::f16: D fp32, A and B bf16, both MN-major
+constexpr uint32_t kDwIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t(PN >> 3) << 17) |
+                              (uint32_t(PM >> 4) << 24);
+
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    k_dw_pair(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmO, const DwKernelArgs g) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(PSTAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 + b); };
+
+  const int rank = int(cluster_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (g.rows + PM - 1) / PM, nt = (g.cols + PN - 1) / PN, ntiles = mt * nt, total = ntiles * g.splits;
+  const int nk = int((g.n + DK - 1) / DK);
+  const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
+  // tile t: share t / ntiles of the tokens' blocks [k0, k1)
+  auto tile_of = [&](int t, int& bm, int& bn, int& sp, int& k0, int& k1) {
+    sp = t / ntiles;
+    banded_tile(t - sp * ntiles, mt, nt, kBand, bm, bn);
+    k0 = int(int64_t(nk) * sp / g.splits);
+    k1 = int(int64_t(nk) * (sp + 1) / g.splits);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(full_bar(s), 1);   // the leader's expect_tx
+      mbar_init(empty_bar(s), 1);  // the leader's commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * PEPI);  // the epilogue warps of both CTAs
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  after_previous();
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  next_may_start();
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs: this CTA's halves)
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += npairs) {
+      int bm, bn, sp, k0, k1;
+      tile_of(t, bm, bn, sp, k0, k1);
+      const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % PSTAGES);
+        ok = mbar_wait(empty_bar(s), ((it / PSTAGES) & 1u) ^ 1u, g.status, 41);
+        if (!ok) break;
+        const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
+        const uint32_t fb = map_rank(full_bar(s), 0);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(full_bar(s), 2 * PSTAGE_BYTES);
+          if (g.chunk_boxes) {
+            tma_load_2d_pair(a_dst, &tmY, ma, kb * DK, fb);
+            tma_load_2d_pair(a_dst + CHUNK, &tmY, ma + 64, kb * DK, fb);
+          } else {
+            tma_load_3d_pair(a_dst, &tmY, kb * DK, ma / 64, fb);
           }
-          const uint32_t to = box + 64u * uint32_t(lane) + 16u * uint32_t(c ^ ((lane >> 1) & 3));
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                       : "memory");
+          tma_load_3d_pair(b_dst, &tmX, kb * DK, nb / 64, fb);
         }
-        const int cu = c0 + SEG * u;
-        if (g.tma_out) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0 && row0 < g.n && cu < g.width) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                             reinterpret_cast<uint64_t>(&tmO)),
-                         "r"(cu), "r"(row0), "r"(box)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-        } else {  // rows that TMA cannot store: lane l writes column l of each
-          __syncwarp();
-          for (int r = 0; r < 32 && row0 + r < g.n; ++r) {
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];"
-                         : "=h"(v)
-                         : "r"(box + 64u * uint32_t(r) + 16u * uint32_t((lane >> 3) ^ ((r >> 1) & 3)) + 2u * uint32_t(lane & 7))
-                         : "memory");
-            if (cu + lane < g.width) g.out[int64_t(row0 + r) * g.ldo + cu + lane] = __ushort_as_bfloat16(v);
-          }
-          __syncwarp();
+        __syncwarp();
+      }
+    }
+    // drain (leader): the pair's last copies have landed; the peer waits for this at
+    // the closing cluster barrier
+    if (rank == 0)
+      for (uint32_t d = it > uint32_t(PSTAGES) ? it - PSTAGES : 0; d < it; ++d)
+        mbar_wait(full_bar(int(d % PSTAGES)), (d / PSTAGES) & 1u, g.status, 42);
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer (leader)
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += npairs) {
+      int bm, bn, sp, k0, k1;
+      tile_of(t, bm, bn, sp, k0, k1);
+      const int buf = int(tc & 1u);
+      if (tc >= 2) ok = mbar_wait_cluster_relaxed(tempty_bar(buf), ((tc >> 1) & 1u) ^ 1u, g.status, 43);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % PSTAGES);
+        ok = mbar_wait(full_bar(s), (it / PSTAGES) & 1u, g.status, 44);
+        if (!ok) break;
+        tc_fence_after();
+        // 64-column chunks 8 KB apart, 16 tokens (2 KB) a product
+        const uint64_t ad = sdesc(base + uint32_t(s) * PSTAGE_BYTES, CHUNK, 1024);
+        const uint64_t bd = sdesc(base + uint32_t(s) * PSTAGE_BYTES + HALF_STAGE, CHUNK, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_pair(tmem + uint32_t(buf) * PN, ad + uint64_t(128 * kk), bd + uint64_t(128 * kk), kDwIdesc,
+                          kb != k0 || kk != 0 ? 1u : 0u);
+          mma_commit_pair(empty_bar(s));
+          if (kb + 1 == k1) mma_commit_pair(tfull_bar(buf));
         }
+        __syncwarp();
+      }
+      if (ok) ++tc;
+    }
+    // every product issued here has finished before the accumulators are freed
+    if (tc > 0 && ok) mbar_wait(tfull_bar(int((tc - 1) & 1u)), ((tc - 1) >> 1) & 1u, g.status, 46);
+  } else if (warp >= 4) {
+    // ---------------- output (both CTAs: this CTA's 128 rows)
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t te0 = map_rank(tempty_bar(0), 0);
+    const uint32_t box = base + PSTAGES * PSTAGE_BYTES + uint32_t(warp - 4) * OUT_BOX;
+    uint32_t tc = 0;
+    for (int t = pair; t < total; t += npairs, ++tc) {
+      int bm, bn, sp, k0, k1;
+      tile_of(t, bm, bn, sp, k0, k1);
+      const uint32_t buf = tc & 1u;
+      if (!mbar_wait(tfull_bar(int(buf)), (tc >> 1) & 1u, g.status, 45)) break;
+      tc_fence_after();
+      const int row0 = bm * PM + 128 * rank + 32 * q, c0 = bn * PN + 64 * part;
+      uint32_t r[64];
+      const uint32_t at = tmem + (uint32_t(32 * q) << 16) + buf * PN + uint32_t(64 * part);
+      tmem_ld32(at, r);
+      tmem_ld32(at + 32, r + 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * buf);
+      const int row = row0 + lane;
+      if (g.part) {
+        float* o = g.part + (int64_t(sp) * g.rows + row) * g.cols + c0;  // (cols is a multiple of 16)
+        if (row < g.rows) {
+#pragma unroll
+          for (int j = 0; j < 64; j += 4)
+            if (c0 + j < g.cols)
+              *reinterpret_cast<float4*>(o + j) = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
+                                                              __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+        }
+        continue;
+      }
+      if (g.accumulate && row < g.rows) {
+        const __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (c0 + j < g.cols) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(o[j]));
+      }
+      // the warp's two bf16 boxes of 32 columns, 64-byte swizzle (as in k_linear_pair)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+        __syncwarp();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[32 * u + j]);
+        put_box(v, box, lane);
+        store_box(g.out, g.ldo, g.rows, g.cols, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
@@ -660,6 +864,41 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   void* args[] = {&tx, &tw, &g};
   const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear<true>) : reinterpret_cast<const void*>(k_linear<false>);
   return launch_clusters(k, int(tiles), g.split, THREADS, smem, args, s);
+}
+
+// A product of few tiles and many tokens leaves most pairs idle: it is split while the
+// shares keep eight blocks (512 tokens) and the pairs (half the SMs) hold them all.
+int dw_splits(int64_t n, int64_t rows, int64_t cols) {
+  const int64_t tiles = ((rows + PM - 1) / PM) * ((cols + PN - 1) / PN), nk = (n + DK - 1) / DK;
+  return int(std::max<int64_t>(1, std::min<int64_t>({sm_count() / 2 / tiles, nk / 8, 16})));
+}
+
+int launch_dw(const DwArgs& a, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (once_per_device(kOnceDwAttr) &&
+      cudaFuncSetAttribute(k_dw_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
+    return check("bq_linear_fp8_dw (shared memory attribute)");
+  DwKernelArgs g;
+  g.out = static_cast<__nv_bfloat16*>(a.dw);
+  g.ldo = a.ld_dw, g.n = a.n, g.rows = a.rows, g.cols = a.cols, g.status = a.status;
+  g.splits = dw_splits(a.n, a.rows, a.cols);
+  g.part = g.splits > 1 ? a.part : nullptr;
+  g.chunk_boxes = a.padded ? 0 : 1;
+  g.accumulate = a.accumulate;
+  g.tma_out = !g.part && a.ld_dw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
+  CUtensorMap ty, tx, to;
+  if (int rc = encode_map_chunks(&ty, a.dy, a.rows, a.n, a.ld_dy, a.padded ? 2 : 0)) return rc;
+  if (int rc = encode_map_chunks(&tx, a.x, a.cols, a.n, a.ld_x, 2)) return rc;
+  to = tx;  // (unused without tma_out)
+  if (g.tma_out)
+    if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw)) return rc;
+  const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
+  void* args[] = {&ty, &tx, &to, &g};
+  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, pair_slots())), 2,
+                               PAIR_THREADS, DW_SMEM, args, s))
+    return rc;
+  if (!g.part) return BQ_OK;
+  return launch_dw_join(a.part, g.splits, a.rows, a.cols, int64_t(a.rows) * a.cols, a.dw, a.ld_dw, a.accumulate, stream);
 }
 
 }  // namespace bq

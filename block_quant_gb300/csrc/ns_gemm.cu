@@ -28,8 +28,6 @@
 #include <vector>
 
 #include "bq_internal.h"
-#include "pdl.h"
-#include "row_ops.h"
 #include "tmem_ptx.h"
 #include "umma_ptx.h"
 
@@ -52,6 +50,7 @@ constexpr int GEMM_SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 256 /*barriers
 constexpr int kSymmetric = BQ_NS_SYMMETRIC;
 
 
+
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits
 // 7-9 = 1, 10-12 = 1), A K-major (bit 15 = 0), B major in bit 16, N >> 3 in bits
 // 17-22, M >> 4 in bits 24-28.
@@ -71,10 +70,6 @@ struct GemmArgs {
   int ntiles;  // tiles that run (symmetric: those touching the upper triangle), set by the launcher
   int a_sym;   // the A operand is such a symmetric result: its tiles below the stored ones are read transposed
   int b_sym;   // the same for a K-major B operand
-  int a_mn = 0;  // the A operand is given transposed (MN-major) throughout
-  int band = 1 << 16;  // row blocks of a band of CTA-pair tiles (banded_tile)
-  int splits = 1;      // CTA pairs: shares of the k-blocks, each a part of its own if part is given
-  float* part = nullptr;  // [splits][M][N] fp32 sums instead of D
 };
 
 // A symmetric result is stored as the 128 x 256 output tiles that touch its
@@ -138,30 +133,6 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& g, uint32_t tmem, 
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (col0 + j < g.N) drow[col0 + j] = (j & 1) ? o2[j >> 1].y : o2[j >> 1].x;
-    }
-  }
-}
-
-// the same tile as fp32 sums of split sp
-__device__ __forceinline__ void epilogue_part(const GemmArgs& g, uint32_t tmem, uint32_t col_base, int m0, int n0, int q,
-                                              int lane, int c_lo, int c_hi, int sp) {
-  const int row = m0 + 32 * q + lane;
-  float* prow = g.part + (int64_t(sp) * g.M + row) * g.N;
-  for (int c = c_lo; c < c_hi; ++c) {
-    uint32_t r[32];
-    tmem_ld32(tmem + (uint32_t(32 * q) << 16) + col_base + uint32_t(32 * c), r);
-    const int col0 = n0 + 32 * c;
-    if (row >= g.M || col0 >= g.N) continue;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      if (col0 + j + 4 <= g.N && (g.N & 3) == 0) {
-        *reinterpret_cast<float4*>(prow + col0 + j) = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
-                                                                  __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col0 + j + e < g.N) prow[col0 + j + e] = __uint_as_float(r[j + e]);
-      }
     }
   }
 }
@@ -358,7 +329,7 @@ constexpr int GEMM2_SMEM = STAGES2 * STAGE2_BYTES + 1024 /*align*/ + 256 /*barri
 // D = alpha * (A B) + beta * C with B given as [K x N] N-contiguous (tmB: a 3-D
 // map of 64-column chunks, two chunks a copy) and A K-major (tmA: boxes of 64
 // columns x 128 rows; with a_sym, tmAt's two-chunk boxes give the transposed
-// reads of A's k-blocks below its stored tiles; with a_mn, of all of them).  Pairs walk the 256 x 256 tiles t = cluster, + clusters, ..., row
+// reads of A's k-blocks below its stored tiles).  Pairs walk the 256 x 256 tiles t = cluster, + clusters, ..., row
 // blocks fastest.  A pair tile's rows start at a multiple of 256, so its two
 // 128-row halves of a k-block are stored or transposed together and one
 // instruction descriptor serves both.
@@ -378,16 +349,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 
   const uint32_t rank = cluster_rank();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mt = (g.M + PM - 1) / PM, nt = (g.N + PM - 1) / PM, ntiles = g.ntiles * g.splits;
-  const int band = min(g.band, mt);
+  const int mt = (g.M + PM - 1) / PM, ntiles = g.ntiles;
   const int nk = (g.K + BK - 1) / BK;
-  // tile t of split t / g.ntiles sums that share of the k-blocks
-  auto tile_of = [&](int t, int& bm, int& bn, int& sp, int& k0, int& k1) {
-    sp = g.splits > 1 ? t / g.ntiles : 0;
-    banded_tile(t - sp * g.ntiles, mt, nt, band, bm, bn);
-    k0 = g.splits > 1 ? int(int64_t(nk) * sp / g.splits) : 0;
-    k1 = g.splits > 1 ? int(int64_t(nk) * (sp + 1) / g.splits) : nk;
-  };
   const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES2; ++s) {
@@ -400,7 +363,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  after_previous();  // (of launches that may start early)
   if (warp == 1) tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS_P);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
@@ -412,10 +374,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
-      int bm, bn, sp, k0, k1;
-      tile_of(t, bm, bn, sp, k0, k1);
-      const int ma = bm * PM + 128 * int(rank), nb = bn * PM + 128 * int(rank);
-      for (int kb = k0; kb < k1; ++kb, ++it) {
+      const int ma = (t % mt) * PM + 128 * int(rank), nb = (t / mt) * PM + 128 * int(rank);
+      for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = int(it % STAGES2);
         if (!mbar_wait(empty_bar(s), ((it / STAGES2) & 1u) ^ 1u, g.status, 11)) {
           ok = false;
@@ -425,7 +385,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t b_dst = a_dst + HALF_STAGE;
         const uint32_t fb = map_rank(full_bar(s), 0);
         if (rank == 0) mbar_expect_tx(full_bar(s), 2 * STAGE2_BYTES);
-        if (g.a_mn || (g.a_sym && !sym_stored(ma, kb * BK))) {
+        if (g.a_sym && !sym_stored(ma, kb * BK)) {
           tma_load_3d_pair(a_dst, &tmAt, kb * BK, ma / 64, fb);  // two 64-row chunks
         } else {
           tma_load_2d_pair(a_dst, &tmA, kb * BK, ma, fb);
@@ -443,14 +403,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     uint32_t it = 0, tc = 0;
     bool ok = true;
     for (int t = pair; ok && t < ntiles; t += npairs) {
-      int bm, bn, sp, k0, k1;
-      tile_of(t, bm, bn, sp, k0, k1);
-      const int m0 = bm * PM;
+      const int m0 = (t % mt) * PM;
       const int buf = int(tc & 1u);
       if (tc >= 2 && !mbar_wait_cluster(tempty_bar(buf), ((tc >> 1) & 1u) ^ 1u, g.status, 15)) break;
       tc_fence_after();
       const uint32_t acc = tmem + uint32_t(buf) * BN;
-      for (int kb = k0; kb < k1; ++kb, ++it) {
+      for (int kb = 0; kb < nk; ++kb, ++it) {
         const int s = int(it % STAGES2);
         if (!mbar_wait(full_bar(s), (it / STAGES2) & 1u, g.status, 13)) {
           ok = false;
@@ -459,14 +417,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         tc_fence_after();
         const uint32_t a_addr = base + uint32_t(s) * STAGE2_BYTES;
         const uint32_t b_addr = a_addr + HALF_STAGE;
-        const bool a_t = g.a_mn || (g.a_sym && !sym_stored(m0, kb * BK));
+        const bool a_t = g.a_sym && !sym_stored(m0, kb * BK);
         const uint32_t id = idesc_bf16(PM, BN, 1, a_t ? 1 : 0);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
           const uint64_t ad = a_t ? sdesc(a_addr + uint32_t(kk) * 16u * 128u, BK * 128, 1024)
                                   : sdesc(a_addr + 32u * kk, 16, 1024);
           const uint64_t bd = sdesc(b_addr + uint32_t(kk) * 16u * 128u, BK * 128, 1024);
-          mma_bf16_pair(acc, ad, bd, id, kb != k0 || kk != 0 ? 1u : 0u);
+          mma_bf16_pair(acc, ad, bd, id, (kb | kk) != 0 ? 1u : 0u);
         }
         mma_commit_pair(empty_bar(s));
       }
@@ -481,18 +439,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t te0 = map_rank(tempty_bar(0), 0), te1 = map_rank(tempty_bar(1), 0);
     uint32_t tc = 0;
     for (int t = pair; t < ntiles; t += npairs) {
-      int bm, bn, sp, k0, k1;
-      tile_of(t, bm, bn, sp, k0, k1);
-      const int m0 = bm * PM + 128 * int(rank), n0 = bn * PM;
+      const int m0 = (t % mt) * PM + 128 * int(rank), n0 = (t / mt) * PM;
       const int buf = int(tc & 1u);
       const bool ok = mbar_wait(tfull_bar(buf), (tc >> 1) & 1u, g.status, 14);
       tc_fence_after();
       if (!ok) break;
       const int half = (warp - 2) >> 2;
-      if (g.part)
-        epilogue_part(g, tmem, uint32_t(buf) * BN, m0, n0, q, lane, half * (BN / 64), (half + 1) * (BN / 64), sp);
-      else
-        epilogue_tile(g, tmem, uint32_t(buf) * BN, m0, n0, q, lane, half * (BN / 64), (half + 1) * (BN / 64));
+      epilogue_tile(g, tmem, uint32_t(buf) * BN, m0, n0, q, lane, half * (BN / 64), (half + 1) * (BN / 64));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(buf ? te1 : te0);
@@ -788,29 +741,26 @@ int pair_slots() {
   return cached[dev];
 }
 
-// early: the launch may overlap the kernel before it.
 // B X on CTA pairs: A K-major (ta; tat for the transposed k-blocks of a symmetric
 // A), B [K x N] N-contiguous (tb)
 int gemm_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tat, const GemmArgs& g,
-              cudaStream_t s, bool early = false) {
+              cudaStream_t s) {
   if (int rc = gemm_attrs()) return rc;
   GemmArgs a = g;
   a.ntiles = ((g.M + PM - 1) / PM) * ((g.N + PM - 1) / PM);
   if (a.ntiles == 0) return BQ_OK;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(2 * std::min(a.ntiles * a.splits, pair_slots())));
+  cfg.gridDim = dim3(unsigned(2 * std::min(a.ntiles, pair_slots())));
   cfg.blockDim = dim3(GEMM_THREADS);
   cfg.dynamicSmemBytes = GEMM2_SMEM;
   cfg.stream = s;
   cfg.attrs = at;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = early ? 2 : 1;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, k_gemm_2, ta, tb, tat, a) != cudaSuccess) return check("bq_muon_ns (pair gemm)");
   return check("bq_muon_ns (pair gemm)");
 }
@@ -1048,30 +998,9 @@ int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows,
   return BQ_OK;
 }
 
-// A product of few tiles and many rows leaves most pairs idle: it is split while the
-// shares keep eight k-blocks (512 rows) and the pairs (half the SMs) hold them all.
-int gemm_tn_splits(int64_t t, int64_t m, int64_t n) {
-  const int64_t tiles = ((m + PM - 1) / PM) * ((n + PM - 1) / PM), nk = (t + BK - 1) / BK;
-  return int(std::max<int64_t>(1, std::min<int64_t>({sm_count() / 2 / tiles, nk / 8, 16})));
-}
-
-// The weight gradient's product on the CTA pairs: A and B both MN-major, their
-// rows the summed index.  The pitches are multiples of 64 elements with the
-// padding allocated, which a 64-column chunk of the last columns reads.
-int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t t, int m, int n, void* D,
-                   int64_t ldd, int accumulate, float* part, int* status, void* stream) {
-  CUtensorMap ta, tb;
-  if (int rc = make_map3(&ta, A, m, t, lda, 2)) return rc;
-  if (int rc = make_map3(&tb, B, n, t, ldb, 2)) return rc;
-  auto* d = static_cast<__nv_bfloat16*>(D);
-  GemmArgs g{m, n, int(t), 1.f, accumulate ? 1.f : 0.f, accumulate ? d : nullptr, d, ldd, ldd, status, 0, 0, 0, 0};
-  g.a_mn = 1;
-  g.band = 8;
-  g.splits = gemm_tn_splits(t, m, n);
-  if (g.splits == 1) return gemm_pair(ta, tb, ta, g, static_cast<cudaStream_t>(stream), true);
-  g.part = part;
-  if (int rc = gemm_pair(ta, tb, ta, g, static_cast<cudaStream_t>(stream), true)) return rc;
-  return launch_dw_join(part, g.splits, m, n, int64_t(m) * n, D, ldd, accumulate, stream);
+int encode_map_chunks(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int chunks) {
+  if (chunks > 0) return make_map3(static_cast<CUtensorMap*>(map), base, cols, rows, pitch, chunks);
+  return make_map(static_cast<CUtensorMap*>(map), base, cols, rows, pitch, 64);
 }
 
 int muon_ns(int batch, const bq_mat* mats, int steps, float a, float b, float c, float eps, void* ws, size_t ws_bytes,

@@ -58,7 +58,7 @@ LinearWs linear_ws(int64_t n, int64_t rows, int64_t cols) {
   p.x = kStatusBytes;
   p.dy = p.x + up(size_t(n) * size_t(up64(cols)) * 2);
   p.part = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
-  const int splits = gemm_tn_splits(n, rows, cols);
+  const int splits = dw_splits(n, rows, cols);
   const size_t dw = p.part + (splits > 1 ? size_t(splits) * size_t(rows) * size_t(cols) * 4 : 0);
   p.bytes = std::max({dx, dw, fwd});
   return p;
@@ -186,7 +186,7 @@ int bq_quant_rows_fp8(const void* x, int64_t ld_x, int64_t n, int64_t cols, uint
   ld_scale = pitch(ld_scale, cols <= 128 ? 1 : 2, n);
   if (ld_x < cols || ld_codes < cols || ld_scale < n) return fail(BQ_EINVAL, who, "pitch below the width");
   if (off(x, 2) || off(code_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
-  return launch_quant_rows(x, ld_x, n, int(cols), codes, ld_codes, code_scale, ld_scale, stream);
+  return launch_quant_rows(x, ld_x, n, int(cols), codes, ld_codes, code_scale, ld_scale, false, stream);
 }
 
 int bq_linear_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
@@ -235,7 +235,7 @@ int bq_linear_fp8_dx(const void* dy, int64_t ld_dy, const uint8_t* w, int64_t ld
   auto* codes = base + p.codes;
   auto* scales = reinterpret_cast<float*>(base + p.scales);
   const int64_t ldc = up16(rows), lds = up4(n);
-  if (int rc = launch_quant_rows(dy, ld_dy, n, int(rows), codes, ldc, scales, lds, stream)) return rc;
+  if (int rc = launch_quant_rows(dy, ld_dy, n, int(rows), codes, ldc, scales, lds, true, stream)) return rc;
   return launch_linear_fp8(LinearArgs{codes, scales, w, w_scale, dx, ldc, lds, ld_w, ld_dx, n, int(rows), int(cols), 1,
                                       static_cast<int*>(ws), nullptr},
                            stream);
@@ -266,15 +266,19 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
   if (off(dy, 2) || off(x_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
   auto* base = static_cast<unsigned char*>(ws);
   const int64_t ldxb = up64(cols);
-  // dy as it stands where the product's copies can read it: whole 64-column chunks
-  // inside each row, 16-byte aligned rows
-  const bool copy = off(dy, 16) || ld_dy % 8 || rows % 64;
+  if (n <= kDwFewTokens)
+    return launch_dw_few(dy, ld_dy, x, ld_x, x_scale, ld_scale, int(n), int(rows), int(cols), dw, ld_dw,
+                         accumulate ? 1 : 0, stream);
+  // dy as it stands where its rows are 16-byte aligned, as the product's copies want them
+  const bool copy = off(dy, 16) || ld_dy % 8;
   const int64_t lda = copy ? up64(rows) : ld_dy;
   if (int rc = launch_dw_inputs(x, ld_x, x_scale, ld_scale, n, int(cols), base + p.x, ldxb, copy ? dy : nullptr, ld_dy,
                                 int(rows), base + p.dy, lda, stream))
     return rc;
-  return launch_gemm_tn(copy ? base + p.dy : dy, lda, base + p.x, ldxb, n, int(rows), int(cols), dw, ld_dw,
-                        accumulate ? 1 : 0, reinterpret_cast<float*>(base + p.part), static_cast<int*>(ws), stream);
+  return launch_dw(DwArgs{copy ? base + p.dy : dy, base + p.x, dw, reinterpret_cast<float*>(base + p.part),
+                          static_cast<int*>(ws), lda, ldxb, ld_dw, n, int(rows), int(cols), copy || rows % 64 == 0,
+                          accumulate ? 1 : 0},
+                   stream);
 }
 
 int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream) {

@@ -123,6 +123,49 @@ __device__ __forceinline__ uint4 load_packed(const __nv_bfloat16* row, int c0, i
   return w;
 }
 
+// Eight consecutive columns a lane (c0 + 8 lane ..) of a row at any 2-byte alignment: the
+// aligned 16-byte words that hold them, shifted.  Every word read holds some of the row,
+// so it lies in the row's allocation.
+__device__ __forceinline__ uint4 load_shifted(const __nv_bfloat16* row, int c0, int cols, int lane) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row + c0), end = reinterpret_cast<uintptr_t>(row + cols);
+  const uint4* p = reinterpret_cast<const uint4*>(a & ~uintptr_t(15));
+  const int m = int(a & 15) >> 1;  // elements to drop: the same in every lane
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  if (reinterpret_cast<uintptr_t>(p + lane) < end) w = __ldg(p + lane);
+  if (m == 0) {
+    // (elements past the row are masked below)
+  } else {
+    uint4 n = make_uint4(__shfl_down_sync(0xFFFFFFFFu, w.x, 1), __shfl_down_sync(0xFFFFFFFFu, w.y, 1),
+                         __shfl_down_sync(0xFFFFFFFFu, w.z, 1), __shfl_down_sync(0xFFFFFFFFu, w.w, 1));
+    if (lane == 31) {
+      n = make_uint4(0u, 0u, 0u, 0u);
+      if (reinterpret_cast<uintptr_t>(p + 32) < end) n = __ldg(p + 32);
+    }
+    uint32_t u[8] = {w.x, w.y, w.z, w.w, n.x, n.y, n.z, n.w};
+    if (m & 4) {
+#pragma unroll
+      for (int i = 0; i < 6; ++i) u[i] = u[i + 2 < 8 ? i + 2 : 7];
+    }
+    if (m & 2) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) u[i] = u[i + 1];
+    }
+    if (m & 1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(u[i], u[i + 1], 16);
+    }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  const int left = cols - c0 - 8 * lane;  // of this lane's columns inside the row
+  if (left < 8) {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = left >= 2 * i + 2 ? u[i] : left == 2 * i + 1 ? u[i] & 0xFFFFu : 0u;
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  return w;
+}
+
 template <bool VEC>
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* row, int c0, int cols, int lane, const float* v) {
   if (VEC) {
@@ -997,8 +1040,8 @@ __global__ void __launch_bounds__(VPT <= 2 ? 1024 : 512, 1) k_norm_many(const No
   }
 }
 
-// a warp quantises N spans of a row
-template <bool VEC, int N>
+// a warp quantises N spans of a row.  IN: x's rows are whole vectors; OUT: the codes' are.
+template <bool IN, bool OUT, int N>
 __global__ void __launch_bounds__(32 * kRowWarps)
     k_quant_rows(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t n, int cols, uint8_t* __restrict__ codes,
                  int64_t ldc, float* __restrict__ scale, int64_t lds, int segs) {
@@ -1009,10 +1052,12 @@ __global__ void __launch_bounds__(32 * kRowWarps)
   const int64_t t = item / segs;
   if (t >= n) return;
   const int c0 = int(item - t * segs) * N * kSpan;
-  uint4 w[N];
+  if (OUT) {
+    uint4 w[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) w[j] = load_packed<VEC>(x + t * ldx, c0 + kSpan * j, cols, lane);
-  if (VEC && N > 1) {
+    for (int j = 0; j < N; ++j)
+      w[j] = IN ? load_packed<true>(x + t * ldx, c0 + kSpan * j, cols, lane)
+                : load_shifted(x + t * ldx, c0 + kSpan * j, cols, lane);
     float2 v[N][4];
 #pragma unroll
     for (int j = 0; j < N; ++j) unpack8(w[j], v[j]);
@@ -1022,8 +1067,8 @@ __global__ void __launch_bounds__(32 * kRowWarps)
     for (int j = 0; j < N; ++j) {
       if (c0 + kSpan * j >= cols) break;
       float v[8];
-      unpack8(w[j], v);
-      quant_span<VEC>(v, c0 + kSpan * j, cols, lane, codes + t * ldc, scale + t, lds);
+      load_bf16<false>(x + t * ldx, c0 + kSpan * j, cols, lane, v);
+      quant_span<false>(v, c0 + kSpan * j, cols, lane, codes + t * ldc, scale + t, lds);
     }
   }
 }
@@ -1058,11 +1103,78 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_dw_inputs(const DwInputs a) 
     *reinterpret_cast<uint4*>(a.x_out + t * a.ldo + c) = pack8(v);
   } else if (item < a.items) {
     const int64_t i = item - a.x_items, t = i / a.y_spans;
-    const int c0 = int(i - t * a.y_spans) * kSpan;
+    const int c0 = int(i - t * a.y_spans) * kSpan, c = c0 + 8 * lane;
+    const uint4 w = load_shifted(a.dy + t * a.ldy, c0, a.rows, lane);
+    if (c < a.rows) *reinterpret_cast<uint4*>(a.dy_out + t * a.ldyo + c) = w;  // (the pitch covers whole vectors)
+  }
+}
+
+// dw (+)= sum over up to kDwFewTokens tokens of dy[t]^T bf16(x[t]): a CTA holds its 64 rows
+// of dY^T and 256 columns of X in shared memory and writes a 64 x 256 tile, a thread 8 rows
+// x 8 columns of it.  Bound by the write: the products on the tensor cores pay a tile's
+// whole set-up for a k-block.
+constexpr int kFewRows = 64, kFewCols = 256;
+__global__ void __launch_bounds__(256)
+    k_dw_few(const __nv_bfloat16* __restrict__ dy, int64_t ldy, const uint8_t* __restrict__ codes, int64_t ldc,
+             const float* __restrict__ scale, int64_t lds, int n, int rows, int cols, __nv_bfloat16* __restrict__ dw,
+             int64_t ldw, int accumulate) {
+  __shared__ __align__(16) float x[kDwFewTokens][kFewCols], y[kDwFewTokens][kFewRows];
+  const int tid = threadIdx.x;
+  const int col_tiles = (cols + kFewCols - 1) / kFewCols;
+  const int r0 = int(blockIdx.x) / col_tiles * kFewRows, c0 = int(blockIdx.x) % col_tiles * kFewCols;
+  after_previous();
+  next_may_start();
+  for (int i = tid; i < n * (kFewCols / 8); i += 256) {  // (cols is a multiple of 16)
+    const int t = i / (kFewCols / 8), c = 8 * (i % (kFewCols / 8));
+    float v[8] = {};
+    if (c0 + c < cols) {
+      decode8(__ldg(reinterpret_cast<const uint2*>(codes + t * ldc + c0 + c)), v);
+      const float s = __ldg(scale + int64_t((c0 + c) >> 7) * lds + t);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + 32 * e + lane;
-      if (c < a.rows) a.dy_out[t * a.ldyo + c] = a.dy[t * a.ldy + c];
+      for (int e = 0; e < 8; ++e) v[e] = __bfloat162float(__float2bfloat16_rn(__fmul_rn(v[e], s)));
+    }
+    *reinterpret_cast<float4*>(&x[t][c]) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(&x[t][c + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  for (int i = tid; i < n * kFewRows; i += 256) {
+    const int t = i / kFewRows, r = i % kFewRows;
+    y[t][r] = r0 + r < rows ? __bfloat162float(dy[t * ldy + r0 + r]) : 0.f;
+  }
+  __syncthreads();
+  const int lane = tid & 31, r1 = 8 * (tid >> 5), c1 = 8 * lane;
+  float2 acc[8][4] = {};
+  for (int t = 0; t < n; ++t) {
+    const float4 a = *reinterpret_cast<const float4*>(&x[t][c1]), b = *reinterpret_cast<const float4*>(&x[t][c1 + 4]);
+    const float2 xv[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float2 f = dup(y[t][r1 + r]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[r][e] = fma2(f, xv[e], acc[r][e]);
+    }
+  }
+  if (c0 + c1 >= cols) return;
+  const bool vec = ldw % 8 == 0 && (reinterpret_cast<uintptr_t>(dw) & 15) == 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int row = r0 + r1 + r;
+    if (row >= rows) break;
+    __nv_bfloat16* o = dw + int64_t(row) * ldw + c0 + c1;
+    if (vec) {
+      if (accumulate) {
+        float2 old[4];
+        unpack8(*reinterpret_cast<const uint4*>(o), old);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] = make_float2(acc[r][e].x + old[e].x, acc[r][e].y + old[e].y);
+      }
+      *reinterpret_cast<uint4*>(o) = pack8(acc[r]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = e & 1 ? acc[r][e >> 1].y : acc[r][e >> 1].x;
+        if (accumulate) v += __bfloat162float(o[e]);
+        o[e] = __float2bfloat16_rn(v);
+      }
     }
   }
 }
@@ -1477,18 +1589,20 @@ int launch_rmsnorm(const RmsnormArgs& r, void* stream) {
   return check("bq_rmsnorm");
 }
 
+// pad: the codes' rows may be written up to the next multiple of 8
 int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* codes, int64_t ldc, float* scale,
-                      int64_t lds, void* stream) {
+                      int64_t lds, bool pad, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool vec = cols % 8 == 0 && vec_ok(x, ldx, 8) && (reinterpret_cast<uintptr_t>(codes) & 7) == 0 && ldc % 8 == 0;
+  const bool in = cols % 8 == 0 && vec_ok(x, ldx, 8);
+  const bool out = (pad || cols % 8 == 0) && (reinterpret_cast<uintptr_t>(codes) & 7) == 0 && ldc % 8 == 0;
   // four spans a warp share one division pass (8192 x 14336: 57 us, 75 with one); one
   // where that would not give every scheduler a warp
   const int spans = (cols + kSpan - 1) / kSpan;
   const int each = n * ((spans + 3) / 4) >= int64_t(sm_count()) * 4 ? 4 : 1;
   const int segs = (spans + each - 1) / each;
   const int64_t ctas = (n * segs + kRowWarps - 1) / kRowWarps;
-  auto* k = each == 4 ? (vec ? k_quant_rows<true, 4> : k_quant_rows<false, 4>)
-                      : (vec ? k_quant_rows<true, 1> : k_quant_rows<false, 1>);
+  auto* k = each == 4 ? (!out ? k_quant_rows<false, false, 4> : in ? k_quant_rows<true, true, 4> : k_quant_rows<false, true, 4>)
+                      : (!out ? k_quant_rows<false, false, 1> : in ? k_quant_rows<true, true, 1> : k_quant_rows<false, true, 1>);
   launch_after(k, unsigned(ctas), 32 * kRowWarps, 0, s, static_cast<const __nv_bfloat16*>(x), ldx, n, cols, codes, ldc,
                scale, lds, segs);
   return check("bq_quant_rows_fp8");
@@ -1506,6 +1620,14 @@ int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int6
   launch_after(k_dw_inputs, unsigned((a.items + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, 0,
                static_cast<cudaStream_t>(stream), a);
   return check("bq_linear_fp8_dw (inputs)");
+}
+
+int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds,
+                  int n, int rows, int cols, void* dw, int64_t ld_dw, int accumulate, void* stream) {
+  const int64_t tiles = int64_t((rows + kFewRows - 1) / kFewRows) * ((cols + kFewCols - 1) / kFewCols);
+  launch_after(k_dw_few, unsigned(tiles), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(dy),
+               ld_dy, codes, ldc, scale, lds, n, rows, cols, static_cast<__nv_bfloat16*>(dw), ld_dw, accumulate);
+  return check("bq_linear_fp8_dw");
 }
 
 int launch_dw_join(const float* part, int parts, int64_t m, int n, int64_t stride, void* out, int64_t ldo, int accumulate,

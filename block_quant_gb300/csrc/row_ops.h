@@ -50,8 +50,9 @@ struct RmsnormGradArgs {
 size_t rmsnorm_grad_bytes(int64_t n, int64_t cols);
 int launch_rmsnorm_grad(const RmsnormGradArgs& a, void* ws, void* stream);  // n may be 0
 
+// pad: the codes' rows may be written up to the next multiple of 8
 int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* codes, int64_t ldc, float* scale,
-                      int64_t lds, void* stream);
+                      int64_t lds, bool pad, void* stream);
 // bf16 rows of X (from FP8 rows) and of dY (dy NULL: not wanted) at pitches ldo, ldyo
 int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
                      int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
@@ -74,11 +75,24 @@ struct LinearArgs {
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 
-// D [m, n] (+)= A^T B over t rows, bf16, A [t, m] and B [t, n] with pitches that
-// are multiples of 64 elements (ns_gemm.cu).  A product with too few tiles for the GPU is
-// split over the rows, its fp32 parts (gemm_tn_splits of them, m * n values each) in part.
-int gemm_tn_splits(int64_t t, int64_t m, int64_t n);
-int launch_gemm_tn(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t t, int m, int n, void* D,
-                   int64_t ldd, int accumulate, float* part, int* status, void* stream);
+// D [rows, cols] (+)= dY^T X over n tokens, bf16 (linear_fp8.cu): dy [n, rows] with 16-byte
+// aligned rows (padded: its pitch covers the next multiple of 64 columns), x [n, cols] with
+// a pitch that does.  A product with too few tiles for the GPU is split over the tokens, its
+// fp32 parts (dw_splits of them, rows * cols values each) in part.
+struct DwArgs {
+  const void *dy, *x;
+  void* dw;
+  float* part;
+  int* status;
+  int64_t ld_dy, ld_x, ld_dw, n;
+  int rows, cols, padded, accumulate;
+};
+int dw_splits(int64_t n, int64_t rows, int64_t cols);
+int launch_dw(const DwArgs& a, void* stream);
+
+// few tokens: the sum of outer products, straight from dy and the FP8 rows
+constexpr int kDwFewTokens = 16;
+int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds,
+                  int n, int rows, int cols, void* dw, int64_t ld_dw, int accumulate, void* stream);
 
 }  // namespace bq

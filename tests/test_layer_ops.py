@@ -390,7 +390,8 @@ def test_quant_rows(cuda, cols):
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 300, 4096), (2, 130, 144), (8, 256, 1024), (33, 257, 1040), (64, 200, 2064),
           (100, 64, 8192), (128, 128, 128), (129, 300, 272), (256, 256, 256), (300, 520, 2064), (513, 1000, 528),
-          (1030, 2881, 272), (2048, 1024, 640), (700, 4000, 1536), (2000, 2050, 2064), (4100, 1000, 1040)]
+          (1030, 2881, 272), (2048, 1024, 640), (700, 4000, 1536), (2000, 2050, 2064), (4100, 1000, 1040), (16, 200, 528),
+          (17, 72, 272), (90, 1904, 304), (1100, 520, 400)]
 
 
 def workspace(n, rows, cols, dev):
