@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
     tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
   };
+  if (threadIdx.x == 32) fetch_map(&tmX), fetch_map(&tmW);
   after_previous();
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 32) fetch_map(&tmX), fetch_map(&tmW), fetch_map(&tmS), fetch_map(&tmO);
   after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
@@ -562,7 +564,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // product's fp32 sums leave from registers.
 constexpr int DK = 64;                          // tokens of a k-block
 constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
-constexpr int DW_SMEM = 1024 + PSTAGES * PSTAGE_BYTES + PEPI * OUT_BOX;
+constexpr int DW_STAGES = 6;
+constexpr int DW_SMEM = 1024 + DW_STAGES * PSTAGE_BYTES + PEPI * OUT_BOX;
 
 struct DwKernelArgs {
   __nv_bfloat16* out;
@@ -584,13 +587,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4];
+  __shared__ __align__(8) uint64_t bars[2 * DW_STAGES + 4];
   __shared__ uint32_t tmem_slot;
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
-  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(PSTAGES + s); };
-  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + b); };
-  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 + b); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(DW_STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + 2 + b); };
 
   const int rank = int(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     k1 = int(int64_t(nk) * (sp + 1) / g.splits);
   };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < PSTAGES; ++s) {
+    for (int s = 0; s < DW_STAGES; ++s) {
       mbar_init(full_bar(s), 1);   // the leader's expect_tx
       mbar_init(empty_bar(s), 1);  // the leader's commit
     }
@@ -615,6 +618,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 32) fetch_map(&tmY), fetch_map(&tmX), fetch_map(&tmO);
   after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
@@ -632,8 +636,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       tile_of(t, bm, bn, sp, k0, k1);
       const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
       for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = int(it % PSTAGES);
-        ok = mbar_wait(empty_bar(s), ((it / PSTAGES) & 1u) ^ 1u, g.status, 41);
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(empty_bar(s), ((it / DW_STAGES) & 1u) ^ 1u, g.status, 41);
         if (!ok) break;
         const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
         const uint32_t fb = map_rank(full_bar(s), 0);
@@ -653,8 +657,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     // drain (leader): the pair's last copies have landed; the peer waits for this at
     // the closing cluster barrier
     if (rank == 0)
-      for (uint32_t d = it > uint32_t(PSTAGES) ? it - PSTAGES : 0; d < it; ++d)
-        mbar_wait(full_bar(int(d % PSTAGES)), (d / PSTAGES) & 1u, g.status, 42);
+      for (uint32_t d = it > uint32_t(DW_STAGES) ? it - DW_STAGES : 0; d < it; ++d)
+        mbar_wait(full_bar(int(d % DW_STAGES)), (d / DW_STAGES) & 1u, g.status, 42);
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer (leader)
     uint32_t it = 0, tc = 0;
@@ -667,8 +671,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = int(it % PSTAGES);
-        ok = mbar_wait(full_bar(s), (it / PSTAGES) & 1u, g.status, 44);
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(full_bar(s), (it / DW_STAGES) & 1u, g.status, 44);
         if (!ok) break;
         tc_fence_after();
         // 64-column chunks 8 KB apart, 16 tokens (2 KB) a product
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     // ---------------- output (both CTAs: this CTA's 128 rows)
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t te0 = map_rank(tempty_bar(0), 0);
-    const uint32_t box = base + PSTAGES * PSTAGE_BYTES + uint32_t(warp - 4) * OUT_BOX;
+    const uint32_t box = base + DW_STAGES * PSTAGE_BYTES + uint32_t(warp - 4) * OUT_BOX;
     uint32_t tc = 0;
     for (int t = pair; t < total; t += npairs, ++tc) {
       int bm, bn, sp, k0, k1;
