@@ -17,7 +17,8 @@ enum { BF16 = 1, FP32 = 2, FP8 = 4 }; /* what an argument may be: 1 << BQ_ROWS_*
 static int (*g_call)(int, const void*);
 static PyObject *g_kinds;                 /* torch dtype -> kind (0, 1, 2); 32, 64: id types */
 static PyObject *g_fill;                  /* called with an unknown dtype: its kind or None */
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device;
+static int64_t g_device; /* of the tensors read so far in this call; -1: none (the GIL is held throughout) */
 
 typedef struct {
   int64_t p, ld, rows, cols, kind;
@@ -37,8 +38,18 @@ static int64_t kind_of(PyObject* x, const char* name) {
   return k ? PyLong_AsLongLong(k) : -1;
 }
 
-static int pointer_of(PyObject* x, int64_t* p) {
-  PyObject* v = PyObject_CallMethodNoArgs(x, s_data_ptr);
+/* the tensor's address; all of a call's tensors must be on one GPU */
+static int pointer_of(PyObject* x, const char* name, int64_t* p) {
+  PyObject* v = PyObject_CallMethodNoArgs(x, s_get_device);
+  if (!v) return -1;
+  const int64_t d = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  if (d < 0 || (g_device >= 0 && d != g_device)) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, d < 0 ? "%s is not on a GPU" : "%s is on another GPU", name);
+    return -1;
+  }
+  g_device = d;
+  v = PyObject_CallMethodNoArgs(x, s_data_ptr);
   if (!v) return -1;
   *p = (int64_t)PyLong_AsUnsignedLongLong(v);
   Py_DECREF(v);
@@ -79,7 +90,7 @@ static int mat(PyObject* x, const char* name, int kinds, int64_t rows, int64_t c
     return -1;
   }
   m->ld = st[0], m->rows = s[0], m->cols = s[1];
-  return pointer_of(x, &m->p);
+  return pointer_of(x, name, &m->p);
 }
 
 /* a matrix that may be None: zeros */
@@ -116,7 +127,7 @@ static int vec(PyObject* x, const char* name, int kinds, int64_t n, int64_t* p, 
   }
   if (kind) *kind = k;
   if (got) *got = len;
-  return pointer_of(x, p);
+  return pointer_of(x, name, p);
 }
 
 /* one fp32 scale per 128 x 128 tile, contiguous, of any shape */
@@ -137,7 +148,7 @@ static int tiles(PyObject* x, const char* name, int64_t rows, int64_t cols, int6
                  (long long)rows, (long long)cols);
     return -1;
   }
-  return contiguous(x, name) ? -1 : pointer_of(x, p);
+  return contiguous(x, name) ? -1 : pointer_of(x, name, p);
 }
 
 /* FP8 rows: codes and their scales [ceil(cols / 128), n] */
@@ -146,7 +157,9 @@ static int code_rows(PyObject* codes, PyObject* scale, int64_t n, int64_t cols, 
   return mat(scale, "code_scale", FP32, (c->cols + 127) / 128, c->rows, s);
 }
 
+/* the start of every call */
 static int args_are(Py_ssize_t n, Py_ssize_t want) {
+  g_device = -1;
   if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", n, want);
   return n == want;
 }
@@ -306,6 +319,7 @@ PyMODINIT_FUNC PyInit__bqcall(void) {
   s_stride = PyUnicode_InternFromString("stride");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous) return NULL;
+  s_get_device = PyUnicode_InternFromString("get_device");
+  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_get_device) return NULL;
   return PyModule_Create(&module);
 }

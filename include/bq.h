@@ -407,7 +407,11 @@ int bq_muon_ns_noalloc(int batch, const bq_mat* mats, int steps, float a, float 
  *   - matrices are row-major with a row pitch ld_* in elements (>= their width; of
  *     a matrix with at most one row it may be anything from the width up);
  *   - n (rows, one per token) may be 0: nothing is read, and only a gradient that
- *     is not accumulated is written (zeros).
+ *     is not accumulated is written (zeros);
+ *   - a workspace's size depends on the current device (its SMs): query it with the
+ *     device current that the call will run on;
+ *   - kernels may be set up while the kernel before them on the stream still runs
+ *     (programmatic dependent launch); they touch memory after it has completed.
  * Common errors: BQ_EINVAL (a NULL argument, a negative count, a pitch below the
  * width, an unknown kind; n above 2^27, cols above 65536, rows above 2^30),
  * BQ_EALIGN (a pointer not aligned to its element type; where more is asked for,

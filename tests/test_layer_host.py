@@ -202,3 +202,5 @@ def test_binding_refuses_shapes_and_types():
         with pytest.raises(bq.BQError) as e:
             call()
         assert e.value.code == bq.BQ_EINVAL
+    with pytest.raises(bq.BQError, match="not on a GPU"):  # right shapes and types
+        bq.embed(t, ids, out, stream=0)

@@ -242,12 +242,17 @@ def test_rmsnorm(cuda, cols, residual):
 @pytest.mark.parametrize("n,cols", [(5000, 256), (2600, 520), (1300, 4096), (700, 8192), (640, 8200), (650, 16384)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_rmsnorm_many_rows(cuda, n, cols, residual):
-    """Counts of rows that the resident CTAs share: every row as the same row alone."""
+    """Counts of rows that the resident CTAs share: every row as the same row alone, zeros,
+    tiny values, infinities and NaN among them."""
     import torch
 
     rng = np.random.default_rng(cols)
-    x, _ = bf16(rng.standard_normal((n, cols)), cuda, 8)
-    r, _ = bf16(rng.standard_normal((n, cols)), cuda)
+    a = rng.standard_normal((n, cols))
+    a[3] = 0
+    a[4] *= 2.0 ** -120
+    a[5, 17], a[6, 3], a[7, cols - 1] = np.inf, np.nan, -np.inf
+    x, _ = bf16(a, cuda, 8)
+    r, _ = bf16(rng.standard_normal((n, cols)) * (np.arange(n) > 8)[:, None], cuda)
     w, _ = bf16(1 + 0.3 * rng.standard_normal(cols), cuda)
     got, want = [], []
     for rows in (n, 50):
@@ -262,7 +267,7 @@ def test_rmsnorm_many_rows(cuda, n, cols, residual):
             outs.append((h if residual else y, y, codes, scale.t(), rstd))
         (got if rows == n else want).extend(torch.cat(t) for t in zip(*outs))
     for a, b in zip(got, want):
-        assert torch.equal(a, b)
+        assert torch.equal(a, b) or bool(((a == b) | ((a != a) & (b != b))).all())
 
 
 def test_rmsnorm_in_place_and_parts(cuda):
@@ -391,7 +396,7 @@ def test_quant_rows(cuda, cols):
 SHAPES = [(1, 1, 16), (1, 128, 128), (1, 300, 4096), (2, 130, 144), (8, 256, 1024), (33, 257, 1040), (64, 200, 2064),
           (100, 64, 8192), (128, 128, 128), (129, 300, 272), (256, 256, 256), (300, 520, 2064), (513, 1000, 528),
           (1030, 2881, 272), (2048, 1024, 640), (700, 4000, 1536), (2000, 2050, 2064), (4100, 1000, 1040), (16, 200, 528),
-          (17, 72, 272), (90, 1904, 304), (1100, 520, 400)]
+          (17, 72, 272), (90, 1904, 304), (1100, 520, 400), (2000, 3000, 4096), (1950, 4096, 3008)]
 
 
 def workspace(n, rows, cols, dev):
