@@ -87,7 +87,10 @@ struct LinArgs {
 
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
 // share of the k-blocks, and the shares are added in order through distributed
-// shared memory.
+// shared memory.  For few rows, where the weight's bytes and then the start of a CTA count:
+// 1 row of 8192 x 8192 takes 14.2 us (4.7 TB/s; its bytes alone are 9.9), 333 rows of 2880 x
+// 4096 take 12.5 (72 MB through L2, and about 5 us from the launch to the first product and
+// from the last to the stores).
 template <bool TRANS>
 __global__ void __launch_bounds__(THREADS, 2)
     k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const LinArgs g) {
@@ -124,7 +127,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
     tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
   };
-  if (threadIdx.x == 32) fetch_map(&tmX), fetch_map(&tmW);
   after_previous();
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
@@ -278,23 +280,25 @@ __global__ void __launch_bounds__(THREADS, 2)
 // epilogue warps' registers (64 a thread); its bf16 rows leave through shared memory
 // and TMA stores while the next tile's products run.
 //
-// What bounds it is the hand-over of an accumulator: products done -> epilogue warps
-// read it -> both CTAs' arrivals -> next products, about 800 cycles.  A k-block is
-// therefore two products of N = 128 with an accumulator each (four in all, every
-// column of tensor memory): while one is handed over the other three hold 768 cycles
-// of products, against 512 with two accumulators of N = 256.
+// Two accumulators of N = 256 fill tensor memory: k-block it sums into accumulator it & 1
+// while the epilogue reads the other.  Four of N = 128 (two products a k-block, three
+// waiting while one is read) took 391 us where these take 335 (8192 rows, 14336 x 4096):
+// the products of one k-block, 512 cycles, then read X from shared memory twice.
+//
+// What bounds it: with the epilogue's reading taken out the same products and copies take
+// 258 us on a clock that power holds down (twice the rate of a library's bf16 product: 252);
+// the hand-over of an accumulator (products done -> read by 32 warps -> their arrivals ->
+// next product), which one k-block does not quite hide, makes it 285 without the reading
+// and 306 with it, and the adding 335: 2.87 PFLOP/s.  In a run of seconds, under the power
+// limit, 383 us.
 constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
 constexpr int HALF_STAGE = 128 * BK;            // 16 KB
 constexpr int PSTAGE_BYTES = 2 * HALF_STAGE;
-#ifndef BQ_UNITS
-#define BQ_UNITS 1
-#endif
-constexpr int UNITS = BQ_UNITS, UN = PN / UNITS;       // products (accumulators) of a k-block
 // Sixteen epilogue warps, four per tensor-memory lane quarter: part p of a quarter
-// reads columns 32p .. 32p + 31 of every accumulator.  Five warpgroups with TMA (warp
+// reads columns 64p .. 64p + 63 of every accumulator.  Five warpgroups with TMA (warp
 // 0) and MMA (warp 1); of the launch's 640 x 96 registers the first group keeps 56 a
 // thread and the epilogue takes 104.
-constexpr int PEPI = 16, PCOLS = UN / 4, SEG = 32 * UNITS;  // SEG: columns from one 32-column box to the next
+constexpr int PEPI = 16, PCOLS = PN / 4;
 constexpr int PAIR_THREADS = 128 + 32 * PEPI;
 constexpr int kRegsLaunch = 96, kRegsIssue = 56, kRegsEpilogue = 104;
 static_assert(128 * kRegsIssue + 32 * PEPI * kRegsEpilogue <= PAIR_THREADS * kRegsLaunch, "register split");
@@ -310,7 +314,7 @@ constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OU
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
 constexpr int kPairTmem = 2 * PN;
 // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
-// 5952 take 28 us there and 17 us on k_linear) and at least so many tiles (half of the pairs that run at once are 38): 32 tiles of 32
+// 5952 take 28 us there and 17 us on k_linear) and at least so many tiles: 32 tiles of 32
 // k-blocks take 16.6 us here and 15.7 us on k_linear's smaller tiles, 56 take 18.6 and
 // 24.0 us, 64 take 17.5 and 24.1 us.
 constexpr int kPairMin = 44;
@@ -377,13 +381,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4 * UNITS];
+  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4];
   __shared__ uint32_t tmem_slot;
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(PSTAGES + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * PSTAGES + a); };               // accumulator a:
-  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 * UNITS + a); };  // k-block parity x unit
+  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 + b); };
 
   const int rank = int(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -395,13 +399,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       mbar_init(full_bar(s), 1);   // the leader's expect_tx
       mbar_init(empty_bar(s), 1);  // the leader's commit
     }
-    for (int a = 0; a < 2 * UNITS; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * PEPI);  // the epilogue warps of both CTAs
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * PEPI);  // the epilogue warps of both CTAs
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x == 32) fetch_map(&tmX), fetch_map(&tmW), fetch_map(&tmS), fetch_map(&tmO);
   after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
@@ -448,9 +451,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         for (uint32_t d = it > uint32_t(PSTAGES) ? it - PSTAGES : 0; d < it; ++d)
           mbar_wait(full_bar(int(d % PSTAGES)), (d / PSTAGES) & 1u, g.status, 32);
     } else if (warp == 1 && rank == 0) {
-      // ---------------- MMA issuer (leader).  A product's N are half of each CTA's: unit
-      // u takes columns UN / 2 u .. of both halves of the tile
-      const uint32_t id = idesc_e4m3(PM, UN, TRANS ? 1 : 0);
+      // ---------------- MMA issuer (leader)
+      const uint32_t id = idesc_e4m3(PM, PN, TRANS ? 1 : 0);
       const uint32_t total = uint32_t((ntiles - pair + npairs - 1) / npairs) * uint32_t(nk);
       uint32_t it = 0;
       bool ok = true;
@@ -462,27 +464,21 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         // K-major: rows 128 bytes apart, 32-code k slices 32 bytes apart; MN-major: a
         // column is a byte, 32 k rows of 128 bytes a slice
         const uint64_t ad = sdesc(a_addr, 16, 1024), bd = TRANS ? sdesc(b_addr, BK * 128, 1024) : sdesc(b_addr, 16, 1024);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int acc = buf * UNITS + u;
-          if (it >= 2) ok = ok && mbar_wait_cluster_relaxed(tempty_bar(acc), ((it >> 1) & 1u) ^ 1u, g.status, 33);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)
-              mma_e4m3_pair(tmem + uint32_t(acc) * UN, ad + uint64_t(2 * kk),
-                            bd + uint64_t(TRANS ? 4 * u + 256 * kk : 512 * u + 2 * kk), id, kk != 0 ? 1u : 0u);
-            mma_commit_pair(tfull_bar(acc));
-            if (u == UNITS - 1) mma_commit_pair(empty_bar(s));
-          }
-          __syncwarp();
-        }
+        if (it >= 2) ok = mbar_wait_cluster_relaxed(tempty_bar(buf), ((it >> 1) & 1u) ^ 1u, g.status, 33);
         if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_e4m3_pair(tmem + uint32_t(buf) * PN, ad + uint64_t(2 * kk), bd + uint64_t(TRANS ? 256 * kk : 2 * kk), id,
+                          kk != 0 ? 1u : 0u);
+          mma_commit_pair(tfull_bar(buf));
+          mma_commit_pair(empty_bar(s));
+        }
+        __syncwarp();
       }
       // every product issued here has finished before the accumulators are freed
-      if (it > 0 && ok)
-        mbar_wait(tfull_bar(int((it - 1) & 1u) * UNITS + UNITS - 1), ((it - 1) >> 1) & 1u, g.status, 36);
+      if (it > 0 && ok) mbar_wait(tfull_bar(int((it - 1) & 1u)), ((it - 1) >> 1) & 1u, g.status, 36);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
@@ -499,11 +495,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       int bm, bn;
       banded_tile(t, mt, nt, kBand, bm, bn);
       const int row0 = bm * PM + 128 * rank + 32 * q;                        // the warp's first row of out
-      const int c0 = bn * PN + 128 * (part >> 1) + PCOLS * (part & 1);       // its columns: unit u's from c0 + 64u
+      const int c0 = bn * PN + PCOLS * part;                                 // its 64 columns
       const float* ws = TRANS ? g.ws + (c0 >> 7) : g.ws + int64_t(c0 >> 7) * g.tile_cols;
-      float acc[UNITS * PCOLS];
+      float acc[PCOLS];
 #pragma unroll
-      for (int j = 0; j < UNITS * PCOLS; ++j) acc[j] = 0.f;
+      for (int j = 0; j < PCOLS; ++j) acc[j] = 0.f;
       // W's scales for 32 k-blocks, block kb + l in lane l
       float wl = 0.f, wn = c0 < g.width && lane < nk ? __ldg(ws + lane * ws_step) : 0.f;
       for (int kb = 0; kb < nk; ++kb, ++it) {
@@ -513,29 +509,23 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
         const uint32_t buf = it & 1u, l = it % SLOTS;
         const float w = __shfl_sync(0xFFFFFFFFu, wl, kb & 31);
-        float f = 0.f;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const uint32_t a = buf * UNITS + u;
-          ok = ok && mbar_wait(tfull_bar(int(a)), (it >> 1) & 1u, g.status, 35);
-          tc_fence_after();
-          if (u == 0) {
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(my_scale + l * SLOT_BYTES) : "memory");
-            f *= w;
-          }
-#pragma unroll
-          for (int j = 0; j < PCOLS; j += 32) {
-            uint32_t r[32];
-            tmem_ld32(acc0 + a * UN + uint32_t(j), r);
-            if (j + 32 == PCOLS) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * a);
-            }
-            add_scaled<32>(acc + u * PCOLS + j, r, f);
-          }
-        }
+        ok = mbar_wait(tfull_bar(int(buf)), (it >> 1) & 1u, g.status, 35);
         if (!ok) break;
+        tc_fence_after();
+        float f;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(my_scale + l * SLOT_BYTES) : "memory");
+        f *= w;
+#pragma unroll
+        for (int j = 0; j < PCOLS; j += 32) {
+          uint32_t r[32];
+          tmem_ld32(acc0 + buf * PN + uint32_t(j), r);
+          if (j + 32 == PCOLS) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * buf);
+          }
+          add_scaled<32>(acc + j, r, f);
+        }
       }
       if (!ok) break;
 #pragma unroll
@@ -543,7 +533,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
         __syncwarp();
         put_box(acc + 32 * u, box, lane);
-        store_box(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + SEG * u, box, lane);
+        store_box(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
@@ -561,7 +551,9 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // dW = dY^T X in bf16 on the same pairs and tiles: both operands MN-major (a token's row
 // holds 64-column chunks of 128 bytes), the summed index is the tokens, one accumulator of
 // a tile's whole sum, two of them in turn.  The tile leaves as in k_linear_pair; a split
-// product's fp32 sums leave from registers.
+// product's fp32 sums leave from registers.  Bound by the products: 8192 tokens, 14336 x
+// 4096 take 546 us with X's conversion to bf16 (15), 1.76 PFLOP/s, and 592 in a run of
+// seconds under the power limit; a library's bf16 product of that size reaches 1.91 and 1.7.
 constexpr int DK = 64;                          // tokens of a k-block
 constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
 constexpr int DW_STAGES = 6;
@@ -618,7 +610,6 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x == 32) fetch_map(&tmY), fetch_map(&tmX), fetch_map(&tmO);
   after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();

@@ -67,11 +67,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// a tensor map (a kernel parameter) into the cache that the copies read it from
-__device__ __forceinline__ void fetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
 // c MN-major 64 x 64 chunks in one copy: a 3-D map {64 columns, rows, 64-column
 // chunks} (chunk stride 128 bytes) lands them 8 KB apart, the layout of c
 // separate 64 x 64 boxes
