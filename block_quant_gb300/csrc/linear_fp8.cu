@@ -562,13 +562,20 @@ constexpr int DW_SMEM = 1024 + DW_STAGES * PSTAGE_BYTES + PEPI * OUT_BOX;
 
 struct DwKernelArgs {
   __nv_bfloat16* out;
-  float* part;           // [splits][rows][cols], or NULL
+  float* part;           // a split product's shares (k_dw_join), or NULL
   int64_t ldo, n;
   int rows, cols, splits;
   int chunk_boxes;       // dY's copies bring one chunk each, not two
   int accumulate, tma_out;
   int* status;
 };
+
+// A share's values as the epilogue warps hold them: float4 j of lane l (columns 4j .. of its
+// row) at 32 j + l of warp w's 512, so that every store is whole lines (by rows, 16 bytes a
+// lane, the same stores took 4 us longer).
+__device__ __forceinline__ int64_t share_at(int t, int rank, int w) {
+  return ((int64_t(t) * 2 + rank) * PEPI + w) * 512;
+}
 
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both MN-major
 constexpr uint32_t kDwIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t(PN >> 3) << 17) |
@@ -706,14 +713,12 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * buf);
       const int row = row0 + lane;
       if (g.part) {
-        float* o = g.part + (int64_t(sp) * g.rows + row) * g.cols + c0;  // (cols is a multiple of 16)
-        if (row < g.rows) {
+        float4* o = reinterpret_cast<float4*>(g.part) + share_at(t, rank, warp - 4) + lane;
+        if (row0 < g.rows && c0 < g.cols)
 #pragma unroll
-          for (int j = 0; j < 64; j += 4)
-            if (c0 + j < g.cols)
-              *reinterpret_cast<float4*>(o + j) = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
-                                                              __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
-        }
+          for (int j = 0; j < 16; ++j)
+            o[32 * j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                    __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
         continue;
       }
       if (g.accumulate && row < g.rows) {
@@ -742,6 +747,39 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+
+// dw = sum of the shares in order (+ dw): a warp takes 32 rows x 16 columns
+__global__ void __launch_bounds__(256) k_dw_join(const DwKernelArgs g) {
+  after_previous();
+  next_may_start();
+  const int mt = (g.rows + PM - 1) / PM, nt = (g.cols + PN - 1) / PN, ntiles = mt * nt;
+  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, h = int(i & 3), w = int(i >> 2) & (PEPI - 1), rank = int(i >> 6) & 1, t = int(i >> 7);
+  int bm, bn;
+  banded_tile(t, mt, nt, kBand, bm, bn);
+  const int row = bm * PM + 128 * rank + 32 * (w & 3) + lane, c0 = bn * PN + 64 * (w >> 2) + 16 * h;
+  if (row >= g.rows || c0 >= g.cols) return;
+  const float4* p = reinterpret_cast<const float4*>(g.part) + share_at(t, rank, w) + 128 * h + lane;
+  float4 v[4] = {};
+  for (int k = 0; k < g.splits; ++k, p += share_at(ntiles, 0, 0))
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = p[32 * j];
+      v[j].x += x.x, v[j].y += x.y, v[j].z += x.z, v[j].w += x.w;
+    }
+  const float* f = reinterpret_cast<const float*>(v);
+  __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;  // (cols is a multiple of 16)
+  alignas(16) __nv_bfloat16 y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = __float2bfloat16_rn(g.accumulate ? f[e] + __bfloat162float(o[e]) : f[e]);
+  if (g.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0) {
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+    *reinterpret_cast<uint4*>(o + 8) = *reinterpret_cast<const uint4*>(y + 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = y[e];
   }
 }
 
@@ -862,11 +900,24 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   return launch_clusters(k, int(tiles), g.split, THREADS, smem, args, s);
 }
 
-// A product of few tiles and many tokens leaves most pairs idle: it is split while the
-// shares keep eight blocks (512 tokens) and the pairs (half the SMs) hold them all.
+size_t dw_part_bytes(int splits, int64_t rows, int64_t cols) {
+  return splits > 1 ? size_t(splits) * size_t((rows + PM - 1) / PM) * size_t((cols + PN - 1) / PN) * PM * PN * 4 : 0;
+}
+
+// A product of few tiles and many tokens leaves most pairs idle: its tokens are split where
+// that costs less, by the times of 1, 6 and 16 tiles: 0.29 us a k-block, and for shares a
+// launch, their stores and their sums.  1024 x 1024: 1000 tokens 11.4 us in one, 13.2 in two
+// and 15.0 in four shares; 8000 tokens 43.7, 31.9 and 27.4.
 int dw_splits(int64_t n, int64_t rows, int64_t cols) {
   const int64_t tiles = ((rows + PM - 1) / PM) * ((cols + PN - 1) / PN), nk = (n + DK - 1) / DK;
-  return int(std::max<int64_t>(1, std::min<int64_t>({sm_count() / 2 / tiles, nk / 8, 16})));
+  const int most = int(std::min<int64_t>({sm_count() / 2 / tiles, nk, 16}));
+  int best = 1;
+  double least = 0.29 * double(nk);
+  for (int s = 2; s <= most; ++s) {
+    const double us = 0.29 * double((nk + s - 1) / s) + 2.2 + s * (0.25 + 0.045 * double(tiles));
+    if (us < least) least = us, best = s;
+  }
+  return best;
 }
 
 int launch_dw(const DwArgs& a, void* stream) {
@@ -894,7 +945,8 @@ int launch_dw(const DwArgs& a, void* stream) {
                                PAIR_THREADS, DW_SMEM, args, s))
     return rc;
   if (!g.part) return BQ_OK;
-  return launch_dw_join(a.part, g.splits, a.rows, a.cols, int64_t(a.rows) * a.cols, a.dw, a.ld_dw, a.accumulate, stream);
+  launch_after(k_dw_join, unsigned(tiles / g.splits * 16), 256, 0, s, g);
+  return check("bq_linear_fp8_dw (join)");
 }
 
 }  // namespace bq

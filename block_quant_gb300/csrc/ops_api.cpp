@@ -58,8 +58,7 @@ LinearWs linear_ws(int64_t n, int64_t rows, int64_t cols) {
   p.x = kStatusBytes;
   p.dy = p.x + up(size_t(n) * size_t(up64(cols)) * 2);
   p.part = p.dy + up(size_t(n) * size_t(up64(rows)) * 2);
-  const int splits = dw_splits(n, rows, cols);
-  const size_t dw = p.part + (splits > 1 ? size_t(splits) * size_t(rows) * size_t(cols) * 4 : 0);
+  const size_t dw = p.part + dw_part_bytes(dw_splits(n, rows, cols), rows, cols);
   p.bytes = std::max({dx, dw, fwd});
   return p;
 }

@@ -1185,35 +1185,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// dw = sum of the parts in order (+ dw), bf16: eight values a thread (n, a multiple of 16)
-__global__ void __launch_bounds__(256) k_dw_join(const float* __restrict__ part, int parts, int64_t m, int n, int64_t stride,
-                                                 __nv_bfloat16* __restrict__ out, int64_t ldo, int accumulate) {
-  after_previous();
-  next_may_start();
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, r = i / (n / 8);
-  if (r >= m) return;
-  const int c = 8 * int(i - r * (n / 8));
-  __nv_bfloat16* o = out + r * ldo + c;
-  const float* p = part + r * n + c;
-  float v[8] = {};
-  for (int k = 0; k < parts; ++k, p += stride) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-  }
-  if (ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-    if (accumulate) {
-      float old[8];
-      unpack8(*reinterpret_cast<const uint4*>(o), old);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += old[e];
-    }
-    *reinterpret_cast<uint4*>(o) = pack8(v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __float2bfloat16_rn(accumulate ? v[e] + __bfloat162float(o[e]) : v[e]);
-  }
-}
-
 // ---------------------------------------------------------------- norm gradient
 
 struct NormGradArgs {
@@ -1648,13 +1619,6 @@ int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t l
   launch_after(k_dw_few, unsigned(tiles), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(dy),
                ld_dy, codes, ldc, scale, lds, n, rows, cols, static_cast<__nv_bfloat16*>(dw), ld_dw, accumulate);
   return check("bq_linear_fp8_dw");
-}
-
-int launch_dw_join(const float* part, int parts, int64_t m, int n, int64_t stride, void* out, int64_t ldo, int accumulate,
-                   void* stream) {
-  launch_after(k_dw_join, unsigned((m * (n / 8) + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream), part, parts, m, n,
-               stride, static_cast<__nv_bfloat16*>(out), ldo, accumulate);
-  return check("bq_linear_fp8_dw (join)");
 }
 
 size_t rmsnorm_grad_bytes(int64_t n, int64_t cols) {

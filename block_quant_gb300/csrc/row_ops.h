@@ -56,9 +56,6 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
 // bf16 rows of X (from FP8 rows) and of dY (dy NULL: not wanted) at pitches ldo, ldyo
 int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
                      int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
-int launch_dw_join(const float* part, int parts, int64_t m, int n, int64_t stride, void* out, int64_t ldo, int accumulate,
-                   void* stream);
-
 // FP8 projections (linear_fp8.cu)
 struct LinearArgs {
   const uint8_t* x;      // codes [n, red], pitch ldx (a multiple of 16)
@@ -78,7 +75,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream);
 // D [rows, cols] (+)= dY^T X over n tokens, bf16 (linear_fp8.cu): dy [n, rows] with 16-byte
 // aligned rows (padded: its pitch covers the next multiple of 64 columns), x [n, cols] with
 // a pitch that does.  A product with too few tiles for the GPU is split over the tokens, its
-// fp32 parts (dw_splits of them, rows * cols values each) in part.
+// fp32 shares in part (dw_part_bytes).
 struct DwArgs {
   const void *dy, *x;
   void* dw;
@@ -88,6 +85,7 @@ struct DwArgs {
   int rows, cols, padded, accumulate;
 };
 int dw_splits(int64_t n, int64_t rows, int64_t cols);
+size_t dw_part_bytes(int splits, int64_t rows, int64_t cols);
 int launch_dw(const DwArgs& a, void* stream);
 
 // few tokens: the sum of outer products, straight from dy and the FP8 rows
