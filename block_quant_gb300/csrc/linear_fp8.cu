@@ -314,12 +314,6 @@ static_assert(SLOTS > PSTAGES + 2, "scale slots");
 constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
 constexpr int kPairTmem = 2 * PN;
-// The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
-// 5952 take 28 us there and 17 us on k_linear) and at least so many tiles: 32 tiles of 32
-// k-blocks take 16.6 us here and 15.7 us on k_linear's smaller tiles, 56 take 18.6 and
-// 24.0 us, 64 take 17.5 and 24.1 us.
-constexpr int kPairMin = 44;
-
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
@@ -363,13 +357,19 @@ __device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int r
     }
   } else {
     __syncwarp();
-    for (int r = 0; r < 32 && row0 + r < rows; ++r) {
-      uint16_t v;
-      asm volatile("ld.shared.u16 %0, [%1];"
-                   : "=h"(v)
-                   : "r"(box + 64u * uint32_t(r) + 16u * uint32_t((lane >> 3) ^ ((r >> 1) & 3)) + 2u * uint32_t(lane & 7))
-                   : "memory");
-      if (c0 + lane < cols) out[int64_t(row0 + r) * ldo + c0 + lane] = __ushort_as_bfloat16(v);
+    __nv_bfloat16* o = out + int64_t(row0) * ldo + c0 + lane;
+    const int below = c0 + lane < cols ? rows - row0 : 0;
+    for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows' loads before their stores
+      uint16_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v[e])
+                     : "r"(box + 64u * uint32_t(r0 + e) + 16u * uint32_t((lane >> 3) ^ (((r0 + e) >> 1) & 3)) + 2u * uint32_t(lane & 7))
+                     : "memory");
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (r0 + e < below) o[int64_t(r0 + e) * ldo] = __ushort_as_bfloat16(v[e]);
     }
     __syncwarp();
   }
@@ -860,8 +860,24 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   CUtensorMap tx, tw, ts, to;
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
-  if (pairs > 0x7FFFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  if (a.n > BM && pairs >= kPairMin) {
+  const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
+  if (tiles > 0x7FFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
+  // k_linear: k-blocks are split while that leaves every CTA resident (a second wave costs a whole
+  // set-up: 64 tiles of 64 k-blocks, 14.0 us by 4 and 17.7 us by 8) and a share has one
+  // at least, by 8 four (24 tiles of 16: 5.2 us by 4, 6.3 us by 8; 3 tiles of 94: 12.2 and
+  // 8.7 us)
+  while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk >= (g.split == 4 ? 32 : g.split * 2))
+    g.split *= 2;
+  // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
+  // 5952 take 28 us there and 17 us on k_linear), where the waves of their tiles take less
+  // time, by the times of 20 products of 200 to 4000 rows: a wave of pairs 0.40 us a k-block and
+  // 2.5 us, of k_linear's CTAs, two an SM, 0.52 and 6.  337 rows of 11840 x 4512 (two waves or
+  // one): 38.3 us on pairs, 26.4 on k_linear; 849 of 6336 x 8144 (two and two): 62.8 and 96.1;
+  // 512 of 8192 x 4096 (one and one): 18.4 and 24.2.
+  const int64_t waves = (tiles * g.split + 2 * sm_count() - 1) / (2 * sm_count());
+  const double us_pair = 4 + double((pairs + pair_slots() - 1) / pair_slots()) * (0.40 * nk + 2.5);
+  const double us_one = 2 + double(waves) * (0.52 * ((nk + g.split - 1) / g.split) + 6);
+  if (a.n > BM && us_pair < us_one) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (unused without tma_out)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
@@ -880,19 +896,12 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
                                  : reinterpret_cast<const void*>(k_linear_pair<false>);
     return launch_clusters(k, int(std::min<int64_t>(pairs, pair_slots())), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
-  const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
   // two CTAs share an SM.  The X stages come last, and a product reads 128 rows of
   // the last one whatever it holds: what follows it is spare shared memory
   g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
   const int stage = B_STAGE + g.a_rows * BK, spare = (BM - g.a_rows) * BK;
   const int part = BM * kPartPitch * 4;
   g.stages = std::min(kMaxStages, (kSmem - 1024 - spare) / stage);
-  // k-blocks are split while that leaves every CTA resident (a second wave costs a whole
-  // set-up: 64 tiles of 64 k-blocks, 14.0 us by 4 and 17.7 us by 8) and a share has one
-  // at least, by 8 four (24 tiles of 16: 5.2 us by 4, 6.3 us by 8; 3 tiles of 94: 12.2 and
-  // 8.7 us)
-  while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk >= (g.split == 4 ? 32 : g.split * 2))
-    g.split *= 2;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   const int smem = 1024 + std::max(part, g.stages * stage + spare);
   void* args[] = {&tx, &tw, &g};
