@@ -250,13 +250,25 @@ __global__ void __launch_bounds__(THREADS, 2)
     float v[BN / 32];
 #pragma unroll
     for (int j = 0; j < BN / 32; ++j) v[j] = 0.f;
-    for (int c = 0; c < g.split; ++c) {
-      const uint32_t at = map_rank(part0, uint32_t(c)) + 4u * uint32_t(r * kPartPitch + lane);
+    if (g.split == 1) {
 #pragma unroll
-      for (int j = 0; j < BN / 32; ++j) {
-        float x;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at + 128u * j) : "memory");
-        v[j] += x;
+      for (int j = 0; j < BN / 32; ++j) v[j] = part[r * kPartPitch + lane + 32 * j];
+    } else {
+      for (int c0 = 0; c0 < g.split; c0 += 4) {  // four shares' loads set out together
+        float x[4][BN / 32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c0 + c >= g.split) break;
+          const uint32_t at = map_rank(part0, uint32_t(c0 + c)) + 4u * uint32_t(r * kPartPitch + lane);
+#pragma unroll
+          for (int j = 0; j < BN / 32; ++j)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[c][j]) : "r"(at + 128u * j) : "memory");
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c0 + c < g.split)
+#pragma unroll
+            for (int j = 0; j < BN / 32; ++j) v[j] += x[c][j];
       }
     }
     __nv_bfloat16* o = g.out + int64_t(m0 + r) * g.ldo + n0;
