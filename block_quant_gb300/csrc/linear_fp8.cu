@@ -309,11 +309,11 @@ constexpr int HALF_STAGE = 128 * BK;            // 16 KB
 constexpr int PSTAGE_BYTES = 2 * HALF_STAGE;
 // Sixteen epilogue warps, four per tensor-memory lane quarter: part p of a quarter
 // reads columns 64p .. 64p + 63 of every accumulator.  Five warpgroups with TMA (warp
-// 0) and MMA (warp 1); of the launch's 640 x 96 registers the first group keeps 56 a
-// thread and the epilogue takes 104.
+// 0) and MMA (warp 1); of the launch's 640 x 96 registers the first group keeps 32 a
+// thread and the epilogue takes 112.
 constexpr int PEPI = 16, PCOLS = PN / 4;
 constexpr int PAIR_THREADS = 128 + 32 * PEPI;
-constexpr int kRegsLaunch = 96, kRegsIssue = 56, kRegsEpilogue = 104;
+constexpr int kRegsLaunch = 96, kRegsIssue = 32, kRegsEpilogue = 112;
 static_assert(128 * kRegsIssue + 32 * PEPI * kRegsEpilogue <= PAIR_THREADS * kRegsLaunch, "register split");
 constexpr int OUT_BOX = 32 * 64;                // 32 rows x 32 bf16 of out, one a warp
 // X's scales of a k-block (128 rows of this CTA) are copied with the stages, on the same
@@ -336,25 +336,33 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
-// A warp's box of out, 32 rows x 32 bf16 in shared memory with 64-byte swizzle: 16-byte word
-// c of row r at word c ^ ((r >> 1) & 3).  v: the lane's row.
+// A warp's box of out, 32 rows x COLS bf16 (32 or 64) in shared memory, swizzled as its store
+// reads it: 16-byte word c of row r at word c ^ ((r >> 1) & 3), or c ^ (r & 7)
+template <int COLS>
+__device__ __forceinline__ uint32_t box_word(uint32_t box, int r, int c) {
+  return box + 2u * COLS * uint32_t(r) + 16u * uint32_t(COLS == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7));
+}
+
+// v: the lane's row
+template <int COLS>
 __device__ __forceinline__ void put_box(const float* v, uint32_t box, int lane) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < COLS / 8; ++c) {
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const __nv_bfloat162 p = __floats2bfloat162_rn(v[8 * c + 2 * e], v[8 * c + 2 * e + 1]);
       o[e] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    const uint32_t to = box + 64u * uint32_t(lane) + 16u * uint32_t(c ^ ((lane >> 1) & 3));
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_word<COLS>(box, lane, c)), "r"(o[0]), "r"(o[1]),
+                 "r"(o[2]), "r"(o[3])
                  : "memory");
   }
 }
 
 // the box to out's row0.., c0.., clipped to rows x cols: by TMA, or where out's rows are not
-// 16-byte aligned by plain stores, lane l column l of each row
+// 16-byte aligned by plain stores, lane l columns l, l + 32 of each row
+template <int COLS>
 __device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int tma_out,
                                           const CUtensorMap* map, int row0, int c0, uint32_t box, int lane) {
   if (tma_out) {
@@ -369,19 +377,23 @@ __device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int r
     }
   } else {
     __syncwarp();
-    __nv_bfloat16* o = out + int64_t(row0) * ldo + c0 + lane;
-    const int below = c0 + lane < cols ? rows - row0 : 0;
-    for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows' loads before their stores
-      uint16_t v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        asm volatile("ld.shared.u16 %0, [%1];"
-                     : "=h"(v[e])
-                     : "r"(box + 64u * uint32_t(r0 + e) + 16u * uint32_t((lane >> 3) ^ (((r0 + e) >> 1) & 3)) + 2u * uint32_t(lane & 7))
-                     : "memory");
+    for (int k = 0; k < COLS; k += 32) {
+      const int c = lane + k, below = c0 + c < cols ? rows - row0 : 0;
+      __nv_bfloat16* o = out + int64_t(row0) * ldo + c0 + c;
+#pragma unroll 1
+      for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows' loads before their stores
+        uint16_t v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (r0 + e < below) o[int64_t(r0 + e) * ldo] = __ushort_as_bfloat16(v[e]);
+        for (int e = 0; e < 8; ++e)
+          asm volatile("ld.shared.u16 %0, [%1];"
+                       : "=h"(v[e])
+                       : "r"(box_word<COLS>(box, r0 + e, c >> 3) + 2u * uint32_t(c & 7))
+                       : "memory");
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (r0 + e < below) o[int64_t(r0 + e) * ldo] = __ushort_as_bfloat16(v[e]);
+      }
     }
     __syncwarp();
   }
@@ -545,8 +557,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       for (int u = 0; u < 2; ++u) {
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
         __syncwarp();
-        put_box(acc + 32 * u, box, lane);
-        store_box(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
+        put_box<32>(acc + 32 * u, box, lane);
+        store_box<32>(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
@@ -569,8 +581,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // seconds under the power limit; a library's bf16 product of that size reaches 1.91 and 1.7.
 constexpr int DK = 64;                          // tokens of a k-block
 constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
-constexpr int DW_STAGES = 6;
-constexpr int DW_SMEM = 1024 + DW_STAGES * PSTAGE_BYTES + PEPI * OUT_BOX;
+constexpr int DW_STAGES = 5, DW_BOX = 32 * 128;  // (a warp's staging of out: 32 rows x 64 bf16)
+constexpr int DW_SMEM = 1024 + DW_STAGES * PSTAGE_BYTES + PEPI * DW_BOX;
 
 struct DwKernelArgs {
   __nv_bfloat16* out;
@@ -707,7 +719,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     // ---------------- output (both CTAs: this CTA's 128 rows)
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t te0 = map_rank(tempty_bar(0), 0);
-    const uint32_t box = base + DW_STAGES * PSTAGE_BYTES + uint32_t(warp - 4) * OUT_BOX;
+    const uint32_t box = base + DW_STAGES * PSTAGE_BYTES + uint32_t(warp - 4) * DW_BOX;
     uint32_t tc = 0;
     for (int t = pair; t < total; t += npairs, ++tc) {
       int bm, bn, sp, k0, k1;
@@ -739,17 +751,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         for (int j = 0; j < 64; ++j)
           if (c0 + j < g.cols) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(o[j]));
       }
-      // the warp's two bf16 boxes of 32 columns, 64-byte swizzle (as in k_linear_pair)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
-        __syncwarp();
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[32 * u + j]);
-        put_box(v, box, lane);
-        store_box(g.out, g.ldo, g.rows, g.cols, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
-      }
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+      __syncwarp();
+      put_box<64>(reinterpret_cast<const float*>(r), box, lane);
+      store_box<64>(g.out, g.ldo, g.rows, g.cols, g.tma_out, &tmO, row0, c0, box, lane);
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
   }
@@ -899,7 +904,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
       g.xs = a.scale_ws, g.ld_xs = ld;
     }
     if (a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
-      if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo)) return rc;
+      if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo, 32)) return rc;
       g.tma_out = 1;
     }
     if (int rc = encode_map_scales(&ts, g.xs, a.n, nk, g.ld_xs)) return rc;
@@ -959,7 +964,7 @@ int launch_dw(const DwArgs& a, void* stream) {
   if (int rc = encode_map_chunks(&tx, a.x, a.cols, a.n, a.ld_x, 2)) return rc;
   to = tx;  // (unused without tma_out)
   if (g.tma_out)
-    if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw)) return rc;
+    if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw, 64)) return rc;
   const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
   void* args[] = {&ty, &tx, &to, &g};
   if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, pair_slots())), 2,

@@ -984,15 +984,16 @@ int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, in
   return BQ_OK;
 }
 
-int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch) {
+int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int box_cols) {
   EncodeTiled enc = encoder();
   if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");
   const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(pitch) * 2};
-  const cuuint32_t box[2] = {32u, 32u};
+  const cuuint32_t box[2] = {cuuint32_t(box_cols), 32u};
   const cuuint32_t estr[2] = {1u, 1u};
   const CUresult r = enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(BQ_EINVAL, "bq_linear_fp8: tensor map encoding failed (" + std::to_string(int(r)) + ")");
   return BQ_OK;

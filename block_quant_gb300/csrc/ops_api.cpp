@@ -265,7 +265,7 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
   if (off(dy, 2) || off(x_scale, 4)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
   auto* base = static_cast<unsigned char*>(ws);
   const int64_t ldxb = up64(cols);
-  if (n <= kDwFewTokens)
+  if (dw_few(n, rows, cols))
     return launch_dw_few(dy, ld_dy, x, ld_x, x_scale, ld_scale, int(n), int(rows), int(cols), dw, ld_dw,
                          accumulate ? 1 : 0, stream);
   // dy as it stands where its rows are 16-byte aligned, as the product's copies want them

@@ -1115,48 +1115,52 @@ __global__ void __launch_bounds__(32 * kRowWarps) k_dw_inputs(const DwInputs a) 
   }
 }
 
-// dw (+)= sum over up to kDwFewTokens tokens of dy[t]^T bf16(x[t]): a CTA holds its 64 rows
-// of dY^T and 256 columns of X in shared memory and writes a 64 x 256 tile, a thread 8 rows
-// x 8 columns of it.  Bound by the write: the products on the tensor cores pay a tile's
-// whole set-up for a k-block.
-constexpr int kFewRows = 64, kFewCols = 256;
+// dw (+)= sum over few tokens of dy[t]^T bf16(x[t]): a CTA holds its 64 rows of dY^T and 256
+// columns of X in shared memory, 16 tokens at a time, and writes a 64 x 256 tile, a thread 8
+// rows x 8 columns of it.  Bound by the write for a token or two (4096 x 4096: 8.4 us, 4 TB/s), by
+// fp32 multiply-adds then; one launch, where the products on the tensor cores convert X first.
+constexpr int kFewRows = 64, kFewCols = 256, kFewDeep = 16;  // (tokens in shared memory at once)
 __global__ void __launch_bounds__(256)
     k_dw_few(const __nv_bfloat16* __restrict__ dy, int64_t ldy, const uint8_t* __restrict__ codes, int64_t ldc,
              const float* __restrict__ scale, int64_t lds, int n, int rows, int cols, __nv_bfloat16* __restrict__ dw,
              int64_t ldw, int accumulate) {
-  __shared__ __align__(16) float x[kDwFewTokens][kFewCols], y[kDwFewTokens][kFewRows];
+  __shared__ __align__(16) float x[kFewDeep][kFewCols], y[kFewDeep][kFewRows];
   const int tid = threadIdx.x;
   const int col_tiles = (cols + kFewCols - 1) / kFewCols;
   const int r0 = int(blockIdx.x) / col_tiles * kFewRows, c0 = int(blockIdx.x) % col_tiles * kFewCols;
   after_previous();
   next_may_start();
-  for (int i = tid; i < n * (kFewCols / 8); i += 256) {  // (cols is a multiple of 16)
-    const int t = i / (kFewCols / 8), c = 8 * (i % (kFewCols / 8));
-    float v[8] = {};
-    if (c0 + c < cols) {
-      decode8(__ldg(reinterpret_cast<const uint2*>(codes + t * ldc + c0 + c)), v);
-      const float s = __ldg(scale + int64_t((c0 + c) >> 7) * lds + t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __bfloat162float(__float2bfloat16_rn(__fmul_rn(v[e], s)));
-    }
-    *reinterpret_cast<float4*>(&x[t][c]) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(&x[t][c + 4]) = make_float4(v[4], v[5], v[6], v[7]);
-  }
-  for (int i = tid; i < n * kFewRows; i += 256) {
-    const int t = i / kFewRows, r = i % kFewRows;
-    y[t][r] = r0 + r < rows ? __bfloat162float(dy[t * ldy + r0 + r]) : 0.f;
-  }
-  __syncthreads();
   const int lane = tid & 31, r1 = 8 * (tid >> 5), c1 = 8 * lane;
   float2 acc[8][4] = {};
-  for (int t = 0; t < n; ++t) {
-    const float4 a = *reinterpret_cast<const float4*>(&x[t][c1]), b = *reinterpret_cast<const float4*>(&x[t][c1 + 4]);
-    const float2 xv[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
+  for (int t0 = 0; t0 < n; t0 += kFewDeep) {
+    const int deep = min(kFewDeep, n - t0);
+    if (t0) __syncthreads();
+    for (int i = tid; i < deep * (kFewCols / 8); i += 256) {  // (cols is a multiple of 16)
+      const int t = i / (kFewCols / 8), c = 8 * (i % (kFewCols / 8));
+      float v[8] = {};
+      if (c0 + c < cols) {
+        decode8(__ldg(reinterpret_cast<const uint2*>(codes + (t0 + t) * ldc + c0 + c)), v);
+        const float s = __ldg(scale + int64_t((c0 + c) >> 7) * lds + t0 + t);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float2 f = dup(y[t][r1 + r]);
+        for (int e = 0; e < 8; ++e) v[e] = __bfloat162float(__float2bfloat16_rn(__fmul_rn(v[e], s)));
+      }
+      *reinterpret_cast<float4*>(&x[t][c]) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(&x[t][c + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    for (int i = tid; i < deep * kFewRows; i += 256) {
+      const int t = i / kFewRows, r = i % kFewRows;
+      y[t][r] = r0 + r < rows ? __bfloat162float(dy[(t0 + t) * ldy + r0 + r]) : 0.f;
+    }
+    __syncthreads();
+    for (int t = 0; t < deep; ++t) {
+      const float4 a = *reinterpret_cast<const float4*>(&x[t][c1]), b = *reinterpret_cast<const float4*>(&x[t][c1 + 4]);
+      const float2 xv[4] = {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[r][e] = fma2(f, xv[e], acc[r][e]);
+      for (int r = 0; r < 8; ++r) {
+        const float2 f = dup(y[t][r1 + r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] = fma2(f, xv[e], acc[r][e]);
+      }
     }
   }
   if (c0 + c1 >= cols) return;
@@ -1611,6 +1615,16 @@ int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int6
   launch_after(k_dw_inputs, unsigned((a.items + kRowWarps - 1) / kRowWarps), 32 * kRowWarps, 0,
                static_cast<cudaStream_t>(stream), a);
   return check("bq_linear_fp8_dw (inputs)");
+}
+
+// By the times of 1 to 128 tokens and 512 x 512 to 14336 x 4096.  512 x 512, 16 tokens: 4.4 us
+// here, 6.5 on the tensor cores; 32: 7.2 and 6.8.  2880 x 4096, 1 token: 6.6 and 9.6; 16: 13.6
+// and 10.2.  14336 x 4096, 1 token: 26.5 and 23.3.
+bool dw_few(int64_t n, int64_t rows, int64_t cols) {
+  const int64_t tiles = ((rows + kFewRows - 1) / kFewRows) * ((cols + kFewCols - 1) / kFewCols), sms = sm_count();
+  const int64_t pairs = ((rows + 255) / 256) * ((cols + 255) / 256), waves = (pairs + sms / 2 - 1) / (sms / 2);
+  return 2.0 + double(rows) * double(cols) / 3e6 + 0.12 * double(n) * double((tiles + sms - 1) / sms) <
+         5.0 + 1.6 * double(waves) + 0.3 * double(n / 64);
 }
 
 int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds,

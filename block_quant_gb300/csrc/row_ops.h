@@ -89,7 +89,7 @@ size_t dw_part_bytes(int splits, int64_t rows, int64_t cols);
 int launch_dw(const DwArgs& a, void* stream);
 
 // few tokens: the sum of outer products, straight from dy and the FP8 rows
-constexpr int kDwFewTokens = 16;
+bool dw_few(int64_t n, int64_t rows, int64_t cols);
 int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds,
                   int n, int rows, int cols, void* dw, int64_t ld_dw, int accumulate, void* stream);
 
