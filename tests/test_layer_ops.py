@@ -472,6 +472,29 @@ def test_linear_dw(cuda, n, rows, cols, accumulate):
     assert outside_kept(dw, flat, 0, 0.5)
 
 
+# outer products in one and in several chunks of tokens, products in one and in several
+# shares, with rows that end inside a tile; gradients whose rows are not aligned
+@pytest.mark.parametrize("pitch,shift", [(0, 0), (8, 0), (3, 1)])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,rows,cols", [(16, 70, 272), (24, 250, 528), (33, 300, 16), (65, 1000, 2064), (130, 700, 528),
+                                         (2300, 250, 272), (4100, 520, 272), (5000, 100, 1040)])
+def test_linear_dw_rows_and_shares(cuda, n, rows, cols, accumulate, pitch, shift):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    x, xs, xv = fp8_rows(rng, n, cols, cuda)
+    dy, dv = bf16(rng.standard_normal((n, rows)), cuda)
+    dw, flat = empty(rows, cols, cuda, torch.bfloat16, pitch, shift, -0.25)
+    ws = workspace(n, rows, cols, cuda)
+    bq.linear_fp8_dw(dy, x, xs, dw, ws, accumulate=accumulate)
+    bq.linear_check(ws)
+    mag = np.abs(dv).T @ np.abs(xv)
+    ref = dv.T @ xv + (-0.25 if accumulate else 0)
+    tol = U * 1.001 * (np.abs(ref) + mag) + n * 2.0 ** -23 * mag  # (as above)
+    assert np.all(np.abs(f64(dw) - ref) <= tol)
+    assert outside_kept(dw, flat, shift, -0.25)
+
+
 def test_linear_of_no_tokens(cuda):
     import torch
 
