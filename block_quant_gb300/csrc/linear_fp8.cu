@@ -808,34 +808,35 @@ __global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x
   if (i < n) out[int64_t(blockIdx.y) * ldo + i] = x[int64_t(blockIdx.y) * ldx + i];
 }
 
-// Clusters of two k_linear_pair CTAs that fit the device at once (cached per
-// device; half the SMs if the occupancy query fails)
-int pair_slots() {
+// Clusters of `size` CTAs that fit the device at once with an SM for each CTA (k_linear_pair's
+// shared memory sees to that; cached per device; the SMs' share if the occupancy query fails).
+// 152 SMs hold 76 of two, 46 of three, 36 of four, 15 of eight.
+int cluster_slots(int size) {
   static std::mutex mu;
-  static int cached[64] = {0};
+  static int cached[64][9] = {};
+  const int share = sm_count() / size;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count() / 2;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return share;
   std::lock_guard<std::mutex> lock(mu);
-  if (cached[dev] == 0) {
+  int& n = cached[dev][size];
+  if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.x = unsigned(size);
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(2 * sm_count()));
+    cfg.gridDim = dim3(unsigned(size * sm_count()));
     cfg.blockDim = dim3(PAIR_THREADS);
     cfg.dynamicSmemBytes = PAIR_SMEM;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, k_linear_pair<false>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      n = share;
     }
-    cached[dev] = n;
   }
-  return cached[dev];
+  return n;
 }
 
 int launch_clusters(const void* kernel, int clusters, int size, int threads, int smem, void** args, cudaStream_t s) {
@@ -879,21 +880,27 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
   const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
   if (tiles > 0x7FFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  // k_linear: k-blocks are split while that leaves every CTA resident (a second wave costs a whole
-  // set-up: 64 tiles of 64 k-blocks, 14.0 us by 4 and 17.7 us by 8) and a share has one
-  // at least, by 8 four (24 tiles of 16: 5.2 us by 4, 6.3 us by 8; 3 tiles of 94: 12.2 and
-  // 8.7 us)
-  while (g.split < 8 && tiles * g.split * 2 <= int64_t(sm_count()) * 2 && nk >= (g.split == 4 ? 32 : g.split * 2))
-    g.split *= 2;
+  // k_linear: into how many CTAs to split a tile's k-blocks, by the times of 30 products.  A
+  // CTA alone on its SM takes 0.35 us a k-block (transposed 0.40), two on one 0.4 to 0.6 each, and a
+  // join by rows and shares; not into a second wave (75 tiles of 16 k-blocks: 8.5 us by 2, 14.9
+  // by 4).  128 rows and more, 48 tiles of 16: 8.2 us by 2, 10.1 by 4; 50 of 105: 23.6 by 2, 28.2
+  // by 3, 26.8 by 4; 100 of 64: 27.9 in one, 20.7 by 2; one row, 64 tiles of 64: 15.1 by 2,
+  // 13.7 by 4.
+  const int64_t waves = (tiles + 2 * sm_count() - 1) / (2 * sm_count());
+  const double one = a.transposed ? 0.40 : 0.35, full = double(std::min<int64_t>(a.n, BM)) / BM;
+  double us_one = tiles <= sm_count() ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
+  for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * cluster_slots(k); ++k) {
+    const int share = (nk + k - 1) / k;
+    const double us = (tiles <= cluster_slots(k) ? 5 + one * share : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share) +
+                      (k - 1) * (0.25 + 0.55 * full);
+    if (us < us_one) us_one = us, g.split = k;
+  }
   // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
-  // 5952 take 28 us there and 17 us on k_linear), where the waves of their tiles take less
-  // time, by the times of 20 products of 200 to 4000 rows: a wave of pairs 0.40 us a k-block and
-  // 2.5 us, of k_linear's CTAs, two an SM, 0.52 and 6.  337 rows of 11840 x 4512 (two waves or
-  // one): 38.3 us on pairs, 26.4 on k_linear; 849 of 6336 x 8144 (two and two): 62.8 and 96.1;
-  // 512 of 8192 x 4096 (one and one): 18.4 and 24.2.
-  const int64_t waves = (tiles * g.split + 2 * sm_count() - 1) / (2 * sm_count());
-  const double us_pair = 4 + double((pairs + pair_slots() - 1) / pair_slots()) * (0.40 * nk + 2.5);
-  const double us_one = 2 + double(waves) * (0.52 * ((nk + g.split - 1) / g.split) + 6);
+  // 5952 take 28 us there and 17 us on k_linear), where their tiles take less time: 0.40 us a k-block
+  // and 2.5 us a wave.  337 rows of 11840 x 4512 (two waves, or one of k_linear's): 38.3 us on
+  // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 62.8 and 96.1; 512 of 8192 x
+  // 4096 (one and one): 18.4 and 24.2.
+  const double us_pair = 4 + double((pairs + cluster_slots(2) - 1) / cluster_slots(2)) * (0.40 * nk + 2.5);
   if (a.n > BM && us_pair < us_one) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (unused without tma_out)
@@ -911,7 +918,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
     void* args[] = {&tx, &tw, &ts, &to, &g};
     const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
                                  : reinterpret_cast<const void*>(k_linear_pair<false>);
-    return launch_clusters(k, int(std::min<int64_t>(pairs, pair_slots())), 2, PAIR_THREADS, PAIR_SMEM, args, s);
+    return launch_clusters(k, int(std::min<int64_t>(pairs, cluster_slots(2))), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
   // two CTAs share an SM.  The X stages come last, and a product reads 128 rows of
   // the last one whatever it holds: what follows it is spare shared memory
@@ -967,7 +974,7 @@ int launch_dw(const DwArgs& a, void* stream) {
     if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw, 64)) return rc;
   const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
   void* args[] = {&ty, &tx, &to, &g};
-  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, pair_slots())), 2,
+  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, cluster_slots(2))), 2,
                                PAIR_THREADS, DW_SMEM, args, s))
     return rc;
   if (!g.part) return BQ_OK;
