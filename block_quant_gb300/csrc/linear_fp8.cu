@@ -89,8 +89,8 @@ struct LinArgs {
 // share of the k-blocks, and the shares are added in order through distributed
 // shared memory.  For few rows, where the weight's bytes and then the start of a CTA count:
 // 1 row of 8192 x 8192 takes 14.2 us (4.7 TB/s; its bytes alone are 9.9), 333 rows of 2880 x
-// 4096 take 12.5 (72 MB through L2, and about 5 us from the launch to the first product and
-// from the last to the stores).
+// 4096 take 11.7 (0.6 us of set-up, 0.9 to the first product, 16 k-blocks at 0.35 to 0.44, 3 for
+// the join and the stores).
 template <bool TRANS>
 __global__ void __launch_bounds__(THREADS, 2)
     k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const LinArgs g) {
@@ -577,8 +577,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // holds 64-column chunks of 128 bytes), the summed index is the tokens, one accumulator of
 // a tile's whole sum, two of them in turn.  The tile leaves as in k_linear_pair; a split
 // product's fp32 sums leave from registers.  Bound by the products: 8192 tokens, 14336 x
-// 4096 take 546 us with X's conversion to bf16 (15), 1.76 PFLOP/s, and 592 in a run of
+// 4096 take 520 us with X's conversion to bf16 (15), 1.85 PFLOP/s, and 587 in a run of
 // seconds under the power limit; a library's bf16 product of that size reaches 1.91 and 1.7.
+// Few tokens are bound by the tiles' stores (64: 24 us for 117 MB of dW, 4.9 TB/s; with two
+// stores of 64-byte rows a warp in place of one of whole lines 33).
 constexpr int DK = 64;                          // tokens of a k-block
 constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
 constexpr int DW_STAGES = 5, DW_BOX = 32 * 128;  // (a warp's staging of out: 32 rows x 64 bf16)
