@@ -810,35 +810,40 @@ __global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x
   if (i < n) out[int64_t(blockIdx.y) * ldo + i] = x[int64_t(blockIdx.y) * ldx + i];
 }
 
-// Clusters of `size` CTAs that fit the device at once with an SM for each CTA (k_linear_pair's
-// shared memory sees to that; cached per device; the SMs' share if the occupancy query fails).
-// 152 SMs hold 76 of two, 46 of three, 36 of four, 15 of eight.
-int cluster_slots(int size) {
+// slots[k]: clusters of k CTAs that fit the device at once with an SM for each CTA
+// (k_linear_pair's shared memory sees to that), k = 1 .. 8: 152 SMs hold 76 of two, 46 of
+// three, 36 of four, 15 of eight.  Found once per device; the SMs' share where the occupancy
+// query fails.
+const int* cluster_slots() {
   static std::mutex mu;
-  static int cached[64][9] = {};
-  const int share = sm_count() / size;
+  static int cached[65][9] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return share;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 64;
   std::lock_guard<std::mutex> lock(mu);
-  int& n = cached[dev][size];
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = unsigned(size);
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(unsigned(size * sm_count()));
-    cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = PAIR_SMEM;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_linear_pair<false>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = share;
+  int* slots = cached[dev];
+  if (slots[1] == 0) {
+    const int sms = sm_count();
+    cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM);
+    for (int size = 2; size <= 8; ++size) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = unsigned(size);
+      at[0].val.clusterDim.y = 1;
+      at[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(unsigned(size * sms));
+      cfg.blockDim = dim3(PAIR_THREADS);
+      cfg.dynamicSmemBytes = PAIR_SMEM;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&slots[size], k_linear_pair<false>, &cfg) != cudaSuccess || slots[size] < 1) {
+        cudaGetLastError();
+        slots[size] = sms / size;
+      }
     }
+    slots[1] = sms;
   }
-  return n;
+  return slots;
 }
 
 int launch_clusters(const void* kernel, int clusters, int size, int threads, int smem, void** args, cudaStream_t s) {
@@ -888,12 +893,13 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   // by 4).  128 rows and more, 48 tiles of 16: 8.2 us by 2, 10.1 by 4; 50 of 105: 23.6 by 2, 28.2
   // by 3, 26.8 by 4; 100 of 64: 27.9 in one, 20.7 by 2; one row, 64 tiles of 64: 15.1 by 2,
   // 13.7 by 4.
-  const int64_t waves = (tiles + 2 * sm_count() - 1) / (2 * sm_count());
+  const int* slots = cluster_slots();
+  const int64_t waves = (tiles + 2 * slots[1] - 1) / (2 * slots[1]);
   const double one = a.transposed ? 0.40 : 0.35, full = double(std::min<int64_t>(a.n, BM)) / BM;
-  double us_one = tiles <= sm_count() ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
-  for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * cluster_slots(k); ++k) {
+  double us_one = tiles <= slots[1] ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
+  for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * slots[k]; ++k) {
     const int share = (nk + k - 1) / k;
-    const double us = (tiles <= cluster_slots(k) ? 5 + one * share : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share) +
+    const double us = (tiles <= slots[k] ? 5 + one * share : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share) +
                       (k - 1) * (0.25 + 0.55 * full);
     if (us < us_one) us_one = us, g.split = k;
   }
@@ -902,7 +908,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   // and 2.5 us a wave.  337 rows of 11840 x 4512 (two waves, or one of k_linear's): 38.3 us on
   // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 62.8 and 96.1; 512 of 8192 x
   // 4096 (one and one): 18.4 and 24.2.
-  const double us_pair = 4 + double((pairs + cluster_slots(2) - 1) / cluster_slots(2)) * (0.40 * nk + 2.5);
+  const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
   if (a.n > BM && us_pair < us_one) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (unused without tma_out)
@@ -920,7 +926,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
     void* args[] = {&tx, &tw, &ts, &to, &g};
     const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
                                  : reinterpret_cast<const void*>(k_linear_pair<false>);
-    return launch_clusters(k, int(std::min<int64_t>(pairs, cluster_slots(2))), 2, PAIR_THREADS, PAIR_SMEM, args, s);
+    return launch_clusters(k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
   // two CTAs share an SM.  The X stages come last, and a product reads 128 rows of
   // the last one whatever it holds: what follows it is spare shared memory
@@ -976,7 +982,7 @@ int launch_dw(const DwArgs& a, void* stream) {
     if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw, 64)) return rc;
   const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
   void* args[] = {&ty, &tx, &to, &g};
-  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, cluster_slots(2))), 2,
+  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, cluster_slots()[2])), 2,
                                PAIR_THREADS, DW_SMEM, args, s))
     return rc;
   if (!g.part) return BQ_OK;
