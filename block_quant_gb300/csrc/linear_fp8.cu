@@ -899,8 +899,8 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   double us_one = tiles <= slots[1] ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
   for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * slots[k]; ++k) {
     const int share = (nk + k - 1) / k;
-    const double us = (tiles <= slots[k] ? 5 + one * share : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share) +
-                      (k - 1) * (0.25 + 0.55 * full);
+    const double us = tiles <= slots[k] ? 5 + one * share + (k - 1) * (0.12 + 0.2 * full)
+                                        : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share + (k - 1) * (0.25 + 0.55 * full);
     if (us < us_one) us_one = us, g.split = k;
   }
   // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
