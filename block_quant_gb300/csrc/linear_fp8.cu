@@ -295,13 +295,13 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Two accumulators of N = 256 fill tensor memory: k-block it sums into accumulator it & 1
 // while the epilogue reads the other.  A product takes the tensor cores 512 cycles a
 // k-block for N = 128 and 192 as well (X's rows, read from shared memory, set its pace), so
-// four accumulators of N = 128 took 391 us and 192-column tiles 387 where these take 335
+// four accumulators of N = 128 took 391 us and 192-column tiles 387 where these take 340
 // (8192 rows, 14336 x 4096).
 //
 // What bounds it: from one product's start to the next on the same accumulator pass about
 // 1400 cycles (512 of products, 370 until the epilogue sees them done, 400 to read them and
 // add half, 100 until the last arrival starts the next), so a k-block takes 700; and power,
-// which holds the clock near 1.7 GHz.  335 us are 2.87 PFLOP/s, in a run of seconds 383 us.
+// which holds the clock near 1.7 GHz.  340 us are 2.83 PFLOP/s, in a run of seconds 380 us.
 // Without the epilogue's reading and adding the same products and copies take 258 us, at
 // 1.5 GHz (twice the rate of a library's bf16 product: 252).
 constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
