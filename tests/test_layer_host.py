@@ -204,3 +204,10 @@ def test_binding_refuses_shapes_and_types():
         assert e.value.code == bq.BQ_EINVAL
     with pytest.raises(bq.BQError, match="not on a GPU"):  # right shapes and types
         bq.embed(t, ids, out, stream=0)
+
+
+def test_packed_call_refuses_what_it_does_not_know(built):
+    words = bytes(8 * 24)
+    assert built.bq_call(99, words) == INV
+    assert built.bq_call(-1, words) == INV
+    assert built.bq_call(0, None) == INV

@@ -534,3 +534,107 @@ def test_linear_same_bits_again_and_rows_apart(cuda):
     assert bad[7] and bad.sum() == 1
     keep = np.arange(n) != 7
     assert torch.equal(a[torch.as_tensor(keep)], b[torch.as_tensor(keep)])
+
+
+# ----------------------------------------------------------------------------- streams, graphs, large offsets
+
+
+def test_another_stream_and_a_graph(cuda):
+    """One step's chain on a stream of its own, then captured and replayed on new inputs:
+    the same bits as on the current stream."""
+    import torch
+
+    n, rows, cols, vocab = 300, 520, 272, 700
+    rng = np.random.default_rng(7)
+    table, ts, _ = fp8_weight(rng, vocab, cols, cuda)
+    w, ws_, _ = fp8_weight(rng, rows, cols, cuda)
+    gain = bf16(rng.standard_normal(cols), cuda)[0]
+    new = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device=cuda)  # noqa: E731
+    ids = new(n, t=torch.int64)
+    ws = workspace(n, rows, cols, cuda)
+    ws_e = new(bq.embed_grad_workspace(n, vocab, cols), t=torch.uint8)
+    ws_n = new(bq.rmsnorm_grad_workspace(n, cols), t=torch.uint8)
+    x, h, dh, dx, dy = new(n, cols), new(n, cols), new(n, cols), new(n, cols), new(n, rows)
+    q, qs, rstd = new(n, cols, t=torch.uint8), new(3, n, t=torch.float32), new(n, t=torch.float32)
+    y, dw, dg, dt = new(n, rows), new(rows, cols), new(cols), new(vocab, cols)
+
+    def chain():
+        bq.embed(table, ids, x, table_scale=ts)
+        bq.rmsnorm(x, gain, 1e-5, residual=x, h=h, codes=q, code_scale=qs, rstd=rstd)
+        bq.linear_fp8(q, qs, w, ws_, y, ws)
+        bq.linear_fp8_dw(dy, q, qs, dw, ws)
+        bq.linear_fp8_dx(dy, w, ws_, dh, ws)
+        bq.rmsnorm_grad(dh, h, gain, rstd, dx, dg, ws_n)
+        bq.embed_grad(dx, ids, dt, ws_e)
+        return [t.clone() for t in (x, h, q, qs, rstd, y, dw, dh, dx, dg, dt)]
+
+    def inputs(seed):
+        r = np.random.default_rng(seed)
+        ids.copy_(torch.as_tensor(r.integers(0, vocab, n)))
+        dy.copy_(torch.as_tensor(r.standard_normal((n, rows)).astype(np.float32)))
+
+    want = []
+    for seed in (1, 2, 3):
+        inputs(seed)
+        want.append(chain())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        inputs(1)
+        got = chain()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = chain()
+    for seed in (2, 3):
+        inputs(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[seed - 1]))
+    bq.linear_check(ws)
+
+
+def test_offsets_past_32_bits(cuda):
+    """Tables, batches and outputs of more than 2^31 elements: their last rows."""
+    import torch
+
+    rng = np.random.default_rng(3)
+    rows, cols = 525000, 4096  # 2.15 G elements, 4.3 GB
+    assert rows * cols > 2 ** 31
+    big = torch.zeros(rows, cols, dtype=torch.bfloat16, device=cuda)
+    last, lv = bf16(rng.standard_normal((3, cols)), cuda)
+    big[-3:] = last
+    ids = torch.tensor([rows - 1, 0, rows - 3, rows - 1], device=cuda)
+    out = torch.empty(4, cols, dtype=torch.bfloat16, device=cuda)
+    bq.embed(big, ids, out)
+    assert torch.equal(out[0], last[2]) and torch.equal(out[2], last[0]) and not out[1].any()
+    ws = torch.empty(bq.embed_grad_workspace(4, rows, cols), dtype=torch.uint8, device=cuda)
+    dy, dv = bf16(rng.standard_normal((4, cols)), cuda)
+    bq.embed_grad(dy, ids, big, ws)
+    want = dv[0] + dv[3]
+    assert np.all(np.abs(f64(big[-1]) - want) <= U * np.abs(want) + 2 * E * (np.abs(dv[0]) + np.abs(dv[3])))
+    assert torch.equal(big[-3], dy[2]) and torch.equal(big[0], dy[1]) and not big[-2].any() and not big[1:-3].any()
+
+    # as many rows through the norm: the last ones as by themselves
+    big[-3:] = last
+    gain = bf16(rng.standard_normal(cols), cuda)[0]
+    q = torch.empty(rows, cols, dtype=torch.uint8, device=cuda)
+    qs = torch.empty(cols // 128, rows, device=cuda)
+    bq.rmsnorm(big, gain, 1e-5, codes=q, code_scale=qs)
+    q1, qs1 = torch.empty(3, cols, dtype=torch.uint8, device=cuda), torch.empty(cols // 128, 3, device=cuda)
+    bq.rmsnorm(last, gain, 1e-5, codes=q1, code_scale=qs1)
+    assert torch.equal(q[-3:], q1) and torch.equal(qs[:, -3:], qs1)
+
+    # and a product that writes as many
+    k = 32
+    w, ws_, wv = fp8_weight(rng, cols, k, cuda)
+    x, xs, xv = fp8_rows(rng, 256, k, cuda)
+    many = x.repeat(rows // 256 + 1, 1)[:rows].contiguous()
+    scales = xs.repeat(1, rows // 256 + 1)[:, :rows].contiguous()
+    ws = workspace(rows, cols, k, cuda)
+    bq.linear_fp8(many, scales, w, ws_, big, ws)
+    bq.linear_check(ws)
+    at = (rows - 200 + np.arange(200)) % 256
+    ref = xv[at] @ wv.T
+    assert np.all(np.abs(f64(big[-200:]) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(xv[at], wv.T, k))
