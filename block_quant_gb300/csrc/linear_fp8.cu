@@ -81,7 +81,7 @@ struct LinArgs {
   int tile_cols;         // W's tiles in a row of tiles
   int split, stages;     // CTAs of a cluster that share a tile's k-blocks; pipeline stages
   int a_rows;            // rows of X that a stage holds (a multiple of 8, <= 128)
-  int tma_out;           // out takes TMA stores (16-byte aligned rows)
+  int bytes;             // of a store into out (store_bytes)
   int* status;
 };
 
@@ -360,12 +360,57 @@ __device__ __forceinline__ void put_box(const float* v, uint32_t box, int lane) 
   }
 }
 
-// the box to out's row0.., c0.., clipped to rows x cols: by TMA, or where out's rows are not
-// 16-byte aligned by plain stores, lane l columns l, l + 32 of each row
+// the box by plain stores of `bytes` (8, 4 or 2, as out's rows are aligned), a row's pieces
+// beside one another in the warp, eight loads before their stores
+template <int COLS, int BYTES>
+__device__ __forceinline__ void store_pieces(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int row0, int c0,
+                                             uint32_t box, int lane) {
+  constexpr int N = BYTES / 2, LANES = COLS / N < 32 ? COLS / N : 32, EACH = 32 / LANES;  // lanes a row, rows at once
+#pragma unroll
+  for (int k = 0; k < COLS; k += LANES * N) {
+    const int c = k + lane % LANES * N, left = cols - c0 - c;
+#pragma unroll 1
+    for (int r0 = lane / LANES; r0 < 32; r0 += 8 * EACH) {
+      uint32_t v[8][BYTES == 8 ? 2 : 1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (r0 + e * EACH >= 32) continue;
+        const uint32_t at = box_word<COLS>(box, r0 + e * EACH, c >> 3) + 2u * uint32_t(c & 7);
+        if constexpr (BYTES == 8)
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[e][0]), "=r"(v[e][1]) : "r"(at) : "memory");
+        else if constexpr (BYTES == 4)
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[e][0]) : "r"(at) : "memory");
+        else
+          asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v[e][0]) : "r"(at) : "memory");
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = r0 + e * EACH;
+        if (r >= 32 || row0 + r >= rows || left <= 0) continue;
+        __nv_bfloat16* o = out + int64_t(row0 + r) * ldo + c0 + c;
+        if (left >= N) {
+          if constexpr (BYTES == 8)
+            *reinterpret_cast<uint2*>(o) = make_uint2(v[e][0], v[e][1]);
+          else if constexpr (BYTES == 4)
+            *reinterpret_cast<uint32_t*>(o) = v[e][0];
+          else
+            *reinterpret_cast<uint16_t*>(o) = uint16_t(v[e][0]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (j < left) reinterpret_cast<uint16_t*>(o)[j] = uint16_t(v[e][j >> 1] >> (16 * (j & 1)));
+        }
+      }
+    }
+  }
+}
+
+// the box to out's row0.., c0.., clipped to rows x cols: by TMA where out's rows are 16-byte
+// aligned (`bytes`, as store_bytes has it)
 template <int COLS>
-__device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int tma_out,
+__device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int bytes,
                                           const CUtensorMap* map, int row0, int c0, uint32_t box, int lane) {
-  if (tma_out) {
+  if (bytes == 16) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0 && row0 < rows && c0 < cols) {
@@ -377,26 +422,22 @@ __device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int r
     }
   } else {
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < COLS; k += 32) {
-      const int c = lane + k, below = c0 + c < cols ? rows - row0 : 0;
-      __nv_bfloat16* o = out + int64_t(row0) * ldo + c0 + c;
-#pragma unroll 1
-      for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows' loads before their stores
-        uint16_t v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          asm volatile("ld.shared.u16 %0, [%1];"
-                       : "=h"(v[e])
-                       : "r"(box_word<COLS>(box, r0 + e, c >> 3) + 2u * uint32_t(c & 7))
-                       : "memory");
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (r0 + e < below) o[int64_t(r0 + e) * ldo] = __ushort_as_bfloat16(v[e]);
-      }
-    }
+    if (bytes == 8)
+      store_pieces<COLS, 8>(out, ldo, rows, cols, row0, c0, box, lane);
+    else if (bytes == 4)
+      store_pieces<COLS, 4>(out, ldo, rows, cols, row0, c0, box, lane);
+    else
+      store_pieces<COLS, 2>(out, ldo, rows, cols, row0, c0, box, lane);
     __syncwarp();
   }
+}
+
+// the widest store that out's rows are aligned to.  A copy by TMA clips rows at whole 16-byte
+// words only: where they end inside one it would write zeros past their end
+int store_bytes(const void* out, int64_t ldo, int cols) {
+  int bytes = cols % 8 ? 8 : 16;
+  while (bytes > 2 && (ldo * 2 % bytes || reinterpret_cast<uintptr_t>(out) % bytes)) bytes /= 2;
+  return bytes;
 }
 
 template <bool TRANS>
@@ -558,7 +599,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
         __syncwarp();
         put_box<32>(acc + 32 * u, box, lane);
-        store_box<32>(g.out, g.ldo, g.n, g.width, g.tma_out, &tmO, row0, c0 + 32 * u, box, lane);
+        store_box<32>(g.out, g.ldo, g.n, g.width, g.bytes, &tmO, row0, c0 + 32 * u, box, lane);
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
@@ -592,7 +633,7 @@ struct DwKernelArgs {
   int64_t ldo, n;
   int rows, cols, splits;
   int chunk_boxes;       // dY's copies bring one chunk each, not two
-  int accumulate, tma_out;
+  int accumulate, bytes;
   int* status;
 };
 
@@ -756,7 +797,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
       __syncwarp();
       put_box<64>(reinterpret_cast<const float*>(r), box, lane);
-      store_box<64>(g.out, g.ldo, g.rows, g.cols, g.tma_out, &tmO, row0, c0, box, lane);
+      store_box<64>(g.out, g.ldo, g.rows, g.cols, g.bytes, &tmO, row0, c0, box, lane);
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
   }
@@ -880,7 +921,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.xs = a.x_scale, g.ws = a.w_scale, g.out = static_cast<__nv_bfloat16*>(a.out);
   g.ld_xs = a.ld_xs, g.ldo = a.ldo, g.n = int(a.n), g.width = width, g.red = red;
   g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
-  g.split = 1, g.stages = 0, g.a_rows = BM, g.tma_out = 0;
+  g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
   const int nk = (red + BK - 1) / BK;
   CUtensorMap tx, tw, ts, to;
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
@@ -911,17 +952,15 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
   if (a.n > BM && us_pair < us_one) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
-    to = tx;  // (unused without tma_out)
+    to = tx;  // (not read by plain stores)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
       const int64_t ld = (a.n + 3) / 4 * 4;
       k_copy_scales<<<dim3(unsigned((a.n + 255) / 256), unsigned(nk)), 256, 0, s>>>(a.x_scale, a.ld_xs, a.n, a.scale_ws, ld);
       if (int rc = check("bq_linear_fp8 (scales)")) return rc;
       g.xs = a.scale_ws, g.ld_xs = ld;
     }
-    if (a.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+    if (g.bytes == 16)
       if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo, 32)) return rc;
-      g.tma_out = 1;
-    }
     if (int rc = encode_map_scales(&ts, g.xs, a.n, nk, g.ld_xs)) return rc;
     void* args[] = {&tx, &tw, &ts, &to, &g};
     const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
@@ -973,12 +1012,12 @@ int launch_dw(const DwArgs& a, void* stream) {
   g.part = g.splits > 1 ? a.part : nullptr;
   g.chunk_boxes = a.padded ? 0 : 1;
   g.accumulate = a.accumulate;
-  g.tma_out = !g.part && a.ld_dw % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 15) == 0;
+  g.bytes = store_bytes(a.dw, a.ld_dw, a.cols);
   CUtensorMap ty, tx, to;
   if (int rc = encode_map_chunks(&ty, a.dy, a.rows, a.n, a.ld_dy, a.padded ? 2 : 0)) return rc;
   if (int rc = encode_map_chunks(&tx, a.x, a.cols, a.n, a.ld_x, 2)) return rc;
-  to = tx;  // (unused without tma_out)
-  if (g.tma_out)
+  to = tx;  // (not read by plain stores)
+  if (g.bytes == 16)
     if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw, 64)) return rc;
   const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
   void* args[] = {&ty, &tx, &to, &g};

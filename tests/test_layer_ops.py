@@ -430,6 +430,24 @@ def test_linear(cuda, n, rows, cols):
         assert outside_kept(out, flat, shift)
 
 
+# many rows whose outputs are aligned to 16, 8, 4 and 2 bytes, and end inside a store
+@pytest.mark.parametrize("rows,pitch,shift", [(1997, 3, 0), (1996, 0, 0), (1995, 1, 4), (1998, 0, 0), (1997, 1, 2), (1997, 0, 1)])
+def test_linear_output_alignment(cuda, rows, pitch, shift):
+    import torch
+
+    n, cols = 4001, 272
+    rng = np.random.default_rng(rows + pitch)
+    x, xs, xv = fp8_rows(rng, n, cols, cuda)
+    w, ws_, wv = fp8_weight(rng, rows, cols, cuda)
+    out, flat = empty(n, rows, cuda, torch.bfloat16, pitch, shift)
+    ws = workspace(n, rows, cols, cuda)
+    bq.linear_fp8(x, xs, w, ws_, out, ws)
+    bq.linear_check(ws)
+    ref = xv @ wv.T
+    assert np.all(np.abs(f64(out) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(xv, wv.T, cols))
+    assert outside_kept(out, flat, shift)
+
+
 @pytest.mark.parametrize("n,rows,cols", SHAPES)
 def test_linear_dx(cuda, n, rows, cols):
     import torch
