@@ -190,9 +190,6 @@ int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, 
 // map whose boxes hold that many chunks (the last chunk of the last row reads up to the
 // next multiple of 64 columns: the pitch must cover it); 0, a 2-D map with boxes of one
 int encode_map_chunks(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int chunks);
-// a 2-D tiled tensor map over the fp32 scales of FP8 rows, [groups][pitch]: boxes of
-// one group's scales of 128 rows
-int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, int64_t pitch);
 // a 2-D tiled tensor map over bf16 rows (pitch in elements) for stores of boxes of 32 rows
 // and 32 (64-byte swizzle) or 64 columns (128-byte)
 int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int box_cols);

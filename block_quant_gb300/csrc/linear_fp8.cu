@@ -295,13 +295,13 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Two accumulators of N = 256 fill tensor memory: k-block it sums into accumulator it & 1
 // while the epilogue reads the other.  A product takes the tensor cores 512 cycles a
 // k-block for N = 128 and 192 as well (X's rows, read from shared memory, set its pace), so
-// four accumulators of N = 128 took 391 us and 192-column tiles 387 where these take 340
-// (8192 rows, 14336 x 4096).
+// four accumulators of N = 128 took 391 us and 192-column tiles 387 where these took 340
+// (8192 rows, 14336 x 4096; 347 since the scales have a ring of their own).
 //
 // What bounds it: from one product's start to the next on the same accumulator pass about
 // 1400 cycles (512 of products, 370 until the epilogue sees them done, 400 to read them and
 // add half, 100 until the last arrival starts the next), so a k-block takes 700; and power,
-// which holds the clock near 1.7 GHz.  340 us are 2.83 PFLOP/s, in a run of seconds 380 us.
+// which holds the clock near 1.7 GHz.  347 us are 2.77 PFLOP/s.
 // Without the epilogue's reading and adding the same products and copies take 258 us, at
 // 1.5 GHz (twice the rate of a library's bf16 product: 252).
 constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
@@ -316,16 +316,31 @@ constexpr int PAIR_THREADS = 128 + 32 * PEPI;
 constexpr int kRegsLaunch = 96, kRegsIssue = 32, kRegsEpilogue = 112;
 static_assert(128 * kRegsIssue + 32 * PEPI * kRegsEpilogue <= PAIR_THREADS * kRegsLaunch, "register split");
 constexpr int OUT_BOX = 32 * 64;                // 32 rows x 32 bf16 of out, one a warp
-// X's scales of a k-block (128 rows of this CTA) are copied with the stages, on the same
-// barrier: a plain load would queue behind the stages' copies.  An accumulator that is
-// full says that they have landed.  Slot it % SLOTS is free when the producer holds
-// stage it: its stage's last products were issued after every epilogue warp had handed
-// over the accumulators of k-block it - PSTAGES - 2.
+// X's scales of a k-block (128 rows of this CTA) come through a ring of their own, up to
+// SLOTS k-blocks ahead: loads by the epilogue warps themselves would queue behind the
+// stages' copies.  Warp 2 copies them with cp.async, four scales a lane, and each CTA has its
+// own two barriers a slot: its 32 lanes' copies complete the one, its epilogue warps, when
+// they have read the slot, the other.  Every access is of the generic proxy and every
+// hand-over a release and an acquire within the CTA, so nothing else has to order a
+// slot's readers and its next copy (a bulk copy into a slot that plain loads read would want a
+// proxy fence a warp and k-block).  A warp takes its scale before it waits for the products;
+// taken a k-block ahead, between the reading of the accumulator and the additions, it cost
+// 367 us in place of 347 (8192 rows, 14336 x 4096; spills).
 constexpr int SLOTS = 8, SLOT_BYTES = 128 * 4;
-static_assert(SLOTS > PSTAGES + 2, "scale slots");
 constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
 constexpr int kPairTmem = 2 * PN;
+
+// `bytes` (0 to 16, the rest zeros) to 16-byte aligned shared memory
+__device__ __forceinline__ void copy16_clipped(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// arrives on the barrier (whose count includes it) when this thread's copies so far have landed
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
@@ -443,17 +458,19 @@ int store_bytes(const void* out, int64_t ldo, int cols) {
 template <bool TRANS>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                  const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmO, const LinArgs g) {
+                  const __grid_constant__ CUtensorMap tmO, const LinArgs g) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4];
+  __shared__ __align__(8) uint64_t bars[2 * PSTAGES + 4 + 2 * SLOTS];
   __shared__ uint32_t tmem_slot;
   const uint32_t bar0 = smem_addr(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(PSTAGES + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * PSTAGES + 2 + b); };
+  auto sfull_bar = [&](int l) { return bar0 + 8u * uint32_t(2 * PSTAGES + 4 + l); };
+  auto sempty_bar = [&](int l) { return bar0 + 8u * uint32_t(2 * PSTAGES + 4 + SLOTS + l); };
 
   const int rank = int(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -468,6 +485,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull_bar(b), 1);
       mbar_init(tempty_bar(b), 2 * PEPI);  // the epilogue warps of both CTAs
+    }
+    for (int l = 0; l < SLOTS; ++l) {
+      mbar_init(sfull_bar(l), 32);     // warp 2's lanes
+      mbar_init(sempty_bar(l), PEPI);  // this CTA's epilogue warps
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -494,14 +515,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         banded_tile(t, mt, nt, kBand, bm, bn);
         const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
         for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = int(it % PSTAGES), l = int(it % SLOTS);
+          const int s = int(it % PSTAGES);
           ok = mbar_wait(empty_bar(s), ((it / PSTAGES) & 1u) ^ 1u, g.status, 31);
           if (!ok) break;
           const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
           const uint32_t fb = map_rank(full_bar(s), 0);
           if (elect_one()) {
-            if (rank == 0) mbar_expect_tx(full_bar(s), 2 * (PSTAGE_BYTES + SLOT_BYTES));
-            tma_load_2d_pair(base + OFF_SCALES + uint32_t(l) * SLOT_BYTES, &tmS, ma, kb, fb);
+            if (rank == 0) mbar_expect_tx(full_bar(s), 2 * PSTAGE_BYTES);
             tma_load_2d_pair(a_dst, &tmX, kb * BK, ma, fb);
             if (TRANS)
               tma_load_2d_pair(b_dst, &tmW, nb, kb * BK, fb);
@@ -545,6 +565,25 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       }
       // every product issued here has finished before the accumulators are freed
       if (it > 0 && ok) mbar_wait(tfull_bar(int((it - 1) & 1u)), ((it - 1) >> 1) & 1u, g.status, 36);
+    } else if (warp == 2) {
+      // ---------------- X's scales (both CTAs: this CTA's 128 rows)
+      const uint32_t dst = base + OFF_SCALES + 16u * uint32_t(lane);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        int bm, bn;
+        banded_tile(t, mt, nt, kBand, bm, bn);
+        const int row = bm * PM + 128 * rank + 4 * lane, bytes = 4 * max(0, min(4, g.n - row));
+        const float* xs = g.xs + (bytes ? row : 0);  // (rows past the last read as 0)
+        for (int kb = 0; kb < nk; ++kb, ++it, xs += g.ld_xs) {
+          const int l = int(it % SLOTS);
+          ok = mbar_wait(sempty_bar(l), ((it / SLOTS) & 1u) ^ 1u, g.status, 37);
+          if (!ok) break;
+          copy16_clipped(dst + uint32_t(l) * SLOT_BYTES, xs, bytes);
+          copies_arrive(sfull_bar(l));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the CTA
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
@@ -575,12 +614,16 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
         const uint32_t buf = it & 1u, l = it % SLOTS;
         const float w = __shfl_sync(0xFFFFFFFFu, wl, kb & 31);
-        ok = mbar_wait(tfull_bar(int(buf)), (it >> 1) & 1u, g.status, 35);
+        ok = mbar_wait(sfull_bar(int(l)), (it / SLOTS) & 1u, g.status, 38);
         if (!ok) break;
-        tc_fence_after();
         float f;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(my_scale + l * SLOT_BYTES) : "memory");
         f *= w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(sempty_bar(int(l)));
+        ok = mbar_wait(tfull_bar(int(buf)), (it >> 1) & 1u, g.status, 35);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int j = 0; j < PCOLS; j += 32) {
           uint32_t r[32];
@@ -843,7 +886,7 @@ __global__ void __launch_bounds__(256) k_dw_join(const DwKernelArgs g) {
   }
 }
 
-// X's scales at a pitch whose rows bulk copies can read
+// X's scales at a pitch whose rows 16-byte copies can read
 __global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x, int64_t ldx, int64_t n,
                                                      float* __restrict__ out, int64_t ldo) {
   after_previous();
@@ -923,7 +966,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
   g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
   const int nk = (red + BK - 1) / BK;
-  CUtensorMap tx, tw, ts, to;
+  CUtensorMap tx, tw, to;
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
   const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
@@ -961,8 +1004,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
     }
     if (g.bytes == 16)
       if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo, 32)) return rc;
-    if (int rc = encode_map_scales(&ts, g.xs, a.n, nk, g.ld_xs)) return rc;
-    void* args[] = {&tx, &tw, &ts, &to, &g};
+    void* args[] = {&tx, &tw, &to, &g};
     const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
                                  : reinterpret_cast<const void*>(k_linear_pair<false>);
     return launch_clusters(k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);

@@ -970,20 +970,6 @@ int encode_map_codes(void* map, const void* base, int64_t inner, int64_t outer, 
   return BQ_OK;
 }
 
-int encode_map_scales(void* map, const void* base, int64_t n, int64_t groups, int64_t pitch) {
-  EncodeTiled enc = encoder();
-  if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");
-  const cuuint64_t dims[2] = {cuuint64_t(n), cuuint64_t(groups)};
-  const cuuint64_t strides[1] = {cuuint64_t(pitch) * 4};
-  const cuuint32_t box[2] = {128u, 1u};
-  const cuuint32_t estr[2] = {1u, 1u};
-  const CUresult r = enc(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
-                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return set_error(BQ_EINVAL, "bq_linear_fp8: tensor map encoding failed (" + std::to_string(int(r)) + ")");
-  return BQ_OK;
-}
-
 int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows, int64_t pitch, int box_cols) {
   EncodeTiled enc = encoder();
   if (!enc) return set_error(BQ_EDEVICE, "bq_linear_fp8: cuTensorMapEncodeTiled unavailable");

@@ -513,6 +513,47 @@ def test_linear_dw_rows_and_shares(cuda, n, rows, cols, accumulate, pitch, shift
     assert outside_kept(dw, flat, shift, -0.25)
 
 
+def integer_rows(rng, n, cols, top, dev):
+    """FP8 rows of small integers whose scales are powers of two, no two groups of a row
+    beside one another the same: (codes, scales, values in fp64)."""
+    import torch
+
+    v = rng.integers(-2, 3, (n, cols)).astype(np.float32)
+    g = -(-cols // 128)
+    power = (np.arange(g)[:, None] * 3 + rng.integers(0, top, (1, n)) + rng.integers(0, 2, (g, n))) % top
+    scale = (2.0 ** power).astype(np.float32)
+    codes = e4m3_encode(v)
+    return torch.as_tensor(codes).to(dev), torch.as_tensor(scale).to(dev), L.decode_rows(codes, scale)
+
+
+# every sum is a whole number below 2^24, so exact in any order: a k-block that took another
+# block's or another tile's scales would show.  Several tiles a CTA pair, k-blocks more
+# and fewer than its ring of scales has slots, rows that end inside a lane's four scales, scales
+# at a pitch that copies by 16 bytes cannot read
+@pytest.mark.parametrize("n,rows,cols,spare", [(4100, 4200, 528, 0), (4098, 3000, 2064, 2), (4099, 2600, 5136, 1)])
+def test_linear_scales_exact(cuda, n, rows, cols, spare):
+    import torch
+
+    rng = np.random.default_rng(n)
+    x, s, xv = integer_rows(rng, n, cols, 8, cuda)
+    xs = torch.full((s.shape[0], n + spare), float("nan"), device=cuda)[:, :n]
+    xs.copy_(s)
+    wv = rng.integers(-2, 3, (rows, cols)).astype(np.float32)
+    tiles = (2.0 ** rng.integers(0, 4, (-(-rows // 128), -(-cols // 128)))).astype(np.float32)
+    codes = e4m3_encode(wv)
+    wv = L.decode_tiles(codes, tiles)
+    w, ws_ = torch.as_tensor(codes).to(cuda), torch.as_tensor(tiles).to(cuda)
+    # |sum| <= 2 * 2 * 2^7 * 2^3 * cols < 2^12 * 5136 = 1.25 * 2^24 at worst; as drawn:
+    ref = torch.as_tensor(xv).to(cuda) @ torch.as_tensor(wv).to(cuda).t()
+    assert float((torch.as_tensor(np.abs(xv)).to(cuda) @ torch.as_tensor(np.abs(wv)).to(cuda).t()).max()) < 2 ** 24
+    ws = workspace(n, rows, cols, cuda)
+    for _ in range(3):
+        out = torch.zeros(n, rows, dtype=torch.bfloat16, device=cuda)
+        bq.linear_fp8(x, xs, w, ws_, out, ws)
+        bq.linear_check(ws)
+        assert torch.equal(out, ref.float().bfloat16())
+
+
 def test_linear_of_no_tokens(cuda):
     import torch
 
