@@ -37,7 +37,7 @@ SOURCES = {
     "linear_fp8.cu": ["-lineinfo"],
 }
 BINDING = "binding.c"  # CPython module: argument marshalling of the layer operators
-HEADERS = ["bq_internal.h", "fp8_codes.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
+HEADERS = ["bq_internal.h", "fp8_codes.h", "once.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
 
 
 def nvcc():

@@ -197,7 +197,6 @@ int encode_map_bf16_out(void* map, const void* base, int64_t cols, int64_t rows,
 // errors
 int set_error(int code, const std::string& msg);
 int sm_count();  // SMs of the current device (cached per device)
-bool once_per_device(int key);  // true once per (current device, key); keys below
-constexpr int kOnceStripAttr = 0, kOnceGemmAttr = 1, kOnceTileAttr = 2, kOnceLinearAttr = 3, kOnceRingAttr = 4, kOnceDwAttr = 5;
+int current_device();  // -1 if there is none
 
 }  // namespace bq

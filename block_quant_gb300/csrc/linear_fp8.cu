@@ -18,6 +18,7 @@
 #include <string>
 
 #include "bq_internal.h"
+#include "once.h"
 #include "pdl.h"
 #include "row_ops.h"
 #include "tmem_ptx.h"
@@ -953,12 +954,16 @@ int launch_clusters(const void* kernel, int clusters, int size, int threads, int
 
 int launch_linear_fp8(const LinearArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (once_per_device(kOnceLinearAttr) &&
-      (cudaFuncSetAttribute(k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-       cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
-       cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
-       cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess))
-    return check("bq_linear_fp8 (shared memory attribute)");
+  static OncePerDevice once;
+  if (int rc = once.run(current_device(), [] {
+        if (cudaFuncSetAttribute(k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess)
+          return check("bq_linear_fp8 (shared memory attribute)");
+        return int(BQ_OK);
+      }))
+    return rc;
   const int width = a.transposed ? a.cols : a.rows, red = a.transposed ? a.rows : a.cols;
   LinArgs g;
   g.xs = a.x_scale, g.ws = a.w_scale, g.out = static_cast<__nv_bfloat16*>(a.out);
@@ -1044,9 +1049,13 @@ int dw_splits(int64_t n, int64_t rows, int64_t cols) {
 
 int launch_dw(const DwArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (once_per_device(kOnceDwAttr) &&
-      cudaFuncSetAttribute(k_dw_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
-    return check("bq_linear_fp8_dw (shared memory attribute)");
+  static OncePerDevice once;
+  if (int rc = once.run(current_device(), [] {
+        if (cudaFuncSetAttribute(k_dw_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
+          return check("bq_linear_fp8_dw (shared memory attribute)");
+        return int(BQ_OK);
+      }))
+    return rc;
   DwKernelArgs g;
   g.out = static_cast<__nv_bfloat16*>(a.dw);
   g.ldo = a.ld_dw, g.n = a.n, g.rows = a.rows, g.cols = a.cols, g.status = a.status;

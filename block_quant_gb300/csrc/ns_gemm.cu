@@ -28,6 +28,7 @@
 #include <vector>
 
 #include "bq_internal.h"
+#include "once.h"
 #include "tmem_ptx.h"
 #include "umma_ptx.h"
 
@@ -688,11 +689,13 @@ int check_mat(const bq_mat& t) {
 // the GEMM kernels' shared-memory attributes, set once per device (they belong
 // to the current device)
 int gemm_attrs() {
-  if (once_per_device(kOnceGemmAttr) &&
-      (cudaFuncSetAttribute(k_gemm_p, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM) != cudaSuccess ||
-       cudaFuncSetAttribute(k_gemm_2, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM2_SMEM) != cudaSuccess))
-    return check("bq_muon_ns (gemm shared memory attributes)");
-  return BQ_OK;
+  static OncePerDevice once;
+  return once.run(current_device(), [] {
+    if (cudaFuncSetAttribute(k_gemm_p, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(k_gemm_2, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM2_SMEM) != cudaSuccess)
+      return check("bq_muon_ns (gemm shared memory attributes)");
+    return int(BQ_OK);
+  });
 }
 
 int gemm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tat, const CUtensorMap& tbt,

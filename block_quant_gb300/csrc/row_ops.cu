@@ -15,6 +15,7 @@
 
 #include "bq_internal.h"
 #include "fp8_codes.h"
+#include "once.h"
 #include "pdl.h"
 #include "row_ops.h"
 #include "umma_ptx.h"
@@ -1535,15 +1536,17 @@ namespace {
 
 // the ring kernels' shared-memory attribute, set once per device
 int ring_attrs() {
-  if (!once_per_device(kOnceRingAttr)) return BQ_OK;
-  const void* kernels[] = {reinterpret_cast<const void*>(k_norm_many<1>), reinterpret_cast<const void*>(k_norm_many<2>),
-                           reinterpret_cast<const void*>(k_norm_many<4>),
-                           reinterpret_cast<const void*>(k_norm_grad_many<1>),
-                           reinterpret_cast<const void*>(k_norm_grad_many<2>)};
-  for (const void* k : kernels)
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
-      return check("bq_rmsnorm (shared memory attribute)");
-  return BQ_OK;
+  static OncePerDevice once;
+  return once.run(current_device(), [] {
+    const void* kernels[] = {reinterpret_cast<const void*>(k_norm_many<1>), reinterpret_cast<const void*>(k_norm_many<2>),
+                             reinterpret_cast<const void*>(k_norm_many<4>),
+                             reinterpret_cast<const void*>(k_norm_grad_many<1>),
+                             reinterpret_cast<const void*>(k_norm_grad_many<2>)};
+    for (const void* k : kernels)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) != cudaSuccess)
+        return check("bq_rmsnorm (shared memory attribute)");
+    return int(BQ_OK);
+  });
 }
 
 }  // namespace

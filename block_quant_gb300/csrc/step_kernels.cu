@@ -32,6 +32,7 @@
 
 #include "bq_internal.h"
 #include "fp8_codes.h"
+#include "once.h"
 #include "tmem_ptx.h"
 
 namespace bq {
@@ -1480,14 +1481,17 @@ int launch_adam8(const DevTables& t, const AdamArgs& a, void* stream) {
     const int grid = std::min(t.n_strips, sms * kStripCtas);
     const size_t smem = sizeof(TmaStage) * kRing + 2 * kRing * sizeof(uint64_t) +
                         2 * size_t(t.max_strip_tiles) * sizeof(uint32_t);
-    if (once_per_device(kOnceStripAttr)) {  // the attribute belongs to the current device
-      // the 227 KB opt-in limit covers static and dynamic shared memory; 1 KB is
-      // left for the static part (k_strip<true> keeps its TMEM address there)
-      constexpr int kDyn = 227 * 1024 - 1024;
-      if (cudaFuncSetAttribute(k_strip<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDyn) != cudaSuccess ||
-          cudaFuncSetAttribute(k_strip<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDyn) != cudaSuccess)
-        return check_launch("bq_step_adam8 (strip shared memory attribute)");
-    }
+    static OncePerDevice once;
+    if (int rc = once.run(current_device(), [] {
+          // the 227 KB opt-in limit covers static and dynamic shared memory; 1 KB is
+          // left for the static part (k_strip<true> keeps its TMEM address there)
+          constexpr int kDyn = 227 * 1024 - 1024;
+          if (cudaFuncSetAttribute(k_strip<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDyn) != cudaSuccess ||
+              cudaFuncSetAttribute(k_strip<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDyn) != cudaSuccess)
+            return check_launch("bq_step_adam8 (strip shared memory attribute)");
+          return int(BQ_OK);
+        }))
+      return rc;
     if (fp8)
       k_strip<true><<<grid, kStripThreads, smem, s>>>(t.strips, t.n_strips, a);
     else
@@ -1504,9 +1508,13 @@ int launch_adam8(const DevTables& t, const AdamArgs& a, void* stream) {
   if (t.n_tiles) {
     const int grid = std::min(t.n_tiles, sms * kTileCtasPerSm);
     constexpr int kTileP = 8 * kThreads * 2 * int(sizeof(float4));  // a 128x128 tile's p' (64 KB)
-    if (once_per_device(kOnceTileAttr) &&
-        cudaFuncSetAttribute(k_tile<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileP) != cudaSuccess)
-      return check_launch("bq_step_adam8 (tile shared memory attribute)");
+    static OncePerDevice once;
+    if (int rc = once.run(current_device(), [] {
+          if (cudaFuncSetAttribute(k_tile<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileP) != cudaSuccess)
+            return check_launch("bq_step_adam8 (tile shared memory attribute)");
+          return int(BQ_OK);
+        }))
+      return rc;
     if (fp8)
       k_tile<true><<<grid, kThreads, kTileP, s>>>(t.tiles, t.n_tiles, a);
     else
