@@ -18,7 +18,6 @@ static int (*g_call)(int, const void*);
 static PyObject *g_kinds;                 /* torch dtype -> kind (0, 1, 2); 32, 64: id types */
 static PyObject *g_fill;                  /* called with an unknown dtype: its kind or None */
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device;
-static int64_t g_device; /* of the tensors read so far in this call; -1: none (the GIL is held throughout) */
 
 typedef struct {
   int64_t p, ld, rows, cols, kind;
@@ -38,17 +37,18 @@ static int64_t kind_of(PyObject* x, const char* name) {
   return k ? PyLong_AsLongLong(k) : -1;
 }
 
-/* the tensor's address; all of a call's tensors must be on one GPU */
-static int pointer_of(PyObject* x, const char* name, int64_t* p) {
+/* the tensor's address; all of a call's tensors must be on one GPU: *dev, -1 before the first
+ * (each call's own: Python code that runs in between may make other calls) */
+static int pointer_of(int64_t* dev, PyObject* x, const char* name, int64_t* p) {
   PyObject* v = PyObject_CallMethodNoArgs(x, s_get_device);
   if (!v) return -1;
   const int64_t d = PyLong_AsLongLong(v);
   Py_DECREF(v);
-  if (d < 0 || (g_device >= 0 && d != g_device)) {
+  if (d < 0 || (*dev >= 0 && d != *dev)) {
     if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, d < 0 ? "%s is not on a GPU" : "%s is on another GPU", name);
     return -1;
   }
-  g_device = d;
+  *dev = d;
   v = PyObject_CallMethodNoArgs(x, s_data_ptr);
   if (!v) return -1;
   *p = (int64_t)PyLong_AsUnsignedLongLong(v);
@@ -67,7 +67,7 @@ static int ints(PyObject* t, int n, int64_t* v, const char* name) {
 }
 
 /* rows, cols: -1 for any */
-static int mat(PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
+static int mat(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
   if (x == Py_None) {
     PyErr_Format(PyExc_ValueError, "%s is None", name);
     return -1;
@@ -90,13 +90,13 @@ static int mat(PyObject* x, const char* name, int kinds, int64_t rows, int64_t c
     return -1;
   }
   m->ld = st[0], m->rows = s[0], m->cols = s[1];
-  return pointer_of(x, name, &m->p);
+  return pointer_of(dev, x, name, &m->p);
 }
 
 /* a matrix that may be None: zeros */
-static int opt(PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
+static int opt(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
   memset(m, 0, sizeof *m);
-  return x == Py_None ? 0 : mat(x, name, kinds, rows, cols, m);
+  return x == Py_None ? 0 : mat(dev, x, name, kinds, rows, cols, m);
 }
 
 static int contiguous(PyObject* x, const char* name) {
@@ -109,7 +109,7 @@ static int contiguous(PyObject* x, const char* name) {
 }
 
 /* n: -1 for any; returns the length in *got */
-static int vec(PyObject* x, const char* name, int kinds, int64_t n, int64_t* p, int64_t* kind, int64_t* got) {
+static int vec(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t n, int64_t* p, int64_t* kind, int64_t* got) {
   if (x == Py_None) {
     PyErr_Format(PyExc_ValueError, "%s is None", name);
     return -1;
@@ -127,11 +127,11 @@ static int vec(PyObject* x, const char* name, int kinds, int64_t n, int64_t* p, 
   }
   if (kind) *kind = k;
   if (got) *got = len;
-  return pointer_of(x, name, p);
+  return pointer_of(dev, x, name, p);
 }
 
 /* one fp32 scale per 128 x 128 tile, contiguous, of any shape */
-static int tiles(PyObject* x, const char* name, int64_t rows, int64_t cols, int64_t* p) {
+static int tiles(int64_t* dev, PyObject* x, const char* name, int64_t rows, int64_t cols, int64_t* p) {
   if (x == Py_None) {
     PyErr_Format(PyExc_ValueError, "%s is None", name);
     return -1;
@@ -148,18 +148,17 @@ static int tiles(PyObject* x, const char* name, int64_t rows, int64_t cols, int6
                  (long long)rows, (long long)cols);
     return -1;
   }
-  return contiguous(x, name) ? -1 : pointer_of(x, name, p);
+  return contiguous(x, name) ? -1 : pointer_of(dev, x, name, p);
 }
 
 /* FP8 rows: codes and their scales [ceil(cols / 128), n] */
-static int code_rows(PyObject* codes, PyObject* scale, int64_t n, int64_t cols, Mat* c, Mat* s) {
-  if (mat(codes, "codes", FP8, n, cols, c)) return -1;
-  return mat(scale, "code_scale", FP32, (c->cols + 127) / 128, c->rows, s);
+static int code_rows(int64_t* dev, PyObject* codes, PyObject* scale, int64_t n, int64_t cols, Mat* c, Mat* s) {
+  if (mat(dev, codes, "codes", FP8, n, cols, c)) return -1;
+  return mat(dev, scale, "code_scale", FP32, (c->cols + 127) / 128, c->rows, s);
 }
 
 /* the start of every call */
 static int args_are(Py_ssize_t n, Py_ssize_t want) {
-  g_device = -1;
   if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments, expected %zd", n, want);
   return n == want;
 }
@@ -186,10 +185,11 @@ static int integer(PyObject* o, int64_t* v) {
 /* workspace: pointer and bytes come as integers; stream likewise */
 
 static PyObject* f_embed(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* table ids out scale table_scale stream */
+  int64_t dev = -1;
   Mat t, o;
   int64_t ids, bits, count, ts = 0, st;
-  if (!args_are(n, 6) || mat(a[0], "table", BF16 | FP8, -1, -1, &t) || vec(a[1], "ids", 0, -1, &ids, &bits, &count) ||
-      mat(a[2], "out", BF16, count, t.cols, &o) || (t.kind == 2 && tiles(a[4], "table_scale", t.rows, t.cols, &ts)) ||
+  if (!args_are(n, 6) || mat(&dev, a[0], "table", BF16 | FP8, -1, -1, &t) || vec(&dev, a[1], "ids", 0, -1, &ids, &bits, &count) ||
+      mat(&dev, a[2], "out", BF16, count, t.cols, &o) || (t.kind == 2 && tiles(&dev, a[4], "table_scale", t.rows, t.cols, &ts)) ||
       integer(a[5], &st))
     return NULL;
   const double f = PyFloat_AsDouble(a[3]);
@@ -198,10 +198,11 @@ static PyObject* f_embed(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* 
 }
 
 static PyObject* f_embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy ids out ws bytes scale accumulate stream */
+  int64_t dev = -1;
   Mat d, o;
   int64_t ids, bits, count, ws, wb, st;
-  if (!args_are(n, 8) || vec(a[1], "ids", 0, -1, &ids, &bits, &count) || mat(a[2], "out", BF16 | FP32, -1, -1, &o) ||
-      mat(a[0], "dy", BF16, count, o.cols, &d) || integer(a[3], &ws) || integer(a[4], &wb) || integer(a[7], &st))
+  if (!args_are(n, 8) || vec(&dev, a[1], "ids", 0, -1, &ids, &bits, &count) || mat(&dev, a[2], "out", BF16 | FP32, -1, -1, &o) ||
+      mat(&dev, a[0], "dy", BF16, count, o.cols, &d) || integer(a[3], &ws) || integer(a[4], &wb) || integer(a[7], &st))
     return NULL;
   const double f = PyFloat_AsDouble(a[5]);
   const int acc = PyObject_IsTrue(a[6]);
@@ -211,16 +212,17 @@ static PyObject* f_embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) 
 
 static PyObject* f_rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   /* x weight eps residual h y codes code_scale rstd stream */
+  int64_t dev = -1;
   Mat x, r, h, y, c, s;
   int64_t w, q = 0, st;
-  if (!args_are(n, 10) || mat(a[0], "x", BF16, -1, -1, &x) || vec(a[1], "weight", BF16, x.cols, &w, NULL, NULL) ||
-      opt(a[3], "residual", BF16, x.rows, x.cols, &r) || opt(a[4], "h", BF16, x.rows, x.cols, &h) ||
-      opt(a[5], "y", BF16, x.rows, x.cols, &y))
+  if (!args_are(n, 10) || mat(&dev, a[0], "x", BF16, -1, -1, &x) || vec(&dev, a[1], "weight", BF16, x.cols, &w, NULL, NULL) ||
+      opt(&dev, a[3], "residual", BF16, x.rows, x.cols, &r) || opt(&dev, a[4], "h", BF16, x.rows, x.cols, &h) ||
+      opt(&dev, a[5], "y", BF16, x.rows, x.cols, &y))
     return NULL;
   memset(&c, 0, sizeof c);
   memset(&s, 0, sizeof s);
-  if (a[6] != Py_None && code_rows(a[6], a[7], x.rows, x.cols, &c, &s)) return NULL;
-  if ((a[8] != Py_None && vec(a[8], "rstd", FP32, x.rows, &q, NULL, NULL)) || integer(a[9], &st)) return NULL;
+  if (a[6] != Py_None && code_rows(&dev, a[6], a[7], x.rows, x.cols, &c, &s)) return NULL;
+  if ((a[8] != Py_None && vec(&dev, a[8], "rstd", FP32, x.rows, &q, NULL, NULL)) || integer(a[9], &st)) return NULL;
   const double eps = PyFloat_AsDouble(a[2]);
   if (PyErr_Occurred()) return NULL;
   RUN(2, x.p, x.ld, r.p, r.ld, w, word(eps), x.rows, x.cols, h.p, h.ld, y.p, y.ld, c.p, c.ld, s.p, s.ld, q, st);
@@ -228,12 +230,13 @@ static PyObject* f_rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 static PyObject* f_rmsnorm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   /* dy h weight rstd dx dw ws bytes dh accumulate stream */
+  int64_t dev = -1;
   Mat y, h, g, x;
   int64_t w, q, dw, kind, ws, wb, st;
-  if (!args_are(n, 11) || mat(a[1], "h", BF16, -1, -1, &h) || mat(a[0], "dy", BF16, h.rows, h.cols, &y) ||
-      vec(a[2], "weight", BF16, h.cols, &w, NULL, NULL) || vec(a[3], "rstd", FP32, h.rows, &q, NULL, NULL) ||
-      mat(a[4], "dx", BF16, h.rows, h.cols, &x) || vec(a[5], "dw", BF16 | FP32, h.cols, &dw, &kind, NULL) ||
-      opt(a[8], "dh", BF16, h.rows, h.cols, &g) || integer(a[6], &ws) || integer(a[7], &wb) || integer(a[10], &st))
+  if (!args_are(n, 11) || mat(&dev, a[1], "h", BF16, -1, -1, &h) || mat(&dev, a[0], "dy", BF16, h.rows, h.cols, &y) ||
+      vec(&dev, a[2], "weight", BF16, h.cols, &w, NULL, NULL) || vec(&dev, a[3], "rstd", FP32, h.rows, &q, NULL, NULL) ||
+      mat(&dev, a[4], "dx", BF16, h.rows, h.cols, &x) || vec(&dev, a[5], "dw", BF16 | FP32, h.cols, &dw, &kind, NULL) ||
+      opt(&dev, a[8], "dh", BF16, h.rows, h.cols, &g) || integer(a[6], &ws) || integer(a[7], &wb) || integer(a[10], &st))
     return NULL;
   const int acc = PyObject_IsTrue(a[9]);
   if (PyErr_Occurred()) return NULL;
@@ -241,39 +244,43 @@ static PyObject* f_rmsnorm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n
 }
 
 static PyObject* f_quant_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* x codes code_scale stream */
+  int64_t dev = -1;
   Mat x, c, s;
   int64_t st;
-  if (!args_are(n, 4) || mat(a[0], "x", BF16, -1, -1, &x) || code_rows(a[1], a[2], x.rows, x.cols, &c, &s) ||
+  if (!args_are(n, 4) || mat(&dev, a[0], "x", BF16, -1, -1, &x) || code_rows(&dev, a[1], a[2], x.rows, x.cols, &c, &s) ||
       integer(a[3], &st))
     return NULL;
   RUN(4, x.p, x.ld, x.rows, x.cols, c.p, c.ld, s.p, s.ld, st);
 }
 
 static PyObject* f_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* codes code_scale w w_scale out ws bytes stream */
+  int64_t dev = -1;
   Mat c, s, w, o;
   int64_t ts, ws, wb, st;
-  if (!args_are(n, 8) || mat(a[2], "w", FP8, -1, -1, &w) || code_rows(a[0], a[1], -1, w.cols, &c, &s) ||
-      tiles(a[3], "w_scale", w.rows, w.cols, &ts) || mat(a[4], "out", BF16, c.rows, w.rows, &o) || integer(a[5], &ws) ||
+  if (!args_are(n, 8) || mat(&dev, a[2], "w", FP8, -1, -1, &w) || code_rows(&dev, a[0], a[1], -1, w.cols, &c, &s) ||
+      tiles(&dev, a[3], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[4], "out", BF16, c.rows, w.rows, &o) || integer(a[5], &ws) ||
       integer(a[6], &wb) || integer(a[7], &st))
     return NULL;
   RUN(5, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, o.p, o.ld, ws, wb, st);
 }
 
 static PyObject* f_linear_dx(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy w w_scale dx ws bytes stream */
+  int64_t dev = -1;
   Mat y, w, x;
   int64_t ts, ws, wb, st;
-  if (!args_are(n, 7) || mat(a[1], "w", FP8, -1, -1, &w) || mat(a[0], "dy", BF16, -1, w.rows, &y) ||
-      tiles(a[2], "w_scale", w.rows, w.cols, &ts) || mat(a[3], "dx", BF16, y.rows, w.cols, &x) || integer(a[4], &ws) ||
+  if (!args_are(n, 7) || mat(&dev, a[1], "w", FP8, -1, -1, &w) || mat(&dev, a[0], "dy", BF16, -1, w.rows, &y) ||
+      tiles(&dev, a[2], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[3], "dx", BF16, y.rows, w.cols, &x) || integer(a[4], &ws) ||
       integer(a[5], &wb) || integer(a[6], &st))
     return NULL;
   RUN(6, y.p, y.ld, w.p, w.ld, ts, y.rows, w.rows, w.cols, x.p, x.ld, ws, wb, st);
 }
 
 static PyObject* f_linear_dw(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy codes code_scale dw ws bytes accumulate stream */
+  int64_t dev = -1;
   Mat y, c, s, d;
   int64_t ws, wb, st;
-  if (!args_are(n, 8) || mat(a[0], "dy", BF16, -1, -1, &y) || code_rows(a[1], a[2], y.rows, -1, &c, &s) ||
-      mat(a[3], "dw", BF16, y.cols, c.cols, &d) || integer(a[4], &ws) || integer(a[5], &wb) || integer(a[7], &st))
+  if (!args_are(n, 8) || mat(&dev, a[0], "dy", BF16, -1, -1, &y) || code_rows(&dev, a[1], a[2], y.rows, -1, &c, &s) ||
+      mat(&dev, a[3], "dw", BF16, y.cols, c.cols, &d) || integer(a[4], &ws) || integer(a[5], &wb) || integer(a[7], &st))
     return NULL;
   const int acc = PyObject_IsTrue(a[6]);
   if (PyErr_Occurred()) return NULL;
