@@ -410,8 +410,9 @@ def muon_ns_noalloc(mats, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, stre
 # ----------------------------------------------------------------------------- layer operators
 #
 # Matrices are 2-D torch tensors on the GPU whose last dimension is contiguous (a
-# row pitch is read off the tensor); 1-D tensors are contiguous.  Outputs are the
-# caller's, as everywhere.  Shapes and types are checked by the marshalling module
+# row pitch is read off the tensor); 1-D tensors and workspaces (of any type) are
+# contiguous, and all of a call's tensors on one GPU.  Outputs are the caller's, as
+# everywhere.  Shapes, types and GPUs are checked by the marshalling module
 # (csrc/binding.c), the rest by the library.
 
 _KIND_NAMES = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
@@ -435,17 +436,17 @@ def _layer():
     return _calls
 
 
-def _run(name, *args):
+def _read(name, *args):
     try:
-        rc = getattr(_calls or _layer(), name)(*args)
+        return getattr(_calls or _layer(), name)(*args)
     except (ValueError, AttributeError) as e:  # AttributeError: not a tensor
         raise BQError(BQ_EINVAL, f"invalid argument: {e}") from None
+
+
+def _run(name, *args):
+    rc = _read(name, *args)
     if rc != BQ_OK:
         _check(rc)
-
-
-def _ws(ws):
-    return (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def embed(table, ids, out, scale=1.0, table_scale=None, stream=None):
@@ -463,7 +464,7 @@ def embed_grad_workspace(n, rows, cols):
 def embed_grad(dy, ids, out, ws, scale=1.0, accumulate=False, stream=None):
     """out[v] = scale * sum of dy[t] over the tokens t of id v, every row of out
     written (accumulate: added to the rows that tokens name); out bf16 or fp32."""
-    _run("embed_grad", dy, ids, out, *_ws(ws), scale, accumulate, _stream(stream))
+    _run("embed_grad", dy, ids, out, ws, scale, accumulate, _stream(stream))
 
 
 def rmsnorm(x, weight, eps, residual=None, h=None, y=None, codes=None, code_scale=None, rstd=None, stream=None):
@@ -482,7 +483,7 @@ def rmsnorm_grad_workspace(n, cols):
 def rmsnorm_grad(dy, h, weight, rstd, dx, dw, ws, dh=None, accumulate=False, stream=None):
     """dx (of x and residual alike; dh, the gradient of h past the norm, is added) and
     dw (bf16 or fp32; accumulate: added to it) from dy and the forward's h and rstd."""
-    _run("rmsnorm_grad", dy, h, weight, rstd, dx, dw, *_ws(ws), dh, accumulate, _stream(stream))
+    _run("rmsnorm_grad", dy, h, weight, rstd, dx, dw, ws, dh, accumulate, _stream(stream))
 
 
 def quant_rows_fp8(x, codes, code_scale, stream=None):
@@ -501,21 +502,20 @@ def linear_fp8_workspace(n, rows, cols):
 def linear_fp8(codes, code_scale, w, w_scale, out, ws, stream=None):
     """out [n, rows] = X W^T: X the FP8 rows (codes [n, cols], code_scale), W the FP8
     weight [rows, cols] with its tile scales."""
-    _run("linear_fp8", codes, code_scale, w, w_scale, out, *_ws(ws), _stream(stream))
+    _run("linear_fp8", codes, code_scale, w, w_scale, out, ws, _stream(stream))
 
 
 def linear_fp8_dx(dy, w, w_scale, dx, ws, stream=None):
     """dx [n, cols] = Q W: Q the FP8 rows of dy [n, rows] (quantised in the call)."""
-    _run("linear_fp8_dx", dy, w, w_scale, dx, *_ws(ws), _stream(stream))
+    _run("linear_fp8_dx", dy, w, w_scale, dx, ws, _stream(stream))
 
 
 def linear_fp8_dw(dy, codes, code_scale, dw, ws, accumulate=False, stream=None):
     """dw [rows, cols] = dy^T X (accumulate: added to dw), X the forward's FP8 rows."""
-    _run("linear_fp8_dw", dy, codes, code_scale, dw, *_ws(ws), accumulate, _stream(stream))
+    _run("linear_fp8_dw", dy, codes, code_scale, dw, ws, accumulate, _stream(stream))
 
 
 def linear_check(ws, stream=None):
     """Synchronise the stream and raise if a device wait of a projection on this
     workspace timed out since the last check."""
-    bp, bb = _ws(ws)
-    _check(load().bq_linear_check(bp, bb, _stream(stream)))
+    _check(load().bq_linear_check(*_read("workspace", ws), _stream(stream)))

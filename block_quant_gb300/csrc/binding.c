@@ -17,7 +17,7 @@ enum { BF16 = 1, FP32 = 2, FP8 = 4 }; /* what an argument may be: 1 << BQ_ROWS_*
 static int (*g_call)(int, const void*);
 static PyObject *g_kinds;                 /* torch dtype -> kind (0, 1, 2); 32, 64: id types */
 static PyObject *g_fill;                  /* called with an unknown dtype: its kind or None */
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_nbytes;
 
 typedef struct {
   int64_t p, ld, rows, cols, kind;
@@ -151,6 +151,20 @@ static int tiles(int64_t* dev, PyObject* x, const char* name, int64_t rows, int6
   return contiguous(x, name) ? -1 : pointer_of(dev, x, name, p);
 }
 
+/* a contiguous tensor of any type and shape: its address and bytes */
+static int workspace(int64_t* dev, PyObject* x, int64_t* p, int64_t* bytes) {
+  if (x == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "ws is None");
+    return -1;
+  }
+  if (contiguous(x, "ws")) return -1;
+  PyObject* v = PyObject_GetAttr(x, s_nbytes);
+  if (!v) return -1;
+  *bytes = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  return PyErr_Occurred() ? -1 : pointer_of(dev, x, "ws", p);
+}
+
 /* FP8 rows: codes and their scales [ceil(cols / 128), n] */
 static int code_rows(int64_t* dev, PyObject* codes, PyObject* scale, int64_t n, int64_t cols, Mat* c, Mat* s) {
   if (mat(dev, codes, "codes", FP8, n, cols, c)) return -1;
@@ -182,7 +196,7 @@ static int integer(PyObject* o, int64_t* v) {
     Py_END_ALLOW_THREADS return PyLong_FromLong(rc); \
   } while (0)
 
-/* workspace: pointer and bytes come as integers; stream likewise */
+/* a stream comes as an integer */
 
 static PyObject* f_embed(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* table ids out scale table_scale stream */
   int64_t dev = -1;
@@ -197,15 +211,15 @@ static PyObject* f_embed(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* 
   RUN(0, t.p, t.kind, ts, t.rows, t.cols, t.ld, ids, bits, count, word(f), o.p, o.ld, st);
 }
 
-static PyObject* f_embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy ids out ws bytes scale accumulate stream */
+static PyObject* f_embed_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy ids out ws scale accumulate stream */
   int64_t dev = -1;
   Mat d, o;
   int64_t ids, bits, count, ws, wb, st;
-  if (!args_are(n, 8) || vec(&dev, a[1], "ids", 0, -1, &ids, &bits, &count) || mat(&dev, a[2], "out", BF16 | FP32, -1, -1, &o) ||
-      mat(&dev, a[0], "dy", BF16, count, o.cols, &d) || integer(a[3], &ws) || integer(a[4], &wb) || integer(a[7], &st))
+  if (!args_are(n, 7) || vec(&dev, a[1], "ids", 0, -1, &ids, &bits, &count) || mat(&dev, a[2], "out", BF16 | FP32, -1, -1, &o) ||
+      mat(&dev, a[0], "dy", BF16, count, o.cols, &d) || workspace(&dev, a[3], &ws, &wb) || integer(a[6], &st))
     return NULL;
-  const double f = PyFloat_AsDouble(a[5]);
-  const int acc = PyObject_IsTrue(a[6]);
+  const double f = PyFloat_AsDouble(a[4]);
+  const int acc = PyObject_IsTrue(a[5]);
   if (PyErr_Occurred()) return NULL;
   RUN(1, d.p, d.ld, ids, bits, count, word(f), o.rows, o.cols, o.p, o.kind, o.ld, acc, ws, wb, st);
 }
@@ -229,16 +243,16 @@ static PyObject* f_rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 static PyObject* f_rmsnorm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  /* dy h weight rstd dx dw ws bytes dh accumulate stream */
+  /* dy h weight rstd dx dw ws dh accumulate stream */
   int64_t dev = -1;
   Mat y, h, g, x;
   int64_t w, q, dw, kind, ws, wb, st;
-  if (!args_are(n, 11) || mat(&dev, a[1], "h", BF16, -1, -1, &h) || mat(&dev, a[0], "dy", BF16, h.rows, h.cols, &y) ||
+  if (!args_are(n, 10) || mat(&dev, a[1], "h", BF16, -1, -1, &h) || mat(&dev, a[0], "dy", BF16, h.rows, h.cols, &y) ||
       vec(&dev, a[2], "weight", BF16, h.cols, &w, NULL, NULL) || vec(&dev, a[3], "rstd", FP32, h.rows, &q, NULL, NULL) ||
       mat(&dev, a[4], "dx", BF16, h.rows, h.cols, &x) || vec(&dev, a[5], "dw", BF16 | FP32, h.cols, &dw, &kind, NULL) ||
-      opt(&dev, a[8], "dh", BF16, h.rows, h.cols, &g) || integer(a[6], &ws) || integer(a[7], &wb) || integer(a[10], &st))
+      opt(&dev, a[7], "dh", BF16, h.rows, h.cols, &g) || workspace(&dev, a[6], &ws, &wb) || integer(a[9], &st))
     return NULL;
-  const int acc = PyObject_IsTrue(a[9]);
+  const int acc = PyObject_IsTrue(a[8]);
   if (PyErr_Occurred()) return NULL;
   RUN(3, y.p, y.ld, h.p, h.ld, w, q, g.p, g.ld, h.rows, h.cols, x.p, x.ld, dw, kind, acc, ws, wb, st);
 }
@@ -253,38 +267,45 @@ static PyObject* f_quant_rows(PyObject* self, PyObject* const* a, Py_ssize_t n) 
   RUN(4, x.p, x.ld, x.rows, x.cols, c.p, c.ld, s.p, s.ld, st);
 }
 
-static PyObject* f_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* codes code_scale w w_scale out ws bytes stream */
+static PyObject* f_linear(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* codes code_scale w w_scale out ws stream */
   int64_t dev = -1;
   Mat c, s, w, o;
   int64_t ts, ws, wb, st;
-  if (!args_are(n, 8) || mat(&dev, a[2], "w", FP8, -1, -1, &w) || code_rows(&dev, a[0], a[1], -1, w.cols, &c, &s) ||
-      tiles(&dev, a[3], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[4], "out", BF16, c.rows, w.rows, &o) || integer(a[5], &ws) ||
-      integer(a[6], &wb) || integer(a[7], &st))
+  if (!args_are(n, 7) || mat(&dev, a[2], "w", FP8, -1, -1, &w) || code_rows(&dev, a[0], a[1], -1, w.cols, &c, &s) ||
+      tiles(&dev, a[3], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[4], "out", BF16, c.rows, w.rows, &o) ||
+      workspace(&dev, a[5], &ws, &wb) || integer(a[6], &st))
     return NULL;
   RUN(5, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, o.p, o.ld, ws, wb, st);
 }
 
-static PyObject* f_linear_dx(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy w w_scale dx ws bytes stream */
+static PyObject* f_linear_dx(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy w w_scale dx ws stream */
   int64_t dev = -1;
   Mat y, w, x;
   int64_t ts, ws, wb, st;
-  if (!args_are(n, 7) || mat(&dev, a[1], "w", FP8, -1, -1, &w) || mat(&dev, a[0], "dy", BF16, -1, w.rows, &y) ||
-      tiles(&dev, a[2], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[3], "dx", BF16, y.rows, w.cols, &x) || integer(a[4], &ws) ||
-      integer(a[5], &wb) || integer(a[6], &st))
+  if (!args_are(n, 6) || mat(&dev, a[1], "w", FP8, -1, -1, &w) || mat(&dev, a[0], "dy", BF16, -1, w.rows, &y) ||
+      tiles(&dev, a[2], "w_scale", w.rows, w.cols, &ts) || mat(&dev, a[3], "dx", BF16, y.rows, w.cols, &x) ||
+      workspace(&dev, a[4], &ws, &wb) || integer(a[5], &st))
     return NULL;
   RUN(6, y.p, y.ld, w.p, w.ld, ts, y.rows, w.rows, w.cols, x.p, x.ld, ws, wb, st);
 }
 
-static PyObject* f_linear_dw(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy codes code_scale dw ws bytes accumulate stream */
+static PyObject* f_linear_dw(PyObject* self, PyObject* const* a, Py_ssize_t n) { /* dy codes code_scale dw ws accumulate stream */
   int64_t dev = -1;
   Mat y, c, s, d;
   int64_t ws, wb, st;
-  if (!args_are(n, 8) || mat(&dev, a[0], "dy", BF16, -1, -1, &y) || code_rows(&dev, a[1], a[2], y.rows, -1, &c, &s) ||
-      mat(&dev, a[3], "dw", BF16, y.cols, c.cols, &d) || integer(a[4], &ws) || integer(a[5], &wb) || integer(a[7], &st))
+  if (!args_are(n, 7) || mat(&dev, a[0], "dy", BF16, -1, -1, &y) || code_rows(&dev, a[1], a[2], y.rows, -1, &c, &s) ||
+      mat(&dev, a[3], "dw", BF16, y.cols, c.cols, &d) || workspace(&dev, a[4], &ws, &wb) || integer(a[6], &st))
     return NULL;
-  const int acc = PyObject_IsTrue(a[6]);
+  const int acc = PyObject_IsTrue(a[5]);
   if (PyErr_Occurred()) return NULL;
   RUN(7, y.p, y.ld, c.p, c.ld, s.p, s.ld, c.rows, y.cols, c.cols, d.p, d.ld, acc, ws, wb, st);
+}
+
+/* the workspace of a check: (address, bytes) */
+static PyObject* f_workspace(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  int64_t dev = -1, p, bytes;
+  if (!args_are(n, 1) || workspace(&dev, a[0], &p, &bytes)) return NULL;
+  return Py_BuildValue("LL", (long long)p, (long long)bytes);
 }
 
 /* bind(address of bq_call, dict of kinds, function that adds to it) */
@@ -315,6 +336,7 @@ static PyMethodDef methods[] = {
     FN("linear_fp8", f_linear),
     FN("linear_fp8_dx", f_linear_dx),
     FN("linear_fp8_dw", f_linear_dw),
+    FN("workspace", f_workspace),
     {NULL, NULL, 0, NULL},
 };
 
@@ -327,6 +349,7 @@ PyMODINIT_FUNC PyInit__bqcall(void) {
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
   s_get_device = PyUnicode_InternFromString("get_device");
-  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_get_device) return NULL;
+  s_nbytes = PyUnicode_InternFromString("nbytes");
+  if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_is_contiguous || !s_get_device || !s_nbytes) return NULL;
   return PyModule_Create(&module);
 }

@@ -111,3 +111,39 @@ def test_a_call_made_while_another_reads_its_tensors(library):
         with pytest.raises(bq.BQError, match="another GPU"):
             embed(ids=Tensor("odd", 4, gpu=1), out=Tensor("bf16", 4, 16, gpu=1))  # the table is on GPU 0
         assert len(library.calls) == int(nested)  # the inner one alone
+
+
+WS = Tensor("u8", 1 << 20)
+X, W, F8, S = Tensor("bf16", 4, 16), Tensor("bf16", 16), Tensor("u8", 4, 16), Tensor("f32", 1, 4)
+WITH_WORKSPACE = {
+    "embed_grad": lambda ws: bq.embed_grad(X, Tensor("i64", 4), Tensor("bf16", 10, 16), ws, stream=0),
+    "rmsnorm_grad": lambda ws: bq.rmsnorm_grad(X, X, W, Tensor("f32", 4), X, W, ws, stream=0),
+    "linear_fp8": lambda ws: bq.linear_fp8(F8, S, Tensor("u8", 8, 16), Tensor("f32", 1), Tensor("bf16", 4, 8), ws, stream=0),
+    "linear_fp8_dx": lambda ws: bq.linear_fp8_dx(Tensor("bf16", 4, 8), Tensor("u8", 8, 16), Tensor("f32", 1), X, ws, stream=0),
+    "linear_fp8_dw": lambda ws: bq.linear_fp8_dw(Tensor("bf16", 4, 8), F8, S, Tensor("bf16", 8, 16), ws, stream=0),
+}
+
+
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_workspaces(library, name):
+    """A workspace in host memory, on another GPU, with gaps, or that is no tensor, never
+    reaches the library; one of any type on the call's GPU does."""
+    call = WITH_WORKSPACE[name]
+    for ws in (WS, Tensor("f32", 3, 5, 7)):
+        call(ws)
+    assert len(library.calls) == 2
+    for ws in (Tensor("u8", 1 << 20, gpu=-1), Tensor("u8", 1 << 20, gpu=1), Tensor("u8", 1 << 20, contiguous=False), None,
+               P, "ws"):
+        with pytest.raises(bq.BQError) as e:
+            call(ws)
+        assert e.value.code == bq.BQ_EINVAL
+    assert len(library.calls) == 2
+
+
+def test_the_checked_workspace_is_on_a_gpu():
+    import torch
+
+    for ws in (torch.zeros(256, dtype=torch.uint8), None, P):
+        with pytest.raises(bq.BQError) as e:
+            bq.linear_check(ws, stream=0)
+        assert e.value.code == bq.BQ_EINVAL
