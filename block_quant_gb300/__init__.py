@@ -411,13 +411,21 @@ def muon_ns_noalloc(mats, steps=5, a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, stre
 #
 # Matrices are 2-D torch tensors on the GPU whose last dimension is contiguous (a
 # row pitch is read off the tensor); 1-D tensors and workspaces (of any type) are
-# contiguous, and all of a call's tensors on one GPU.  Outputs are the caller's, as
+# contiguous, and all of a call's tensors on the current device.  Outputs are the caller's, as
 # everywhere.  Shapes, types and GPUs are checked by the marshalling module
 # (csrc/binding.c), the rest by the library.
 
 _KIND_NAMES = {"torch.bfloat16": ROWS_BF16, "torch.float32": ROWS_FP32, "torch.float8_e4m3fn": ROWS_FP8,
                "torch.uint8": ROWS_FP8, "torch.int32": 32, "torch.int64": 64}
 _calls = None
+
+
+def _current_device():
+    """The function that tells torch's current device, the short one where torch has it (it is
+    called once a tensor on a GPU has been seen, so CUDA is up)."""
+    import torch
+
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _layer():
@@ -431,7 +439,8 @@ def _layer():
         loader = importlib.machinery.ExtensionFileLoader("_bqcall", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_bqcall", loader))
         loader.exec_module(module)
-        module.bind(C.cast(lib.bq_call, C.c_void_p).value, {}, lambda dtype: _KIND_NAMES.get(str(dtype)))
+        module.bind(C.cast(lib.bq_call, C.c_void_p).value, {}, lambda dtype: _KIND_NAMES.get(str(dtype)),
+                    _current_device())
         _calls = module
     return _calls
 

@@ -17,6 +17,7 @@ enum { BF16 = 1, FP32 = 2, FP8 = 4 }; /* what an argument may be: 1 << BQ_ROWS_*
 static int (*g_call)(int, const void*);
 static PyObject *g_kinds;                 /* torch dtype -> kind (0, 1, 2); 32, 64: id types */
 static PyObject *g_fill;                  /* called with an unknown dtype: its kind or None */
+static PyObject *g_current;               /* called without arguments: the current device */
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_get_device, *s_nbytes;
 
 typedef struct {
@@ -165,6 +166,17 @@ static int workspace(int64_t* dev, PyObject* x, int64_t* p, int64_t* bytes) {
   return PyErr_Occurred() ? -1 : pointer_of(dev, x, "ws", p);
 }
 
+/* the library launches on the current device: it must be the tensors' */
+static int on_current(int64_t dev) {
+  PyObject* v = PyObject_CallNoArgs(g_current);
+  if (!v) return 0;
+  const int64_t d = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  if (d != dev && !PyErr_Occurred())
+    PyErr_Format(PyExc_ValueError, "the tensors are on GPU %lld, the current device is %lld", (long long)dev, (long long)d);
+  return !PyErr_Occurred();
+}
+
 /* FP8 rows: codes and their scales [ceil(cols / 128), n] */
 static int code_rows(int64_t* dev, PyObject* codes, PyObject* scale, int64_t n, int64_t cols, Mat* c, Mat* s) {
   if (mat(dev, codes, "codes", FP8, n, cols, c)) return -1;
@@ -192,6 +204,7 @@ static int integer(PyObject* o, int64_t* v) {
   do {                                           \
     const int64_t words_[] = {__VA_ARGS__};      \
     int rc;                                      \
+    if (!on_current(dev)) return NULL;           \
     Py_BEGIN_ALLOW_THREADS rc = g_call(op, words_);  \
     Py_END_ALLOW_THREADS return PyLong_FromLong(rc); \
   } while (0)
@@ -304,13 +317,13 @@ static PyObject* f_linear_dw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 /* the workspace of a check: (address, bytes) */
 static PyObject* f_workspace(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t dev = -1, p, bytes;
-  if (!args_are(n, 1) || workspace(&dev, a[0], &p, &bytes)) return NULL;
+  if (!args_are(n, 1) || workspace(&dev, a[0], &p, &bytes) || !on_current(dev)) return NULL;
   return Py_BuildValue("LL", (long long)p, (long long)bytes);
 }
 
-/* bind(address of bq_call, dict of kinds, function that adds to it) */
+/* bind(address of bq_call, dict of kinds, function that adds to it, current device's function) */
 static PyObject* f_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!args_are(n, 3)) return NULL;
+  if (!args_are(n, 4)) return NULL;
   void* p = PyLong_AsVoidPtr(a[0]);
   if (PyErr_Occurred()) return NULL;
   if (!PyDict_Check(a[1])) {
@@ -322,6 +335,8 @@ static PyObject* f_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_XSETREF(g_kinds, a[1]);
   Py_INCREF(a[2]);
   Py_XSETREF(g_fill, a[2]);
+  Py_INCREF(a[3]);
+  Py_XSETREF(g_current, a[3]);
   Py_RETURN_NONE;
 }
 

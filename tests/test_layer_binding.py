@@ -53,7 +53,7 @@ class Library:
     KINDS = {"bf16": 0, "f32": 1, "u8": 2, "i32": 32, "i64": 64}
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.current = [], 0
         self.entry = C.CFUNCTYPE(C.c_int, C.c_int, C.c_void_p)(self._call)
 
     def _call(self, op, words):
@@ -61,7 +61,8 @@ class Library:
         return 0
 
     def bind(self, module, fill=None):
-        module.bind(C.cast(self.entry, C.c_void_p).value, dict(self.KINDS), fill or (lambda dtype: None))
+        module.bind(C.cast(self.entry, C.c_void_p).value, dict(self.KINDS), fill or (lambda dtype: None),
+                    lambda: self.current)
 
 
 @pytest.fixture
@@ -105,6 +106,7 @@ def test_a_call_made_while_another_reads_its_tensors(library):
         return 64
 
     module = bq._layer()
+    library.current = 1
     for nested in (False, True):
         library.bind(module, fill)
         library.calls.clear()
@@ -147,3 +149,23 @@ def test_the_checked_workspace_is_on_a_gpu():
         with pytest.raises(bq.BQError) as e:
             bq.linear_check(ws, stream=0)
         assert e.value.code == bq.BQ_EINVAL
+
+
+def test_the_current_device_is_the_tensors(library):
+    """A call runs on the current device's stream, by its sizes: tensors elsewhere are refused."""
+    with pytest.raises(bq.BQError, match="current device") as e:
+        embed(gpu=1)
+    assert e.value.code == bq.BQ_EINVAL and not library.calls
+    library.current = 1
+    embed(gpu=1)
+    assert len(library.calls) == 1
+    for call in WITH_WORKSPACE.values():
+        with pytest.raises(bq.BQError, match="current device"):
+            call(WS)
+    with pytest.raises(bq.BQError, match="current device"):
+        bq.rmsnorm(X, W, 1e-5, y=X, stream=0)
+    with pytest.raises(bq.BQError, match="current device"):
+        bq.quant_rows_fp8(X, F8, S, stream=0)
+    with pytest.raises(bq.BQError, match="current device"):
+        bq.linear_check(WS, stream=0)
+    assert len(library.calls) == 1
