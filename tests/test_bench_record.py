@@ -25,6 +25,30 @@ def test_code_digest_ignores_comments_only(tmp_path):
     assert bench.code_digest([a]) != bench.code_digest([d])
 
 
+def test_record_covers_the_headers_of_its_sources():
+    """A change of any project header that the recorded kernels include drops the record."""
+    import json
+    import re
+
+    def included(path):
+        with open(path) as f:
+            names = re.findall(r'^\s*#include "([^"]+)"', f.read(), flags=re.M)
+        return [os.path.normpath(os.path.join(os.path.dirname(path), n)) for n in names]
+
+    with open(os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
+        record = json.load(f)
+    public = os.path.join(bench.ROOT, "include", "bq.h")  # declarations and error codes: what callers see
+    for call, rec in record.items():
+        listed = {os.path.join(bench.ROOT, name) for name in rec["sources"]}
+        todo, seen = list(listed), set()
+        while todo:
+            p = todo.pop()
+            if p in seen or p == public:
+                continue
+            seen.add(p)
+            assert p in listed, f"{call}: {os.path.relpath(p, bench.ROOT)} is included but not listed"
+            todo += included(p)
+
 
 def test_reference_config_matches_library_group():
     """Both arms print the same workload config: the reference arm computes the
