@@ -697,3 +697,85 @@ def test_offsets_past_32_bits(cuda):
     at = (rows - 200 + np.arange(200)) % 256
     ref = xv[at] @ wv.T
     assert np.all(np.abs(f64(big[-200:]) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(xv[at], wv.T, k))
+
+
+# ----------------------------------------------------------------------------- row quantiser, group by group
+
+
+def quantise(y):
+    """(codes, scales [groups, n]) of fp32 rows by the rule of the codes, each operation
+    rounded to fp32 once: s = a / 448, code = e4m3(y * (448 / a)).  Ordinary groups only."""
+    n, cols = y.shape
+    g = -(-cols // 128)
+    p = np.zeros((n, g * 128), np.float32)
+    p[:, :cols] = y
+    a = np.abs(p.reshape(n, g, 128)).max(axis=2)
+    r = np.repeat(np.float32(448) / a, 128, axis=1)[:, :cols]
+    return e4m3_encode(y * r), (a / np.float32(448)).T
+
+
+@pytest.mark.parametrize("cols", [1, 8, 100, 128, 130, 264, 1032, 2881])
+def test_quant_rows_zero_and_tiny(cuda, cols):
+    """Rows of zeros have scales and codes of 0; rows whose 448 / a overflows get their codes by
+    dividing by the scale: 2^-130 / s is within 2^-10 of 448, every code the largest."""
+    import torch
+
+    n = 19
+    x, _ = bf16(np.random.default_rng(cols).standard_normal((n, cols)), cuda)
+    x[3], x[4], x[5] = 0, 2.0 ** -130, -(2.0 ** -130)
+    codes = torch.full((n, cols), 0x55, dtype=torch.uint8, device=cuda)
+    scale = torch.empty(-(-cols // 128), n, device=cuda)
+    bq.quant_rows_fp8(x, codes, scale)
+    assert not codes[3].any() and not scale[:, 3].any()
+    assert torch.all(codes[4] == 0x7E) and torch.all(codes[5] == 0xFE)
+
+
+# many rows (four spans a warp) and few (one); rows of whole words, rows that are not, codes that
+# are not.  A warp's groups are of every kind beside one another
+@pytest.mark.parametrize("n,cols,pitch,shift", [(1300, 4096, 0, 0), (700, 1032, 8, 0), (1300, 264, 3, 1), (650, 2872, 5, 3),
+                                                (1300, 2881, 0, 0), (1300, 131, 2, 1), (40, 1032, 0, 0), (40, 1032, 3, 1),
+                                                (40, 1031, 0, 0)])
+def test_quant_rows_groups(cuda, n, cols, pitch, shift):
+    import torch
+
+    rng = np.random.default_rng(n + cols)
+    g = -(-cols // 128)
+    kind = rng.choice(["plain", "zero", "tiny", "nan", "inf"], (n, g), p=[0.6, 0.1, 0.1, 0.1, 0.1])
+    kind[::3] = "plain"  # (rows whose warps see nothing else)
+    spread = lambda v: np.repeat(v, 128, axis=1)[:, :cols]  # noqa: E731
+    of = spread(kind)
+    factor = np.exp(4 * rng.standard_normal((n, g)))
+    a = rng.standard_normal((n, cols)) * spread(factor)
+    a[of == "zero"] = 0
+    a[of == "tiny"] *= (2.0 ** -125 / spread(factor))[of == "tiny"]
+    first = np.arange(g) * 128
+    at = np.minimum(first[None, :] + rng.integers(0, 128, (n, g)), cols - 1)
+    rows = np.broadcast_to(np.arange(n)[:, None], (n, g))
+    a[rows[kind == "nan"], at[kind == "nan"]] = np.nan
+    a[rows[kind == "inf"], at[kind == "inf"]] = -np.inf
+    x, xv = bf16(a, cuda, pitch, shift)
+    codes = torch.full((n, cols), 0x55, dtype=torch.uint8, device=cuda)
+    scale = torch.empty(g, n, device=cuda)
+    bq.quant_rows_fp8(x, codes, scale)
+    got, s = codes.cpu().numpy(), scale.cpu().numpy()
+    plain, zero, tiny = of == "plain", of == "zero", of == "tiny"
+    # ordinary groups bit for bit
+    ordinary = np.where(plain, xv, 1.0).astype(np.float32)
+    want, want_s = quantise(ordinary)
+    assert np.array_equal(got[plain], want[plain])
+    assert np.array_equal(s.T[kind == "plain"], want_s.T[kind == "plain"])
+    assert not (got[zero] & 0x7F).any() and not s.T[kind == "zero"].any()
+    # tiny groups: a scale within half a step of the subnormals, codes within half a step of y / s
+    top = np.where(tiny, np.abs(xv), 0)
+    top = np.pad(top, ((0, 0), (0, g * 128 - cols))).reshape(n, g, 128).max(axis=2)
+    st = s.T.astype(np.float64)
+    assert np.all(np.abs(st - top / 448)[kind == "tiny"] <= 2.0 ** -150)
+    v, sv = e4m3_decode(got).astype(np.float64), spread(st)
+    with np.errstate(invalid="ignore"):
+        y = xv / sv
+        off = np.abs(v - np.clip(y, -448, 448)) <= 2.0 ** -4 * np.abs(v) * 1.001 + 2.0 ** -10 * 1.001
+    assert np.all(off[tiny])
+    # a NaN makes its group's scale NaN; an infinity makes its scale infinite and its own code NaN
+    assert np.all(np.isnan(s.T[kind == "nan"]))
+    assert np.all(np.isposinf(s.T[kind == "inf"]))
+    assert np.all(np.isnan(e4m3_decode(got[rows[kind == "inf"], at[kind == "inf"]])))
