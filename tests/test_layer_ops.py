@@ -779,3 +779,25 @@ def test_quant_rows_groups(cuda, n, cols, pitch, shift):
     assert np.all(np.isnan(s.T[kind == "nan"]))
     assert np.all(np.isposinf(s.T[kind == "inf"]))
     assert np.all(np.isnan(e4m3_decode(got[rows[kind == "inf"], at[kind == "inf"]])))
+
+
+# the input gradient against rows quantised here, bit for bit the quantiser's
+@pytest.mark.parametrize("n,rows,cols", [(33, 257, 1040), (300, 520, 2064), (2048, 1024, 640), (700, 4000, 1536),
+                                         (4100, 1000, 1040), (1100, 520, 400), (1950, 4096, 3008), (1300, 1001, 272)])
+def test_linear_dx_of_rows_quantised_apart(cuda, n, rows, cols):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    w, ws_, wv = fp8_weight(rng, rows, cols, cuda)
+    dy, dv = bf16(rng.standard_normal((n, rows)), cuda)
+    q, qs = quantise(dv.astype(np.float32))
+    codes, scale = torch.empty(n, rows, dtype=torch.uint8, device=cuda), torch.empty(-(-rows // 128), n, device=cuda)
+    bq.quant_rows_fp8(dy, codes, scale)
+    assert np.array_equal(codes.cpu().numpy(), q) and np.array_equal(scale.cpu().numpy(), qs)
+    qv = L.decode_rows(q, qs)
+    dx = torch.empty(n, cols, dtype=torch.bfloat16, device=cuda)
+    ws = workspace(n, rows, cols, cuda)
+    bq.linear_fp8_dx(dy, w, ws_, dx, ws)
+    bq.linear_check(ws)
+    ref = qv @ wv
+    assert np.all(np.abs(f64(dx) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(qv, wv, rows))
