@@ -801,3 +801,53 @@ def test_linear_dx_of_rows_quantised_apart(cuda, n, rows, cols):
     bq.linear_check(ws)
     ref = qv @ wv
     assert np.all(np.abs(f64(dx) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(qv, wv, rows))
+
+
+# ----------------------------------------------------------------------------- products of whole numbers: exact
+
+
+def small_integers(rng, shape, dev):
+    import torch
+
+    v = rng.integers(-3, 4, shape).astype(np.float32)
+    return torch.as_tensor(v).bfloat16().to(dev), v.astype(np.float64)
+
+
+# Every product is a whole number of at most 3 * 2 * 2^3 and every sum below 2^24, so exact
+# however it is split: a token, a share or a tail left out or counted twice shows
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,rows,cols", SHAPES + [(16, 70, 272), (24, 250, 528), (33, 300, 16), (65, 1000, 2064), (130, 700, 528),
+                                                  (2300, 250, 272), (4100, 520, 272), (5000, 100, 1040), (8191, 1024, 1024),
+                                                  (63, 520, 528), (64, 520, 528)])
+def test_linear_dw_exact(cuda, n, rows, cols, accumulate):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    x, xs, xv = integer_rows(rng, n, cols, 4, cuda)
+    dy, dv = small_integers(rng, (n, rows), cuda)
+    dw, old = small_integers(rng, (rows, cols), cuda)
+    assert n * 48 < 2 ** 24
+    ref = torch.as_tensor(dv).to(cuda).t() @ torch.as_tensor(xv).to(cuda)
+    if accumulate:
+        ref += torch.as_tensor(old).to(cuda)
+    ws = workspace(n, rows, cols, cuda)
+    bq.linear_fp8_dw(dy, x, xs, dw, ws, accumulate=accumulate)
+    bq.linear_check(ws)
+    assert torch.equal(dw, ref.float().bfloat16())
+
+
+@pytest.mark.parametrize("n,rows,cols", SHAPES)
+def test_linear_exact(cuda, n, rows, cols):
+    import torch
+
+    rng = np.random.default_rng(n + rows + cols)
+    x, xs, xv = integer_rows(rng, n, cols, 8, cuda)
+    codes = e4m3_encode(rng.integers(-2, 3, (rows, cols)).astype(np.float32))
+    tiles = (2.0 ** rng.integers(0, 3, (-(-rows // 128), -(-cols // 128)))).astype(np.float32)
+    wv = L.decode_tiles(codes, tiles)
+    assert 4 * 2 ** 9 * cols <= 2 ** 24
+    ref = torch.as_tensor(xv).to(cuda) @ torch.as_tensor(wv).to(cuda).t()
+    out, ws = torch.empty(n, rows, dtype=torch.bfloat16, device=cuda), workspace(n, rows, cols, cuda)
+    bq.linear_fp8(x, xs, torch.as_tensor(codes).to(cuda), torch.as_tensor(tiles).to(cuda), out, ws)
+    bq.linear_check(ws)
+    assert torch.equal(out, ref.float().bfloat16())
