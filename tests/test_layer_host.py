@@ -211,3 +211,37 @@ def test_packed_call_refuses_what_it_does_not_know(built):
     assert built.bq_call(99, words) == INV
     assert built.bq_call(-1, words) == INV
     assert built.bq_call(0, None) == INV
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_gathered_weights_are_one_run(built, seed):
+    """A matrix whose shards lie on several devices: in the gathered buffers (the devices' shards
+    one after another) its codes are one row-major run from its start and its tile scales one
+    run from its first slot, as the projections and the lookup read them."""
+    rng = np.random.default_rng(seed)
+    descs = []
+    for _ in range(int(rng.integers(3, 12))):
+        if rng.random() < 0.3:
+            descs.append((1, int(rng.integers(1, 3000)), 256, bq.ADAM_FLAT256, 0))
+            continue
+        rows, cols = int(rng.integers(2, 2000)), 16 * int(rng.integers(1, 60))
+        descs.append((rows, cols, int(np.lcm(128 * cols, 256)), bq.ADAM_FLAT256, 1))
+    spanning = 0
+    for V in (1, 2, 3, 8):
+        t = bq.plan(descs, V, start_align=16).export()
+        S, n, ni = int(t[3]), int(t[4]), int(t[5])
+        starts = t[8:8 + 7 * n].reshape(n, 7)[:, 0]
+        rows = t[8 + 7 * n:8 + 7 * n + 7 * ni].reshape(ni, 7)  # dev, tensor, t_off, len, local_off, mslot, fslot
+        for i, (r, c, _, _, fp8) in enumerate(descs):
+            if not fp8:
+                continue
+            mine = rows[rows[:, 1] == i]
+            spanning += len(mine) > 1
+            at, slot, first = 0, int(mine[0, 6]), int(mine[0, 0] * S + mine[0, 4])
+            assert first == starts[i] and first % 16 == 0
+            for dev, _, off, size, local, _, fslot in mine:
+                assert off == at and dev * S + local == first + at  # no gap in the codes
+                assert off % (128 * c) == 0 and fslot == slot + off // (128 * c) * -(-c // 128)  # nor in the scales
+                at += int(size)
+            assert at == r * c
+    assert spanning

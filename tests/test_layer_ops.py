@@ -851,3 +851,49 @@ def test_linear_exact(cuda, n, rows, cols):
     bq.linear_fp8(x, xs, torch.as_tensor(codes).to(cuda), torch.as_tensor(tiles).to(cuda), out, ws)
     bq.linear_check(ws)
     assert torch.equal(out, ref.float().bfloat16())
+
+
+# ----------------------------------------------------------------------------- parameters gathered from several devices
+
+
+def test_weights_gathered_from_several_devices(cuda):
+    """The staging buffers of a layout over several devices, all of whose shards are held here
+    (what an AllGather leaves): a weight cut by device boundaries is read from its start and
+    its first scale slot."""
+    import torch
+
+    shapes = [(300, 272), (1, 777), (900, 528), (129, 2064)]
+    descs = [(r, c, int(np.lcm(128 * c, 256)) if r > 1 else 256, bq.ADAM_FLAT256, int(r > 1)) for r, c in shapes]
+    layout = bq.plan(descs, 4)
+    t = layout.export()
+    S, n, ni, nf = int(t[3]), int(t[4]), int(t[5]), int(t[7])
+    places = t[8 + 7 * n:8 + 7 * n + 7 * ni].reshape(ni, 7)
+    tables = torch.empty(layout.upload_bytes(0, 4), dtype=torch.uint8, device=cuda)
+    shard = layout.upload(0, 4, tables)
+    rng = np.random.default_rng(4)
+    master = torch.as_tensor(rng.standard_normal(4 * S).astype(np.float32)).to(cuda)
+    codes, scales = torch.zeros(4 * S, dtype=torch.uint8, device=cuda), torch.zeros(nf, device=cuda)
+    bq.quant_fp8(shard, master, codes, scales)
+    spanning = 0
+    for i, (r, c) in enumerate(shapes):
+        if r == 1:
+            continue
+        mine = places[places[:, 1] == i]
+        spanning += len(mine) > 1
+        at, slot = int(mine[0, 0] * S + mine[0, 4]), int(mine[0, 6])
+        w, ws_ = codes[at:at + r * c].view(r, c), scales[slot:slot + -(-r // 128) * -(-c // 128)]
+        wv, m = L.decode_tiles(w.cpu().numpy(), ws_.cpu().numpy()), f64(master[at:at + r * c].view(r, c))
+        s = L.spread_tiles(ws_.cpu().numpy(), r, c)
+        assert np.all(np.abs(wv - m) <= 2.0 ** -4 * np.abs(wv) * 1.001 + 2.0 ** -10 * s * 1.001)
+        x, xs, xv = fp8_rows(rng, 40, c, cuda)
+        out, ws = torch.empty(40, r, dtype=torch.bfloat16, device=cuda), workspace(40, r, c, cuda)
+        bq.linear_fp8(x, xs, w, ws_, out, ws)
+        bq.linear_check(ws)
+        ref = xv @ wv.T
+        assert np.all(np.abs(f64(out) - ref) <= U * 1.001 * np.abs(ref) + sum_tol(xv, wv.T, c))
+        ids = torch.as_tensor(rng.integers(0, r, 50)).to(cuda)
+        rows = torch.empty(50, c, dtype=torch.bfloat16, device=cuda)
+        bq.embed(w, ids, rows, table_scale=ws_)
+        want = wv[ids.cpu().numpy()]
+        assert np.all(np.abs(f64(rows) - want) <= U * 1.001 * np.abs(want))
+    assert spanning
