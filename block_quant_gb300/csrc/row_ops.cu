@@ -1370,8 +1370,11 @@ bool vec_ok(const void* p, int64_t ld, int values) { return aligned16(p) && ld %
 
 // The norm's warps a row and spans a warp (VPT), within row_threads(VPT) threads for rows
 // of up to 65536 columns.  Four spans a warp: what a warp does once a row is a third of
-// its instructions with two (4096 columns: 43.5 us with two, 41.3 with four); fewer where
-// four would leave a fifth or more of the lanes idle.  One shape for any number of rows,
+// its instructions with two (4096 columns: 43.5 us with two, 41.3 with four); also for 3 and
+// 9 spans, although a quarter of the lanes idle (8192 rows and 700 rows: 8.6 and 3.9 us with
+// four, 10.5 and 3.2 with two; 22.5 and 4.4, 23.9 and 4.6).  Two for 2, 5 and 6 spans, where
+// few rows gain more than many lose (with two 8.7 and 2.8, 15.9 and 3.0, 17.7 and 3.1; with
+// four 8.3 and 3.0, 15.6 and 3.8, 16.8 and 3.9).  One shape for any number of rows,
 // so that a row's sum does not depend on the rows beside it.
 // Rows that are not aligned are bound by their 2-byte accesses and want the warps (4095
 // columns: 69 us with two spans, 94 us with four).
