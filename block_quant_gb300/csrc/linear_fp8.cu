@@ -895,6 +895,35 @@ __global__ void __launch_bounds__(256) k_copy_scales(const float* __restrict__ x
   if (i < n) out[int64_t(blockIdx.y) * ldo + i] = x[int64_t(blockIdx.y) * ldx + i];
 }
 
+// k_linear's stages and dynamic shared memory for a_rows rows of X a stage.  The X stages come
+// last, and a product reads 128 rows of the last one whatever it holds: what follows it is
+// spare shared memory.
+struct SmallPlan {
+  int stages, smem;
+};
+constexpr SmallPlan small_plan(int a_rows) {
+  const int stage = B_STAGE + a_rows * BK, spare = (BM - a_rows) * BK, part = BM * kPartPitch * 4;
+  const int fit = (kSmem - 1024 - spare) / stage, stages = fit < kMaxStages ? fit : kMaxStages;
+  const int bytes = stages * stage + spare;
+  return {stages, 1024 + (part > bytes ? part : bytes)};
+}
+
+// The CTAs of a cluster wait for one another while they hold tensor memory, so a CTA must never
+// wait for columns that a CTA of another cluster kernel holds on its SM (each cluster could
+// hold what the other needs on another SM).  Shared memory sees to that: an SM holds two
+// CTAs of k_linear (their columns fit) or one of a pair's, never both, and never one
+// of either beside a pair of the Newton-Schulz products (which asserts the same).
+constexpr bool small_ctas_are(int per_sm, int beside) {
+  for (int rows = 8; rows <= BM; rows += 8)
+    if (small_plan(rows).smem < kClusterSmemLeast || (per_sm + 1) * small_plan(rows).smem <= kSmemOfSm ||
+        small_plan(rows).smem + beside <= kSmemOfSm)
+      return false;
+  return true;
+}
+static_assert(2 * kTmemCols <= 512 && small_ctas_are(2, PAIR_SMEM) && small_ctas_are(2, DW_SMEM), "k_linear's CTAs");
+static_assert(2 * PAIR_SMEM > kSmemOfSm && 2 * DW_SMEM > kSmemOfSm && PAIR_SMEM + DW_SMEM > kSmemOfSm, "the pairs' CTAs");
+static_assert(PAIR_SMEM >= kClusterSmemLeast && DW_SMEM >= kClusterSmemLeast, "beside the Newton-Schulz pairs");
+
 // slots[k]: clusters of k CTAs that fit the device at once with an SM for each CTA
 // (k_linear_pair's shared memory sees to that), k = 1 .. 8: 152 SMs hold 76 of two, 46 of
 // three, 36 of four, 15 of eight.  Found once per device; the SMs' share where the occupancy
@@ -1014,17 +1043,13 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
                                  : reinterpret_cast<const void*>(k_linear_pair<false>);
     return launch_clusters(k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
-  // two CTAs share an SM.  The X stages come last, and a product reads 128 rows of
-  // the last one whatever it holds: what follows it is spare shared memory
   g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
-  const int stage = B_STAGE + g.a_rows * BK, spare = (BM - g.a_rows) * BK;
-  const int part = BM * kPartPitch * 4;
-  g.stages = std::min(kMaxStages, (kSmem - 1024 - spare) / stage);
+  const SmallPlan plan = small_plan(g.a_rows);
+  g.stages = plan.stages;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
-  const int smem = 1024 + std::max(part, g.stages * stage + spare);
   void* args[] = {&tx, &tw, &g};
   const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear<true>) : reinterpret_cast<const void*>(k_linear<false>);
-  return launch_clusters(k, int(tiles), g.split, THREADS, smem, args, s);
+  return launch_clusters(k, int(tiles), g.split, THREADS, plan.smem, args, s);
 }
 
 size_t dw_part_bytes(int splits, int64_t rows, int64_t cols) {

@@ -326,6 +326,8 @@ constexpr int PM = 256, STAGES2 = 6;
 constexpr int HALF_STAGE = 128 * BK * 2;       // 128 rows (or columns) x 64 bf16: 16 KB
 constexpr int STAGE2_BYTES = 2 * HALF_STAGE;   // one CTA's part of a k-block
 constexpr int GEMM2_SMEM = STAGES2 * STAGE2_BYTES + 1024 /*align*/ + 256 /*barriers*/;
+static_assert(2 * GEMM2_SMEM > kSmemOfSm && GEMM2_SMEM + kClusterSmemLeast > kSmemOfSm,
+              "no other cluster that holds tensor memory on a pair's SMs");
 
 // D = alpha * (A B) + beta * C with B given as [K x N] N-contiguous (tmB: a 3-D
 // map of 64-column chunks, two chunks a copy) and A K-major (tmA: boxes of 64

@@ -11,6 +11,11 @@ namespace bq {
 
 constexpr long long kWaitCycles = 1ll << 32;  // ~2 s at 2 GHz
 
+// An SM's shared memory, and the least that a CTA of a kernel asks for whose clusters hold tensor
+// memory (k_linear, the CTA pairs): what keeps CTAs off one SM whose columns do not
+// fit beside one another, so that no two clusters can wait for each other's columns.
+constexpr int kSmemOfSm = 228 * 1024, kClusterSmemLeast = 87 * 1024;
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
