@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 // What bounds it: from one product's start to the next on the same accumulator pass about
 // 1400 cycles (512 of products, 370 until the epilogue sees them done, 400 to read them and
 // add half, 100 until the last arrival starts the next), so a k-block takes 700; and power,
-// which holds the clock near 1.7 GHz.  347 us are 2.77 PFLOP/s.
+// which holds the clock near 1.7 GHz.  347 us are 2.77 PFLOP/s, in a run of seconds 390 us.
 // Without the epilogue's reading and adding the same products and copies take 258 us, at
 // 1.5 GHz (twice the rate of a library's bf16 product: 252).
 constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
@@ -1024,8 +1024,8 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
   // 5952 take 28 us there and 17 us on k_linear), where their tiles take less time: 0.40 us a k-block
   // and 2.5 us a wave.  337 rows of 11840 x 4512 (two waves, or one of k_linear's): 38.3 us on
-  // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 62.8 and 96.1; 512 of 8192 x
-  // 4096 (one and one): 18.4 and 24.2.
+  // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 64.2 and 96.1; 512 of 8192 x
+  // 4096 (one and one): 18.5 and 24.2.
   const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
   if (a.n > BM && us_pair < us_one) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;

@@ -445,7 +445,7 @@ int bq_embed_grad(const void* dy, int64_t ld_dy, const void* ids, int id_bits, i
 
 /* bq_rmsnorm - residual addition, root-mean-square norm, 8-bit output.  Per row:
  *   h = bf16(x + residual)  (residual NULL: h = x and nothing is written to h);
- *   rstd = 1 / sqrt(mean(h^2) + eps);  y = (h * rstd) * weight  in fp32;
+ *   rstd = 1 / sqrt(mean(h^2) + eps)  in fp32 (a sum of squares past 3e38 overflows);  y = (h * rstd) * weight  in fp32;
  *   y_out = bf16(y) if not NULL;  codes, code_scale of y if not NULL: per 128
  *   values a = max |y|, s = a / 448, code = e4m3(y * (448 / a)), as bq_step_adam8.
  * rstd (fp32, n) may be NULL.  x, residual, weight, h, y: bf16.  h may be x or
