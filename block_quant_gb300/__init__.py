@@ -33,6 +33,8 @@ SYMBOLS = [
     "bq_embed", "bq_embed_grad_workspace", "bq_embed_grad", "bq_rmsnorm", "bq_rmsnorm_grad_workspace",
     "bq_rmsnorm_grad", "bq_quant_rows_fp8", "bq_linear_fp8_workspace", "bq_linear_fp8", "bq_linear_fp8_dx",
     "bq_linear_fp8_dw", "bq_linear_check", "bq_call",
+    "bq_loss_fp8_workspace", "bq_loss_fp8_grad_workspace", "bq_cross_entropy_fp8", "bq_cross_entropy_fp8_grad",
+    "bq_distill_fp8", "bq_distill_fp8_grad",
 ]
 
 
@@ -136,6 +138,13 @@ def load():
     lib.bq_linear_fp8_dx.argtypes = [P, L, P, L, P, L, L, L, P, L, P, S, P]
     lib.bq_linear_fp8_dw.argtypes = [P, L, P, L, P, L, L, L, L, P, L, I, P, S, P]
     lib.bq_linear_check.argtypes = [P, S, P]
+    lib.bq_loss_fp8_workspace.argtypes = [L, L, L, C.POINTER(S)]
+    lib.bq_loss_fp8_grad_workspace.argtypes = [L, L, L, C.POINTER(S)]
+    head = [P, L, P, L, P, L, P, L, L, L]
+    lib.bq_cross_entropy_fp8.argtypes = head + [P, I, F, P, P, P, S, P]
+    lib.bq_cross_entropy_fp8_grad.argtypes = head + [P, I, F, P, P, P, P, L, P, L, I, P, S, P]
+    lib.bq_distill_fp8.argtypes = head + [P, I, L, P, I, L, L, F, P, P, P, L, P, S, P]
+    lib.bq_distill_fp8_grad.argtypes = head + [P, I, L, P, I, L, L, F, P, P, L, P, P, L, P, L, I, P, S, P]
     lib.bq_call.argtypes = [I, C.c_char_p]
     for name in SYMBOLS:
         if name not in ("bq_strerror", "bq_last_error", "bq_layout_free", "bq_shard_free"):
@@ -524,7 +533,53 @@ def linear_fp8_dw(dy, codes, code_scale, dw, ws, accumulate=False, stream=None):
     _run("linear_fp8_dw", dy, codes, code_scale, dw, ws, accumulate, _stream(stream))
 
 
+def loss_fp8_workspace(n, rows, cols):
+    """Bytes for cross_entropy_fp8 and distill_fp8 of n tokens and a vocabulary of rows words of
+    width cols; zero the first 256 once before the first use."""
+    b = C.c_size_t()
+    _check(load().bq_loss_fp8_workspace(int(n), int(rows), int(cols), C.byref(b)))
+    return b.value
+
+
+def loss_fp8_grad_workspace(n, rows, cols):
+    """Bytes for cross_entropy_fp8_grad and distill_fp8_grad, as loss_fp8_workspace."""
+    b = C.c_size_t()
+    _check(load().bq_loss_fp8_grad_workspace(int(n), int(rows), int(cols), C.byref(b)))
+    return b.value
+
+
+def cross_entropy_fp8(codes, code_scale, w, w_scale, targets, loss, lse, ws, scale=1.0, stream=None):
+    """loss[t] = lse[t] - z[t, targets[t]] with z = scale * X W^T, which is never kept, and
+    lse = log sum exp z; X the FP8 rows, W the FP8 weight of the head.  A target outside the
+    vocabulary, as padding has, gives 0."""
+    _run("cross_entropy_fp8", codes, code_scale, w, w_scale, targets, loss, lse, ws, scale, _stream(stream))
+
+
+def cross_entropy_fp8_grad(codes, code_scale, w, w_scale, targets, loss, lse, dloss, dx, dw, ws, scale=1.0,
+                           accumulate=False, stream=None):
+    """dx and dw (bf16, either may be None; accumulate: added to dw) from dloss, the gradient of
+    loss, and what the forward call has written."""
+    _run("cross_entropy_fp8_grad", codes, code_scale, w, w_scale, targets, loss, lse, dloss, dx, dw, ws, scale,
+         accumulate, _stream(stream))
+
+
+def distill_fp8(codes, code_scale, w, w_scale, ids, teacher, loss, lse, logp, ws, scale=1.0, stream=None):
+    """The divergence from a teacher of which ids [n, k] and teacher [n, k] (bf16 or fp32) give each
+    token's top logits: loss[t] = sum_i q_i (log q_i - logp[t, i]), q = softmax(scale * teacher),
+    logp[t, i] = z[t, ids[t, i]] - lse[t] with z = scale * X W^T.  Pairs with an id outside the vocabulary
+    or a logit of -inf do not count (their logp is 0)."""
+    _run("distill_fp8", codes, code_scale, w, w_scale, ids, teacher, loss, lse, logp, ws, scale, _stream(stream))
+
+
+def distill_fp8_grad(codes, code_scale, w, w_scale, ids, teacher, lse, logp, dloss, dx, dw, ws, scale=1.0,
+                     accumulate=False, stream=None):
+    """dx and dw (bf16, either may be None; accumulate: added to dw) from dloss, the gradient of
+    loss, and what the forward call has written."""
+    _run("distill_fp8_grad", codes, code_scale, w, w_scale, ids, teacher, lse, logp, dloss, dx, dw, ws, scale,
+         accumulate, _stream(stream))
+
+
 def linear_check(ws, stream=None):
-    """Synchronise the stream and raise if a device wait of a projection on this
+    """Synchronise the stream and raise if a device wait of a projection or a loss on this
     workspace timed out since the last check."""
     _check(load().bq_linear_check(*_read("workspace", ws), _stream(stream)))

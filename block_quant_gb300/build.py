@@ -35,9 +35,10 @@ SOURCES = {
     "ops_api.cpp": [],
     "row_ops.cu": ["-lineinfo"],
     "linear_fp8.cu": ["-lineinfo"],
+    "loss_fp8.cu": ["-lineinfo"],
 }
 BINDING = "binding.c"  # CPython module: argument marshalling of the layer operators
-HEADERS = ["bq_internal.h", "fp8_codes.h", "once.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
+HEADERS = ["bq_internal.h", "fp8_codes.h", "loss_tile.h", "once.h", "pair_tiles.h", "pdl.h", "row_ops.h", "tmem_ptx.h", "umma_ptx.h"]
 
 
 def nvcc():

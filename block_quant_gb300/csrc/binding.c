@@ -67,18 +67,8 @@ static int ints(PyObject* t, int n, int64_t* v, const char* name) {
   return ok && !PyErr_Occurred() ? 0 : -1;
 }
 
-/* rows, cols: -1 for any */
-static int mat(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
-  if (x == Py_None) {
-    PyErr_Format(PyExc_ValueError, "%s is None", name);
-    return -1;
-  }
-  m->kind = kind_of(x, name);
-  if (m->kind < 0) return -1;
-  if (m->kind > 2 || !(kinds >> m->kind & 1)) {
-    PyErr_Format(PyExc_ValueError, "%s has a type that is not taken", name);
-    return -1;
-  }
+/* rows, columns and pitch of a 2-D tensor with contiguous rows; rows, cols: -1 for any */
+static int shape_of(PyObject* x, const char* name, int64_t rows, int64_t cols, Mat* m) {
   int64_t s[2], st[2];
   if (ints(PyObject_GetAttr(x, s_shape), 2, s, name) || ints(PyObject_CallMethodNoArgs(x, s_stride), 2, st, name)) return -1;
   if ((rows >= 0 && s[0] != rows) || (cols >= 0 && s[1] != cols)) {
@@ -91,7 +81,22 @@ static int mat(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t r
     return -1;
   }
   m->ld = st[0], m->rows = s[0], m->cols = s[1];
-  return pointer_of(dev, x, name, &m->p);
+  return 0;
+}
+
+/* rows, cols: -1 for any */
+static int mat(int64_t* dev, PyObject* x, const char* name, int kinds, int64_t rows, int64_t cols, Mat* m) {
+  if (x == Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s is None", name);
+    return -1;
+  }
+  m->kind = kind_of(x, name);
+  if (m->kind < 0) return -1;
+  if (m->kind > 2 || !(kinds >> m->kind & 1)) {
+    PyErr_Format(PyExc_ValueError, "%s has a type that is not taken", name);
+    return -1;
+  }
+  return shape_of(x, name, rows, cols, m) ? -1 : pointer_of(dev, x, name, &m->p);
 }
 
 /* a matrix that may be None: zeros */
@@ -107,6 +112,23 @@ static int contiguous(PyObject* x, const char* name) {
   Py_DECREF(v);
   if (!ok) PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
   return ok ? 0 : -1;
+}
+
+/* a matrix of ids (int32 or int64): m->kind their bits */
+static int id_mat(int64_t* dev, PyObject* x, const char* name, int64_t rows, int64_t cols, Mat* m) {
+  if (x == Py_None) {
+    PyErr_Format(PyExc_ValueError, "%s is None", name);
+    return -1;
+  }
+  const int64_t k = kind_of(x, name);
+  if (k < 0) return -1;
+  if (k != 32 && k != 64) {
+    PyErr_Format(PyExc_ValueError, "%s has a type that is not taken", name);
+    return -1;
+  }
+  if (shape_of(x, name, rows, cols, m)) return -1;
+  m->kind = k;
+  return pointer_of(dev, x, name, &m->p);
 }
 
 /* n: -1 for any; returns the length in *got */
@@ -314,6 +336,77 @@ static PyObject* f_linear_dw(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   RUN(7, y.p, y.ld, c.p, c.ld, s.p, s.ld, c.rows, y.cols, c.cols, d.p, d.ld, acc, ws, wb, st);
 }
 
+/* the rows and the weight of a loss: a[0 .. 3] codes code_scale w w_scale */
+static int loss_head(int64_t* dev, PyObject* const* a, Mat* c, Mat* s, Mat* w, int64_t* ts) {
+  return mat(dev, a[2], "w", FP8, -1, -1, w) || code_rows(dev, a[0], a[1], -1, w->cols, c, s) ||
+         tiles(dev, a[3], "w_scale", w->rows, w->cols, ts);
+}
+
+static PyObject* f_cross_entropy(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  /* codes code_scale w w_scale targets loss lse ws scale stream */
+  int64_t dev = -1;
+  Mat c, s, w;
+  int64_t ts, y, bits, loss, lse, ws, wb, st;
+  if (!args_are(n, 10) || loss_head(&dev, a, &c, &s, &w, &ts) || vec(&dev, a[4], "targets", 0, c.rows, &y, &bits, NULL) ||
+      vec(&dev, a[5], "loss", FP32, c.rows, &loss, NULL, NULL) || vec(&dev, a[6], "lse", FP32, c.rows, &lse, NULL, NULL) ||
+      workspace(&dev, a[7], &ws, &wb) || integer(a[9], &st))
+    return NULL;
+  const double f = PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred()) return NULL;
+  RUN(8, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, y, bits, word(f), loss, lse, ws, wb, st);
+}
+
+static PyObject* f_cross_entropy_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  /* codes code_scale w w_scale targets loss lse dloss dx dw ws scale accumulate stream */
+  int64_t dev = -1;
+  Mat c, s, w, dx, dw;
+  int64_t ts, y, bits, loss, lse, dl, ws, wb, st;
+  if (!args_are(n, 14) || loss_head(&dev, a, &c, &s, &w, &ts) || vec(&dev, a[4], "targets", 0, c.rows, &y, &bits, NULL) ||
+      vec(&dev, a[5], "loss", FP32, c.rows, &loss, NULL, NULL) || vec(&dev, a[6], "lse", FP32, c.rows, &lse, NULL, NULL) ||
+      vec(&dev, a[7], "dloss", FP32, c.rows, &dl, NULL, NULL) || opt(&dev, a[8], "dx", BF16, c.rows, w.cols, &dx) ||
+      opt(&dev, a[9], "dw", BF16, w.rows, w.cols, &dw) || workspace(&dev, a[10], &ws, &wb) || integer(a[13], &st))
+    return NULL;
+  const double f = PyFloat_AsDouble(a[11]);
+  const int acc = PyObject_IsTrue(a[12]);
+  if (PyErr_Occurred()) return NULL;
+  RUN(9, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, y, bits, word(f), loss, lse, dl, dx.p, dx.ld, dw.p,
+      dw.ld, acc, ws, wb, st);
+}
+
+static PyObject* f_distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  /* codes code_scale w w_scale ids teacher loss lse logp ws scale stream */
+  int64_t dev = -1;
+  Mat c, s, w, y, z, p;
+  int64_t ts, loss, lse, ws, wb, st;
+  if (!args_are(n, 12) || loss_head(&dev, a, &c, &s, &w, &ts) || id_mat(&dev, a[4], "ids", c.rows, -1, &y) ||
+      mat(&dev, a[5], "teacher", BF16 | FP32, c.rows, y.cols, &z) || vec(&dev, a[6], "loss", FP32, c.rows, &loss, NULL, NULL) ||
+      vec(&dev, a[7], "lse", FP32, c.rows, &lse, NULL, NULL) || mat(&dev, a[8], "logp", FP32, c.rows, y.cols, &p) ||
+      workspace(&dev, a[9], &ws, &wb) || integer(a[11], &st))
+    return NULL;
+  const double f = PyFloat_AsDouble(a[10]);
+  if (PyErr_Occurred()) return NULL;
+  RUN(10, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, y.p, y.kind, y.ld, z.p, z.kind, z.ld, y.cols, word(f),
+      loss, lse, p.p, p.ld, ws, wb, st);
+}
+
+static PyObject* f_distill_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  /* codes code_scale w w_scale ids teacher lse logp dloss dx dw ws scale accumulate stream */
+  int64_t dev = -1;
+  Mat c, s, w, y, z, p, dx, dw;
+  int64_t ts, lse, dl, ws, wb, st;
+  if (!args_are(n, 15) || loss_head(&dev, a, &c, &s, &w, &ts) || id_mat(&dev, a[4], "ids", c.rows, -1, &y) ||
+      mat(&dev, a[5], "teacher", BF16 | FP32, c.rows, y.cols, &z) || vec(&dev, a[6], "lse", FP32, c.rows, &lse, NULL, NULL) ||
+      mat(&dev, a[7], "logp", FP32, c.rows, y.cols, &p) || vec(&dev, a[8], "dloss", FP32, c.rows, &dl, NULL, NULL) ||
+      opt(&dev, a[9], "dx", BF16, c.rows, w.cols, &dx) || opt(&dev, a[10], "dw", BF16, w.rows, w.cols, &dw) ||
+      workspace(&dev, a[11], &ws, &wb) || integer(a[14], &st))
+    return NULL;
+  const double f = PyFloat_AsDouble(a[12]);
+  const int acc = PyObject_IsTrue(a[13]);
+  if (PyErr_Occurred()) return NULL;
+  RUN(11, c.p, c.ld, s.p, s.ld, w.p, w.ld, ts, c.rows, w.rows, w.cols, y.p, y.kind, y.ld, z.p, z.kind, z.ld, y.cols, word(f),
+      lse, p.p, p.ld, dl, dx.p, dx.ld, dw.p, dw.ld, acc, ws, wb, st);
+}
+
 /* the workspace of a check: (address, bytes) */
 static PyObject* f_workspace(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   int64_t dev = -1, p, bytes;
@@ -351,6 +444,10 @@ static PyMethodDef methods[] = {
     FN("linear_fp8", f_linear),
     FN("linear_fp8_dx", f_linear_dx),
     FN("linear_fp8_dw", f_linear_dw),
+    FN("cross_entropy_fp8", f_cross_entropy),
+    FN("cross_entropy_fp8_grad", f_cross_entropy_grad),
+    FN("distill_fp8", f_distill),
+    FN("distill_fp8_grad", f_distill_grad),
     FN("workspace", f_workspace),
     {NULL, NULL, 0, NULL},
 };

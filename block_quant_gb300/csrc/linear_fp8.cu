@@ -18,7 +18,9 @@
 #include <string>
 
 #include "bq_internal.h"
+#include "loss_tile.h"
 #include "once.h"
+#include "pair_tiles.h"
 #include "pdl.h"
 #include "row_ops.h"
 #include "tmem_ptx.h"
@@ -33,7 +35,6 @@ int check(const char* what) {
   return BQ_OK;
 }
 
-constexpr int BK = 128;  // a k-block: one scale group, 128 bytes of codes
 constexpr int BM = 128, BN = 128;
 constexpr int EPI_WARPS = 8;                   // two per tensor-memory lane quarter, each half of a tile's columns
 constexpr int THREADS = 64 + 32 * EPI_WARPS;   // warp 0 TMA, warp 1 MMA + TMEM, then the epilogue
@@ -61,18 +62,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// acc += f * r
-template <int N>
-__device__ __forceinline__ void add_scaled(float* acc, const uint32_t* r, float f) {
-#pragma unroll
-  for (int j = 0; j < N; j += 2) {
-    const float2 o = __ffma2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), make_float2(f, f),
-                                make_float2(acc[j], acc[j + 1]));
-    acc[j] = o.x;
-    acc[j + 1] = o.y;
-  }
-}
-
 struct LinArgs {
   const float *xs, *ws;  // scales of X [groups][ld_xs] and of W's tiles
   __nv_bfloat16* out;
@@ -84,6 +73,12 @@ struct LinArgs {
   int a_rows;            // rows of X that a stage holds (a multiple of 8, <= 128)
   int bytes;             // of a store into out (store_bytes)
   int* status;
+  // a tile's end other than rows of out (loss_tile.h)
+  float2* stats;
+  uint8_t* at;
+  const float* lse;
+  int64_t ld_stats;
+  float zscale;
 };
 
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
@@ -92,7 +87,7 @@ struct LinArgs {
 // 1 row of 8192 x 8192 takes 14.2 us (4.7 TB/s; its bytes alone are 9.9), 333 rows of 2880 x
 // 4096 take 11.7 (0.6 us of set-up, 0.9 to the first product, 16 k-blocks at 0.35 to 0.44, 3 for
 // the join and the stores).
-template <bool TRANS>
+template <bool TRANS, int END = kTileOut>
 __global__ void __launch_bounds__(THREADS, 2)
     k_linear(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const LinArgs g) {
   extern __shared__ unsigned char smem_raw[];
@@ -272,6 +267,19 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int j = 0; j < BN / 32; ++j) v[j] += x[c][j];
       }
     }
+    if constexpr (END == kTileStats) {
+      row_stats(v, cols, g.zscale, lane, g.stats + int64_t(n0 >> 7) * g.ld_stats + m0 + r,
+                g.at + int64_t(n0 >> 7) * g.ld_stats + m0 + r);
+      continue;
+    }
+    if constexpr (END == kTileProbs) {
+      const float lse = __ldg(g.lse + m0 + r);
+      __half* u = reinterpret_cast<__half*>(g.out) + int64_t(m0 + r) * g.ldo + n0;
+#pragma unroll
+      for (int j = 0; j < BN / 32; ++j)
+        if (lane + 32 * j < cols) u[lane + 32 * j] = __float2half_rn(scaled_prob(v[j] * g.zscale, lse));
+      continue;
+    }
     __nv_bfloat16* o = g.out + int64_t(m0 + r) * g.ldo + n0;
 #pragma unroll
     for (int j = 0; j < BN / 32; ++j)
@@ -305,18 +313,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 // which holds the clock near 1.7 GHz.  347 us are 2.77 PFLOP/s, in a run of seconds 390 us.
 // Without the epilogue's reading and adding the same products and copies take 258 us, at
 // 1.5 GHz (twice the rate of a library's bf16 product: 252).
-constexpr int PM = 256, PN = 256, PSTAGES = 5, kBand = 8;
-constexpr int HALF_STAGE = 128 * BK;            // 16 KB
-constexpr int PSTAGE_BYTES = 2 * HALF_STAGE;
-// Sixteen epilogue warps, four per tensor-memory lane quarter: part p of a quarter
-// reads columns 64p .. 64p + 63 of every accumulator.  Five warpgroups with TMA (warp
-// 0) and MMA (warp 1); of the launch's 640 x 96 registers the first group keeps 32 a
-// thread and the epilogue takes 112.
-constexpr int PEPI = 16, PCOLS = PN / 4;
-constexpr int PAIR_THREADS = 128 + 32 * PEPI;
-constexpr int kRegsLaunch = 96, kRegsIssue = 32, kRegsEpilogue = 112;
-static_assert(128 * kRegsIssue + 32 * PEPI * kRegsEpilogue <= PAIR_THREADS * kRegsLaunch, "register split");
-constexpr int OUT_BOX = 32 * 64;                // 32 rows x 32 bf16 of out, one a warp
+constexpr int PSTAGES = 5;
 // X's scales of a k-block (128 rows of this CTA) come through a ring of their own, up to
 // SLOTS k-blocks ahead: loads by the epilogue warps themselves would queue behind the
 // stages' copies.  Warp 2 copies them with cp.async, four scales a lane, and each CTA has its
@@ -330,17 +327,6 @@ constexpr int OUT_BOX = 32 * 64;                // 32 rows x 32 bf16 of out, one
 constexpr int SLOTS = 8, SLOT_BYTES = 128 * 4;
 constexpr int OFF_OUT = PSTAGES * PSTAGE_BYTES, OFF_SCALES = OFF_OUT + PEPI * OUT_BOX;
 constexpr int PAIR_SMEM = 1024 + OFF_SCALES + SLOTS * SLOT_BYTES;
-constexpr int kPairTmem = 2 * PN;
-
-// `bytes` (0 to 16, the rest zeros) to 16-byte aligned shared memory
-__device__ __forceinline__ void copy16_clipped(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// arrives on the barrier (whose count includes it) when this thread's copies so far have landed
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
@@ -352,111 +338,7 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
-// A warp's box of out, 32 rows x COLS bf16 (32 or 64) in shared memory, swizzled as its store
-// reads it: 16-byte word c of row r at word c ^ ((r >> 1) & 3), or c ^ (r & 7)
-template <int COLS>
-__device__ __forceinline__ uint32_t box_word(uint32_t box, int r, int c) {
-  return box + 2u * COLS * uint32_t(r) + 16u * uint32_t(COLS == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7));
-}
-
-// v: the lane's row
-template <int COLS>
-__device__ __forceinline__ void put_box(const float* v, uint32_t box, int lane) {
-#pragma unroll
-  for (int c = 0; c < COLS / 8; ++c) {
-    uint32_t o[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[8 * c + 2 * e], v[8 * c + 2 * e + 1]);
-      o[e] = *reinterpret_cast<const uint32_t*>(&p);
-    }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_word<COLS>(box, lane, c)), "r"(o[0]), "r"(o[1]),
-                 "r"(o[2]), "r"(o[3])
-                 : "memory");
-  }
-}
-
-// the box by plain stores of `bytes` (8, 4 or 2, as out's rows are aligned), a row's pieces
-// beside one another in the warp, eight loads before their stores
-template <int COLS, int BYTES>
-__device__ __forceinline__ void store_pieces(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int row0, int c0,
-                                             uint32_t box, int lane) {
-  constexpr int N = BYTES / 2, LANES = COLS / N < 32 ? COLS / N : 32, EACH = 32 / LANES;  // lanes a row, rows at once
-#pragma unroll
-  for (int k = 0; k < COLS; k += LANES * N) {
-    const int c = k + lane % LANES * N, left = cols - c0 - c;
-#pragma unroll 1
-    for (int r0 = lane / LANES; r0 < 32; r0 += 8 * EACH) {
-      uint32_t v[8][BYTES == 8 ? 2 : 1];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (r0 + e * EACH >= 32) continue;
-        const uint32_t at = box_word<COLS>(box, r0 + e * EACH, c >> 3) + 2u * uint32_t(c & 7);
-        if constexpr (BYTES == 8)
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[e][0]), "=r"(v[e][1]) : "r"(at) : "memory");
-        else if constexpr (BYTES == 4)
-          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[e][0]) : "r"(at) : "memory");
-        else
-          asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v[e][0]) : "r"(at) : "memory");
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = r0 + e * EACH;
-        if (r >= 32 || row0 + r >= rows || left <= 0) continue;
-        __nv_bfloat16* o = out + int64_t(row0 + r) * ldo + c0 + c;
-        if (left >= N) {
-          if constexpr (BYTES == 8)
-            *reinterpret_cast<uint2*>(o) = make_uint2(v[e][0], v[e][1]);
-          else if constexpr (BYTES == 4)
-            *reinterpret_cast<uint32_t*>(o) = v[e][0];
-          else
-            *reinterpret_cast<uint16_t*>(o) = uint16_t(v[e][0]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (j < left) reinterpret_cast<uint16_t*>(o)[j] = uint16_t(v[e][j >> 1] >> (16 * (j & 1)));
-        }
-      }
-    }
-  }
-}
-
-// the box to out's row0.., c0.., clipped to rows x cols: by TMA where out's rows are 16-byte
-// aligned (`bytes`, as store_bytes has it)
-template <int COLS>
-__device__ __forceinline__ void store_box(__nv_bfloat16* out, int64_t ldo, int rows, int cols, int bytes,
-                                          const CUtensorMap* map, int row0, int c0, uint32_t box, int lane) {
-  if (bytes == 16) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0 && row0 < rows && c0 < cols) {
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                       reinterpret_cast<uint64_t>(map)),
-                   "r"(c0), "r"(row0), "r"(box)
-                   : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-  } else {
-    __syncwarp();
-    if (bytes == 8)
-      store_pieces<COLS, 8>(out, ldo, rows, cols, row0, c0, box, lane);
-    else if (bytes == 4)
-      store_pieces<COLS, 4>(out, ldo, rows, cols, row0, c0, box, lane);
-    else
-      store_pieces<COLS, 2>(out, ldo, rows, cols, row0, c0, box, lane);
-    __syncwarp();
-  }
-}
-
-// the widest store that out's rows are aligned to.  A copy by TMA clips rows at whole 16-byte
-// words only: where they end inside one it would write zeros past their end
-int store_bytes(const void* out, int64_t ldo, int cols) {
-  int bytes = cols % 8 ? 8 : 16;
-  while (bytes > 2 && (ldo * 2 % bytes || reinterpret_cast<uintptr_t>(out) % bytes)) bytes /= 2;
-  return bytes;
-}
-
-template <bool TRANS>
+template <bool TRANS, int END = kTileOut>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmO, const LinArgs g) {
@@ -638,12 +520,26 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
       }
       if (!ok) break;
+      if constexpr (END == kTileStats) {
+        if (c0 < g.width) {
+          const int64_t at = int64_t(c0 / PCOLS) * g.ld_stats + row0 + lane;
+          lane_stats<PCOLS>(acc, g.width - c0, g.zscale, row0 + lane < g.n, g.stats + at, g.at + at);
+        }
+      } else {
+        if constexpr (END == kTileProbs) {
+          const float lse = row0 + lane < g.n ? __ldg(g.lse + row0 + lane) : kNoTarget;
+          lane_probs<PCOLS>(acc, g.width - c0, g.zscale, lse);
+        }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
-        __syncwarp();
-        put_box<32>(acc + 32 * u, box, lane);
-        store_box<32>(g.out, g.ldo, g.n, g.width, g.bytes, &tmO, row0, c0 + 32 * u, box, lane);
+        for (int u = 0; u < 2; ++u) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+          __syncwarp();
+          if constexpr (END == kTileProbs)
+            put_box<32, __half>(acc + 32 * u, box, lane);
+          else
+            put_box<32>(acc + 32 * u, box, lane);
+          store_box<32>(g.out, g.ldo, g.n, g.width, g.bytes, &tmO, row0, c0 + 32 * u, box, lane);
+        }
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
@@ -666,11 +562,6 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 // seconds under the power limit; a library's bf16 product of that size reaches 1.91 and 1.7.
 // Few tokens are bound by the tiles' stores (64: 24 us for 117 MB of dW, 4.9 TB/s; with two
 // stores of 64-byte rows a warp in place of one of whole lines 33).
-constexpr int DK = 64;                          // tokens of a k-block
-constexpr int CHUNK = DK * 128;                 // 64 tokens x 64 columns of bf16: 8 KB, two an operand
-constexpr int DW_STAGES = 5, DW_BOX = 32 * 128;  // (a warp's staging of out: 32 rows x 64 bf16)
-constexpr int DW_SMEM = 1024 + DW_STAGES * PSTAGE_BYTES + PEPI * DW_BOX;
-
 struct DwKernelArgs {
   __nv_bfloat16* out;
   float* part;           // a split product's shares (k_dw_join), or NULL
@@ -680,13 +571,6 @@ struct DwKernelArgs {
   int accumulate, bytes;
   int* status;
 };
-
-// A share's values as the epilogue warps hold them: float4 j of lane l (columns 4j .. of its
-// row) at 32 j + l of warp w's 512, so that every store is whole lines (by rows, 16 bytes a
-// lane, the same stores took 4 us longer).
-__device__ __forceinline__ int64_t share_at(int t, int rank, int w) {
-  return ((int64_t(t) * 2 + rank) * PEPI + w) * 512;
-}
 
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both MN-major
 constexpr uint32_t kDwIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t(PN >> 3) << 17) |
@@ -928,6 +812,8 @@ static_assert(PAIR_SMEM >= kClusterSmemLeast && DW_SMEM >= kClusterSmemLeast, "b
 // (k_linear_pair's shared memory sees to that), k = 1 .. 8: 152 SMs hold 76 of two, 46 of
 // three, 36 of four, 15 of eight.  Found once per device; the SMs' share where the occupancy
 // query fails.
+}  // namespace
+
 const int* cluster_slots() {
   static std::mutex mu;
   static int cached[65][9] = {};
@@ -960,7 +846,8 @@ const int* cluster_slots() {
   return slots;
 }
 
-int launch_clusters(const void* kernel, int clusters, int size, int threads, int smem, void** args, cudaStream_t s) {
+int launch_clusters(const char* what, const void* kernel, int clusters, int size, int threads, int smem, void** args,
+                    cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -976,10 +863,8 @@ int launch_clusters(const void* kernel, int clusters, int size, int threads, int
   cfg.attrs = at;
   cfg.numAttrs = 2;
   cudaLaunchKernelExC(&cfg, kernel, args);
-  return check("bq_linear_fp8");
+  return check(what);
 }
-
-}  // namespace
 
 int launch_linear_fp8(const LinearArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -988,7 +873,11 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
         if (cudaFuncSetAttribute(k_linear<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear_pair<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess)
+            cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear_pair<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear_pair<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess)
           return check("bq_linear_fp8 (shared memory attribute)");
         return int(BQ_OK);
       }))
@@ -999,6 +888,10 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.ld_xs = a.ld_xs, g.ldo = a.ldo, g.n = int(a.n), g.width = width, g.red = red;
   g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
   g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
+  g.stats = nullptr, g.at = nullptr, g.lse = nullptr, g.ld_stats = 0, g.zscale = 1.f;
+  const int end = a.loss ? a.loss->end : int(kTileOut);
+  if (a.loss) g.stats = a.loss->stats, g.at = a.loss->at, g.lse = a.loss->lse, g.ld_stats = a.loss->ld_stats, g.zscale = a.loss->zscale;
+  if (end != kTileOut) g.bytes = 16;
   const int nk = (red + BK - 1) / BK;
   CUtensorMap tx, tw, to;
   if (int rc = encode_map_codes(&tw, a.w, a.cols, a.rows, a.ldw, 128)) return rc;
@@ -1036,20 +929,27 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
       if (int rc = check("bq_linear_fp8 (scales)")) return rc;
       g.xs = a.scale_ws, g.ld_xs = ld;
     }
-    if (g.bytes == 16)
-      if (int rc = encode_map_bf16_out(&to, a.out, width, a.n, a.ldo, 32)) return rc;
+    if (g.bytes == 16 && end != kTileStats)  // (probabilities: whole 16-byte words, zeros past the width)
+      if (int rc = encode_map_bf16_out(&to, a.out, end == kTileProbs ? (width + 7) / 8 * 8 : width, a.n, a.ldo, 32)) return rc;
     void* args[] = {&tx, &tw, &to, &g};
-    const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear_pair<true>)
-                                 : reinterpret_cast<const void*>(k_linear_pair<false>);
-    return launch_clusters(k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);
+    const void* k = end == kTileStats   ? reinterpret_cast<const void*>(k_linear_pair<false, kTileStats>)
+                    : end == kTileProbs ? reinterpret_cast<const void*>(k_linear_pair<false, kTileProbs>)
+                    : a.transposed      ? reinterpret_cast<const void*>(k_linear_pair<true>)
+                                        : reinterpret_cast<const void*>(k_linear_pair<false>);
+    if (a.loss) a.loss->part_cols = PCOLS;
+    return launch_clusters("bq_linear_fp8", k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
   g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
   const SmallPlan plan = small_plan(g.a_rows);
   g.stages = plan.stages;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   void* args[] = {&tx, &tw, &g};
-  const void* k = a.transposed ? reinterpret_cast<const void*>(k_linear<true>) : reinterpret_cast<const void*>(k_linear<false>);
-  return launch_clusters(k, int(tiles), g.split, THREADS, plan.smem, args, s);
+  const void* k = end == kTileStats   ? reinterpret_cast<const void*>(k_linear<false, kTileStats>)
+                  : end == kTileProbs ? reinterpret_cast<const void*>(k_linear<false, kTileProbs>)
+                  : a.transposed      ? reinterpret_cast<const void*>(k_linear<true>)
+                                      : reinterpret_cast<const void*>(k_linear<false>);
+  if (a.loss) a.loss->part_cols = BN;
+  return launch_clusters("bq_linear_fp8", k, int(tiles), g.split, THREADS, plan.smem, args, s);
 }
 
 size_t dw_part_bytes(int splits, int64_t rows, int64_t cols) {
@@ -1097,7 +997,7 @@ int launch_dw(const DwArgs& a, void* stream) {
     if (int rc = encode_map_bf16_out(&to, a.dw, a.cols, a.rows, a.ld_dw, 64)) return rc;
   const int64_t tiles = int64_t((a.rows + PM - 1) / PM) * ((a.cols + PN - 1) / PN) * g.splits;
   void* args[] = {&ty, &tx, &to, &g};
-  if (int rc = launch_clusters(reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, cluster_slots()[2])), 2,
+  if (int rc = launch_clusters("bq_linear_fp8_dw", reinterpret_cast<const void*>(k_dw_pair), int(std::min<int64_t>(tiles, cluster_slots()[2])), 2,
                                PAIR_THREADS, DW_SMEM, args, s))
     return rc;
   if (!g.part) return BQ_OK;

@@ -1,0 +1,823 @@
+// Softmax losses over an FP8 head (sm_103a): cross entropy of a class, and the divergence from
+// a teacher's top logits, with their gradients.  With z = scale * X W^T (n tokens, a vocabulary
+// of `rows`) and a row's targets q (weights of a few ids, of sum 1):
+//   loss = sum_i q_i (log q_i - log p_i),  p = softmax(z),
+//   dX = diag(g) scale U W,  dW = (diag(g) U)^T scale X,  U = p - q.
+// z is never kept.  Forward: every tile of logits leaves the product (linear_fp8.cu) as its rows'
+// statistics (loss_tile.h), which one launch joins.  Gradient: pieces of the vocabulary, one
+// after another; a piece's logits are made again and leave as U in fp16, which two
+// products read, with the piece of W for dX and with X for that piece of dW.
+//
+// fp16 and not bf16 or E4M3: U is in [-1, 1] and W and X are brought to a common power of two
+// first, so all three keep eleven bits over the top 28 powers of two, at the rate of bf16 products;
+// what the results lose is their own rounding to bf16.  (E4M3 rows of U would make dX half as
+// expensive and 2.5 % wrong.)
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "bq_internal.h"
+#include "loss_tile.h"
+#include "once.h"
+#include "pair_tiles.h"
+#include "pdl.h"
+#include "row_ops.h"
+#include "tmem_ptx.h"
+#include "umma_ptx.h"
+
+namespace bq {
+namespace {
+
+int check(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return set_error(BQ_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+  return BQ_OK;
+}
+
+constexpr int kMaxPairs = 1024;  // of a row
+
+__device__ __forceinline__ void decode16(const uint4& w, float* v) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {  // (NaN are passed over)
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+  return v;
+}
+
+// a row's targets
+struct Targets {
+  const void *ids, *teacher;
+  int64_t ld_ids, ld_teacher;
+  float scale;
+  int rows, k, id_bits, teacher_kind;
+
+  // the id of pair i of row t, -1 outside the vocabulary
+  __device__ __forceinline__ int id(int64_t t, int i) const {
+    const int64_t at = t * ld_ids + i;
+    const int64_t v = id_bits == 64 ? __ldg(static_cast<const long long*>(ids) + at) : int64_t(__ldg(static_cast<const int*>(ids) + at));
+    return v >= 0 && v < rows ? int(v) : -1;
+  }
+  // the teacher's logit, scaled
+  __device__ __forceinline__ float logit(int64_t t, int i) const {
+    const int64_t at = t * ld_teacher + i;
+    return scale * (teacher_kind == BQ_ROWS_FP32 ? __ldg(static_cast<const float*>(teacher) + at)
+                                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(teacher)[at]));
+  }
+  // a pair counts if its id is a word and the teacher gives it any weight
+  __device__ __forceinline__ int kept_id(int64_t t, int i, float* z) const {
+    const int v = id(t, i);
+    *z = 0.f;
+    if (!teacher || v < 0) return v;
+    *z = logit(t, i);
+    return *z == -INFINITY ? -1 : v;
+  }
+};
+
+// the teacher's softmax over a row's pairs, by a warp: its maximum and the log of its sum; false
+// if no pair counts
+__device__ __forceinline__ bool teacher_sum(const Targets& y, int64_t t, int lane, float* top, float* log_sum) {
+  float m = -INFINITY;
+  bool any = false;
+  for (int i = lane; i < y.k; i += 32) {
+    float z;
+    if (y.kept_id(t, i, &z) >= 0) any = true, m = fmaxf(m, z);
+  }
+  m = warp_max(m);
+  float s = 0.f;
+  for (int i = lane; i < y.k; i += 32) {
+    float z;
+    if (y.kept_id(t, i, &z) >= 0) s += expf(z - m);
+  }
+  *top = m;
+  *log_sum = logf(warp_sum(s));
+  return __any_sync(0xFFFFFFFFu, any);
+}
+
+// ---------------------------------------------------------------- forward
+
+struct PickArgs {
+  const uint8_t *x, *w;
+  const float *xs, *ws;
+  float* out;
+  int64_t ldx, ld_xs, ldw, ld_out, n;
+  int cols;
+  Targets y;
+};
+
+// The logits of the targets, a warp each, by reading their rows of W: bound by those bytes.
+__global__ void __launch_bounds__(256) k_loss_pick(const PickArgs g) {
+  after_previous();
+  next_may_start();
+  const int lane = threadIdx.x & 31;
+  const int64_t pairs = g.n * g.y.k, step = int64_t(gridDim.x) * 8;
+  const int tile_cols = (g.cols + 127) / 128;
+  for (int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); p < pairs; p += step) {
+    const int64_t t = p / g.y.k;
+    const int i = int(p - t * g.y.k), v = g.y.id(t, i);
+    float sum = 0.f;
+    if (v >= 0) {
+      const uint8_t *x = g.x + t * g.ldx, *w = g.w + int64_t(v) * g.ldw;
+      const float* ws = g.ws + int64_t(v >> 7) * tile_cols;
+      for (int c = 16 * lane; c < g.cols; c += 512) {
+        float a[16], b[16], d = 0.f;
+        decode16(__ldg(reinterpret_cast<const uint4*>(x + c)), a);
+        decode16(__ldg(reinterpret_cast<const uint4*>(w + c)), b);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) d = fmaf(a[e], b[e], d);
+        sum = fmaf(d, __ldg(g.xs + int64_t(c >> 7) * g.ld_xs + t) * __ldg(ws + (c >> 7)), sum);
+      }
+      sum = warp_sum(sum) * g.y.scale;
+    }
+    if (lane == 0) g.out[t * g.ld_out + i] = sum;
+  }
+}
+
+struct JoinArgs {
+  const float2* stats;
+  const uint8_t* at;
+  int64_t ld_stats, n, ld_logp;
+  float *loss, *lse, *logp;  // logp (or, of classes, loss) holds the targets' logits
+  int parts, part_cols, group;  // rows of a CTA: 1, 2, .. 32
+  Targets y;
+};
+
+__device__ __forceinline__ RowStats shuffled(const RowStats& a, int d) {
+  return {__shfl_xor_sync(0xFFFFFFFFu, a.m, d), __shfl_xor_sync(0xFFFFFFFFu, a.s, d), __shfl_xor_sync(0xFFFFFFFFu, a.at, d)};
+}
+
+// A row's statistics from its parts', its log-sum, and its loss.
+__global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
+  __shared__ float sm[32][33], ss[32][33];
+  __shared__ int sa[32][33];
+  after_previous();
+  next_may_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane & (g.group - 1), each = 32 / g.group;
+  const int64_t row = int64_t(blockIdx.x) * g.group + r;
+  RowStats a{-INFINITY, 0.f, 0};
+  bool some = false;
+  if (row < g.n)
+    for (int p0 = warp * each + lane / g.group; p0 < g.parts; p0 += 4 * 32 * each) {
+      float2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = p0 + e * 32 * each;
+        if (p < g.parts) v[e] = g.stats[int64_t(p) * g.ld_stats + row];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int p = p0 + e * 32 * each;
+        if (p >= g.parts) continue;
+        const RowStats b{v[e].x, v[e].y, p};
+        a = some ? joined(a, b) : b;
+        some = true;
+      }
+    }
+  // (a lane without a part holds the statistics of one logit of -inf, which add exp(-inf))
+  for (int d = g.group; d < 32; d <<= 1) a = joined(a, shuffled(a, d));
+  if (lane < g.group) sm[warp][lane] = a.m, ss[warp][lane] = a.s, sa[warp][lane] = a.at;
+  __syncthreads();
+  const int64_t t = int64_t(blockIdx.x) * g.group + warp;
+  if (warp >= g.group || t >= g.n) return;
+  a = {sm[lane][warp], ss[lane][warp], sa[lane][warp]};
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) a = joined(a, shuffled(a, d));
+  const int best = a.at * g.part_cols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
+  const float more = log1pf(a.s);
+  if (lane == 0) g.lse[t] = a.m + more;
+  if (!g.y.teacher) {
+    const int v = g.y.id(t, 0);
+    if (lane == 0) g.loss[t] = v < 0 ? 0.f : v == best ? more : more + (a.m - g.loss[t]);
+    return;
+  }
+  float top, log_sum, sum = 0.f;
+  const bool any = teacher_sum(g.y, t, lane, &top, &log_sum);
+  for (int i = lane; i < g.y.k; i += 32) {
+    float z;
+    const int v = g.y.kept_id(t, i, &z);
+    float* at = g.logp + t * g.ld_logp + i;
+    const float logp = v < 0 ? 0.f : v == best ? -more : (*at - a.m) - more;
+    *at = logp;
+    if (v < 0) continue;
+    const float log_q = (z - top) - log_sum, q = expf(log_q);
+    if (q != 0.f) sum += q * (log_q - logp);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) g.loss[t] = any ? sum : 0.f;
+}
+
+// ---------------------------------------------------------------- gradient: operands
+
+constexpr int kPrepCtas = 304;
+constexpr int kHeadroom = 5;  // values of 448 x the largest scale below 2^15
+
+// 2^e that brings 448 x `top` into [2^13, 2^15): fp16 holds what it scales
+__device__ __forceinline__ int power_for(float top) {
+  return top > 0.f ? max(-126, min(126, kHeadroom - ilogbf(top))) : 0;
+}
+
+struct PrepArgs {
+  Targets y;
+  const float *xs, *ws, *lse, *dloss;
+  float *off, *tops;  // off: a row's log-sum, or kNoTarget; tops: each CTA's largest scale of X and of W
+  int64_t ld_xs, n, w_tiles;
+  int groups;
+};
+
+__device__ __forceinline__ float finite_abs(float v) {
+  v = fabsf(v);
+  return v <= 3.402823e38f ? v : 0.f;
+}
+
+// which rows have a target, and the largest scales
+__global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
+  __shared__ float top[2][8];
+  after_previous();
+  next_may_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float mx = 0.f, mw = 0.f;
+  for (int64_t t = int64_t(blockIdx.x) * 8 + warp; t < g.n; t += int64_t(gridDim.x) * 8) {
+    bool any = false;
+    for (int i = lane; i < g.y.k; i += 32) {
+      float z;
+      any |= g.y.kept_id(t, i, &z) >= 0;
+    }
+    any = __any_sync(0xFFFFFFFFu, any);
+    if (lane == 0) g.off[t] = any ? g.lse[t] : kNoTarget;
+    if (!any) continue;
+    const float f = g.dloss[t];
+    for (int j = lane; j < g.groups; j += 32) mx = fmaxf(mx, finite_abs(g.xs[int64_t(j) * g.ld_xs + t] * f));
+  }
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < g.w_tiles; i += int64_t(gridDim.x) * 256)
+    mw = fmaxf(mw, finite_abs(g.ws[i]));
+  mx = warp_max(mx), mw = warp_max(mw);
+  if (lane == 0) top[0][warp] = mx, top[1][warp] = mw;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float m = 0.f;
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, top[threadIdx.x][i]);
+    g.tops[threadIdx.x * kPrepCtas + blockIdx.x] = m;
+  }
+}
+
+// every thread of a CTA: the largest of `count` values
+__device__ __forceinline__ float largest(const float* v, int count) {
+  __shared__ float top[8];
+  float m = 0.f;
+  for (int i = threadIdx.x; i < count; i += 256) m = fmaxf(m, v[i]);
+  m = warp_max(m);
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = top[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, top[i]);
+  return m;
+}
+
+struct HalfArgs {
+  const uint8_t* codes;
+  const float *scale, *off, *dloss, *tops;
+  __half* out;
+  float* back;  // the factor that takes the power of two back
+  int64_t ldc, lds, ldo, n;
+  int cols, count;
+};
+
+// fp16 rows: of X, each times its loss's gradient (rows without a target: zeros, whatever they
+// hold), or of the weight (WEIGHT: scales by tiles)
+template <bool WEIGHT>
+__global__ void __launch_bounds__(256) k_loss_half(const HalfArgs g) {
+  after_previous();
+  next_may_start();
+  const int e = power_for(largest(g.tops, g.count));
+  const float up = ldexpf(1.f, e);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
+  const int words = g.cols / 16;
+  const int64_t items = g.n * words, step = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < items; i += step) {
+    const int64_t t = i / words;
+    const int c = 16 * int(i - t * words);
+    float f;
+    if constexpr (WEIGHT)
+      f = __ldg(g.scale + (t >> 7) * g.lds + (c >> 7));
+    else
+      f = __ldg(g.off + t) == kNoTarget ? 0.f : __ldg(g.scale + int64_t(c >> 7) * g.lds + t) * __ldg(g.dloss + t);
+    f *= up;
+    float v[16];
+    decode16(__ldg(reinterpret_cast<const uint4*>(g.codes + t * g.ldc + c)), v);
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = two16(v[2 * j] * f, v[2 * j + 1] * f, __half());
+    if (!WEIGHT && __ldg(g.off + t) == kNoTarget)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = 0;
+    uint4* to = reinterpret_cast<uint4*>(g.out + t * g.ldo + c);
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+struct FixArgs {
+  Targets y;
+  const float *off, *logp, *loss;
+  __half* u;
+  int64_t ldu, ld_logp, n;
+  int v0, len;
+};
+
+// U at the targets of a piece of the vocabulary: p - q by the forward pass's log-probability, which
+// keeps what is left of it where both are near 1
+__global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
+  __shared__ float sq[4][kMaxPairs];
+  __shared__ int sid[4][kMaxPairs];
+  after_previous();
+  next_may_start();
+  const float unit = float(1 << kProbBits);
+  if (!g.y.teacher) {
+    const int64_t t = int64_t(blockIdx.x) * 128 + threadIdx.x;
+    if (t >= g.n) return;
+    const int v = g.y.id(t, 0) - g.v0;
+    if (v >= 0 && v < g.len) g.u[t * g.ldu + v] = __float2half_rn(unit * expm1f(-g.loss[t]));
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = int64_t(blockIdx.x) * 4 + warp;
+  if (t >= g.n || g.off[t] == kNoTarget) return;
+  float top, log_sum;
+  teacher_sum(g.y, t, lane, &top, &log_sum);
+  for (int i = lane; i < g.y.k; i += 32) {
+    float z;
+    const int v = g.y.kept_id(t, i, &z);
+    sid[warp][i] = v;
+    sq[warp][i] = v < 0 ? 0.f : expf((z - top) - log_sum);
+  }
+  __syncwarp();
+  for (int i = lane; i < g.y.k; i += 32) {
+    const int id = sid[warp][i], v = id - g.v0;
+    if (id < 0 || v < 0 || v >= g.len) continue;
+    float q = 0.f;  // (the same sum, in the same order, for every pair of this id)
+    for (int j = 0; j < g.y.k; ++j)
+      if (sid[warp][j] == id) q += sq[warp][j];
+    g.u[t * g.ldu + v] = __float2half_rn(unit * (expm1f(g.logp[t * g.ld_logp + i]) + (1.f - q)));
+  }
+}
+
+// ---------------------------------------------------------------- gradient: products
+// out = A B on CTA pairs, fp16 operands and fp32 sums, 256 x 256 tiles as in the weight gradient of a
+// projection: dX's piece = U W (A: rows of U, K-major), dW's rows = U^T X (A: columns of U, MN-major).
+// Bound by the tensor cores.
+
+struct ProductArgs {
+  __nv_bfloat16* out;
+  float* part;          // shares of the sum [splits][tiles], or NULL
+  const float* back;    // factors of out: of the launch, of the operands' powers of two, and of its rows
+  const float *row_factor, *off;
+  float factor;
+  int64_t ldo;
+  int m, n, k;          // rows and columns of out, summed index
+  int splits, add;      // add: to the shares as they are
+  int accumulate, bytes;
+  int* status;
+};
+
+// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B fp16 (0), majors in bits 15, 16
+__host__ __device__ constexpr uint32_t product_idesc(bool a_k_major) {
+  return (1u << 4) | (uint32_t(!a_k_major) << 15) | (1u << 16) | (uint32_t(PN >> 3) << 17) | (uint32_t(PM >> 4) << 24);
+}
+
+__device__ __forceinline__ float row_factor(const ProductArgs& g, int row) {
+  const float f = g.factor;
+  if (!g.row_factor || row >= g.m) return f;
+  return f * __ldg(g.row_factor + row);
+}
+
+template <bool A_KMAJOR>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    k_loss_product(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmO, const ProductArgs g) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  __shared__ __align__(8) uint64_t bars[2 * DW_STAGES + 4];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(DW_STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + 2 + b); };
+
+  const int rank = int(cluster_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (g.m + PM - 1) / PM, nt = (g.n + PN - 1) / PN, ntiles = mt * nt, total = ntiles * g.splits;
+  const int nk = (g.k + DK - 1) / DK;
+  const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
+  // tile t: share t / ntiles of the k-blocks [k0, k1)
+  auto tile_of = [&](int t, int& bm, int& bn, int& k0, int& k1) {
+    const int sp = t / ntiles;
+    banded_tile(t - sp * ntiles, mt, nt, kBand, bm, bn);
+    k0 = int(int64_t(nk) * sp / g.splits);
+    k1 = int(int64_t(nk) * (sp + 1) / g.splits);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < DW_STAGES; ++s) {
+      mbar_init(full_bar(s), 1);   // the leader's expect_tx
+      mbar_init(empty_bar(s), 1);  // the leader's commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * PEPI);  // the epilogue warps of both CTAs
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  after_previous();
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  next_may_start();
+
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs: this CTA's halves)
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += npairs) {
+      int bm, bn, k0, k1;
+      tile_of(t, bm, bn, k0, k1);
+      const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(empty_bar(s), ((it / DW_STAGES) & 1u) ^ 1u, g.status, 51);
+        if (!ok) break;
+        const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
+        const uint32_t fb = map_rank(full_bar(s), 0);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(full_bar(s), 2 * PSTAGE_BYTES);
+          if (A_KMAJOR)
+            tma_load_2d_pair(a_dst, &tmA, kb * DK * 2, ma, fb);  // (the map counts bytes)
+          else
+            tma_load_3d_pair(a_dst, &tmA, kb * DK, ma / 64, fb);
+          tma_load_3d_pair(b_dst, &tmB, kb * DK, nb / 64, fb);
+        }
+        __syncwarp();
+      }
+    }
+    // drain (leader): the pair's last copies have landed; the peer waits for this at
+    // the closing cluster barrier
+    if (rank == 0)
+      for (uint32_t d = it > uint32_t(DW_STAGES) ? it - DW_STAGES : 0; d < it; ++d)
+        mbar_wait(full_bar(int(d % DW_STAGES)), (d / DW_STAGES) & 1u, g.status, 52);
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer (leader)
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < total; t += npairs) {
+      int bm, bn, k0, k1;
+      tile_of(t, bm, bn, k0, k1);
+      const int buf = int(tc & 1u);
+      if (tc >= 2) ok = mbar_wait_cluster_relaxed(tempty_bar(buf), ((tc >> 1) & 1u) ^ 1u, g.status, 53);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(full_bar(s), (it / DW_STAGES) & 1u, g.status, 54);
+        if (!ok) break;
+        tc_fence_after();
+        // 16 of the summed index a product: MN-major 2 KB on (64-column chunks 8 KB apart), K-major
+        // 32 bytes on (rows 128 bytes apart)
+        const uint32_t a_addr = base + uint32_t(s) * PSTAGE_BYTES;
+        const uint64_t ad = A_KMAJOR ? sdesc(a_addr, 16, 1024) : sdesc(a_addr, CHUNK, 1024);
+        const uint64_t bd = sdesc(a_addr + HALF_STAGE, CHUNK, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_pair(tmem + uint32_t(buf) * PN, ad + uint64_t((A_KMAJOR ? 2 : 128) * kk), bd + uint64_t(128 * kk),
+                          product_idesc(A_KMAJOR), kb != k0 || kk != 0 ? 1u : 0u);
+          mma_commit_pair(empty_bar(s));
+          if (kb + 1 == k1) mma_commit_pair(tfull_bar(buf));
+        }
+        __syncwarp();
+      }
+      if (ok) ++tc;
+    }
+    // every product issued here has finished before the accumulators are freed
+    if (tc > 0 && ok) mbar_wait(tfull_bar(int((tc - 1) & 1u)), ((tc - 1) >> 1) & 1u, g.status, 56);
+  } else if (warp >= 4) {
+    // ---------------- output (both CTAs: this CTA's 128 rows)
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t te0 = map_rank(tempty_bar(0), 0);
+    const uint32_t box = base + DW_STAGES * PSTAGE_BYTES + uint32_t(warp - 4) * DW_BOX;
+    const float back = g.part ? 1.f : __ldg(g.back);
+    uint32_t tc = 0;
+    for (int t = pair; t < total; t += npairs, ++tc) {
+      int bm, bn, k0, k1;
+      tile_of(t, bm, bn, k0, k1);
+      const uint32_t buf = tc & 1u;
+      if (!mbar_wait(tfull_bar(int(buf)), (tc >> 1) & 1u, g.status, 55)) break;
+      tc_fence_after();
+      const int row0 = bm * PM + 128 * rank + 32 * q, c0 = bn * PN + 64 * part;
+      uint32_t r[64];
+      const uint32_t at = tmem + (uint32_t(32 * q) << 16) + buf * PN + uint32_t(64 * part);
+      tmem_ld32(at, r);
+      tmem_ld32(at + 32, r + 32);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * buf);
+      const int row = row0 + lane;
+      if (g.part) {
+        float4* o = reinterpret_cast<float4*>(g.part) + share_at(t, rank, warp - 4) + lane;
+        if (row0 < g.m && c0 < g.n)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                                   __uint_as_float(r[4 * j + 3]));
+            if (g.add) {
+              const float4 x = o[32 * j];
+              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            o[32 * j] = v;
+          }
+        continue;
+      }
+      const float f = row_factor(g, row);
+      const bool none = g.off && row < g.m && __ldg(g.off + row) == kNoTarget;
+#pragma unroll
+      for (int j = 0; j < 64; ++j) r[j] = none ? 0u : __float_as_uint(__uint_as_float(r[j]) * f * back);
+      if (g.accumulate && row < g.m) {
+        const __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (c0 + j < g.n) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(o[j]));
+      }
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
+      __syncwarp();
+      put_box<64>(reinterpret_cast<const float*>(r), box, lane);
+      store_box<64>(g.out, g.ldo, g.m, g.n, g.bytes, &tmO, row0, c0, box, lane);
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (the lanes that stored)
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+static_assert(2 * DW_SMEM > kSmemOfSm && DW_SMEM >= kClusterSmemLeast, "a pair's CTA has its SM's tensor memory to itself");
+
+// out = the shares' sum in order, times its factors (+ out): a warp takes 32 rows x 16 columns
+__global__ void __launch_bounds__(256) k_loss_sum(const ProductArgs g) {
+  after_previous();
+  next_may_start();
+  const int mt = (g.m + PM - 1) / PM, nt = (g.n + PN - 1) / PN, ntiles = mt * nt;
+  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, h = int(i & 3), w = int(i >> 2) & (PEPI - 1), rank = int(i >> 6) & 1, t = int(i >> 7);
+  int bm, bn;
+  banded_tile(t, mt, nt, kBand, bm, bn);
+  const int row = bm * PM + 128 * rank + 32 * (w & 3) + lane, c0 = bn * PN + 64 * (w >> 2) + 16 * h;
+  if (row >= g.m || c0 >= g.n) return;
+  const float4* p = reinterpret_cast<const float4*>(g.part) + share_at(t, rank, w) + 128 * h + lane;
+  float4 v[4] = {};
+  for (int k = 0; k < g.splits; ++k, p += share_at(ntiles, 0, 0))
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = p[32 * j];
+      v[j].x += x.x, v[j].y += x.y, v[j].z += x.z, v[j].w += x.w;
+    }
+  const float f = row_factor(g, row), back = __ldg(g.back);
+  const bool none = g.off && __ldg(g.off + row) == kNoTarget;
+  const float* x = reinterpret_cast<const float*>(v);
+  __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;  // (the width is a multiple of 16)
+  alignas(16) __nv_bfloat16 y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float d = none ? 0.f : x[e] * f * back;
+    y[e] = __float2bfloat16_rn(g.accumulate ? d + __bfloat162float(o[e]) : d);
+  }
+  if (g.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0) {
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+    *reinterpret_cast<uint4*>(o + 8) = *reinterpret_cast<const uint4*>(y + 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = y[e];
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr size_t kStatus = 256;
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+size_t scale_bytes(int64_t n, int64_t cols) { return up(size_t((cols + 127) / 128) * size_t(up_to(n, 4)) * 4); }
+
+struct ForwardWs {
+  size_t scales, stats, at, bytes;
+};
+
+ForwardWs forward_ws(int64_t n, int64_t rows, int64_t cols) {
+  ForwardWs p;
+  const size_t parts = size_t((rows + PCOLS - 1) / PCOLS);
+  p.scales = kStatus;
+  p.stats = p.scales + scale_bytes(n, cols);
+  p.at = p.stats + up(parts * size_t(n) * 8);
+  p.bytes = p.at + up(parts * size_t(n));
+  return p;
+}
+
+struct GradWs {
+  int64_t piece;      // words of a piece of the vocabulary, a multiple of 256
+  int pieces, dx_splits;
+  int64_t ldh;        // pitch of the fp16 rows of X and W
+  size_t scales, tops, back, off, x, u, w, dx, dw, bytes;
+};
+
+int64_t piece_len(const GradWs& p, int64_t rows, int i) { return std::min(p.piece, rows - i * p.piece); }
+
+// U and the piece of W in fp16 take 256 MB each at most, unless 256 words do not fit
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+
+GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
+  GradWs p;
+  p.ldh = up_to(cols, 64);
+  const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>({n, p.ldh, 1})) / 256 * 256);
+  const int64_t pieces = (rows + most - 1) / most;
+  p.piece = up_to((rows + pieces - 1) / pieces, 256);
+  p.pieces = int((rows + p.piece - 1) / p.piece);
+  p.dx_splits = dw_splits(p.piece, n, cols);
+  p.scales = kStatus;
+  p.tops = p.scales + scale_bytes(n, cols);
+  p.back = p.tops + up(2 * kPrepCtas * 4);
+  p.off = p.back + 256;
+  p.x = p.off + up(size_t(n) * 4);
+  p.u = p.x + up(size_t(n) * size_t(p.ldh) * 2);
+  p.w = p.u + up(size_t(n) * size_t(p.piece) * 2);
+  p.dx = p.w + up(size_t(p.piece) * size_t(p.ldh) * 2);
+  const bool shares = p.pieces > 1 || p.dx_splits > 1;
+  p.dw = p.dx + (shares ? size_t(p.dx_splits) * size_t((n + PM - 1) / PM) * size_t((cols + PN - 1) / PN) * PM * PN * 4 : 0);
+  size_t dw = 0;
+  for (int i : {0, p.pieces - 1}) {
+    const int64_t len = piece_len(p, rows, i);
+    dw = std::max(dw, dw_part_bytes(dw_splits(n, len, cols), len, cols));
+  }
+  p.bytes = p.dw + dw;
+  return p;
+}
+
+Targets targets(const LossArgs& a) {
+  Targets y;
+  y.ids = a.ids, y.teacher = a.teacher, y.ld_ids = a.ld_ids, y.ld_teacher = a.ld_teacher, y.scale = a.scale;
+  y.rows = a.rows, y.k = a.k, y.id_bits = a.id_bits, y.teacher_kind = a.teacher_kind;
+  return y;
+}
+
+unsigned ctas_for(int64_t items, int64_t each, int64_t most) {
+  return unsigned(std::max<int64_t>(1, std::min<int64_t>(most, (items + each - 1) / each)));
+}
+
+// sum_splits: shares to add up after the product, 0 to leave them
+int launch_product(bool dx, const CUtensorMap& ta, const CUtensorMap& tb, ProductArgs g, int sum_splits, cudaStream_t s) {
+  const char* what = dx ? "loss gradient (dx)" : "loss gradient (dw)";
+  CUtensorMap to = tb;  // (not read by plain stores and shares)
+  if (!g.part && g.bytes == 16)
+    if (int rc = encode_map_bf16_out(&to, g.out, g.n, g.m, g.ldo, 64)) return rc;
+  const int64_t tiles = int64_t((g.m + PM - 1) / PM) * ((g.n + PN - 1) / PN), total = tiles * g.splits;
+  CUtensorMap a = ta, b = tb;
+  void* args[] = {&a, &b, &to, &g};
+  const void* k = dx ? reinterpret_cast<const void*>(k_loss_product<true>) : reinterpret_cast<const void*>(k_loss_product<false>);
+  if (int rc = launch_clusters(what, k, int(std::min<int64_t>(total, cluster_slots()[2])), 2, PAIR_THREADS, DW_SMEM, args, s)) return rc;
+  if (!g.part || !sum_splits) return BQ_OK;
+  g.splits = sum_splits;
+  launch_after(k_loss_sum, unsigned(tiles * 16), 256, 0, s, g);
+  return check(what);
+}
+
+}  // namespace
+
+size_t loss_bytes(int64_t n, int64_t rows, int64_t cols) { return forward_ws(n, rows, cols).bytes; }
+size_t loss_grad_bytes(int64_t n, int64_t rows, int64_t cols) { return grad_ws(n, rows, cols).bytes; }
+
+int launch_loss(const LossArgs& a, void* ws, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto* base = static_cast<unsigned char*>(ws);
+  const ForwardWs p = forward_ws(a.n, a.rows, a.cols);
+  PickArgs pick;
+  pick.x = a.x, pick.w = a.w, pick.xs = a.x_scale, pick.ws = a.w_scale;
+  pick.out = a.teacher ? a.logp : a.loss, pick.ld_out = a.teacher ? a.ld_logp : 1;
+  pick.ldx = a.ldx, pick.ld_xs = a.ld_xs, pick.ldw = a.ldw, pick.n = a.n, pick.cols = a.cols;
+  pick.y = targets(a);
+  launch_after(k_loss_pick, ctas_for(a.n * a.k, 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
+  if (int rc = check("loss (targets)")) return rc;
+  LossTile tile = {};
+  tile.end = kTileStats, tile.zscale = a.scale;
+  tile.stats = reinterpret_cast<float2*>(base + p.stats), tile.at = base + p.at, tile.ld_stats = a.n;
+  LinearArgs l{a.x, a.x_scale, a.w, a.w_scale, base, a.ldx, a.ld_xs, a.ldw, a.rows, a.n, a.rows, a.cols, 0,
+               static_cast<int*>(ws), reinterpret_cast<float*>(base + p.scales), &tile};
+  if (int rc = launch_linear_fp8(l, stream)) return rc;
+  JoinArgs j;
+  j.stats = tile.stats, j.at = tile.at, j.ld_stats = a.n, j.n = a.n, j.ld_logp = a.ld_logp;
+  j.loss = a.loss, j.lse = a.lse, j.logp = a.logp;
+  j.part_cols = tile.part_cols, j.parts = (a.rows + tile.part_cols - 1) / tile.part_cols;
+  j.group = 1;
+  while (j.group < 32 && a.n > int64_t(j.group) * sm_count()) j.group *= 2;
+  j.y = pick.y;
+  launch_after(k_loss_join, unsigned((a.n + j.group - 1) / j.group), 1024, 0, s, j);
+  return check("loss (join)");
+}
+
+int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  static OncePerDevice once;
+  if (int rc = once.run(current_device(), [] {
+        if (cudaFuncSetAttribute(k_loss_product<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(k_loss_product<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
+          return check("loss gradient (shared memory attribute)");
+        return int(BQ_OK);
+      }))
+    return rc;
+  auto* base = static_cast<unsigned char*>(ws);
+  const GradWs p = grad_ws(a.n, a.rows, a.cols);
+  int* status = static_cast<int*>(ws);
+  float *tops = reinterpret_cast<float*>(base + p.tops), *back = reinterpret_cast<float*>(base + p.back);
+  float* off = reinterpret_cast<float*>(base + p.off);
+  auto *x16 = reinterpret_cast<__half*>(base + p.x), *u = reinterpret_cast<__half*>(base + p.u), *w16 = reinterpret_cast<__half*>(base + p.w);
+  const int64_t tile_cols = (a.cols + 127) / 128;
+
+  PrepArgs prep;
+  prep.y = targets(a);
+  prep.xs = a.x_scale, prep.ws = a.w_scale, prep.lse = a.lse, prep.dloss = a.dloss, prep.off = off, prep.tops = tops;
+  prep.ld_xs = a.ld_xs, prep.n = a.n, prep.w_tiles = tile_cols * ((a.rows + 127) / 128), prep.groups = int(tile_cols);
+  const int prep_ctas = int(ctas_for(std::max<int64_t>(a.n * 32, prep.w_tiles), 256, kPrepCtas));
+  launch_after(k_loss_prep, unsigned(prep_ctas), 256, 0, s, prep);
+  if (int rc = check("loss gradient (targets)")) return rc;
+
+  const int64_t half_ctas = int64_t(sm_count()) * 16;
+  CUtensorMap tx, tw, tu;
+  if (a.dw) {
+    HalfArgs h{a.x, a.x_scale, off, a.dloss, tops, x16, back, a.ldx, a.ld_xs, p.ldh, a.n, a.cols, prep_ctas};
+    launch_after(k_loss_half<false>, ctas_for(a.n * (a.cols / 16), 256, half_ctas), 256, 0, s, h);
+    if (int rc = check("loss gradient (rows)")) return rc;
+    if (int rc = encode_map_chunks(&tx, x16, a.cols, a.n, p.ldh, 2)) return rc;
+  }
+  const float unscale = a.scale * (1.f / float(1 << kProbBits));
+  for (int i = 0; i < p.pieces; ++i) {
+    const int64_t v0 = i * p.piece, len = piece_len(p, a.rows, i);
+    const uint8_t* w = a.w + v0 * a.ldw;
+    const float* w_scale = a.w_scale + v0 / 128 * tile_cols;
+    if (a.dx) {
+      HalfArgs h{w, w_scale, nullptr, nullptr, tops + kPrepCtas, w16, back + 1, a.ldw, tile_cols, p.ldh, len, a.cols, prep_ctas};
+      launch_after(k_loss_half<true>, ctas_for(len * (a.cols / 16), 256, half_ctas), 256, 0, s, h);
+      if (int rc = check("loss gradient (weight)")) return rc;
+    }
+    LossTile tile = {};
+    tile.end = kTileProbs, tile.zscale = a.scale, tile.lse = off;
+    LinearArgs l{a.x, a.x_scale, w, w_scale, u, a.ldx, a.ld_xs, a.ldw, p.piece, a.n, int(len), a.cols, 0, status,
+                 reinterpret_cast<float*>(base + p.scales), &tile};
+    if (int rc = launch_linear_fp8(l, stream)) return rc;
+    FixArgs f{prep.y, off, a.logp, a.loss, u, p.piece, a.ld_logp, a.n, int(v0), int(len)};
+    launch_after(k_loss_fix, unsigned((a.n + (a.teacher ? 3 : 127)) / (a.teacher ? 4 : 128)), 128, 0, s, f);
+    if (int rc = check("loss gradient (targets of a piece)")) return rc;
+    if (a.dx) {
+      if (int rc = encode_map_codes(&tu, u, 2 * len, a.n, 2 * p.piece, 128)) return rc;
+      if (int rc = encode_map_chunks(&tw, w16, a.cols, len, p.ldh, 2)) return rc;
+      ProductArgs g = {};
+      g.out = static_cast<__nv_bfloat16*>(a.dx), g.ldo = a.ld_dx, g.m = int(a.n), g.n = a.cols, g.k = int(len);
+      g.part = p.pieces > 1 || p.dx_splits > 1 ? reinterpret_cast<float*>(base + p.dx) : nullptr;
+      g.back = back + 1, g.row_factor = a.dloss, g.off = off, g.factor = unscale;
+      g.splits = std::min(p.dx_splits, (g.k + DK - 1) / DK), g.add = i > 0, g.bytes = store_bytes(a.dx, a.ld_dx, a.cols), g.status = status;
+      if (int rc = launch_product(true, tu, tw, g, i + 1 == p.pieces ? p.dx_splits : 0, s)) return rc;
+    }
+    if (a.dw) {
+      if (int rc = encode_map_chunks(&tu, u, len, a.n, p.piece, 2)) return rc;
+      ProductArgs g = {};
+      g.out = static_cast<__nv_bfloat16*>(a.dw) + v0 * a.ld_dw, g.ldo = a.ld_dw, g.m = int(len), g.n = a.cols, g.k = int(a.n);
+      g.splits = dw_splits(a.n, len, a.cols);
+      g.part = g.splits > 1 ? reinterpret_cast<float*>(base + p.dw) : nullptr;
+      g.back = back, g.factor = unscale, g.accumulate = a.accumulate;
+      g.bytes = store_bytes(g.out, a.ld_dw, a.cols), g.status = status;
+      if (int rc = launch_product(false, tu, tx, g, g.splits, s)) return rc;
+    }
+  }
+  return BQ_OK;
+}
+
+}  // namespace bq

@@ -1,0 +1,116 @@
+// What a loss takes from a tile of logits while it is in registers: each row's softmax
+// statistics, or the values of its probabilities.
+//
+// The statistics of a set of logits are its maximum m and s = the sum of exp(z - m) over all
+// but one logit that attains m: the log of their sum is m + log1p(s), and a logit that
+// is the maximum has the log-probability -log1p(s), which keeps its relative precision however near
+// to 0 it is (with the maximum in the sum it would be lost beside its 1).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fp8_codes.h"
+
+namespace bq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoTarget = -INFINITY;  // in the place of a row's log-sum: the row's values are 0
+// Probabilities (and their differences from a target's weight, in [-1, 1]) are held as fp16 times
+// 2^14: eleven bits down to 2^-28, and room to 4 where the forward's sum and these differ.
+constexpr int kProbBits = 14;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct RowStats {
+  float m, s;
+  int at;  // where the maximum is
+};
+
+// statistics of two sets
+__device__ __forceinline__ RowStats joined(RowStats a, RowStats b) {
+  const bool swap = b.m > a.m;
+  const RowStats hi = swap ? b : a, lo = swap ? a : b;
+  const float f = lo.m == hi.m ? 1.f : ex2((lo.m - hi.m) * kLog2e);
+  return {hi.m, fmaf(lo.s + 1.f, f, hi.s), lo.m == hi.m ? min(a.at, b.at) : hi.at};
+}
+
+// 2^kProbBits exp(z - lse), 0 in a row without a target
+__device__ __forceinline__ float scaled_prob(float z, float lse) {
+  return lse == kNoTarget ? 0.f : ex2(fmaf(z - lse, kLog2e, float(kProbBits)));
+}
+
+// of a lane's row: N logits' products, of which the first `cols` count
+template <int N>
+__device__ __forceinline__ void lane_stats(float* z, int cols, float zscale, bool on, float2* stats, uint8_t* at) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) z[j] *= zscale;
+  if (cols < N)
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j >= cols) z[j] = -INFINITY;
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is in s)
+#pragma unroll
+  for (int j = 0; j < N; ++j) m4[j & 3] = fmaxf(m4[j & 3], z[j]);
+  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  float s[2] = {0.f, 0.f};
+  int count = -1, where = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float e = ex2((z[j] - m) * kLog2e);
+    if (z[j] == m)
+      ++count, where = j;
+    else
+      s[j & 1] += e;
+  }
+  if (on) {
+    *stats = make_float2(m, s[0] + s[1] + float(count));
+    *at = uint8_t(where);
+  }
+}
+
+// of a warp's row: the products of columns lane + 32 j < cols
+__device__ __forceinline__ void row_stats(const float* v, int cols, float zscale, int lane, float2* stats, uint8_t* at) {
+  float z[4], m = -INFINITY, s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    z[j] = lane + 32 * j < cols ? v[j] * zscale : -INFINITY;
+    m = fmaxf(m, z[j]);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  int count = 0, where = 128;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (z[j] == m)
+      ++count, where = min(where, lane + 32 * j);
+    else
+      s += ex2((z[j] - m) * kLog2e);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+  count = __reduce_add_sync(0xFFFFFFFFu, count);
+  where = __reduce_min_sync(0xFFFFFFFFu, where);
+  if (lane == 0) {
+    *stats = make_float2(m, s + float(count - 1));
+    *at = uint8_t(where);
+  }
+}
+
+// z: a lane's row of products, of which the first `cols` count, becomes its scaled probabilities
+template <int N>
+__device__ __forceinline__ void lane_probs(float* z, int cols, float zscale, float lse) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float p = ex2(fmaf(z[j] * zscale - lse, kLog2e, float(kProbBits)));
+    z[j] = lse == kNoTarget || j >= cols ? 0.f : p;
+  }
+}
+
+}  // namespace bq

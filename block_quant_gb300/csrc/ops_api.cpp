@@ -1,8 +1,9 @@
 // C ABI of the layer operators: argument checks and dispatch to the kernels of
-// row_ops.cu, linear_fp8.cu and ns_gemm.cu.
+// row_ops.cu, linear_fp8.cu and loss_fp8.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "bq_internal.h"
@@ -77,6 +78,60 @@ int check_weight(const char* who, const uint8_t* w, int64_t ldw, const float* w_
   if (off(w, 16) || ldw % 16 || off(w_scale, 4))
     return fail(BQ_EALIGN, who, "weight codes 16-byte aligned with a pitch multiple of 16, scales 4-byte aligned");
   return BQ_OK;
+}
+
+// the operands that a loss and its gradient share; sizes are checked, n > 0
+int check_loss(const char* who, LossArgs& a) {
+  a.ldx = a.n == 1 ? std::max(up16(a.ldx), int64_t(a.cols)) : a.ldx;
+  a.ldw = a.rows == 1 ? std::max(up16(a.ldw), int64_t(a.cols)) : a.ldw;
+  a.ld_xs = pitch(a.ld_xs, a.cols <= 128 ? 1 : 2, a.n);
+  a.ld_ids = pitch(a.ld_ids, a.n, a.k), a.ld_teacher = pitch(a.ld_teacher, a.n, a.k), a.ld_logp = pitch(a.ld_logp, a.n, a.k);
+  if (int rc = check_weight(who, a.w, a.ldw, a.w_scale, a.cols)) return rc;
+  if (!a.x || !a.x_scale || !a.ids || !a.lse) return fail(BQ_EINVAL, who, "NULL argument");
+  if (a.ldx < a.cols || a.ld_xs < a.n || a.ld_ids < a.k || (a.teacher && (a.ld_teacher < a.k || a.ld_logp < a.k)))
+    return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(a.x, 16) || a.ldx % 16) return fail(BQ_EALIGN, who, "codes must be 16-byte aligned with a pitch multiple of 16");
+  if (off(a.x_scale, 4) || off(a.ids, uintptr_t(a.id_bits / 8)) || off(a.teacher, a.teacher_kind == BQ_ROWS_FP32 ? 4 : 2) ||
+      off(a.loss, 4) || off(a.lse, 4) || off(a.logp, 4) || off(a.dloss, 4) || off(a.dx, 2) || off(a.dw, 2))
+    return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  return BQ_OK;
+}
+
+// what a loss call asks of its sizes, types and factor whatever n is
+int check_targets(const char* who, int64_t n, int64_t rows, int64_t cols, int64_t k, int id_bits, int teacher_kind, float scale) {
+  if (int rc = check_linear(who, n, rows, cols)) return rc;
+  if (id_bits != 32 && id_bits != 64) return fail(BQ_EINVAL, who, "ids must have 32 or 64 bits");
+  if (k < 1 || k > 1024) return fail(BQ_EINVAL, who, "k outside [1, 1024]");
+  if (teacher_kind != BQ_ROWS_BF16 && teacher_kind != BQ_ROWS_FP32) return fail(BQ_EINVAL, who, "teacher kind must be bf16 or fp32");
+  if (!std::isfinite(scale)) return fail(BQ_EINVAL, who, "scale must be finite");
+  return BQ_OK;
+}
+
+int run_loss(const char* who, LossArgs a, void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_ws(who, ws, ws_bytes, loss_bytes(a.n, a.rows, a.cols))) return rc;
+  if (a.n == 0) return BQ_OK;
+  if (int rc = check_loss(who, a)) return rc;
+  if (!a.loss) return fail(BQ_EINVAL, who, "NULL argument");
+  return launch_loss(a, ws, stream);
+}
+
+int run_loss_grad(const char* who, LossArgs a, void* ws, size_t ws_bytes, void* stream) {
+  if (int rc = check_ws(who, ws, ws_bytes, loss_grad_bytes(a.n, a.rows, a.cols))) return rc;
+  if (!a.dx && !a.dw && a.n > 0) return fail(BQ_EINVAL, who, "no output");
+  a.ld_dw = pitch(a.ld_dw, a.rows, a.cols);
+  if (a.dw && a.ld_dw < a.cols) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (off(a.dw, 2)) return fail(BQ_EALIGN, who, "pointer not aligned to its element type");
+  if (a.n == 0) {
+    if (a.accumulate || !a.dw) return BQ_OK;
+    const cudaError_t e = cudaMemset2DAsync(a.dw, size_t(a.ld_dw) * 2, 0, size_t(a.cols) * 2, size_t(a.rows),
+                                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BQ_OK : fail(BQ_ECUDA, who, cudaGetErrorString(e));
+  }
+  a.ld_dx = pitch(a.ld_dx, a.n, a.cols);
+  if (a.dx && a.ld_dx < a.cols) return fail(BQ_EINVAL, who, "pitch below the width");
+  if (int rc = check_loss(who, a)) return rc;
+  if (!a.dloss) return fail(BQ_EINVAL, who, "NULL argument");
+  return launch_loss_grad(a, ws, stream);
 }
 
 }  // namespace
@@ -280,6 +335,84 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
                    stream);
 }
 
+int bq_loss_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(BQ_EINVAL, "bq_loss_fp8_workspace", "NULL argument");
+  if (int rc = check_linear("bq_loss_fp8_workspace", n, rows, cols)) return rc;
+  *bytes = loss_bytes(n, rows, cols);
+  return BQ_OK;
+}
+
+int bq_loss_fp8_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(BQ_EINVAL, "bq_loss_fp8_grad_workspace", "NULL argument");
+  if (int rc = check_linear("bq_loss_fp8_grad_workspace", n, rows, cols)) return rc;
+  *bytes = loss_grad_bytes(n, rows, cols);
+  return BQ_OK;
+}
+
+int bq_cross_entropy_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                         int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* targets,
+                         int target_bits, float scale, float* loss, float* lse, void* ws, size_t ws_bytes,
+                         bq_stream_t stream) {
+  const char* who = "bq_cross_entropy_fp8";
+  if (int rc = check_targets(who, n, rows, cols, 1, target_bits, BQ_ROWS_BF16, scale)) return rc;
+  LossArgs a = {};
+  a.x = x, a.x_scale = x_scale, a.w = w, a.w_scale = w_scale, a.ids = targets, a.loss = loss, a.lse = lse;
+  a.ldx = ld_x, a.ld_xs = ld_scale, a.ldw = ld_w, a.ld_ids = 1, a.n = n, a.scale = scale;
+  a.rows = int(rows), a.cols = int(cols), a.k = 1, a.id_bits = target_bits;
+  return run_loss(who, a, ws, ws_bytes, stream);
+}
+
+int bq_cross_entropy_fp8_grad(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                              int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols,
+                              const void* targets, int target_bits, float scale, const float* loss, const float* lse,
+                              const float* dloss, void* dx, int64_t ld_dx, void* dw, int64_t ld_dw, int accumulate,
+                              void* ws, size_t ws_bytes, bq_stream_t stream) {
+  const char* who = "bq_cross_entropy_fp8_grad";
+  if (int rc = check_targets(who, n, rows, cols, 1, target_bits, BQ_ROWS_BF16, scale)) return rc;
+  if (n > 0 && !loss) return fail(BQ_EINVAL, who, "NULL argument");
+  LossArgs a = {};
+  a.x = x, a.x_scale = x_scale, a.w = w, a.w_scale = w_scale, a.ids = targets;
+  a.loss = const_cast<float*>(loss), a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dx = dx, a.dw = dw;
+  a.ldx = ld_x, a.ld_xs = ld_scale, a.ldw = ld_w, a.ld_ids = 1, a.ld_dx = ld_dx, a.ld_dw = ld_dw, a.n = n, a.scale = scale;
+  a.rows = int(rows), a.cols = int(cols), a.k = 1, a.id_bits = target_bits, a.accumulate = accumulate ? 1 : 0;
+  return run_loss_grad(who, a, ws, ws_bytes, stream);
+}
+
+int bq_distill_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                   int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* ids,
+                   int id_bits, int64_t ld_ids, const void* teacher, int teacher_kind, int64_t ld_teacher, int64_t k,
+                   float scale, float* loss, float* lse, float* logp, int64_t ld_logp, void* ws, size_t ws_bytes,
+                   bq_stream_t stream) {
+  const char* who = "bq_distill_fp8";
+  if (int rc = check_targets(who, n, rows, cols, k, id_bits, teacher_kind, scale)) return rc;
+  if (n > 0 && (!teacher || !logp)) return fail(BQ_EINVAL, who, "NULL argument");
+  LossArgs a = {};
+  a.x = x, a.x_scale = x_scale, a.w = w, a.w_scale = w_scale, a.ids = ids, a.teacher = teacher;
+  a.loss = loss, a.lse = lse, a.logp = logp;
+  a.ldx = ld_x, a.ld_xs = ld_scale, a.ldw = ld_w, a.ld_ids = ld_ids, a.ld_teacher = ld_teacher, a.ld_logp = ld_logp;
+  a.n = n, a.scale = scale, a.rows = int(rows), a.cols = int(cols), a.k = int(k), a.id_bits = id_bits;
+  a.teacher_kind = teacher_kind;
+  return run_loss(who, a, ws, ws_bytes, stream);
+}
+
+int bq_distill_fp8_grad(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                        int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* ids,
+                        int id_bits, int64_t ld_ids, const void* teacher, int teacher_kind, int64_t ld_teacher, int64_t k,
+                        float scale, const float* lse, const float* logp, int64_t ld_logp, const float* dloss, void* dx,
+                        int64_t ld_dx, void* dw, int64_t ld_dw, int accumulate, void* ws, size_t ws_bytes,
+                        bq_stream_t stream) {
+  const char* who = "bq_distill_fp8_grad";
+  if (int rc = check_targets(who, n, rows, cols, k, id_bits, teacher_kind, scale)) return rc;
+  if (n > 0 && (!teacher || !logp)) return fail(BQ_EINVAL, who, "NULL argument");
+  LossArgs a = {};
+  a.x = x, a.x_scale = x_scale, a.w = w, a.w_scale = w_scale, a.ids = ids, a.teacher = teacher;
+  a.lse = const_cast<float*>(lse), a.logp = const_cast<float*>(logp), a.dloss = dloss, a.dx = dx, a.dw = dw;
+  a.ldx = ld_x, a.ld_xs = ld_scale, a.ldw = ld_w, a.ld_ids = ld_ids, a.ld_teacher = ld_teacher, a.ld_logp = ld_logp;
+  a.ld_dx = ld_dx, a.ld_dw = ld_dw, a.n = n, a.scale = scale, a.rows = int(rows), a.cols = int(cols), a.k = int(k);
+  a.id_bits = id_bits, a.teacher_kind = teacher_kind, a.accumulate = accumulate ? 1 : 0;
+  return run_loss_grad(who, a, ws, ws_bytes, stream);
+}
+
 int bq_linear_check(void* ws, size_t ws_bytes, bq_stream_t stream) {
   if (!ws || ws_bytes < kStatusBytes) return fail(BQ_EINVAL, "bq_linear_check", "bad workspace");
   int status = 0;
@@ -330,6 +463,20 @@ int bq_call(int op, const void* args) {
     case BQ_CALL_LINEAR_DW:
       return bq_linear_fp8_dw(p(0), q(1), b(2), q(3), s(4), q(5), q(6), q(7), q(8), p(9), q(10), int(q(11)), p(12),
                               size_t(q(13)), st(14));
+    case BQ_CALL_CROSS_ENTROPY:
+      return bq_cross_entropy_fp8(b(0), q(1), s(2), q(3), b(4), q(5), s(6), q(7), q(8), q(9), p(10), int(q(11)), f(12),
+                                  s(13), s(14), p(15), size_t(q(16)), st(17));
+    case BQ_CALL_CROSS_ENTROPY_GRAD:
+      return bq_cross_entropy_fp8_grad(b(0), q(1), s(2), q(3), b(4), q(5), s(6), q(7), q(8), q(9), p(10), int(q(11)),
+                                       f(12), s(13), s(14), s(15), p(16), q(17), p(18), q(19), int(q(20)), p(21),
+                                       size_t(q(22)), st(23));
+    case BQ_CALL_DISTILL:
+      return bq_distill_fp8(b(0), q(1), s(2), q(3), b(4), q(5), s(6), q(7), q(8), q(9), p(10), int(q(11)), q(12), p(13),
+                            int(q(14)), q(15), q(16), f(17), s(18), s(19), s(20), q(21), p(22), size_t(q(23)), st(24));
+    case BQ_CALL_DISTILL_GRAD:
+      return bq_distill_fp8_grad(b(0), q(1), s(2), q(3), b(4), q(5), s(6), q(7), q(8), q(9), p(10), int(q(11)), q(12),
+                                 p(13), int(q(14)), q(15), q(16), f(17), s(18), s(19), q(20), s(21), p(22), q(23), p(24),
+                                 q(25), int(q(26)), p(27), size_t(q(28)), st(29));
     default: return fail(BQ_EINVAL, "bq_call", "unknown call");
   }
 }

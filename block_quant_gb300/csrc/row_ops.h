@@ -3,6 +3,8 @@
 // unless said otherwise.
 #pragma once
 
+#include <vector_types.h>
+
 #include <cstddef>
 #include <cstdint>
 
@@ -56,6 +58,19 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
 // bf16 rows of X (from FP8 rows) and of dY (dy NULL: not wanted) at pitches ldo, ldyo
 int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
                      int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
+// What k_linear and k_linear_pair do with a tile of products: rows of out, or, for a loss
+// (loss_fp8.cu), statistics of each row's part of the tile or its scaled probabilities
+enum TileEnd { kTileOut = 0, kTileStats = 1, kTileProbs = 2 };
+struct LossTile {
+  int end;
+  float zscale;      // a logit is zscale times the product
+  float2* stats;     // kTileStats: [part][ld_stats] and
+  uint8_t* at;       // the largest logit's column in its part
+  int64_t ld_stats;
+  const float* lse;  // kTileProbs: one a row
+  int part_cols;     // set by the launch: columns of a part
+};
+
 // FP8 projections (linear_fp8.cu)
 struct LinearArgs {
   const uint8_t* x;      // codes [n, red], pitch ldx (a multiple of 16)
@@ -69,6 +84,7 @@ struct LinearArgs {
   int* status;
   float* scale_ws;       // room for x_scale at a pitch of n + 3 at most (not used if x_scale is 16-byte
                          // aligned and ld_xs a multiple of 4)
+  LossTile* loss = nullptr;  // kTileProbs: out is fp16, 16-byte aligned, its pitch a multiple of 8 that covers the width
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 
@@ -92,5 +108,25 @@ int launch_dw(const DwArgs& a, void* stream);
 bool dw_few(int64_t n, int64_t rows, int64_t cols);
 int launch_dw_few(const void* dy, int64_t ld_dy, const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds,
                   int n, int rows, int cols, void* dw, int64_t ld_dw, int accumulate, void* stream);
+
+// Softmax losses over an FP8 head (loss_fp8.cu).  Targets of row t: pair i < k of ids (32 or 64
+// bits, pitch ld_ids), with the teacher's logits (NULL: one pair of weight 1, a class).
+struct LossArgs {
+  const uint8_t* x;
+  const float* x_scale;
+  const uint8_t* w;
+  const float* w_scale;
+  const void *ids, *teacher;
+  float *loss, *lse, *logp;  // forward: written; gradient: read (a class's logp is -loss)
+  const float* dloss;
+  void *dx, *dw;             // gradient, either may be NULL
+  int64_t ldx, ld_xs, ldw, ld_ids, ld_teacher, ld_logp, ld_dx, ld_dw, n;
+  float scale;
+  int rows, cols, k, id_bits, teacher_kind, accumulate;
+};
+size_t loss_bytes(int64_t n, int64_t rows, int64_t cols);
+size_t loss_grad_bytes(int64_t n, int64_t rows, int64_t cols);
+int launch_loss(const LossArgs& a, void* ws, void* stream);
+int launch_loss_grad(const LossArgs& a, void* ws, void* stream);
 
 }  // namespace bq

@@ -498,6 +498,58 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
                      int64_t ld_scale, int64_t n, int64_t rows, int64_t cols, void* dw, int64_t ld_dw, int accumulate,
                      void* ws, size_t ws_bytes, bq_stream_t stream);
 
+/* bq_cross_entropy_fp8, bq_distill_fp8 - the softmax losses of a language model's head
+ * and their gradients, without the logits: with the FP8 rows X (n x cols) and the FP8
+ * weight W (rows x cols, a row per word) of bq_linear_fp8,
+ *   z[t, v] = scale * sum_c X[t, c] W[v, c]   (never stored),
+ *   lse[t] = log sum_v exp(z[t, v]),  p = exp(z - lse);
+ * scale is a factor of the logits (1 / temperature; finite).
+ *   bq_cross_entropy_fp8: targets (int32 or int64, target_bits), one a row:
+ *     loss[t] = lse[t] - z[t, targets[t]].  A target outside [0, rows), as padding has,
+ *     makes loss[t] 0 and gives the row no gradient.
+ *   bq_distill_fp8: k pairs a row (1 <= k <= 1024), ids (int32 or int64) and the teacher's
+ *     logits (teacher_kind BQ_ROWS_BF16 or BQ_ROWS_FP32).  A pair counts if its id is in
+ *     [0, rows) and its logit is not -infinity; q = softmax(scale * teacher) over the
+ *     row's pairs that count (an id may occur twice: both count);
+ *     logp[t, i] = z[t, ids[t, i]] - lse[t], 0 for a pair that does not count;
+ *     loss[t] = sum_i q_i (log q_i - logp[t, i]); a row of which no pair counts has
+ *     loss 0 and no gradient.
+ * loss and lse (n) are fp32, logp (n x k, pitch ld_logp) too; lse is written for every
+ * row.  log-probabilities near 0 keep their relative precision.
+ *   The *_grad calls take what the forward call has written and dloss (fp32, n), the
+ * gradient of loss.  With u[t, v] = p[t, v] - (the weight of v among t's targets, where p
+ * is taken as exp(-loss) or exp(logp)), 0 in rows without a target, whatever they hold:
+ *     dx [n, cols]    = scale * diag(dloss) u W        (NULL: not wanted)
+ *     dw [rows, cols] = scale * (diag(dloss) u)^T X    (NULL; accumulate: += )
+ * both bf16, rounded once from fp32 sums.  The logits are made again in pieces of the vocabulary; u,
+ * W and dloss * X are held as fp16, times powers of two that keep eleven bits of
+ * each over 2^28 below its largest magnitude.
+ * Sums are taken in an order that the sizes and the GPU fix.  Operands are aligned as in
+ * bq_linear_fp8, n may be 0.  ws: bq_loss_fp8_workspace or bq_loss_fp8_grad_workspace bytes
+ * (either serves cross entropy and distillation), used and checked as bq_linear_fp8's. */
+int bq_loss_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
+int bq_loss_fp8_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
+int bq_cross_entropy_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                         int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* targets,
+                         int target_bits, float scale, float* loss, float* lse, void* ws, size_t ws_bytes,
+                         bq_stream_t stream);
+int bq_cross_entropy_fp8_grad(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                              int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols,
+                              const void* targets, int target_bits, float scale, const float* loss, const float* lse,
+                              const float* dloss, void* dx, int64_t ld_dx, void* dw, int64_t ld_dw, int accumulate,
+                              void* ws, size_t ws_bytes, bq_stream_t stream);
+int bq_distill_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                   int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* ids,
+                   int id_bits, int64_t ld_ids, const void* teacher, int teacher_kind, int64_t ld_teacher, int64_t k,
+                   float scale, float* loss, float* lse, float* logp, int64_t ld_logp, void* ws, size_t ws_bytes,
+                   bq_stream_t stream);
+int bq_distill_fp8_grad(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
+                        int64_t ld_w, const float* w_scale, int64_t n, int64_t rows, int64_t cols, const void* ids,
+                        int id_bits, int64_t ld_ids, const void* teacher, int teacher_kind, int64_t ld_teacher, int64_t k,
+                        float scale, const float* lse, const float* logp, int64_t ld_logp, const float* dloss, void* dx,
+                        int64_t ld_dx, void* dw, int64_t ld_dw, int accumulate, void* ws, size_t ws_bytes,
+                        bq_stream_t stream);
+
 /* bq_linear_check - synchronise `stream` and read the workspace's device error
  * word: every wait of the tensor-core kernels gives up after about two seconds,
  * records where and lets the kernel exit.  BQ_OK if it is clear; otherwise it is
@@ -516,7 +568,11 @@ enum {
   BQ_CALL_QUANT_ROWS = 4,
   BQ_CALL_LINEAR = 5,
   BQ_CALL_LINEAR_DX = 6,
-  BQ_CALL_LINEAR_DW = 7
+  BQ_CALL_LINEAR_DW = 7,
+  BQ_CALL_CROSS_ENTROPY = 8,
+  BQ_CALL_CROSS_ENTROPY_GRAD = 9,
+  BQ_CALL_DISTILL = 10,
+  BQ_CALL_DISTILL_GRAD = 11
 };
 int bq_call(int op, const void* args);
 
