@@ -42,6 +42,7 @@ constexpr int B_STAGE = BN * BK;
 constexpr int kMaxStages = 8;
 constexpr int kPartPitch = BN + 1;             // floats of a row of a split's partial tile in shared memory
 constexpr int kTmemCols = 2 * BN;
+static_assert(BN == 2 * kPartCols, "a lane's columns are a part");
 constexpr int kAhead = 4;                      // k-blocks from a scale's load to its use
 constexpr int kSmem = 112 * 1024;               // dynamic shared memory at most: two CTAs per SM
 
@@ -76,9 +77,11 @@ struct LinArgs {
   // a tile's end other than rows of out (loss_tile.h)
   float2* stats;
   uint8_t* at;
-  const float* lse;
+  const float *lse, *loss, *factor;
+  const int* target;
   int64_t ld_stats;
   float zscale;
+  int first;
 };
 
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
@@ -105,8 +108,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cluster_rank());
   const int tile = int(blockIdx.x) / g.split;
-  const int nt = (g.width + BN - 1) / BN;
-  const int m0 = (tile / nt) * BM, n0 = (tile % nt) * BN;
+  const int nt = (g.width + BN - 1) / BN, mt = (g.n + BM - 1) / BM;
+  // a loss's tiles: the rows' blocks fastest, so that a head larger than L2 is read once (333 rows of 50001 x
+  // 2880: 83 us by columns, 66 so)
+  const int m0 = (END == kTileOut ? tile / nt : tile % mt) * BM, n0 = (END == kTileOut ? tile % nt : tile / mt) * BN;
   const int nk = (g.red + BK - 1) / BK;
   const int k0 = int(int64_t(nk) * rank / g.split), blocks = int(int64_t(nk) * (rank + 1) / g.split) - k0;
   const uint32_t b_base = base, a_base = base + uint32_t(g.stages) * B_STAGE;
@@ -231,18 +236,58 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   }
   __syncwarp();
+  if constexpr (END == kTileStats) {
+    // whole sums leave from registers, a lane's row and half of the tile's columns each
+    if (g.split == 1 && warp >= 2 && q < quarters) {
+      const int row = m0 + 32 * q + lane, c0 = n0 + half * (BN / 2);
+      if (c0 < g.width) {
+        const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row;
+        lane_stats<kPartCols>(acc, g.width - c0, g.zscale, row < g.n, g.stats + at, g.at + at);
+      }
+    }
+  }
   __syncthreads();  // the stages are free: every copy has landed and every product is done
   float* part = reinterpret_cast<float*>(gbase);
-  if (warp >= 2 && q < quarters) {
+  if (warp >= 2 && q < quarters && !(END == kTileStats && g.split == 1)) {
     float* prow = part + (32 * q + lane) * kPartPitch + half * (BN / 2);
 #pragma unroll
     for (int j = 0; j < BN / 2; ++j) prow[j] = acc[j];
   }
   cluster_sync();  // (every thread) the cluster's partial tiles are written
-  const int rows = min(BM, g.n - m0), cols = min(BN, g.width - n0);
+  const int rows = END == kTileStats && g.split == 1 ? 0 : min(BM, g.n - m0), cols = min(BN, g.width - n0);
   // each CTA finishes its share of the tile's rows: lane l columns l, l + 32, ...
   const uint32_t part0 = smem_addr(part);
-  for (int r = rank * (THREADS / 32) + warp; r < rows; r += g.split * (THREADS / 32)) {
+  // (probabilities: the log-sum and the class of the warp's i-th row come ahead, in lane i)
+  constexpr int EPI_ROWS = THREADS / 32;
+  static_assert(BM <= 32 * EPI_ROWS, "a lane a row");
+  float lses = 0.f;
+  int classes = -1, nth = 0;
+  if constexpr (END == kTileProbs) {
+    const int r = rank * EPI_ROWS + warp + lane * g.split * EPI_ROWS;
+    if (r < rows) lses = __ldg(g.lse + m0 + r), classes = __ldg(g.target + m0 + r);
+  }
+  if constexpr (END == kTileTriples) {
+    for (int t = rank * EPI_ROWS + warp; 3 * t < rows; t += g.split * EPI_ROWS) {
+      float v[BN / 32] = {};
+      for (int c = 0; c < g.split; ++c) {
+        const uint32_t at = map_rank(part0, uint32_t(c)) + 4u * uint32_t(3 * t * kPartPitch + lane);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+          for (int j = 0; j < BN / 32; ++j) {
+            float x;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at + 4u * uint32_t(e * kPartPitch) + 128u * j) : "memory");
+            v[j] += x;
+          }
+      }
+      const bool none = __ldg(g.lse + t) == kNoTarget;  // (whatever W holds)
+      const float f = g.zscale * __ldg(g.factor + t);
+      __nv_bfloat16* o = g.out + int64_t(t) * g.ldo + n0;
+#pragma unroll
+      for (int j = 0; j < BN / 32; ++j)
+        if (lane + 32 * j < cols) o[lane + 32 * j] = __float2bfloat16_rn(none ? 0.f : f * v[j]);
+    }
+  } else for (int r = rank * EPI_ROWS + warp; r < rows; r += g.split * EPI_ROWS, ++nth) {
     float v[BN / 32];
 #pragma unroll
     for (int j = 0; j < BN / 32; ++j) v[j] = 0.f;
@@ -268,16 +313,21 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
     }
     if constexpr (END == kTileStats) {
-      row_stats(v, cols, g.zscale, lane, g.stats + int64_t(n0 >> 7) * g.ld_stats + m0 + r,
-                g.at + int64_t(n0 >> 7) * g.ld_stats + m0 + r);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (kPartCols * h < cols) {
+          const int64_t at = int64_t(n0 / kPartCols + h) * g.ld_stats + m0 + r;
+          row_stats<2>(v + 2 * h, cols - kPartCols * h, g.zscale, lane, g.stats + at, g.at + at);
+        }
       continue;
     }
     if constexpr (END == kTileProbs) {
-      const float lse = __ldg(g.lse + m0 + r);
+      const float lse = __shfl_sync(0xFFFFFFFFu, lses, nth);
+      const int y = __shfl_sync(0xFFFFFFFFu, classes, nth) - g.first - n0 - lane;
       __half* u = reinterpret_cast<__half*>(g.out) + int64_t(m0 + r) * g.ldo + n0;
 #pragma unroll
       for (int j = 0; j < BN / 32; ++j)
-        if (lane + 32 * j < cols) u[lane + 32 * j] = __float2half_rn(scaled_prob(v[j] * g.zscale, lse));
+        if (lane + 32 * j < cols) u[lane + 32 * j] = __float2half_rn(y == 32 * j ? scaled_rest(__ldg(g.loss + m0 + r)) : scaled_prob(v[j] * g.zscale, lse));
       continue;
     }
     __nv_bfloat16* o = g.out + int64_t(m0 + r) * g.ldo + n0;
@@ -488,6 +538,10 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       float acc[PCOLS];
 #pragma unroll
       for (int j = 0; j < PCOLS; ++j) acc[j] = 0.f;
+      float lse = kNoTarget;
+      int y = -1;
+      if constexpr (END == kTileProbs)
+        if (row0 + lane < g.n) lse = __ldg(g.lse + row0 + lane), y = __ldg(g.target + row0 + lane) - g.first - c0;
       // W's scales for 32 k-blocks, block kb + l in lane l
       float wl = 0.f, wn = c0 < g.width && lane < nk ? __ldg(ws + lane * ws_step) : 0.f;
       for (int kb = 0; kb < nk; ++kb, ++it) {
@@ -522,21 +576,24 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       if (!ok) break;
       if constexpr (END == kTileStats) {
         if (c0 < g.width) {
-          const int64_t at = int64_t(c0 / PCOLS) * g.ld_stats + row0 + lane;
-          lane_stats<PCOLS>(acc, g.width - c0, g.zscale, row0 + lane < g.n, g.stats + at, g.at + at);
+          const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row0 + lane;
+          lane_stats<kPartCols>(acc, g.width - c0, g.zscale, row0 + lane < g.n, g.stats + at, g.at + at);
         }
       } else {
-        if constexpr (END == kTileProbs) {
-          const float lse = row0 + lane < g.n ? __ldg(g.lse + row0 + lane) : kNoTarget;
-          lane_probs<PCOLS>(acc, g.width - c0, g.zscale, lse);
-        }
+        if constexpr (END == kTileProbs) lane_probs<PCOLS>(acc, g.width - c0, g.zscale, lse);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
           __syncwarp();
-          if constexpr (END == kTileProbs)
+          if constexpr (END == kTileProbs) {
             put_box<32, __half>(acc + 32 * u, box, lane);
-          else
+            if (y >= 32 * u && y < 32 * u + 32) {  // the row's class
+              const __half f = __float2half_rn(scaled_rest(__ldg(g.loss + row0 + lane)));
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(box_word<32>(box, lane, (y & 31) >> 3) + 2u * uint32_t(y & 7)),
+                           "h"(__half_as_ushort(f))
+                           : "memory");
+            }
+          } else
             put_box<32>(acc + 32 * u, box, lane);
           store_box<32>(g.out, g.ldo, g.n, g.width, g.bytes, &tmO, row0, c0 + 32 * u, box, lane);
         }
@@ -876,6 +933,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
             cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear<true, kTileTriples>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear_pair<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear_pair<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess)
           return check("bq_linear_fp8 (shared memory attribute)");
@@ -888,9 +946,14 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.ld_xs = a.ld_xs, g.ldo = a.ldo, g.n = int(a.n), g.width = width, g.red = red;
   g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
   g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
-  g.stats = nullptr, g.at = nullptr, g.lse = nullptr, g.ld_stats = 0, g.zscale = 1.f;
+  g.stats = nullptr, g.at = nullptr, g.lse = nullptr, g.loss = nullptr, g.factor = nullptr, g.target = nullptr;
+  g.ld_stats = 0, g.zscale = 1.f, g.first = 0;
   const int end = a.loss ? a.loss->end : int(kTileOut);
-  if (a.loss) g.stats = a.loss->stats, g.at = a.loss->at, g.lse = a.loss->lse, g.ld_stats = a.loss->ld_stats, g.zscale = a.loss->zscale;
+  if (a.loss) {
+    g.stats = a.loss->stats, g.at = a.loss->at, g.ld_stats = a.loss->ld_stats, g.zscale = a.loss->zscale;
+    g.lse = a.loss->lse, g.loss = a.loss->loss, g.target = a.loss->target, g.first = a.loss->first;
+    g.factor = a.loss->factor;
+  }
   if (end != kTileOut) g.bytes = 16;
   const int nk = (red + BK - 1) / BK;
   CUtensorMap tx, tw, to;
@@ -936,7 +999,6 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
                     : end == kTileProbs ? reinterpret_cast<const void*>(k_linear_pair<false, kTileProbs>)
                     : a.transposed      ? reinterpret_cast<const void*>(k_linear_pair<true>)
                                         : reinterpret_cast<const void*>(k_linear_pair<false>);
-    if (a.loss) a.loss->part_cols = PCOLS;
     return launch_clusters("bq_linear_fp8", k, int(std::min<int64_t>(pairs, slots[2])), 2, PAIR_THREADS, PAIR_SMEM, args, s);
   }
   g.a_rows = int(std::min<int64_t>(BM, (a.n + 7) / 8 * 8));
@@ -944,11 +1006,11 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.stages = plan.stages;
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   void* args[] = {&tx, &tw, &g};
-  const void* k = end == kTileStats   ? reinterpret_cast<const void*>(k_linear<false, kTileStats>)
-                  : end == kTileProbs ? reinterpret_cast<const void*>(k_linear<false, kTileProbs>)
-                  : a.transposed      ? reinterpret_cast<const void*>(k_linear<true>)
-                                      : reinterpret_cast<const void*>(k_linear<false>);
-  if (a.loss) a.loss->part_cols = BN;
+  const void* k = end == kTileStats     ? reinterpret_cast<const void*>(k_linear<false, kTileStats>)
+                  : end == kTileProbs   ? reinterpret_cast<const void*>(k_linear<false, kTileProbs>)
+                  : end == kTileTriples ? reinterpret_cast<const void*>(k_linear<true, kTileTriples>)
+                  : a.transposed        ? reinterpret_cast<const void*>(k_linear<true>)
+                                        : reinterpret_cast<const void*>(k_linear<false>);
   return launch_clusters("bq_linear_fp8", k, int(tiles), g.split, THREADS, plan.smem, args, s);
 }
 

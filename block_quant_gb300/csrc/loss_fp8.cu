@@ -8,10 +8,10 @@
 // after another; a piece's logits are made again and leave as U in fp16, which two
 // products read, with the piece of W for dX and with X for that piece of dW.
 //
-// fp16 and not bf16 or E4M3: U is in [-1, 1] and W and X are brought to a common power of two
+// fp16 and not bf16 or E4M3: U is in [-1, 1] and W and g X are brought to a common power of two
 // first, so all three keep eleven bits over the top 28 powers of two, at the rate of bf16 products;
-// what the results lose is their own rounding to bf16.  (E4M3 rows of U would make dX half as
-// expensive and 2.5 % wrong.)
+// what the results lose is their own rounding to bf16.  (E4M3 rows of U would make dX
+// half as expensive and 2.5 % wrong.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -122,31 +122,53 @@ struct PickArgs {
   Targets y;
 };
 
-// The logits of the targets, a warp each, by reading their rows of W: bound by those bytes.
+// The sum over a lane's codes (16 at 16 lane, 16 lane + 512, ..) of X's row times W's, by their scales;
+// four loads of each set out together.
+__device__ __forceinline__ float lane_dot(const uint8_t* x, const float* xs, int64_t ld_xs, const uint8_t* w, const float* ws,
+                                          int cols, int lane) {
+  float sum = 0.f;
+  for (int c0 = 16 * lane; c0 < cols; c0 += 2048) {
+    uint4 a[4], b[4];
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = c0 + 512 * e;
+      if (c >= cols) continue;
+      b[e] = __ldg(reinterpret_cast<const uint4*>(w + c));
+      a[e] = __ldg(reinterpret_cast<const uint4*>(x + c));
+      f[e] = __ldg(xs + int64_t(c >> 7) * ld_xs) * __ldg(ws + (c >> 7));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c0 + 512 * e >= cols) continue;
+      float u[16], v[16], d = 0.f;
+      decode16(a[e], u);
+      decode16(b[e], v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d = fmaf(u[i], v[i], d);
+      sum = fmaf(d, f[e], sum);
+    }
+  }
+  return sum;
+}
+
+// the logit of word v in row t, by a warp
+__device__ __forceinline__ float picked(const PickArgs& g, int64_t t, int v, int lane) {
+  return g.y.scale * warp_sum(lane_dot(g.x + t * g.ldx, g.xs + t, g.ld_xs, g.w + int64_t(v) * g.ldw,
+                                       g.ws + int64_t(v >> 7) * ((g.cols + 127) / 128), g.cols, lane));
+}
+
+// The logits of the teacher's words, a warp each, by reading their rows of W: bound by those bytes.
 __global__ void __launch_bounds__(256) k_loss_pick(const PickArgs g) {
   after_previous();
   next_may_start();
   const int lane = threadIdx.x & 31;
   const int64_t pairs = g.n * g.y.k, step = int64_t(gridDim.x) * 8;
-  const int tile_cols = (g.cols + 127) / 128;
   for (int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); p < pairs; p += step) {
     const int64_t t = p / g.y.k;
     const int i = int(p - t * g.y.k), v = g.y.id(t, i);
-    float sum = 0.f;
-    if (v >= 0) {
-      const uint8_t *x = g.x + t * g.ldx, *w = g.w + int64_t(v) * g.ldw;
-      const float* ws = g.ws + int64_t(v >> 7) * tile_cols;
-      for (int c = 16 * lane; c < g.cols; c += 512) {
-        float a[16], b[16], d = 0.f;
-        decode16(__ldg(reinterpret_cast<const uint4*>(x + c)), a);
-        decode16(__ldg(reinterpret_cast<const uint4*>(w + c)), b);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) d = fmaf(a[e], b[e], d);
-        sum = fmaf(d, __ldg(g.xs + int64_t(c >> 7) * g.ld_xs + t) * __ldg(ws + (c >> 7)), sum);
-      }
-      sum = warp_sum(sum) * g.y.scale;
-    }
-    if (lane == 0) g.out[t * g.ld_out + i] = sum;
+    const float z = v >= 0 ? picked(g, t, v, lane) : 0.f;
+    if (lane == 0) g.out[t * g.ld_out + i] = z;
   }
 }
 
@@ -154,9 +176,9 @@ struct JoinArgs {
   const float2* stats;
   const uint8_t* at;
   int64_t ld_stats, n, ld_logp;
-  float *loss, *lse, *logp;  // logp (or, of classes, loss) holds the targets' logits
-  int parts, part_cols, group;  // rows of a CTA: 1, 2, .. 32
-  Targets y;
+  float *loss, *lse, *logp;  // logp holds the targets' logits; a class's is taken here
+  int parts, group;  // group: rows of a CTA, 1, 2, .. 32
+  PickArgs pick;
 };
 
 __device__ __forceinline__ RowStats shuffled(const RowStats& a, int d) {
@@ -170,8 +192,16 @@ __global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
   after_previous();
   next_may_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Targets& y = g.pick.y;
   const int r = lane & (g.group - 1), each = 32 / g.group;
-  const int64_t row = int64_t(blockIdx.x) * g.group + r;
+  const int64_t row = int64_t(blockIdx.x) * g.group + r, t = int64_t(blockIdx.x) * g.group + warp;
+  const bool mine = warp < g.group && t < g.n;  // the row that this warp finishes
+  float z = 0.f;
+  int v = -1;
+  if (!y.teacher && mine) {
+    v = y.id(t, 0);
+    if (v >= 0) z = picked(g.pick, t, v, lane);
+  }
   RowStats a{-INFINITY, 0.f, 0};
   bool some = false;
   if (row < g.n)
@@ -195,24 +225,21 @@ __global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
   for (int d = g.group; d < 32; d <<= 1) a = joined(a, shuffled(a, d));
   if (lane < g.group) sm[warp][lane] = a.m, ss[warp][lane] = a.s, sa[warp][lane] = a.at;
   __syncthreads();
-  const int64_t t = int64_t(blockIdx.x) * g.group + warp;
-  if (warp >= g.group || t >= g.n) return;
+  if (!mine) return;
   a = {sm[lane][warp], ss[lane][warp], sa[lane][warp]};
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) a = joined(a, shuffled(a, d));
-  const int best = a.at * g.part_cols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
+  const int best = a.at * kPartCols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
   const float more = log1pf(a.s);
   if (lane == 0) g.lse[t] = a.m + more;
-  if (!g.y.teacher) {
-    const int v = g.y.id(t, 0);
-    if (lane == 0) g.loss[t] = v < 0 ? 0.f : v == best ? more : more + (a.m - g.loss[t]);
+  if (!y.teacher) {
+    if (lane == 0) g.loss[t] = v < 0 ? 0.f : v == best ? more : more + (a.m - z);
     return;
   }
   float top, log_sum, sum = 0.f;
-  const bool any = teacher_sum(g.y, t, lane, &top, &log_sum);
-  for (int i = lane; i < g.y.k; i += 32) {
-    float z;
-    const int v = g.y.kept_id(t, i, &z);
+  const bool any = teacher_sum(y, t, lane, &top, &log_sum);
+  for (int i = lane; i < y.k; i += 32) {
+    v = y.kept_id(t, i, &z);
     float* at = g.logp + t * g.ld_logp + i;
     const float logp = v < 0 ? 0.f : v == best ? -more : (*at - a.m) - more;
     *at = logp;
@@ -238,6 +265,7 @@ struct PrepArgs {
   Targets y;
   const float *xs, *ws, *lse, *dloss;
   float *off, *tops;  // off: a row's log-sum, or kNoTarget; tops: each CTA's largest scale of X and of W
+  int* target;        // a class, -1 for none
   int64_t ld_xs, n, w_tiles;
   int groups;
 };
@@ -261,7 +289,10 @@ __global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
       any |= g.y.kept_id(t, i, &z) >= 0;
     }
     any = __any_sync(0xFFFFFFFFu, any);
-    if (lane == 0) g.off[t] = any ? g.lse[t] : kNoTarget;
+    if (lane == 0) {
+      g.off[t] = any ? g.lse[t] : kNoTarget;
+      g.target[t] = g.y.teacher ? -1 : g.y.id(t, 0);
+    }
     if (!any) continue;
     const float f = g.dloss[t];
     for (int j = lane; j < g.groups; j += 32) mx = fmaxf(mx, finite_abs(g.xs[int64_t(j) * g.ld_xs + t] * f));
@@ -292,72 +323,67 @@ __device__ __forceinline__ float largest(const float* v, int count) {
   return m;
 }
 
+// fp16 rows of X, each times its loss's gradient (rows without a target: zeros, whatever they hold),
+// or of W (off NULL)
 struct HalfArgs {
   const uint8_t* codes;
   const float *scale, *off, *dloss, *tops;
   __half* out;
   float* back;  // the factor that takes the power of two back
   int64_t ldc, lds, ldo, n;
-  int cols, count;
+  int cols, count, ctas;
 };
 
-// fp16 rows: of X, each times its loss's gradient (rows without a target: zeros, whatever they
-// hold), or of the weight (WEIGHT: scales by tiles)
-template <bool WEIGHT>
-__global__ void __launch_bounds__(256) k_loss_half(const HalfArgs g) {
-  after_previous();
-  next_may_start();
+__device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
   const int e = power_for(largest(g.tops, g.count));
   const float up = ldexpf(1.f, e);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
+  if (cta == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
   const int words = g.cols / 16;
-  const int64_t items = g.n * words, step = int64_t(gridDim.x) * 256;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < items; i += step) {
+  const int64_t items = g.n * words, step = int64_t(g.ctas) * 256;
+  for (int64_t i = int64_t(cta) * 256 + threadIdx.x; i < items; i += step) {
     const int64_t t = i / words;
     const int c = 16 * int(i - t * words);
-    float f;
-    if constexpr (WEIGHT)
-      f = __ldg(g.scale + (t >> 7) * g.lds + (c >> 7));
-    else
-      f = __ldg(g.off + t) == kNoTarget ? 0.f : __ldg(g.scale + int64_t(c >> 7) * g.lds + t) * __ldg(g.dloss + t);
-    f *= up;
-    float v[16];
-    decode16(__ldg(reinterpret_cast<const uint4*>(g.codes + t * g.ldc + c)), v);
-    uint32_t o[8];
+    uint32_t o[8] = {};
+    if (!g.off || __ldg(g.off + t) != kNoTarget) {
+      const float f = up * (g.off ? __ldg(g.scale + int64_t(c >> 7) * g.lds + t) * __ldg(g.dloss + t)
+                                  : __ldg(g.scale + (t >> 7) * g.lds + (c >> 7)));
+      float v[16];
+      decode16(__ldg(reinterpret_cast<const uint4*>(g.codes + t * g.ldc + c)), v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = two16(v[2 * j] * f, v[2 * j + 1] * f, __half());
-    if (!WEIGHT && __ldg(g.off + t) == kNoTarget)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = 0;
+      for (int j = 0; j < 8; ++j) o[j] = two16(v[2 * j] * f, v[2 * j + 1] * f, __half());
+    }
     uint4* to = reinterpret_cast<uint4*>(g.out + t * g.ldo + c);
     to[0] = make_uint4(o[0], o[1], o[2], o[3]);
     to[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
+// X's (x.ctas CTAs of the launch, 0: none) and a piece of W's
+__global__ void __launch_bounds__(256) k_loss_half(const HalfArgs x, const HalfArgs w) {
+  after_previous();
+  next_may_start();
+  if (int(blockIdx.x) < x.ctas)
+    half_rows(x, int(blockIdx.x));
+  else
+    half_rows(w, int(blockIdx.x) - x.ctas);
+}
+
 struct FixArgs {
   Targets y;
-  const float *off, *logp, *loss;
+  const float *off, *logp;
   __half* u;
   int64_t ldu, ld_logp, n;
   int v0, len;
 };
 
-// U at the targets of a piece of the vocabulary: p - q by the forward pass's log-probability, which
-// keeps what is left of it where both are near 1
+// U at a teacher's words in a piece of the vocabulary: p - q by the forward pass's log-probability, which
+// keeps what is left of it where both are near 1 (a class's is put into its tile, loss_tile.h)
 __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
   __shared__ float sq[4][kMaxPairs];
   __shared__ int sid[4][kMaxPairs];
   after_previous();
   next_may_start();
   const float unit = float(1 << kProbBits);
-  if (!g.y.teacher) {
-    const int64_t t = int64_t(blockIdx.x) * 128 + threadIdx.x;
-    if (t >= g.n) return;
-    const int v = g.y.id(t, 0) - g.v0;
-    if (v >= 0 && v < g.len) g.u[t * g.ldu + v] = __float2half_rn(unit * expm1f(-g.loss[t]));
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = int64_t(blockIdx.x) * 4 + warp;
   if (t >= g.n || g.off[t] == kNoTarget) return;
@@ -380,39 +406,296 @@ __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
   }
 }
 
-// ---------------------------------------------------------------- gradient: products
-// out = A B on CTA pairs, fp16 operands and fp32 sums, 256 x 256 tiles as in the weight gradient of a
-// projection: dX's piece = U W (A: rows of U, K-major), dW's rows = U^T X (A: columns of U, MN-major).
-// Bound by the tensor cores.
+// ---------------------------------------------------------------- gradient: few tokens
+// dX of at most 42 tokens: U as the sum of three E4M3 values, whose products with W's codes are an FP8
+// projection (k_linear, transposed) of three rows a token, as many as its tile of 128 has room
+// for anyway.  It reads W as it is, once, where fp16 operands are written and read: 16 tokens of 128256
+// x 4096 take 103 us so (its bytes alone 78), and 505 by fp16 pieces.
+constexpr int kFewTokens = 42;
 
-struct ProductArgs {
+struct SplitArgs {
+  const __half* u;
+  uint8_t* codes;  // rows 3 t, 3 t + 1, 3 t + 2 of token t
+  float* scale;    // [groups][lds]
+  int64_t ldu, ldc, lds;
+  int n, len;
+};
+
+// A warp takes 128 values of a token.  The scales are powers of two, 2^4 apart: what a term leaves
+// (16 of its scales at most, half the largest step) is 256 of the next one's, and what the third leaves is below
+// 2^-12 of the value, or 2^-25 of the group's largest (half the smallest step, 2^-10, of a scale that is
+// 2^-8 of the first, the largest being 224 of the first or more).
+__global__ void __launch_bounds__(256) k_loss_split(const SplitArgs g) {
+  after_previous();
+  next_may_start();
+  const int lane = threadIdx.x & 31, groups = (g.len + 127) / 128;
+  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (i >= int64_t(g.n) * groups) return;
+  const int t = int(i / groups), j = int(i - int64_t(t) * groups), c = 128 * j + 4 * lane;
+  float v[4], top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = c + e < g.len ? __half2float(g.u[t * g.ldu + c + e]) : 0.f;
+    top = fmaxf(top, fabsf(v[e]));
+  }
+  top = warp_max(top);
+  // 2^e, e the least with top <= 448 * 2^e (top is an fp16 value: 2^-24 at least unless it is 0)
+  int e0 = top > 0.f && top <= 65504.f ? ilogbf(top) - 8 : 0;
+  if (top > ldexpf(448.f, e0)) ++e0;
+#pragma unroll
+  for (int term = 0; term < 3; ++term) {
+    const float s = top <= 65504.f ? ldexpf(1.f, e0 - 4 * term) : top, back = ldexpf(1.f, 4 * term - e0);
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint8_t q = uint8_t(__nv_cvt_float_to_fp8(v[e] * back, __NV_SATFINITE, __NV_E4M3));
+      v[e] -= __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3))) * s;
+      w |= uint32_t(q) << (8 * e);
+    }
+    const int64_t row = 3 * int64_t(t) + term;
+    if (c < g.ldc) *reinterpret_cast<uint32_t*>(g.codes + row * g.ldc + c) = w;
+    if (lane == 0) g.scale[int64_t(j) * g.lds + row] = s;
+  }
+}
+
+// ---------------------------------------------------------------- gradient: dX = U W
+// On CTA pairs, 256 x 256 tiles, fp16 operands and fp32 sums: U's rows K-major, W's words
+// MN-major.  Tiles left over after whole waves of pairs are cut into `parts` equal parts of their
+// summed index, taken in turn by all pairs, a part of every tile before the next part: 28 tiles left
+// of 256 on 76 pairs take three rounds of an eighth, not a wave.  (Cutting them into as many
+// pieces as there are pairs, each pair's at an offset of its own, balances them exactly and took longer, 828 us
+// against 705 for 4096 x 32256 x 4096: pairs at different offsets read nothing that others have read.)
+// Sums of a tile leave as shares, one per part, which pieces of the vocabulary add to; k_loss_sums
+// adds a tile's shares in order.
+//
+// W's fp16 words come from a launch before (k_loss_half).  Spreading its codes to fp16 inside
+// this kernel, by six warps between a ring of codes and the products' operands, took 1225 us where
+// this and that launch take 705 (4096 x 32256 x 4096): 250 of it the spreading, 130 its fences and cluster-wide
+// arrivals, and 815 were left without both.
+
+// Which tiles, and which parts of their k-blocks, a pair works on: its share of the whole waves'
+// tiles, then of the parts of those left.
+struct Shares {
+  int tiles, whole, parts;
+
+  __host__ __device__ int left() const { return tiles - whole; }
+  // where a tile's share of a part is kept, in tiles
+  __host__ __device__ int at(int tile, int part) const { return part == 0 ? tile : tiles + (part - 1) * left() + tile - whole; }
+  __host__ __device__ int64_t kept() const { return tiles + int64_t(parts - 1) * left(); }
+};
+
+struct DxArgs {
+  float* part;
+  const float *row_factor, *off, *back;  // back: takes back W's power of two
   __nv_bfloat16* out;
-  float* part;          // shares of the sum [splits][tiles], or NULL
-  const float* back;    // factors of out: of the launch, of the operands' powers of two, and of its rows
-  const float *row_factor, *off;
   float factor;
   int64_t ldo;
-  int m, n, k;          // rows and columns of out, summed index
-  int splits, add;      // add: to the shares as they are
-  int accumulate, bytes;
+  int m, n, k;          // tokens, columns, words
+  int add;
+  Shares sh;
   int* status;
 };
+
+// piece of work i of a pair: false after the last
+__device__ __forceinline__ bool dx_segment(const Shares& sh, int pair, int npairs, int nk, int i, int& tile, int& at, int& k0, int& k1) {
+  const int t = pair + i * npairs;
+  if (t < sh.whole) {
+    tile = at = t, k0 = 0, k1 = nk;
+    return true;
+  }
+  const int r = t - sh.whole, part = sh.left() ? r / sh.left() : sh.parts;
+  if (part >= sh.parts) return false;
+  tile = sh.whole + r - part * sh.left();
+  at = sh.at(tile, part);
+  k0 = int(int64_t(nk) * part / sh.parts), k1 = int(int64_t(nk) * (part + 1) / sh.parts);
+  return true;
+}
 
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B fp16 (0), majors in bits 15, 16
 __host__ __device__ constexpr uint32_t product_idesc(bool a_k_major) {
   return (1u << 4) | (uint32_t(!a_k_major) << 15) | (1u << 16) | (uint32_t(PN >> 3) << 17) | (uint32_t(PM >> 4) << 24);
 }
 
-__device__ __forceinline__ float row_factor(const ProductArgs& g, int row) {
-  const float f = g.factor;
-  if (!g.row_factor || row >= g.m) return f;
-  return f * __ldg(g.row_factor + row);
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+    k_loss_dx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const DxArgs g) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  __shared__ __align__(8) uint64_t bars[2 * DW_STAGES + 4];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t bar0 = smem_addr(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(DW_STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * DW_STAGES + 2 + b); };
+
+  const int rank = int(cluster_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int mt = (g.m + PM - 1) / PM, nt = (g.n + PN - 1) / PN;
+  const int nk = (g.k + DK - 1) / DK;
+  const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < DW_STAGES; ++s) {
+      mbar_init(full_bar(s), 1);   // the leader's expect_tx
+      mbar_init(empty_bar(s), 1);  // the leader's commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), 2 * PEPI);  // the epilogue warps of both CTAs
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  after_previous();
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  next_may_start();
+
+  int tile, at, k0, k1;
+  if (warp == 0) {
+    // ---------------- TMA producer (both CTAs: this CTA's halves)
+    uint32_t it = 0;
+    bool ok = true;
+    for (int i = 0; ok && dx_segment(g.sh, pair, npairs, nk, i, tile, at, k0, k1); ++i) {
+      int bm, bn;
+      banded_tile(tile, mt, nt, kBand, bm, bn);
+      const int ma = bm * PM + 128 * rank, nb = bn * PN + 128 * rank;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(empty_bar(s), ((it / DW_STAGES) & 1u) ^ 1u, g.status, 61);
+        if (!ok) break;
+        const uint32_t a_dst = base + uint32_t(s) * PSTAGE_BYTES, b_dst = a_dst + HALF_STAGE;
+        const uint32_t fb = map_rank(full_bar(s), 0);
+        if (elect_one()) {
+          if (rank == 0) mbar_expect_tx(full_bar(s), 2 * PSTAGE_BYTES);
+          tma_load_2d_pair(a_dst, &tmA, kb * DK * 2, ma, fb);  // (the map counts bytes)
+          tma_load_3d_pair(b_dst, &tmB, kb * DK, nb / 64, fb);
+        }
+        __syncwarp();
+      }
+    }
+    // drain (leader): the pair's last copies have landed; the peer waits for this at
+    // the closing cluster barrier
+    if (rank == 0)
+      for (uint32_t d = it > uint32_t(DW_STAGES) ? it - DW_STAGES : 0; d < it; ++d)
+        mbar_wait(full_bar(int(d % DW_STAGES)), (d / DW_STAGES) & 1u, g.status, 62);
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer (leader)
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int i = 0; ok && dx_segment(g.sh, pair, npairs, nk, i, tile, at, k0, k1); ++i) {
+      if (k0 == k1) continue;
+      const int buf = int(tc & 1u);
+      if (tc >= 2) ok = mbar_wait_cluster_relaxed(tempty_bar(buf), ((tc >> 1) & 1u) ^ 1u, g.status, 63);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = int(it % DW_STAGES);
+        ok = mbar_wait(full_bar(s), (it / DW_STAGES) & 1u, g.status, 64);
+        if (!ok) break;
+        tc_fence_after();
+        // 16 words a product: U's rows 32 bytes on, W's 2 KB (64-column chunks 8 KB apart)
+        const uint32_t a_addr = base + uint32_t(s) * PSTAGE_BYTES;
+        const uint64_t ad = sdesc(a_addr, 16, 1024), bd = sdesc(a_addr + HALF_STAGE, CHUNK, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < DK / 16; ++kk)
+            mma_bf16_pair(tmem + uint32_t(buf) * PN, ad + uint64_t(2 * kk), bd + uint64_t(128 * kk),
+                          product_idesc(true), kb != k0 || kk != 0 ? 1u : 0u);
+          mma_commit_pair(empty_bar(s));
+          if (kb + 1 == k1) mma_commit_pair(tfull_bar(buf));
+        }
+        __syncwarp();
+      }
+      if (ok) ++tc;
+    }
+    // every product issued here has finished before the accumulators are freed
+    if (tc > 0 && ok) mbar_wait(tfull_bar(int((tc - 1) & 1u)), ((tc - 1) >> 1) & 1u, g.status, 66);
+  } else if (warp >= 4) {
+    // ---------------- shares (both CTAs: this CTA's 128 rows)
+    const int q = warp & 3, part = (warp - 4) >> 2;
+    const uint32_t te0 = map_rank(tempty_bar(0), 0);
+    uint32_t tc = 0;
+    for (int i = 0; dx_segment(g.sh, pair, npairs, nk, i, tile, at, k0, k1); ++i) {
+      if (k0 == k1 && g.add) continue;
+      int bm, bn;
+      banded_tile(tile, mt, nt, kBand, bm, bn);
+      const int row0 = bm * PM + 128 * rank + 32 * q, c0 = bn * PN + PCOLS * part;
+      uint32_t r[PCOLS];
+      if (k0 < k1) {
+        const uint32_t buf = tc & 1u;
+        if (!mbar_wait(tfull_bar(int(buf)), (tc >> 1) & 1u, g.status, 65)) break;
+        tc_fence_after();
+        const uint32_t from = tmem + (uint32_t(32 * q) << 16) + buf * PN + uint32_t(PCOLS * part);
+        tmem_ld32(from, r);
+        tmem_ld32(from + 32, r + 32);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(te0 + 8u * buf);
+        ++tc;
+      } else {  // (no k-block of this piece: the share begins as zeros)
+#pragma unroll
+        for (int j = 0; j < PCOLS; ++j) r[j] = 0u;
+      }
+      if (row0 >= g.m || c0 >= g.n) continue;
+      float4* o = reinterpret_cast<float4*>(g.part) + share_at(at, rank, warp - 4) + lane;
+#pragma unroll
+      for (int j = 0; j < PCOLS / 4; ++j) {
+        float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
+                               __uint_as_float(r[4 * j + 3]));
+        if (g.add) {
+          const float4 x = o[32 * j];
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        o[32 * j] = v;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+static_assert(2 * DW_SMEM > kSmemOfSm && DW_SMEM >= kClusterSmemLeast, "a pair's CTA has its SM's tensor memory to itself");
+
+// 16 values of a row of a sum of shares, rounded to out (+ out)
+__device__ __forceinline__ void put16(const float* x, __nv_bfloat16* o, bool aligned, bool accumulate) {
+  alignas(16) __nv_bfloat16 y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = __float2bfloat16_rn(accumulate ? x[e] + __bfloat162float(o[e]) : x[e]);
+  if (aligned) {
+    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
+    *reinterpret_cast<uint4*>(o + 8) = *reinterpret_cast<const uint4*>(y + 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = y[e];
+  }
 }
 
-template <bool A_KMAJOR>
+// ---------------------------------------------------------------- gradient: dW = U^T X
+// The weight gradient of a projection (k_dw_pair) with fp16 operands, out times a factor: bound by
+// the tensor cores, for few tokens by the stores.
+
+struct DwPieceArgs {
+  __nv_bfloat16* out;
+  float* part;        // shares of the sum [splits][tiles], or NULL
+  const float* back;  // takes back X's power of two
+  float factor;
+  int64_t ldo;
+  int m, n, k;        // words, columns, tokens
+  int splits, accumulate, bytes;
+  int* status;
+};
+
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
-    k_loss_product(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmO, const ProductArgs g) {
+    k_loss_dw(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmO, const DwPieceArgs g) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -471,10 +754,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         const uint32_t fb = map_rank(full_bar(s), 0);
         if (elect_one()) {
           if (rank == 0) mbar_expect_tx(full_bar(s), 2 * PSTAGE_BYTES);
-          if (A_KMAJOR)
-            tma_load_2d_pair(a_dst, &tmA, kb * DK * 2, ma, fb);  // (the map counts bytes)
-          else
-            tma_load_3d_pair(a_dst, &tmA, kb * DK, ma / 64, fb);
+          tma_load_3d_pair(a_dst, &tmA, kb * DK, ma / 64, fb);
           tma_load_3d_pair(b_dst, &tmB, kb * DK, nb / 64, fb);
         }
         __syncwarp();
@@ -501,16 +781,14 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         ok = mbar_wait(full_bar(s), (it / DW_STAGES) & 1u, g.status, 54);
         if (!ok) break;
         tc_fence_after();
-        // 16 of the summed index a product: MN-major 2 KB on (64-column chunks 8 KB apart), K-major
-        // 32 bytes on (rows 128 bytes apart)
+        // 64-column chunks 8 KB apart, 16 tokens (2 KB) a product
         const uint32_t a_addr = base + uint32_t(s) * PSTAGE_BYTES;
-        const uint64_t ad = A_KMAJOR ? sdesc(a_addr, 16, 1024) : sdesc(a_addr, CHUNK, 1024);
-        const uint64_t bd = sdesc(a_addr + HALF_STAGE, CHUNK, 1024);
+        const uint64_t ad = sdesc(a_addr, CHUNK, 1024), bd = sdesc(a_addr + HALF_STAGE, CHUNK, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < DK / 16; ++kk)
-            mma_bf16_pair(tmem + uint32_t(buf) * PN, ad + uint64_t((A_KMAJOR ? 2 : 128) * kk), bd + uint64_t(128 * kk),
-                          product_idesc(A_KMAJOR), kb != k0 || kk != 0 ? 1u : 0u);
+            mma_bf16_pair(tmem + uint32_t(buf) * PN, ad + uint64_t(128 * kk), bd + uint64_t(128 * kk),
+                          product_idesc(false), kb != k0 || kk != 0 ? 1u : 0u);
           mma_commit_pair(empty_bar(s));
           if (kb + 1 == k1) mma_commit_pair(tfull_bar(buf));
         }
@@ -546,21 +824,13 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         float4* o = reinterpret_cast<float4*>(g.part) + share_at(t, rank, warp - 4) + lane;
         if (row0 < g.m && c0 < g.n)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float4 v = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]), __uint_as_float(r[4 * j + 2]),
-                                   __uint_as_float(r[4 * j + 3]));
-            if (g.add) {
-              const float4 x = o[32 * j];
-              v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            }
-            o[32 * j] = v;
-          }
+          for (int j = 0; j < 16; ++j)
+            o[32 * j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                    __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
         continue;
       }
-      const float f = row_factor(g, row);
-      const bool none = g.off && row < g.m && __ldg(g.off + row) == kNoTarget;
 #pragma unroll
-      for (int j = 0; j < 64; ++j) r[j] = none ? 0u : __float_as_uint(__uint_as_float(r[j]) * f * back);
+      for (int j = 0; j < 64; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * g.factor * back);
       if (g.accumulate && row < g.m) {
         const __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;
 #pragma unroll
@@ -582,14 +852,36 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tmem_dealloc_pair(tmem, kPairTmem);
   }
 }
-static_assert(2 * DW_SMEM > kSmemOfSm && DW_SMEM >= kClusterSmemLeast, "a pair's CTA has its SM's tensor memory to itself");
 
-// out = the shares' sum in order, times its factors (+ out): a warp takes 32 rows x 16 columns
-__global__ void __launch_bounds__(256) k_loss_sum(const ProductArgs g) {
-  after_previous();
-  next_may_start();
+// dx = the shares' sum in order, times its row's factor: warp i takes 32 rows x 16 columns
+__device__ __forceinline__ void sum_dx(const DxArgs& g, int64_t i) {
+  const int mt = (g.m + PM - 1) / PM, nt = (g.n + PN - 1) / PN;
+  const int lane = threadIdx.x & 31, h = int(i & 3), w = int(i >> 2) & (PEPI - 1), rank = int(i >> 6) & 1, t = int(i >> 7);
+  int bm, bn;
+  banded_tile(t, mt, nt, kBand, bm, bn);
+  const int row = bm * PM + 128 * rank + 32 * (w & 3) + lane, c0 = bn * PN + 64 * (w >> 2) + 16 * h;
+  if (row >= g.m || c0 >= g.n) return;
+  const int count = t < g.sh.whole ? 1 : g.sh.parts;
+  float4 v[4] = {};
+  for (int k = 0; k < count; ++k) {
+    const float4* p = reinterpret_cast<const float4*>(g.part) + share_at(g.sh.at(t, k), rank, w) + 128 * h + lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = p[32 * j];
+      v[j].x += x.x, v[j].y += x.y, v[j].z += x.z, v[j].w += x.w;
+    }
+  }
+  const bool none = __ldg(g.off + row) == kNoTarget;  // (whatever W holds)
+  const float f = g.factor * __ldg(g.row_factor + row), f2 = __ldg(g.back);
+  float* x = reinterpret_cast<float*>(v);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = none ? 0.f : x[e] * f * f2;
+  put16(x, g.out + int64_t(row) * g.ldo + c0, g.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0, false);
+}
+
+// out = the shares' sum in order, times its factors (+ out): warp i takes 32 rows x 16 columns
+__device__ __forceinline__ void sum_dw(const DwPieceArgs& g, int64_t i) {
   const int mt = (g.m + PM - 1) / PM, nt = (g.n + PN - 1) / PN, ntiles = mt * nt;
-  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, h = int(i & 3), w = int(i >> 2) & (PEPI - 1), rank = int(i >> 6) & 1, t = int(i >> 7);
   int bm, bn;
   banded_tile(t, mt, nt, kBand, bm, bn);
@@ -603,23 +895,22 @@ __global__ void __launch_bounds__(256) k_loss_sum(const ProductArgs g) {
       const float4 x = p[32 * j];
       v[j].x += x.x, v[j].y += x.y, v[j].z += x.z, v[j].w += x.w;
     }
-  const float f = row_factor(g, row), back = __ldg(g.back);
-  const bool none = g.off && __ldg(g.off + row) == kNoTarget;
-  const float* x = reinterpret_cast<const float*>(v);
-  __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;  // (the width is a multiple of 16)
-  alignas(16) __nv_bfloat16 y[16];
+  const float back = __ldg(g.back);
+  float* x = reinterpret_cast<float*>(v);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float d = none ? 0.f : x[e] * f * back;
-    y[e] = __float2bfloat16_rn(g.accumulate ? d + __bfloat162float(o[e]) : d);
-  }
-  if (g.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0) {
-    *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(y);
-    *reinterpret_cast<uint4*>(o + 8) = *reinterpret_cast<const uint4*>(y + 8);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = y[e];
-  }
+  for (int e = 0; e < 16; ++e) x[e] = x[e] * g.factor * back;
+  put16(x, g.out + int64_t(row) * g.ldo + c0, g.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0, g.accumulate);
+}
+
+// the first dx_ctas CTAs: dx's
+__global__ void __launch_bounds__(256) k_loss_sums(const DxArgs dx, const DwPieceArgs dw, int dx_ctas) {
+  after_previous();
+  next_may_start();
+  const int cta = int(blockIdx.x), warp = int(threadIdx.x >> 5);
+  if (cta < dx_ctas)
+    sum_dx(dx, int64_t(cta) * 8 + warp);
+  else
+    sum_dw(dw, int64_t(cta - dx_ctas) * 8 + warp);
 }
 
 // ---------------------------------------------------------------- host
@@ -636,7 +927,7 @@ struct ForwardWs {
 
 ForwardWs forward_ws(int64_t n, int64_t rows, int64_t cols) {
   ForwardWs p;
-  const size_t parts = size_t((rows + PCOLS - 1) / PCOLS);
+  const size_t parts = size_t((rows + kPartCols - 1) / kPartCols);
   p.scales = kStatus;
   p.stats = p.scales + scale_bytes(n, cols);
   p.at = p.stats + up(parts * size_t(n) * 8);
@@ -646,9 +937,11 @@ ForwardWs forward_ws(int64_t n, int64_t rows, int64_t cols) {
 
 struct GradWs {
   int64_t piece;      // words of a piece of the vocabulary, a multiple of 256
-  int pieces, dx_splits;
-  int64_t ldh;        // pitch of the fp16 rows of X and W
-  size_t scales, tops, back, off, x, u, w, dx, dw, bytes;
+  int pieces;
+  int64_t ldh;        // pitch of the fp16 rows of X
+  bool few;           // dx by three E4M3 terms of U, whose codes and scales then lie at w and dx
+  Shares dx_shares;
+  size_t scales, tops, back, off, target, x, u, w, dx, dw, bytes;
 };
 
 int64_t piece_len(const GradWs& p, int64_t rows, int i) { return std::min(p.piece, rows - i * p.piece); }
@@ -656,24 +949,43 @@ int64_t piece_len(const GradWs& p, int64_t rows, int i) { return std::min(p.piec
 // U and the piece of W in fp16 take 256 MB each at most, unless 256 words do not fit
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
+// The tiles left over after whole waves in the parts that cost least: a round of parts takes 0.29 us a k-block (as
+// a projection's weight gradient), and a share is stored and added up.
+Shares dx_shares(int64_t n, int64_t cols, int64_t piece) {
+  Shares sh;
+  const int pairs = cluster_slots()[2], nk = int((piece + DK - 1) / DK);
+  sh.tiles = int(((n + PM - 1) / PM) * ((cols + PN - 1) / PN));
+  sh.whole = sh.tiles / pairs * pairs;
+  sh.parts = 1;
+  const int left = sh.left();
+  double least = 0;
+  for (int parts = 1; left && parts <= std::min(nk, 24); ++parts) {
+    const double us = 0.29 * ((nk + parts - 1) / parts) * ((left * parts + pairs - 1) / pairs) + parts * (0.25 + 0.045 * left);
+    if (parts == 1 || us < least) least = us, sh.parts = parts;
+  }
+  return sh;
+}
+
 GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
   GradWs p;
   p.ldh = up_to(cols, 64);
-  const int64_t most = std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>({n, p.ldh, 1})) / 256 * 256);
+  p.few = n <= kFewTokens && n * rows * 2 <= kPieceBytes;
+  const int64_t most = p.few ? up_to(rows, 256)
+                              : std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>({n, p.ldh, 1})) / 256 * 256);
   const int64_t pieces = (rows + most - 1) / most;
   p.piece = up_to((rows + pieces - 1) / pieces, 256);
   p.pieces = int((rows + p.piece - 1) / p.piece);
-  p.dx_splits = dw_splits(p.piece, n, cols);
+  p.dx_shares = dx_shares(n, cols, p.piece);
   p.scales = kStatus;
   p.tops = p.scales + scale_bytes(n, cols);
   p.back = p.tops + up(2 * kPrepCtas * 4);
   p.off = p.back + 256;
-  p.x = p.off + up(size_t(n) * 4);
+  p.target = p.off + up(size_t(n) * 4);
+  p.x = p.target + up(size_t(n) * 4);
   p.u = p.x + up(size_t(n) * size_t(p.ldh) * 2);
   p.w = p.u + up(size_t(n) * size_t(p.piece) * 2);
-  p.dx = p.w + up(size_t(p.piece) * size_t(p.ldh) * 2);
-  const bool shares = p.pieces > 1 || p.dx_splits > 1;
-  p.dw = p.dx + (shares ? size_t(p.dx_splits) * size_t((n + PM - 1) / PM) * size_t((cols + PN - 1) / PN) * PM * PN * 4 : 0);
+  p.dx = p.w + up(p.few ? size_t(3 * n) * size_t(p.piece) : size_t(p.piece) * size_t(p.ldh) * 2);
+  p.dw = p.dx + up(p.few ? size_t(p.piece / 128) * size_t(up_to(3 * n, 4)) * 4 : size_t(p.dx_shares.kept()) * PM * PN * 4);
   size_t dw = 0;
   for (int i : {0, p.pieces - 1}) {
     const int64_t len = piece_len(p, rows, i);
@@ -694,23 +1006,6 @@ unsigned ctas_for(int64_t items, int64_t each, int64_t most) {
   return unsigned(std::max<int64_t>(1, std::min<int64_t>(most, (items + each - 1) / each)));
 }
 
-// sum_splits: shares to add up after the product, 0 to leave them
-int launch_product(bool dx, const CUtensorMap& ta, const CUtensorMap& tb, ProductArgs g, int sum_splits, cudaStream_t s) {
-  const char* what = dx ? "loss gradient (dx)" : "loss gradient (dw)";
-  CUtensorMap to = tb;  // (not read by plain stores and shares)
-  if (!g.part && g.bytes == 16)
-    if (int rc = encode_map_bf16_out(&to, g.out, g.n, g.m, g.ldo, 64)) return rc;
-  const int64_t tiles = int64_t((g.m + PM - 1) / PM) * ((g.n + PN - 1) / PN), total = tiles * g.splits;
-  CUtensorMap a = ta, b = tb;
-  void* args[] = {&a, &b, &to, &g};
-  const void* k = dx ? reinterpret_cast<const void*>(k_loss_product<true>) : reinterpret_cast<const void*>(k_loss_product<false>);
-  if (int rc = launch_clusters(what, k, int(std::min<int64_t>(total, cluster_slots()[2])), 2, PAIR_THREADS, DW_SMEM, args, s)) return rc;
-  if (!g.part || !sum_splits) return BQ_OK;
-  g.splits = sum_splits;
-  launch_after(k_loss_sum, unsigned(tiles * 16), 256, 0, s, g);
-  return check(what);
-}
-
 }  // namespace
 
 size_t loss_bytes(int64_t n, int64_t rows, int64_t cols) { return forward_ws(n, rows, cols).bytes; }
@@ -722,11 +1017,13 @@ int launch_loss(const LossArgs& a, void* ws, void* stream) {
   const ForwardWs p = forward_ws(a.n, a.rows, a.cols);
   PickArgs pick;
   pick.x = a.x, pick.w = a.w, pick.xs = a.x_scale, pick.ws = a.w_scale;
-  pick.out = a.teacher ? a.logp : a.loss, pick.ld_out = a.teacher ? a.ld_logp : 1;
+  pick.out = a.logp, pick.ld_out = a.ld_logp;
   pick.ldx = a.ldx, pick.ld_xs = a.ld_xs, pick.ldw = a.ldw, pick.n = a.n, pick.cols = a.cols;
   pick.y = targets(a);
-  launch_after(k_loss_pick, ctas_for(a.n * a.k, 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
-  if (int rc = check("loss (targets)")) return rc;
+  if (a.teacher) {
+    launch_after(k_loss_pick, ctas_for(a.n * a.k, 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
+    if (int rc = check("loss (targets)")) return rc;
+  }
   LossTile tile = {};
   tile.end = kTileStats, tile.zscale = a.scale;
   tile.stats = reinterpret_cast<float2*>(base + p.stats), tile.at = base + p.at, tile.ld_stats = a.n;
@@ -736,10 +1033,10 @@ int launch_loss(const LossArgs& a, void* ws, void* stream) {
   JoinArgs j;
   j.stats = tile.stats, j.at = tile.at, j.ld_stats = a.n, j.n = a.n, j.ld_logp = a.ld_logp;
   j.loss = a.loss, j.lse = a.lse, j.logp = a.logp;
-  j.part_cols = tile.part_cols, j.parts = (a.rows + tile.part_cols - 1) / tile.part_cols;
+  j.parts = (a.rows + kPartCols - 1) / kPartCols;
   j.group = 1;
   while (j.group < 32 && a.n > int64_t(j.group) * sm_count()) j.group *= 2;
-  j.y = pick.y;
+  j.pick = pick;
   launch_after(k_loss_join, unsigned((a.n + j.group - 1) / j.group), 1024, 0, s, j);
   return check("loss (join)");
 }
@@ -748,8 +1045,8 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   static OncePerDevice once;
   if (int rc = once.run(current_device(), [] {
-        if (cudaFuncSetAttribute(k_loss_product<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(k_loss_product<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
+        if (cudaFuncSetAttribute(k_loss_dx, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(k_loss_dw, cudaFuncAttributeMaxDynamicSharedMemorySize, DW_SMEM) != cudaSuccess)
           return check("loss gradient (shared memory attribute)");
         return int(BQ_OK);
       }))
@@ -759,23 +1056,24 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   int* status = static_cast<int*>(ws);
   float *tops = reinterpret_cast<float*>(base + p.tops), *back = reinterpret_cast<float*>(base + p.back);
   float* off = reinterpret_cast<float*>(base + p.off);
+  int* target = reinterpret_cast<int*>(base + p.target);
   auto *x16 = reinterpret_cast<__half*>(base + p.x), *u = reinterpret_cast<__half*>(base + p.u), *w16 = reinterpret_cast<__half*>(base + p.w);
   const int64_t tile_cols = (a.cols + 127) / 128;
 
   PrepArgs prep;
   prep.y = targets(a);
-  prep.xs = a.x_scale, prep.ws = a.w_scale, prep.lse = a.lse, prep.dloss = a.dloss, prep.off = off, prep.tops = tops;
+  prep.xs = a.x_scale, prep.ws = a.w_scale, prep.lse = a.lse, prep.dloss = a.dloss, prep.off = off, prep.tops = tops, prep.target = target;
   prep.ld_xs = a.ld_xs, prep.n = a.n, prep.w_tiles = tile_cols * ((a.rows + 127) / 128), prep.groups = int(tile_cols);
   const int prep_ctas = int(ctas_for(std::max<int64_t>(a.n * 32, prep.w_tiles), 256, kPrepCtas));
   launch_after(k_loss_prep, unsigned(prep_ctas), 256, 0, s, prep);
   if (int rc = check("loss gradient (targets)")) return rc;
 
   const int64_t half_ctas = int64_t(sm_count()) * 16;
-  CUtensorMap tx, tw, tu;
+  CUtensorMap tx, tw, tu, to;
+  HalfArgs hx = {}, hw = {};
   if (a.dw) {
-    HalfArgs h{a.x, a.x_scale, off, a.dloss, tops, x16, back, a.ldx, a.ld_xs, p.ldh, a.n, a.cols, prep_ctas};
-    launch_after(k_loss_half<false>, ctas_for(a.n * (a.cols / 16), 256, half_ctas), 256, 0, s, h);
-    if (int rc = check("loss gradient (rows)")) return rc;
+    hx = {a.x, a.x_scale, off, a.dloss, tops, x16, back, a.ldx, a.ld_xs, p.ldh, a.n, a.cols, prep_ctas,
+          int(ctas_for(a.n * (a.cols / 16), 256, half_ctas))};
     if (int rc = encode_map_chunks(&tx, x16, a.cols, a.n, p.ldh, 2)) return rc;
   }
   const float unscale = a.scale * (1.f / float(1 << kProbBits));
@@ -783,38 +1081,74 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
     const int64_t v0 = i * p.piece, len = piece_len(p, a.rows, i);
     const uint8_t* w = a.w + v0 * a.ldw;
     const float* w_scale = a.w_scale + v0 / 128 * tile_cols;
-    if (a.dx) {
-      HalfArgs h{w, w_scale, nullptr, nullptr, tops + kPrepCtas, w16, back + 1, a.ldw, tile_cols, p.ldh, len, a.cols, prep_ctas};
-      launch_after(k_loss_half<true>, ctas_for(len * (a.cols / 16), 256, half_ctas), 256, 0, s, h);
-      if (int rc = check("loss gradient (weight)")) return rc;
+    if (a.dx && !p.few)
+      hw = {w, w_scale, nullptr, nullptr, tops + kPrepCtas, w16, back + 1, a.ldw, tile_cols, p.ldh, len, a.cols, prep_ctas,
+            int(ctas_for(len * (a.cols / 16), 256, half_ctas))};
+    if (hx.ctas + hw.ctas > 0) {
+      launch_after(k_loss_half, unsigned(hx.ctas + hw.ctas), 256, 0, s, hx, hw);
+      if (int rc = check("loss gradient (operands)")) return rc;
+      hx.ctas = 0;
     }
     LossTile tile = {};
     tile.end = kTileProbs, tile.zscale = a.scale, tile.lse = off;
+    tile.target = target, tile.loss = a.loss, tile.first = int(v0);
     LinearArgs l{a.x, a.x_scale, w, w_scale, u, a.ldx, a.ld_xs, a.ldw, p.piece, a.n, int(len), a.cols, 0, status,
                  reinterpret_cast<float*>(base + p.scales), &tile};
     if (int rc = launch_linear_fp8(l, stream)) return rc;
-    FixArgs f{prep.y, off, a.logp, a.loss, u, p.piece, a.ld_logp, a.n, int(v0), int(len)};
-    launch_after(k_loss_fix, unsigned((a.n + (a.teacher ? 3 : 127)) / (a.teacher ? 4 : 128)), 128, 0, s, f);
-    if (int rc = check("loss gradient (targets of a piece)")) return rc;
-    if (a.dx) {
+    if (a.teacher) {
+      FixArgs f{prep.y, off, a.logp, u, p.piece, a.ld_logp, a.n, int(v0), int(len)};
+      launch_after(k_loss_fix, unsigned((a.n + 3) / 4), 128, 0, s, f);
+      if (int rc = check("loss gradient (targets of a piece)")) return rc;
+    }
+    DxArgs gx = {};
+    DwPieceArgs gw = {};
+    unsigned dx_sums = 0, dw_sums = 0;
+    if (a.dx && p.few) {
+      auto* codes = reinterpret_cast<uint8_t*>(base + p.w);
+      auto* scale = reinterpret_cast<float*>(base + p.dx);
+      const int64_t lds = up_to(3 * a.n, 4), ldc = up_to(len, 16);
+      SplitArgs f{u, codes, scale, p.piece, ldc, lds, int(a.n), int(len)};
+      launch_after(k_loss_split, unsigned((a.n * ((len + 127) / 128) + 7) / 8), 256, 0, s, f);
+      if (int rc = check("loss gradient (few tokens)")) return rc;
+      LossTile triples = {};
+      triples.end = kTileTriples, triples.zscale = unscale, triples.lse = off, triples.factor = a.dloss;
+      LinearArgs d{codes, scale, w, w_scale, a.dx, ldc, lds, a.ldw, a.ld_dx, 3 * a.n, int(len), a.cols, 1, status, nullptr, &triples};
+      if (int rc = launch_linear_fp8(d, stream)) return rc;
+    } else if (a.dx) {
       if (int rc = encode_map_codes(&tu, u, 2 * len, a.n, 2 * p.piece, 128)) return rc;
       if (int rc = encode_map_chunks(&tw, w16, a.cols, len, p.ldh, 2)) return rc;
-      ProductArgs g = {};
-      g.out = static_cast<__nv_bfloat16*>(a.dx), g.ldo = a.ld_dx, g.m = int(a.n), g.n = a.cols, g.k = int(len);
-      g.part = p.pieces > 1 || p.dx_splits > 1 ? reinterpret_cast<float*>(base + p.dx) : nullptr;
-      g.back = back + 1, g.row_factor = a.dloss, g.off = off, g.factor = unscale;
-      g.splits = std::min(p.dx_splits, (g.k + DK - 1) / DK), g.add = i > 0, g.bytes = store_bytes(a.dx, a.ld_dx, a.cols), g.status = status;
-      if (int rc = launch_product(true, tu, tw, g, i + 1 == p.pieces ? p.dx_splits : 0, s)) return rc;
+      DxArgs& g = gx;
+      g.part = reinterpret_cast<float*>(base + p.dx), g.row_factor = a.dloss, g.off = off, g.back = back + 1;
+      g.out = static_cast<__nv_bfloat16*>(a.dx), g.factor = unscale, g.ldo = a.ld_dx;
+      g.m = int(a.n), g.n = a.cols, g.k = int(len);
+      g.add = i > 0, g.sh = p.dx_shares, g.status = status;
+      void* args[] = {&tu, &tw, &g};
+      const int pairs = std::min(cluster_slots()[2], g.sh.whole ? g.sh.tiles : g.sh.left() * g.sh.parts);
+      if (int rc = launch_clusters("loss gradient (dx)", reinterpret_cast<const void*>(k_loss_dx), pairs, 2, PAIR_THREADS, DW_SMEM, args, s))
+        return rc;
+      if (i + 1 == p.pieces) dx_sums = unsigned(g.sh.tiles) * 16;
     }
     if (a.dw) {
       if (int rc = encode_map_chunks(&tu, u, len, a.n, p.piece, 2)) return rc;
-      ProductArgs g = {};
+      DwPieceArgs& g = gw;
       g.out = static_cast<__nv_bfloat16*>(a.dw) + v0 * a.ld_dw, g.ldo = a.ld_dw, g.m = int(len), g.n = a.cols, g.k = int(a.n);
       g.splits = dw_splits(a.n, len, a.cols);
       g.part = g.splits > 1 ? reinterpret_cast<float*>(base + p.dw) : nullptr;
       g.back = back, g.factor = unscale, g.accumulate = a.accumulate;
       g.bytes = store_bytes(g.out, a.ld_dw, a.cols), g.status = status;
-      if (int rc = launch_product(false, tu, tx, g, g.splits, s)) return rc;
+      to = tx;  // (not read by plain stores and shares)
+      if (!g.part && g.bytes == 16)
+        if (int rc = encode_map_bf16_out(&to, g.out, a.cols, len, a.ld_dw, 64)) return rc;
+      const int64_t tiles = int64_t((g.m + PM - 1) / PM) * ((g.n + PN - 1) / PN);
+      void* args[] = {&tu, &tx, &to, &g};
+      if (int rc = launch_clusters("loss gradient (dw)", reinterpret_cast<const void*>(k_loss_dw),
+                                   int(std::min<int64_t>(tiles * g.splits, cluster_slots()[2])), 2, PAIR_THREADS, DW_SMEM, args, s))
+        return rc;
+      if (g.part) dw_sums = unsigned(tiles * 16);
+    }
+    if (dx_sums + dw_sums > 0) {
+      launch_after(k_loss_sums, dx_sums + dw_sums, 256, 0, s, gx, gw, int(dx_sums));
+      if (int rc = check("loss gradient (sums)")) return rc;
     }
   }
   return BQ_OK;

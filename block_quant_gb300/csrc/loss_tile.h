@@ -46,6 +46,9 @@ __device__ __forceinline__ float scaled_prob(float z, float lse) {
   return lse == kNoTarget ? 0.f : ex2(fmaf(z - lse, kLog2e, float(kProbBits)));
 }
 
+// 2^kProbBits (p - 1) of a class whose loss is -log p, precise where p is near 1
+__device__ __forceinline__ float scaled_rest(float loss) { return float(1 << kProbBits) * expm1f(-loss); }
+
 // of a lane's row: N logits' products, of which the first `cols` count
 template <int N>
 __device__ __forceinline__ void lane_stats(float* z, int cols, float zscale, bool on, float2* stats, uint8_t* at) {
@@ -75,19 +78,20 @@ __device__ __forceinline__ void lane_stats(float* z, int cols, float zscale, boo
   }
 }
 
-// of a warp's row: the products of columns lane + 32 j < cols
+// of a warp's row: the products of columns lane + 32 j < cols, j < J
+template <int J>
 __device__ __forceinline__ void row_stats(const float* v, int cols, float zscale, int lane, float2* stats, uint8_t* at) {
-  float z[4], m = -INFINITY, s = 0.f;
+  float z[J], m = -INFINITY, s = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     z[j] = lane + 32 * j < cols ? v[j] * zscale : -INFINITY;
     m = fmaxf(m, z[j]);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-  int count = 0, where = 128;
+  int count = 0, where = 255;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     if (z[j] == m)
       ++count, where = min(where, lane + 32 * j);
     else

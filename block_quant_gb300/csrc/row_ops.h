@@ -59,16 +59,23 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
 int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
                      int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
 // What k_linear and k_linear_pair do with a tile of products: rows of out, or, for a loss
-// (loss_fp8.cu), statistics of each row's part of the tile or its scaled probabilities
-enum TileEnd { kTileOut = 0, kTileStats = 1, kTileProbs = 2 };
+// (loss_fp8.cu), statistics of each row's part of the tile, its scaled probabilities, or the sum of
+// three rows of products, a token's
+enum TileEnd { kTileOut = 0, kTileStats = 1, kTileProbs = 2, kTileTriples = 3 };
+constexpr int kPartCols = 64;  // of statistics
 struct LossTile {
   int end;
   float zscale;      // a logit is zscale times the product
   float2* stats;     // kTileStats: [part][ld_stats] and
   uint8_t* at;       // the largest logit's column in its part
   int64_t ld_stats;
-  const float* lse;  // kTileProbs: one a row
-  int part_cols;     // set by the launch: columns of a part
+  // kTileProbs: each row's log-sum, its class (-1: none) and loss, and the first word's number
+  const float* lse;
+  const int* target;
+  const float* loss;
+  int first;
+  // kTileTriples (transposed, at most 42 tokens): each token's factor beside zscale, lse as above
+  const float* factor;
 };
 
 // FP8 projections (linear_fp8.cu)

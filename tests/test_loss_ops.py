@@ -203,7 +203,12 @@ class Head:
             du = d[:, None] * (p + u) + 2.0 ** -19 * O.weights_of(self.pairs, self.rows)
         du = g[:, None] * (du + 2.0 ** -39)
         if dx is not None:
-            by = du @ np.abs(self.w64) + (2.2 * H + (self.rows + 8) * 2.0 ** -23) * size_x
+            # at most 42 tokens: u as three E4M3 terms, off by 2^-12 of itself and 2^-25 of its 128 words' largest
+            few = np.zeros_like(u)
+            if self.n <= 42:
+                for j in range(0, self.rows, 128):
+                    few[:, j:j + 128] = 2.0 ** -25 * u[:, j:j + 128].max(axis=1, keepdims=True)
+            by = (du + g[:, None] * few) @ np.abs(self.w64) + (2.2 * H + (self.rows + 8) * 2.0 ** -23) * size_x
             near(f64(dx), want_x, by + U * 1.001 * np.abs(want_x) + U * by)
             assert np.all(f64(dx)[~some] == 0)
         if dw is not None:
@@ -215,7 +220,7 @@ class Head:
             near(f64(dw), want, by + U * 1.001 * np.abs(want) + U * by)
 
 
-SIZES = [(1, 1, 16), (1, 130, 128), (2, 300, 144), (7, 256, 272), (33, 1000, 512), (128, 257, 128), (129, 640, 256),
+SIZES = [(1, 1, 16), (42, 1300, 160), (43, 1300, 160), (1, 130, 128), (2, 300, 144), (7, 256, 272), (33, 1000, 512), (128, 257, 128), (129, 640, 256),
          (200, 2049, 400), (300, 4100, 1040), (520, 1500, 2064)]
 
 
@@ -242,3 +247,51 @@ def test_gradients(cuda, n, rows, cols, k):
     dw, fw = empty(rows, cols, cuda, torch.bfloat16)
     c.grad(torch.as_tensor(g).to(cuda), dx, dw)
     c.check_grads(g, dx, dw)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(2500, 300, 2000), (3000, 700, 4112), (260, 40000, 528)])
+def test_gradients_of_many_tiles(cuda, n, rows, cols):
+    """More tiles of dx than pairs of CTAs, and few tiles whose sums are shared out."""
+    test_gradients(cuda, n, rows, cols, None)
+
+
+def test_gradients_in_pieces(cuda):
+    """More words than one piece of the vocabulary holds (256 MB of fp16), the last one short, against whole
+    sums on the GPU in fp64."""
+    import torch
+
+    n, rows, cols = 9000, 3 * 14848 + 129, 128
+    c = Head.__new__(Head)
+    gen = torch.Generator(device=cuda).manual_seed(3)
+    codes = torch.randint(0, 256, (rows, cols), generator=gen, device=cuda, dtype=torch.int32)
+    codes = torch.where((codes & 0x7F) == 0x7F, codes - 1, codes).to(torch.uint8)
+    w_scale = (0.5 + torch.rand(-(-rows // 128), 1, generator=gen, device=cuda)) * 2e-4
+    x = torch.randint(0, 256, (n, cols), generator=gen, device=cuda, dtype=torch.int32)
+    x = torch.where((x & 0x7F) == 0x7F, x - 1, x).to(torch.uint8)
+    x_scale = (0.5 + torch.rand(1, n, generator=gen, device=cuda)) * 1e-3
+    y = torch.randint(0, rows, (n,), generator=gen, device=cuda)
+    y[::7] = -1
+    w64 = codes.view(torch.float8_e4m3fn).double() * w_scale.double().repeat_interleave(128, 0)[:rows]
+    x64 = x.view(torch.float8_e4m3fn).double() * x_scale.double().t()
+    c.n, c.rows, c.cols, c.k, c.scale, c.dev = n, rows, cols, None, 1.0, cuda
+    c.head, c.t = (x, x_scale, codes, w_scale), y
+    c.forward()
+    g = torch.randn(n, generator=gen, device=cuda) / n
+    dx, _ = empty(n, cols, cuda, torch.bfloat16)
+    dw, _ = empty(rows, cols, cuda, torch.bfloat16)
+    c.grad(g, dx, dw)
+    z = x64 @ w64.t()
+    lse = torch.logsumexp(z, 1)
+    seen = y >= 0
+    at = z.gather(1, y.clamp(min=0)[:, None])[:, 0]
+    assert float((c.lse.double() - lse).abs().max()) < 1e-5 and float((c.loss.double() - torch.where(seen, lse - at, 0)).abs().max()) < 1e-5
+    u = torch.exp(z.sub_(lse[:, None]))
+    u[seen, y[seen]] -= 1
+    u *= torch.where(seen, g.double(), 0)[:, None]
+    want_x, want_w = u @ w64, u.t() @ x64
+    # roundings of u, X (2^-11 each) and the result (2^-8), random in sign: far below in the norm
+    assert float((dx.double() - want_x).norm() / want_x.norm()) < 2 ** -8
+    assert float((dw.double() - want_w).norm() / want_w.norm()) < 2 ** -8
+    size_x, size_w = u.abs() @ w64.abs(), u.abs().t() @ x64.abs()
+    assert bool(((dx.double() - want_x).abs() <= U * 1.01 * want_x.abs() + 2.5 * H * size_x).all())
+    assert bool(((dw.double() - want_w).abs() <= U * 1.01 * want_w.abs() + 2.5 * H * size_w).all())
