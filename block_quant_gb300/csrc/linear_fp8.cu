@@ -923,6 +923,51 @@ int launch_clusters(const char* what, const void* kernel, int clusters, int size
   return check(what);
 }
 
+namespace {
+// Which kernel a product takes, and k_linear's CTAs a tile.
+struct LinearPlan {
+  bool pairs;
+  int split;
+};
+LinearPlan linear_plan(int64_t n, int64_t width, int64_t red, int transposed) {
+  LinearPlan p{false, 1};
+  const int nk = int((red + BK - 1) / BK);
+  const int64_t pairs = ((n + PM - 1) / PM) * ((width + PN - 1) / PN), tiles = ((n + BM - 1) / BM) * ((width + BN - 1) / BN);
+  // k_linear: into how many CTAs to split a tile's k-blocks, by the times of 30 products.  A
+  // CTA alone on its SM takes 0.35 us a k-block (transposed 0.40), two on one 0.4 to 0.6 each, and a
+  // join by rows and shares; not into a second wave (75 tiles of 16 k-blocks: 8.5 us by 2, 14.9
+  // by 4).  128 rows and more, 48 tiles of 16: 8.2 us by 2, 10.1 by 4; 50 of 105: 23.6 by 2, 28.2
+  // by 3, 26.8 by 4; 100 of 64: 27.9 in one, 20.7 by 2; one row, 64 tiles of 64: 15.1 by 2,
+  // 13.7 by 4.
+  const int* slots = cluster_slots();
+  const int64_t waves = (tiles + 2 * slots[1] - 1) / (2 * slots[1]);
+  const double one = transposed ? 0.40 : 0.35, full = double(std::min<int64_t>(n, BM)) / BM;
+  double us_one = tiles <= slots[1] ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
+  for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * slots[k]; ++k) {
+    const int share = (nk + k - 1) / k;
+    const double us = tiles <= slots[k] ? 5 + one * share + (k - 1) * (0.12 + 0.2 * full)
+                                        : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share + (k - 1) * (0.25 + 0.55 * full);
+    if (us < us_one) us_one = us, p.split = k;
+  }
+  // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
+  // 5952 take 28 us there and 17 us on k_linear), where their tiles take less time: 0.40 us a k-block
+  // and 2.5 us a wave.  337 rows of 11840 x 4512 (two waves, or one of k_linear's): 38.3 us on
+  // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 64.2 and 96.1; 512 of 8192 x
+  // 4096 (one and one): 18.5 and 24.2.
+  const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
+  p.pairs = n > BM && us_pair < us_one;
+  return p;
+}
+
+}  // namespace
+
+bool linear_on_pairs(int64_t n, int64_t width, int64_t red) { return linear_plan(n, width, red, 0).pairs; }
+
+int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream) {
+  k_copy_scales<<<dim3(unsigned((n + 255) / 256), unsigned(groups)), 256, 0, static_cast<cudaStream_t>(stream)>>>(x, ldx, n, out, ldo);
+  return check("bq_linear_fp8 (scales)");
+}
+
 int launch_linear_fp8(const LinearArgs& a, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   static OncePerDevice once;
@@ -961,35 +1006,15 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   const int64_t pairs = ((a.n + PM - 1) / PM) * ((width + PN - 1) / PN);
   const int64_t tiles = ((a.n + BM - 1) / BM) * ((width + BN - 1) / BN);
   if (tiles > 0x7FFFFFF) return set_error(BQ_EINVAL, "bq_linear_fp8: too many tiles");
-  // k_linear: into how many CTAs to split a tile's k-blocks, by the times of 30 products.  A
-  // CTA alone on its SM takes 0.35 us a k-block (transposed 0.40), two on one 0.4 to 0.6 each, and a
-  // join by rows and shares; not into a second wave (75 tiles of 16 k-blocks: 8.5 us by 2, 14.9
-  // by 4).  128 rows and more, 48 tiles of 16: 8.2 us by 2, 10.1 by 4; 50 of 105: 23.6 by 2, 28.2
-  // by 3, 26.8 by 4; 100 of 64: 27.9 in one, 20.7 by 2; one row, 64 tiles of 64: 15.1 by 2,
-  // 13.7 by 4.
+  const LinearPlan way = linear_plan(a.n, width, red, a.transposed);
+  g.split = way.split;
   const int* slots = cluster_slots();
-  const int64_t waves = (tiles + 2 * slots[1] - 1) / (2 * slots[1]);
-  const double one = a.transposed ? 0.40 : 0.35, full = double(std::min<int64_t>(a.n, BM)) / BM;
-  double us_one = tiles <= slots[1] ? 5 + one * nk : 2 + double(waves) * (6 + 0.52 * nk);
-  for (int k = 2; k <= 8 && k <= nk && tiles <= 2 * slots[k]; ++k) {
-    const int share = (nk + k - 1) / k;
-    const double us = tiles <= slots[k] ? 5 + one * share + (k - 1) * (0.12 + 0.2 * full)
-                                        : 6 + (k == 2 ? 0.4 + 0.1 * full : 0.45 + 0.15 * full) * share + (k - 1) * (0.25 + 0.55 * full);
-    if (us < us_one) us_one = us, g.split = k;
-  }
-  // The pairs take more than 128 rows (fewer leave one of the CTAs idle: 12 rows of 11048 x
-  // 5952 take 28 us there and 17 us on k_linear), where their tiles take less time: 0.40 us a k-block
-  // and 2.5 us a wave.  337 rows of 11840 x 4512 (two waves, or one of k_linear's): 38.3 us on
-  // pairs, 25.5 on k_linear; 849 of 6336 x 8144 (two and two): 64.2 and 96.1; 512 of 8192 x
-  // 4096 (one and one): 18.5 and 24.2.
-  const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
-  if (a.n > BM && us_pair < us_one) {
+  if (way.pairs) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (not read by plain stores)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {
       const int64_t ld = (a.n + 3) / 4 * 4;
-      k_copy_scales<<<dim3(unsigned((a.n + 255) / 256), unsigned(nk)), 256, 0, s>>>(a.x_scale, a.ld_xs, a.n, a.scale_ws, ld);
-      if (int rc = check("bq_linear_fp8 (scales)")) return rc;
+      if (int rc = launch_copy_scales(a.x_scale, a.ld_xs, a.n, nk, a.scale_ws, ld, stream)) return rc;
       g.xs = a.scale_ws, g.ld_xs = ld;
     }
     if (g.bytes == 16 && end != kTileStats)  // (probabilities: whole 16-byte words, zeros past the width)

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
   }
 }
 
-// every thread of a CTA: the largest of `count` values
+// every thread of a CTA of 256: the largest of `count` values
 __device__ __forceinline__ float largest(const float* v, int count) {
   __shared__ float top[8];
   float m = 0.f;
@@ -1060,10 +1060,19 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   auto *x16 = reinterpret_cast<__half*>(base + p.x), *u = reinterpret_cast<__half*>(base + p.u), *w16 = reinterpret_cast<__half*>(base + p.w);
   const int64_t tile_cols = (a.cols + 127) / 128;
 
+  // X's scales as the pairs read them, copied once for all pieces
+  const bool pairs = linear_on_pairs(a.n, std::min<int64_t>(p.piece, a.rows), a.cols);
+  const float* xs = a.x_scale;
+  int64_t ld_xs = a.ld_xs;
+  if (pairs && (ld_xs % 4 || (reinterpret_cast<uintptr_t>(xs) & 15))) {
+    auto* to = reinterpret_cast<float*>(base + p.scales);
+    if (int rc = launch_copy_scales(xs, ld_xs, a.n, tile_cols, to, up_to(a.n, 4), stream)) return rc;
+    xs = to, ld_xs = up_to(a.n, 4);
+  }
   PrepArgs prep;
   prep.y = targets(a);
-  prep.xs = a.x_scale, prep.ws = a.w_scale, prep.lse = a.lse, prep.dloss = a.dloss, prep.off = off, prep.tops = tops, prep.target = target;
-  prep.ld_xs = a.ld_xs, prep.n = a.n, prep.w_tiles = tile_cols * ((a.rows + 127) / 128), prep.groups = int(tile_cols);
+  prep.xs = xs, prep.ws = a.w_scale, prep.lse = a.lse, prep.dloss = a.dloss, prep.off = off, prep.tops = tops, prep.target = target;
+  prep.ld_xs = ld_xs, prep.n = a.n, prep.w_tiles = tile_cols * ((a.rows + 127) / 128), prep.groups = int(tile_cols);
   const int prep_ctas = int(ctas_for(std::max<int64_t>(a.n * 32, prep.w_tiles), 256, kPrepCtas));
   launch_after(k_loss_prep, unsigned(prep_ctas), 256, 0, s, prep);
   if (int rc = check("loss gradient (targets)")) return rc;
@@ -1072,7 +1081,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   CUtensorMap tx, tw, tu, to;
   HalfArgs hx = {}, hw = {};
   if (a.dw) {
-    hx = {a.x, a.x_scale, off, a.dloss, tops, x16, back, a.ldx, a.ld_xs, p.ldh, a.n, a.cols, prep_ctas,
+    hx = {a.x, xs, off, a.dloss, tops, x16, back, a.ldx, ld_xs, p.ldh, a.n, a.cols, prep_ctas,
           int(ctas_for(a.n * (a.cols / 16), 256, half_ctas))};
     if (int rc = encode_map_chunks(&tx, x16, a.cols, a.n, p.ldh, 2)) return rc;
   }
@@ -1084,15 +1093,15 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
     if (a.dx && !p.few)
       hw = {w, w_scale, nullptr, nullptr, tops + kPrepCtas, w16, back + 1, a.ldw, tile_cols, p.ldh, len, a.cols, prep_ctas,
             int(ctas_for(len * (a.cols / 16), 256, half_ctas))};
+    LossTile tile = {};
     if (hx.ctas + hw.ctas > 0) {
       launch_after(k_loss_half, unsigned(hx.ctas + hw.ctas), 256, 0, s, hx, hw);
       if (int rc = check("loss gradient (operands)")) return rc;
       hx.ctas = 0;
     }
-    LossTile tile = {};
     tile.end = kTileProbs, tile.zscale = a.scale, tile.lse = off;
     tile.target = target, tile.loss = a.loss, tile.first = int(v0);
-    LinearArgs l{a.x, a.x_scale, w, w_scale, u, a.ldx, a.ld_xs, a.ldw, p.piece, a.n, int(len), a.cols, 0, status,
+    LinearArgs l{a.x, xs, w, w_scale, u, a.ldx, ld_xs, a.ldw, p.piece, a.n, int(len), a.cols, 0, status,
                  reinterpret_cast<float*>(base + p.scales), &tile};
     if (int rc = launch_linear_fp8(l, stream)) return rc;
     if (a.teacher) {

@@ -94,6 +94,9 @@ struct LinearArgs {
   LossTile* loss = nullptr;  // kTileProbs: out is fp16, 16-byte aligned, its pitch a multiple of 8 that covers the width
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
+bool linear_on_pairs(int64_t n, int64_t width, int64_t red);  // whether out = x W^T takes the CTA pairs
+// X's scales [groups][ldx] at a pitch whose rows 16-byte copies can read
+int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream);
 
 // D [rows, cols] (+)= dY^T X over n tokens, bf16 (linear_fp8.cu): dy [n, rows] with 16-byte
 // aligned rows (padded: its pitch covers the next multiple of 64 columns), x [n, cols] with
