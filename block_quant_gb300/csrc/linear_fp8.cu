@@ -81,7 +81,7 @@ struct LinArgs {
   const int* target;
   int64_t ld_stats;
   float zscale;
-  int first;
+  int first, late;
 };
 
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
     tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
   };
-  after_previous();
+  if (END != kTileProbs || !g.late) after_previous();
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  if (END == kTileProbs && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  after_previous();
+  if (END != kTileProbs || !g.late) after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmem);
   }
+  if (END == kTileProbs && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- weight gradient
@@ -992,12 +994,12 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.tile_cols = (a.cols + 127) / 128, g.status = a.status;
   g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
   g.stats = nullptr, g.at = nullptr, g.lse = nullptr, g.loss = nullptr, g.factor = nullptr, g.target = nullptr;
-  g.ld_stats = 0, g.zscale = 1.f, g.first = 0;
+  g.ld_stats = 0, g.zscale = 1.f, g.first = 0, g.late = 0;
   const int end = a.loss ? a.loss->end : int(kTileOut);
   if (a.loss) {
     g.stats = a.loss->stats, g.at = a.loss->at, g.ld_stats = a.loss->ld_stats, g.zscale = a.loss->zscale;
     g.lse = a.loss->lse, g.loss = a.loss->loss, g.target = a.loss->target, g.first = a.loss->first;
-    g.factor = a.loss->factor;
+    g.factor = a.loss->factor, g.late = a.loss->late;
   }
   if (end != kTileOut) g.bytes = 16;
   const int nk = (red + BK - 1) / BK;

@@ -690,6 +690,7 @@ struct DwPieceArgs {
   int64_t ldo;
   int m, n, k;        // words, columns, tokens
   int splits, accumulate, bytes;
+  int late;           // the launch before is dx's, which this one does not need: it waits for its end at its own
   int* status;
 };
 
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  after_previous();
+  if (!g.late) after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
@@ -851,6 +852,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmem);
   }
+  if (g.late) after_previous();
 }
 
 // dx = the shares' sum in order, times its row's factor: warp i takes 32 rows x 16 columns
@@ -1061,7 +1063,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   const int64_t tile_cols = (a.cols + 127) / 128;
 
   // X's scales as the pairs read them, copied once for all pieces
-  const bool pairs = linear_on_pairs(a.n, std::min<int64_t>(p.piece, a.rows), a.cols);
+  const bool pairs = linear_on_pairs(a.n, piece_len(p, a.rows, 0), a.cols) || linear_on_pairs(a.n, piece_len(p, a.rows, p.pieces - 1), a.cols);
   const float* xs = a.x_scale;
   int64_t ld_xs = a.ld_xs;
   if (pairs && (ld_xs % 4 || (reinterpret_cast<uintptr_t>(xs) & 15))) {
@@ -1095,6 +1097,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
             int(ctas_for(len * (a.cols / 16), 256, half_ctas))};
     LossTile tile = {};
     if (hx.ctas + hw.ctas > 0) {
+      tile.late = 1;
       launch_after(k_loss_half, unsigned(hx.ctas + hw.ctas), 256, 0, s, hx, hw);
       if (int rc = check("loss gradient (operands)")) return rc;
       hx.ctas = 0;
@@ -1143,7 +1146,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
       g.out = static_cast<__nv_bfloat16*>(a.dw) + v0 * a.ld_dw, g.ldo = a.ld_dw, g.m = int(len), g.n = a.cols, g.k = int(a.n);
       g.splits = dw_splits(a.n, len, a.cols);
       g.part = g.splits > 1 ? reinterpret_cast<float*>(base + p.dw) : nullptr;
-      g.back = back, g.factor = unscale, g.accumulate = a.accumulate;
+      g.back = back, g.factor = unscale, g.accumulate = a.accumulate, g.late = a.dx && !p.few;
       g.bytes = store_bytes(g.out, a.ld_dw, a.cols), g.status = status;
       to = tx;  // (not read by plain stores and shares)
       if (!g.part && g.bytes == 16)

@@ -74,6 +74,9 @@ struct LossTile {
   const int* target;
   const float* loss;
   int first;
+  // late: the launch before neither writes what this one reads nor reads what it writes, and has itself waited
+  // for all that came before: this one begins beside it and waits for its end at its own
+  int late;
   // kTileTriples (transposed, at most 42 tokens): each token's factor beside zscale, lse as above
   const float* factor;
 };
