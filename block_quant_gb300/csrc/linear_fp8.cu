@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       tma_load_2d(b_base + uint32_t(s) * B_STAGE, &tmW, kb * BK, n0, full_bar(s));
     tma_load_2d(a_base + uint32_t(s) * a_stage, &tmX, kb * BK, m0, full_bar(s));
   };
-  if (END != kTileProbs || !g.late) after_previous();
+  if (END == kTileOut || END == kTileTriples || !g.late) after_previous();
   if (threadIdx.x == 0) {
     for (int s = 0; s < g.stages; ++s) {
       mbar_init(full_bar(s), 1);
@@ -264,10 +264,11 @@ __global__ void __launch_bounds__(THREADS, 2)
   int classes = -1, nth = 0;
   if constexpr (END == kTileProbs) {
     const int r = rank * EPI_ROWS + warp + lane * g.split * EPI_ROWS;
-    if (r < rows) lses = __ldg(g.lse + m0 + r), classes = __ldg(g.target + m0 + r);
+    if (r < rows) lses = __ldcg(g.lse + m0 + r), classes = __ldcg(g.target + m0 + r);
   }
   if constexpr (END == kTileTriples) {
-    for (int t = rank * EPI_ROWS + warp; 3 * t < rows; t += g.split * EPI_ROWS) {
+    for (int t = rank * EPI_ROWS + warp; 3 * t + 2 < rows; t += g.split * EPI_ROWS) {
+      const int token = m0 / BM * (BM / 3) + t;
       float v[BN / 32] = {};
       for (int c = 0; c < g.split; ++c) {
         const uint32_t at = map_rank(part0, uint32_t(c)) + 4u * uint32_t(3 * t * kPartPitch + lane);
@@ -280,9 +281,9 @@ __global__ void __launch_bounds__(THREADS, 2)
             v[j] += x;
           }
       }
-      const bool none = __ldg(g.lse + t) == kNoTarget;  // (whatever W holds)
-      const float f = g.zscale * __ldg(g.factor + t);
-      __nv_bfloat16* o = g.out + int64_t(t) * g.ldo + n0;
+      const bool none = __ldg(g.lse + token) == kNoTarget;  // (whatever W holds)
+      const float f = g.zscale * __ldg(g.factor + token);
+      __nv_bfloat16* o = g.out + int64_t(token) * g.ldo + n0;
 #pragma unroll
       for (int j = 0; j < BN / 32; ++j)
         if (lane + 32 * j < cols) o[lane + 32 * j] = __float2bfloat16_rn(none ? 0.f : f * v[j]);
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       __half* u = reinterpret_cast<__half*>(g.out) + int64_t(m0 + r) * g.ldo + n0;
 #pragma unroll
       for (int j = 0; j < BN / 32; ++j)
-        if (lane + 32 * j < cols) u[lane + 32 * j] = __float2half_rn(y == 32 * j ? scaled_rest(__ldg(g.loss + m0 + r)) : scaled_prob(v[j] * g.zscale, lse));
+        if (lane + 32 * j < cols) u[lane + 32 * j] = __float2half_rn(y == 32 * j ? scaled_rest(__ldcg(g.loss + m0 + r)) : scaled_prob(v[j] * g.zscale, lse));
       continue;
     }
     __nv_bfloat16* o = g.out + int64_t(m0 + r) * g.ldo + n0;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if (END == kTileProbs && g.late) after_previous();
+  if ((END == kTileStats || END == kTileProbs) && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (END != kTileProbs || !g.late) after_previous();
+  if (END == kTileOut || END == kTileTriples || !g.late) after_previous();
   if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kPairTmem);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers exist and the columns are held before any remote use
@@ -542,7 +543,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       float lse = kNoTarget;
       int y = -1;
       if constexpr (END == kTileProbs)
-        if (row0 + lane < g.n) lse = __ldg(g.lse + row0 + lane), y = __ldg(g.target + row0 + lane) - g.first - c0;
+        if (row0 + lane < g.n) lse = __ldcg(g.lse + row0 + lane), y = __ldcg(g.target + row0 + lane) - g.first - c0;
       // W's scales for 32 k-blocks, block kb + l in lane l
       float wl = 0.f, wn = c0 < g.width && lane < nk ? __ldg(ws + lane * ws_step) : 0.f;
       for (int kb = 0; kb < nk; ++kb, ++it) {
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
           if constexpr (END == kTileProbs) {
             put_box<32, __half>(acc + 32 * u, box, lane);
             if (y >= 32 * u && y < 32 * u + 32) {  // the row's class
-              const __half f = __float2half_rn(scaled_rest(__ldg(g.loss + row0 + lane)));
+              const __half f = __float2half_rn(scaled_rest(__ldcg(g.loss + row0 + lane)));
               asm volatile("st.shared.b16 [%0], %1;" ::"r"(box_word<32>(box, lane, (y & 31) >> 3) + 2u * uint32_t(y & 7)),
                            "h"(__half_as_ushort(f))
                            : "memory");
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmem);
   }
-  if (END == kTileProbs && g.late) after_previous();
+  if ((END == kTileStats || END == kTileProbs) && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- weight gradient
@@ -930,9 +931,10 @@ namespace {
 struct LinearPlan {
   bool pairs;
   int split;
+  double us;  // k_linear's
 };
 LinearPlan linear_plan(int64_t n, int64_t width, int64_t red, int transposed) {
-  LinearPlan p{false, 1};
+  LinearPlan p{false, 1, 0};
   const int nk = int((red + BK - 1) / BK);
   const int64_t pairs = ((n + PM - 1) / PM) * ((width + PN - 1) / PN), tiles = ((n + BM - 1) / BM) * ((width + BN - 1) / BN);
   // k_linear: into how many CTAs to split a tile's k-blocks, by the times of 30 products.  A
@@ -958,12 +960,14 @@ LinearPlan linear_plan(int64_t n, int64_t width, int64_t red, int transposed) {
   // 4096 (one and one): 18.5 and 24.2.
   const double us_pair = 4 + double((pairs + slots[2] - 1) / slots[2]) * (0.40 * nk + 2.5);
   p.pairs = n > BM && us_pair < us_one;
+  p.us = us_one;
   return p;
 }
 
 }  // namespace
 
 bool linear_on_pairs(int64_t n, int64_t width, int64_t red) { return linear_plan(n, width, red, 0).pairs; }
+double linear_small_us(int64_t n, int64_t width, int64_t red) { return linear_plan(n, width, red, 1).us; }
 
 int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream) {
   k_copy_scales<<<dim3(unsigned((n + 255) / 256), unsigned(groups)), 256, 0, static_cast<cudaStream_t>(stream)>>>(x, ldx, n, out, ldo);
@@ -1011,7 +1015,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   const LinearPlan way = linear_plan(a.n, width, red, a.transposed);
   g.split = way.split;
   const int* slots = cluster_slots();
-  if (way.pairs) {
+  if (way.pairs && end != kTileTriples) {
     if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, 128)) return rc;
     to = tx;  // (not read by plain stores)
     if (a.ld_xs % 4 || (reinterpret_cast<uintptr_t>(a.x_scale) & 15)) {

@@ -122,53 +122,69 @@ struct PickArgs {
   Targets y;
 };
 
-// The sum over a lane's codes (16 at 16 lane, 16 lane + 512, ..) of X's row times W's, by their scales;
-// four loads of each set out together.
-__device__ __forceinline__ float lane_dot(const uint8_t* x, const float* xs, int64_t ld_xs, const uint8_t* w, const float* ws,
-                                          int cols, int lane) {
-  float sum = 0.f;
-  for (int c0 = 16 * lane; c0 < cols; c0 += 2048) {
-    uint4 a[4], b[4];
-    float f[4];
+// The logits of words v[0 .. P) in row t, by a warp, the same in every lane: a lane takes 16 codes of each
+// 512.  X's are decoded once for all P, and two steps' loads set out together.  (Bound by instructions, the
+// decoding above all, where P is 1: 262144 pairs of 4096 codes took 275 us with a word a warp.)
+template <int P>
+__device__ __forceinline__ void picked(const PickArgs& g, int64_t t, const int (&v)[P], int lane, float (&z)[P]) {
+  constexpr int STEPS = P == 1 ? 4 : 2;
+  const uint8_t* x = g.x + t * g.ldx;
+  const float* xs = g.xs + t;
+  const int tile_cols = (g.cols + 127) / 128;
+  float sum[P] = {};
+  for (int c0 = 16 * lane; c0 < g.cols; c0 += 512 * STEPS) {
+    uint4 a[STEPS], b[STEPS][P];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < STEPS; ++e) {
       const int c = c0 + 512 * e;
-      if (c >= cols) continue;
-      b[e] = __ldg(reinterpret_cast<const uint4*>(w + c));
+      if (c >= g.cols) continue;
       a[e] = __ldg(reinterpret_cast<const uint4*>(x + c));
-      f[e] = __ldg(xs + int64_t(c >> 7) * ld_xs) * __ldg(ws + (c >> 7));
+#pragma unroll
+      for (int i = 0; i < P; ++i) b[e][i] = __ldg(reinterpret_cast<const uint4*>(g.w + int64_t(v[i]) * g.ldw + c));
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (c0 + 512 * e >= cols) continue;
-      float u[16], v[16], d = 0.f;
+    for (int e = 0; e < STEPS; ++e) {
+      const int c = c0 + 512 * e;
+      if (c >= g.cols) continue;
+      const float f = __ldg(xs + int64_t(c >> 7) * g.ld_xs);
+      float u[16];
       decode16(a[e], u);
-      decode16(b[e], v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) d = fmaf(u[i], v[i], d);
-      sum = fmaf(d, f[e], sum);
+      for (int i = 0; i < P; ++i) {
+        float w[16];
+        decode16(b[e][i], w);
+        float2 d = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) d = fma2(make_float2(u[j], u[j + 1]), make_float2(w[j], w[j + 1]), d);
+        sum[i] = fmaf(d.x + d.y, f * __ldg(g.ws + int64_t(v[i] >> 7) * tile_cols + (c >> 7)), sum[i]);
+      }
     }
   }
-  return sum;
+#pragma unroll
+  for (int i = 0; i < P; ++i) z[i] = g.y.scale * warp_sum(sum[i]);
 }
 
-// the logit of word v in row t, by a warp
-__device__ __forceinline__ float picked(const PickArgs& g, int64_t t, int v, int lane) {
-  return g.y.scale * warp_sum(lane_dot(g.x + t * g.ldx, g.xs + t, g.ld_xs, g.w + int64_t(v) * g.ldw,
-                                       g.ws + int64_t(v >> 7) * ((g.cols + 127) / 128), g.cols, lane));
-}
-
-// The logits of the teacher's words, a warp each, by reading their rows of W: bound by those bytes.
+// The logits of the teacher's words, four a warp, by reading their rows of W: bound by those bytes.
 __global__ void __launch_bounds__(256) k_loss_pick(const PickArgs g) {
   after_previous();
   next_may_start();
-  const int lane = threadIdx.x & 31;
-  const int64_t pairs = g.n * g.y.k, step = int64_t(gridDim.x) * 8;
-  for (int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); p < pairs; p += step) {
-    const int64_t t = p / g.y.k;
-    const int i = int(p - t * g.y.k), v = g.y.id(t, i);
-    const float z = v >= 0 ? picked(g, t, v, lane) : 0.f;
-    if (lane == 0) g.out[t * g.ld_out + i] = z;
+  constexpr int P = 4;
+  const int lane = threadIdx.x & 31, per_row = (g.y.k + P - 1) / P;
+  const int64_t items = g.n * per_row, step = int64_t(gridDim.x) * 8;
+  for (int64_t p = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5); p < items; p += step) {
+    const int64_t t = p / per_row;
+    const int i0 = P * int(p - t * per_row);
+    int v[P];
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int id = i0 + i < g.y.k ? g.y.id(t, i0 + i) : -1;  // (what a pair without a word gets is not read)
+      any |= id >= 0;
+      v[i] = max(id, 0);
+    }
+    float z[P] = {};
+    if (any) picked<P>(g, t, v, lane, z);
+    if (lane < P && i0 + lane < g.y.k) g.out[t * g.ld_out + i0 + lane] = lane == 0 ? z[0] : lane == 1 ? z[1] : lane == 2 ? z[2] : z[3];
   }
 }
 
@@ -200,7 +216,12 @@ __global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
   int v = -1;
   if (!y.teacher && mine) {
     v = y.id(t, 0);
-    if (v >= 0) z = picked(g.pick, t, v, lane);
+    if (v >= 0) {
+      const int one[1] = {v};
+      float got[1];
+      picked<1>(g.pick, t, one, lane, got);
+      z = got[0];
+    }
   }
   RowStats a{-INFINITY, 0.f, 0};
   bool some = false;
@@ -334,27 +355,43 @@ struct HalfArgs {
   int cols, count, ctas;
 };
 
+// A warp takes up to 1024 codes of a row, a lane 8 of each 256, so that loads and stores are whole lines;
+// bound by memory (32256 x 4096: 58 us, 396 MB; 75 with 16 codes a lane).
 __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
   const int e = power_for(largest(g.tops, g.count));
   const float up = ldexpf(1.f, e);
   if (cta == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
-  const int words = g.cols / 16;
-  const int64_t items = g.n * words, step = int64_t(g.ctas) * 256;
-  for (int64_t i = int64_t(cta) * 256 + threadIdx.x; i < items; i += step) {
-    const int64_t t = i / words;
-    const int c = 16 * int(i - t * words);
-    uint32_t o[8] = {};
-    if (!g.off || __ldg(g.off + t) != kNoTarget) {
-      const float f = up * (g.off ? __ldg(g.scale + int64_t(c >> 7) * g.lds + t) * __ldg(g.dloss + t)
-                                  : __ldg(g.scale + (t >> 7) * g.lds + (c >> 7)));
-      float v[16];
-      decode16(__ldg(reinterpret_cast<const uint4*>(g.codes + t * g.ldc + c)), v);
+  const int lane = threadIdx.x & 31, spans = (g.cols + 1023) / 1024;
+  const int64_t items = g.n * spans, step = int64_t(g.ctas) * 8;
+  for (int64_t i = int64_t(cta) * 8 + (threadIdx.x >> 5); i < items; i += step) {
+    const int64_t t = i / spans;
+    const int c0 = 1024 * int(i - t * spans) + 8 * lane;
+    const bool none = g.off && __ldg(g.off + t) == kNoTarget;
+    const float row = g.off ? up * __ldg(g.dloss + t) : up;
+    uint2 q[4];
+    float f[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = two16(v[2 * j] * f, v[2 * j + 1] * f, __half());
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 256 * k;
+      if (c >= g.cols) continue;
+      q[k] = __ldg(reinterpret_cast<const uint2*>(g.codes + t * g.ldc + c));
+      f[k] = __ldg(g.off ? g.scale + int64_t(c >> 7) * g.lds + t : g.scale + (t >> 7) * g.lds + (c >> 7));
     }
-    uint4* to = reinterpret_cast<uint4*>(g.out + t * g.ldo + c);
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 256 * k;
+      if (c >= g.cols) continue;
+      const uint32_t w[2] = {q[k].x, q[k].y};
+      uint32_t o[4] = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3)));
+        // (X's: the scale times the gradient first, as the power of two was found)
+        const float s = f[k] * row;
+        if (!none) o[j] = two16(v.x * s, v.y * s, __half());
+      }
+      *reinterpret_cast<uint4*>(g.out + t * g.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -407,15 +444,16 @@ __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
 }
 
 // ---------------------------------------------------------------- gradient: few tokens
-// dX of at most 42 tokens: U as the sum of three E4M3 values, whose products with W's codes are an FP8
-// projection (k_linear, transposed) of three rows a token, as many as its tile of 128 has room
-// for anyway.  It reads W as it is, once, where fp16 operands are written and read: 16 tokens of 128256
-// x 4096 take 103 us so (its bytes alone 78), and 505 by fp16 pieces.
-constexpr int kFewTokens = 42;
+// dX of few tokens: U as the sum of three E4M3 values, whose products with W's codes are an FP8
+// projection (k_linear, transposed) of three rows a token, 42 tokens a tile of 128.  It reads W as it is,
+// where fp16 operands are written and read: 16 tokens of 128256 x 4096 take 103 us so (W's bytes alone 78),
+// and 505 by fp16 pieces.
+constexpr int kTokensOfTile = 42;
+int64_t triple_rows(int64_t n) { return n / kTokensOfTile * 128 + 3 * (n % kTokensOfTile); }
 
 struct SplitArgs {
   const __half* u;
-  uint8_t* codes;  // rows 3 t, 3 t + 1, 3 t + 2 of token t
+  uint8_t* codes;  // rows as triple_rows counts them
   float* scale;    // [groups][lds]
   int64_t ldu, ldc, lds;
   int n, len;
@@ -452,7 +490,7 @@ __global__ void __launch_bounds__(256) k_loss_split(const SplitArgs g) {
       v[e] -= __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3))) * s;
       w |= uint32_t(q) << (8 * e);
     }
-    const int64_t row = 3 * int64_t(t) + term;
+    const int64_t row = int64_t(t / kTokensOfTile) * 128 + 3 * (t % kTokensOfTile) + term;
     if (c < g.ldc) *reinterpret_cast<uint32_t*>(g.codes + row * g.ldc + c) = w;
     if (lane == 0) g.scale[int64_t(j) * g.lds + row] = s;
   }
@@ -804,7 +842,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     const int q = warp & 3, part = (warp - 4) >> 2;
     const uint32_t te0 = map_rank(tempty_bar(0), 0);
     const uint32_t box = base + DW_STAGES * PSTAGE_BYTES + uint32_t(warp - 4) * DW_BOX;
-    const float back = g.part ? 1.f : __ldg(g.back);
+    const float back = g.part ? 1.f : __ldcg(g.back);
     uint32_t tc = 0;
     for (int t = pair; t < total; t += npairs, ++tc) {
       int bm, bn, k0, k1;
@@ -968,10 +1006,19 @@ Shares dx_shares(int64_t n, int64_t cols, int64_t piece) {
   return sh;
 }
 
+// Whether dx takes three E4M3 terms of U: where the FP8 product of three rows a token costs less than
+// W in fp16 (3 bytes a value at 5.3 TB/s) and its product (0.29 us a k-block and round of tiles).
+bool few_tokens(int64_t n, int64_t rows, int64_t cols) {
+  if (n * rows * 2 > kPieceBytes) return false;
+  const double tiles = double((n + PM - 1) / PM) * double((cols + PN - 1) / PN);
+  const double rounds = std::max(tiles / cluster_slots()[2], 0.25);
+  return linear_small_us(triple_rows(n), cols, rows) < double(rows) * double(cols) * 3 / 5.3e6 + 0.29 * rounds * double(rows) / DK;
+}
+
 GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
   GradWs p;
   p.ldh = up_to(cols, 64);
-  p.few = n <= kFewTokens && n * rows * 2 <= kPieceBytes;
+  p.few = few_tokens(n, rows, cols);
   const int64_t most = p.few ? up_to(rows, 256)
                               : std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>({n, p.ldh, 1})) / 256 * 256);
   const int64_t pieces = (rows + most - 1) / most;
@@ -986,8 +1033,8 @@ GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
   p.x = p.target + up(size_t(n) * 4);
   p.u = p.x + up(size_t(n) * size_t(p.ldh) * 2);
   p.w = p.u + up(size_t(n) * size_t(p.piece) * 2);
-  p.dx = p.w + up(p.few ? size_t(3 * n) * size_t(p.piece) : size_t(p.piece) * size_t(p.ldh) * 2);
-  p.dw = p.dx + up(p.few ? size_t(p.piece / 128) * size_t(up_to(3 * n, 4)) * 4 : size_t(p.dx_shares.kept()) * PM * PN * 4);
+  p.dx = p.w + up(p.few ? size_t(triple_rows(n)) * size_t(p.piece) : size_t(p.piece) * size_t(p.ldh) * 2);
+  p.dw = p.dx + up(p.few ? size_t(p.piece / 128) * size_t(up_to(triple_rows(n), 4)) * 4 : size_t(p.dx_shares.kept()) * PM * PN * 4);
   size_t dw = 0;
   for (int i : {0, p.pieces - 1}) {
     const int64_t len = piece_len(p, rows, i);
@@ -1022,12 +1069,17 @@ int launch_loss(const LossArgs& a, void* ws, void* stream) {
   pick.out = a.logp, pick.ld_out = a.ld_logp;
   pick.ldx = a.ldx, pick.ld_xs = a.ld_xs, pick.ldw = a.ldw, pick.n = a.n, pick.cols = a.cols;
   pick.y = targets(a);
+  // the targets' logits beside the product, which reads nothing of theirs (but for a copy of X's scales, it is the
+  // next launch)
+  const bool pick_first = a.teacher && (!linear_on_pairs(a.n, a.rows, a.cols) ||
+                                        (a.ld_xs % 4 == 0 && (reinterpret_cast<uintptr_t>(a.x_scale) & 15) == 0));
   if (a.teacher) {
-    launch_after(k_loss_pick, ctas_for(a.n * a.k, 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
+    launch_after(k_loss_pick, ctas_for(a.n * ((a.k + 3) / 4), 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
     if (int rc = check("loss (targets)")) return rc;
   }
   LossTile tile = {};
   tile.end = kTileStats, tile.zscale = a.scale;
+  tile.late = pick_first;
   tile.stats = reinterpret_cast<float2*>(base + p.stats), tile.at = base + p.at, tile.ld_stats = a.n;
   LinearArgs l{a.x, a.x_scale, a.w, a.w_scale, base, a.ldx, a.ld_xs, a.ldw, a.rows, a.n, a.rows, a.cols, 0,
                static_cast<int*>(ws), reinterpret_cast<float*>(base + p.scales), &tile};
@@ -1084,7 +1136,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   HalfArgs hx = {}, hw = {};
   if (a.dw) {
     hx = {a.x, xs, off, a.dloss, tops, x16, back, a.ldx, ld_xs, p.ldh, a.n, a.cols, prep_ctas,
-          int(ctas_for(a.n * (a.cols / 16), 256, half_ctas))};
+          int(ctas_for(a.n * ((a.cols + 1023) / 1024), 8, half_ctas))};
     if (int rc = encode_map_chunks(&tx, x16, a.cols, a.n, p.ldh, 2)) return rc;
   }
   const float unscale = a.scale * (1.f / float(1 << kProbBits));
@@ -1094,7 +1146,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
     const float* w_scale = a.w_scale + v0 / 128 * tile_cols;
     if (a.dx && !p.few)
       hw = {w, w_scale, nullptr, nullptr, tops + kPrepCtas, w16, back + 1, a.ldw, tile_cols, p.ldh, len, a.cols, prep_ctas,
-            int(ctas_for(len * (a.cols / 16), 256, half_ctas))};
+            int(ctas_for(len * ((a.cols + 1023) / 1024), 8, half_ctas))};
     LossTile tile = {};
     if (hx.ctas + hw.ctas > 0) {
       tile.late = 1;
@@ -1118,13 +1170,13 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
     if (a.dx && p.few) {
       auto* codes = reinterpret_cast<uint8_t*>(base + p.w);
       auto* scale = reinterpret_cast<float*>(base + p.dx);
-      const int64_t lds = up_to(3 * a.n, 4), ldc = up_to(len, 16);
+      const int64_t lds = up_to(triple_rows(a.n), 4), ldc = up_to(len, 16);
       SplitArgs f{u, codes, scale, p.piece, ldc, lds, int(a.n), int(len)};
       launch_after(k_loss_split, unsigned((a.n * ((len + 127) / 128) + 7) / 8), 256, 0, s, f);
       if (int rc = check("loss gradient (few tokens)")) return rc;
       LossTile triples = {};
       triples.end = kTileTriples, triples.zscale = unscale, triples.lse = off, triples.factor = a.dloss;
-      LinearArgs d{codes, scale, w, w_scale, a.dx, ldc, lds, a.ldw, a.ld_dx, 3 * a.n, int(len), a.cols, 1, status, nullptr, &triples};
+      LinearArgs d{codes, scale, w, w_scale, a.dx, ldc, lds, a.ldw, a.ld_dx, triple_rows(a.n), int(len), a.cols, 1, status, nullptr, &triples};
       if (int rc = launch_linear_fp8(d, stream)) return rc;
     } else if (a.dx) {
       if (int rc = encode_map_codes(&tu, u, 2 * len, a.n, 2 * p.piece, 128)) return rc;

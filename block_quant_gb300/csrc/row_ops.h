@@ -66,6 +66,10 @@ constexpr int kPartCols = 64;  // of statistics
 struct LossTile {
   int end;
   float zscale;      // a logit is zscale times the product
+  // late (statistics, probabilities): the launch before neither writes what this one reads nor reads what it
+  // writes, and has itself waited for all that came before: this one begins beside it and waits for its end at
+  // its own
+  int late;
   float2* stats;     // kTileStats: [part][ld_stats] and
   uint8_t* at;       // the largest logit's column in its part
   int64_t ld_stats;
@@ -74,10 +78,8 @@ struct LossTile {
   const int* target;
   const float* loss;
   int first;
-  // late: the launch before neither writes what this one reads nor reads what it writes, and has itself waited
-  // for all that came before: this one begins beside it and waits for its end at its own
-  int late;
-  // kTileTriples (transposed, at most 42 tokens): each token's factor beside zscale, lse as above
+  // kTileTriples (transposed): rows 3 i, 3 i + 1, 3 i + 2 of each 128 are token 42 j + i's, i < 42; each token's
+  // factor beside zscale, lse as above
   const float* factor;
 };
 
@@ -98,6 +100,7 @@ struct LinearArgs {
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 bool linear_on_pairs(int64_t n, int64_t width, int64_t red);  // whether out = x W^T takes the CTA pairs
+double linear_small_us(int64_t n, int64_t width, int64_t red);  // what out = x W costs without them
 // X's scales [groups][ldx] at a pitch whose rows 16-byte copies can read
 int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream);
 

@@ -5,9 +5,10 @@
 Every weight is read as the optimizer step leaves it: E4M3 codes with one scale per
 128 x 128 tile, at its place in the FP8 staging buffer (the AllGather's result, here of
 one device).  The forward pass is lookup, residual norm with FP8 rows, and FP8
-projections; the backward pass the operators' gradients, bf16, which the pack and the
-8-bit Adam step turn into the next codes.  torch does the elementwise rest: the
-squared ReLU, the softmax and the loss.
+projections, and a loss over the head that keeps no logits (cross entropy, or the divergence
+from a teacher's top logits); the backward pass the operators' gradients, bf16, which the pack
+and the 8-bit Adam step turn into the next codes.  torch does the elementwise rest: the
+squared ReLU.
 
 The task: the next token is a fixed permutation of the current one, so the loss falls
 from log(vocab) towards zero.
@@ -81,6 +82,8 @@ class Model:
         self.ws = new(need, torch.uint8)
         self.ws_embed = new(bq.embed_grad_workspace(tokens, vocab, width), torch.uint8)
         self.ws_norm = new(bq.rmsnorm_grad_workspace(tokens, width), torch.uint8)
+        self.ws_loss = new(bq.loss_fp8_workspace(tokens, vocab, width), torch.uint8)
+        self.ws_loss_grad = new(bq.loss_fp8_grad_workspace(tokens, vocab, width), torch.uint8)
         self.t = 0
 
     # ------------------------------------------------------------------ parameters as gathered
@@ -129,7 +132,8 @@ class Model:
 
     # ------------------------------------------------------------------ one step
 
-    def forward(self, ids):
+    def encode(self, ids):
+        """The last norm's FP8 rows, and what the backward pass needs."""
         x, h, tape = self._rows(self.width), None, []
         codes, scales = self.weight("embed")
         bq.embed(codes, ids, x, table_scale=scales)
@@ -142,12 +146,20 @@ class Model:
             x = self._linear(f"down{i}", inner)
             tape.append((norm, rows, u, inner))
         _, norm, rows = self._norm("norm", x, h)
-        return self._linear("head", rows), (tape, norm, rows)
+        return rows, (tape, norm, rows)
+
+    def forward(self, ids):
+        rows, saved = self.encode(ids)
+        return self._linear("head", rows), saved
 
     def backward(self, ids, dlogits, saved):
         """Fills self.grads from the gradient of the logits."""
-        tape, norm, rows = saved
-        dh = self._norm_grad(norm, self._linear_grad("head", dlogits, rows), None)
+        self.backward_rows(ids, self._linear_grad("head", dlogits, saved[2]), saved)
+
+    def backward_rows(self, ids, drows, saved):
+        """Fills self.grads but for the head's from the gradient of the last norm's output."""
+        tape, norm, _ = saved
+        dh = self._norm_grad(norm, drows, None)
         for i in reversed(range(self.layers)):
             norm, rows, u, inner = tape[i]
             da = self._linear_grad(f"down{i}", dh, inner)
@@ -155,23 +167,45 @@ class Model:
             dh = self._norm_grad(norm, self._linear_grad(f"up{i}", du, rows), dh)
         bq.embed_grad(dh, ids, self.grads["embed"], self.ws_embed)
 
-    def step(self, ids, targets, lr, eps):
-        logits, saved = self.forward(ids)
-        log_p = torch.log_softmax(logits.float(), 1)
-        loss = -log_p.gather(1, targets[:, None]).mean()
-        d = log_p.exp()
-        d[torch.arange(self.n, device=self.dev), targets] -= 1
-        self.backward(ids, (d / self.n).bfloat16(), saved)
+    def _vector(self):
+        return torch.empty(self.n, device=self.dev)
+
+    def cross_entropy(self, rows, targets, dloss):
+        """Each token's loss and the gradient of rows; fills the head's."""
+        head, loss, lse, dx = (*rows, *self.weight("head")), self._vector(), self._vector(), self._rows(self.width)
+        bq.cross_entropy_fp8(*head, targets, loss, lse, self.ws_loss)
+        bq.cross_entropy_fp8_grad(*head, targets, loss, lse, dloss, dx, self.grads["head"], self.ws_loss_grad)
+        return loss, dx
+
+    def distill(self, rows, ids, teacher, dloss, temperature=1.0):
+        """The same against a teacher's top logits: ids and teacher [tokens, k]."""
+        head, loss, lse, dx = (*rows, *self.weight("head")), self._vector(), self._vector(), self._rows(self.width)
+        logp = torch.empty(ids.shape, device=self.dev)
+        bq.distill_fp8(*head, ids, teacher, loss, lse, logp, self.ws_loss, scale=1 / temperature)
+        bq.distill_fp8_grad(*head, ids, teacher, lse, logp, dloss, dx, self.grads["head"], self.ws_loss_grad,
+                            scale=1 / temperature)
+        return loss, dx
+
+    def step(self, ids, targets, lr, eps, teacher=None):
+        """One step on targets, or, with the teacher's logits [tokens, k] of them, on targets [tokens, k]."""
+        rows, saved = self.encode(ids)
+        dloss = torch.full((self.n,), 1 / self.n, device=self.dev)
+        if teacher is None:
+            loss, dx = self.cross_entropy(rows, targets, dloss)
+        else:
+            loss, dx = self.distill(rows, targets, teacher, dloss)
+        self.backward_rows(ids, dx, saved)
         self.t += 1
         bq.pack(self.shard, self.grad_ptrs, self.dbuf, 1.0)
         hp = bq.adam_hparams(lr, 0.9, 0.95, eps, self.t)
         bq.step_adam8(self.shard, self.dbuf, self.master, self.m, self.v, self.m_scale, self.v_scale, hp, self.codes,
                       self.scales)
-        return loss
+        return loss.mean()
 
     def check(self):
         """Raises if a device wait of the steps so far gave up."""
-        bq.linear_check(self.ws)
+        for ws in (self.ws, self.ws_loss, self.ws_loss_grad):
+            bq.linear_check(ws)
         bq.shard_check(self.shard)
 
 

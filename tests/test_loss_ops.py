@@ -203,11 +203,10 @@ class Head:
             du = d[:, None] * (p + u) + 2.0 ** -19 * O.weights_of(self.pairs, self.rows)
         du = g[:, None] * (du + 2.0 ** -39)
         if dx is not None:
-            # at most 42 tokens: u as three E4M3 terms, off by 2^-12 of itself and 2^-25 of its 128 words' largest
+            # few tokens' u as three E4M3 terms, off by 2^-12 of itself and 2^-25 of its 128 words' largest
             few = np.zeros_like(u)
-            if self.n <= 42:
-                for j in range(0, self.rows, 128):
-                    few[:, j:j + 128] = 2.0 ** -25 * u[:, j:j + 128].max(axis=1, keepdims=True)
+            for j in range(0, self.rows, 128):
+                few[:, j:j + 128] = 2.0 ** -25 * u[:, j:j + 128].max(axis=1, keepdims=True)
             by = (du + g[:, None] * few) @ np.abs(self.w64) + (2.2 * H + (self.rows + 8) * 2.0 ** -23) * size_x
             near(f64(dx), want_x, by + U * 1.001 * np.abs(want_x) + U * by)
             assert np.all(f64(dx)[~some] == 0)
@@ -220,7 +219,7 @@ class Head:
             near(f64(dw), want, by + U * 1.001 * np.abs(want) + U * by)
 
 
-SIZES = [(1, 1, 16), (42, 1300, 160), (43, 1300, 160), (1, 130, 128), (2, 300, 144), (7, 256, 272), (33, 1000, 512), (128, 257, 128), (129, 640, 256),
+SIZES = [(1, 1, 16), (42, 1300, 160), (43, 1300, 160), (85, 9000, 144), (1, 130, 128), (2, 300, 144), (7, 256, 272), (33, 1000, 512), (128, 257, 128), (129, 640, 256),
          (200, 2049, 400), (300, 4100, 1040), (520, 1500, 2064)]
 
 
@@ -295,3 +294,382 @@ def test_gradients_in_pieces(cuda):
     size_x, size_w = u.abs() @ w64.abs(), u.abs().t() @ x64.abs()
     assert bool(((dx.double() - want_x).abs() <= U * 1.01 * want_x.abs() + 2.5 * H * size_x).all())
     assert bool(((dw.double() - want_w).abs() <= U * 1.01 * want_w.abs() + 2.5 * H * size_w).all())
+
+
+# ----------------------------------------------------------------------------- layouts
+
+
+@pytest.mark.parametrize("k,teacher", [(None, None), (6, "bf16")])
+@pytest.mark.parametrize("n,rows,cols", [(5, 300, 144), (150, 1000, 272), (400, 2500, 512)])
+def test_pitches_and_alignments(cuda, n, rows, cols, k, teacher):
+    """Rows with spare columns (NaN codes, NaN scales), ids and logits inside wider matrices, outputs at odd
+    addresses whose surroundings stay as they were."""
+    import torch
+
+    for pitch, spare, shift, out_pitch in ((16, 3, 1, 5), (32, 1, 2, 2), (0, 4, 4, 4), (0, 0, 0, 24)):
+        c = Head(cuda, n, rows, cols, k=k, teacher=teacher, pitch=pitch, spare=spare, seed=pitch)
+        c.forward()
+        c.check_forward()
+        g = c.rng.standard_normal(n).astype(np.float32)
+        dx, fx = empty(n, cols, cuda, torch.bfloat16, out_pitch, shift)
+        dw, fw = empty(rows, cols, cuda, torch.bfloat16, out_pitch, shift)
+        c.grad(torch.as_tensor(g).to(cuda), dx, dw)
+        c.check_grads(g, dx, dw)
+        assert outside_kept(dx, fx, shift) and outside_kept(dw, fw, shift)
+
+
+@pytest.mark.parametrize("n,rows,cols", [(3, 400, 128), (140, 900, 256), (1500, 500, 256)])
+def test_one_output_and_accumulation(cuda, n, rows, cols):
+    import torch
+
+    c = Head(cuda, n, rows, cols, seed=2).forward()
+    g = torch.as_tensor(c.rng.standard_normal(n).astype(np.float32)).to(cuda)
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(g, dx, dw)
+    x, w = torch.empty_like(dx), torch.empty_like(dw)
+    c.grad(g, x, None)
+    c.grad(g, None, w)
+    assert torch.equal(x, dx) and torch.equal(w, dw)
+    old = torch.as_tensor(c.rng.standard_normal((rows, cols)).astype(np.float32)).to(cuda).bfloat16()
+    w.copy_(old)
+    c.grad(g, x, w, accumulate=True)
+    assert torch.equal(x, dx)  # never added to
+    c.check_grads(f64(g), x, w, old=f64(old))
+
+
+def test_no_tokens(cuda):
+    import torch
+
+    c = Head(cuda, 1, 30, 32)
+    none = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device=cuda)  # noqa: E731
+    head = none(0, 32, t=torch.uint8), none(1, 0), c.w, c.ws_
+    dw = torch.full((30, 32), 3.0, dtype=torch.bfloat16, device=cuda)
+    ws, wg = workspace(bq.loss_fp8_workspace(0, 30, 32), cuda), workspace(bq.loss_fp8_grad_workspace(0, 30, 32), cuda)
+    bq.cross_entropy_fp8(*head, none(0, t=torch.int64), none(0), none(0), ws)
+    bq.cross_entropy_fp8_grad(*head, none(0, t=torch.int64), none(0), none(0), none(0), none(0, 32, t=torch.bfloat16), dw, wg,
+                              accumulate=True)
+    assert bool((dw == 3).all())
+    bq.distill_fp8_grad(*head, none(0, 4, t=torch.int32), none(0, 4), none(0), none(0, 4), none(0), None, dw, wg)
+    assert not dw.any()
+
+
+# ----------------------------------------------------------------------------- masks, infinities, sure predictions
+
+
+@pytest.mark.parametrize("n", [6, 150, 600])
+@pytest.mark.parametrize("k", [None, 4])
+def test_rows_without_a_target_hold_anything(cuda, n, k):
+    """NaN codes, NaN and infinite scales, dloss and logits in rows without a target reach nothing but those
+    rows' own log-sums."""
+    import torch
+
+    rows, cols = 700, 256
+
+    def none(c):
+        if k is None:
+            c.targets[1::3] = -1
+        else:
+            c.ids[1::3] = -1
+            c.z[1::3] = float("nan")
+            c.z[2, :] = -np.inf  # every weight 0: no target either
+            c.z[0, 1] = -np.inf
+
+    c = Head(cuda, n, rows, cols, k=k, seed=5, edit=none)
+    some = c.pairs[2].any(axis=1)
+    g = c.rng.standard_normal(n).astype(np.float32)
+    out = []
+    for broken in (False, True):
+        if broken:
+            c.x[1::3] = 0x7F
+            c.xs[:, 1::3] = float("nan")
+            c.xs[0, 4::6] = float("inf")
+            g[~some] = np.where(np.arange((~some).sum()) % 2, np.nan, np.inf)
+        c.forward()
+        dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+        c.grad(torch.as_tensor(g).to(cuda), dx, dw)
+        assert np.all(f64(c.loss)[~some] == 0) and np.all(f64(dx)[~some] == 0)
+        out.append([f64(t) for t in (c.loss, c.lse[torch.as_tensor(some).to(cuda)], dx, dw)])
+    assert all(np.array_equal(a, b) for a, b in zip(*out))
+    c.check_grads(np.where(some, g, 0), dx, dw)
+
+
+@pytest.mark.parametrize("n", [4, 200])
+def test_a_row_of_nan_stays_alone(cuda, n):
+    import torch
+
+    rows, cols = 500, 144
+    c = Head(cuda, n, rows, cols, seed=6, edit=lambda c: c.targets.__setitem__(slice(None), np.arange(n) % rows))
+    c.x[2, 5] = 0x7F
+    c.forward()
+    bad = np.arange(n) == 2
+    for t in (c.loss, c.lse):
+        assert np.array_equal(np.isnan(f64(t)), bad)
+    dx = empty(n, cols, cuda, torch.bfloat16)[0]
+    dw = empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(torch.ones(n, device=cuda), dx, dw)
+    assert np.array_equal(np.isnan(f64(dx)).any(axis=1), bad) and np.isnan(f64(dx)[2]).all()
+    assert np.isnan(f64(dw)).all()  # a sum over tokens, that one among them
+
+
+def test_a_weight_of_nan_reaches_every_row_with_a_target(cuda):
+    import torch
+
+    for n in (3, 300):
+        c = Head(cuda, n, 400, 128, seed=7, edit=lambda c: c.targets.__setitem__(0, -1))
+        c.w[133, 7] = 0xFF
+        c.forward()
+        some = c.pairs[2].any(axis=1)
+        assert np.array_equal(np.isnan(f64(c.loss)), some)
+        dx = empty(n, 128, cuda, torch.bfloat16)[0]
+        c.grad(torch.ones(n, device=cuda), dx, None)
+        assert np.array_equal(np.isnan(f64(dx)).any(axis=1), some) and np.all(f64(dx)[~some] == 0)
+
+
+def test_sure_predictions_and_ties(cuda):
+    """Losses far below what fp32 holds beside 1, and equal logits (the same words several times)."""
+    import torch
+
+    n, rows, cols = 40, 900, 128
+
+    c = Head(cuda, n, rows, cols, scale=6.0, seed=8)
+    c.forward().check_forward()
+    loss, _, _ = O.loss(c.logits, c.pairs)
+    assert np.sum((loss > 0) & (loss < 1e-6)) >= 3
+    g = c.rng.standard_normal(n).astype(np.float32)
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(torch.as_tensor(g).to(cuda), dx, dw)
+    c.check_grads(g, dx, dw)
+    # every word the same: each has the probability 1 / rows, whichever the target
+    c.w[:] = c.w[:1].clone()
+    c.ws_[:] = 0.01
+    c.forward()
+    some = c.pairs[2].any(axis=1)
+    # (exact but for the log, the sum of 899 ones and the difference to a logit read apart: 6e-8 of each)
+    z = np.abs(f64(c.lse)) + 1
+    assert np.all(np.abs(f64(c.loss) - np.log(rows))[some] <= 1e-5 * z[some])
+
+
+@pytest.mark.parametrize("n", [3, 70])
+def test_teachers(cuda, n):
+    """One id many times, the most pairs, logits of the type's lowest value and infinities beside others."""
+    import torch
+
+    rows, cols, k = 600, 128, 1024
+
+    def edit(c):
+        c.ids[0] = 17
+        c.ids[1, :] = np.arange(k) % 9
+        c.z[1, ::2] = torch.finfo(torch.float32).min
+        c.z[2] = torch.finfo(torch.float32).min
+        c.ids[2] = np.arange(k) % rows
+
+    c = Head(cuda, n, rows, cols, scale=0.5, k=k, seed=9, edit=edit)
+    c.forward().check_forward()
+    g = c.rng.standard_normal(n).astype(np.float32)
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(torch.as_tensor(g).to(cuda), dx, dw)
+    c.check_grads(g, dx, dw)
+
+
+def test_one_pair_of_weight_one_is_a_class(cuda):
+    """A teacher that knows one word says what a class says."""
+    import torch
+
+    n, rows, cols = 130, 800, 256
+    a = Head(cuda, n, rows, cols, seed=10).forward()
+    g = torch.as_tensor(a.rng.standard_normal(n).astype(np.float32)).to(cuda)
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    a.grad(g, dx, dw)
+    want = [f64(t) for t in (a.loss, a.lse, dx, dw)]
+    a.k, a.t, a.z = 1, a.t[:, None].contiguous(), torch.zeros(n, 1, device=cuda)
+    a.forward()
+    a.grad(g, dx, dw)
+    for got, w in zip((a.loss, a.lse, dx, dw), want):
+        # (the target's logit is read by the same code; q is 1 and log q 0)
+        near(f64(got), w, 2 * U * np.abs(w) + 1e-30 if got.dtype == torch.bfloat16 else 4 * E * np.abs(w))
+
+
+# ----------------------------------------------------------------------------- derivatives of the kernels' own losses
+
+
+@pytest.mark.parametrize("k", [None, 8])
+def test_gradients_match_differences_of_the_losses(cuda, k):
+    """The losses' derivative along the factor of the logits is sum(dx * x) / scale, and sum(dw * w) / scale."""
+    import torch
+
+    n, rows, cols, d = 300, 3000, 512, 2.0 ** -6
+    c = Head(cuda, n, rows, cols, k=k, seed=11)
+    if k:
+        c.z.zero_()  # (the teacher's softmax has the factor too: q the same for all)
+        c.pairs = O.teacher_pairs(c.ids, np.zeros((n, k)), 1.0, rows)
+    g = torch.rand(n, device=cuda) / n
+    totals = {}
+    for f in (1 - d, 1 + d, 1 - 2 * d, 1 + 2 * d, 1.0):
+        c.scale = f
+        c.forward()
+        totals[f] = float((c.loss.double() * g.double()).sum())
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(g, dx, dw)
+    slope = (8 * (totals[1 + d] - totals[1 - d]) - (totals[1 + 2 * d] - totals[1 - 2 * d])) / (12 * d)
+    by_x, by_w = float((f64(dx) * c.x64).sum()), float((f64(dw) * c.w64).sum())
+    # the differences are off by their fifth derivative's d^4 / 30 and the losses' 1e-6 / d; the sums by
+    # the roundings of dx and dw, 2^-9 of each term at random
+    for got, terms in ((by_x, f64(dx) * c.x64), (by_w, f64(dw) * c.w64)):
+        assert abs(got - slope) <= 2e-4 * abs(slope) + 1e-4 + 6 * U * np.sqrt(np.sum(terms ** 2))
+
+
+# ----------------------------------------------------------------------------- streams, graphs, workspaces, offsets
+
+
+@pytest.mark.parametrize("k", [None, 5])
+def test_one_workspace_another_stream_and_graphs(cuda, k):
+    """Sizes and inputs in turn on one workspace, on a stream of its own, and in two captured graphs that share
+    it, replayed on new inputs: the bits of calls with workspaces of their own."""
+    import torch
+
+    sizes = [(2, 900, 144), (50, 2000, 256), (300, 1500, 512), (700, 700, 272), (1100, 3000, 256)]
+    cases = [[Head(cuda, *s, k=k, seed=20 + i) for i in range(2)] for s in sizes]
+    need = max(max(bq.loss_fp8_workspace(*s), bq.loss_fp8_grad_workspace(*s)) for s in sizes)
+    shared = workspace(need, cuda)
+
+    def buffers(c):
+        new = lambda *s, t=torch.float32: torch.full(s, 9.0, dtype=t, device=cuda)  # noqa: E731
+        b = dict(loss=new(c.n), lse=new(c.n), dx=new(c.n, c.cols, t=torch.bfloat16), dw=new(c.rows, c.cols, t=torch.bfloat16),
+                 g=torch.linspace(-1, 1, c.n, device=cuda))
+        if k:
+            b["logp"] = new(c.n, k)
+        return b
+
+    def step(c, b, ws):
+        if k is None:
+            bq.cross_entropy_fp8(*c.head, c.t, b["loss"], b["lse"], ws)
+            bq.cross_entropy_fp8_grad(*c.head, c.t, b["loss"], b["lse"], b["g"], b["dx"], b["dw"], ws)
+        else:
+            bq.distill_fp8(*c.head, c.t, c.z, b["loss"], b["lse"], b["logp"], ws)
+            bq.distill_fp8_grad(*c.head, c.t, c.z, b["lse"], b["logp"], b["g"], b["dx"], b["dw"], ws)
+
+    want = {}
+    for i, pair in enumerate(cases):
+        for j, c in enumerate(pair):
+            b = buffers(c)
+            step(c, b, workspace(need, cuda, fill=0x3C))
+            want[i, j] = {name: t.clone() for name, t in b.items()}
+    same = lambda b, w: all(torch.equal(b[name], w[name]) for name in w)  # noqa: E731
+    for _ in range(3):
+        for i, pair in enumerate(cases):
+            for j, c in enumerate(pair):
+                b = buffers(c)
+                step(c, b, shared)
+                assert same(b, want[i, j]), (i, j)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i, pair in enumerate(cases):
+            b = buffers(pair[0])
+            step(pair[0], b, shared)
+            assert same(b, want[i, 0])
+    side.synchronize()
+
+    graphs = []
+    for i in (1, 3):  # (their inputs are copied in before each replay)
+        c, b = cases[i][0], buffers(cases[i][0])
+        held = [t.clone() for t in (*c.head, c.t)] + ([c.z.clone()] if k else [])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(c, b, shared)
+        graphs.append((i, graph, b, held))
+    for turn in range(3):
+        for i, graph, b, held in graphs:
+            j = (turn + i) % 2
+            c, src = cases[i][0], cases[i][j]
+            fresh = held if j == 0 else [*src.head, src.t] + ([src.z] if k else [])
+            for to, t in zip([*c.head, c.t] + ([c.z] if k else []), fresh):
+                to.copy_(t)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert same(b, want[i, j]), (turn, i)
+    bq.linear_check(shared)
+
+
+def test_offsets_past_32_bits(cuda):
+    """A head of more than 2^31 codes, whose gradient has more than 2^32 bytes: targets among its last words."""
+    import torch
+
+    rows, cols, n = 263000, 8192, 5
+    assert rows * cols > 2 ** 31
+    gen = torch.Generator(device=cuda).manual_seed(1)
+    w = torch.randint(0, 0x58, (rows, cols), generator=gen, device=cuda, dtype=torch.uint8)
+    w[-3000:] |= 0x80
+    ws_ = torch.full((-(-rows // 128), cols // 128), 2.0 ** -9, device=cuda)
+    x = torch.randint(0, 0x50, (n, cols), generator=gen, device=cuda, dtype=torch.uint8)
+    xs = torch.full((cols // 128, n), 2.0 ** -10, device=cuda)
+    y = torch.tensor([rows - 1, rows - 2999, 0, -1, rows], device=cuda)
+    loss, lse, g = torch.empty(n, device=cuda), torch.empty(n, device=cuda), torch.tensor([1.0, -2.0, 0.5, 3.0, 1.0], device=cuda)
+    bq.cross_entropy_fp8(x, xs, w, ws_, y, loss, lse, workspace(bq.loss_fp8_workspace(n, rows, cols), cuda))
+    dx = torch.empty(n, cols, dtype=torch.bfloat16, device=cuda)
+    dw = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device=cuda)
+    bq.cross_entropy_fp8_grad(x, xs, w, ws_, y, loss, lse, g, dx, dw, workspace(bq.loss_fp8_grad_workspace(n, rows, cols), cuda))
+    x64 = x.view(torch.float8_e4m3fn).double() * 2.0 ** -10
+    z = torch.cat([x64 @ (w[i:i + 20000].view(torch.float8_e4m3fn).double() * 2.0 ** -9).t() for i in range(0, rows, 20000)], 1)
+    want = torch.logsumexp(z, 1)
+    assert float((lse.double() - want).abs().max()) < 1e-5
+    seen = [0, 1, 2]
+    for t in seen:
+        assert abs(float(loss[t]) - float(want[t] - z[t, y[t]])) < 1e-5
+    u = torch.exp(z - want[:, None])
+    for t in seen:
+        u[t, y[t]] -= 1
+    u *= torch.where((y >= 0) & (y < rows), g, 0).double()[:, None]
+    for part in (slice(0, 300), slice(rows - 3100, rows)):
+        ref = u[:, part].t() @ x64
+        size = u[:, part].abs().t() @ x64.abs()
+        assert bool(((dw[part].double() - ref).abs() <= U * 1.01 * ref.abs() + 2.5 * H * size).all())
+    ref = sum(u[:, i:i + 20000] @ (w[i:i + 20000].view(torch.float8_e4m3fn).double() * 2.0 ** -9) for i in range(0, rows, 20000))
+    size = sum(u[:, i:i + 20000].abs() @ (w[i:i + 20000].view(torch.float8_e4m3fn).double().abs() * 2.0 ** -9)
+               for i in range(0, rows, 20000))
+    assert bool(((dx.double() - ref).abs() <= U * 1.01 * ref.abs() + 2.5 * H * size).all())
+    assert not dx[3:].any()
+    assert bool(torch.isfinite(dw.view(torch.int16)[::1000].view(torch.bfloat16)).all())
+
+
+# ----------------------------------------------------------------------------- as a model uses them
+
+
+@pytest.mark.parametrize("k", [None, 6])
+def test_the_example_models_head(cuda, k):
+    """The last norm's rows, the loss and its gradients as a training step runs them, against fp64 on the same
+    FP8 rows and weights."""
+    import os
+    import sys
+
+    import torch
+
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from fp8_lm import Model
+
+    vocab, width, n = 900, 256, 300
+    m = Model(vocab, width, 256, 1, n, cuda, seed=3)
+    ids = torch.randint(0, vocab, (n,), device=cuda)
+    rows, _ = m.encode(ids)
+    c = Head.__new__(Head)
+    codes, scales = m.weight("head")
+    c.x64, c.w64 = L.decode_rows(rows[0].cpu().numpy(), rows[1].cpu().numpy()), L.decode_tiles(codes.cpu().numpy(), scales.cpu().numpy())
+    c.n, c.rows, c.cols, c.k, c.scale, c.dev = n, vocab, width, k, 1.0, cuda
+    c.logits, c.size = O.logits(c.x64, c.w64, 1.0)
+    c.off = (width + 4) * 2.0 ** -23 * c.size.max(axis=1)
+    rng = np.random.default_rng(0)
+    g = rng.random(n).astype(np.float32) / n
+    dloss = torch.as_tensor(g).to(cuda)
+    if k is None:
+        y = rng.integers(-1, vocab, n)
+        c.pairs = O.class_pairs(y, vocab)
+        loss, dx = m.cross_entropy(rows, torch.as_tensor(y).to(cuda), dloss)
+    else:
+        y, z = rng.integers(0, vocab, (n, k)), rng.standard_normal((n, k)).astype(np.float32)
+        c.pairs = O.teacher_pairs(y, z, 1.0, vocab)
+        loss, dx = m.distill(rows, torch.as_tensor(y).to(cuda), torch.as_tensor(z).to(cuda), dloss)
+    want, lse, c_logp = O.loss(c.logits, c.pairs)
+    near(f64(loss), want, 2e-5 * (1 + np.abs(want)))
+    c.check_grads(g, dx, m.grads["head"])
+    m.step(ids, torch.as_tensor(y).to(cuda), 1e-3, 1e-4, teacher=None if k is None else torch.as_tensor(z).to(cuda))
+    m.check()
