@@ -79,9 +79,12 @@ struct LinArgs {
   uint8_t* at;
   const float *lse, *loss, *factor;
   const int* target;
-  int64_t ld_stats;
+  const uint32_t* records;
+  const uint16_t* words;
+  float* picked;
+  int64_t ld_stats, ld_records, ld_picked;
   float zscale;
-  int first, late;
+  int first, late, listed;
 };
 
 // One 128 x 128 tile of out per cluster; CTA r of the cluster's `split` sums its
@@ -105,6 +108,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   auto tfull_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * kMaxStages + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * uint32_t(2 * kMaxStages + 2 + b); };
 
+  constexpr bool STATS = END == kTileStats || END == kTilePicks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cluster_rank());
   const int tile = int(blockIdx.x) / g.split;
@@ -236,25 +240,33 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   }
   __syncwarp();
-  if constexpr (END == kTileStats) {
+  __syncthreads();  // the stages are free: every copy has landed and every product is done
+  float* part = reinterpret_cast<float*>(gbase);
+  if constexpr (STATS) {
     // whole sums leave from registers, a lane's row and half of the tile's columns each
     if (g.split == 1 && warp >= 2 && q < quarters) {
       const int row = m0 + 32 * q + lane, c0 = n0 + half * (BN / 2);
       if (c0 < g.width) {
         const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row;
+        const uint32_t* records = g.records + int64_t(c0 / kPartCols) * g.ld_records + row;
+        uint32_t record = 0;
+        if constexpr (END == kTilePicks)
+          if (row < g.n) record = __ldcg(records);
         lane_stats<kPartCols>(acc, g.width - c0, g.zscale, row < g.n, g.stats + at, g.at + at);
+        if constexpr (END == kTilePicks) {
+          lane_picks<kPartCols>(acc, record, records + g.ld_records, g.words + int64_t(row) * g.listed,
+                                g.picked + row * g.ld_picked, smem_addr(part) + 2048u * uint32_t(warp - 2), lane);
+        }
       }
     }
   }
-  __syncthreads();  // the stages are free: every copy has landed and every product is done
-  float* part = reinterpret_cast<float*>(gbase);
-  if (warp >= 2 && q < quarters && !(END == kTileStats && g.split == 1)) {
+  if (warp >= 2 && q < quarters && !(STATS && g.split == 1)) {
     float* prow = part + (32 * q + lane) * kPartPitch + half * (BN / 2);
 #pragma unroll
     for (int j = 0; j < BN / 2; ++j) prow[j] = acc[j];
   }
   cluster_sync();  // (every thread) the cluster's partial tiles are written
-  const int rows = END == kTileStats && g.split == 1 ? 0 : min(BM, g.n - m0), cols = min(BN, g.width - n0);
+  const int rows = STATS && g.split == 1 ? 0 : min(BM, g.n - m0), cols = min(BN, g.width - n0);
   // each CTA finishes its share of the tile's rows: lane l columns l, l + 32, ...
   const uint32_t part0 = smem_addr(part);
   // (probabilities: the log-sum and the class of the warp's i-th row come ahead, in lane i)
@@ -313,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int j = 0; j < BN / 32; ++j) v[j] += x[c][j];
       }
     }
-    if constexpr (END == kTileStats) {
+    if constexpr (STATS) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (kPartCols * h < cols) {
@@ -342,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  if ((END == kTileStats || END == kTileProbs) && g.late) after_previous();
+  if ((STATS || END == kTileProbs) && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -576,10 +588,21 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
         }
       }
       if (!ok) break;
-      if constexpr (END == kTileStats) {
+      if constexpr (END == kTileStats || END == kTilePicks) {
         if (c0 < g.width) {
           const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row0 + lane;
-          lane_stats<kPartCols>(acc, g.width - c0, g.zscale, row0 + lane < g.n, g.stats + at, g.at + at);
+          int row = row0 + lane;
+          // (what follows is not to be computed ahead of the k-blocks and held over them: with spills in their loop a tile took
+          // 1.3 us more of 14)
+          if constexpr (END == kTilePicks) asm volatile("" : "+r"(row));
+          const uint32_t* records = g.records + int64_t(c0 / kPartCols) * g.ld_records + row;
+          uint32_t record = 0;
+          if constexpr (END == kTilePicks)
+            if (row < g.n) record = __ldcg(records);
+          lane_stats<kPartCols>(acc, g.width - c0, g.zscale, row < g.n, g.stats + at, g.at + at);
+          if constexpr (END == kTilePicks)
+            lane_picks<kPartCols>(acc, record, records + g.ld_records, g.words + int64_t(row) * g.listed, g.picked + row * g.ld_picked,
+                                  base + OFF_OUT + uint32_t(warp - 4) * OUT_BOX, lane);
         }
       } else {
         if constexpr (END == kTileProbs) lane_probs<PCOLS>(acc, g.width - c0, g.zscale, lse);
@@ -610,7 +633,7 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, kPairTmem);
   }
-  if ((END == kTileStats || END == kTileProbs) && g.late) after_previous();
+  if (END != kTileOut && g.late) after_previous();
 }
 
 // ---------------------------------------------------------------- weight gradient
@@ -967,6 +990,10 @@ LinearPlan linear_plan(int64_t n, int64_t width, int64_t red, int transposed) {
 }  // namespace
 
 bool linear_on_pairs(int64_t n, int64_t width, int64_t red) { return linear_plan(n, width, red, 0).pairs; }
+bool linear_whole_tiles(int64_t n, int64_t width, int64_t red) {
+  const LinearPlan p = linear_plan(n, width, red, 0);
+  return p.pairs || p.split == 1;
+}
 double linear_small_us(int64_t n, int64_t width, int64_t red) { return linear_plan(n, width, red, 1).us; }
 
 int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream) {
@@ -984,6 +1011,8 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
             cudaFuncSetAttribute(k_linear_pair<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear<false, kTilePicks>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+            cudaFuncSetAttribute(k_linear_pair<false, kTilePicks>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear<true, kTileTriples>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear_pair<false, kTileStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess ||
             cudaFuncSetAttribute(k_linear_pair<false, kTileProbs>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM) != cudaSuccess)
@@ -999,11 +1028,14 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   g.split = 1, g.stages = 0, g.a_rows = BM, g.bytes = store_bytes(a.out, a.ldo, width);
   g.stats = nullptr, g.at = nullptr, g.lse = nullptr, g.loss = nullptr, g.factor = nullptr, g.target = nullptr;
   g.ld_stats = 0, g.zscale = 1.f, g.first = 0, g.late = 0;
+  g.records = nullptr, g.words = nullptr, g.picked = nullptr, g.ld_records = g.ld_picked = 0, g.listed = 0;
   const int end = a.loss ? a.loss->end : int(kTileOut);
   if (a.loss) {
     g.stats = a.loss->stats, g.at = a.loss->at, g.ld_stats = a.loss->ld_stats, g.zscale = a.loss->zscale;
     g.lse = a.loss->lse, g.loss = a.loss->loss, g.target = a.loss->target, g.first = a.loss->first;
     g.factor = a.loss->factor, g.late = a.loss->late;
+    g.records = a.loss->records, g.words = a.loss->words, g.picked = a.loss->picked, g.ld_records = a.loss->ld_records;
+    g.ld_picked = a.loss->ld_picked, g.listed = a.loss->listed;
   }
   if (end != kTileOut) g.bytes = 16;
   const int nk = (red + BK - 1) / BK;
@@ -1023,10 +1055,11 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
       if (int rc = launch_copy_scales(a.x_scale, a.ld_xs, a.n, nk, a.scale_ws, ld, stream)) return rc;
       g.xs = a.scale_ws, g.ld_xs = ld;
     }
-    if (g.bytes == 16 && end != kTileStats)  // (probabilities: whole 16-byte words, zeros past the width)
+    if (g.bytes == 16 && end != kTileStats && end != kTilePicks)  // (probabilities: whole 16-byte words, zeros past the width)
       if (int rc = encode_map_bf16_out(&to, a.out, end == kTileProbs ? (width + 7) / 8 * 8 : width, a.n, a.ldo, 32)) return rc;
     void* args[] = {&tx, &tw, &to, &g};
     const void* k = end == kTileStats   ? reinterpret_cast<const void*>(k_linear_pair<false, kTileStats>)
+                    : end == kTilePicks ? reinterpret_cast<const void*>(k_linear_pair<false, kTilePicks>)
                     : end == kTileProbs ? reinterpret_cast<const void*>(k_linear_pair<false, kTileProbs>)
                     : a.transposed      ? reinterpret_cast<const void*>(k_linear_pair<true>)
                                         : reinterpret_cast<const void*>(k_linear_pair<false>);
@@ -1038,6 +1071,7 @@ int launch_linear_fp8(const LinearArgs& a, void* stream) {
   if (int rc = encode_map_codes(&tx, a.x, red, a.n, a.ldx, g.a_rows)) return rc;
   void* args[] = {&tx, &tw, &g};
   const void* k = end == kTileStats     ? reinterpret_cast<const void*>(k_linear<false, kTileStats>)
+                  : end == kTilePicks   ? reinterpret_cast<const void*>(k_linear<false, kTilePicks>)
                   : end == kTileProbs   ? reinterpret_cast<const void*>(k_linear<false, kTileProbs>)
                   : end == kTileTriples ? reinterpret_cast<const void*>(k_linear<true, kTileTriples>)
                   : a.transposed        ? reinterpret_cast<const void*>(k_linear<true>)

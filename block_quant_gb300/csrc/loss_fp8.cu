@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <string>
 
 #include "bq_internal.h"
@@ -75,19 +76,19 @@ struct Targets {
     const int64_t v = id_bits == 64 ? __ldg(static_cast<const long long*>(ids) + at) : int64_t(__ldg(static_cast<const int*>(ids) + at));
     return v >= 0 && v < rows ? int(v) : -1;
   }
-  // the teacher's logit, scaled
   __device__ __forceinline__ float logit(int64_t t, int i) const {
     const int64_t at = t * ld_teacher + i;
-    return scale * (teacher_kind == BQ_ROWS_FP32 ? __ldg(static_cast<const float*>(teacher) + at)
-                                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(teacher)[at]));
+    return teacher_kind == BQ_ROWS_FP32 ? __ldg(static_cast<const float*>(teacher) + at)
+                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(teacher)[at]);
   }
-  // a pair counts if its id is a word and the teacher gives it any weight
+  // a pair counts if its id is a word and the teacher gives it any weight; z: its logit times the factor
   __device__ __forceinline__ int kept_id(int64_t t, int i, float* z) const {
     const int v = id(t, i);
     *z = 0.f;
     if (!teacher || v < 0) return v;
-    *z = logit(t, i);
-    return *z == -INFINITY ? -1 : v;
+    const float l = logit(t, i);
+    *z = scale * l;
+    return l == -INFINITY ? -1 : v;
   }
 };
 
@@ -164,6 +165,72 @@ __device__ __forceinline__ void picked(const PickArgs& g, int64_t t, const int (
   for (int i = 0; i < P; ++i) z[i] = g.y.scale * warp_sum(sum[i]);
 }
 
+// Where the teacher's words are many, their logits are taken from the tiles of the product (kTilePicks) that holds
+// them anyway; this sorts each row's words and finds where each part of the vocabulary begins.  4096 tokens
+// of 32000 x 4096, 64 words each: 499 us in all so, 605 by k_loss_pick; 16 words each: 478 and 465.
+struct SortArgs {
+  Targets y;
+  uint32_t* records;  // [parts + 1][ld]
+  uint16_t* words;    // [n][k]
+  int64_t n, ld;
+  int parts;
+};
+constexpr int kSortFew = 256;  // words of a row at most, of 16 rows a CTA; of 4 rows kMaxPairs
+constexpr int kSortSlots = 16 * (kSortFew + 1);
+static_assert(4 * (kMaxPairs + 1) <= kSortSlots && 10 * kSortSlots <= 48 * 1024, "a CTA's words");
+
+__global__ void __launch_bounds__(1024) k_loss_sort(const SortArgs g) {
+  __shared__ int ids[kSortSlots], sorted[kSortSlots];
+  __shared__ uint16_t order[kSortSlots];
+  after_previous();
+  next_may_start();
+  const int k = g.y.k, pitch = k + 1, group = k <= kSortFew ? 16 : 4;
+  const int64_t t0 = int64_t(blockIdx.x) * group;
+  for (int i = threadIdx.x; i < group * k; i += 1024) {
+    const int r = i / k, j = i - r * k;
+    const int v = t0 + r < g.n ? g.y.id(t0 + r, j) : -1;
+    ids[r * pitch + j] = v < 0 ? INT_MAX : v;  // (last, in no part)
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < group * k; i += 1024) {
+    const int r = i / k, j = i - r * k, v = ids[r * pitch + j];
+    int rank = 0;
+    for (int e = 0; e < k; ++e) {
+      const int x = ids[r * pitch + e];
+      rank += x < v || (x == v && e < j);
+    }
+    sorted[r * pitch + rank] = v, order[r * pitch + rank] = uint16_t(j);
+    if (t0 + r < g.n) g.words[(t0 + r) * k + rank] = uint16_t(j << 6 | (v & 63));
+  }
+  __syncthreads();
+  // lanes along the rows: the place of row r's first word from 64 w on
+  const int r = int(threadIdx.x) % group;
+  if (t0 + r >= g.n) return;
+  const int* mine = sorted + r * pitch;
+  auto place = [&](int w) {
+    int lo = 0, hi = k;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (mine[mid] < w * kPartCols)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+  // (a thread's parts one after another, so that each search is one)
+  const int threads = 1024 / group, each = (g.parts + 1 + threads - 1) / threads;
+  const int w0 = int(threadIdx.x) / group * each, w1 = min(w0 + each, g.parts + 1);
+  int at = w0 < w1 ? place(w0) : 0;
+  for (int w = w0; w < w1; ++w) {
+    int next = at;
+    while (next < k && mine[next] < (w + 1) * kPartCols) ++next;
+    const uint32_t first = next > at ? uint32_t(order[r * pitch + at]) << 6 | uint32_t(mine[at] & 63) : 0u;
+    g.records[int64_t(w) * g.ld + t0 + r] = words_record(uint32_t(at), uint32_t(next - at), first);
+    at = next;
+  }
+}
+
 // The logits of the teacher's words, four a warp, by reading their rows of W: bound by those bytes.
 __global__ void __launch_bounds__(256) k_loss_pick(const PickArgs g) {
   after_previous();
@@ -193,7 +260,7 @@ struct JoinArgs {
   const uint8_t* at;
   int64_t ld_stats, n, ld_logp;
   float *loss, *lse, *logp;  // logp holds the targets' logits; a class's is taken here
-  int parts, group;  // group: rows of a CTA, 1, 2, .. 32
+  int parts, group;  // group: rows of a CTA, 1, 2, .. kJoinWarps
   PickArgs pick;
 };
 
@@ -202,9 +269,11 @@ __device__ __forceinline__ RowStats shuffled(const RowStats& a, int d) {
 }
 
 // A row's statistics from its parts', its log-sum, and its loss.
-__global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
-  __shared__ float sm[32][33], ss[32][33];
-  __shared__ int sa[32][33];
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) k_loss_join(const JoinArgs g) {
+  __shared__ float sm[kJoinWarps][kJoinWarps + 1], ss[kJoinWarps][kJoinWarps + 1];
+  __shared__ int sa[kJoinWarps][kJoinWarps + 1];
   after_previous();
   next_may_start();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -226,16 +295,16 @@ __global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
   RowStats a{-INFINITY, 0.f, 0};
   bool some = false;
   if (row < g.n)
-    for (int p0 = warp * each + lane / g.group; p0 < g.parts; p0 += 4 * 32 * each) {
+    for (int p0 = warp * each + lane / g.group; p0 < g.parts; p0 += 4 * kJoinWarps * each) {
       float2 v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int p = p0 + e * 32 * each;
+        const int p = p0 + e * kJoinWarps * each;
         if (p < g.parts) v[e] = g.stats[int64_t(p) * g.ld_stats + row];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int p = p0 + e * 32 * each;
+        const int p = p0 + e * kJoinWarps * each;
         if (p >= g.parts) continue;
         const RowStats b{v[e].x, v[e].y, p};
         a = some ? joined(a, b) : b;
@@ -247,9 +316,9 @@ __global__ void __launch_bounds__(1024) k_loss_join(const JoinArgs g) {
   if (lane < g.group) sm[warp][lane] = a.m, ss[warp][lane] = a.s, sa[warp][lane] = a.at;
   __syncthreads();
   if (!mine) return;
-  a = {sm[lane][warp], ss[lane][warp], sa[lane][warp]};
+  a = {sm[lane % kJoinWarps][warp], ss[lane % kJoinWarps][warp], sa[lane % kJoinWarps][warp]};
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) a = joined(a, shuffled(a, d));
+  for (int d = 1; d < kJoinWarps; d <<= 1) a = joined(a, shuffled(a, d));
   const int best = a.at * kPartCols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
   const float more = log1pf(a.s);
   if (lane == 0) g.lse[t] = a.m + more;
@@ -470,29 +539,32 @@ __global__ void __launch_bounds__(256) k_loss_split(const SplitArgs g) {
   const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (i >= int64_t(g.n) * groups) return;
   const int t = int(i / groups), j = int(i - int64_t(t) * groups), c = 128 * j + 4 * lane;
-  float v[4], top = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = c + e < g.len ? __half2float(g.u[t * g.ldu + c + e]) : 0.f;
-    top = fmaxf(top, fabsf(v[e]));
-  }
-  top = warp_max(top);
+  // (whole words: U's pitch covers them)
+  const uint2 q = c < g.ldu ? *reinterpret_cast<const uint2*>(g.u + t * g.ldu + c) : make_uint2(0u, 0u);
+  float2 v[2] = {__half22float2(*reinterpret_cast<const __half2*>(&q.x)), __half22float2(*reinterpret_cast<const __half2*>(&q.y))};
+  if (c >= g.len) v[0].x = 0.f;
+  if (c + 1 >= g.len) v[0].y = 0.f;
+  if (c + 2 >= g.len) v[1].x = 0.f;
+  if (c + 3 >= g.len) v[1].y = 0.f;
+  float top = warp_max(fmaxf(fmaxf(fabsf(v[0].x), fabsf(v[0].y)), fmaxf(fabsf(v[1].x), fabsf(v[1].y))));
   // 2^e, e the least with top <= 448 * 2^e (top is an fp16 value: 2^-24 at least unless it is 0)
   int e0 = top > 0.f && top <= 65504.f ? ilogbf(top) - 8 : 0;
   if (top > ldexpf(448.f, e0)) ++e0;
+  const int64_t row = int64_t(t / kTokensOfTile) * 128 + 3 * (t % kTokensOfTile);
+  float s = ldexpf(1.f, e0), back = ldexpf(1.f, -e0);
 #pragma unroll
   for (int term = 0; term < 3; ++term) {
-    const float s = top <= 65504.f ? ldexpf(1.f, e0 - 4 * term) : top, back = ldexpf(1.f, 4 * term - e0);
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t q = uint8_t(__nv_cvt_float_to_fp8(v[e] * back, __NV_SATFINITE, __NV_E4M3));
-      v[e] -= __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3))) * s;
-      w |= uint32_t(q) << (8 * e);
+    for (int e = 0; e < 2; ++e) {
+      const __nv_fp8x2_storage_t code = __nv_cvt_float2_to_fp8x2(mul2(v[e], dup(back)), __NV_SATFINITE, __NV_E4M3);
+      const float2 d = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3)));
+      v[e] = fma2(d, dup(-s), v[e]);  // (exact)
+      w |= uint32_t(code) << (16 * e);
     }
-    const int64_t row = int64_t(t / kTokensOfTile) * 128 + 3 * (t % kTokensOfTile) + term;
-    if (c < g.ldc) *reinterpret_cast<uint32_t*>(g.codes + row * g.ldc + c) = w;
-    if (lane == 0) g.scale[int64_t(j) * g.lds + row] = s;
+    if (c < g.ldc) *reinterpret_cast<uint32_t*>(g.codes + (row + term) * g.ldc + c) = w;
+    if (lane == 0) g.scale[int64_t(j) * g.lds + row + term] = top <= 65504.f ? s : top;
+    s *= 0.0625f, back *= 16.f;
   }
 }
 
@@ -962,17 +1034,29 @@ int64_t up_to(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 size_t scale_bytes(int64_t n, int64_t cols) { return up(size_t((cols + 127) / 128) * size_t(up_to(n, 4)) * 4); }
 
 struct ForwardWs {
-  size_t scales, stats, at, bytes;
+  size_t scales, stats, at, records, words, bytes;
 };
 
-ForwardWs forward_ws(int64_t n, int64_t rows, int64_t cols) {
+// k: a teacher's words taken from the tiles, 0 for none
+ForwardWs forward_ws(int64_t n, int64_t rows, int64_t cols, int64_t k) {
   ForwardWs p;
   const size_t parts = size_t((rows + kPartCols - 1) / kPartCols);
   p.scales = kStatus;
   p.stats = p.scales + scale_bytes(n, cols);
   p.at = p.stats + up(parts * size_t(n) * 8);
-  p.bytes = p.at + up(parts * size_t(n));
+  p.records = p.at + up(parts * size_t(n));
+  p.words = p.records + (k ? up((parts + 1) * size_t(n) * 4) : 0);
+  p.bytes = p.words + up(size_t(n) * size_t(k) * 2);
   return p;
+}
+
+// Whether a teacher's words are sorted and taken from the tiles, by the times of 32 losses: where three quarters of what
+// reading their rows of W takes (5 TB/s) are more than the sort (10 us, 0.18 a word of a row, and its records) and 0.9 us
+// a round of tiles for looking at the records.
+bool from_tiles(int64_t n, int64_t rows, int64_t cols, int64_t k) {
+  const double pick = double(n) * double(k) * double(cols) / 5e6, sort = 10 + 0.18 * double(k) + double(n) * double(rows) / 64 / 0.6e6;
+  const double rounds = double((n + PM - 1) / PM) * double((rows + PN - 1) / PN) / cluster_slots()[2];
+  return 0.75 * pick > sort + 0.9 * rounds && linear_whole_tiles(n, rows, cols);
 }
 
 struct GradWs {
@@ -990,8 +1074,8 @@ int64_t piece_len(const GradWs& p, int64_t rows, int i) { return std::min(p.piec
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 
 // The tiles left over after whole waves in the parts that cost least: a round of parts takes 0.29 us a k-block (as
-// a projection's weight gradient), and a share is stored and added up.
-Shares dx_shares(int64_t n, int64_t cols, int64_t piece) {
+// a projection's weight gradient), and a share is stored and added up.  us: what the product takes.
+Shares dx_shares(int64_t n, int64_t cols, int64_t piece, double* us = nullptr) {
   Shares sh;
   const int pairs = cluster_slots()[2], nk = int((piece + DK - 1) / DK);
   sh.tiles = int(((n + PM - 1) / PM) * ((cols + PN - 1) / PN));
@@ -999,20 +1083,21 @@ Shares dx_shares(int64_t n, int64_t cols, int64_t piece) {
   sh.parts = 1;
   const int left = sh.left();
   double least = 0;
-  for (int parts = 1; left && parts <= std::min(nk, 24); ++parts) {
-    const double us = 0.29 * ((nk + parts - 1) / parts) * ((left * parts + pairs - 1) / pairs) + parts * (0.25 + 0.045 * left);
-    if (parts == 1 || us < least) least = us, sh.parts = parts;
+  for (int parts = 1; left && parts <= std::min(nk, 64); ++parts) {
+    const double t = 0.29 * ((nk + parts - 1) / parts) * ((left * parts + pairs - 1) / pairs) + parts * (0.25 + 0.045 * left);
+    if (parts == 1 || t < least) least = t, sh.parts = parts;
   }
+  if (us) *us = least + 0.29 * nk * (sh.whole / pairs);
   return sh;
 }
 
-// Whether dx takes three E4M3 terms of U: where the FP8 product of three rows a token costs less than
-// W in fp16 (3 bytes a value at 5.3 TB/s) and its product (0.29 us a k-block and round of tiles).
+// Whether dx takes three E4M3 terms of U: where splitting U (5 bytes a value at 4 TB/s) and the FP8 product of three
+// rows a token cost less than W in fp16 (3 bytes a value at 6 TB/s) and its product.
 bool few_tokens(int64_t n, int64_t rows, int64_t cols) {
   if (n * rows * 2 > kPieceBytes) return false;
-  const double tiles = double((n + PM - 1) / PM) * double((cols + PN - 1) / PN);
-  const double rounds = std::max(tiles / cluster_slots()[2], 0.25);
-  return linear_small_us(triple_rows(n), cols, rows) < double(rows) * double(cols) * 3 / 5.3e6 + 0.29 * rounds * double(rows) / DK;
+  double us = 0;
+  dx_shares(n, cols, rows, &us);
+  return double(n) * double(rows) * 5 / 4e6 + linear_small_us(triple_rows(n), cols, rows) < double(rows) * double(cols) * 3 / 6e6 + 3 + us;
 }
 
 GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
@@ -1057,13 +1142,15 @@ unsigned ctas_for(int64_t items, int64_t each, int64_t most) {
 
 }  // namespace
 
-size_t loss_bytes(int64_t n, int64_t rows, int64_t cols) { return forward_ws(n, rows, cols).bytes; }
+// (of a class or of any teacher)
+size_t loss_bytes(int64_t n, int64_t rows, int64_t cols) { return forward_ws(n, rows, cols, kMaxPairs).bytes; }
 size_t loss_grad_bytes(int64_t n, int64_t rows, int64_t cols) { return grad_ws(n, rows, cols).bytes; }
 
 int launch_loss(const LossArgs& a, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto* base = static_cast<unsigned char*>(ws);
-  const ForwardWs p = forward_ws(a.n, a.rows, a.cols);
+  const bool tiles = a.teacher && from_tiles(a.n, a.rows, a.cols, a.k);
+  const ForwardWs p = forward_ws(a.n, a.rows, a.cols, tiles ? a.k : 0);
   PickArgs pick;
   pick.x = a.x, pick.w = a.w, pick.xs = a.x_scale, pick.ws = a.w_scale;
   pick.out = a.logp, pick.ld_out = a.ld_logp;
@@ -1071,15 +1158,24 @@ int launch_loss(const LossArgs& a, void* ws, void* stream) {
   pick.y = targets(a);
   // the targets' logits beside the product, which reads nothing of theirs (but for a copy of X's scales, it is the
   // next launch)
-  const bool pick_first = a.teacher && (!linear_on_pairs(a.n, a.rows, a.cols) ||
+  const bool pick_first = a.teacher && !tiles && (!linear_on_pairs(a.n, a.rows, a.cols) ||
                                         (a.ld_xs % 4 == 0 && (reinterpret_cast<uintptr_t>(a.x_scale) & 15) == 0));
-  if (a.teacher) {
+  if (tiles) {
+    SortArgs sort;
+    sort.y = pick.y, sort.n = a.n, sort.parts = (a.rows + kPartCols - 1) / kPartCols;
+    sort.records = reinterpret_cast<uint32_t*>(base + p.records), sort.ld = a.n, sort.words = reinterpret_cast<uint16_t*>(base + p.words);
+    const int group = a.k <= kSortFew ? 16 : 4;
+    launch_after(k_loss_sort, unsigned((a.n + group - 1) / group), 1024, 0, s, sort);
+    if (int rc = check("loss (teacher's words)")) return rc;
+  } else if (a.teacher) {
     launch_after(k_loss_pick, ctas_for(a.n * ((a.k + 3) / 4), 8, int64_t(sm_count()) * 64), 256, 0, s, pick);
     if (int rc = check("loss (targets)")) return rc;
   }
   LossTile tile = {};
-  tile.end = kTileStats, tile.zscale = a.scale;
+  tile.end = tiles ? kTilePicks : kTileStats, tile.zscale = a.scale;
   tile.late = pick_first;
+  tile.records = reinterpret_cast<uint32_t*>(base + p.records), tile.ld_records = a.n, tile.words = reinterpret_cast<uint16_t*>(base + p.words);
+  tile.picked = a.logp, tile.ld_picked = a.ld_logp, tile.listed = a.k;
   tile.stats = reinterpret_cast<float2*>(base + p.stats), tile.at = base + p.at, tile.ld_stats = a.n;
   LinearArgs l{a.x, a.x_scale, a.w, a.w_scale, base, a.ldx, a.ld_xs, a.ldw, a.rows, a.n, a.rows, a.cols, 0,
                static_cast<int*>(ws), reinterpret_cast<float*>(base + p.scales), &tile};
@@ -1089,9 +1185,9 @@ int launch_loss(const LossArgs& a, void* ws, void* stream) {
   j.loss = a.loss, j.lse = a.lse, j.logp = a.logp;
   j.parts = (a.rows + kPartCols - 1) / kPartCols;
   j.group = 1;
-  while (j.group < 32 && a.n > int64_t(j.group) * sm_count()) j.group *= 2;
+  while (j.group < kJoinWarps && a.n > int64_t(j.group) * 2 * sm_count()) j.group *= 2;
   j.pick = pick;
-  launch_after(k_loss_join, unsigned((a.n + j.group - 1) / j.group), 1024, 0, s, j);
+  launch_after(k_loss_join, unsigned((a.n + j.group - 1) / j.group), 32 * kJoinWarps, 0, s, j);
   return check("loss (join)");
 }
 

@@ -78,6 +78,42 @@ __device__ __forceinline__ void lane_stats(float* z, int cols, float zscale, boo
   }
 }
 
+// A row's listed words in a part of the vocabulary, as one word: the place of the first in the row's list (11 bits),
+// their count (5 bits, 31 for that many or more) and the first entry (16: place among the row's words << 6 | column).
+__host__ __device__ constexpr uint32_t words_record(uint32_t start, uint32_t count, uint32_t first) {
+  return start | (count < 31 ? count : 31u) << 11 | first << 16;
+}
+
+// The logits z of a lane's row's listed words, by their record; `next` is the record of the row's next part.  (Registers have
+// no index: the lanes' logits go through 2 KB of shared memory of the warp's own, 16 columns at a time, 16-byte word c
+// of lane l at c ^ ((l >> 1) & 3) of its 64 bytes, which keeps the banks apart.)
+template <int N>
+__device__ __forceinline__ void lane_picks(const float* z, uint32_t record, const uint32_t* next, const uint16_t* words,
+                                           float* picked, uint32_t box, int lane) {
+  uint32_t at = record & 0x7FFu, left = record >> 11 & 31u, entry = record >> 16;
+  if (!__any_sync(0xFFFFFFFFu, left > 0)) return;
+  if (left == 31u) left = (__ldcg(next) & 0x7FFu) - at;
+  const uint32_t mine = box + 64u * uint32_t(lane), turn = uint32_t(lane >> 1) & 3u;
+#pragma unroll
+  for (int c0 = 0; c0 < N; c0 += 16) {
+    const bool here = left > 0 && (entry & 63u) < uint32_t(c0 + 16);
+    if (!__any_sync(0xFFFFFFFFu, here)) continue;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((c ^ turn) << 4)), "f"(z[c0 + 4 * c]),
+                   "f"(z[c0 + 4 * c + 1]), "f"(z[c0 + 4 * c + 2]), "f"(z[c0 + 4 * c + 3])
+                   : "memory");
+    while (left > 0 && (entry & 63u) < uint32_t(c0 + 16)) {  // (its own bytes: no other lane's)
+      const uint32_t col = entry & 15u;
+      float v;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(mine + (((col >> 2) ^ turn) << 4) + 4u * (col & 3u)) : "memory");
+      picked[entry >> 6] = v;
+      if (--left > 0) entry = __ldcg(words + ++at);
+    }
+  }
+  __syncwarp();
+}
+
 // of a warp's row: the products of columns lane + 32 j < cols, j < J
 template <int J>
 __device__ __forceinline__ void row_stats(const float* v, int cols, float zscale, int lane, float2* stats, uint8_t* at) {

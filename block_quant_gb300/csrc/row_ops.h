@@ -59,9 +59,9 @@ int launch_quant_rows(const void* x, int64_t ldx, int64_t n, int cols, uint8_t* 
 int launch_dw_inputs(const uint8_t* codes, int64_t ldc, const float* scale, int64_t lds, int64_t n, int cols, void* x_out,
                      int64_t ldo, const void* dy, int64_t ldy, int rows, void* dy_out, int64_t ldyo, void* stream);
 // What k_linear and k_linear_pair do with a tile of products: rows of out, or, for a loss
-// (loss_fp8.cu), statistics of each row's part of the tile, its scaled probabilities, or the sum of
-// three rows of products, a token's
-enum TileEnd { kTileOut = 0, kTileStats = 1, kTileProbs = 2, kTileTriples = 3 };
+// (loss_fp8.cu), statistics of each row's part of the tile (and the logits of the row's listed words in
+// it), its scaled probabilities, or the sum of three rows of products, a token's
+enum TileEnd { kTileOut = 0, kTileStats = 1, kTileProbs = 2, kTileTriples = 3, kTilePicks = 4 };
 constexpr int kPartCols = 64;  // of statistics
 struct LossTile {
   int end;
@@ -73,6 +73,13 @@ struct LossTile {
   float2* stats;     // kTileStats: [part][ld_stats] and
   uint8_t* at;       // the largest logit's column in its part
   int64_t ld_stats;
+  // kTilePicks (statistics too; not where k_linear splits a tile): records[w][t] (loss_tile.h; w to the number of parts)
+  // of row t's listed words in part w, words[t][..], whose logits go to picked[t][..]
+  const uint32_t* records;
+  const uint16_t* words;
+  float* picked;
+  int64_t ld_records, ld_picked;
+  int listed;        // pitch of words
   // kTileProbs: each row's log-sum, its class (-1: none) and loss, and the first word's number
   const float* lse;
   const int* target;
@@ -100,6 +107,7 @@ struct LinearArgs {
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 bool linear_on_pairs(int64_t n, int64_t width, int64_t red);  // whether out = x W^T takes the CTA pairs
+bool linear_whole_tiles(int64_t n, int64_t width, int64_t red);  // whether it takes one CTA or pair a tile
 double linear_small_us(int64_t n, int64_t width, int64_t red);  // what out = x W costs without them
 // X's scales [groups][ldx] at a pitch whose rows 16-byte copies can read
 int launch_copy_scales(const float* x, int64_t ldx, int64_t n, int64_t groups, float* out, int64_t ldo, void* stream);

@@ -17,8 +17,9 @@ def class_pairs(targets, rows):
 
 def teacher_pairs(ids, logits, scale, rows):
     """The same of a teacher's top logits: the softmax over the pairs that count."""
-    ids, z = np.asarray(ids, np.int64), scale * np.asarray(logits, np.float64)
+    ids, z = np.asarray(ids, np.int64), np.asarray(logits, np.float64)
     kept = (ids >= 0) & (ids < rows) & ~np.isneginf(z)
+    z = scale * np.where(kept, z, 0)
     top = np.max(np.where(kept, z, -np.inf), axis=1, keepdims=True)
     e = np.where(kept, np.exp(np.where(kept, z - np.where(np.isfinite(top), top, 0), 0)), 0)
     total = e.sum(axis=1, keepdims=True)
@@ -37,14 +38,13 @@ def log_sum(z):
 
 
 def log_probs(z, ids):
-    """z[t, ids[t, i]] - log_sum(z)[t], exact for probabilities near 1 too."""
-    out = np.zeros(ids.shape)
-    for t in range(z.shape[0]):
-        for i, v in enumerate(ids[t]):
-            d = z[t] - z[t, v]
-            d[v] = -np.inf
-            out[t, i] = -np.logaddexp.reduce(np.append(d, 0.0)) if d.max() > 0 else -np.log1p(np.exp(d).sum())
-    return out
+    """z[t, ids[t, i]] - log_sum(z)[t], exact for probabilities near 1 too: the largest logit stays out of the
+    sum of exponentials."""
+    best = z.argmax(axis=1)[:, None]
+    behind = z - np.take_along_axis(z, best, 1)
+    others = np.exp(behind)
+    np.put_along_axis(others, best, 0.0, 1)
+    return np.take_along_axis(behind, ids, 1) - np.log1p(others.sum(axis=1, keepdims=True))
 
 
 def loss(z, pairs):
@@ -59,8 +59,7 @@ def weights_of(pairs, rows):
     """The targets' weights as a matrix [n, rows]."""
     ids, q, _ = pairs
     out = np.zeros((ids.shape[0], rows))
-    for t in range(ids.shape[0]):
-        np.add.at(out[t], ids[t], q[t])
+    np.add.at(out, (np.arange(ids.shape[0])[:, None], ids), q)
     return out
 
 

@@ -219,6 +219,21 @@ class Head:
             near(f64(dw), want, by + U * 1.001 * np.abs(want) + U * by)
 
 
+# (words enough to be taken from the tiles of the product: of CTA pairs and of single CTAs, lists of more and fewer words a row)
+TEACHERS = [(2000, 900, 1024, 130), (1500, 1300, 2064, 257), (4000, 130, 528, 100), (1000, 2500, 4112, 70), (3000, 400, 512, 1024)]
+
+
+@pytest.mark.parametrize("n,rows,cols,k", TEACHERS)
+@pytest.mark.parametrize("scale", [1.0, -0.5])
+def test_distill_of_many_words(cuda, n, rows, cols, k, scale):
+    """Several words of a row in one part of the vocabulary, all of them, and none."""
+    def edit(c):
+        c.ids[::3] = 64 + c.rng.integers(0, 64, c.ids[::3].shape)
+        c.ids[1] = -1
+
+    Head(cuda, n, rows, cols, scale=scale, k=k, teacher="fp32", bits=32, spare=2, edit=edit).forward().check_forward()
+
+
 SIZES = [(1, 1, 16), (42, 1300, 160), (43, 1300, 160), (85, 9000, 144), (1, 130, 128), (2, 300, 144), (7, 256, 272), (33, 1000, 512), (128, 257, 128), (129, 640, 256),
          (200, 2049, 400), (300, 4100, 1040), (520, 1500, 2064)]
 
