@@ -260,13 +260,29 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
     }
   }
-  if (warp >= 2 && q < quarters && !(STATS && g.split == 1)) {
+  if constexpr (END == kTileProbs) {  // the same
+    const int row = m0 + 32 * q + lane, c0 = n0 + half * (BN / 2);
+    if (g.split == 1 && warp >= 2 && row < g.n && c0 < g.width) {
+      const int y = __ldcg(g.target + row) - g.first - c0;
+      lane_probs<BN / 2>(acc, g.width - c0, g.zscale, __ldcg(g.lse + row));
+      // (out's pitch covers the tile's columns: zeros past the width)
+      __half* u = reinterpret_cast<__half*>(g.out) + int64_t(row) * g.ldo + c0;
+#pragma unroll
+      for (int j = 0; j < BN / 2; j += 8)
+        *reinterpret_cast<uint4*>(u + j) =
+            make_uint4(two16(acc[j], acc[j + 1], __half()), two16(acc[j + 2], acc[j + 3], __half()),
+                       two16(acc[j + 4], acc[j + 5], __half()), two16(acc[j + 6], acc[j + 7], __half()));
+      if (y >= 0 && y < BN / 2) u[y] = __float2half_rn(scaled_rest(__ldcg(g.loss + row)));
+    }
+  }
+  const bool gone = (STATS || END == kTileProbs) && g.split == 1;
+  if (warp >= 2 && q < quarters && !gone) {
     float* prow = part + (32 * q + lane) * kPartPitch + half * (BN / 2);
 #pragma unroll
     for (int j = 0; j < BN / 2; ++j) prow[j] = acc[j];
   }
   cluster_sync();  // (every thread) the cluster's partial tiles are written
-  const int rows = STATS && g.split == 1 ? 0 : min(BM, g.n - m0), cols = min(BN, g.width - n0);
+  const int rows = gone ? 0 : min(BM, g.n - m0), cols = min(BN, g.width - n0);
   // each CTA finishes its share of the tile's rows: lane l columns l, l + 32, ...
   const uint32_t part0 = smem_addr(part);
   // (probabilities: the log-sum and the class of the warp's i-th row come ahead, in lane i)
@@ -590,11 +606,8 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       if (!ok) break;
       if constexpr (END == kTileStats || END == kTilePicks) {
         if (c0 < g.width) {
-          const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row0 + lane;
-          int row = row0 + lane;
-          // (what follows is not to be computed ahead of the k-blocks and held over them: with spills in their loop a tile took
-          // 1.3 us more of 14)
-          if constexpr (END == kTilePicks) asm volatile("" : "+r"(row));
+          const int row = row0 + lane;
+          const int64_t at = int64_t(c0 / kPartCols) * g.ld_stats + row;
           const uint32_t* records = g.records + int64_t(c0 / kPartCols) * g.ld_records + row;
           uint32_t record = 0;
           if constexpr (END == kTilePicks)

@@ -103,7 +103,7 @@ struct LinearArgs {
   int* status;
   float* scale_ws;       // room for x_scale at a pitch of n + 3 at most (not used if x_scale is 16-byte
                          // aligned and ld_xs a multiple of 4)
-  LossTile* loss = nullptr;  // kTileProbs: out is fp16, 16-byte aligned, its pitch a multiple of 8 that covers the width
+  LossTile* loss = nullptr;  // kTileProbs: out is fp16, 16-byte aligned, its pitch a multiple of 256 that covers the width
 };
 int launch_linear_fp8(const LinearArgs& a, void* stream);
 bool linear_on_pairs(int64_t n, int64_t width, int64_t red);  // whether out = x W^T takes the CTA pairs
