@@ -63,6 +63,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// A scale: of a loss's tiles, which may begin before the launch before has ended, from L2.
+template <int END>
+__device__ __forceinline__ float scale_at(const float* p) {
+  return END == kTileOut || END == kTileTriples ? __ldg(p) : __ldcg(p);
+}
+
 struct LinArgs {
   const float *xs, *ws;  // scales of X [groups][ld_xs] and of W's tiles
   __nv_bfloat16* out;
@@ -205,21 +211,21 @@ __global__ void __launch_bounds__(THREADS, 2)
     const float* ws = (TRANS ? g.ws + (n0 >> 7) : g.ws + int64_t(n0 >> 7) * g.tile_cols) + k0 * ws_step;
     // scales come kAhead blocks before their use (their loads queue behind the stages'
     // copies); W's for 32 blocks at a time, block b in lane b
-    float xn[kAhead], wl = 0.f, wn = lane < blocks ? __ldg(ws + lane * ws_step) : 0.f;
+    float xn[kAhead], wl = 0.f, wn = lane < blocks ? scale_at<END>(ws + lane * ws_step) : 0.f;
 #pragma unroll
-    for (int b = 0; b < kAhead; ++b) xn[b] = on && b < blocks ? __ldg(xs + b * g.ld_xs) : 0.f;
+    for (int b = 0; b < kAhead; ++b) xn[b] = on && b < blocks ? scale_at<END>(xs + b * g.ld_xs) : 0.f;
     bool ok = true;
     for (int it0 = 0; it0 < blocks; it0 += kAhead) {
       if ((it0 & 31) == 0) {
         wl = wn;
-        wn = it0 + 32 + lane < blocks ? __ldg(ws + (it0 + 32 + lane) * ws_step) : 0.f;
+        wn = it0 + 32 + lane < blocks ? scale_at<END>(ws + (it0 + 32 + lane) * ws_step) : 0.f;
       }
 #pragma unroll
       for (int b = 0; b < kAhead; ++b) {
         const int it = it0 + b;
         if (it >= blocks) continue;  // (no early exit: its copies of the sums would spill)
         const float f = xn[b] * __shfl_sync(0xFFFFFFFFu, wl, it & 31);
-        if (on && it + kAhead < blocks) xn[b] = __ldg(xs + int64_t(it + kAhead) * g.ld_xs);
+        if (on && it + kAhead < blocks) xn[b] = scale_at<END>(xs + int64_t(it + kAhead) * g.ld_xs);
         const int buf = it & 1;
         ok = ok && mbar_wait(tfull_bar(buf), uint32_t((it >> 1) & 1), g.status, 25);
         tc_fence_after();
@@ -573,11 +579,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
       if constexpr (END == kTileProbs)
         if (row0 + lane < g.n) lse = __ldcg(g.lse + row0 + lane), y = __ldcg(g.target + row0 + lane) - g.first - c0;
       // W's scales for 32 k-blocks, block kb + l in lane l
-      float wl = 0.f, wn = c0 < g.width && lane < nk ? __ldg(ws + lane * ws_step) : 0.f;
+      float wl = 0.f, wn = c0 < g.width && lane < nk ? scale_at<END>(ws + lane * ws_step) : 0.f;
       for (int kb = 0; kb < nk; ++kb, ++it) {
         if ((kb & 31) == 0) {
           wl = wn;
-          wn = c0 < g.width && kb + 32 + lane < nk ? __ldg(ws + int64_t(kb + 32 + lane) * ws_step) : 0.f;
+          wn = c0 < g.width && kb + 32 + lane < nk ? scale_at<END>(ws + int64_t(kb + 32 + lane) * ws_step) : 0.f;
         }
         const uint32_t buf = it & 1u, l = it % SLOTS;
         const float w = __shfl_sync(0xFFFFFFFFu, wl, kb & 31);

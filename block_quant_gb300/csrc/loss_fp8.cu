@@ -436,7 +436,7 @@ __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
     const int64_t t = i / spans;
     const int c0 = 1024 * int(i - t * spans) + 8 * lane;
     const bool none = g.off && __ldg(g.off + t) == kNoTarget;
-    const float row = g.off ? up * __ldg(g.dloss + t) : up;
+    const float row = g.off ? __ldg(g.dloss + t) : 1.f;
     uint2 q[4];
     float f[4];
 #pragma unroll
@@ -455,8 +455,7 @@ __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3)));
-        // (X's: the scale times the gradient first, as the power of two was found)
-        const float s = f[k] * row;
+        const float s = (f[k] * row) * up;  // (in this order: the power of two is the products')
         if (!none) o[j] = two16(v.x * s, v.y * s, __half());
       }
       *reinterpret_cast<uint4*>(g.out + t * g.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -943,10 +942,11 @@ __global__ void __launch_bounds__(PAIR_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 64; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * g.factor * back);
       if (g.accumulate && row < g.m) {
-        const __nv_bfloat16* o = g.out + int64_t(row) * g.ldo + c0;
+        // (from L2: this may have begun before the launch before ended)
+        const auto* o = reinterpret_cast<const unsigned short*>(g.out + int64_t(row) * g.ldo + c0);
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          if (c0 + j < g.n) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(o[j]));
+          if (c0 + j < g.n) r[j] = __float_as_uint(__uint_as_float(r[j]) + bf16f(__ldcg(o + j)));
       }
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
       __syncwarp();

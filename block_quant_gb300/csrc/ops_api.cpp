@@ -104,6 +104,7 @@ int check_targets(const char* who, int64_t n, int64_t rows, int64_t cols, int64_
   if (k < 1 || k > 1024) return fail(BQ_EINVAL, who, "k outside [1, 1024]");
   if (teacher_kind != BQ_ROWS_BF16 && teacher_kind != BQ_ROWS_FP32) return fail(BQ_EINVAL, who, "teacher kind must be bf16 or fp32");
   if (!std::isfinite(scale)) return fail(BQ_EINVAL, who, "scale must be finite");
+  if (((n + 127) / 128) * ((rows + 127) / 128) > 0x7FFFFFF) return fail(BQ_EINVAL, who, "too many tiles of logits");
   return BQ_OK;
 }
 

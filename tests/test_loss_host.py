@@ -78,7 +78,7 @@ SHARED = [(dict(n=-1), INV), (dict(n=2 ** 27 + 1), INV), (dict(rows=0), INV), (d
           (dict(w=None), INV), (dict(ws_=None), INV), (dict(lse=None), INV), (dict(ldx=16), INV), (dict(ldw=16), INV),
           (dict(ldx=40), ALIGN), (dict(ldw=40), ALIGN), (dict(x=P + 8), ALIGN), (dict(w=P + 4), ALIGN), (dict(xs=P + 2), ALIGN),
           (dict(ws_=P + 1), ALIGN), (dict(lse=P + 2), ALIGN), (dict(bits=16), INV), (dict(scale=float("nan")), INV),
-          (dict(scale=float("inf")), INV), (dict(ws=None), INV), (dict(ws=P + 128), ALIGN), (dict(wb=512), NOSPC),
+          (dict(scale=float("inf")), INV), (dict(n=2 ** 21, rows=2 ** 21), INV), (dict(ws=None), INV), (dict(ws=P + 128), ALIGN), (dict(wb=512), NOSPC),
           (dict(lds=3, cols=144, ldx=144, ldw=144, ldd=144, ldg=144), INV)]
 GRAD = [(dict(dloss=None), INV), (dict(dx=None, dw=None), INV), (dict(ldd=31), INV), (dict(ldg=31), INV), (dict(dx=P + 1), ALIGN),
         (dict(dw=P + 1), ALIGN), (dict(dloss=P + 2), ALIGN)]

@@ -504,6 +504,50 @@ def test_one_pair_of_weight_one_is_a_class(cuda):
         near(f64(got), w, 2 * U * np.abs(w) + 1e-30 if got.dtype == torch.bfloat16 else 4 * E * np.abs(w))
 
 
+@pytest.mark.parametrize("n", [5, 90, 300])
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 60])
+def test_sizes_of_gradients(cuda, n, size):
+    """Gradients far from 1, and rows whose own differ by 2^16: fp16 operands by common powers of two."""
+    import torch
+
+    rows, cols = 700, 256
+    c = Head(cuda, n, rows, cols, seed=14).forward()
+    g = (c.rng.standard_normal(n) * size * 2.0 ** -c.rng.integers(0, 17, n)).astype(np.float32)
+    dx, dw = empty(n, cols, cuda, torch.bfloat16)[0], empty(rows, cols, cuda, torch.bfloat16)[0]
+    c.grad(torch.as_tensor(g).to(cuda), dx, dw)
+    c.check_grads(g, dx, dw)
+
+
+def test_gradients_accumulated_over_micro_batches(cuda):
+    """The weight's gradient summed over calls on the same buffers, each before the last has been read: the bits of
+    calls with a pause between."""
+    import torch
+
+    for n, rows, cols, k in ((520, 900, 256, None), (260, 3000, 512, 3)):
+        cs = [Head(cuda, n, rows, cols, k=k, seed=30 + i).forward() for i in range(3)]
+        ws = workspace(bq.loss_fp8_grad_workspace(n, rows, cols), cuda)
+        g = torch.linspace(0.5, 1, n, device=cuda) / n
+        x, xs = torch.empty_like(cs[0].x.contiguous()), torch.empty_like(cs[0].xs.contiguous())
+        sums = []
+        for pause in (True, False):
+            dw, dxs = torch.zeros(rows, cols, dtype=torch.bfloat16, device=cuda), []
+            for turn in range(6):
+                c = cs[turn % 3]
+                x.copy_(c.x), xs.copy_(c.xs)  # the same memory for every micro-batch
+                head, c.head = c.head, (x, xs, c.w, c.ws_)
+                dx = torch.empty(n, cols, dtype=torch.bfloat16, device=cuda)
+                if k is None:
+                    bq.cross_entropy_fp8_grad(*c.head, c.t, c.loss, c.lse, g, dx, dw, ws, accumulate=True)
+                else:
+                    bq.distill_fp8_grad(*c.head, c.t, c.z, c.lse, c.logp, g, dx, dw, ws, accumulate=True)
+                c.head = head
+                dxs.append(dx)
+                if pause:
+                    torch.cuda.synchronize()
+            sums.append([dw, *dxs])
+        assert all(torch.equal(a, b) for a, b in zip(*sums))
+
+
 # ----------------------------------------------------------------------------- derivatives of the kernels' own losses
 
 
@@ -542,7 +586,7 @@ def test_one_workspace_another_stream_and_graphs(cuda, k):
     it, replayed on new inputs: the bits of calls with workspaces of their own."""
     import torch
 
-    sizes = [(2, 900, 144), (50, 2000, 256), (300, 1500, 512), (700, 700, 272), (1100, 3000, 256)]
+    sizes = [(2, 900, 144), (50, 2000, 256), (301, 1500, 512), (702, 700, 272), (1101, 3000, 256)]
     cases = [[Head(cuda, *s, k=k, seed=20 + i) for i in range(2)] for s in sizes]
     need = max(max(bq.loss_fp8_workspace(*s), bq.loss_fp8_grad_workspace(*s)) for s in sizes)
     shared = workspace(need, cuda)
