@@ -1070,8 +1070,8 @@ struct GradWs {
 
 int64_t piece_len(const GradWs& p, int64_t rows, int i) { return std::min(p.piece, rows - i * p.piece); }
 
-// U and the piece of W in fp16 take 256 MB each at most, unless 256 words do not fit
-constexpr int64_t kPieceBytes = int64_t(256) << 20;
+// U takes 512 MB at most and the piece of W in fp16 1 GB, unless 256 words do not fit
+constexpr int64_t kPieceBytes = int64_t(512) << 20, kPieceWeight = int64_t(1) << 30;
 
 // The tiles left over after whole waves in the parts that cost least: a round of parts takes 0.29 us a k-block (as
 // a projection's weight gradient), and a share is stored and added up.  us: what the product takes.
@@ -1105,7 +1105,7 @@ GradWs grad_ws(int64_t n, int64_t rows, int64_t cols) {
   p.ldh = up_to(cols, 64);
   p.few = few_tokens(n, rows, cols);
   const int64_t most = p.few ? up_to(rows, 256)
-                              : std::max<int64_t>(256, kPieceBytes / (2 * std::max<int64_t>({n, p.ldh, 1})) / 256 * 256);
+                              : std::max<int64_t>(256, std::min(kPieceBytes / std::max<int64_t>(n, 1), kPieceWeight / p.ldh) / 512 * 256);
   const int64_t pieces = (rows + most - 1) / most;
   p.piece = up_to((rows + pieces - 1) / pieces, 256);
   p.pieces = int((rows + p.piece - 1) / p.piece);

@@ -270,7 +270,7 @@ def test_gradients_of_many_tiles(cuda, n, rows, cols):
 
 
 def test_gradients_in_pieces(cuda):
-    """More words than one piece of the vocabulary holds (256 MB of fp16), the last one short, against whole
+    """More words than one piece of the vocabulary holds (512 MB of fp16), the last one short, against whole
     sums on the GPU in fp64."""
     import torch
 
