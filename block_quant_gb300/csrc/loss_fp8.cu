@@ -373,6 +373,9 @@ __global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float mx = 0.f, mw = 0.f;
   for (int64_t t = int64_t(blockIdx.x) * 8 + warp; t < g.n; t += int64_t(gridDim.x) * 8) {
+    // (loads that need nothing of one another set out together)
+    const float f = g.dloss[t], lse = g.lse[t];
+    float x = lane < g.groups ? finite_abs(g.xs[int64_t(lane) * g.ld_xs + t] * f) : 0.f;
     bool any = false;
     for (int i = lane; i < g.y.k; i += 32) {
       float z;
@@ -380,12 +383,12 @@ __global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
     }
     any = __any_sync(0xFFFFFFFFu, any);
     if (lane == 0) {
-      g.off[t] = any ? g.lse[t] : kNoTarget;
+      g.off[t] = any ? lse : kNoTarget;
       g.target[t] = g.y.teacher ? -1 : g.y.id(t, 0);
     }
     if (!any) continue;
-    const float f = g.dloss[t];
-    for (int j = lane; j < g.groups; j += 32) mx = fmaxf(mx, finite_abs(g.xs[int64_t(j) * g.ld_xs + t] * f));
+    for (int j = lane + 32; j < g.groups; j += 32) x = fmaxf(x, finite_abs(g.xs[int64_t(j) * g.ld_xs + t] * f));
+    mx = fmaxf(mx, x);
   }
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < g.w_tiles; i += int64_t(gridDim.x) * 256)
     mw = fmaxf(mw, finite_abs(g.ws[i]));
@@ -427,18 +430,18 @@ struct HalfArgs {
 // A warp takes up to 1024 codes of a row, a lane 8 of each 256, so that loads and stores are whole lines;
 // bound by memory (32256 x 4096: 58 us, 396 MB; 75 with 16 codes a lane).
 __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
-  const int e = power_for(largest(g.tops, g.count));
-  const float up = ldexpf(1.f, e);
-  if (cta == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
   const int lane = threadIdx.x & 31, spans = (g.cols + 1023) / 1024;
   const int64_t items = g.n * spans, step = int64_t(g.ctas) * 8;
-  for (int64_t i = int64_t(cta) * 8 + (threadIdx.x >> 5); i < items; i += step) {
-    const int64_t t = i / spans;
-    const int c0 = 1024 * int(i - t * spans) + 8 * lane;
-    const bool none = g.off && __ldg(g.off + t) == kNoTarget;
-    const float row = g.off ? __ldg(g.dloss + t) : 1.f;
-    uint2 q[4];
-    float f[4];
+  int64_t i = int64_t(cta) * 8 + (threadIdx.x >> 5), t = 0;
+  int c0 = 0;
+  uint2 q[4];
+  float f[4], row = 1.f;
+  bool none = false;
+  auto load = [&] {
+    t = i / spans;
+    c0 = 1024 * int(i - t * spans) + 8 * lane;
+    none = g.off && __ldg(g.off + t) == kNoTarget;
+    row = g.off ? __ldg(g.dloss + t) : 1.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = c0 + 256 * k;
@@ -446,6 +449,12 @@ __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
       q[k] = __ldg(reinterpret_cast<const uint2*>(g.codes + t * g.ldc + c));
       f[k] = __ldg(g.off ? g.scale + int64_t(c >> 7) * g.lds + t : g.scale + (t >> 7) * g.lds + (c >> 7));
     }
+  };
+  if (i < items) load();  // (beside the search for the largest)
+  const int e = power_for(largest(g.tops, g.count));
+  const float up = ldexpf(1.f, e);
+  if (cta == 0 && threadIdx.x == 0) *g.back = ldexpf(1.f, -e);
+  while (i < items) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = c0 + 256 * k;
@@ -460,6 +469,7 @@ __device__ __forceinline__ void half_rows(const HalfArgs& g, int cta) {
       }
       *reinterpret_cast<uint4*>(g.out + t * g.ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+    if ((i += step) < items) load();
   }
 }
 
@@ -1236,6 +1246,9 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
     if (int rc = encode_map_chunks(&tx, x16, a.cols, a.n, p.ldh, 2)) return rc;
   }
   const float unscale = a.scale * (1.f / float(1 << kProbBits));
+  // dW beside dx.  Few tokens' dx is bound by memory, as dW is: of a large head they only slow each other (16 tokens of 128256 x
+  // 4096: 366 us in turn, 377 beside), of a small one dW hides its start (4 of 1298 x 608: 22.5 and 20.3)
+  const bool dw_early = a.dx && (!p.few || int64_t(a.rows) * a.cols <= int64_t(1) << 24);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, len = piece_len(p, a.rows, i);
     const uint8_t* w = a.w + v0 * a.ldw;
@@ -1294,7 +1307,7 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
       g.out = static_cast<__nv_bfloat16*>(a.dw) + v0 * a.ld_dw, g.ldo = a.ld_dw, g.m = int(len), g.n = a.cols, g.k = int(a.n);
       g.splits = dw_splits(a.n, len, a.cols);
       g.part = g.splits > 1 ? reinterpret_cast<float*>(base + p.dw) : nullptr;
-      g.back = back, g.factor = unscale, g.accumulate = a.accumulate, g.late = a.dx && !p.few;
+      g.back = back, g.factor = unscale, g.accumulate = a.accumulate, g.late = dw_early;
       g.bytes = store_bytes(g.out, a.ld_dw, a.cols), g.status = status;
       to = tx;  // (not read by plain stores and shares)
       if (!g.part && g.bytes == 16)
