@@ -581,15 +581,15 @@ __global__ void __launch_bounds__(256) k_loss_split(const SplitArgs g) {
 // On CTA pairs, 256 x 256 tiles, fp16 operands and fp32 sums: U's rows K-major, W's words
 // MN-major.  Tiles left over after whole waves of pairs are cut into `parts` equal parts of their
 // summed index, taken in turn by all pairs, a part of every tile before the next part: 28 tiles left
-// of 256 on 76 pairs take three rounds of an eighth, not a wave.  (Cutting them into as many
-// pieces as there are pairs, each pair's at an offset of its own, balances them exactly and took longer, 828 us
-// against 705 for 4096 x 32256 x 4096: pairs at different offsets read nothing that others have read.)
+// of 256 on 76 pairs take three rounds of an eighth, not a wave (4096 x 32256 x 4096: 575 us, 633 with
+// whole tiles).  Cutting them into as many pieces as there are pairs, each pair's at an offset of its own, balances them
+// exactly and took 6 % longer than equal parts: pairs at different offsets read nothing that others have read.
 // Sums of a tile leave as shares, one per part, which pieces of the vocabulary add to; k_loss_sums
 // adds a tile's shares in order.
 //
 // W's fp16 words come from a launch before (k_loss_half).  Spreading its codes to fp16 inside
 // this kernel, by six warps between a ring of codes and the products' operands, took 1225 us where
-// this and that launch take 705 (4096 x 32256 x 4096): 250 of it the spreading, 130 its fences and cluster-wide
+// this and that launch take 633 (4096 x 32256 x 4096): 250 of it the spreading, 130 its fences and cluster-wide
 // arrivals, and 815 were left without both.
 
 // Which tiles, and which parts of their k-blocks, a pair works on: its share of the whole waves'
