@@ -525,8 +525,9 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
  * W and dloss * X are held as fp16, times powers of two that keep eleven bits of
  * each over 2^28 below its largest magnitude.
  * Sums are taken in an order that the sizes and the GPU fix.  Operands are aligned as in
- * bq_linear_fp8, n may be 0; n / 128 * rows / 128, each rounded up, is below 2^27 (BQ_EINVAL).  ws: bq_loss_fp8_workspace or bq_loss_fp8_grad_workspace bytes
- * (either serves cross entropy and distillation), used and checked as bq_linear_fp8's. */
+ * bq_linear_fp8, n may be 0; n / 128 * rows / 128, each rounded up, is below 2^27
+ * (BQ_EINVAL).  ws: bq_loss_fp8_workspace or bq_loss_fp8_grad_workspace bytes (either
+ * serves cross entropy and distillation), used and checked as bq_linear_fp8's. */
 int bq_loss_fp8_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
 int bq_loss_fp8_grad_workspace(int64_t n, int64_t rows, int64_t cols, size_t* bytes);
 int bq_cross_entropy_fp8(const uint8_t* x, int64_t ld_x, const float* x_scale, int64_t ld_scale, const uint8_t* w,
