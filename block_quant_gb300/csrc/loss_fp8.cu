@@ -81,32 +81,31 @@ struct Targets {
     return teacher_kind == BQ_ROWS_FP32 ? __ldg(static_cast<const float*>(teacher) + at)
                                         : __bfloat162float(static_cast<const __nv_bfloat16*>(teacher)[at]);
   }
-  // a pair counts if its id is a word and the teacher gives it any weight; z: its logit times the factor
-  __device__ __forceinline__ int kept_id(int64_t t, int i, float* z) const {
+  // a pair counts if its id is a word and the teacher gives it any weight; l: its logit
+  __device__ __forceinline__ int kept_id(int64_t t, int i, float* l) const {
     const int v = id(t, i);
-    *z = 0.f;
+    *l = 0.f;
     if (!teacher || v < 0) return v;
-    const float l = logit(t, i);
-    *z = scale * l;
-    return l == -INFINITY ? -1 : v;
+    *l = logit(t, i);
+    return *l == -INFINITY ? -1 : v;
   }
+  // scale * (l - top).  The difference first, of halves: products of finite logits and the factor may overflow (a
+  // row of the type's lowest value), and so may differences of them.
+  __device__ __forceinline__ float behind(float l, float top) const { return 2.f * (scale * (0.5f * l - 0.5f * top)); }
 };
 
-// the teacher's softmax over a row's pairs, by a warp: its maximum and the log of its sum; false
-// if no pair counts
+// the teacher's softmax over a row's pairs, by a warp: the logit whose product with the factor is largest and the
+// log of its sum; false if no pair counts
 __device__ __forceinline__ bool teacher_sum(const Targets& y, int64_t t, int lane, float* top, float* log_sum) {
-  float m = -INFINITY;
+  const float sign = y.scale < 0.f ? -1.f : 1.f;
+  float m = -INFINITY, l;
   bool any = false;
-  for (int i = lane; i < y.k; i += 32) {
-    float z;
-    if (y.kept_id(t, i, &z) >= 0) any = true, m = fmaxf(m, z);
-  }
-  m = warp_max(m);
+  for (int i = lane; i < y.k; i += 32)
+    if (y.kept_id(t, i, &l) >= 0) any = true, m = fmaxf(m, sign * l);
+  m = sign * warp_max(m);
   float s = 0.f;
-  for (int i = lane; i < y.k; i += 32) {
-    float z;
-    if (y.kept_id(t, i, &z) >= 0) s += expf(z - m);
-  }
+  for (int i = lane; i < y.k; i += 32)
+    if (y.kept_id(t, i, &l) >= 0) s += expf(y.behind(l, m));
   *top = m;
   *log_sum = logf(warp_sum(s));
   return __any_sync(0xFFFFFFFFu, any);
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_loss_join(const JoinArgs g)
     const float logp = v < 0 ? 0.f : v == best ? -more : (*at - a.m) - more;
     *at = logp;
     if (v < 0) continue;
-    const float log_q = (z - top) - log_sum, q = expf(log_q);
+    const float log_q = y.behind(z, top) - log_sum, q = expf(log_q);
     if (q != 0.f) sum += q * (log_q - logp);
   }
   sum = warp_sum(sum);
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
     float z;
     const int v = g.y.kept_id(t, i, &z);
     sid[warp][i] = v;
-    sq[warp][i] = v < 0 ? 0.f : expf((z - top) - log_sum);
+    sq[warp][i] = v < 0 ? 0.f : expf(g.y.behind(z, top) - log_sum);
   }
   __syncwarp();
   for (int i = lane; i < g.y.k; i += 32) {
