@@ -490,8 +490,9 @@ struct FixArgs {
   int v0, len;
 };
 
-// U at a teacher's words in a piece of the vocabulary: p - q by the forward pass's log-probability, which
-// keeps what is left of it where both are near 1 (a class's is put into its tile, loss_tile.h)
+// U at a teacher's words in a piece of the vocabulary: p - q by the forward pass's log-probability.  Where p is
+// above 1/2 it is the others' weights less 1 - p, which keeps what is left of it where p and q are near 1, below
+// it p - q itself, which keeps it where they are small (a class's is put into its tile, loss_tile.h)
 __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
   __shared__ float sq[4][kMaxPairs];
   __shared__ int sid[4][kMaxPairs];
@@ -513,10 +514,17 @@ __global__ void __launch_bounds__(128) k_loss_fix(const FixArgs g) {
   for (int i = lane; i < g.y.k; i += 32) {
     const int id = sid[warp][i], v = id - g.v0;
     if (id < 0 || v < 0 || v >= g.len) continue;
-    float q = 0.f;  // (the same sum, in the same order, for every pair of this id)
-    for (int j = 0; j < g.y.k; ++j)
-      if (sid[warp][j] == id) q += sq[warp][j];
-    g.u[t * g.ldu + v] = __float2half_rn(unit * (expm1f(g.logp[t * g.ld_logp + i]) + (1.f - q)));
+    float q = 0.f, others = 0.f;  // (the same sums, in the same order, for every pair of this id)
+    for (int j = 0; j < g.y.k; ++j) {
+      const float w = sq[warp][j];
+      if (sid[warp][j] == id)
+        q += w;
+      else
+        others += w;
+    }
+    const float logp = g.logp[t * g.ld_logp + i];
+    others += 0.f * q;  // (a weight that is NaN)
+    g.u[t * g.ldu + v] = __float2half_rn(unit * (logp > -0.6931472f ? expm1f(logp) + others : expf(logp) - q));
   }
 }
 

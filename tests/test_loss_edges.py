@@ -1,11 +1,11 @@
 """The losses over an FP8 head on the GPU where their arithmetic has an edge: teachers whose scaled
-logits do not fit fp32.  Tolerances as in test_loss_ops.py."""
+logits do not fit fp32, or give next to nothing to a word.  Tolerances as in test_loss_ops.py."""
 
 import numpy as np
 import pytest
 
 import block_quant_gb300 as bq
-from test_loss_ops import Head, empty
+from test_loss_ops import Head, empty, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,48 @@ def test_teachers_of_the_types_limits(cuda, n, teacher, scale):
         return  # (gradients below bf16's smallest normal value)
     g = c.rng.standard_normal(n).astype(np.float32)
     c.check_grads(g, *both_grads(c, g))
+
+
+@pytest.mark.parametrize("n", [5, 70, 300])
+@pytest.mark.parametrize("teacher", ["fp32", "bf16"])
+def test_small_weights_of_a_teacher(cuda, n, teacher):
+    """Words to which teacher and student give little, down to 2^-30: what u = p - q holds of them."""
+    def edit(c):
+        c.ids[:] = np.argsort(c.rng.random(c.ids.shape), axis=1) + 16 * c.rng.integers(0, 30, (n, 1))
+        c.z[:] = -torch_like(c, np.arange(c.k) * (0.02 + 0.02 * c.rng.random((n, 1))))
+
+    c = Head(cuda, n, 600, 128, scale=64.0, k=16, teacher=teacher, seed=41, edit=edit)
+    q = c.pairs[1]
+    assert np.sum(q > 0.5) and np.sum((q < 2.0 ** -14) & (q > 2.0 ** -28)) > n
+    c.forward().check_forward()
+    g = c.rng.standard_normal(n).astype(np.float32)
+    c.check_grads(g, *both_grads(c, g))
+
+
+def torch_like(c, v):
+    import torch
+
+    return torch.as_tensor(v).to(c.z.dtype)
+
+
+@pytest.mark.parametrize("n", [6, 200])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.filterwarnings("ignore:invalid value")
+def test_a_teacher_without_weights_stays_in_its_row(cuda, n, bad):
+    """Logits that have no softmax, alone and beside others, whatever the student makes of their words."""
+    def edit(c):
+        c.ids[::2] = -1
+        c.ids[::2, 0] = np.arange(c.ids[::2].shape[0])
+        c.z[2, 0] = bad
+        c.ids[3] = np.arange(c.k) + 5
+        c.z[3, 1] = bad
+
+    c = Head(cuda, n, 400, 128, scale=8.0, k=5, teacher="fp32", seed=42, edit=edit)
+    c.x[2], c.xs[:, 2] = c.w[1], 4 * c.ws_[0, 0]  # (sure of its word)
+    c.forward()
+    wrong = np.isin(np.arange(n), [2, 3])
+    assert float(c.logp[2, 0]) > -0.5
+    assert np.array_equal(np.isnan(f64(c.loss)), wrong)
+    dx, dw = both_grads(c, np.ones(n, np.float32))
+    assert np.array_equal(np.isnan(f64(dx)).all(axis=1), wrong) and np.array_equal(np.isnan(f64(dx)).any(axis=1), wrong)
+    assert np.isnan(f64(dw)[1]).all() and np.isnan(f64(dw)[6]).all()
