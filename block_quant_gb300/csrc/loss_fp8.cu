@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_loss_join(const JoinArgs g)
   a = {sm[lane % kJoinWarps][warp], ss[lane % kJoinWarps][warp], sa[lane % kJoinWarps][warp]};
 #pragma unroll
   for (int d = 1; d < kJoinWarps; d <<= 1) a = joined(a, shuffled(a, d));
-  const int best = a.at * kPartCols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
+  // (an infinite logit that is the maximum is inf - inf behind it, as any other: no word is the best)
+  const int best = isinf(a.m) ? -1 : a.at * kPartCols + int(g.at[int64_t(a.at) * g.ld_stats + t]);
   const float more = log1pf(a.s);
   if (lane == 0) g.lse[t] = a.m + more;
   if (!y.teacher) {
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(256) k_loss_prep(const PrepArgs g) {
     }
     any = __any_sync(0xFFFFFFFFu, any);
     if (lane == 0) {
-      g.off[t] = any ? lse : kNoTarget;
+      // (an infinite log-sum: an infinite logit, or all -inf, and no softmax)
+      g.off[t] = !any ? kNoTarget : isinf(lse) ? nanf("") : lse;
       g.target[t] = g.y.teacher ? -1 : g.y.id(t, 0);
     }
     if (!any) continue;

@@ -515,7 +515,8 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
  *     loss[t] = sum_i q_i (log q_i - logp[t, i]); a row of which no pair counts has
  *     loss 0 and no gradient.
  * loss and lse (n) are fp32, logp (n x k, pitch ld_logp) too; lse is written for every
- * row.  log-probabilities near 0 keep their relative precision.
+ * row.  log-probabilities near 0 keep their relative precision.  Logits past fp32 are
+ * infinities: a row whose largest is one has losses and gradients that are infinite or NaN.
  *   The *_grad calls take what the forward call has written and dloss (fp32, n), the
  * gradient of loss.  With u[t, v] = p[t, v] - (the weight of v among t's targets, where p
  * is taken as exp(-loss) or exp(logp)), 0 in rows without a target, whatever they hold:

@@ -1,5 +1,6 @@
 """The losses over an FP8 head on the GPU where their arithmetic has an edge: teachers whose scaled
-logits do not fit fp32, or give next to nothing to a word.  Tolerances as in test_loss_ops.py."""
+logits do not fit fp32, or that give next to nothing to a word, and logits that do not fit
+it.  Tolerances as in test_loss_ops.py."""
 
 import numpy as np
 import pytest
@@ -98,3 +99,40 @@ def test_a_teacher_without_weights_stays_in_its_row(cuda, n, bad):
     dx, dw = both_grads(c, np.ones(n, np.float32))
     assert np.array_equal(np.isnan(f64(dx)).all(axis=1), wrong) and np.array_equal(np.isnan(f64(dx)).any(axis=1), wrong)
     assert np.isnan(f64(dw)[1]).all() and np.isnan(f64(dw)[6]).all()
+
+
+@pytest.mark.parametrize("n", [8, 300])
+@pytest.mark.parametrize("k", [None, 2])
+def test_infinite_logits_are_not_hidden(cuda, n, k):
+    """Logits past fp32 are infinities: a largest one has no log-probability (inf - inf), and the losses and
+    gradients of its row are not finite, whichever the target; a row without a target gives nothing."""
+    import torch
+
+    rows, cols, scale = 200, 16, 1e36
+    up, down = 0x7E, 0xFE  # 448 and -448: 448 * 16 * scale is past fp32's largest
+    x, xs = torch.full((n, cols), 0x38, dtype=torch.uint8, device=cuda), torch.ones(1, n, device=cuda)  # 1.0
+    ws_ = torch.ones(2, 1, device=cuda)
+    words = torch.tensor([3, 5, 0, -1], device=cuda).repeat(n // 4)
+    none = (words < 0).cpu().numpy()
+    for case, lse in (("largest", np.inf), ("all", -np.inf)):
+        w = torch.full((rows, cols), down if case == "all" else 0, dtype=torch.uint8, device=cuda)
+        if case == "largest":
+            w[3], w[5] = up, down
+        c = Head.__new__(Head)
+        c.n, c.rows, c.cols, c.k, c.scale, c.dev, c.head = n, rows, cols, k, scale, cuda, (x, xs, w, ws_)
+        if k is None:
+            c.t = words
+        else:
+            c.t, c.z = torch.stack([words, torch.where(words < 0, words, 7)], 1).contiguous(), torch.zeros(n, k, device=cuda)
+        c.forward()
+        loss = f64(c.loss)
+        assert np.all(f64(c.lse) == lse)
+        # the largest and, where all are -inf, every word: inf - inf; the others: inf
+        undefined = (f64(words) == 3) | (case == "all")
+        assert np.all(loss[none] == 0)
+        assert np.all(np.isnan(loss[undefined & ~none])) and np.all(loss[~undefined & ~none] == np.inf)
+        if k:
+            assert np.all(f64(c.logp)[none] == 0) and not np.any(np.isfinite(f64(c.logp)[~none]))
+        dx, dw = both_grads(c, np.ones(n, np.float32))
+        assert np.all(np.isnan(f64(dx)[~none])) and np.all(f64(dx)[none] == 0)
+        assert np.all(np.isnan(f64(dw)[3]))
