@@ -1256,7 +1256,9 @@ int launch_loss_grad(const LossArgs& a, void* ws, void* stream) {
   }
   const float unscale = a.scale * (1.f / float(1 << kProbBits));
   // dW beside dx.  Few tokens' dx is bound by memory, as dW is: of a large head they only slow each other (16 tokens of 128256 x
-  // 4096: 366 us in turn, 377 beside), of a small one dW hides its start (4 of 1298 x 608: 22.5 and 20.3)
+  // 4096: 363 us in turn, 372 beside; of 64000 x 4096: 196.6 and 198.5), of a small one dW hides its start (4 of 1298 x 608: 22.6
+  // and 19.0; 16 of 8192 x 2048, 2^24 codes: 36.9 and 35.5).  Between 2^24 and 2^27 codes beside still gains 1 to 2 %
+  // (16 of 32000 x 4096: 111.5 and 109.9)
   const bool dw_early = a.dx && (!p.few || int64_t(a.rows) * a.cols <= int64_t(1) << 24);
   for (int i = 0; i < p.pieces; ++i) {
     const int64_t v0 = i * p.piece, len = piece_len(p, a.rows, i);

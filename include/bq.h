@@ -523,8 +523,9 @@ int bq_linear_fp8_dw(const void* dy, int64_t ld_dy, const uint8_t* x, int64_t ld
  *     dx [n, cols]    = scale * diag(dloss) u W        (NULL: not wanted)
  *     dw [rows, cols] = scale * (diag(dloss) u)^T X    (NULL; accumulate: += )
  * both bf16, rounded once from fp32 sums.  The logits are made again in pieces of the vocabulary; u,
- * W and dloss * X are held as fp16, times powers of two that keep eleven bits of
- * each over 2^28 below its largest magnitude.
+ * W and dloss * X are held as fp16, times a power of two for all of each: eleven bits down to
+ * 2^-28 of its largest magnitude (u: of 1), fewer below, none under 2^-39.  (dx of few tokens
+ * takes u as three E4M3 terms, off by 2^-12 of itself or 2^-25 of its 128 words' largest, and W as it is.)
  * Sums are taken in an order that the sizes and the GPU fix.  Operands are aligned as in
  * bq_linear_fp8, n may be 0; n / 128 * rows / 128, each rounded up, is below 2^27
  * (BQ_EINVAL).  ws: bq_loss_fp8_workspace or bq_loss_fp8_grad_workspace bytes (either
